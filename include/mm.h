@@ -420,6 +420,131 @@ int mm_selftest_layer_barrier_timeout(const uint16_t* hidden, const uint16_t* ro
                                       int H, int E, int I, int top_k, int renorm, int barrier,
                                       uint16_t* out, void* stream);
 
+/* Element types of the entry points that take more than one. */
+enum { MM_DTYPE_FP32 = 0, MM_DTYPE_BF16 = 1, MM_DTYPE_FP16 = 2 };
+
+/*
+ * Routing from given router logits, with what training the router needs: the
+ * top-k ids and weights as mm_route gives them, the per-expert counts, the
+ * sums of the probabilities and the balance loss.
+ *
+ *   p[t,:]       = softmax(logits[t,:])                      (fp32)
+ *   topk_ids[t,:]= the top_k largest logits (equal logits: the lower id), in
+ *                  ascending order of the id
+ *   topk_w[t,j]  = p[t, topk_ids[t,j]]; with renorm divided by their sum
+ *   expert_counts[e] = tokens that selected e;  prob_sums[e] = sum_t p[t,e]
+ *   loss         = E * sum_e (expert_counts[e] / (n top_k)) * (prob_sums[e] / n)
+ *                  over the n counted tokens (0 when n == 0); 1 under a
+ *                  perfectly even load
+ *
+ * logits [T,E] of dtype MM_DTYPE_FP32 or MM_DTYPE_BF16; token_mask [T] bytes
+ * or NULL: a token whose byte is 0 (padding) gets weights 0 and enters neither
+ * the counts, the sums nor the loss, whatever its logits hold (NaN and
+ * infinities included); its ids are still distinct and in range. A row whose
+ * logits are all -inf is treated as masked. An expert with logit -inf has
+ * p = 0 and is selected only when fewer than top_k others remain. A NaN or
+ * +inf logit of a counted token makes that row's p NaN, and with it prob_sums
+ * and loss. All sums are fp32 in a fixed order: the outputs are the same on
+ * every call. topk_ids [T,top_k], topk_w [T,top_k], expert_counts [E],
+ * prob_sums [E], loss [1]. T == 0 writes zero counts, sums and loss.
+ *
+ * logits need the alignment of their elements only. workspace: at least
+ * mm_route_logits_workspace_size(T, E) bytes, 16-byte aligned (NULL if that
+ * is 0); calls with distinct workspaces may overlap.
+ */
+int mm_route_logits(const void* logits, int dtype, const uint8_t* token_mask, int T, int E,
+                    int top_k, int renorm, int32_t* topk_ids, float* topk_w,
+                    int32_t* expert_counts, float* prob_sums, float* loss, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mm_route_logits needs (-1 for invalid sizes). Host-only. */
+int64_t mm_route_logits_workspace_size(int T, int E);
+
+/*
+ * The gradient of mm_route_logits with respect to the logits:
+ *   d_logits[t,e] = dL/dlogits for dL = sum d_topk_w * dtopk_w + d_loss * dloss
+ * (the counts are constants). logits, token_mask and renorm as in the forward
+ * call, topk_ids its result. expert_counts: its result, or the sum of the
+ * results of several replicas, in which case the loss differentiated is the
+ * one over all their tokens (n = sum of the counts / top_k). d_topk_w
+ * [T,top_k] fp32 or NULL; d_loss [1] fp32 on the device or NULL. d_logits
+ * [T,E] of the logits' dtype, zero for masked tokens. An id outside [0, E) or
+ * repeated within its row is ignored. T == 0 is a no-op.
+ */
+int mm_route_logits_backward(const void* logits, int dtype, const uint8_t* token_mask,
+                             const int32_t* topk_ids, const int32_t* expert_counts,
+                             const float* d_topk_w, const float* d_loss, int T, int E, int top_k,
+                             int renorm, void* d_logits, void* stream);
+
+/*
+ * Microscaled 4-bit floats ("MXFP4"): blocks of 32 consecutive columns of a
+ * row share one scale 2^(s - 127) (byte s; 255 makes the block NaN); the
+ * values are e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *
+ * codes  [batch, rows, K/2] bytes, the even column in the low nibble.
+ * scales [batch, ceil(rows/128), ceil(K/128), 512] bytes: tiles of 128 rows x
+ *        128 columns; the byte of row r, block c = k/32 is at
+ *        (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4 of its tile, and bytes of
+ *        rows or columns outside the matrix are 0. (The order in which the
+ *        tensor cores take scales; a tile is one contiguous load.)
+ *
+ * mm_mxfp4_quantize: s = max(floor(log2 max|x|) - 2, -127) + 127 per block,
+ * codes = x 2^(127 - s) to the nearest e2m1, ties to the even code, beyond 6
+ * to 6. A block that holds an infinity or a NaN becomes NaN. x
+ * [batch, rows, K] of any MM_DTYPE. K % 32 == 0 (else MM_ERR_UNSUPPORTED);
+ * x, codes and scales 16-byte aligned. batch == 0 or rows == 0: no-op.
+ */
+int mm_mxfp4_quantize(const void* x, int dtype, int batch, int rows, int K, uint8_t* codes,
+                      uint8_t* scales, void* stream);
+
+/* Bytes of the scales of [batch, rows, K] (-1 for invalid sizes). Host-only. */
+int64_t mm_mxfp4_scales_size(int batch, int rows, int K);
+
+/*
+ * The values of stored 4-bit matrices, out [batch, rows, K] of any MM_DTYPE.
+ * Every value is exact in fp32 and bf16; fp16 rounds, beyond its range to
+ * infinity or zero. Otherwise as mm_mxfp4_quantize.
+ */
+int mm_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int batch, int rows, int K,
+                        void* out, int dtype, void* stream);
+
+/*
+ * C[M,N] = A B^T of a [M,K] and b [N,K] in 4-bit floats, on the block-scaled
+ * tensor cores with fp32 accumulation: one rounding to out_dtype
+ * (MM_DTYPE_BF16) or none (MM_DTYPE_FP32). M, N >= 0, K % 32 == 0. Scales and
+ * alignment as above. M == 0 or N == 0: no-op.
+ */
+int mm_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                  const uint8_t* b_scales, int M, int N, int K, void* c, int out_dtype,
+                  void* stream);
+
+/*
+ * The experts of the layer with 4-bit weights and 4-bit activations, for a
+ * routing that is given (mm_route, mm_route_logits):
+ *   xq       = quantise(hidden[t])                      (blocks of 32 along H)
+ *   g, u     = W_gate[e] xq, W_up[e] xq                 (fp32 accumulation)
+ *   a        = quantise(silu(g) * u)                    (from fp32, along I)
+ *   out[t,:] = sum_j topk_w[t,j] * (W_down[e_j] a)      (fp32, slot order; one
+ *                                                        rounding to bf16)
+ * hidden [T,H] bf16, topk_ids [T,top_k], topk_w [T,top_k] fp32. Weights as
+ * mm_mxfp4_quantize stores them: w_gate_up of [2E, I, H] (batch 2e the gate,
+ * 2e + 1 the up matrix of expert e: the codes are those of [E, 2I, H]), w_down
+ * of [E, H, I]. out [T,H] bf16. H and I multiples of 64, otherwise the limits
+ * of mm_moe_forward. Ids outside [0, E) or repeated within a row are dropped
+ * and flag MM_ERR_DEVICE, as in mm_align. The result is the same on every
+ * call. workspace (256-byte aligned) of at least
+ * mm_moe_experts_mxfp4_workspace_size bytes is required; calls with distinct
+ * workspaces may overlap. T == 0 is a no-op.
+ */
+int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const float* topk_w,
+                         const uint8_t* w_gate_up, const uint8_t* w_gate_up_scales,
+                         const uint8_t* w_down, const uint8_t* w_down_scales, int T, int H, int E,
+                         int I, int top_k, uint16_t* out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace mm_moe_experts_mxfp4 needs (-1 for invalid sizes). Host-only. */
+int64_t mm_moe_experts_mxfp4_workspace_size(int T, int H, int E, int I, int top_k);
+
 /* Frees the internal workspaces of every device. Not thread-safe with calls in flight. */
 void mm_shutdown(void);
 

@@ -15,4 +15,7 @@ from ._lib import (  # noqa: F401
     mm_moe_workspace_layout, mm_moe_workspace_size, forward_routing, WS_LAYOUT_FIELDS,
     mm_poll_device_status, mm_route, mm_selftest_wait_timeout, mm_selftest_layer_barrier_timeout,
     mm_shutdown, status_string,
+    MM_DTYPE_BF16, MM_DTYPE_FP16, MM_DTYPE_FP32, mm_moe_experts_mxfp4,
+    mm_moe_experts_mxfp4_workspace_size, mm_mxfp4_dequantize, mm_mxfp4_gemm, mm_mxfp4_quantize,
+    mm_mxfp4_scales_shape, mm_route_logits, mm_route_logits_backward, mxfp4_tile_scales,
 )

@@ -22,6 +22,7 @@ MM_ERR_CUDA = 3
 MM_ERR_NO_MEMORY = 4
 MM_ERR_DEVICE = 5
 MM_ERR_TIMEOUT = 6
+MM_DTYPE_FP32, MM_DTYPE_BF16, MM_DTYPE_FP16 = 0, 1, 2
 MM_GEMM_GATE_UP = 0
 MM_GEMM_DOWN = 1
 FORWARD_BLOCK_M = 16  # expert segments are padded to this multiple by mm_moe_forward
@@ -56,6 +57,16 @@ SIGNATURES = {
     "mm_selftest_wait_timeout": (_I, [_P]),
     "mm_selftest_layer_barrier_timeout": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P,
                                                _P]),
+    "mm_route_logits": (_I, [_P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "mm_route_logits_workspace_size": (_I64, [_I, _I]),
+    "mm_route_logits_backward": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "mm_mxfp4_quantize": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "mm_mxfp4_scales_size": (_I64, [_I, _I, _I]),
+    "mm_mxfp4_dequantize": (_I, [_P, _P, _I, _I, _I, _P, _I, _P]),
+    "mm_mxfp4_gemm": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _I, _P]),
+    "mm_moe_experts_mxfp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ,
+                                  _P]),
+    "mm_moe_experts_mxfp4_workspace_size": (_I64, [_I, _I, _I, _I, _I]),
     "mm_shutdown": (None, []),
 }
 
@@ -466,6 +477,229 @@ def mm_selftest_layer_barrier_timeout(hidden, router_w, w_gate_up, w_down, top_k
         _ptr(w_gate_up, torch.bfloat16, "w_gate_up"), _ptr(w_down, torch.bfloat16, "w_down"),
         T, H, E, I, top_k, int(bool(renorm)), barrier, _ptr(out, torch.bfloat16, "out"),
         _stream(stream)), "mm_selftest_layer_barrier_timeout")
+    return out
+
+
+_DTYPES = {torch.float32: MM_DTYPE_FP32, torch.bfloat16: MM_DTYPE_BF16,
+           torch.float16: MM_DTYPE_FP16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _shape(t, shape, name: str) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _mask_ptr(mask, T: int):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"token_mask must be bool or uint8, got {mask.dtype}")
+    _shape(mask, (T,), "token_mask")
+    return _ptr(mask, mask.dtype, "token_mask")
+
+
+def _run(name: str, stream, tensors, made, call) -> None:
+    """call(stream handle) on the device of `tensors` (all on one), on `stream`
+    or that device's current stream. `made`: tensors allocated here, kept
+    from reuse by their own stream until a foreign stream is done with them."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: all tensors must be on {dev}, got {t.device}")
+    if stream is not None:
+        s = (stream if isinstance(stream, torch.cuda.Stream)
+             else torch.cuda.ExternalStream(int(stream), device=dev))
+        for t in made:
+            if t.numel():
+                t.record_stream(s)
+    else:
+        s = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        _check(call(s.cuda_stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(s.cuda_stream), name)
+
+
+def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=None):
+    """Top-k routing of given router logits [T, E] (float32 or bfloat16) with
+    the statistics of the balance loss. Returns (topk_ids int32 [T, k],
+    topk_w fp32 [T, k], expert_counts int32 [E], prob_sums fp32 [E],
+    loss fp32 [1]). token_mask [T] (bool or uint8): zero for padding tokens."""
+    dt = _dtype(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    x = _ptr(logits, logits.dtype, "logits")
+    mask = _mask_ptr(token_mask, T)
+    need = int(lib().mm_route_logits_workspace_size(T, E))
+    ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=dev)
+    w = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    sums = torch.empty(E, dtype=torch.float32, device=dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
+    _run("mm_route_logits", stream, (logits, token_mask), (ids, w, counts, sums, loss, ws),
+         lambda st: lib().mm_route_logits(x, dt, mask, T, E, top_k, int(bool(renorm)),
+                                          ids.data_ptr(), w.data_ptr(), counts.data_ptr(),
+                                          sums.data_ptr(), loss.data_ptr(),
+                                          ws.data_ptr() if need > 0 else None, max(need, 0), st))
+    return ids, w, counts, sums, loss
+
+
+def mm_route_logits_backward(logits, topk_ids, expert_counts, renorm: bool, d_topk_w=None,
+                             d_loss=None, token_mask=None, stream=None):
+    """The gradient of mm_route_logits: d_logits [T, E] of the logits' dtype
+    from d_topk_w [T, k] fp32 and / or d_loss [1] fp32. expert_counts may be
+    the sum over several replicas (the loss is then the one over all of them)."""
+    dt = _dtype(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    _shape(topk_ids, (T, k), "topk_ids")
+    _shape(expert_counts, (E,), "expert_counts")
+    _shape(d_topk_w, (T, k), "d_topk_w")
+    if d_loss is not None and d_loss.numel() != 1:
+        raise ValueError("d_loss must hold one value")
+    grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    args = (_ptr(logits, logits.dtype, "logits"), dt, _mask_ptr(token_mask, T),
+            _ptr(topk_ids, torch.int32, "topk_ids"),
+            _ptr(expert_counts, torch.int32, "expert_counts"),
+            _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(d_loss, torch.float32, "d_loss"), T, E,
+            k, int(bool(renorm)), grad.data_ptr())
+    _run("mm_route_logits_backward", stream,
+         (logits, token_mask, topk_ids, expert_counts, d_topk_w, d_loss), (grad,),
+         lambda st: lib().mm_route_logits_backward(*args, st))
+    return grad
+
+
+def mm_mxfp4_scales_shape(rows: int, K: int) -> tuple:
+    """Shape of the scale tiles of one [rows, K] matrix."""
+    return ((rows + 127) // 128, (K + 127) // 128, 512)
+
+
+def mxfp4_tile_scales(scales):
+    """Scale bytes [..., rows, K/32] in plain row order -> the stored tiles
+    [..., ceil(rows/128), ceil(K/128), 512] (weight preparation, done once)."""
+    lead, (rows, cols) = scales.shape[:-2], scales.shape[-2:]
+    rt, kt, _ = mm_mxfp4_scales_shape(rows, cols * 32)
+    s = scales.new_zeros((*lead, rt * 128, kt * 4))
+    s[..., :rows, :cols] = scales
+    s = s.reshape(-1, rt, 4, 32, kt, 4).permute(0, 1, 4, 3, 2, 5)
+    return s.reshape(*lead, rt, kt, 512).contiguous()
+
+
+def mm_mxfp4_quantize(x, stream=None):
+    """x [rows, K] or [batch, rows, K] (float32, bfloat16, float16; K % 32 == 0)
+    as microscaled 4-bit floats. Returns (codes uint8 [..., rows, K/2],
+    scales uint8 [..., ceil(rows/128), ceil(K/128), 512])."""
+    dt = _dtype(x, "x")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must have 2 or 3 dimensions")
+    lead, (rows, K) = x.shape[:-2], x.shape[-2:]
+    batch = lead[0] if lead else 1
+    xp = _ptr(x, x.dtype, "x")
+    if K % 32 != 0 or K == 0:
+        raise MMError(MM_ERR_UNSUPPORTED if K else MM_ERR_INVALID_ARG, "mm_mxfp4_quantize")
+    codes = torch.empty((*lead, rows, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*lead, *mm_mxfp4_scales_shape(rows, K)), dtype=torch.uint8,
+                         device=x.device)
+    _run("mm_mxfp4_quantize", stream, (x,), (codes, scales),
+         lambda st: lib().mm_mxfp4_quantize(xp, dt, batch, rows, K, codes.data_ptr(),
+                                            scales.data_ptr(), st))
+    return codes, scales
+
+
+def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
+    """The values [..., rows, K] of codes [..., rows, K/2] and their scale tiles."""
+    if codes.dim() not in (2, 3):
+        raise ValueError("codes must have 2 or 3 dimensions")
+    lead, (rows, half) = codes.shape[:-2], codes.shape[-2:]
+    K, batch = 2 * half, (lead[0] if lead else 1)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    cp, sp = _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales")
+    _shape(scales, (*lead, *mm_mxfp4_scales_shape(rows, K)), "scales")
+    out = torch.empty((*lead, rows, K), dtype=dtype, device=codes.device)
+    _run("mm_mxfp4_dequantize", stream, (codes, scales), (out,),
+         lambda st: lib().mm_mxfp4_dequantize(cp, sp, batch, rows, K, out.data_ptr(),
+                                              _DTYPES[dtype], st))
+    return out
+
+
+def _matrix(codes, scales, name: str):
+    """(rows, K) and the pointers of one 4-bit matrix (a leading dimension of 1 allowed)."""
+    if codes.dim() == 3 and codes.shape[0] == 1:
+        codes, scales = codes[0], scales[0]
+    if codes.dim() != 2:
+        raise ValueError(f"{name} must be one matrix, got codes of shape {tuple(codes.shape)}")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    _shape(scales, mm_mxfp4_scales_shape(rows, K), f"{name} scales")
+    return rows, K, _ptr(codes, torch.uint8, name), _ptr(scales, torch.uint8, f"{name} scales")
+
+
+def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, stream=None):
+    """C [M, N] = A B^T of two 4-bit matrices [M, K] and [N, K]; bfloat16 or float32."""
+    M, K, a, sa = _matrix(a_codes, a_scales, "a")
+    N, Kb, b, sb = _matrix(b_codes, b_scales, "b")
+    if K != Kb:
+        raise ValueError(f"a has {K} columns, b has {Kb}")
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    c = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
+    _run("mm_mxfp4_gemm", stream, (a_codes, a_scales, b_codes, b_scales), (c,),
+         lambda st: lib().mm_mxfp4_gemm(a, sa, b, sb, M, N, K, c.data_ptr(), _DTYPES[out_dtype],
+                                        st))
+    return c
+
+
+def mm_moe_experts_mxfp4_workspace_size(T: int, H: int, E: int, I: int, top_k: int) -> int:
+    return int(lib().mm_moe_experts_mxfp4_workspace_size(T, H, E, I, top_k))
+
+
+def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, w_down,
+                         w_down_scales, out=None, workspace=None, stream=None):
+    """The experts of the layer with 4-bit weights for a given routing; returns
+    out [T, H] bf16. w_gate_up: codes [2E, I, H/2] (or [E, 2I, H/2]) with the
+    scale tiles of 2E matrices [I, H]; w_down: codes [E, H, I/2]. workspace:
+    uint8 of mm_moe_experts_mxfp4_workspace_size bytes (allocated per call if
+    None)."""
+    T, H = hidden.shape
+    k = topk_ids.shape[1]
+    E, _, half = w_down.shape
+    I = 2 * half
+    _shape(topk_ids, (T, k), "topk_ids")
+    _shape(topk_w, (T, k), "topk_w")
+    _shape(w_down, (E, H, half), "w_down")
+    if tuple(w_gate_up.shape) != (E, 2 * I, H // 2):
+        _shape(w_gate_up, (2 * E, I, H // 2), "w_gate_up")
+    _shape(w_gate_up_scales, (2 * E, *mm_mxfp4_scales_shape(I, H)), "w_gate_up_scales")
+    _shape(w_down_scales, (E, *mm_mxfp4_scales_shape(H, I)), "w_down_scales")
+    args = (_ptr(hidden, torch.bfloat16, "hidden"), _ptr(topk_ids, torch.int32, "topk_ids"),
+            _ptr(topk_w, torch.float32, "topk_w"), _ptr(w_gate_up, torch.uint8, "w_gate_up"),
+            _ptr(w_gate_up_scales, torch.uint8, "w_gate_up_scales"),
+            _ptr(w_down, torch.uint8, "w_down"), _ptr(w_down_scales, torch.uint8, "w_down_scales"))
+    made = []
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        made.append(out)
+    _shape(out, (T, H), "out")
+    if workspace is None:
+        need = mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k)
+        workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=hidden.device)
+        made.append(workspace)
+    outp, ws = _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace")
+    _run("mm_moe_experts_mxfp4", stream,
+         (hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, w_down, w_down_scales, out,
+          workspace), made,
+         lambda st: lib().mm_moe_experts_mxfp4(*args, T, H, E, I, k, outp, ws, workspace.numel(),
+                                               st))
     return out
 
 

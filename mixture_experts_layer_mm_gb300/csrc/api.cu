@@ -151,6 +151,17 @@ int current_status_word(unsigned** out) {
   return rc;
 }
 
+int current_device_info(int* sms, unsigned** status) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DevState* s = nullptr;
+  const int rc = device_state(&s);
+  if (rc == MM_OK) {
+    *sms = s->sms;
+    *status = s->status;
+  }
+  return rc;
+}
+
 }  // namespace mm
 
 extern "C" {

@@ -72,6 +72,8 @@ inline cudaError_t smem_attr_once(DeviceFlags& done, Kern kern, int bytes) {
 // Device address of the current device's status word (see
 // mm_poll_device_status); sets up the device state on first use.
 int current_status_word(unsigned** out);
+// The same with the SM count of the current device.
+int current_device_info(int* sms, unsigned** status);
 
 // Outputs of the grouping step (see mm_align) when the router runs it itself.
 struct AlignOut {
@@ -153,6 +155,11 @@ bool make_tensor_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_
 bool make_tensor_map_sw128(CUtensorMap* m, const void* base, uint32_t rank,
                            const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
+// Tensor map of 4-bit codes, a row-major [rows, K/2] byte matrix read in boxes
+// of 128 bytes (256 columns) x box_rows rows with the 128-byte swizzle.
+bool make_tensor_map_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K,
+                           uint32_t box_rows);
+
 // Whether the gate_up GEMM gathers token rows with TMA tile::gather4 (few rows
 // per expert) rather than with cp.async loader warps.
 bool gate_up_gathers_rows(int T, int top_k, int E);
@@ -231,5 +238,52 @@ cudaError_t launch_moe_decode(const uint16_t* hidden, const uint16_t* router_w, 
 cudaError_t launch_add_rmsnorm(const uint16_t* x, uint16_t* residual, const uint16_t* weight,
                                float eps, int T, int H, uint16_t* normed, int num_sms,
                                bool after_prev, cudaStream_t st);
+
+// Routing from given logits with the balance statistics, and its gradient
+// (route_logits.cu). workspace: route_logits_workspace(T, E) bytes.
+long long route_logits_workspace(int T, int E);
+cudaError_t launch_route_logits(const void* logits, bool is_bf16, const uint8_t* mask, int T, int E,
+                                int top_k, int renorm, int32_t* ids, float* w, int32_t* counts,
+                                float* prob_sums, float* loss, void* workspace, int num_sms,
+                                cudaStream_t st);
+cudaError_t launch_route_logits_backward(const void* logits, bool is_bf16, const uint8_t* mask,
+                                         const int32_t* ids, const int32_t* counts, const float* dw,
+                                         const float* dloss, int T, int E, int top_k, int renorm,
+                                         void* grad, int num_sms, cudaStream_t st);
+
+// Microscaled 4-bit rows (mxfp4.cu): dtype is an MM_DTYPE, K % 32 == 0.
+cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int rows, int K,
+                               uint8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long batch,
+                                 int rows, int K, void* out, int dtype, cudaStream_t st);
+// Row r of codes / scales = hidden[sorted[r] / top_k] quantised, for the real
+// slots of the grouping.
+cudaError_t launch_mx_gather_quantize(const uint16_t* hidden, const int32_t* sorted,
+                                      const int32_t* offsets, int T, int top_k, int E, int H,
+                                      long long capacity, uint8_t* codes, uint8_t* scales,
+                                      int num_sms, bool after_prev, cudaStream_t st);
+// out[t] = bf16(sum_j w[t,j] y[t top_k + j]).
+cudaError_t launch_mx_combine(const float* y, const int32_t* ids, const float* w, int T, int E,
+                              int top_k, int H, uint16_t* out, int num_sms, bool after_prev,
+                              cudaStream_t st);
+
+// Products of 4-bit matrices (mxfp4_gemm.cu). The experts' segments begin at
+// multiples of kMxBlockM rows (capacity rows in all) and make at most
+// max_chunks chunks of kMxBlockM rows.
+constexpr int kMxBlockM = 128;
+cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                           const uint8_t* b_scales, int M, int N, int K, void* c, bool out_fp32,
+                           int num_sms, unsigned* err, cudaStream_t st);
+cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
+                                      const uint8_t* w, const uint8_t* w_scales,
+                                      const int32_t* offsets, const int32_t* counts, int E, int I,
+                                      int H, long long capacity, long long max_chunks,
+                                      uint8_t* act, uint8_t* act_scales, int num_sms,
+                                      unsigned* err, bool after_prev, cudaStream_t st);
+cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
+                                   const uint8_t* w_scales, const int32_t* sorted,
+                                   const int32_t* offsets, const int32_t* counts, int E, int H,
+                                   int I, long long capacity, long long max_chunks, float* y,
+                                   int num_sms, unsigned* err, bool after_prev, cudaStream_t st);
 
 }  // namespace mm

@@ -1,0 +1,335 @@
+// Microscaled 4-bit rows: quantisation, the way back, and the two row passes
+// of the 4-bit experts (token rows quantised into segment order, and the
+// weighted sum of a token's expert outputs). The format is in mx_device.cuh.
+//
+// Per block of 32: e = floor(log2 max|x|) - 2, scale byte e + 127, codes
+// e2m1(x 2^-e) to nearest even, saturating at 6. x 2^-e is a product with a
+// power of two and exact, except where it underflows, far below the border
+// 0.25 of the code 0; so the one rounding is the conversion to e2m1.
+//
+// A lane takes 16 consecutive columns, two lanes a block; the lanes of a row
+// are a power of two (all 32 from K = 512 on). One pass: a row is read once,
+// its codes and scale bytes are written once, so the kernels are bound by
+// memory.
+#include "mm.h"
+#include "mm_internal.h"
+#include "mx_device.cuh"
+
+#include <cuda_fp16.h>
+
+namespace mm {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kMxThreads = 256;
+constexpr int kMxWarps = kMxThreads / 32;
+
+struct Raw16f { uint4 r[4]; };  // 16 float32
+struct Raw16h { uint4 r[2]; };  // 16 bf16 or fp16
+
+template <int DT> struct MxIn;  // storage of 16 input values
+template <> struct MxIn<MM_DTYPE_FP32> { using Raw = Raw16f; static constexpr int kBytes = 4; };
+template <> struct MxIn<MM_DTYPE_BF16> { using Raw = Raw16h; static constexpr int kBytes = 2; };
+template <> struct MxIn<MM_DTYPE_FP16> { using Raw = Raw16h; static constexpr int kBytes = 2; };
+
+template <int DT>
+__device__ __forceinline__ void load16(const unsigned char* p, typename MxIn<DT>::Raw& raw) {
+#pragma unroll
+  for (int i = 0; i < MxIn<DT>::kBytes; ++i) raw.r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+}
+
+template <int DT>
+__device__ __forceinline__ void zero16(typename MxIn<DT>::Raw& raw) {
+#pragma unroll
+  for (int i = 0; i < MxIn<DT>::kBytes; ++i) raw.r[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack16(const typename MxIn<DT>::Raw& raw, float (&v)[16]) {
+  if constexpr (DT == MM_DTYPE_FP32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[4 * i] = __uint_as_float(raw.r[i].x);
+      v[4 * i + 1] = __uint_as_float(raw.r[i].y);
+      v[4 * i + 2] = __uint_as_float(raw.r[i].z);
+      v[4 * i + 3] = __uint_as_float(raw.r[i].w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {raw.r[i].x, raw.r[i].y, raw.r[i].z, raw.r[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == MM_DTYPE_BF16) {
+          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          v[8 * i + 2 * j] = f.x;
+          v[8 * i + 2 * j + 1] = f.y;
+        }
+      }
+    }
+  }
+}
+
+// The 16 values of this lane, half a block: codes (8 bytes) and, in every
+// lane of a group of 8, the four scale bytes of the group's 128 columns.
+__device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t& scales4) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(kAll, amax, 1));
+  const uint32_t s = mx_scale_byte(amax);
+  const float inv = mx_inv_scale(s);
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = v[i] * inv;
+    b[i] = v[8 + i] * inv;
+  }
+  uint32_t q = s << (8 * ((threadIdx.x >> 1) & 3));
+  q |= __shfl_xor_sync(kAll, q, 2);
+  q |= __shfl_xor_sync(kAll, q, 4);
+  scales4 = q;
+  return make_uint2(mx_pack8(a), mx_pack8(b));
+}
+
+// A row handed to a group of 2^lanes_log2 lanes: columns
+// [16 * lane, 16 * lane + 16) of every span of 16 << lanes_log2. Columns at or
+// past K of the last scale tile give zero scale bytes and no codes. src NULL:
+// a padding row (zero scale bytes only). All lanes of the warp call this.
+template <int DT, int U>
+__device__ __forceinline__ void quantize_row(const unsigned char* src, int K, int lanes_log2,
+                                             uint8_t* codes, uint8_t* scale_row, bool active) {
+  const int lane = threadIdx.x & ((1 << lanes_log2) - 1);
+  const int span = 16 << lanes_log2;
+  const int kp = (K + kMxTile - 1) / kMxTile * kMxTile;
+  for (int c0 = lane * 16; c0 - lane * 16 < kp; c0 += U * span) {
+    typename MxIn<DT>::Raw raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * span;
+      if (src != nullptr && c < K)
+        load16<DT>(src + (size_t)c * MxIn<DT>::kBytes, raw[u]);
+      else
+        zero16<DT>(raw[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * span;
+      if (c - lane * 16 >= kp) break;  // the same for every lane of the group
+      float v[16];
+      unpack16<DT>(raw[u], v);
+      uint32_t s4;
+      const uint2 code = encode16(v, s4);
+      if (active && c < K && src != nullptr)
+        *reinterpret_cast<uint2*>(codes + c / 2) = code;
+      if (active && (threadIdx.x & 7) == 0 && c < kp)
+        *reinterpret_cast<uint32_t*>(scale_row + (size_t)(c / kMxTile) * kMxTileBytes) = s4;
+    }
+  }
+}
+
+// Lanes of a row (log2): enough for 16 columns a lane, at least the 8 of one
+// scale tile (so that a group's four bytes come from one row).
+__host__ __device__ __forceinline__ int row_lanes_log2(int K) {
+  return K > 256 ? 5 : K > 128 ? 4 : 3;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const unsigned char* __restrict__ x,
+                                                                 long long prows, int rows, int rp,
+                                                                 int K, int lanes_log2,
+                                                                 uint8_t* __restrict__ codes,
+                                                                 uint8_t* __restrict__ scales) {
+  const int per_warp = 32 >> lanes_log2;
+  const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
+                        ((threadIdx.x & 31) >> lanes_log2);
+  const bool active = row < prows;
+  const long long b = active ? row / rp : 0;
+  const int r = active ? (int)(row - b * rp) : 0;
+  const bool real = active && r < rows;
+  const int kt = (int)mx_tiles(K);
+  const size_t at = (size_t)(b * rows + r) * K;
+  quantize_row<DT, 4>(real ? x + at * MxIn<DT>::kBytes : nullptr, K, lanes_log2, codes + at / 2,
+                      scales + (size_t)b * (rp / kMxTile) * kt * kMxTileBytes +
+                          mx_scale_offset(r, 0, kt),
+                      active);
+}
+
+// Two e2m1 of a byte as two floats.
+__device__ __forceinline__ float2 decode2(uint32_t byte) {
+  uint32_t h;
+  asm("{ .reg .b8 b, z;\n\t"
+      "mov.b16 {b, z}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b; }"
+      : "=r"(h)
+      : "h"((uint16_t)byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+
+// One lane: 16 columns (8 code bytes, one scale byte) of one row.
+template <int DT>
+__global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long nrows, int rows,
+    int K, int lanes_log2, unsigned char* __restrict__ out) {
+  const int per_warp = 32 >> lanes_log2;
+  const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
+                        ((threadIdx.x & 31) >> lanes_log2);
+  if (row >= nrows) return;
+  const int lane = threadIdx.x & ((1 << lanes_log2) - 1);
+  const long long b = row / rows;
+  const int r = (int)(row - b * rows);
+  const int kt = (int)mx_tiles(K);
+  const uint8_t* srow =
+      scales + (size_t)b * mx_tiles(rows) * kt * kMxTileBytes + mx_scale_offset(r, 0, kt);
+#pragma unroll 4
+  for (int c = lane * 16; c < K; c += 16 << lanes_log2) {
+    const uint2 code = __ldg(reinterpret_cast<const uint2*>(codes + ((size_t)row * K + c) / 2));
+    const float s =
+        mx_scale(__ldg(srow + (size_t)(c / kMxTile) * kMxTileBytes + (c / kMxBlock) % 4));
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = decode2(((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xffu);
+      v[2 * i] = f.x * s;
+      v[2 * i + 1] = f.y * s;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)row * K + c) * MxIn<DT>::kBytes);
+    if constexpr (DT == MM_DTYPE_FP32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dst[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (DT == MM_DTYPE_BF16) {
+          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        } else {
+          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+// Token rows of the experts' segments: row r of xs = hidden[sorted[r] / k]
+// quantised, for the real slots (padding rows are never read). One warp per
+// slot, so a token is quantised once per expert it goes to: hidden stays in
+// L2, and no launch for a separate quantised copy stands in the chain.
+__global__ void __launch_bounds__(kMxThreads) mx_gather_quantize_kernel(
+    const unsigned char* __restrict__ hidden, const int32_t* __restrict__ sorted,
+    const int32_t* __restrict__ offsets, int E, int top_k, int Tk, int H,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const int rows = __ldg(offsets + E);
+  const int kt = (int)mx_tiles(H);
+  const int step = gridDim.x * kMxWarps;
+  for (int r = blockIdx.x * kMxWarps + (threadIdx.x >> 5); r < rows; r += step) {
+    const int f = __ldg(sorted + r);
+    if (f >= Tk) continue;
+    quantize_row<MM_DTYPE_BF16, 4>(hidden + (size_t)(f / top_k) * H * 2, H, 5,
+                                   codes + (size_t)r * (H / 2), scales + mx_scale_offset(r, 0, kt),
+                                   true);
+  }
+}
+
+// out[t] = bf16(sum_j w[t,j] y[t k + j]) in slot order, 4 columns a thread. A
+// slot whose id the grouping dropped (outside [0, E), or a repeat within the
+// token) has no row in y and adds nothing.
+__global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
+    const float4* __restrict__ y, const int32_t* __restrict__ ids, const float* __restrict__ w,
+    int T, int E, int top_k, int h4, uint2* __restrict__ out) {
+  pdl_wait();
+  const long long n = (long long)T * h4;
+  for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kMxThreads) {
+    const int t = (int)(i / h4), h = (int)(i - (long long)t * h4);
+    const size_t f0 = (size_t)t * top_k;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int j = 0; j < top_k; ++j) {
+      const int id = __ldg(ids + f0 + j);
+      bool use = id >= 0 && id < E;
+      for (int jj = 0; jj < j; ++jj) use &= __ldg(ids + f0 + jj) != id;
+      if (!use) continue;
+      const float wj = __ldg(w + f0 + j);
+      const float4 v = __ldg(y + (f0 + j) * h4 + h);
+      s.x += wj * v.x;
+      s.y += wj * v.y;
+      s.z += wj * v.z;
+      s.w += wj * v.w;
+    }
+    out[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int rows, int K,
+                               uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  const int rp = (int)(mx_tiles(rows) * kMxTile), ll = row_lanes_log2(K);
+  const long long prows = batch * rp;
+  const long long per_block = (long long)kMxWarps * (32 >> ll);
+  const dim3 grid((unsigned)((prows + per_block - 1) / per_block)), block(kMxThreads);
+  const unsigned char* p = static_cast<const unsigned char*>(x);
+  if (dtype == MM_DTYPE_FP32)
+    return launch_k(mx_quantize_kernel<MM_DTYPE_FP32>, grid, block, 0, st, false, p, prows, rows, rp,
+                    K, ll, codes, scales);
+  if (dtype == MM_DTYPE_BF16)
+    return launch_k(mx_quantize_kernel<MM_DTYPE_BF16>, grid, block, 0, st, false, p, prows, rows, rp,
+                    K, ll, codes, scales);
+  return launch_k(mx_quantize_kernel<MM_DTYPE_FP16>, grid, block, 0, st, false, p, prows, rows, rp,
+                  K, ll, codes, scales);
+}
+
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long batch,
+                                 int rows, int K, void* out, int dtype, cudaStream_t st) {
+  const int ll = row_lanes_log2(K);
+  const long long nrows = batch * rows;
+  const long long per_block = (long long)kMxWarps * (32 >> ll);
+  const dim3 grid((unsigned)((nrows + per_block - 1) / per_block)), block(kMxThreads);
+  unsigned char* p = static_cast<unsigned char*>(out);
+  if (dtype == MM_DTYPE_FP32)
+    return launch_k(mx_dequantize_kernel<MM_DTYPE_FP32>, grid, block, 0, st, false, codes, scales,
+                    nrows, rows, K, ll, p);
+  if (dtype == MM_DTYPE_BF16)
+    return launch_k(mx_dequantize_kernel<MM_DTYPE_BF16>, grid, block, 0, st, false, codes, scales,
+                    nrows, rows, K, ll, p);
+  return launch_k(mx_dequantize_kernel<MM_DTYPE_FP16>, grid, block, 0, st, false, codes, scales,
+                  nrows, rows, K, ll, p);
+}
+
+cudaError_t launch_mx_gather_quantize(const uint16_t* hidden, const int32_t* sorted,
+                                      const int32_t* offsets, int T, int top_k, int E, int H,
+                                      long long capacity, uint8_t* codes, uint8_t* scales,
+                                      int num_sms, bool after_prev, cudaStream_t st) {
+  const long long want = (capacity + kMxWarps - 1) / kMxWarps;
+  const int grid = (int)(want < 8LL * num_sms ? want : 8LL * num_sms);
+  return launch_k(mx_gather_quantize_kernel, dim3(grid), dim3(kMxThreads), 0, st, after_prev,
+                  reinterpret_cast<const unsigned char*>(hidden), sorted, offsets, E, top_k,
+                  T * top_k, H, codes, scales);
+}
+
+cudaError_t launch_mx_combine(const float* y, const int32_t* ids, const float* w, int T, int E,
+                              int top_k, int H, uint16_t* out, int num_sms, bool after_prev,
+                              cudaStream_t st) {
+  const long long want = ((long long)T * (H / 4) + kMxThreads - 1) / kMxThreads;
+  const int grid = (int)(want < 16LL * num_sms ? want : 16LL * num_sms);
+  return launch_k(mx_combine_kernel, dim3(grid), dim3(kMxThreads), 0, st, after_prev,
+                  reinterpret_cast<const float4*>(y), ids, w, T, E, top_k, H / 4,
+                  reinterpret_cast<uint2*>(out));
+}
+
+}  // namespace mm

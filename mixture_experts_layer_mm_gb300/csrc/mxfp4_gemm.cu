@@ -1,0 +1,519 @@
+// Products of microscaled 4-bit matrices on the sm_103a tensor cores
+// (tcgen05.mma kind::mxf4 with block scales, accumulators in tensor memory,
+// operands staged by TMA). One kernel, three epilogues:
+//
+//   dense    C[r, n] = x_r . w_n                       (bf16 or fp32)
+//   gate_up  act[r, i] = Q(silu(g) u), g = x_r . w_i (gate), u = x_r . w_i (up)
+//            for the rows r of every expert's segment; Q: 4-bit blocks along i
+//   down     y[f, h] = x_r . w_h, f = sorted[r] the (token, slot) of row r
+//
+// Orientation as in gemm.cu: the weight rows are the MMA's M side (128 rows
+// an MMA), the token rows its N side (any multiple of 16 up to 128). A tile
+// is (chunk of up to 128 rows of one segment, m-tile); a stage holds 256
+// columns of two 128-row weight tiles (A0, A1) and of the chunk's rows (B),
+// 128 bytes a row, plus their scale tiles. Segments begin at multiples of 128
+// rows, so a chunk's scale bytes are whole tiles.
+//
+// The products of two e2m1 values and two powers of two are exact; the
+// accumulation is in fp32 in tensor memory.
+//
+// gate_up's blocks run along i, which is the lane of tensor memory: a block
+// is one column of one warp's 32 lanes, its maximum one redux, and the codes
+// of 8 columns are turned into row order by three exchanges between lanes.
+// The activation is quantised from the fp32 product and is rounded once.
+#include <algorithm>
+
+#include "mm.h"
+#include "mm_internal.h"
+#include "mx_device.cuh"
+
+namespace mm {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kBN = 128;   // token rows per chunk
+constexpr int kStages = 4;
+constexpr int kStageK = 256;                // columns per stage (128 bytes a row)
+constexpr int kTileBytes = 128 * 128;       // 128 rows of one stage
+constexpr int kScaleStage = 2 * kMxTileBytes;  // scale bytes of 128 rows of one stage
+constexpr int kStageBytes = 3 * kTileBytes + 3 * kScaleStage;
+constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = kStages * kStageStride + 1024;
+static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
+
+// Warp roles: 0 = nothing but the prologue, 1 = MMA issuer, 2-9 = epilogue,
+// 10-13 = producers (one per ring slot).
+constexpr int kEpiWarp0 = 2, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
+constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
+constexpr int kThreads = (kProdWarp0 + kStages) * 32;
+
+// Tensor memory: D0 and D1 (128 columns each), then per ring slot the scale
+// columns of its two 128-column halves: A0, A1, B, 4 columns each.
+constexpr uint32_t kScaleCol0 = 2 * kBN, kScaleCols = 32;
+constexpr uint32_t kTmemCols = 512;
+
+enum { kDense = 0, kGateUp = 1, kDown = 2 };
+
+struct MxGemmArgs {
+  const int32_t* offsets;  // [E + 1] first row of each segment (NULL: dense)
+  const int32_t* counts;   // [E] rows of each segment
+  const int32_t* sorted;   // down: (token, slot) of a row
+  const uint8_t* w_scales;
+  const uint8_t* x_scales;
+  void* out;               // dense: C; gate_up: act codes; down: y
+  uint8_t* act_scales;     // gate_up
+  unsigned* err;
+  int E, rows;    // rows: of the one segment of a dense product
+  int N, K;       // output columns (gate_up: intermediates), reduction
+  int n_mtiles;
+  int out_fp32;   // dense
+};
+
+__device__ __forceinline__ bool stopped(const int* flag) {
+  return *reinterpret_cast<const volatile int*>(flag) != 0;
+}
+
+__device__ __forceinline__ void stop(int* flag, unsigned* err) {
+  *reinterpret_cast<volatile int*>(flag) = 1;
+  atomicOr(err, kDevErrTimeout);
+}
+
+struct Tile {
+  int e, m, row0, nrows;
+};
+
+__device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int* first_chunk,
+                                        const int* off, const int* cnt) {
+  Tile t;
+  const int ch = tile / n_mtiles;
+  t.m = tile - ch * n_mtiles;
+  int lo = 0, hi = E;  // first_chunk[lo] <= ch < first_chunk[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_chunk[mid] <= ch)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  t.e = lo;
+  const int in = (ch - first_chunk[lo]) * kBN;
+  t.row0 = off[lo] + in;
+  t.nrows = min(kBN, cnt[lo] - in);
+  return t;
+}
+
+// The first two m-tile halves of a tile in the weight matrices: 128-row tile
+// index (also of the scales) and code row of A0; A1 exists if has1.
+struct WeightAt {
+  int row0, row1;
+  long long st0, st1;  // scale tile rows
+  bool has1;
+};
+
+template <int MODE>
+__device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& t) {
+  WeightAt w;
+  const int tiles = (a.N + 127) / 128;  // scale tile rows per weight matrix
+  if (MODE == kGateUp) {  // two matrices per expert: gate, up
+    w.row0 = 2 * t.e * a.N + t.m * 128;
+    w.row1 = w.row0 + a.N;
+    w.st0 = (long long)(2 * t.e) * tiles + t.m;
+    w.st1 = w.st0 + tiles;
+    w.has1 = true;
+  } else {
+    w.row0 = t.e * a.N + t.m * 256;
+    w.row1 = w.row0 + 128;
+    w.st0 = (long long)t.e * tiles + 2 * t.m;
+    w.st1 = w.st0 + 1;
+    w.has1 = 2 * t.m + 1 < tiles;
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint32_t spread4(uint32_t x) {  // nibble n -> byte n
+  x = (x | (x << 8)) & 0x00FF00FFu;
+  return (x | (x << 4)) & 0x0F0F0F0Fu;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const MxGemmArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int stop_s;
+  __shared__ int off_s[kMaxExperts], cnt_s[kMaxExperts], first_s[kMaxExperts + 1];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = a.E;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = tid; i < E; i += kThreads) {
+    off_s[i] = a.offsets != nullptr ? a.offsets[i] : 0;
+    cnt_s[i] = a.counts != nullptr ? a.counts[i] : a.rows;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < E ? (cnt_s[e] + kBN - 1) / kBN : 0;
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (e < E) first_s[e] = run + incl - c;
+      run += __shfl_sync(kAll, incl, 31);
+    }
+    if (lane == 0) first_s[E] = run;
+  }
+  __syncthreads();
+  const int total = first_s[E] * a.n_mtiles;
+  if ((int)blockIdx.x >= total) return;  // uniform across the CTA
+
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint64_t* full = bars;
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* done = tempty + 1;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(tempty), kEpiThreads);
+    mbar_init(smem_u32(done), 1);
+    stop_s = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_s;
+  const int k_tiles = (a.K + 127) / 128;         // scale tiles per row
+  const int nk = (a.K + kStageK - 1) / kStageK;  // stages per tile
+
+  if (warp >= kProdWarp0) {
+    // ---------------------------------------------------- producers (10-13) ---
+    // Warp 10 + s owns ring slot s: a warp's copies that signal another
+    // barrier than its previous ones would wait for those to land.
+    const int slot = warp - kProdWarp0;
+    if (lane == 0) {
+      const uint64_t pol_w = l2_policy_evict_normal();
+      const uint64_t pol_x = l2_policy_evict_last();
+      const uint32_t st = smem_base + slot * kStageStride;
+      const uint32_t sc = st + 3 * kTileBytes;
+      const uint32_t fb = smem_u32(&full[slot]);
+      uint32_t use = 0;
+      int q = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        if (stopped(&stop_s)) break;
+        const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+        const WeightAt w = weights_of<MODE>(a, t);
+        const int nbox = (t.nrows + 31) / 32;  // boxes of 32 token rows
+        for (int kb = 0; kb < nk; ++kb) {
+          const bool mine = q == slot;
+          if (++q == kStages) q = 0;
+          if (!mine) continue;
+          if (!mbar_wait(smem_u32(&empty[slot]), (use & 1u) ^ 1u)) {
+            stop(&stop_s, a.err);
+            ok = false;
+            break;
+          }
+          const int kt = 2 * kb;  // first scale tile of the stage
+          const uint32_t sb = min(2, k_tiles - kt) * kMxTileBytes;
+          mbar_arrive_expect_tx(
+              fb, (w.has1 ? 2u : 1u) * (kTileBytes + sb) + (uint32_t)nbox * 4096u + sb);
+          tma_load_2d(st, &tmW, fb, kb * 128, w.row0, pol_w);
+          bulk_load(sc, a.w_scales + (w.st0 * k_tiles + kt) * kMxTileBytes, sb, fb);
+          if (w.has1) {
+            tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
+            bulk_load(sc + kScaleStage, a.w_scales + (w.st1 * k_tiles + kt) * kMxTileBytes, sb, fb);
+          }
+          for (int b = 0; b < nbox; ++b)
+            tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX, fb, kb * 128, t.row0 + 32 * b, pol_x);
+          bulk_load(sc + 2 * kScaleStage,
+                    a.x_scales + ((long long)(t.row0 / 128) * k_tiles + kt) * kMxTileBytes, sb, fb);
+          ++use;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer ---
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, it = 0;
+      for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+        if (stopped(&stop_s)) break;
+        const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+        const bool has1 = weights_of<MODE>(a, t).has1;
+        if (!mbar_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
+          stop(&stop_s, a.err);
+          break;
+        }
+        tc_fence_after();
+        const int n_mma = (t.nrows + 15) & ~15;
+        bool ok = true;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(smem_u32(&full[s]), ph)) {
+            stop(&stop_s, a.err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_base + s * kStageStride;
+          const uint32_t sc = st + 3 * kTileBytes;
+          // Each slot has scale columns of its own: the MMAs that read their
+          // last contents were complete before the slot was filled again.
+          const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols;
+          const int halves = min(2, k_tiles - 2 * kb);
+          const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
+          for (int h = 0; h < halves; ++h) {
+            tmem_cp_scales(tsc + h * 12, sdesc_scales(sc + h * kMxTileBytes));
+            if (has1)
+              tmem_cp_scales(tsc + h * 12 + 4, sdesc_scales(sc + kScaleStage + h * kMxTileBytes));
+            tmem_cp_scales(tsc + h * 12 + 8, sdesc_scales(sc + 2 * kScaleStage + h * kMxTileBytes));
+          }
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint32_t idesc = idesc_mxf4(128, n_mma, (kk & 1) * 2);
+            const uint32_t col = tsc + (kk >> 1) * 12;
+            const uint64_t da0 = sdesc_kmajor<128>(st + kk * 32);
+            const uint64_t db = sdesc_kmajor<128>(st + 2 * kTileBytes + kk * 32);
+            const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
+            umma_mxf4(tmem_base, da0, db, idesc, col, col + 8, acc);
+            if (has1) {
+              const uint64_t da1 = sdesc_kmajor<128>(st + kTileBytes + kk * 32);
+              umma_mxf4(tmem_base + kBN, da1, db, idesc, col + 4, col + 8, acc);
+            }
+          }
+          umma_commit(smem_u32(&empty[s]));
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(smem_u32(tfull));
+      }
+      // Every MMA issued above has finished before the CTA tears down.
+      umma_commit(smem_u32(done));
+      if (!mbar_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ----------------------------------------------------- epilogue (2-9) ---
+    const int q = warp & 3;                    // tensor-memory lane quarter of this warp
+    const int side = (warp - kEpiWarp0) >> 2;  // takes 32-column chunks side, side + 2
+    uint32_t it = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+      if (stopped(&stop_s)) break;
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const bool has1 = weights_of<MODE>(a, t).has1;
+      int f_t[2] = {0, 0};  // down: output row of column `lane` of this warp's chunks
+      if (MODE == kDown) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = (2 * i + side) * 32 + lane;
+          if (c < t.nrows) f_t[i] = __ldg(a.sorted + t.row0 + c);
+        }
+      }
+      if (!mbar_wait(smem_u32(tfull), it & 1u)) {
+        stop(&stop_s, a.err);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int c0 = (2 * i + side) * 32;
+        if (c0 >= t.nrows) break;
+        uint32_t d0[32], d1[32];
+        tmem_ld_32x32b_x32(tb + c0, d0);
+        tmem_ld_32x32b_x32(tb + kBN + c0, d1);
+        tmem_wait_ld();
+        const int ncol = min(32, t.nrows - c0);
+        if (MODE == kGateUp) {
+          // Block (row, q) of the activation: 32 intermediates, one per lane.
+          const int blk = t.m * 4 + q;
+          const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
+          uint32_t my_scale = 0;
+          uint8_t* codes = static_cast<uint8_t*>(a.out);
+#pragma unroll
+          for (int j0 = 0; j0 < 32; j0 += 8) {
+            if (j0 >= ncol) break;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float g = __uint_as_float(d0[j0 + j]), u = __uint_as_float(d1[j0 + j]);
+              // The divide and the exponential are off by a few units of the
+              // 24th bit; the 4-bit rounding that follows keeps 2 bits.
+              const float x = __fdividef(g, 1.0f + __expf(-g)) * u;
+              const uint32_t amax =
+                  __reduce_max_sync(kAll, __float_as_uint(x) & 0x7fffffffu);
+              const uint32_t s = mx_scale_byte(amax);
+              v[j] = x * mx_inv_scale(s);
+              if (lane == j0 + j) my_scale = s;
+            }
+            // Nibble n of r: this lane's row, column j0 + n. Turn 8 columns x
+            // 32 lanes into 4 bytes (8 lanes' nibbles) of one column a lane.
+            const uint32_t r = mx_pack8(v);
+            const uint32_t o = __shfl_xor_sync(kAll, r, 1);
+            const bool odd = lane & 1;  // odd lanes take columns 4-7
+            uint32_t w = odd ? spread4(o >> 16) | (spread4(r >> 16) << 4)
+                             : spread4(r & 0xFFFFu) | (spread4(o & 0xFFFFu) << 4);
+            // w: bytes of 4 columns, lanes pair i = lane / 2; transpose 4 x 4
+            // over i & 3 (lane bits 1 and 2).
+            uint32_t p = __shfl_xor_sync(kAll, w, 2);
+            w = (lane & 2) ? __byte_perm(p, w, 0x7351) : __byte_perm(w, p, 0x6240);
+            // even i: columns 0, 2 as (own, other); odd i: columns 1, 3
+            p = __shfl_xor_sync(kAll, w, 4);
+            w = (lane & 4) ? __byte_perm(p, w, 0x7632) : __byte_perm(w, p, 0x5410);
+            const int col = j0 + (odd ? 4 : 0) + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2;
+            if (real && col < ncol)
+              *reinterpret_cast<uint32_t*>(codes + (size_t)(t.row0 + c0 + col) * (a.N / 2) +
+                                           blk * 16 + (lane >> 3) * 4) = w;
+          }
+          if (lane < ncol)
+            a.act_scales[mx_scale_offset(t.row0 + c0 + lane, blk, (a.N + 127) / 128)] =
+                real ? my_scale : 0;
+        } else if (MODE == kDown) {
+          const int h0 = t.m * 256 + q * 32 + lane;
+          float* y = static_cast<float*>(a.out);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int f = __shfl_sync(kAll, i == 0 ? f_t[0] : f_t[1], j);
+            if (j < ncol) {
+              float* row = y + (size_t)f * a.N;
+              if (h0 < a.N) row[h0] = __uint_as_float(d0[j]);
+              if (h0 + 128 < a.N) row[h0 + 128] = __uint_as_float(d1[j]);
+            }
+          }
+        } else {
+          const int n0 = t.m * 256 + q * 32 + lane;
+          const size_t base = (size_t)(t.row0 + c0) * a.N;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= ncol) break;
+            const size_t at = base + (size_t)j * a.N + n0;
+            if (a.out_fp32) {
+              float* c = static_cast<float*>(a.out);
+              if (n0 < a.N) c[at] = __uint_as_float(d0[j]);
+              if (has1 && n0 + 128 < a.N) c[at + 128] = __uint_as_float(d1[j]);
+            } else {
+              uint16_t* c = static_cast<uint16_t*>(a.out);
+              if (n0 < a.N) c[at] = f32_to_bf16_bits(__uint_as_float(d0[j]));
+              if (has1 && n0 + 128 < a.N) c[at + 128] = f32_to_bf16_bits(__uint_as_float(d1[j]));
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(tempty));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+template <int MODE>
+cudaError_t launch_mode(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& a,
+                        long long max_tiles, int num_sms, bool after_prev, cudaStream_t st) {
+  static DeviceFlags attr_done;
+  if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE>, kSmemBytes); e != cudaSuccess)
+    return e;
+  const int grid = (int)std::min<long long>(max_tiles, num_sms);
+  return launch_k(mx_gemm_kernel<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, after_prev, tmW,
+                  tmX, a);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                           const uint8_t* b_scales, int M, int N, int K, void* c, bool out_fp32,
+                           int num_sms, unsigned* err, cudaStream_t st) {
+  CUtensorMap tmW, tmX;
+  if (!make_tensor_map_codes(&tmW, b_codes, (uint64_t)N, (uint64_t)K, 128) ||
+      !make_tensor_map_codes(&tmX, a_codes, (uint64_t)M, (uint64_t)K, 32))
+    return cudaErrorInvalidValue;
+  MxGemmArgs a = {};
+  a.w_scales = b_scales;
+  a.x_scales = a_scales;
+  a.out = c;
+  a.err = err;
+  a.E = 1;
+  a.rows = M;
+  a.N = N;
+  a.K = K;
+  a.n_mtiles = (N + 255) / 256;
+  a.out_fp32 = out_fp32 ? 1 : 0;
+  const long long tiles = (long long)((M + kBN - 1) / kBN) * a.n_mtiles;
+  return launch_mode<kDense>(tmW, tmX, a, tiles, num_sms, false, st);
+}
+
+cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
+                                      const uint8_t* w, const uint8_t* w_scales,
+                                      const int32_t* offsets, const int32_t* counts, int E, int I,
+                                      int H, long long capacity, long long max_chunks,
+                                      uint8_t* act, uint8_t* act_scales, int num_sms,
+                                      unsigned* err, bool after_prev, cudaStream_t st) {
+  CUtensorMap tmW, tmX;
+  if (!make_tensor_map_codes(&tmW, w, (uint64_t)E * 2 * I, (uint64_t)H, 128) ||
+      !make_tensor_map_codes(&tmX, xs, (uint64_t)capacity, (uint64_t)H, 32))
+    return cudaErrorInvalidValue;
+  MxGemmArgs a = {};
+  a.offsets = offsets;
+  a.counts = counts;
+  a.w_scales = w_scales;
+  a.x_scales = xs_scales;
+  a.out = act;
+  a.act_scales = act_scales;
+  a.err = err;
+  a.E = E;
+  a.N = I;
+  a.K = H;
+  a.n_mtiles = (I + 127) / 128;
+  return launch_mode<kGateUp>(tmW, tmX, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
+}
+
+cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
+                                   const uint8_t* w_scales, const int32_t* sorted,
+                                   const int32_t* offsets, const int32_t* counts, int E, int H,
+                                   int I, long long capacity, long long max_chunks, float* y,
+                                   int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
+  CUtensorMap tmW, tmX;
+  if (!make_tensor_map_codes(&tmW, w, (uint64_t)E * H, (uint64_t)I, 128) ||
+      !make_tensor_map_codes(&tmX, act, (uint64_t)capacity, (uint64_t)I, 32))
+    return cudaErrorInvalidValue;
+  MxGemmArgs a = {};
+  a.sorted = sorted;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.w_scales = w_scales;
+  a.x_scales = act_scales;
+  a.out = y;
+  a.err = err;
+  a.E = E;
+  a.N = H;
+  a.K = I;
+  a.n_mtiles = (H + 255) / 256;
+  return launch_mode<kDown>(tmW, tmX, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
+}
+
+}  // namespace mm
