@@ -506,27 +506,35 @@ def _mask_ptr(mask, T: int):
     return _ptr(mask, mask.dtype, "token_mask")
 
 
-def _run(name: str, stream, tensors, made, call) -> None:
-    """call(stream handle) on the device of `tensors` (all on one), on `stream`
-    or that device's current stream. `made`: tensors allocated here, kept
-    from reuse by their own stream until a foreign stream is done with them."""
-    dev = tensors[0].device
+def _device(name: str, *tensors) -> int:
+    """The index of the one device that all tensors (None: absent) are on."""
+    di = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: all tensors must be on {dev}, got {t.device}")
-    if stream is not None:
+        if t is not None and t.get_device() != di:
+            raise ValueError(f"{name}: all tensors must be on {tensors[0].device}, got {t.device}")
+    return di
+
+
+def _launch(fn, name: str, di: int, stream, made, *args) -> None:
+    """fn(*args, stream handle) on device di, on `stream` or that device's
+    current stream. `made`: tensors allocated for this call; with a stream of
+    the caller's, the allocator keeps them until that stream is done."""
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(di)
+    else:
         s = (stream if isinstance(stream, torch.cuda.Stream)
-             else torch.cuda.ExternalStream(int(stream), device=dev))
+             else torch.cuda.ExternalStream(int(stream), device=di))
         for t in made:
-            if t.numel():
+            if t is not None and t.numel():
                 t.record_stream(s)
+        st = s.cuda_stream
+    if torch._C._cuda_getDevice() == di:
+        rc = fn(*args, st)
     else:
-        s = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        _check(call(s.cuda_stream), name)
-    else:
-        with torch.cuda.device(dev):
-            _check(call(s.cuda_stream), name)
+        with torch.cuda.device(di):
+            rc = fn(*args, st)
+    if rc != MM_OK:
+        raise MMError(rc, name)
 
 
 def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=None):
@@ -539,18 +547,19 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     dev = logits.device
     x = _ptr(logits, logits.dtype, "logits")
     mask = _mask_ptr(token_mask, T)
-    need = int(lib().mm_route_logits_workspace_size(T, E))
+    di = _device("mm_route_logits", logits, token_mask)
+    l = lib()
+    need = l.mm_route_logits_workspace_size(T, E)
     ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=dev)
     w = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     sums = torch.empty(E, dtype=torch.float32, device=dev)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
-    _run("mm_route_logits", stream, (logits, token_mask), (ids, w, counts, sums, loss, ws),
-         lambda st: lib().mm_route_logits(x, dt, mask, T, E, top_k, int(bool(renorm)),
-                                          ids.data_ptr(), w.data_ptr(), counts.data_ptr(),
-                                          sums.data_ptr(), loss.data_ptr(),
-                                          ws.data_ptr() if need > 0 else None, max(need, 0), st))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    _launch(l.mm_route_logits, "mm_route_logits", di, stream, (ids, w, counts, sums, loss, ws),
+            x, dt, mask, T, E, top_k, 1 if renorm else 0, ids.data_ptr(), w.data_ptr(),
+            counts.data_ptr(), sums.data_ptr(), loss.data_ptr(),
+            None if ws is None else ws.data_ptr(), need if need > 0 else 0)
     return ids, w, counts, sums, loss
 
 
@@ -567,15 +576,15 @@ def mm_route_logits_backward(logits, topk_ids, expert_counts, renorm: bool, d_to
     _shape(d_topk_w, (T, k), "d_topk_w")
     if d_loss is not None and d_loss.numel() != 1:
         raise ValueError("d_loss must hold one value")
+    x, mask = _ptr(logits, logits.dtype, "logits"), _mask_ptr(token_mask, T)
+    ids, counts = (_ptr(topk_ids, torch.int32, "topk_ids"),
+                   _ptr(expert_counts, torch.int32, "expert_counts"))
+    dw, dl = _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(d_loss, torch.float32, "d_loss")
+    di = _device("mm_route_logits_backward", logits, token_mask, topk_ids, expert_counts, d_topk_w,
+                 d_loss)
     grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    args = (_ptr(logits, logits.dtype, "logits"), dt, _mask_ptr(token_mask, T),
-            _ptr(topk_ids, torch.int32, "topk_ids"),
-            _ptr(expert_counts, torch.int32, "expert_counts"),
-            _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(d_loss, torch.float32, "d_loss"), T, E,
-            k, int(bool(renorm)), grad.data_ptr())
-    _run("mm_route_logits_backward", stream,
-         (logits, token_mask, topk_ids, expert_counts, d_topk_w, d_loss), (grad,),
-         lambda st: lib().mm_route_logits_backward(*args, st))
+    _launch(lib().mm_route_logits_backward, "mm_route_logits_backward", di, stream, (grad,), x, dt,
+            mask, ids, counts, dw, dl, T, E, k, 1 if renorm else 0, grad.data_ptr())
     return grad
 
 
@@ -607,12 +616,12 @@ def mm_mxfp4_quantize(x, stream=None):
     xp = _ptr(x, x.dtype, "x")
     if K % 32 != 0 or K == 0:
         raise MMError(MM_ERR_UNSUPPORTED if K else MM_ERR_INVALID_ARG, "mm_mxfp4_quantize")
+    di = _device("mm_mxfp4_quantize", x)
     codes = torch.empty((*lead, rows, K // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((*lead, *mm_mxfp4_scales_shape(rows, K)), dtype=torch.uint8,
                          device=x.device)
-    _run("mm_mxfp4_quantize", stream, (x,), (codes, scales),
-         lambda st: lib().mm_mxfp4_quantize(xp, dt, batch, rows, K, codes.data_ptr(),
-                                            scales.data_ptr(), st))
+    _launch(lib().mm_mxfp4_quantize, "mm_mxfp4_quantize", di, stream, (codes, scales), xp, dt,
+            batch, rows, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -626,10 +635,10 @@ def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
     cp, sp = _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales")
     _shape(scales, (*lead, *mm_mxfp4_scales_shape(rows, K)), "scales")
+    di = _device("mm_mxfp4_dequantize", codes, scales)
     out = torch.empty((*lead, rows, K), dtype=dtype, device=codes.device)
-    _run("mm_mxfp4_dequantize", stream, (codes, scales), (out,),
-         lambda st: lib().mm_mxfp4_dequantize(cp, sp, batch, rows, K, out.data_ptr(),
-                                              _DTYPES[dtype], st))
+    _launch(lib().mm_mxfp4_dequantize, "mm_mxfp4_dequantize", di, stream, (out,), cp, sp, batch,
+            rows, K, out.data_ptr(), _DTYPES[dtype])
     return out
 
 
@@ -652,10 +661,10 @@ def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16
         raise ValueError(f"a has {K} columns, b has {Kb}")
     if out_dtype not in _DTYPES:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    di = _device("mm_mxfp4_gemm", a_codes, a_scales, b_codes, b_scales)
     c = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
-    _run("mm_mxfp4_gemm", stream, (a_codes, a_scales, b_codes, b_scales), (c,),
-         lambda st: lib().mm_mxfp4_gemm(a, sa, b, sb, M, N, K, c.data_ptr(), _DTYPES[out_dtype],
-                                        st))
+    _launch(lib().mm_mxfp4_gemm, "mm_mxfp4_gemm", di, stream, (c,), a, sa, b, sb, M, N, K,
+            c.data_ptr(), _DTYPES[out_dtype])
     return c
 
 
@@ -681,25 +690,27 @@ def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, 
         _shape(w_gate_up, (2 * E, I, H // 2), "w_gate_up")
     _shape(w_gate_up_scales, (2 * E, *mm_mxfp4_scales_shape(I, H)), "w_gate_up_scales")
     _shape(w_down_scales, (E, *mm_mxfp4_scales_shape(H, I)), "w_down_scales")
-    args = (_ptr(hidden, torch.bfloat16, "hidden"), _ptr(topk_ids, torch.int32, "topk_ids"),
-            _ptr(topk_w, torch.float32, "topk_w"), _ptr(w_gate_up, torch.uint8, "w_gate_up"),
-            _ptr(w_gate_up_scales, torch.uint8, "w_gate_up_scales"),
-            _ptr(w_down, torch.uint8, "w_down"), _ptr(w_down_scales, torch.uint8, "w_down_scales"))
+    x, ids, w = (_ptr(hidden, torch.bfloat16, "hidden"), _ptr(topk_ids, torch.int32, "topk_ids"),
+                 _ptr(topk_w, torch.float32, "topk_w"))
+    gu, sgu = (_ptr(w_gate_up, torch.uint8, "w_gate_up"),
+               _ptr(w_gate_up_scales, torch.uint8, "w_gate_up_scales"))
+    dn, sdn = (_ptr(w_down, torch.uint8, "w_down"),
+               _ptr(w_down_scales, torch.uint8, "w_down_scales"))
+    l = lib()
     made = []
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
         made.append(out)
     _shape(out, (T, H), "out")
     if workspace is None:
-        need = mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k)
+        need = l.mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k)
         workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=hidden.device)
         made.append(workspace)
     outp, ws = _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace")
-    _run("mm_moe_experts_mxfp4", stream,
-         (hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, w_down, w_down_scales, out,
-          workspace), made,
-         lambda st: lib().mm_moe_experts_mxfp4(*args, T, H, E, I, k, outp, ws, workspace.numel(),
-                                               st))
+    di = _device("mm_moe_experts_mxfp4", hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales,
+                 w_down, w_down_scales, out, workspace)
+    _launch(l.mm_moe_experts_mxfp4, "mm_moe_experts_mxfp4", di, stream, made, x, ids, w, gu, sgu,
+            dn, sdn, T, H, E, I, k, outp, ws, workspace.numel())
     return out
 
 

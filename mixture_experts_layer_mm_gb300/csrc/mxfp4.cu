@@ -32,10 +32,32 @@ template <> struct MxIn<MM_DTYPE_FP32> { using Raw = Raw16f; static constexpr in
 template <> struct MxIn<MM_DTYPE_BF16> { using Raw = Raw16h; static constexpr int kBytes = 2; };
 template <> struct MxIn<MM_DTYPE_FP16> { using Raw = Raw16h; static constexpr int kBytes = 2; };
 
-template <int DT>
+// 32 contiguous bytes a lane in one access: a warp moves 1 KB of whole lines,
+// where two 16-byte accesses would each touch half of them. Needs 32-byte
+// alignment; the kernels' WIDE variants are taken where the caller's buffer
+// has it (rows are multiples of 64 bytes), the others use 16-byte accesses.
+__device__ __forceinline__ void load32(const unsigned char* p, uint4& a, uint4& b) {
+  asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+      : "l"(p));
+}
+__device__ __forceinline__ void store32(unsigned char* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+template <int DT, bool WIDE>
 __device__ __forceinline__ void load16(const unsigned char* p, typename MxIn<DT>::Raw& raw) {
 #pragma unroll
-  for (int i = 0; i < MxIn<DT>::kBytes; ++i) raw.r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  for (int i = 0; i < MxIn<DT>::kBytes; i += 2) {
+    if constexpr (WIDE) {
+      load32(p + 16 * i, raw.r[i], raw.r[i + 1]);
+    } else {
+      raw.r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      raw.r[i + 1] = __ldg(reinterpret_cast<const uint4*>(p) + i + 1);
+    }
+  }
 }
 
 template <int DT>
@@ -99,7 +121,7 @@ __device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t& scales
 // [16 * lane, 16 * lane + 16) of every span of 16 << lanes_log2. Columns at or
 // past K of the last scale tile give zero scale bytes and no codes. src NULL:
 // a padding row (zero scale bytes only). All lanes of the warp call this.
-template <int DT, int U>
+template <int DT, bool WIDE, int U>
 __device__ __forceinline__ void quantize_row(const unsigned char* src, int K, int lanes_log2,
                                              uint8_t* codes, uint8_t* scale_row, bool active) {
   const int lane = threadIdx.x & ((1 << lanes_log2) - 1);
@@ -111,7 +133,7 @@ __device__ __forceinline__ void quantize_row(const unsigned char* src, int K, in
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * span;
       if (src != nullptr && c < K)
-        load16<DT>(src + (size_t)c * MxIn<DT>::kBytes, raw[u]);
+        load16<DT, WIDE>(src + (size_t)c * MxIn<DT>::kBytes, raw[u]);
       else
         zero16<DT>(raw[u]);
     }
@@ -137,22 +159,26 @@ __host__ __device__ __forceinline__ int row_lanes_log2(int K) {
   return K > 256 ? 5 : K > 128 ? 4 : 3;
 }
 
-template <int DT>
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const unsigned char* __restrict__ x,
                                                                  long long prows, int rows, int rp,
                                                                  int K, int lanes_log2,
                                                                  uint8_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales) {
   const int per_warp = 32 >> lanes_log2;
-  const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
-                        ((threadIdx.x & 31) >> lanes_log2);
+  // Consecutive warps take rows r, r + 32, r + 64, r + 96 of a 128-row tile,
+  // then r + 1: the rows whose scale bytes share a 32-byte sector of the tile
+  // are written close together.
+  const long long i = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
+                      ((threadIdx.x & 31) >> lanes_log2);
+  const long long row = (i & ~127LL) + (i & 3) * 32 + (i & 127) / 4;
   const bool active = row < prows;
   const long long b = active ? row / rp : 0;
   const int r = active ? (int)(row - b * rp) : 0;
   const bool real = active && r < rows;
   const int kt = (int)mx_tiles(K);
   const size_t at = (size_t)(b * rows + r) * K;
-  quantize_row<DT, 4>(real ? x + at * MxIn<DT>::kBytes : nullptr, K, lanes_log2, codes + at / 2,
+  quantize_row<DT, WIDE, 4>(real ? x + at * MxIn<DT>::kBytes : nullptr, K, lanes_log2, codes + at / 2,
                       scales + (size_t)b * (rp / kMxTile) * kt * kMxTileBytes +
                           mx_scale_offset(r, 0, kt),
                       active);
@@ -173,11 +199,51 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
 }
 
-// One lane: 16 columns (8 code bytes, one scale byte) of one row.
-template <int DT>
+// The 16 values of 8 code bytes under scale s, written as DT at dst.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void decode16(uint2 code, float s, unsigned char* dst) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = decode2(((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xffu);
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+  uint32_t w[16];
+  if constexpr (DT == MM_DTYPE_FP32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (DT == MM_DTYPE_BF16) {
+        w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MxIn<DT>::kBytes; i += 2) {
+    const uint4 lo = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    const uint4 hi = make_uint4(w[4 * i + 4], w[4 * i + 5], w[4 * i + 6], w[4 * i + 7]);
+    if constexpr (WIDE) {
+      store32(dst + 16 * i, lo, hi);
+    } else {
+      reinterpret_cast<uint4*>(dst)[i] = lo;
+      reinterpret_cast<uint4*>(dst)[i + 1] = hi;
+    }
+  }
+}
+
+// One lane: 16 columns (8 code bytes, one scale byte) of one row, kU spans of
+// the row loaded before any is written.
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long nrows, int rows,
     int K, int lanes_log2, unsigned char* __restrict__ out) {
+  constexpr int kU = 4;
   const int per_warp = 32 >> lanes_log2;
   const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
                         ((threadIdx.x & 31) >> lanes_log2);
@@ -185,40 +251,25 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
   const int lane = threadIdx.x & ((1 << lanes_log2) - 1);
   const long long b = row / rows;
   const int r = (int)(row - b * rows);
-  const int kt = (int)mx_tiles(K);
+  const int kt = (int)mx_tiles(K), span = 16 << lanes_log2;
   const uint8_t* srow =
       scales + (size_t)b * mx_tiles(rows) * kt * kMxTileBytes + mx_scale_offset(r, 0, kt);
-#pragma unroll 4
-  for (int c = lane * 16; c < K; c += 16 << lanes_log2) {
-    const uint2 code = __ldg(reinterpret_cast<const uint2*>(codes + ((size_t)row * K + c) / 2));
-    const float s =
-        mx_scale(__ldg(srow + (size_t)(c / kMxTile) * kMxTileBytes + (c / kMxBlock) % 4));
-    float v[16];
+  const size_t at = (size_t)row * K;
+  for (int c0 = lane * 16; c0 < K; c0 += kU * span) {
+    uint2 code[kU];
+    uint32_t s[kU];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = decode2(((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xffu);
-      v[2 * i] = f.x * s;
-      v[2 * i + 1] = f.y * s;
-    }
-    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)row * K + c) * MxIn<DT>::kBytes);
-    if constexpr (DT == MM_DTYPE_FP32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dst[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (DT == MM_DTYPE_BF16) {
-          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        } else {
-          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+    for (int u = 0; u < kU; ++u) {
+      const int c = c0 + u * span;
+      if (c < K) {
+        code[u] = __ldg(reinterpret_cast<const uint2*>(codes + (at + c) / 2));
+        s[u] = __ldg(srow + (size_t)(c / kMxTile) * kMxTileBytes + (c / kMxBlock) % 4);
       }
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int c = c0 + u * span;
+      if (c < K) decode16<DT, WIDE>(code[u], mx_scale(s[u]), out + (at + c) * MxIn<DT>::kBytes);
     }
   }
 }
@@ -239,7 +290,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_gather_quantize_kernel(
   for (int r = blockIdx.x * kMxWarps + (threadIdx.x >> 5); r < rows; r += step) {
     const int f = __ldg(sorted + r);
     if (f >= Tk) continue;
-    quantize_row<MM_DTYPE_BF16, 4>(hidden + (size_t)(f / top_k) * H * 2, H, 5,
+    quantize_row<MM_DTYPE_BF16, false, 4>(hidden + (size_t)(f / top_k) * H * 2, H, 5,
                                    codes + (size_t)r * (H / 2), scales + mx_scale_offset(r, 0, kt),
                                    true);
   }
@@ -277,21 +328,38 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
 
 }  // namespace
 
+namespace {
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+template <int DT>
+cudaError_t quantize_t(const unsigned char* x, long long prows, int rows, int rp, int K, int ll,
+                       uint8_t* codes, uint8_t* scales, dim3 grid, cudaStream_t st) {
+  return launch_k(aligned32(x) ? mx_quantize_kernel<DT, true> : mx_quantize_kernel<DT, false>, grid,
+                  dim3(kMxThreads), 0, st, false, x, prows, rows, rp, K, ll, codes, scales);
+}
+
+template <int DT>
+cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, long long nrows, int rows,
+                         int K, int ll, unsigned char* out, dim3 grid, cudaStream_t st) {
+  return launch_k(aligned32(out) ? mx_dequantize_kernel<DT, true> : mx_dequantize_kernel<DT, false>,
+                  grid, dim3(kMxThreads), 0, st, false, codes, scales, nrows, rows, K, ll, out);
+}
+
+}  // namespace
+
 cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int rows, int K,
                                uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   const int rp = (int)(mx_tiles(rows) * kMxTile), ll = row_lanes_log2(K);
   const long long prows = batch * rp;
   const long long per_block = (long long)kMxWarps * (32 >> ll);
-  const dim3 grid((unsigned)((prows + per_block - 1) / per_block)), block(kMxThreads);
+  const dim3 grid((unsigned)((prows + per_block - 1) / per_block));
   const unsigned char* p = static_cast<const unsigned char*>(x);
   if (dtype == MM_DTYPE_FP32)
-    return launch_k(mx_quantize_kernel<MM_DTYPE_FP32>, grid, block, 0, st, false, p, prows, rows, rp,
-                    K, ll, codes, scales);
+    return quantize_t<MM_DTYPE_FP32>(p, prows, rows, rp, K, ll, codes, scales, grid, st);
   if (dtype == MM_DTYPE_BF16)
-    return launch_k(mx_quantize_kernel<MM_DTYPE_BF16>, grid, block, 0, st, false, p, prows, rows, rp,
-                    K, ll, codes, scales);
-  return launch_k(mx_quantize_kernel<MM_DTYPE_FP16>, grid, block, 0, st, false, p, prows, rows, rp,
-                  K, ll, codes, scales);
+    return quantize_t<MM_DTYPE_BF16>(p, prows, rows, rp, K, ll, codes, scales, grid, st);
+  return quantize_t<MM_DTYPE_FP16>(p, prows, rows, rp, K, ll, codes, scales, grid, st);
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long batch,
@@ -299,16 +367,13 @@ cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, lo
   const int ll = row_lanes_log2(K);
   const long long nrows = batch * rows;
   const long long per_block = (long long)kMxWarps * (32 >> ll);
-  const dim3 grid((unsigned)((nrows + per_block - 1) / per_block)), block(kMxThreads);
+  const dim3 grid((unsigned)((nrows + per_block - 1) / per_block));
   unsigned char* p = static_cast<unsigned char*>(out);
   if (dtype == MM_DTYPE_FP32)
-    return launch_k(mx_dequantize_kernel<MM_DTYPE_FP32>, grid, block, 0, st, false, codes, scales,
-                    nrows, rows, K, ll, p);
+    return dequantize_t<MM_DTYPE_FP32>(codes, scales, nrows, rows, K, ll, p, grid, st);
   if (dtype == MM_DTYPE_BF16)
-    return launch_k(mx_dequantize_kernel<MM_DTYPE_BF16>, grid, block, 0, st, false, codes, scales,
-                    nrows, rows, K, ll, p);
-  return launch_k(mx_dequantize_kernel<MM_DTYPE_FP16>, grid, block, 0, st, false, codes, scales,
-                  nrows, rows, K, ll, p);
+    return dequantize_t<MM_DTYPE_BF16>(codes, scales, nrows, rows, K, ll, p, grid, st);
+  return dequantize_t<MM_DTYPE_FP16>(codes, scales, nrows, rows, K, ll, p, grid, st);
 }
 
 cudaError_t launch_mx_gather_quantize(const uint16_t* hidden, const int32_t* sorted,

@@ -15,8 +15,8 @@
 // The two terms are formed separately: their own differences cancel, their
 // sum does not.
 //
-// One warp takes one token; lane l holds experts l, l + 32, ... Both passes
-// read each logit once. The sums over tokens stay in the lane that owns the
+// One warp takes one token; lane l holds the Q = 1, 2, 4 or 8 consecutive
+// experts from l Q on (one vector load). Both passes read each logit once. The sums over tokens stay in the lane that owns the
 // expert, then go block by block through the caller's workspace in a fixed
 // order, so every output is the same on every call.
 #include <math.h>
@@ -29,6 +29,10 @@ namespace {
 
 constexpr int kRlThreads = 512;
 constexpr int kRlWarps = kRlThreads / 32;
+// One block does a batch of up to kRlOneBlockTokens alone (one launch, no
+// workspace).
+constexpr int kRlOneBlockWarps = 32;
+constexpr int kRlOneBlockTokens = 128;
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
@@ -38,86 +42,242 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) {
 __device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(uint16_t* p, float v) { *p = f32_to_bf16_bits(v); }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Q consecutive values as one access (p aligned to its size, at most 16 bytes
+// an access).
+template <int Q>
+__device__ __forceinline__ void load_vec(const float* p, float (&l)[Q]) {
+  if constexpr (Q == 1) {
+    l[0] = __ldg(p);
+  } else if constexpr (Q == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    l[0] = v.x;
+    l[1] = v.y;
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-  return v;
+    for (int i = 0; i < Q / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+      l[4 * i] = v.x;
+      l[4 * i + 1] = v.y;
+      l[4 * i + 2] = v.z;
+      l[4 * i + 3] = v.w;
+    }
+  }
 }
+template <int Q>
+__device__ __forceinline__ void load_vec(const uint16_t* p, float (&l)[Q]) {
+  uint32_t w[(Q + 1) / 2];
+  if constexpr (Q == 1) w[0] = __ldg(p);
+  if constexpr (Q == 2) w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  if constexpr (Q == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+  if constexpr (Q == 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    l[q] = __uint_as_float((q & 1) ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16);
+}
+template <int Q>
+__device__ __forceinline__ void store_vec(float* p, const float (&g)[Q]) {
+  if constexpr (Q == 1) *p = g[0];
+  if constexpr (Q == 2) *reinterpret_cast<float2*>(p) = make_float2(g[0], g[1]);
+  if constexpr (Q >= 4) {
+#pragma unroll
+    for (int i = 0; i < Q / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] =
+          make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+  }
+}
+template <int Q>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float (&g)[Q]) {
+  if constexpr (Q == 1) {
+    *p = f32_to_bf16_bits(g[0]);
+  } else {
+    uint32_t w[Q / 2];
+#pragma unroll
+    for (int i = 0; i < Q / 2; ++i)
+      w[i] = (uint32_t)f32_to_bf16_bits(g[2 * i]) | ((uint32_t)f32_to_bf16_bits(g[2 * i + 1]) << 16);
+    if constexpr (Q == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+    if constexpr (Q == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    if constexpr (Q == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
   return v;
 }
 
-// Logits of token t in l[q] (expert lane + 32 q), -INFINITY past E.
+// Logits of token t: l[q] of expert lane Q + q, -INFINITY past E. vec: rows
+// begin at multiples of Q values and E is one, so a lane's values are all in
+// or all out and aligned.
 template <int Q, typename TL>
-__device__ __forceinline__ void load_row(const TL* __restrict__ logits, uint32_t t, int E,
+__device__ __forceinline__ void load_row(const TL* __restrict__ logits, uint32_t t, int E, bool vec,
                                          float (&l)[Q]) {
-  const int lane = threadIdx.x & 31;
-  const TL* row = logits + (size_t)t * E + lane;
+  const int e0 = (threadIdx.x & 31) * Q;
+  const TL* row = logits + (size_t)t * E + e0;
+  if (vec) {
+    if (e0 < E) {
+      load_vec<Q>(row, l);
+    } else {
 #pragma unroll
-  for (int q = 0; q < Q; ++q) l[q] = lane + 32 * q < E ? load_logit(row + 32 * q) : -INFINITY;
+      for (int q = 0; q < Q; ++q) l[q] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = e0 + q < E ? load_logit(row + q) : -INFINITY;
+  }
 }
 
-// p = softmax(l). False (and p = 0) for a row without a logit above -inf.
-template <int Q>
-__device__ __forceinline__ bool softmax_row(const float (&l)[Q], float (&p)[Q]) {
-  float m = -INFINITY;
+template <int Q, typename TL>
+__device__ __forceinline__ void store_row(TL* row, int E, bool vec, const float (&g)[Q]) {
+  const int e0 = (threadIdx.x & 31) * Q;
+  if (vec) {
+    if (e0 < E) store_vec<Q>(row + e0, g);
+  } else {
 #pragma unroll
-  for (int q = 0; q < Q; ++q) m = fmaxf(m, l[q]);
-  m = warp_max(m);
-  bool any = true;
-  if (m == -INFINITY) {  // all -inf: no expert; a NaN among them: the row's p are NaN
+    for (int q = 0; q < Q; ++q)
+      if (e0 + q < E) store_grad(row + e0 + q, g[q]);
+  }
+}
+
+// Sum of v over the lanes below this one.
+__device__ __forceinline__ int exclusive_sum(int v) {
+  const int lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kFullMask, incl, o);
+    if (lane >= o) incl += u;
+  }
+  return incl - v;
+}
+
+// Maximum over the warp; no input is a NaN.
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// e^x for x <= 0 (or NaN): 2^t with t = x log2(e) in two parts, the second the
+// rounding of the first product, so that the error stays at that of the
+// hardware's 2^t (2^-22) for any x. Below 2^-126: 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  const float t = x * kLog2e;
+  const float rest = x > -200.f ? __fmaf_rn(x, kLog2e, -t) : 0.f;
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return __fmaf_rn(r, rest * kLn2, r);
+}
+
+// p = exp(l - m) (not yet divided by the returned sum), m the row's largest
+// logit that is not a NaN. A row without a logit above -inf has p = 0 and
+// sum 0; one that holds a NaN or +inf has a NaN sum.
+template <int Q>
+__device__ __forceinline__ float exp_row(const float (&l)[Q], float m, float (&p)[Q]) {
+  if (m == -INFINITY) {  // all -inf; or NaN among them
     bool nan = false;
 #pragma unroll
     for (int q = 0; q < Q; ++q) nan |= l[q] != l[q];
-    any = __any_sync(kFullMask, nan);
+    nan = __any_sync(kFullMask, nan);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) p[q] = 0.f;
+    return nan ? __uint_as_float(0x7fffffffu) : 0.f;
   }
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    p[q] = any ? expf(l[q] - m) : 0.f;  // exp(-inf) = 0 past E
+    p[q] = exp_neg(l[q] - m);  // 0 past E
     s += p[q];
   }
-  s = warp_sum(s);
-  const float inv = any ? 1.f / s : 0.f;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) p[q] *= inv;
-  return any;
+  return warp_sum(s);
 }
 
-// The top_k largest of l as a bit set over q (bit q: expert lane + 32 q). A
-// logit is compared as an order-preserving uint32 (-0 folded into +0), so
-// one warp-wide maximum finds the value and one minimum the lowest id.
+// Descending order of Q values (compare-exchange networks of 1, 5 and 19
+// steps; values only, no index travels with them).
+__device__ __forceinline__ void order2(float& a, float& b) {
+  const float hi = fmaxf(a, b);
+  b = fminf(a, b);
+  a = hi;
+}
 template <int Q>
-__device__ __forceinline__ uint32_t select_topk(const float (&l)[Q], int E, int top_k) {
-  const int lane = threadIdx.x & 31;
-  uint32_t key[Q], sel = 0;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const uint32_t b = __float_as_uint(l[q] + 0.0f);
-    key[q] = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    if (lane + 32 * q >= E) key[q] = 0;  // below every logit (-inf maps to 0x007fffff)
-    else if (key[q] == 0) key[q] = 1;    // a NaN with the lowest pattern
+__device__ __forceinline__ void sort_desc(float (&v)[Q]) {
+  static_assert(Q == 1 || Q == 2 || Q == 4 || Q == 8, "networks below");
+  if constexpr (Q == 2) order2(v[0], v[1]);
+  if constexpr (Q == 4) {
+    order2(v[0], v[1]); order2(v[2], v[3]);
+    order2(v[0], v[2]); order2(v[1], v[3]);
+    order2(v[1], v[2]);
   }
-  for (int r = 0; r < top_k; ++r) {
-    uint32_t best = 0;
-    int bq = 0;
+  if constexpr (Q == 8) {
+    order2(v[0], v[1]); order2(v[2], v[3]); order2(v[4], v[5]); order2(v[6], v[7]);
+    order2(v[0], v[2]); order2(v[1], v[3]); order2(v[4], v[6]); order2(v[5], v[7]);
+    order2(v[1], v[2]); order2(v[5], v[6]); order2(v[0], v[4]); order2(v[3], v[7]);
+    order2(v[1], v[5]); order2(v[2], v[6]);
+    order2(v[1], v[4]); order2(v[3], v[6]);
+    order2(v[2], v[4]); order2(v[3], v[5]);
+    order2(v[3], v[4]);
+  }
+}
+
+// The top_k largest of the row: bit q of the returned word for expert
+// lane Q + q. Every lane sorts its values; then the warp takes the largest
+// head, drops it from every lane that shows it, and so on until top_k values
+// are gone: that head is the top_k-th largest value, and what is at or above
+// it is the selection. Only when more values equal it than have room (or it
+// is -inf, which NaN and the lanes past E rank as) do the ids decide: the
+// lowest stay. m: the largest value.
+template <int Q>
+__device__ __forceinline__ uint32_t select_topk(const float (&l)[Q], int E, int top_k, float& m) {
+  const int lane = threadIdx.x & 31;
+  float v[Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q)  // strict '>' keeps the lower id of this lane
-      if (key[q] > best) {
-        best = key[q];
-        bq = q;
-      }
-    const uint32_t top = __reduce_max_sync(kFullMask, best);
-    const uint32_t id = best == top ? (uint32_t)(bq * 32 + lane) : 0xffffffffu;
-    const uint32_t win = __reduce_min_sync(kFullMask, id);
-    if (win == id) {
-      sel |= 1u << bq;
+  for (int q = 0; q < Q; ++q) v[q] = fmaxf(l[q], -INFINITY);  // a NaN ranks as -inf
+  sort_desc<Q>(v);
+  float top = redux_max(v[0]);
+  m = top;
+  int left = top_k;
+  while (true) {
+    const bool here = v[0] == top;
+    left -= __popc(__ballot_sync(kFullMask, here));
+    if (left <= 0) break;
+    if (here) {
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (q == bq) key[q] = 0;  // taken
+      for (int q = 0; q + 1 < Q; ++q) v[q] = v[q + 1];
+      v[Q - 1] = -INFINITY;
     }
+    top = redux_max(v[0]);
+  }
+  uint32_t sel = 0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (l[q] >= top) sel |= 1u << q;
+  const uint32_t total = __reduce_add_sync(kFullMask, (uint32_t)__popc(sel));
+  if (total != (uint32_t)top_k) {
+    uint32_t above = 0, equal = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (l[q] > top) above |= 1u << q;
+      if (fmaxf(l[q], -INFINITY) == top && lane * Q + q < E) equal |= 1u << q;
+    }
+    int room = top_k - (int)__reduce_add_sync(kFullMask, (uint32_t)__popc(above));
+    room -= exclusive_sum(__popc(equal));
+    for (; room > 0 && equal != 0; --room) {
+      const uint32_t low = equal & (0u - equal);
+      above |= low;
+      equal ^= low;
+    }
+    sel = above;
   }
   return sel;
 }
@@ -131,67 +291,51 @@ struct RouteLogitsArgs {
   int32_t* counts;   // [E]
   float* prob_sums;  // [E]
   float* loss;       // [1]
-  int T, E, top_k, renorm;
+  int T, E, top_k, renorm, vec;
 };
 
-// Sums over the rows of part_p / part_c in order, then the outputs over the
-// whole batch. One block of kRlThreads; red: [kRlThreads] floats, redi ints.
+// The outputs over the whole batch from its sums, thread e < EP holding
+// expert e's p and c. red, redi: [EP] shared each, free to overwrite. All
+// threads of the block call this (it has barriers).
 template <int EP>
-__device__ __forceinline__ void finish_batch(const float* part_p, const int32_t* part_c, int rows,
-                                             const RouteLogitsArgs& a, float* red, int* redi) {
-  constexpr int G = kRlThreads / EP;  // EP <= 256
-  const int e = threadIdx.x % EP, g = threadIdx.x / EP;
-  float p = 0.f;
-  int c = 0;
-#pragma unroll 8
-  for (int r = g; r < rows; r += G) {
-    p += part_p[(size_t)r * EP + e];
-    c += part_c[(size_t)r * EP + e];
-  }
-  red[threadIdx.x] = p;
-  redi[threadIdx.x] = c;
-  __syncthreads();
-  if (g == 0) {
-    for (int i = 1; i < G; ++i) {
-      p += red[i * EP + e];
-      c += redi[i * EP + e];
-    }
+__device__ __forceinline__ void write_batch(float p, int c, const RouteLogitsArgs& a, float* red,
+                                            int* redi) {
+  const int e = threadIdx.x;
+  if (e < EP) {
     if (e < a.E) {
       a.prob_sums[e] = p;
       a.counts[e] = c;
     }
-  }
-  __syncthreads();
-  // sum_e counts = n k, and the loss (float products summed in a fixed tree).
-  if (g == 0) {
     red[e] = e < a.E ? (float)c * p : 0.f;
     redi[e] = e < a.E ? c : 0;
   }
   __syncthreads();
 #pragma unroll
   for (int o = EP / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) {
-      red[threadIdx.x] += red[threadIdx.x + o];
-      redi[threadIdx.x] += redi[threadIdx.x + o];
+    if (e < o) {
+      red[e] += red[e + o];
+      redi[e] += redi[e + o];
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
+  if (e == 0) {  // sum_e counts = n k
     const float nk = (float)redi[0], n = nk / (float)a.top_k;
     *a.loss = redi[0] > 0 ? (float)a.E * (red[0] / nk) / n : 0.f;
   }
 }
 
-template <int EP, typename TL>
-__global__ void __launch_bounds__(kRlThreads) route_logits_kernel(const TL* __restrict__ logits,
-                                                                  const RouteLogitsArgs a) {
+template <int EP, int W, typename TL>
+__global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restrict__ logits,
+                                                              const RouteLogitsArgs a) {
   constexpr int Q = EP / 32;
-  __shared__ float sp[kRlWarps * EP > kRlThreads ? kRlWarps * EP : kRlThreads];
-  __shared__ int sc[kRlWarps * EP > kRlThreads ? kRlWarps * EP : kRlThreads];
+  __shared__ float sp[W * EP];
+  __shared__ int sc[EP];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t stride = gridDim.x * kRlWarps, T = (uint32_t)a.T;  // t + stride < 2^32
+  const uint32_t stride = gridDim.x * W, T = (uint32_t)a.T;  // t + stride < 2^32
   pdl_wait();
   pdl_trigger();
+  if (threadIdx.x < EP) sc[threadIdx.x] = 0;
+  __syncthreads();
   float psum[Q];
   int cnt[Q];
 #pragma unroll
@@ -200,57 +344,58 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_kernel(const TL* __re
     cnt[q] = 0;
   }
   float next[Q];
-  uint32_t t = blockIdx.x * kRlWarps + warp;
-  if (t < T) load_row<Q>(logits, t, a.E, next);
+  uint32_t t = blockIdx.x * W + warp;
+  if (t < T) load_row<Q>(logits, t, a.E, a.vec, next);
   for (; t < T; t += stride) {
     float l[Q], p[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) l[q] = next[q];
-    if (t + stride < T) load_row<Q>(logits, t + stride, a.E, next);
-    const bool valid = softmax_row<Q>(l, p) && (a.mask == nullptr || a.mask[t] != 0);
-    const uint32_t sel = select_topk<Q>(l, a.E, a.top_k);
-    float total = 0.f;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if ((sel >> q) & 1u) total += p[q];
-    total = warp_sum(total);
-    const float scale = !valid ? 0.f : a.renorm ? 1.f / total : 1.f;
+    if (t + stride < T) load_row<Q>(logits, t + stride, a.E, a.vec, next);
+    float m;
+    const uint32_t sel = select_topk<Q>(l, a.E, a.top_k, m);
+    const float sum = exp_row<Q>(l, m, p);
+    const bool valid = sum != 0.f && (a.mask == nullptr || a.mask[t] != 0);
+    // Weights of the selected: p / sum, or p over the selected p alone.
+    float scale = 0.f;
     if (valid) {
+      const float inv = 1.f / sum;
+      scale = inv;
+      if (a.renorm) {
+        float total = 0.f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          if ((sel >> q) & 1u) total += p[q];
+        total = warp_sum(total);
+        scale = sum == sum ? 1.f / total : sum;  // a NaN in the row: all its weights
+      }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        psum[q] += p[q];
-        cnt[q] += (int)((sel >> q) & 1u);
+        psum[q] += p[q] * inv;
+        if ((sel >> q) & 1u) ++cnt[q];
       }
     }
     // Ascending ids: slot = number of selected experts with a lower id.
-    const uint32_t lt = (1u << lane) - 1u;
-    int base = 0;
+    size_t at = (size_t)t * a.top_k + exclusive_sum(__popc(sel));
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const bool mine = (sel >> q) & 1u;
-      const uint32_t bal = __ballot_sync(kFullMask, mine);
-      if (mine) {
-        const size_t at = (size_t)t * a.top_k + base + __popc(bal & lt);
-        a.ids[at] = lane + 32 * q;
+    for (int q = 0; q < Q; ++q)
+      if ((sel >> q) & 1u) {
+        a.ids[at] = lane * Q + q;
         a.w[at] = valid ? p[q] * scale : 0.f;
+        ++at;
       }
-      base += __popc(bal);
-    }
   }
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    sp[warp * EP + lane + 32 * q] = psum[q];
-    sc[warp * EP + lane + 32 * q] = cnt[q];
+    sp[warp * EP + lane * Q + q] = psum[q];
+    if (cnt[q] != 0) atomicAdd(&sc[lane * Q + q], cnt[q]);  // integers: any order
   }
   __syncthreads();
   float p = 0.f;
   int c = 0;
   if (threadIdx.x < EP) {
 #pragma unroll
-    for (int w = 0; w < kRlWarps; ++w) {
-      p += sp[w * EP + threadIdx.x];
-      c += sc[w * EP + threadIdx.x];
-    }
+    for (int w = 0; w < W; ++w) p += sp[w * EP + threadIdx.x];
+    c = sc[threadIdx.x];
   }
   if (gridDim.x > 1) {
     if (threadIdx.x < EP) {
@@ -260,23 +405,48 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_kernel(const TL* __re
     return;
   }
   __syncthreads();
-  __shared__ float one_p[EP];
-  __shared__ int one_c[EP];
-  if (threadIdx.x < EP) {
-    one_p[threadIdx.x] = p;
-    one_c[threadIdx.x] = c;
-  }
-  __syncthreads();
-  finish_batch<EP>(one_p, one_c, 1, a, sp, sc);
+  write_batch<EP>(p, c, a, sp, sc);
 }
 
+// The blocks' sums, added in block order: EP / 4 threads a row take 4 experts
+// each, kRlFinish / (EP / 4) rows at a time.
+constexpr int kRlFinish = 1024;
+
 template <int EP>
-__global__ void __launch_bounds__(kRlThreads) route_logits_finish_kernel(int rows,
-                                                                         const RouteLogitsArgs a) {
-  __shared__ float red[kRlThreads];
-  __shared__ int redi[kRlThreads];
+__global__ void __launch_bounds__(kRlFinish) route_logits_finish_kernel(int rows,
+                                                                        const RouteLogitsArgs a) {
+  constexpr int C = EP / 4, G = kRlFinish / C;
+  __shared__ float4 ps[G][C];
+  __shared__ int4 cs[G][C];
+  const int c4 = threadIdx.x % C, g = threadIdx.x / C;
   pdl_wait();
-  finish_batch<EP>(a.part_p, a.part_c, rows, a, red, redi);
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  int4 c = make_int4(0, 0, 0, 0);
+  const float4* pp = reinterpret_cast<const float4*>(a.part_p) + c4;
+  const int4* pc = reinterpret_cast<const int4*>(a.part_c) + c4;
+#pragma unroll 8
+  for (int r = g; r < rows; r += G) {
+    const float4 u = pp[(size_t)r * C];
+    const int4 v = pc[(size_t)r * C];
+    p.x += u.x; p.y += u.y; p.z += u.z; p.w += u.w;
+    c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+  }
+  ps[g][c4] = p;
+  cs[g][c4] = c;
+  __syncthreads();
+  float* pf = reinterpret_cast<float*>(ps);  // [G][EP]
+  int* ci = reinterpret_cast<int*>(cs);
+  float sum = 0.f;
+  int cnt = 0;
+  if (threadIdx.x < EP) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      sum += pf[i * EP + threadIdx.x];
+      cnt += ci[i * EP + threadIdx.x];
+    }
+  }
+  __syncthreads();
+  write_batch<EP>(sum, cnt, a, pf, ci);
 }
 
 struct RouteLogitsBwdArgs {
@@ -285,13 +455,14 @@ struct RouteLogitsBwdArgs {
   const int32_t* counts;
   const float* dw;     // NULL: no gradient of the weights
   const float* dloss;  // NULL: no gradient of the loss
-  int T, E, top_k, renorm;
+  int T, E, top_k, renorm, vec;
 };
 
 template <int EP, typename TL>
 __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
     const TL* __restrict__ logits, TL* __restrict__ grad, const RouteLogitsBwdArgs a) {
   constexpr int Q = EP / 32;
+  __shared__ float c_s[EP];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t stride = gridDim.x * kRlWarps, T = (uint32_t)a.T;  // t + stride < 2^32
   pdl_wait();
@@ -302,86 +473,94 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
     float tot = 0.f;  // exact below 2^24, else off by 2^-24: far below the gradient's rounding
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      c[q] = lane + 32 * q < a.E ? (float)__ldg(a.counts + lane + 32 * q) : 0.f;
+      c[q] = lane * Q + q < a.E ? (float)__ldg(a.counts + lane * Q + q) : 0.f;
       tot += c[q];
     }
     tot = warp_sum(tot);
     const float g = a.dloss != nullptr ? __ldg(a.dloss) : 0.f;
     const float f = tot > 0.f ? g * (float)a.E / tot * ((float)a.top_k / tot) : 0.f;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) c[q] *= f;
+    for (int q = 0; q < Q; ++q) {
+      c[q] *= f;
+      if (warp == 0) c_s[lane * Q + q] = c[q];
+    }
   }
+  __syncthreads();
   float next[Q];
   uint32_t t = blockIdx.x * kRlWarps + warp;
-  if (t < T) load_row<Q>(logits, t, a.E, next);
+  if (t < T) load_row<Q>(logits, t, a.E, a.vec, next);
   for (; t < T; t += stride) {
     float l[Q], p[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) l[q] = next[q];
-    if (t + stride < T) load_row<Q>(logits, t + stride, a.E, next);
-    const bool valid = softmax_row<Q>(l, p) && (a.mask == nullptr || a.mask[t] != 0);
-    // dw and the selection, moved to the lanes that own the experts. An id
-    // outside [0, E) or repeated takes no (further) part.
-    float d[Q];
-    uint32_t sel = 0;
+    if (t + stride < T) load_row<Q>(logits, t + stride, a.E, a.vec, next);
+    float m = l[0];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) d[q] = 0.f;
-    if (a.dw != nullptr) {
-      int id = -1;
-      float dwj = 0.f;
-      if (lane < a.top_k) {
-        id = __ldg(a.ids + (size_t)t * a.top_k + lane);
-        dwj = __ldg(a.dw + (size_t)t * a.top_k + lane);
-      }
-      for (int j = 0; j < a.top_k; ++j) {
-        const int e = __shfl_sync(kFullMask, id, j);
-        const float v = __shfl_sync(kFullMask, dwj, j);
+    for (int q = 1; q < Q; ++q) m = fmaxf(m, l[q]);
+    m = redux_max(fmaxf(m, -INFINITY));
+    const float sum = exp_row<Q>(l, m, p);
+    const bool valid = sum != 0.f && (a.mask == nullptr || a.mask[t] != 0);
+    TL* row = grad + (size_t)t * a.E;
+    if (!valid) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-          if (e == lane + 32 * q && e < a.E && !((sel >> q) & 1u)) {
-            sel |= 1u << q;
-            d[q] = v;
-          }
-      }
+      for (int q = 0; q < Q; ++q) p[q] = 0.f;
+      store_row<Q>(row, a.E, a.vec, p);
+      continue;
     }
-    float tot = 0.f, pd = 0.f, pc = 0.f;
+    const float inv = 1.f / sum;
+    float pc = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      if ((sel >> q) & 1u) {
-        tot += p[q];
-        pd += p[q] * d[q];
-      }
+      p[q] *= inv;
       pc += p[q] * c[q];
     }
     pc = warp_sum(pc);
+    // The selected experts, one a lane: lane j < k forms p at its id anew (the
+    // same operations on the same logit). An id outside [0, E) or repeated
+    // within the row takes no part.
+    int id = -1;
+    float pj = 0.f, dj = 0.f, sel_term = 0.f, mean = 0.f;
     if (a.dw != nullptr) {
-      pd = warp_sum(pd);
-      if (a.renorm) tot = warp_sum(tot);
+      if (lane < a.top_k) {
+        id = __ldg(a.ids + (size_t)t * a.top_k + lane);
+        dj = __ldg(a.dw + (size_t)t * a.top_k + lane);
+      }
+      const uint32_t same = __match_any_sync(kFullMask, id);
+      if (id < 0 || id >= a.E || (same & ((1u << lane) - 1u)) != 0) {
+        id = -1;
+        dj = 0.f;
+      }
+      if (id >= 0) pj = exp_neg(load_logit(logits + (size_t)t * a.E + id) - m) * inv;
+      mean = warp_sum(pj * dj);
+      if (a.renorm) {
+        const float tot = warp_sum(pj);
+        const float r = tot > 0.f ? 1.f / tot : 0.f;
+        sel_term = pj * r * (dj - mean * r);
+        mean = 0.f;  // off the selection the weights' gradient is zero
+      } else {
+        sel_term = pj * dj;
+      }
     }
-    // renorm: w_j (dw_j - sum dw w) on the selected; else p (dw - sum dw p).
-    const float inv = a.renorm && tot > 0.f ? 1.f / tot : 0.f;
-    const float mean = a.renorm ? pd * inv : pd;
-    TL* row = grad + (size_t)t * a.E + lane;
+    const float shift = pc + mean;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const bool mine = (sel >> q) & 1u;
-      float g;
-      if (a.renorm)
-        g = mine ? p[q] * inv * (d[q] - mean) : 0.f;
-      else
-        g = p[q] * (d[q] - mean);
-      g += p[q] * (c[q] - pc);
-      if (lane + 32 * q < a.E) store_grad(row + 32 * q, valid ? g : 0.f);
+    for (int q = 0; q < Q; ++q) p[q] *= c[q] - shift;
+    store_row<Q>(row, a.E, a.vec, p);
+    if (a.dw != nullptr) {
+      __syncwarp();  // the row's stores above come before these
+      if (id >= 0) store_grad(row + id, sel_term + pj * (c_s[id] - shift));
     }
   }
 }
 
 template <int EP, typename TL>
 cudaError_t forward_ep(const TL* logits, const RouteLogitsArgs& a, int blocks, cudaStream_t st) {
-  cudaError_t e = launch_k(route_logits_kernel<EP, TL>, dim3(blocks), dim3(kRlThreads), 0, st,
-                           false, logits, a);
-  if (e != cudaSuccess || blocks == 1) return e;
-  return launch_k(route_logits_finish_kernel<EP>, dim3(1), dim3(kRlThreads), 0, st, true, blocks,
+  if (blocks == 1)
+    return launch_k(route_logits_kernel<EP, kRlOneBlockWarps, TL>, dim3(1),
+                    dim3(kRlOneBlockWarps * 32), 0, st, false, logits, a);
+  cudaError_t e = launch_k(route_logits_kernel<EP, kRlWarps, TL>, dim3(blocks), dim3(kRlThreads), 0,
+                           st, false, logits, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(route_logits_finish_kernel<EP>, dim3(1), dim3(kRlFinish), 0, st, true, blocks,
                   a);
 }
 
@@ -408,6 +587,12 @@ cudaError_t backward_t(const TL* logits, TL* grad, const RouteLogitsBwdArgs& a, 
 
 int ep_of(int E) { return E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256; }
 
+// Rows of E values that lanes may take Q at a time.
+bool rows_are_vectors(const void* p, int E, int size) {
+  const int Q = ep_of(E) / 32, bytes = Q * size < 16 ? Q * size : 16;
+  return E % Q == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
 int blocks_for(int T, int num_sms) {
   const int want = (T + kRlWarps - 1) / kRlWarps;
   return want < 2 * num_sms ? want : 2 * num_sms;
@@ -420,7 +605,7 @@ int blocks_for(int T, int num_sms) {
 constexpr int kRlMaxBlocks = 320;
 
 long long route_logits_workspace(int T, int E) {
-  if (T <= kRlWarps) return 0;
+  if (T <= kRlOneBlockTokens) return 0;
   const long long rows = (T + kRlWarps - 1) / kRlWarps;
   return (rows < kRlMaxBlocks ? rows : kRlMaxBlocks) * ep_of(E) * 8;
 }
@@ -429,10 +614,11 @@ cudaError_t launch_route_logits(const void* logits, bool is_bf16, const uint8_t*
                                 int top_k, int renorm, int32_t* ids, float* w, int32_t* counts,
                                 float* prob_sums, float* loss, void* workspace, int num_sms,
                                 cudaStream_t st) {
-  int blocks = T > 0 ? blocks_for(T, num_sms) : 1;
+  int blocks = T > kRlOneBlockTokens ? blocks_for(T, num_sms) : 1;
   if (blocks > kRlMaxBlocks) blocks = kRlMaxBlocks;
   const int EP = ep_of(E);
-  RouteLogitsArgs a = {mask, ids, w, nullptr, nullptr, counts, prob_sums, loss, T, E, top_k, renorm};
+  RouteLogitsArgs a = {mask, ids, w, nullptr, nullptr, counts, prob_sums, loss, T, E, top_k, renorm,
+                       rows_are_vectors(logits, E, is_bf16 ? 2 : 4)};
   if (blocks > 1) {
     a.part_p = static_cast<float*>(workspace);
     a.part_c = reinterpret_cast<int32_t*>(a.part_p + (size_t)blocks * EP);
@@ -445,7 +631,9 @@ cudaError_t launch_route_logits_backward(const void* logits, bool is_bf16, const
                                          const int32_t* ids, const int32_t* counts, const float* dw,
                                          const float* dloss, int T, int E, int top_k, int renorm,
                                          void* grad, int num_sms, cudaStream_t st) {
-  const RouteLogitsBwdArgs a = {mask, ids, counts, dw, dloss, T, E, top_k, renorm};
+  const RouteLogitsBwdArgs a = {mask, ids, counts, dw, dloss, T, E, top_k, renorm,
+                                rows_are_vectors(logits, E, is_bf16 ? 2 : 4) &&
+                                    rows_are_vectors(grad, E, is_bf16 ? 2 : 4)};
   const int blocks = blocks_for(T, num_sms);
   return is_bf16 ? backward_t(static_cast<const uint16_t*>(logits), static_cast<uint16_t*>(grad), a,
                               blocks, st)

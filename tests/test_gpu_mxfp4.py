@@ -84,6 +84,26 @@ def test_quantise_extremes():
     _status_ok()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_buffers_aligned_to_16_bytes_only(dtype):
+    size = torch.empty((), dtype=dtype).element_size()
+    flat = torch.from_numpy(_spread(4, 1, 70 * 96 + 16)[0]).cuda().to(dtype)
+    x = flat[16 // size:16 // size + 70 * 96].view(70, 96)
+    assert x.data_ptr() % 32 == 16
+    codes, scales = mm.mm_mxfp4_quantize(x)
+    same = mm.mm_mxfp4_quantize(x.clone())
+    assert torch.equal(codes, same[0]) and torch.equal(scales, same[1])
+    out = torch.zeros(70 * 96 + 32, dtype=dtype, device="cuda")
+    at = out[16 // size:16 // size + 70 * 96]
+    rc = mm.lib().mm_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), 1, 70, 96,
+                                      at.data_ptr(), mm._lib._DTYPES[dtype],
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == mm.MM_OK
+    assert torch.equal(at.view(70, 96), mm.mm_mxfp4_dequantize(codes, scales, dtype))
+    assert not out[:16 // size].any() and not out[16 // size + 70 * 96:].any()
+    _status_ok()
+
+
 def test_dequantise_every_code_and_scale():
     # Every byte of codes under every scale byte: row r has scale r.
     codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)          # K = 512
