@@ -114,11 +114,21 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint6
 }
 
 // Instruction descriptor of kind::mxf4: e2m1 A and B (1 at bits 7-9 and
-// 10-12), N >> 3 at 17-22, e8m0 scales (bit 23), M >> 7 at 27-28; the byte
-// pair of a scale column that the MMA reads (0 or 2) at 4-5 for B, 29-30 for A.
-__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t pair) {
+// 10-12), N >> 3 at 17-22, e8m0 scales (bit 23), M >> 7 at 27-28; and the byte
+// pair of a scale column that the MMA reads (0 or 2), at 4-5 for B, 29-30 for A.
+__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(M >> 7) << 27) | (pair << 4) | (pair << 29);
+         (static_cast<uint32_t>(M >> 7) << 27);
+}
+__device__ __forceinline__ uint32_t idesc_mxf4_pair(uint32_t pair) {
+  return (pair << 4) | (pair << 29);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
 }
 
 }  // namespace mm

@@ -135,6 +135,34 @@ __device__ __forceinline__ uint32_t spread4(uint32_t x) {  // nibble n -> byte n
   return (x | (x << 4)) & 0x0F0F0F0Fu;
 }
 
+// Issues one stage: the scale tiles of its `steps` / 2 halves to tensor memory,
+// then `steps` MMAs of K = 64 for D0, and for D1 if HAS1. One thread.
+template <bool HAS1>
+__device__ __forceinline__ void issue_stage(uint32_t st, uint32_t tsc, uint32_t d0, uint32_t idesc,
+                                            bool accumulate, int steps) {
+  const uint64_t da0 = sdesc_kmajor<128>(st);
+  const uint64_t da1 = sdesc_kmajor<128>(st + kTileBytes);
+  const uint64_t db = sdesc_kmajor<128>(st + 2 * kTileBytes);
+  const uint64_t sc = sdesc_scales(st + 3 * kTileBytes);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (2 * h >= steps) break;
+    // Descriptor addresses count 16-byte units.
+    tmem_cp_scales(tsc + h * 12, sc + h * (kMxTileBytes / 16));
+    if (HAS1) tmem_cp_scales(tsc + h * 12 + 4, sc + (kScaleStage + h * kMxTileBytes) / 16);
+    tmem_cp_scales(tsc + h * 12 + 8, sc + (2 * kScaleStage + h * kMxTileBytes) / 16);
+  }
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    if (kk >= steps) break;
+    const uint32_t id = idesc | idesc_mxf4_pair((kk & 1) * 2);
+    const uint32_t col = tsc + (kk >> 1) * 12;
+    const uint32_t acc = accumulate || kk != 0;
+    umma_mxf4(d0, da0 + kk * 2, db + kk * 2, id, col, col + 8, acc);
+    if (HAS1) umma_mxf4(d0 + kBN, da1 + kk * 2, db + kk * 2, id, col + 4, col + 8, acc);
+  }
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -253,65 +281,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer ---
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, it = 0;
-      for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
-        if (stopped(&stop_s)) break;
-        const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
-        const bool has1 = weights_of<MODE>(a, t).has1;
-        if (!mbar_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
+    // The whole warp runs the loops, so that stage addresses, descriptors and
+    // columns are warp-uniform values; one elected lane issues.
+    const bool leader = elect_one();
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
+      if (stopped(&stop_s)) break;
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const bool has1 = weights_of<MODE>(a, t).has1;
+      if (!mbar_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
+        stop(&stop_s, a.err);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t idesc = idesc_mxf4(128, (t.nrows + 15) & ~15);
+      bool ok = true;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!mbar_wait(smem_u32(&full[s]), ph)) {
           stop(&stop_s, a.err);
+          ok = false;
           break;
         }
         tc_fence_after();
-        const int n_mma = (t.nrows + 15) & ~15;
-        bool ok = true;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(smem_u32(&full[s]), ph)) {
-            stop(&stop_s, a.err);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = smem_base + s * kStageStride;
-          const uint32_t sc = st + 3 * kTileBytes;
-          // Each slot has scale columns of its own: the MMAs that read their
-          // last contents were complete before the slot was filled again.
-          const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols;
-          const int halves = min(2, k_tiles - 2 * kb);
-          const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
-          for (int h = 0; h < halves; ++h) {
-            tmem_cp_scales(tsc + h * 12, sdesc_scales(sc + h * kMxTileBytes));
-            if (has1)
-              tmem_cp_scales(tsc + h * 12 + 4, sdesc_scales(sc + kScaleStage + h * kMxTileBytes));
-            tmem_cp_scales(tsc + h * 12 + 8, sdesc_scales(sc + 2 * kScaleStage + h * kMxTileBytes));
-          }
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint32_t idesc = idesc_mxf4(128, n_mma, (kk & 1) * 2);
-            const uint32_t col = tsc + (kk >> 1) * 12;
-            const uint64_t da0 = sdesc_kmajor<128>(st + kk * 32);
-            const uint64_t db = sdesc_kmajor<128>(st + 2 * kTileBytes + kk * 32);
-            const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
-            umma_mxf4(tmem_base, da0, db, idesc, col, col + 8, acc);
-            if (has1) {
-              const uint64_t da1 = sdesc_kmajor<128>(st + kTileBytes + kk * 32);
-              umma_mxf4(tmem_base + kBN, da1, db, idesc, col + 4, col + 8, acc);
-            }
-          }
+        const uint32_t st = smem_base + s * kStageStride;
+        // Each slot has scale columns of its own: the MMAs that read their
+        // last contents were complete before the slot was filled again.
+        const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols;
+        const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
+        if (leader) {
+          if (has1 && steps == 4)
+            issue_stage<true>(st, tsc, tmem_base, idesc, kb != 0, 4);
+          else if (has1)
+            issue_stage<true>(st, tsc, tmem_base, idesc, kb != 0, steps);
+          else
+            issue_stage<false>(st, tsc, tmem_base, idesc, kb != 0, steps);
           umma_commit(smem_u32(&empty[s]));
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (!ok) break;
-        umma_commit(smem_u32(tfull));
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      // Every MMA issued above has finished before the CTA tears down.
-      umma_commit(smem_u32(done));
-      if (!mbar_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
+      if (!ok) break;
+      if (leader) umma_commit(smem_u32(tfull));
+      __syncwarp();
     }
+    // Every MMA issued above has finished before the CTA tears down.
+    if (leader) umma_commit(smem_u32(done));
+    __syncwarp();
+    if (!mbar_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
   } else if (warp >= kEpiWarp0) {
     // ----------------------------------------------------- epilogue (2-9) ---
     const int q = warp & 3;                    // tensor-memory lane quarter of this warp
