@@ -41,9 +41,12 @@ constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = kStages * kStageStride + 1024;
 static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 
-// Warp roles: 0 = nothing but the prologue, 1 = MMA issuer, 2-9 = epilogue,
-// 10-13 = producers (one per ring slot).
-constexpr int kEpiWarp0 = 2, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
+// Warp roles: 0 = nothing but the prologue, 1 = MMA issuer, 2-17 = epilogue,
+// 18-21 = producers (one per ring slot). There is one pair of accumulators (the
+// scales take the columns a second pair would need), so the epilogue first
+// empties tensor memory into registers, 16 warps with a 32 x 32 piece of D0 and
+// of D1 each, hands it back to the MMA warp and then does its work.
+constexpr int kEpiWarp0 = 2, kEpiWarps = 16, kEpiThreads = kEpiWarps * 32;
 constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = (kProdWarp0 + kStages) * 32;
 
@@ -234,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nk = (a.K + kStageK - 1) / kStageK;  // stages per tile
 
   if (warp >= kProdWarp0) {
-    // ---------------------------------------------------- producers (10-13) ---
-    // Warp 10 + s owns ring slot s: a warp's copies that signal another
+    // ---------------------------------------------------- producers (18-21) ---
+    // Warp 18 + s owns ring slot s: a warp's copies that signal another
     // barrier than its previous ones would wait for those to land.
     const int slot = warp - kProdWarp0;
     if (lane == 0) {
@@ -333,36 +336,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (!mbar_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
   } else if (warp >= kEpiWarp0) {
-    // ----------------------------------------------------- epilogue (2-9) ---
+    // ----------------------------------------------------- epilogue (2-17) --
     const int q = warp & 3;                    // tensor-memory lane quarter of this warp
-    const int side = (warp - kEpiWarp0) >> 2;  // takes 32-column chunks side, side + 2
+    const int c0 = ((warp - kEpiWarp0) >> 2) * 32;  // first column (token row) of this warp
     uint32_t it = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
       const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
       const bool has1 = weights_of<MODE>(a, t).has1;
-      int f_t[2] = {0, 0};  // down: output row of column `lane` of this warp's chunks
-      if (MODE == kDown) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = (2 * i + side) * 32 + lane;
-          if (c < t.nrows) f_t[i] = __ldg(a.sorted + t.row0 + c);
-        }
-      }
+      int f_t = 0;  // down: output row of column c0 + lane
+      if (MODE == kDown && c0 + lane < t.nrows) f_t = __ldg(a.sorted + t.row0 + c0 + lane);
       if (!mbar_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
         break;
       }
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const int c0 = (2 * i + side) * 32;
-        if (c0 >= t.nrows) break;
-        uint32_t d0[32], d1[32];
+      uint32_t d0[32], d1[32];
+      if (c0 < t.nrows) {
         tmem_ld_32x32b_x32(tb + c0, d0);
         tmem_ld_32x32b_x32(tb + kBN + c0, d1);
         tmem_wait_ld();
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(tempty));
+      if (c0 < t.nrows) {
         const int ncol = min(32, t.nrows - c0);
         if (MODE == kGateUp) {
           // Block (row, q) of the activation: 32 intermediates, one per lane.
@@ -370,20 +368,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
           uint32_t my_scale = 0;
           uint8_t* codes = static_cast<uint8_t*>(a.out);
+          // The divide and the exponential are off by a few units of the 24th
+          // bit; the 4-bit rounding that follows keeps 2 bits.
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float g = __uint_as_float(d0[j]), u = __uint_as_float(d1[j]);
+            d0[j] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * u);
+          }
 #pragma unroll
           for (int j0 = 0; j0 < 32; j0 += 8) {
             if (j0 >= ncol) break;
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float g = __uint_as_float(d0[j0 + j]), u = __uint_as_float(d1[j0 + j]);
-              // The divide and the exponential are off by a few units of the
-              // 24th bit; the 4-bit rounding that follows keeps 2 bits.
-              const float x = __fdividef(g, 1.0f + __expf(-g)) * u;
-              const uint32_t amax =
-                  __reduce_max_sync(kAll, __float_as_uint(x) & 0x7fffffffu);
+              const uint32_t amax = __reduce_max_sync(kAll, d0[j0 + j] & 0x7fffffffu);
               const uint32_t s = mx_scale_byte(amax);
-              v[j] = x * mx_inv_scale(s);
+              v[j] = __uint_as_float(d0[j0 + j]) * mx_inv_scale(s);
               if (lane == j0 + j) my_scale = s;
             }
             // Nibble n of r: this lane's row, column j0 + n. Turn 8 columns x
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* y = static_cast<float*>(a.out);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const int f = __shfl_sync(kAll, i == 0 ? f_t[0] : f_t[1], j);
+            const int f = __shfl_sync(kAll, f_t, j);
             if (j < ncol) {
               float* row = y + (size_t)f * a.N;
               if (h0 < a.N) row[h0] = __uint_as_float(d0[j]);
@@ -439,8 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(smem_u32(tempty));
     }
   }
 
