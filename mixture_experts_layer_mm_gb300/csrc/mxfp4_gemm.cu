@@ -169,7 +169,7 @@ __device__ __forceinline__ void issue_stage(uint32_t st, uint32_t tsc, uint32_t 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const MxGemmArgs a) {
+                   const __grid_constant__ CUtensorMap tmX32, const MxGemmArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
   __shared__ uint32_t tmem_base_s;
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmX32);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
@@ -240,46 +241,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------- producers (18-21) ---
     // Warp 18 + s owns ring slot s: a warp's copies that signal another
     // barrier than its previous ones would wait for those to land.
+    // As in the MMA warp, all lanes run the loop and one issues.
     const int slot = warp - kProdWarp0;
-    if (lane == 0) {
-      const uint64_t pol_w = l2_policy_evict_normal();
-      const uint64_t pol_x = l2_policy_evict_last();
-      const uint32_t st = smem_base + slot * kStageStride;
-      const uint32_t sc = st + 3 * kTileBytes;
-      const uint32_t fb = smem_u32(&full[slot]);
-      uint32_t use = 0;
-      int q = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        if (stopped(&stop_s)) break;
-        const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
-        const WeightAt w = weights_of<MODE>(a, t);
-        const int nbox = (t.nrows + 31) / 32;  // boxes of 32 token rows
-        for (int kb = 0; kb < nk; ++kb) {
-          const bool mine = q == slot;
-          if (++q == kStages) q = 0;
-          if (!mine) continue;
-          if (!mbar_wait(smem_u32(&empty[slot]), (use & 1u) ^ 1u)) {
-            stop(&stop_s, a.err);
-            ok = false;
-            break;
-          }
+    const bool leader = elect_one();
+    const uint64_t pol_w = l2_policy_evict_normal();
+    const uint64_t pol_x = l2_policy_evict_last();
+    const uint32_t st = smem_base + slot * kStageStride;
+    const uint32_t sc = st + 3 * kTileBytes;
+    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
+    uint32_t use = 0;
+    int q = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      if (stopped(&stop_s)) break;
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const WeightAt w = weights_of<MODE>(a, t);
+      // Token rows: one box of 128, or up to three boxes of 32.
+      const int nbox = t.nrows > 96 ? 4 : (t.nrows + 31) / 32;
+      const uint8_t* ws0 = a.w_scales + w.st0 * k_tiles * kMxTileBytes;
+      const uint8_t* ws1 = a.w_scales + w.st1 * k_tiles * kMxTileBytes;
+      const uint8_t* xs = a.x_scales + (long long)(t.row0 / 128) * k_tiles * kMxTileBytes;
+      for (int kb = 0; kb < nk; ++kb) {
+        const bool mine = q == slot;
+        if (++q == kStages) q = 0;
+        if (!mine) continue;
+        if (!mbar_wait(eb, (use & 1u) ^ 1u)) {
+          stop(&stop_s, a.err);
+          ok = false;
+          break;
+        }
+        if (leader) {
           const int kt = 2 * kb;  // first scale tile of the stage
           const uint32_t sb = min(2, k_tiles - kt) * kMxTileBytes;
           mbar_arrive_expect_tx(
               fb, (w.has1 ? 2u : 1u) * (kTileBytes + sb) + (uint32_t)nbox * 4096u + sb);
           tma_load_2d(st, &tmW, fb, kb * 128, w.row0, pol_w);
-          bulk_load(sc, a.w_scales + (w.st0 * k_tiles + kt) * kMxTileBytes, sb, fb);
-          if (w.has1) {
-            tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
-            bulk_load(sc + kScaleStage, a.w_scales + (w.st1 * k_tiles + kt) * kMxTileBytes, sb, fb);
+          if (w.has1) tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
+          if (nbox == 4) {
+            tma_load_2d(st + 2 * kTileBytes, &tmX, fb, kb * 128, t.row0, pol_x);
+          } else {
+            for (int b = 0; b < nbox; ++b)
+              tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX32, fb, kb * 128, t.row0 + 32 * b,
+                          pol_x);
           }
-          for (int b = 0; b < nbox; ++b)
-            tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX, fb, kb * 128, t.row0 + 32 * b, pol_x);
-          bulk_load(sc + 2 * kScaleStage,
-                    a.x_scales + ((long long)(t.row0 / 128) * k_tiles + kt) * kMxTileBytes, sb, fb);
-          ++use;
+          bulk_load(sc, ws0 + kt * kMxTileBytes, sb, fb);
+          if (w.has1) bulk_load(sc + kScaleStage, ws1 + kt * kMxTileBytes, sb, fb);
+          bulk_load(sc + 2 * kScaleStage, xs + kt * kMxTileBytes, sb, fb);
         }
+        __syncwarp();
+        ++use;
       }
     }
   } else if (warp == 1) {
@@ -450,15 +460,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// w: w_rows rows of weight codes; x: x_rows rows of token codes.
 template <int MODE>
-cudaError_t launch_mode(const CUtensorMap& tmW, const CUtensorMap& tmX, const MxGemmArgs& a,
-                        long long max_tiles, int num_sms, bool after_prev, cudaStream_t st) {
+cudaError_t launch_mode(const uint8_t* w, long long w_rows, const uint8_t* x, long long x_rows,
+                        const MxGemmArgs& a, long long max_tiles, int num_sms, bool after_prev,
+                        cudaStream_t st) {
   static DeviceFlags attr_done;
   if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE>, kSmemBytes); e != cudaSuccess)
     return e;
+  CUtensorMap tmW, tmX, tmX32;
+  if (!make_tensor_map_codes(&tmW, w, (uint64_t)w_rows, (uint64_t)a.K, 128) ||
+      !make_tensor_map_codes(&tmX, x, (uint64_t)x_rows, (uint64_t)a.K, 128) ||
+      !make_tensor_map_codes(&tmX32, x, (uint64_t)x_rows, (uint64_t)a.K, 32))
+    return cudaErrorInvalidValue;
   const int grid = (int)std::min<long long>(max_tiles, num_sms);
   return launch_k(mx_gemm_kernel<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, after_prev, tmW,
-                  tmX, a);
+                  tmX, tmX32, a);
 }
 
 }  // namespace
@@ -466,10 +483,6 @@ cudaError_t launch_mode(const CUtensorMap& tmW, const CUtensorMap& tmX, const Mx
 cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                            const uint8_t* b_scales, int M, int N, int K, void* c, bool out_fp32,
                            int num_sms, unsigned* err, cudaStream_t st) {
-  CUtensorMap tmW, tmX;
-  if (!make_tensor_map_codes(&tmW, b_codes, (uint64_t)N, (uint64_t)K, 128) ||
-      !make_tensor_map_codes(&tmX, a_codes, (uint64_t)M, (uint64_t)K, 32))
-    return cudaErrorInvalidValue;
   MxGemmArgs a = {};
   a.w_scales = b_scales;
   a.x_scales = a_scales;
@@ -482,7 +495,7 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   a.n_mtiles = (N + 255) / 256;
   a.out_fp32 = out_fp32 ? 1 : 0;
   const long long tiles = (long long)((M + kBN - 1) / kBN) * a.n_mtiles;
-  return launch_mode<kDense>(tmW, tmX, a, tiles, num_sms, false, st);
+  return launch_mode<kDense>(b_codes, N, a_codes, M, a, tiles, num_sms, false, st);
 }
 
 cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
@@ -491,10 +504,6 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
                                       int H, long long capacity, long long max_chunks,
                                       uint8_t* act, uint8_t* act_scales, int num_sms,
                                       unsigned* err, bool after_prev, cudaStream_t st) {
-  CUtensorMap tmW, tmX;
-  if (!make_tensor_map_codes(&tmW, w, (uint64_t)E * 2 * I, (uint64_t)H, 128) ||
-      !make_tensor_map_codes(&tmX, xs, (uint64_t)capacity, (uint64_t)H, 32))
-    return cudaErrorInvalidValue;
   MxGemmArgs a = {};
   a.offsets = offsets;
   a.counts = counts;
@@ -507,7 +516,8 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
   a.N = I;
   a.K = H;
   a.n_mtiles = (I + 127) / 128;
-  return launch_mode<kGateUp>(tmW, tmX, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
+  return launch_mode<kGateUp>(w, 2LL * E * I, xs, capacity, a, max_chunks * a.n_mtiles, num_sms,
+                              after_prev, st);
 }
 
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
@@ -515,10 +525,6 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
                                    const int32_t* offsets, const int32_t* counts, int E, int H,
                                    int I, long long capacity, long long max_chunks, float* y,
                                    int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
-  CUtensorMap tmW, tmX;
-  if (!make_tensor_map_codes(&tmW, w, (uint64_t)E * H, (uint64_t)I, 128) ||
-      !make_tensor_map_codes(&tmX, act, (uint64_t)capacity, (uint64_t)I, 32))
-    return cudaErrorInvalidValue;
   MxGemmArgs a = {};
   a.sorted = sorted;
   a.offsets = offsets;
@@ -531,7 +537,8 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
   a.N = H;
   a.K = I;
   a.n_mtiles = (H + 255) / 256;
-  return launch_mode<kDown>(tmW, tmX, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
+  return launch_mode<kDown>(w, (long long)E * H, act, capacity, a, max_chunks * a.n_mtiles, num_sms,
+                            after_prev, st);
 }
 
 }  // namespace mm
