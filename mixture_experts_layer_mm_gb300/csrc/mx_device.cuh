@@ -68,6 +68,34 @@ __device__ __forceinline__ uint32_t mx_pack8(const float (&v)[8]) {
   return r;
 }
 
+// ------------------------------------------------- warp-uniform control ---
+//
+// The warps that issue copies and MMAs keep everything those instructions
+// take (addresses, descriptors, coordinates) in uniform registers. That needs
+// control flow and values that the compiler can see to be the same in all
+// lanes: a branch on a vote, a value out of a warp reduction.
+
+// A value all lanes hold, as a warp-uniform one.
+__device__ __forceinline__ int uniform(int v) {
+  return (int)__reduce_max_sync(0xffffffffu, (unsigned)v);
+}
+
+// mbar_wait for a whole converged warp. Bounded: after 64 failed polls (each
+// suspends for a bounded time) the clock is read, which costs as much as a
+// pipeline stage, and the limit of mbar_wait applies.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+
 // ------------------------------------------------ block-scaled tcgen05 ---
 
 // `bytes` contiguous bytes (a multiple of 16, both sides 16-byte aligned)

@@ -41,7 +41,7 @@ constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = kStages * kStageStride + 1024;
 static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 
-// Warp roles: 0 = nothing but the prologue, 1 = MMA issuer, 2-17 = epilogue,
+// Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue,
 // 18-21 = producers (one per ring slot). There is one pair of accumulators (the
 // scales take the columns a second pair would need), so the epilogue first
 // empties tensor memory into registers, 16 warps with a 32 x 32 piece of D0 and
@@ -50,8 +50,10 @@ constexpr int kEpiWarp0 = 2, kEpiWarps = 16, kEpiThreads = kEpiWarps * 32;
 constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = (kProdWarp0 + kStages) * 32;
 
-// Tensor memory: D0 and D1 (128 columns each), then per ring slot the scale
-// columns of its two 128-column halves: A0, A1, B, 4 columns each.
+// Tensor memory: D0 and D1 (128 columns each), then per ring slot and
+// accumulator the scale columns of the slot's two halves of K: weights, token
+// rows, 4 columns each (each issuer brings the token rows' own copy, so that
+// neither depends on the other's order).
 constexpr uint32_t kScaleCol0 = 2 * kBN, kScaleCols = 32;
 constexpr uint32_t kTmemCols = 512;
 
@@ -72,8 +74,9 @@ struct MxGemmArgs {
   int out_fp32;   // dense
 };
 
+// Whether a warp of this CTA gave up a wait (asked by a converged warp).
 __device__ __forceinline__ bool stopped(const int* flag) {
-  return *reinterpret_cast<const volatile int*>(flag) != 0;
+  return __any_sync(kAll, *reinterpret_cast<const volatile int*>(flag) != 0);
 }
 
 __device__ __forceinline__ void stop(int* flag, unsigned* err) {
@@ -98,10 +101,11 @@ __device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int
     else
       hi = mid;
   }
+  lo = uniform(lo);
   t.e = lo;
-  const int in = (ch - first_chunk[lo]) * kBN;
-  t.row0 = off[lo] + in;
-  t.nrows = min(kBN, cnt[lo] - in);
+  const int in = (ch - uniform(first_chunk[lo])) * kBN;
+  t.row0 = uniform(off[lo]) + in;
+  t.nrows = min(kBN, uniform(cnt[lo]) - in);
   return t;
 }
 
@@ -138,31 +142,28 @@ __device__ __forceinline__ uint32_t spread4(uint32_t x) {  // nibble n -> byte n
   return (x | (x << 4)) & 0x0F0F0F0Fu;
 }
 
-// Issues one stage: the scale tiles of its `steps` / 2 halves to tensor memory,
-// then `steps` MMAs of K = 64 for D0, and for D1 if HAS1. One thread.
-template <bool HAS1>
-__device__ __forceinline__ void issue_stage(uint32_t st, uint32_t tsc, uint32_t d0, uint32_t idesc,
-                                            bool accumulate, int steps) {
-  const uint64_t da0 = sdesc_kmajor<128>(st);
-  const uint64_t da1 = sdesc_kmajor<128>(st + kTileBytes);
+// Issues one stage of one accumulator: the scale tiles of its `steps` / 2
+// halves (weights, token rows) to tensor memory, then `steps` MMAs of K = 64.
+// One thread. a_tile 0 or 1: A0 into D0, A1 into D1.
+__device__ __forceinline__ void issue_stage(uint32_t st, int a_tile, uint32_t tsc, uint32_t d,
+                                            uint32_t idesc, bool accumulate, int steps) {
+  const uint64_t da = sdesc_kmajor<128>(st + a_tile * kTileBytes);
   const uint64_t db = sdesc_kmajor<128>(st + 2 * kTileBytes);
-  const uint64_t sc = sdesc_scales(st + 3 * kTileBytes);
+  const uint64_t sa = sdesc_scales(st + 3 * kTileBytes + a_tile * kScaleStage);
+  const uint64_t sb = sdesc_scales(st + 3 * kTileBytes + 2 * kScaleStage);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (2 * h >= steps) break;
     // Descriptor addresses count 16-byte units.
-    tmem_cp_scales(tsc + h * 12, sc + h * (kMxTileBytes / 16));
-    if (HAS1) tmem_cp_scales(tsc + h * 12 + 4, sc + (kScaleStage + h * kMxTileBytes) / 16);
-    tmem_cp_scales(tsc + h * 12 + 8, sc + (2 * kScaleStage + h * kMxTileBytes) / 16);
+    tmem_cp_scales(tsc + h * 8, sa + h * (kMxTileBytes / 16));
+    tmem_cp_scales(tsc + h * 8 + 4, sb + h * (kMxTileBytes / 16));
   }
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     if (kk >= steps) break;
-    const uint32_t id = idesc | idesc_mxf4_pair((kk & 1) * 2);
-    const uint32_t col = tsc + (kk >> 1) * 12;
-    const uint32_t acc = accumulate || kk != 0;
-    umma_mxf4(d0, da0 + kk * 2, db + kk * 2, id, col, col + 8, acc);
-    if (HAS1) umma_mxf4(d0 + kBN, da1 + kk * 2, db + kk * 2, id, col + 4, col + 8, acc);
+    const uint32_t col = tsc + (kk >> 1) * 8;
+    umma_mxf4(d, da + kk * 2, db + kk * 2, idesc | idesc_mxf4_pair((kk & 1) * 2), col, col + 4,
+              accumulate || kk != 0);
   }
 }
 
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) first_s[E] = run;
   }
   __syncthreads();
-  const int total = first_s[E] * a.n_mtiles;
+  const int total = uniform(first_s[E]) * a.n_mtiles;
   if ((int)blockIdx.x >= total) return;  // uniform across the CTA
 
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -214,11 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 2);  // one commit of each issuer
     }
-    mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(tfull), 2);
     mbar_init(smem_u32(tempty), kEpiThreads);
-    mbar_init(smem_u32(done), 1);
+    mbar_init(smem_u32(done), 2);
     stop_s = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -233,7 +234,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = tmem_base_s;
+  // All 512 columns are this CTA's, so they begin at column 0: a constant in
+  // the MMA's operands. (Were it ever otherwise, nothing below would run.)
+  constexpr uint32_t tmem_base = 0;
+  if (tmem_base_s != tmem_base) {
+    if (tid == 0) atomicOr(a.err, kDevErrTimeout);
+    if (warp == 1) tmem_dealloc(tmem_base_s, kTmemCols);
+    return;
+  }
   const int k_tiles = (a.K + 127) / 128;         // scale tiles per row
   const int nk = (a.K + kStageK - 1) / kStageK;  // stages per tile
 
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = q == slot;
         if (++q == kStages) q = 0;
         if (!mine) continue;
-        if (!mbar_wait(eb, (use & 1u) ^ 1u)) {
+        if (!warp_wait(eb, (use & 1u) ^ 1u)) {
           stop(&stop_s, a.err);
           ok = false;
           break;
@@ -292,18 +300,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++use;
       }
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer ---
-    // The whole warp runs the loops, so that stage addresses, descriptors and
-    // columns are warp-uniform values; one elected lane issues.
+  } else if (warp < 2) {
+    // ------------------------------------------------- MMA issuers (0, 1) ---
+    // Warp 0 feeds D0, warp 1 D1. A tcgen05 instruction takes its thread about
+    // 30 cycles and a stage's wait 200 more, together above the 60 cycles an
+    // MMA of N = 128 takes to run, so one thread for both accumulators leaves
+    // the tensor cores waiting (57 us for 8192 x 4096 x 4096; two: DUAL_US).
+    // The whole warp runs the loops, so that addresses, descriptors and columns
+    // are warp-uniform; one elected lane issues.
     const bool leader = elect_one();
+    const uint32_t d = tmem_base + warp * kBN;
     int s = 0;
     uint32_t ph = 0, it = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
       const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
-      const bool has1 = weights_of<MODE>(a, t).has1;
-      if (!mbar_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
+      const bool work = warp == 0 || weights_of<MODE>(a, t).has1;
+      if (!warp_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
         stop(&stop_s, a.err);
         break;
       }
@@ -311,24 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_mxf4(128, (t.nrows + 15) & ~15);
       bool ok = true;
       for (int kb = 0; kb < nk; ++kb) {
-        if (!mbar_wait(smem_u32(&full[s]), ph)) {
+        if (!warp_wait(smem_u32(&full[s]), ph)) {
           stop(&stop_s, a.err);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t st = smem_base + s * kStageStride;
-        // Each slot has scale columns of its own: the MMAs that read their
-        // last contents were complete before the slot was filled again.
-        const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols;
-        const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
         if (leader) {
-          if (has1 && steps == 4)
-            issue_stage<true>(st, tsc, tmem_base, idesc, kb != 0, 4);
-          else if (has1)
-            issue_stage<true>(st, tsc, tmem_base, idesc, kb != 0, steps);
-          else
-            issue_stage<false>(st, tsc, tmem_base, idesc, kb != 0, steps);
+          const uint32_t st = smem_base + s * kStageStride;
+          // Each slot has scale columns of its own: the MMAs that read their
+          // last contents were complete before the slot was filled again.
+          const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols + warp * (kScaleCols / 2);
+          const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
+          if (work && steps == 4)
+            issue_stage(st, warp, tsc, d, idesc, kb != 0, 4);
+          else if (work)
+            issue_stage(st, warp, tsc, d, idesc, kb != 0, steps);
           umma_commit(smem_u32(&empty[s]));
         }
         __syncwarp();
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every MMA issued above has finished before the CTA tears down.
     if (leader) umma_commit(smem_u32(done));
     __syncwarp();
-    if (!mbar_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
+    if (!warp_wait(smem_u32(done), 0)) stop(&stop_s, a.err);
   } else if (warp >= kEpiWarp0) {
     // ----------------------------------------------------- epilogue (2-17) --
     const int q = warp & 3;                    // tensor-memory lane quarter of this warp
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool has1 = weights_of<MODE>(a, t).has1;
       int f_t = 0;  // down: output row of column c0 + lane
       if (MODE == kDown && c0 + lane < t.nrows) f_t = __ldg(a.sorted + t.row0 + c0 + lane);
-      if (!mbar_wait(smem_u32(tfull), it & 1u)) {
+      if (!warp_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
         break;
       }
