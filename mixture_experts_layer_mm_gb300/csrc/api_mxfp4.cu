@@ -38,7 +38,7 @@ bool is_dtype(int d) { return d == MM_DTYPE_FP32 || d == MM_DTYPE_BF16 || d == M
 
 // Workspace of the 4-bit experts.
 struct ExpertsLayout {
-  size_t sorted, offsets, counts, scratch, xs, xs_scales, act, act_scales, y, total;
+  size_t offsets, counts, cursor, pos, xs, xs_scales, act, act_scales, y, y_scale, total;
   long long capacity, max_chunks;
 };
 
@@ -61,15 +61,16 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
     off += round256(bytes);
     return o;
   };
-  L.sorted = take((size_t)L.capacity * 4);
   L.offsets = take((size_t)(E + 1) * 4);
   L.counts = take((size_t)E * 4);
-  L.scratch = take((size_t)align_scratch_ints(T, E, k) * 4);
+  L.cursor = take((size_t)E * 4);
+  L.pos = take((size_t)Tk * 4);
   L.xs = take((size_t)rows * H / 2);
   L.xs_scales = take((size_t)(rows / kMxTile) * mx_tiles(H) * kMxTileBytes);
   L.act = take((size_t)rows * I / 2);
   L.act_scales = take((size_t)(rows / kMxTile) * mx_tiles(I) * kMxTileBytes);
-  L.y = take((size_t)Tk * H * 4);
+  L.y = take((size_t)rows * H * 2);
+  L.y_scale = take((size_t)rows * H / 32);
   L.total = off;
   *out = L;
   return MM_OK;
@@ -215,28 +216,27 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
   unsigned* status = nullptr;
   if ((rc = current_device_info(&sms, &status)) != MM_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int32_t* sorted = at<int32_t>(workspace, L.sorted);
   int32_t* offsets = at<int32_t>(workspace, L.offsets);
   int32_t* counts = at<int32_t>(workspace, L.counts);
   uint8_t* xs = at<uint8_t>(workspace, L.xs);
   uint8_t* xs_scales = at<uint8_t>(workspace, L.xs_scales);
   uint8_t* act = at<uint8_t>(workspace, L.act);
   uint8_t* act_scales = at<uint8_t>(workspace, L.act_scales);
-  float* y = at<float>(workspace, L.y);
+  int32_t* pos = at<int32_t>(workspace, L.pos);
+  uint16_t* y = at<uint16_t>(workspace, L.y);
+  uint8_t* y_scale = at<uint8_t>(workspace, L.y_scale);
   const long long rows = mx_tiles(L.capacity) * kMxTile;
-  cudaError_t e = launch_align(topk_ids, T, top_k, E, kMxBlockM, L.capacity, sorted, offsets,
-                               counts, at<int32_t>(workspace, L.scratch), status, false, st);
-  if (e == cudaSuccess)
-    e = launch_mx_gather_quantize(reinterpret_cast<const uint16_t*>(hidden), sorted, offsets, T,
-                                  top_k, E, H, L.capacity, xs, xs_scales, sms, true, st);
+  cudaError_t e = launch_mx_place(hidden, topk_ids, T, top_k, E, H, offsets, counts,
+                                  at<int32_t>(workspace, L.cursor), pos, xs, xs_scales,
+                                  status, st);
   if (e == cudaSuccess)
     e = launch_mx_experts_gate_up(xs, xs_scales, w_gate_up, w_gate_up_scales, offsets, counts, E, I,
                                   H, rows, L.max_chunks, act, act_scales, sms, status, true, st);
   if (e == cudaSuccess)
-    e = launch_mx_experts_down(act, act_scales, w_down, w_down_scales, sorted, offsets, counts, E,
-                               H, I, rows, L.max_chunks, y, sms, status, true, st);
+    e = launch_mx_experts_down(act, act_scales, w_down, w_down_scales, offsets, counts, E,
+                               H, I, rows, L.max_chunks, y, y_scale, sms, status, true, st);
   if (e == cudaSuccess)
-    e = launch_mx_combine(y, topk_ids, topk_w, T, E, top_k, H, out, sms, true, st);
+    e = launch_mx_combine(y, y_scale, pos, topk_w, T, top_k, H, out, sms, true, st);
   return cuda_status(e);
 }
 

@@ -52,6 +52,24 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
                  : s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
 }
 
+// Expert outputs between the down product and the weighted sum: fp16 under one
+// power of two for each 32 columns, so that the sum reads and the product
+// writes half of fp32's bytes (268 MB each way at 4096 tokens x 8 slots x 2048).
+// The block's largest magnitude lands in [2^14, 2^15), so every value down to
+// 2^-28 of it keeps 11 bits: a rounding of at most 2^-11 per slot, under the
+// 2^-8 of the bf16 output (bf16 here would double that output's rounding error).
+// The byte is the biased exponent of the largest magnitude, kept in [15, 254]
+// so that both factors are normal floats; infinity and NaN pass through fp16.
+__device__ __forceinline__ uint32_t mx_y_byte(uint32_t amax_bits) {
+  return min(max(amax_bits >> 23, 15u), 254u);
+}
+__device__ __forceinline__ float mx_y_inv(uint32_t byte) {  // 2^(141 - byte)
+  return __uint_as_float((268u - byte) << 23);
+}
+__device__ __forceinline__ float mx_y_unit(uint32_t byte) {  // 2^(byte - 141)
+  return __uint_as_float((byte - 14u) << 23);
+}
+
 // Eight floats to e2m1 (nearest, ties to even, beyond 6 to 6), v[0] in the
 // lowest nibble. A NaN only reaches this under the factor 0 of a NaN block
 // and becomes whatever finite code the conversion gives it.

@@ -1,6 +1,7 @@
-// Microscaled 4-bit rows: quantisation, the way back, and the two row passes
-// of the 4-bit experts (token rows quantised into segment order, and the
-// weighted sum of a token's expert outputs). The format is in mx_device.cuh.
+// Microscaled 4-bit rows: quantisation, the way back, and the row passes of
+// the 4-bit experts (the grouping, token rows quantised into their experts'
+// segments, the weighted sum of a token's expert outputs). The format is in
+// mx_device.cuh.
 //
 // Per block of 32: e = floor(log2 max|x|) - 2, scale byte e + 127, codes
 // e2m1(x 2^-e) to nearest even, saturating at 6. x 2^-e is a product with a
@@ -166,12 +167,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const unsigned 
                                                                  uint8_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales) {
   const int per_warp = 32 >> lanes_log2;
-  // Consecutive warps take rows r, r + 32, r + 64, r + 96 of a 128-row tile,
-  // then r + 1: the rows whose scale bytes share a 32-byte sector of the tile
-  // are written close together.
-  const long long i = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
-                      ((threadIdx.x & 31) >> lanes_log2);
-  const long long row = (i & ~127LL) + (i & 3) * 32 + (i & 127) / 4;
+  const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
+                        ((threadIdx.x & 31) >> lanes_log2);
   const bool active = row < prows;
   const long long b = active ? row / rp : 0;
   const int r = active ? (int)(row - b * rp) : 0;
@@ -274,55 +271,262 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
   }
 }
 
-// Token rows of the experts' segments: row r of xs = hidden[sorted[r] / k]
-// quantised, for the real slots (padding rows are never read). One warp per
-// slot, so a token is quantised once per expert it goes to: hidden stays in
-// L2, and no launch for a separate quantised copy stands in the chain.
-__global__ void __launch_bounds__(kMxThreads) mx_gather_quantize_kernel(
-    const unsigned char* __restrict__ hidden, const int32_t* __restrict__ sorted,
-    const int32_t* __restrict__ offsets, int E, int top_k, int Tk, int H,
-    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  pdl_wait();
-  pdl_trigger();
-  const int rows = __ldg(offsets + E);
-  const int kt = (int)mx_tiles(H);
-  const int step = gridDim.x * kMxWarps;
-  for (int r = blockIdx.x * kMxWarps + (threadIdx.x >> 5); r < rows; r += step) {
-    const int f = __ldg(sorted + r);
-    if (f >= Tk) continue;
-    quantize_row<MM_DTYPE_BF16, false, 4>(hidden + (size_t)(f / top_k) * H * 2, H, 5,
-                                   codes + (size_t)r * (H / 2), scales + mx_scale_offset(r, 0, kt),
-                                   true);
+// ---------------------------------------------- rows of the experts' segments
+//
+// Every expert's token rows lie in one segment that begins at a multiple of
+// 128 rows. The order of the rows inside a segment does not matter (rows are
+// independent, and a token's sum runs over its slots), so a row takes the next
+// free place. A slot whose id is outside [0, E) or repeats an earlier one of its
+// token is dropped and flagged, as in the layer's grouping.
+
+// Columns [16 i, 16 i + 16) of a token's row to all its places: `place` in
+// lane j < top_k is the row of slot j (-1: dropped), scale_at its scale offset.
+__device__ __forceinline__ void write_places(const float (&v)[16], int c, int H, int top_k,
+                                             int place, uint8_t* codes, uint8_t* scales,
+                                             size_t scale_at) {
+  uint32_t s4;
+  const uint2 code = encode16(v, s4);
+  const size_t tile = (size_t)(c / kMxTile) * kMxTileBytes;
+  for (int j = 0; j < top_k; ++j) {
+    const int r = __shfl_sync(kAll, place, j);
+    const size_t at = __shfl_sync(kAll, scale_at, j);
+    if (r < 0) continue;
+    if (c < H) *reinterpret_cast<uint2*>(codes + (size_t)r * (H / 2) + c / 2) = code;
+    if ((threadIdx.x & 7) == 0 && c < (int)mx_tiles(H) * kMxTile)
+      *reinterpret_cast<uint32_t*>(scales + at + tile) = s4;
   }
 }
 
-// out[t] = bf16(sum_j w[t,j] y[t k + j]) in slot order, 4 columns a thread. A
-// slot whose id the grouping dropped (outside [0, E), or a repeat within the
-// token) has no row in y and adds nothing.
-__global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
-    const float4* __restrict__ y, const int32_t* __restrict__ ids, const float* __restrict__ w,
-    int T, int E, int top_k, int h4, uint2* __restrict__ out) {
+struct MxPlaceArgs {
+  const unsigned char* hidden;
+  const int32_t* ids;
+  int32_t* offsets;  // [E + 1]
+  int32_t* counts;   // [E]
+  int32_t* cursor;   // [E] next free row (large batches)
+  int32_t* pos;      // [T * top_k] row of a slot, -1 if dropped
+  uint8_t* codes;
+  uint8_t* scales;
+  unsigned* err;
+  int T, E, top_k, H;
+};
+
+// First rows of the segments from the counts, by one warp; off[E] the total.
+__device__ __forceinline__ void scan_segments(const int* cnt, int E, int* off) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const int v = e < E ? (cnt[e] + kMxBlockM - 1) / kMxBlockM * kMxBlockM : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (e < E) off[e] = run + incl - v;
+    run += __shfl_sync(kAll, incl, 31);
+  }
+  if (lane == 0) off[E] = run;
+}
+
+// Up to kPlaceSmallIds slots: one block a token, one launch. Every block counts
+// all slots itself (a few thousand shared-memory adds) and ranks its token
+// among the earlier ones, while its part of the row is on the way.
+constexpr int kPlaceSmallIds = 2048;
+constexpr int kPlaceWarps = 4;
+
+__global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const MxPlaceArgs a) {
+  __shared__ int ids_s[kPlaceSmallIds];
+  __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kNT = kPlaceWarps * 32;
+  const int t = blockIdx.x, k = a.top_k, n = a.T * k;
   pdl_wait();
-  const long long n = (long long)T * h4;
+  pdl_trigger();
+  const unsigned char* row = a.hidden + (size_t)t * a.H * 2;
+  const int hp = (int)mx_tiles(a.H) * kMxTile;
+  int c = tid * 16;
+  Raw16h raw;
+  if (c < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw);
+  for (int i = tid; i < n; i += kNT) ids_s[i] = __ldg(a.ids + i);
+  for (int e = tid; e < a.E; e += kNT) tot[e] = before[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += kNT) {
+    const int id = ids_s[i], i0 = i / k * k;
+    bool drop = id < 0 || id >= a.E;
+    for (int j = i0; j < i && !drop; ++j) drop = ids_s[j] == id;
+    bad |= drop;
+    if (!drop) {
+      atomicAdd(&tot[id], 1);
+      if (i < t * k) atomicAdd(&before[id], 1);
+    }
+  }
+  if (bad && t == 0) atomicOr(a.err, kDevErrBadIds);
+  __syncthreads();
+  if (warp == 0) scan_segments(tot, a.E, off);
+  __syncthreads();
+  if (t == 0)
+    for (int e = tid; e <= a.E; e += kNT) {
+      a.offsets[e] = off[e];
+      if (e < a.E) a.counts[e] = tot[e];
+    }
+  int place = -1;
+  if (lane < k) {
+    const int id = ids_s[t * k + lane];
+    bool drop = id < 0 || id >= a.E;
+    for (int j = 0; j < lane && !drop; ++j) drop = ids_s[t * k + j] == id;
+    if (!drop) place = off[id] + before[id];
+    if (warp == 0) a.pos[t * k + lane] = place;
+  }
+  const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
+  for (; c - lane * 16 < hp; c += kNT * 16) {
+    if (c >= a.H) zero16<MM_DTYPE_BF16>(raw);
+    float v[16];
+    unpack16<MM_DTYPE_BF16>(raw, v);
+    if (c + kNT * 16 < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)(c + kNT * 16) * 2, raw);
+    write_places(v, c, a.H, k, place, a.codes, a.scales, scale_at);
+  }
+}
+
+// Larger batches: one cluster counts the slots, its first block adds the counts
+// up and lays the segments out ...
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupBlocks = 8;
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {  // CTA rank's copy of *p
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThreads)
+    mx_group_kernel(const MxPlaceArgs a) {
+  __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts + 1];
+  const int tid = threadIdx.x;
+  const uint32_t k = a.top_k;
+  pdl_wait();
+  pdl_trigger();
+  for (int e = tid; e < a.E; e += kGroupThreads) tot[e] = 0;
+  __syncthreads();
+  const uint32_t n = (uint32_t)a.T * k;
+  bool bad = false;
+#pragma unroll 4
+  for (uint32_t i = blockIdx.x * kGroupThreads + tid; i < n; i += kGroupBlocks * kGroupThreads) {
+    const int id = __ldg(a.ids + i);
+    bool drop = id < 0 || id >= a.E;
+    for (uint32_t j = i / k * k; j < i; ++j) drop |= __ldg(a.ids + j) == id;
+    bad |= drop;
+    if (!drop) atomicAdd(&tot[id], 1);
+  }
+  if (bad) atomicOr(a.err, kDevErrBadIds);
+  cluster_barrier();
+  if (blockIdx.x == 0) {
+    for (int e = tid; e < a.E; e += kGroupThreads) {
+      int v = 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kGroupBlocks; ++r) v += load_peer(&tot[e], r);
+      sum[e] = v;
+    }
+    __syncthreads();
+    if (tid < 32) scan_segments(sum, a.E, off);
+    __syncthreads();
+    for (int e = tid; e <= a.E; e += kGroupThreads) {
+      a.offsets[e] = off[e];
+      if (e < a.E) {
+        a.counts[e] = sum[e];
+        a.cursor[e] = off[e];
+      }
+    }
+  }
+  cluster_barrier();  // no block ends while its counts are being read
+}
+
+// ... then one warp a token takes the next free rows and fills them.
+__global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs a) {
+  const int lane = threadIdx.x & 31, k = a.top_k;
+  const int t = blockIdx.x * kMxWarps + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
+  constexpr int U = 4;
+  const unsigned char* row = a.hidden + (size_t)t * a.H * 2;
+  const int hp = (int)mx_tiles(a.H) * kMxTile;
+  int place = -1;
+  if (lane < k) place = __ldg(a.ids + (size_t)t * k + lane);
+  const uint32_t same = __match_any_sync(kAll, place);
+  if (place < 0 || place >= a.E || (same & ((1u << lane) - 1u)) != 0)
+    place = -1;
+  else
+    place = atomicAdd(a.cursor + place, 1);
+  if (lane < k) a.pos[(size_t)t * k + lane] = place;
+  const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
+  for (int c0 = lane * 16; c0 - lane * 16 < hp; c0 += U * 512) {
+    Raw16h raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 512;
+      if (c < a.H)
+        load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw[u]);
+      else
+        zero16<MM_DTYPE_BF16>(raw[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 512;
+      if (c - lane * 16 >= hp) break;
+      float v[16];
+      unpack16<MM_DTYPE_BF16>(raw[u], v);
+      write_places(v, c, a.H, k, place, a.codes, a.scales, scale_at);
+    }
+  }
+}
+
+// out[t] = bf16(sum_j w[t,j] y[pos[t k + j]]) in slot order, 8 columns a thread;
+// dropped slots (pos < 0) have no row in y and add nothing. y is fp16 under a
+// power of two for each 32 columns (mx_y_scale).
+__global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
+    const uint4* __restrict__ y, const uint8_t* __restrict__ y_scale,
+    const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int top_k, int h8,
+    uint4* __restrict__ out) {
+  pdl_wait();
+  const long long n = (long long)T * h8;
   for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kMxThreads) {
-    const int t = (int)(i / h4), h = (int)(i - (long long)t * h4);
+    const int t = (int)(i / h8), h = (int)(i - (long long)t * h8);
     const size_t f0 = (size_t)t * top_k;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s[q] = 0.f;
 #pragma unroll 8
     for (int j = 0; j < top_k; ++j) {
-      const int id = __ldg(ids + f0 + j);
-      bool use = id >= 0 && id < E;
-      for (int jj = 0; jj < j; ++jj) use &= __ldg(ids + f0 + jj) != id;
-      if (!use) continue;
+      const int r = __ldg(pos + f0 + j);
+      const bool use = r >= 0;
       const float wj = __ldg(w + f0 + j);
-      const float4 v = __ldg(y + (f0 + j) * h4 + h);
-      s.x += wj * v.x;
-      s.y += wj * v.y;
-      s.z += wj * v.z;
-      s.w += wj * v.w;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      float unit = 0.f;
+      if (use) {
+        v = __ldg(y + (size_t)r * h8 + h);
+        unit = mx_y_unit(__ldg(y_scale + ((size_t)r * h8 + h) / 4));
+      }
+      const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+      const float wu = use ? wj : 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
+        s[2 * q] += wu * (f.x * unit);
+        s[2 * q + 1] += wu * (f.y * unit);
+      }
     }
-    out[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    out[i] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
+                        pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
   }
 }
 
@@ -376,25 +580,29 @@ cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, lo
   return dequantize_t<MM_DTYPE_FP16>(codes, scales, nrows, rows, K, ll, p, grid, st);
 }
 
-cudaError_t launch_mx_gather_quantize(const uint16_t* hidden, const int32_t* sorted,
-                                      const int32_t* offsets, int T, int top_k, int E, int H,
-                                      long long capacity, uint8_t* codes, uint8_t* scales,
-                                      int num_sms, bool after_prev, cudaStream_t st) {
-  const long long want = (capacity + kMxWarps - 1) / kMxWarps;
-  const int grid = (int)(want < 8LL * num_sms ? want : 8LL * num_sms);
-  return launch_k(mx_gather_quantize_kernel, dim3(grid), dim3(kMxThreads), 0, st, after_prev,
-                  reinterpret_cast<const unsigned char*>(hidden), sorted, offsets, E, top_k,
-                  T * top_k, H, codes, scales);
+cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, int top_k, int E,
+                            int H, int32_t* offsets, int32_t* counts, int32_t* cursor,
+                            int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,
+                            cudaStream_t st) {
+  const MxPlaceArgs a = {reinterpret_cast<const unsigned char*>(hidden), ids, offsets, counts,
+                         cursor, pos, codes, scales, err, T, E, top_k, H};
+  if (T * top_k <= kPlaceSmallIds)
+    return launch_k(mx_place_small_kernel, dim3(T), dim3(kPlaceWarps * 32), 0, st, false, a);
+  cudaError_t e = launch_k(mx_group_kernel, dim3(kGroupBlocks), dim3(kGroupThreads), 0, st, false,
+                           a);
+  if (e != cudaSuccess) return e;
+  return launch_k(mx_place_kernel, dim3((T + kMxWarps - 1) / kMxWarps), dim3(kMxThreads), 0, st,
+                  true, a);
 }
 
-cudaError_t launch_mx_combine(const float* y, const int32_t* ids, const float* w, int T, int E,
-                              int top_k, int H, uint16_t* out, int num_sms, bool after_prev,
-                              cudaStream_t st) {
-  const long long want = ((long long)T * (H / 4) + kMxThreads - 1) / kMxThreads;
+cudaError_t launch_mx_combine(const uint16_t* y, const uint8_t* y_scale, const int32_t* pos,
+                              const float* w, int T, int top_k, int H, uint16_t* out, int num_sms,
+                              bool after_prev, cudaStream_t st) {
+  const long long want = ((long long)T * (H / 8) + kMxThreads - 1) / kMxThreads;
   const int grid = (int)(want < 16LL * num_sms ? want : 16LL * num_sms);
   return launch_k(mx_combine_kernel, dim3(grid), dim3(kMxThreads), 0, st, after_prev,
-                  reinterpret_cast<const float4*>(y), ids, w, T, E, top_k, H / 4,
-                  reinterpret_cast<uint2*>(out));
+                  reinterpret_cast<const uint4*>(y), y_scale, pos, w, T, top_k, H / 8,
+                  reinterpret_cast<uint4*>(out));
 }
 
 }  // namespace mm

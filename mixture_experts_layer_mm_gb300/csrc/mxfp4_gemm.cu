@@ -5,7 +5,7 @@
 //   dense    C[r, n] = x_r . w_n                       (bf16 or fp32)
 //   gate_up  act[r, i] = Q(silu(g) u), g = x_r . w_i (gate), u = x_r . w_i (up)
 //            for the rows r of every expert's segment; Q: 4-bit blocks along i
-//   down     y[f, h] = x_r . w_h, f = sorted[r] the (token, slot) of row r
+//   down     y[r, h] = x_r . w_h (fp16 under a power of two for each 32 h)
 //
 // Orientation as in gemm.cu: the weight rows are the MMA's M side (128 rows
 // an MMA), the token rows its N side (any multiple of 16 up to 128). A tile
@@ -26,6 +26,8 @@
 #include "mm.h"
 #include "mm_internal.h"
 #include "mx_device.cuh"
+
+#include <cuda_fp16.h>
 
 namespace mm {
 namespace {
@@ -62,11 +64,10 @@ enum { kDense = 0, kGateUp = 1, kDown = 2 };
 struct MxGemmArgs {
   const int32_t* offsets;  // [E + 1] first row of each segment (NULL: dense)
   const int32_t* counts;   // [E] rows of each segment
-  const int32_t* sorted;   // down: (token, slot) of a row
   const uint8_t* w_scales;
   const uint8_t* x_scales;
   void* out;               // dense: C; gate_up: act codes; down: y
-  uint8_t* act_scales;     // gate_up
+  uint8_t* act_scales;     // gate_up: scales of act; down: block exponents of y
   unsigned* err;
   int E, rows;    // rows: of the one segment of a dense product
   int N, K;       // output columns (gate_up: intermediates), reduction
@@ -365,8 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stopped(&stop_s)) break;
       const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
       const bool has1 = weights_of<MODE>(a, t).has1;
-      int f_t = 0;  // down: output row of column c0 + lane
-      if (MODE == kDown && c0 + lane < t.nrows) f_t = __ldg(a.sorted + t.row0 + c0 + lane);
       if (!warp_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
         break;
@@ -430,16 +429,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.act_scales[mx_scale_offset(t.row0 + c0 + lane, blk, (a.N + 127) / 128)] =
                 real ? my_scale : 0;
         } else if (MODE == kDown) {
+          // Block (row, 32 columns of H) of y: a column of a warp's lanes.
           const int h0 = t.m * 256 + q * 32 + lane;
-          float* y = static_cast<float*>(a.out);
+          __half* y = static_cast<__half*>(a.out) + (size_t)(t.row0 + c0) * a.N + h0;
+          uint8_t* ys = a.act_scales + ((size_t)(t.row0 + c0 + lane) * a.N + t.m * 256 + q * 32) / 32;
+          uint32_t byte0 = 0, byte1 = 0;
+          const bool in0 = h0 < a.N, in1 = h0 + 128 < a.N;  // the same in all lanes
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const int f = __shfl_sync(kAll, f_t, j);
-            if (j < ncol) {
-              float* row = y + (size_t)f * a.N;
-              if (h0 < a.N) row[h0] = __uint_as_float(d0[j]);
-              if (h0 + 128 < a.N) row[h0 + 128] = __uint_as_float(d1[j]);
-            }
+            if (j >= ncol) break;
+            const uint32_t b0 = mx_y_byte(__reduce_max_sync(kAll, d0[j] & 0x7fffffffu));
+            const uint32_t b1 = mx_y_byte(__reduce_max_sync(kAll, d1[j] & 0x7fffffffu));
+            if (lane == j) byte0 = b0;
+            if (lane == j) byte1 = b1;
+            if (in0) y[0] = __float2half_rn(__uint_as_float(d0[j]) * mx_y_inv(b0));
+            if (in1) y[128] = __float2half_rn(__uint_as_float(d1[j]) * mx_y_inv(b1));
+            y += a.N;
+          }
+          if (lane < ncol) {
+            if (in0) ys[0] = (uint8_t)byte0;
+            if (in1) ys[4] = (uint8_t)byte1;
           }
         } else {
           const int n0 = t.m * 256 + q * 32 + lane;
@@ -532,17 +541,16 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
 }
 
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
-                                   const uint8_t* w_scales, const int32_t* sorted,
-                                   const int32_t* offsets, const int32_t* counts, int E, int H,
-                                   int I, long long capacity, long long max_chunks, float* y,
-                                   int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
+                                   const uint8_t* w_scales, const int32_t* offsets,
+                                   const int32_t* counts, int E, int H, int I, long long capacity, long long max_chunks,
+                                   uint16_t* y, uint8_t* y_scale, int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
   MxGemmArgs a = {};
-  a.sorted = sorted;
   a.offsets = offsets;
   a.counts = counts;
   a.w_scales = w_scales;
   a.x_scales = act_scales;
   a.out = y;
+  a.act_scales = y_scale;
   a.err = err;
   a.E = E;
   a.N = H;

@@ -226,7 +226,7 @@ def _experts_ref(d):
     E, I = d["dn"].shape[0], d["dn"].shape[2] * 2
     gu = _np64(mm.mm_mxfp4_dequantize(d["gu"], d["sgu"], torch.float32))
     dn = _np64(mm.mm_mxfp4_dequantize(d["dn"], d["sdn"], torch.float32))
-    y, tol, mag = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+    y, tol, out_mag, block_mag = (np.zeros((T, H)) for _ in range(4))
     for e in range(E):
         t, j = np.nonzero(ids == e)
         if t.size == 0:
@@ -247,9 +247,15 @@ def _experts_ref(d):
         ad = np.abs(dn[e]).T
         np.add.at(y, t, wt * (q @ dn[e].T))
         np.add.at(tol, t, wt * (da @ ad + I * 2.0 ** -23 * ((np.abs(q) + da) @ ad)))
-        np.add.at(mag, t, wt * ((np.abs(q) + da) @ ad))
+        row = np.abs(q @ dn[e].T) + da @ ad
+        np.add.at(out_mag, t, wt * row)
+        np.add.at(block_mag, t, wt * np.repeat(row.reshape(len(t), -1, 32).max(-1), 32, axis=1))
     k = ids.shape[1]
-    tol = tol + (k + 1) * 2.0 ** -24 * mag          # the weighted sum over the slots
+    # Each slot's output is held as fp16 (half a step: 2^-11) under a power of
+    # two that keeps its block's largest value in [2^14, 2^15); below 2^-14
+    # there the step is 2^-24, half of it 2^-39 of that value. Then the weighted
+    # sum over the slots in fp32.
+    tol = tol + (2.0 ** -11 + (k + 2) * 2.0 ** -24) * out_mag + 2.0 ** -39 * block_mag
     return y, tol + (np.abs(y) + tol) * 2.0 ** -8   # one rounding to bf16
 
 

@@ -100,8 +100,8 @@ def test_experts_refusals(L):
     assert call(T=0, hidden=None, ids=None, w=None, gu=None, out=None, ws=None, n=0) == OK
     assert size(4, 96, 8, 64, 2) == -1 and size(-1, 64, 8, 64, 2) == -1
     assert size(1 << 30, 64, 8, 64, 2) == -1
-    # token rows, activations, fp32 rows of the down product
-    assert size(64, 2048, 128, 768, 8) >= 512 * (2048 // 2 + 768 // 2 + 2048 * 4)
+    # token rows, activations, fp16 rows of the down product
+    assert size(64, 2048, 128, 768, 8) >= 512 * (2048 // 2 + 768 // 2 + 2048 * 2)
 
 
 def test_binding_refusals(mmlib):
