@@ -17,10 +17,13 @@
 // The products of two e2m1 values and two powers of two are exact; the
 // accumulation is in fp32 in tensor memory.
 //
-// gate_up's blocks run along i, which is the lane of tensor memory: a block
-// is one column of one warp's 32 lanes, its maximum one redux, and the codes
-// of 8 columns are turned into row order by three exchanges between lanes.
-// The activation is quantised from the fp32 product and is rounded once.
+// gate_up's blocks run along i, which is the lane of tensor memory. The
+// epilogue turns 8 token rows at a time through shared memory, after which four
+// lanes hold a row's block: two exchanges give its maximum, and codes leave
+// four bytes a lane (down and dense: 16 bytes a lane). A warp reduction for
+// every column instead left the epilogue, not the product, in charge (4096
+// tokens: gate_up 90 -> GU_US us, down 93 -> DN_US us). The activation is
+// quantised from the fp32 product and is rounded once.
 #include <algorithm>
 
 #include "mm.h"
@@ -40,17 +43,19 @@ constexpr int kTileBytes = 128 * 128;       // 128 rows of one stage
 constexpr int kScaleStage = 2 * kMxTileBytes;  // scale bytes of 128 rows of one stage
 constexpr int kStageBytes = 3 * kTileBytes + 3 * kScaleStage;
 constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-constexpr int kSmemBytes = kStages * kStageStride + 1024;
+constexpr int kTransposeBytes = 16 * 8 * 36 * 4;  // 16 epilogue warps (see transpose8)
+constexpr int kSmemBytes = kStages * kStageStride + kTransposeBytes + 1024;
 static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 
 // Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue,
-// 18-21 = producers (one per ring slot). There is one pair of accumulators (the
+// 18, 19 = producers (every other ring slot). There is one pair of accumulators (the
 // scales take the columns a second pair would need), so the epilogue first
 // empties tensor memory into registers, 16 warps with a 32 x 32 piece of D0 and
 // of D1 each, hands it back to the MMA warp and then does its work.
 constexpr int kEpiWarp0 = 2, kEpiWarps = 16, kEpiThreads = kEpiWarps * 32;
 constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
-constexpr int kThreads = (kProdWarp0 + kStages) * 32;
+constexpr int kProdWarps = 2;
+constexpr int kThreads = (kProdWarp0 + kProdWarps) * 32;  // 640: 96 registers a thread
 
 // Tensor memory: D0 and D1 (128 columns each), then per ring slot and
 // accumulator the scale columns of the slot's two halves of K: weights, token
@@ -138,9 +143,63 @@ __device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& 
   return w;
 }
 
-__device__ __forceinline__ uint32_t spread4(uint32_t x) {  // nibble n -> byte n
-  x = (x | (x << 8)) & 0x00FF00FFu;
-  return (x | (x << 4)) & 0x0F0F0F0Fu;
+// Epilogue transpose of 32 lanes (output columns) x 8 token rows through this
+// warp's part of shared memory: lane l leaves with columns 8 (l / 8) + i of
+// token row l % 8. Rows of 36 floats keep the 16-byte reads aligned and free
+// of bank conflicts.
+constexpr int kTransposePitch = 36;
+constexpr int kTransposeFloats = 8 * kTransposePitch;
+
+__device__ __forceinline__ void transpose8(float* buf, const float (&x)[8], float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) buf[j * kTransposePitch + lane] = x[j];
+  __syncwarp();
+  const float4* p =
+      reinterpret_cast<const float4*>(buf + (lane & 7) * kTransposePitch + (lane >> 3) * 8);
+  const float4 a = p[0], b = p[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Bits of the largest magnitude of a token row's 32 columns after transpose8.
+__device__ __forceinline__ uint32_t row_amax(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(kAll, m, 8));
+  return max(m, __shfl_xor_sync(kAll, m, 16));
+}
+
+// Columns [n, n + 8) of a dense row that begins at element `row` (N columns):
+// 16-byte stores where N lets every row begin on 16 bytes.
+__device__ __forceinline__ void store_row8(void* out, size_t row, int n, int N, int fp32,
+                                           const float (&v)[8]) {
+  if (fp32) {
+    float* c = static_cast<float*>(out) + row + n;
+    if (N % 8 == 0 && n < N) {
+      reinterpret_cast<float4*>(c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n + i < N) c[i] = v[i];
+    }
+  } else {
+    uint16_t* c = static_cast<uint16_t*>(out) + row + n;
+    if (N % 8 == 0 && n < N) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)f32_to_bf16_bits(v[2 * i]) | ((uint32_t)f32_to_bf16_bits(v[2 * i + 1]) << 16);
+      *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n + i < N) c[i] = f32_to_bf16_bits(v[i]);
+    }
+  }
 }
 
 // Issues one stage of one accumulator: the scale tiles of its `steps` / 2
@@ -247,19 +306,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nk = (a.K + kStageK - 1) / kStageK;  // stages per tile
 
   if (warp >= kProdWarp0) {
-    // ---------------------------------------------------- producers (18-21) ---
-    // Warp 18 + s owns ring slot s: a warp's copies that signal another
-    // barrier than its previous ones would wait for those to land.
-    // As in the MMA warp, all lanes run the loop and one issues.
-    const int slot = warp - kProdWarp0;
+    // ---------------------------------------------------- producers (18, 19) ---
+    // Warp 18 + p fills slots p and p + 2: filling one takes a thread some 400
+    // cycles. As in the MMA warps, all lanes run the loop and one issues.
+    const int first = warp - kProdWarp0;
     const bool leader = elect_one();
     const uint64_t pol_w = l2_policy_evict_normal();
     const uint64_t pol_x = l2_policy_evict_last();
-    const uint32_t st = smem_base + slot * kStageStride;
-    const uint32_t sc = st + 3 * kTileBytes;
-    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
-    uint32_t use = 0;
-    int q = 0;
+    uint32_t ph = 1;  // parity of the empty barriers: the first fill waits for nothing
+    int s = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       if (stopped(&stop_s)) break;
@@ -271,10 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* ws1 = a.w_scales + w.st1 * k_tiles * kMxTileBytes;
       const uint8_t* xs = a.x_scales + (long long)(t.row0 / 128) * k_tiles * kMxTileBytes;
       for (int kb = 0; kb < nk; ++kb) {
-        const bool mine = q == slot;
-        if (++q == kStages) q = 0;
-        if (!mine) continue;
-        if (!warp_wait(eb, (use & 1u) ^ 1u)) {
+        const int slot = s;
+        const uint32_t parity = ph;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if (slot % kProdWarps != first) continue;
+        const uint32_t st = smem_base + slot * kStageStride;
+        const uint32_t sc = st + 3 * kTileBytes;
+        const uint32_t fb = smem_u32(&full[slot]);
+        if (!warp_wait(smem_u32(&empty[slot]), parity)) {
           stop(&stop_s, a.err);
           ok = false;
           break;
@@ -298,7 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_load(sc + 2 * kScaleStage, xs + kt * kMxTileBytes, sb, fb);
         }
         __syncwarp();
-        ++use;
       }
     }
   } else if (warp < 2) {
@@ -382,89 +443,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(tempty));
       if (c0 < t.nrows) {
         const int ncol = min(32, t.nrows - c0);
+        float* buf = reinterpret_cast<float*>(smem_raw + (smem_base - smem_u32(smem_raw)) +
+                                              kStages * kStageStride) +
+                     (warp - kEpiWarp0) * kTransposeFloats;
+        const int tok = lane & 7, part = lane >> 3;  // this lane's place after a transpose
         if (MODE == kGateUp) {
-          // Block (row, q) of the activation: 32 intermediates, one per lane.
-          const int blk = t.m * 4 + q;
+          const int blk = t.m * 4 + q;  // block of 32 intermediates: this warp's lanes
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
-          uint32_t my_scale = 0;
-          uint8_t* codes = static_cast<uint8_t*>(a.out);
-          // The divide and the exponential are off by a few units of the 24th
-          // bit; the 4-bit rounding that follows keeps 2 bits.
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float g = __uint_as_float(d0[j]), u = __uint_as_float(d1[j]);
-            d0[j] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * u);
-          }
+          uint8_t* codes = static_cast<uint8_t*>(a.out) + blk * 16 + part * 4;
+          const int k_tiles_act = (a.N + 127) / 128;
 #pragma unroll
           for (int j0 = 0; j0 < 32; j0 += 8) {
-            if (j0 >= ncol) break;
-            float v[8];
+            if (j0 >= ncol) continue;
+            // The divide and the exponential are off by a few units of the 24th
+            // bit; the 4-bit rounding that follows keeps 2 bits.
+            float x[8], v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint32_t amax = __reduce_max_sync(kAll, d0[j0 + j] & 0x7fffffffu);
-              const uint32_t s = mx_scale_byte(amax);
-              v[j] = __uint_as_float(d0[j0 + j]) * mx_inv_scale(s);
-              if (lane == j0 + j) my_scale = s;
+              const float g = __uint_as_float(d0[j0 + j]), u = __uint_as_float(d1[j0 + j]);
+              x[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
             }
-            // Nibble n of r: this lane's row, column j0 + n. Turn 8 columns x
-            // 32 lanes into 4 bytes (8 lanes' nibbles) of one column a lane.
-            const uint32_t r = mx_pack8(v);
-            const uint32_t o = __shfl_xor_sync(kAll, r, 1);
-            const bool odd = lane & 1;  // odd lanes take columns 4-7
-            uint32_t w = odd ? spread4(o >> 16) | (spread4(r >> 16) << 4)
-                             : spread4(r & 0xFFFFu) | (spread4(o & 0xFFFFu) << 4);
-            // w: bytes of 4 columns, lanes pair i = lane / 2; transpose 4 x 4
-            // over i & 3 (lane bits 1 and 2).
-            uint32_t p = __shfl_xor_sync(kAll, w, 2);
-            w = (lane & 2) ? __byte_perm(p, w, 0x7351) : __byte_perm(w, p, 0x6240);
-            // even i: columns 0, 2 as (own, other); odd i: columns 1, 3
-            p = __shfl_xor_sync(kAll, w, 4);
-            w = (lane & 4) ? __byte_perm(p, w, 0x7632) : __byte_perm(w, p, 0x5410);
-            const int col = j0 + (odd ? 4 : 0) + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2;
-            if (real && col < ncol)
-              *reinterpret_cast<uint32_t*>(codes + (size_t)(t.row0 + c0 + col) * (a.N / 2) +
-                                           blk * 16 + (lane >> 3) * 4) = w;
-          }
-          if (lane < ncol)
-            a.act_scales[mx_scale_offset(t.row0 + c0 + lane, blk, (a.N + 127) / 128)] =
-                real ? my_scale : 0;
-        } else if (MODE == kDown) {
-          // Block (row, 32 columns of H) of y: a column of a warp's lanes.
-          const int h0 = t.m * 256 + q * 32 + lane;
-          __half* y = static_cast<__half*>(a.out) + (size_t)(t.row0 + c0) * a.N + h0;
-          uint8_t* ys = a.act_scales + ((size_t)(t.row0 + c0 + lane) * a.N + t.m * 256 + q * 32) / 32;
-          uint32_t byte0 = 0, byte1 = 0;
-          const bool in0 = h0 < a.N, in1 = h0 + 128 < a.N;  // the same in all lanes
+            transpose8(buf, x, v);
+            const uint32_t sb = mx_scale_byte(row_amax(v));
+            const float inv = mx_inv_scale(sb);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= ncol) break;
-            const uint32_t b0 = mx_y_byte(__reduce_max_sync(kAll, d0[j] & 0x7fffffffu));
-            const uint32_t b1 = mx_y_byte(__reduce_max_sync(kAll, d1[j] & 0x7fffffffu));
-            if (lane == j) byte0 = b0;
-            if (lane == j) byte1 = b1;
-            if (in0) y[0] = __float2half_rn(__uint_as_float(d0[j]) * mx_y_inv(b0));
-            if (in1) y[128] = __float2half_rn(__uint_as_float(d1[j]) * mx_y_inv(b1));
-            y += a.N;
-          }
-          if (lane < ncol) {
-            if (in0) ys[0] = (uint8_t)byte0;
-            if (in1) ys[4] = (uint8_t)byte1;
+            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            const int r = j0 + tok;
+            if (r < ncol) {
+              const long long row = t.row0 + c0 + r;
+              if (real)
+                *reinterpret_cast<uint32_t*>(codes + row * (a.N / 2)) = mx_pack8(v);
+              if (part == 0) a.act_scales[mx_scale_offset(row, blk, k_tiles_act)] = real ? sb : 0;
+            }
           }
         } else {
-          const int n0 = t.m * 256 + q * 32 + lane;
-          const size_t base = (size_t)(t.row0 + c0) * a.N;
+          // Columns n0 + [0, 32) of the output, 8 a lane after the transpose.
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= ncol) break;
-            const size_t at = base + (size_t)j * a.N + n0;
-            if (a.out_fp32) {
-              float* c = static_cast<float*>(a.out);
-              if (n0 < a.N) c[at] = __uint_as_float(d0[j]);
-              if (has1 && n0 + 128 < a.N) c[at + 128] = __uint_as_float(d1[j]);
-            } else {
-              uint16_t* c = static_cast<uint16_t*>(a.out);
-              if (n0 < a.N) c[at] = f32_to_bf16_bits(__uint_as_float(d0[j]));
-              if (has1 && n0 + 128 < a.N) c[at + 128] = f32_to_bf16_bits(__uint_as_float(d1[j]));
+          for (int half = 0; half < 2; ++half) {
+            const int n0 = t.m * 256 + half * 128 + q * 32;
+            if (n0 >= a.N) continue;
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+              if (j0 >= ncol) continue;
+              float x[8], v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                x[j] = __uint_as_float(half == 0 ? d0[j0 + j] : d1[j0 + j]);
+              transpose8(buf, x, v);
+              const int r = j0 + tok, n = n0 + part * 8;
+              const size_t row = (size_t)(t.row0 + c0 + r);
+              if (MODE == kDown) {
+                const uint32_t byte = mx_y_byte(row_amax(v));
+                const float inv = mx_y_inv(byte);
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __half2 p = __floats2half2_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                if (r < ncol) {
+                  *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + row * a.N + n) =
+                      make_uint4(w[0], w[1], w[2], w[3]);
+                  if (part == 0) a.act_scales[(row * a.N + n) / 32] = (uint8_t)byte;
+                }
+              } else if (r < ncol) {
+                store_row8(a.out, row * a.N, n, a.N, a.out_fp32, v);
+              }
             }
           }
         }
