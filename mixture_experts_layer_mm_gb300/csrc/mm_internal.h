@@ -160,6 +160,11 @@ bool make_tensor_map_sw128(CUtensorMap* m, const void* base, uint32_t rank,
 bool make_tensor_map_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K,
                            uint32_t box_rows);
 
+// Tensor map of a 4-D byte tensor (dims[0] contiguous, strides[i] the byte
+// stride of dimension i + 1), with the 128-byte swizzle or none.
+bool make_tensor_map_bytes_4d(CUtensorMap* m, const void* base, const uint64_t* dims,
+                              const uint64_t* strides, const uint32_t* box, bool swizzle128);
+
 // Whether the gate_up GEMM gathers token rows with TMA tile::gather4 (few rows
 // per expert) rather than with cp.async loader warps.
 bool gate_up_gathers_rows(int T, int top_k, int E);

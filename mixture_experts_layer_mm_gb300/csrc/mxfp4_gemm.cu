@@ -17,13 +17,15 @@
 // The products of two e2m1 values and two powers of two are exact; the
 // accumulation is in fp32 in tensor memory.
 //
-// gate_up's blocks run along i, which is the lane of tensor memory. The
-// epilogue turns 8 token rows at a time through shared memory, after which four
-// lanes hold a row's block: two exchanges give its maximum, and codes leave
-// four bytes a lane (down and dense: 16 bytes a lane). A warp reduction for
-// every column instead left the epilogue, not the product, in charge (4096
-// tokens: gate_up 90 -> GU_US us, down 93 -> DN_US us). The activation is
-// quantised from the fp32 product and is rounded once.
+// gate_up's blocks (and those of y) run along the output columns, which are the
+// lanes of tensor memory. The weight tile's rows are loaded in an order (row 4 a
+// + j of a group of 32 at place 8 j + a) that gives a thread of a 16 x 256-bit
+// tensor-memory load four consecutive columns of a token row: a block's maximum
+// is three maxima in the thread and three exchanges for two rows at once, and
+// results leave the thread as they are. (A warp reduction for every column took
+// 90 us for gate_up and 93 for down at 4096 tokens, a transpose through shared
+// memory, whose bandwidth the MMAs need, 63 and 100; this: GU_US and DN_US.) The
+// activation is quantised from the fp32 product and is rounded once.
 #include <algorithm>
 
 #include "mm.h"
@@ -43,8 +45,7 @@ constexpr int kTileBytes = 128 * 128;       // 128 rows of one stage
 constexpr int kScaleStage = 2 * kMxTileBytes;  // scale bytes of 128 rows of one stage
 constexpr int kStageBytes = 3 * kTileBytes + 3 * kScaleStage;
 constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-constexpr int kTransposeBytes = 16 * 8 * 36 * 4;  // 16 epilogue warps (see transpose8)
-constexpr int kSmemBytes = kStages * kStageStride + kTransposeBytes + 1024;
+constexpr int kSmemBytes = kStages * kStageStride + 1024;
 static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 
 // Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue,
@@ -52,7 +53,7 @@ static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 // scales take the columns a second pair would need), so the epilogue first
 // empties tensor memory into registers, 16 warps with a 32 x 32 piece of D0 and
 // of D1 each, hands it back to the MMA warp and then does its work.
-constexpr int kEpiWarp0 = 2, kEpiWarps = 16, kEpiThreads = kEpiWarps * 32;
+constexpr int kEpiWarp0 = 2, kEpiWarps = 16;
 constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kProdWarps = 2;
 constexpr int kThreads = (kProdWarp0 + kProdWarps) * 32;  // 640: 96 registers a thread
@@ -143,63 +144,31 @@ __device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& 
   return w;
 }
 
-// Epilogue transpose of 32 lanes (output columns) x 8 token rows through this
-// warp's part of shared memory: lane l leaves with columns 8 (l / 8) + i of
-// token row l % 8. Rows of 36 floats keep the 16-byte reads aligned and free
-// of bank conflicts.
-constexpr int kTransposePitch = 36;
-constexpr int kTransposeFloats = 8 * kTransposePitch;
-
-__device__ __forceinline__ void transpose8(float* buf, const float (&x)[8], float (&v)[8]) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) buf[j * kTransposePitch + lane] = x[j];
-  __syncwarp();
-  const float4* p =
-      reinterpret_cast<const float4*>(buf + (lane & 7) * kTransposePitch + (lane >> 3) * 8);
-  const float4 a = p[0], b = p[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-// Bits of the largest magnitude of a token row's 32 columns after transpose8.
-__device__ __forceinline__ uint32_t row_amax(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(kAll, m, 8));
-  return max(m, __shfl_xor_sync(kAll, m, 16));
-}
-
-// Columns [n, n + 8) of a dense row that begins at element `row` (N columns):
-// 16-byte stores where N lets every row begin on 16 bytes.
-__device__ __forceinline__ void store_row8(void* out, size_t row, int n, int N, int fp32,
-                                           const float (&v)[8]) {
-  if (fp32) {
-    float* c = static_cast<float*>(out) + row + n;
-    if (N % 8 == 0 && n < N) {
-      reinterpret_cast<float4*>(c)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(c)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < N) c[i] = v[i];
-    }
-  } else {
-    uint16_t* c = static_cast<uint16_t*>(out) + row + n;
-    if (N % 8 == 0 && n < N) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)f32_to_bf16_bits(v[2 * i]) | ((uint32_t)f32_to_bf16_bits(v[2 * i + 1]) << 16);
-      *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < N) c[i] = f32_to_bf16_bits(v[i]);
-    }
+// What one thread of an epilogue warp holds of a 32 x 32 piece of an
+// accumulator: output columns col + j (j < 4, consecutive thanks to the row
+// order of the weight tile) of token rows row(g, c) = 8 g + 2 (lane % 4) + c.
+struct Piece {
+  uint32_t r[2][16];
+  __device__ __forceinline__ float at(int j, int g, int c) const {
+    return __uint_as_float(r[j >> 1][4 * g + 2 * (j & 1) + c]);
   }
+};
+
+__device__ __forceinline__ void load_piece(uint32_t taddr, Piece& p) {
+  tmem_ld_16x256b_x4(taddr, p.r[0]);                // lanes 0-15 of the quarter
+  tmem_ld_16x256b_x4(taddr + (16u << 16), p.r[1]);  // lanes 16-31
+}
+
+// Largest magnitude of the piece's 32 columns for the token rows (g, 0) in the
+// low and (g, 1) in the high half: the upper 16 bits of the float, which hold
+// its exponent. A NaN gives an exponent of 255.
+__device__ __forceinline__ uint32_t amax_pair(const float (&a)[4], const float (&b)[4]) {
+  const float x = max_nan(max_nan(fabsf(a[0]), fabsf(a[1])), max_nan(fabsf(a[2]), fabsf(a[3])));
+  const float y = max_nan(max_nan(fabsf(b[0]), fabsf(b[1])), max_nan(fabsf(b[2]), fabsf(b[3])));
+  uint32_t m = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 4));
+  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 8));
+  return __vmaxu2(m, __shfl_xor_sync(kAll, m, 16));
 }
 
 // Issues one stage of one accumulator: the scale tiles of its `steps` / 2
@@ -227,10 +196,12 @@ __device__ __forceinline__ void issue_stage(uint32_t st, int a_tile, uint32_t ts
   }
 }
 
-template <int MODE>
+template <int MODE, bool PERM>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const __grid_constant__ CUtensorMap tmX32, const MxGemmArgs a) {
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
+                   const MxGemmArgs a) {
+  static_assert(PERM || MODE == kDense, "blocks along the output columns need the row order");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
   __shared__ uint32_t tmem_base_s;
@@ -278,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&empty[s]), 2);  // one commit of each issuer
     }
     mbar_init(smem_u32(tfull), 2);
-    mbar_init(smem_u32(tempty), kEpiThreads);
+    mbar_init(smem_u32(tempty), kEpiWarps);
     mbar_init(smem_u32(done), 2);
     stop_s = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&tmW);
+    if (PERM) tma_prefetch_desc(&tmS);
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmX32);
   }
@@ -322,8 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const WeightAt w = weights_of<MODE>(a, t);
       // Token rows: one box of 128, or up to three boxes of 32.
       const int nbox = t.nrows > 96 ? 4 : (t.nrows + 31) / 32;
-      const uint8_t* ws0 = a.w_scales + w.st0 * k_tiles * kMxTileBytes;
-      const uint8_t* ws1 = a.w_scales + w.st1 * k_tiles * kMxTileBytes;
       const uint8_t* xs = a.x_scales + (long long)(t.row0 / 128) * k_tiles * kMxTileBytes;
       for (int kb = 0; kb < nk; ++kb) {
         const int slot = s;
@@ -344,10 +314,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) {
           const int kt = 2 * kb;  // first scale tile of the stage
           const uint32_t sb = min(2, k_tiles - kt) * kMxTileBytes;
+          const uint32_t wsb = PERM ? kScaleStage : sb;  // a box is always whole
           mbar_arrive_expect_tx(
-              fb, (w.has1 ? 2u : 1u) * (kTileBytes + sb) + (uint32_t)nbox * 4096u + sb);
-          tma_load_2d(st, &tmW, fb, kb * 128, w.row0, pol_w);
-          if (w.has1) tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
+              fb, (w.has1 ? 2u : 1u) * (kTileBytes + wsb) + (uint32_t)nbox * 4096u + sb);
+          if (PERM) {
+            tma_load_4d(st, &tmW, fb, kb * 128, w.row0 / 32, pol_w);
+            tma_load_4d(sc, &tmS, fb, 0, (int)(w.st0 * k_tiles) + kt, pol_w);
+            if (w.has1) {
+              tma_load_4d(st + kTileBytes, &tmW, fb, kb * 128, w.row1 / 32, pol_w);
+              tma_load_4d(sc + kScaleStage, &tmS, fb, 0, (int)(w.st1 * k_tiles) + kt, pol_w);
+            }
+          } else {
+            tma_load_2d(st, &tmW, fb, kb * 128, w.row0, pol_w);
+            bulk_load(sc, a.w_scales + (w.st0 * k_tiles + kt) * kMxTileBytes, sb, fb);
+            if (w.has1) {
+              tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
+              bulk_load(sc + kScaleStage, a.w_scales + (w.st1 * k_tiles + kt) * kMxTileBytes, sb,
+                        fb);
+            }
+          }
           if (nbox == 4) {
             tma_load_2d(st + 2 * kTileBytes, &tmX, fb, kb * 128, t.row0, pol_x);
           } else {
@@ -355,8 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX32, fb, kb * 128, t.row0 + 32 * b,
                           pol_x);
           }
-          bulk_load(sc, ws0 + kt * kMxTileBytes, sb, fb);
-          if (w.has1) bulk_load(sc + kScaleStage, ws1 + kt * kMxTileBytes, sb, fb);
           bulk_load(sc + 2 * kScaleStage, xs + kt * kMxTileBytes, sb, fb);
         }
         __syncwarp();
@@ -433,83 +416,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      uint32_t d0[32], d1[32];
-      if (c0 < t.nrows) {
-        tmem_ld_32x32b_x32(tb + c0, d0);
-        tmem_ld_32x32b_x32(tb + kBN + c0, d1);
-        tmem_wait_ld();
-      }
-      tc_fence_before();
-      mbar_arrive(smem_u32(tempty));
-      if (c0 < t.nrows) {
-        const int ncol = min(32, t.nrows - c0);
-        float* buf = reinterpret_cast<float*>(smem_raw + (smem_base - smem_u32(smem_raw)) +
-                                              kStages * kStageStride) +
-                     (warp - kEpiWarp0) * kTransposeFloats;
-        const int tok = lane & 7, part = lane >> 3;  // this lane's place after a transpose
+      if constexpr (PERM) {
+        Piece p0, p1;
+        if (c0 < t.nrows) {
+          load_piece(tb + c0, p0);
+          load_piece(tb + kBN + c0, p1);
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(tempty));
+        const int ncol = t.nrows - c0;  // token rows of this piece (may exceed 32)
+        if (ncol <= 0) continue;
+        const long long row0 = t.row0 + c0 + 2 * (lane & 3);
+        const int col4 = (lane >> 2) * 4;
         if (MODE == kGateUp) {
-          const int blk = t.m * 4 + q;  // block of 32 intermediates: this warp's lanes
+          const int blk = t.m * 4 + q;       // block of 32 intermediates: this warp's lanes
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
-          uint8_t* codes = static_cast<uint8_t*>(a.out) + blk * 16 + part * 4;
+          uint8_t* codes = static_cast<uint8_t*>(a.out) + row0 * (a.N / 2) + (blk * 32 + col4) / 2;
           const int k_tiles_act = (a.N + 127) / 128;
+          uint32_t my_scale = 0;  // of token row lane / 4's place among the thread's eight
 #pragma unroll
-          for (int j0 = 0; j0 < 32; j0 += 8) {
-            if (j0 >= ncol) continue;
-            // The divide and the exponential are off by a few units of the 24th
-            // bit; the 4-bit rounding that follows keeps 2 bits.
-            float x[8], v[8];
+          for (int g = 0; g < 4; ++g) {
+            float x[2][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float g = __uint_as_float(d0[j0 + j]), u = __uint_as_float(d1[j0 + j]);
-              x[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
-            }
-            transpose8(buf, x, v);
-            const uint32_t sb = mx_scale_byte(row_amax(v));
-            const float inv = mx_inv_scale(sb);
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= inv;
-            const int r = j0 + tok;
-            if (r < ncol) {
-              const long long row = t.row0 + c0 + r;
-              if (real)
-                *reinterpret_cast<uint32_t*>(codes + row * (a.N / 2)) = mx_pack8(v);
-              if (part == 0) a.act_scales[mx_scale_offset(row, blk, k_tiles_act)] = real ? sb : 0;
+              for (int j = 0; j < 4; ++j) {
+                // The divide and the exponential are off by a few units of the
+                // 24th bit; the 4-bit rounding that follows keeps 2 bits.
+                const float gate = p0.at(j, g, c), up = p1.at(j, g, c);
+                x[c][j] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+              }
+            const uint32_t m = amax_pair(x[0], x[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t sb = mx_scale_byte(c == 0 ? m << 16 : m & 0xFFFF0000u);
+              const float inv = mx_inv_scale(sb);
+              if ((lane >> 2) == 2 * g + c) my_scale = sb;
+              const uint16_t two = mx_pack4(x[c][0] * inv, x[c][1] * inv, x[c][2] * inv,
+                                            x[c][3] * inv);
+              if (real && 8 * g + 2 * (lane & 3) + c < ncol)
+                *reinterpret_cast<uint16_t*>(codes + (8 * g + c) * (size_t)(a.N / 2)) = two;
             }
           }
+          // Lanes of one lane / 4 write the scales of token rows 8 g + 2 (lane % 4)
+          // + c with 2 g + c = lane / 4.
+          const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
+          if (r < ncol)
+            a.act_scales[mx_scale_offset(t.row0 + c0 + r, blk, k_tiles_act)] = real ? my_scale : 0;
         } else {
-          // Columns n0 + [0, 32) of the output, 8 a lane after the transpose.
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int n0 = t.m * 256 + half * 128 + q * 32;
-            if (n0 >= a.N) continue;
+            const Piece& p = half == 0 ? p0 : p1;
+            const int n = t.m * 256 + half * 128 + q * 32;
+            if (n >= a.N) continue;
+            const size_t at = (size_t)row0 * a.N + n + col4;
+            uint32_t my_byte = 0;
 #pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 8) {
-              if (j0 >= ncol) continue;
-              float x[8], v[8];
+            for (int g = 0; g < 4; ++g) {
+              float x[2][4];
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                x[j] = __uint_as_float(half == 0 ? d0[j0 + j] : d1[j0 + j]);
-              transpose8(buf, x, v);
-              const int r = j0 + tok, n = n0 + part * 8;
-              const size_t row = (size_t)(t.row0 + c0 + r);
-              if (MODE == kDown) {
-                const uint32_t byte = mx_y_byte(row_amax(v));
-                const float inv = mx_y_inv(byte);
-                uint32_t w[4];
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __half2 p = __floats2half2_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                for (int j = 0; j < 4; ++j) x[c][j] = p.at(j, g, c);
+              uint32_t m = 0;
+              if (MODE == kDown) m = amax_pair(x[0], x[1]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const bool in = 8 * g + 2 * (lane & 3) + c < ncol;
+                const size_t to = at + (size_t)(8 * g + c) * a.N;
+                if (MODE == kDown) {
+                  const uint32_t byte = mx_y_byte(c == 0 ? m << 16 : m & 0xFFFF0000u);
+                  const float inv = mx_y_inv(byte);
+                  if ((lane >> 2) == 2 * g + c) my_byte = byte;
+                  const __half2 lo = __floats2half2_rn(x[c][0] * inv, x[c][1] * inv);
+                  const __half2 hi = __floats2half2_rn(x[c][2] * inv, x[c][3] * inv);
+                  if (in)
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                   *reinterpret_cast<const uint32_t*>(&hi));
+                } else if (a.out_fp32) {
+                  if (in)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) =
+                        make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+                } else if (in) {
+                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+                      make_uint2(bf16x2(x[c][0], x[c][1]), bf16x2(x[c][2], x[c][3]));
                 }
-                if (r < ncol) {
-                  *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + row * a.N + n) =
-                      make_uint4(w[0], w[1], w[2], w[3]);
-                  if (part == 0) a.act_scales[(row * a.N + n) / 32] = (uint8_t)byte;
-                }
-              } else if (r < ncol) {
-                store_row8(a.out, row * a.N, n, a.N, a.out_fp32, v);
               }
             }
+            if (MODE == kDown) {
+              const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
+              if (r < ncol)
+                a.act_scales[((size_t)(t.row0 + c0 + r) * a.N + n) / 32] = (uint8_t)my_byte;
+            }
+          }
+        }
+      } else {
+        // Any N: lane = output column, one value of 32 token rows a lane.
+        uint32_t d0[32], d1[32];
+        if (c0 < t.nrows) {
+          tmem_ld_32x32b_x32(tb + c0, d0);
+          tmem_ld_32x32b_x32(tb + kBN + c0, d1);
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(tempty));
+        const int ncol = t.nrows - c0, n0 = t.m * 256 + q * 32 + lane;
+        const bool in0 = n0 < a.N, in1 = n0 + 128 < a.N;
+        size_t at = (size_t)(t.row0 + c0) * a.N + n0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, at += a.N) {
+          if (j >= ncol) break;
+          const float x0 = __uint_as_float(d0[j]), x1 = __uint_as_float(d1[j]);
+          if (a.out_fp32) {
+            float* c = static_cast<float*>(a.out);
+            if (in0) c[at] = x0;
+            if (in1) c[at + 128] = x1;
+          } else {
+            uint16_t* c = static_cast<uint16_t*>(a.out);
+            if (in0) c[at] = f32_to_bf16_bits(x0);
+            if (in1) c[at + 128] = f32_to_bf16_bits(x1);
           }
         }
       }
@@ -524,22 +553,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// w: w_rows rows of weight codes; x: x_rows rows of token codes.
-template <int MODE>
-cudaError_t launch_mode(const uint8_t* w, long long w_rows, const uint8_t* x, long long x_rows,
-                        const MxGemmArgs& a, long long max_tiles, int num_sms, bool after_prev,
-                        cudaStream_t st) {
+// w: w_rows rows of weight codes (scale_tiles tiles of 512 bytes); x: x_rows
+// rows of token codes.
+template <int MODE, bool PERM>
+cudaError_t launch_mode(const uint8_t* w, long long w_rows, long long scale_tiles, const uint8_t* x,
+                        long long x_rows, const MxGemmArgs& a, long long max_tiles, int num_sms,
+                        bool after_prev, cudaStream_t st) {
   static DeviceFlags attr_done;
-  if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE>, kSmemBytes); e != cudaSuccess)
+  if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE, PERM>, kSmemBytes);
+      e != cudaSuccess)
     return e;
-  CUtensorMap tmW, tmX, tmX32;
-  if (!make_tensor_map_codes(&tmW, w, (uint64_t)w_rows, (uint64_t)a.K, 128) ||
-      !make_tensor_map_codes(&tmX, x, (uint64_t)x_rows, (uint64_t)a.K, 128) ||
-      !make_tensor_map_codes(&tmX32, x, (uint64_t)x_rows, (uint64_t)a.K, 32))
-    return cudaErrorInvalidValue;
+  CUtensorMap tmW, tmS = {}, tmX, tmX32;
+  const uint64_t K = (uint64_t)a.K;
+  bool ok = make_tensor_map_codes(&tmX, x, (uint64_t)x_rows, K, 128) &&
+            make_tensor_map_codes(&tmX32, x, (uint64_t)x_rows, K, 32);
+  if (PERM) {
+    // Shared-memory row p of a group of 32 takes weight row 4 (p % 8) + p / 8:
+    // the boxes run over 8 rows a stride of 4 apart, 4 rows, 4 groups; the
+    // scales' 16-byte rows likewise.
+    const uint64_t wd[4] = {K / 2, 8, 4, (uint64_t)w_rows / 32};
+    const uint64_t ws[3] = {2 * K, K / 2, 16 * K};
+    const uint32_t wb[4] = {128, 8, 4, 4};
+    const uint64_t sd[4] = {16, 8, 4, (uint64_t)scale_tiles};
+    const uint64_t ss[3] = {64, 16, kMxTileBytes};
+    const uint32_t sbx[4] = {16, 8, 4, 2};
+    ok = ok && make_tensor_map_bytes_4d(&tmW, w, wd, ws, wb, true) &&
+         make_tensor_map_bytes_4d(&tmS, a.w_scales, sd, ss, sbx, false);
+  } else {
+    ok = ok && make_tensor_map_codes(&tmW, w, (uint64_t)w_rows, K, 128);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   const int grid = (int)std::min<long long>(max_tiles, num_sms);
-  return launch_k(mx_gemm_kernel<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, after_prev, tmW,
-                  tmX, tmX32, a);
+  return launch_k(mx_gemm_kernel<MODE, PERM>, dim3(grid), dim3(kThreads), kSmemBytes, st,
+                  after_prev, tmW, tmS, tmX, tmX32, a);
 }
 
 }  // namespace
@@ -559,7 +605,13 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   a.n_mtiles = (N + 255) / 256;
   a.out_fp32 = out_fp32 ? 1 : 0;
   const long long tiles = (long long)((M + kBN - 1) / kBN) * a.n_mtiles;
-  return launch_mode<kDense>(b_codes, N, a_codes, M, a, tiles, num_sms, false, st);
+  const long long scale_tiles = (long long)mx_tiles(N) * mx_tiles(K);
+  // Whole groups of 32 output columns: four a lane, in wide stores.
+  if (N % 32 == 0)
+    return launch_mode<kDense, true>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
+                                     st);
+  return launch_mode<kDense, false>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
+                                    st);
 }
 
 cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
@@ -580,8 +632,8 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
   a.N = I;
   a.K = H;
   a.n_mtiles = (I + 127) / 128;
-  return launch_mode<kGateUp>(w, 2LL * E * I, xs, capacity, a, max_chunks * a.n_mtiles, num_sms,
-                              after_prev, st);
+  return launch_mode<kGateUp, true>(w, 2LL * E * I, 2LL * E * mx_tiles(I) * mx_tiles(H), xs, capacity,
+                                    a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
 }
 
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
@@ -600,8 +652,8 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
   a.N = H;
   a.K = I;
   a.n_mtiles = (H + 255) / 256;
-  return launch_mode<kDown>(w, (long long)E * H, act, capacity, a, max_chunks * a.n_mtiles, num_sms,
-                            after_prev, st);
+  return launch_mode<kDown, true>(w, (long long)E * H, (long long)E * mx_tiles(H) * mx_tiles(I), act,
+                                  capacity, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
 }
 
 }  // namespace mm
