@@ -38,7 +38,7 @@ bool is_dtype(int d) { return d == MM_DTYPE_FP32 || d == MM_DTYPE_BF16 || d == M
 
 // Workspace of the 4-bit experts.
 struct ExpertsLayout {
-  size_t offsets, counts, cursor, pos, xs, xs_scales, act, act_scales, y, y_scale, total;
+  size_t counts, cursor, pos, xs, xs_scales, act, act_scales, y, y_scale, total;
   long long capacity, max_chunks;
 };
 
@@ -61,7 +61,6 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
     off += round256(bytes);
     return o;
   };
-  L.offsets = take((size_t)(E + 1) * 4);
   L.counts = take((size_t)E * 4);
   L.cursor = take((size_t)E * 4);
   L.pos = take((size_t)Tk * 4);
@@ -216,7 +215,6 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
   unsigned* status = nullptr;
   if ((rc = current_device_info(&sms, &status)) != MM_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int32_t* offsets = at<int32_t>(workspace, L.offsets);
   int32_t* counts = at<int32_t>(workspace, L.counts);
   uint8_t* xs = at<uint8_t>(workspace, L.xs);
   uint8_t* xs_scales = at<uint8_t>(workspace, L.xs_scales);
@@ -226,15 +224,15 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
   uint16_t* y = at<uint16_t>(workspace, L.y);
   uint8_t* y_scale = at<uint8_t>(workspace, L.y_scale);
   const long long rows = mx_tiles(L.capacity) * kMxTile;
-  cudaError_t e = launch_mx_place(hidden, topk_ids, T, top_k, E, H, offsets, counts,
+  cudaError_t e = launch_mx_place(hidden, topk_ids, T, top_k, E, H, counts,
                                   at<int32_t>(workspace, L.cursor), pos, xs, xs_scales,
                                   status, st);
   if (e == cudaSuccess)
-    e = launch_mx_experts_gate_up(xs, xs_scales, w_gate_up, w_gate_up_scales, offsets, counts, E, I,
-                                  H, rows, L.max_chunks, act, act_scales, sms, status, true, st);
+    e = launch_mx_experts_gate_up(xs, xs_scales, w_gate_up, w_gate_up_scales, counts, topk_ids, T,
+                                  top_k, E, I, H, rows, L.max_chunks, act, act_scales, sms, status, true, st);
   if (e == cudaSuccess)
-    e = launch_mx_experts_down(act, act_scales, w_down, w_down_scales, offsets, counts, E,
-                               H, I, rows, L.max_chunks, y, y_scale, sms, status, true, st);
+    e = launch_mx_experts_down(act, act_scales, w_down, w_down_scales, counts, topk_ids, T,
+                               top_k, E, H, I, rows, L.max_chunks, y, y_scale, sms, status, true, st);
   if (e == cudaSuccess)
     e = launch_mx_combine(y, y_scale, pos, topk_w, T, top_k, H, out, sms, true, st);
   return cuda_status(e);

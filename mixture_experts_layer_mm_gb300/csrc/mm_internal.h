@@ -258,6 +258,8 @@ cudaError_t launch_route_logits_backward(const void* logits, bool is_bf16, const
 
 // Rows of one chunk of the 4-bit products; segments begin at multiples of it.
 constexpr int kMxBlockM = 128;
+// Up to this many slots every kernel of the 4-bit experts groups them by itself.
+constexpr int kMxEarlyIds = 2048;
 
 // Microscaled 4-bit rows (mxfp4.cu): dtype is an MM_DTYPE, K % 32 == 0.
 cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int rows, int K,
@@ -265,11 +267,11 @@ cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int ro
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long batch,
                                  int rows, int K, void* out, int dtype, cudaStream_t st);
 // The 4-bit experts' grouping and token rows: segments of kMxBlockM-row
-// multiples (offsets [E + 1], counts [E]), pos[f] the row of slot f = t top_k +
+// multiples (counts [E] rows in each), pos[f] the row of slot f = t top_k +
 // j (-1: dropped id), and that row of codes / scales = hidden[t] quantised.
 // cursor: [E] scratch.
 cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, int top_k, int E,
-                            int H, int32_t* offsets, int32_t* counts, int32_t* cursor,
+                            int H, int32_t* counts, int32_t* cursor,
                             int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,
                             cudaStream_t st);
 // out[t] = bf16(sum_j w[t,j] y[pos[t top_k + j]]), y fp16 under y_scale (one
@@ -280,19 +282,21 @@ cudaError_t launch_mx_combine(const uint16_t* y, const uint8_t* y_scale, const i
 
 // Products of 4-bit matrices (mxfp4_gemm.cu). The experts' segments begin at
 // multiples of kMxBlockM rows (capacity rows in all) and make at most
-// max_chunks chunks of kMxBlockM rows.
+// max_chunks chunks of kMxBlockM rows. ids [T, top_k]: the routing; with at most
+// kMxEarlyIds slots it is read in place of counts, and before the kernels that
+// precede the launch on its stream have completed (they must not write it).
 cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                            const uint8_t* b_scales, int M, int N, int K, void* c, bool out_fp32,
                            int num_sms, unsigned* err, cudaStream_t st);
 cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
                                       const uint8_t* w, const uint8_t* w_scales,
-                                      const int32_t* offsets, const int32_t* counts, int E, int I,
-                                      int H, long long capacity, long long max_chunks,
+                                      const int32_t* counts, const int32_t* ids, int T,
+                                      int top_k, int E, int I, int H, long long capacity, long long max_chunks,
                                       uint8_t* act, uint8_t* act_scales, int num_sms,
                                       unsigned* err, bool after_prev, cudaStream_t st);
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
-                                   const uint8_t* w_scales, const int32_t* offsets,
-                                   const int32_t* counts, int E, int H, int I, long long capacity, long long max_chunks,
+                                   const uint8_t* w_scales, const int32_t* counts,
+                                   const int32_t* ids, int T, int top_k, int E, int H, int I, long long capacity, long long max_chunks,
                                    uint16_t* y, uint8_t* y_scale, int num_sms, unsigned* err, bool after_prev, cudaStream_t st);
 
 }  // namespace mm

@@ -300,7 +300,6 @@ __device__ __forceinline__ void write_places(const float (&v)[16], int c, int H,
 struct MxPlaceArgs {
   const unsigned char* hidden;
   const int32_t* ids;
-  int32_t* offsets;  // [E + 1]
   int32_t* counts;   // [E]
   int32_t* cursor;   // [E] next free row (large batches)
   int32_t* pos;      // [T * top_k] row of a slot, -1 if dropped
@@ -329,14 +328,13 @@ __device__ __forceinline__ void scan_segments(const int* cnt, int E, int* off) {
   if (lane == 0) off[E] = run;
 }
 
-// Up to kPlaceSmallIds slots: one block a token, one launch. Every block counts
+// Up to kMxEarlyIds slots: one block a token, one launch. Every block counts
 // all slots itself (a few thousand shared-memory adds) and ranks its token
 // among the earlier ones, while its part of the row is on the way.
-constexpr int kPlaceSmallIds = 2048;
 constexpr int kPlaceWarps = 4;
 
 __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const MxPlaceArgs a) {
-  __shared__ int ids_s[kPlaceSmallIds];
+  __shared__ int ids_s[kMxEarlyIds];
   __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kNT = kPlaceWarps * 32;
@@ -366,11 +364,6 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
   __syncthreads();
   if (warp == 0) scan_segments(tot, a.E, off);
   __syncthreads();
-  if (t == 0)
-    for (int e = tid; e <= a.E; e += kNT) {
-      a.offsets[e] = off[e];
-      if (e < a.E) a.counts[e] = tot[e];
-    }
   int place = -1;
   if (lane < k) {
     const int id = ids_s[t * k + lane];
@@ -438,12 +431,9 @@ __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThr
     __syncthreads();
     if (tid < 32) scan_segments(sum, a.E, off);
     __syncthreads();
-    for (int e = tid; e <= a.E; e += kGroupThreads) {
-      a.offsets[e] = off[e];
-      if (e < a.E) {
-        a.counts[e] = sum[e];
-        a.cursor[e] = off[e];
-      }
+    for (int e = tid; e < a.E; e += kGroupThreads) {
+      a.counts[e] = sum[e];
+      a.cursor[e] = off[e];
     }
   }
   cluster_barrier();  // no block ends while its counts are being read
@@ -581,12 +571,12 @@ cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, lo
 }
 
 cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, int top_k, int E,
-                            int H, int32_t* offsets, int32_t* counts, int32_t* cursor,
+                            int H, int32_t* counts, int32_t* cursor,
                             int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,
                             cudaStream_t st) {
-  const MxPlaceArgs a = {reinterpret_cast<const unsigned char*>(hidden), ids, offsets, counts,
+  const MxPlaceArgs a = {reinterpret_cast<const unsigned char*>(hidden), ids, counts,
                          cursor, pos, codes, scales, err, T, E, top_k, H};
-  if (T * top_k <= kPlaceSmallIds)
+  if (T * top_k <= kMxEarlyIds)
     return launch_k(mx_place_small_kernel, dim3(T), dim3(kPlaceWarps * 32), 0, st, false, a);
   cudaError_t e = launch_k(mx_group_kernel, dim3(kGroupBlocks), dim3(kGroupThreads), 0, st, false,
                            a);

@@ -68,14 +68,15 @@ constexpr uint32_t kTmemCols = 512;
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
 struct MxGemmArgs {
-  const int32_t* offsets;  // [E + 1] first row of each segment (NULL: dense)
-  const int32_t* counts;   // [E] rows of each segment
+  const int32_t* counts;   // [E] rows of each segment (NULL: `rows` each)
+  const int32_t* ids;      // [n_ids] the slots' experts instead of counts (small batches)
+  int n_ids, top_k;
   const uint8_t* w_scales;
   const uint8_t* x_scales;
   void* out;               // dense: C; gate_up: act codes; down: y
   uint8_t* act_scales;     // gate_up: scales of act; down: block exponents of y
   unsigned* err;
-  int E, rows;    // rows: of the one segment of a dense product
+  int E, rows;    // rows: of the one segment of a dense product (else 0)
   int N, K;       // output columns (gate_up: intermediates), reduction
   int n_mtiles;
   int out_fp32;   // dense
@@ -95,8 +96,10 @@ struct Tile {
   int e, m, row0, nrows;
 };
 
+// Chunks of a segment follow one another, and segments begin at whole chunks:
+// chunk ch of the table is rows [128 ch, 128 ch + 128) of the token matrix.
 __device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int* first_chunk,
-                                        const int* off, const int* cnt) {
+                                        const int* cnt) {
   Tile t;
   const int ch = tile / n_mtiles;
   t.m = tile - ch * n_mtiles;
@@ -110,9 +113,8 @@ __device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int
   }
   lo = uniform(lo);
   t.e = lo;
-  const int in = (ch - uniform(first_chunk[lo])) * kBN;
-  t.row0 = uniform(off[lo]) + in;
-  t.nrows = min(kBN, uniform(cnt[lo]) - in);
+  t.row0 = ch * kBN;
+  t.nrows = min(kBN, uniform(cnt[lo]) - (ch - uniform(first_chunk[lo])) * kBN);
   return t;
 }
 
@@ -206,38 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
   __shared__ uint32_t tmem_base_s;
   __shared__ int stop_s;
-  __shared__ int off_s[kMaxExperts], cnt_s[kMaxExperts], first_s[kMaxExperts + 1];
+  __shared__ int cnt_s[kMaxExperts], first_s[kMaxExperts + 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = a.E;
-  pdl_wait();
-  pdl_trigger();
-  for (int i = tid; i < E; i += kThreads) {
-    off_s[i] = a.offsets != nullptr ? a.offsets[i] : 0;
-    cnt_s[i] = a.counts != nullptr ? a.counts[i] : a.rows;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int run = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < E ? (cnt_s[e] + kBN - 1) / kBN : 0;
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (e < E) first_s[e] = run + incl - c;
-      run += __shfl_sync(kAll, incl, 31);
-    }
-    if (lane == 0) first_s[E] = run;
-  }
-  __syncthreads();
-  const int total = uniform(first_s[E]) * a.n_mtiles;
-  if ((int)blockIdx.x >= total) return;  // uniform across the CTA
-
-  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint64_t* full = bars;
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
@@ -259,6 +233,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmX32);
   }
+  // With the slots' ids at hand (a small batch) the segments are counted here,
+  // while the kernels before this one still run, and the first weights are
+  // fetched; only the token rows wait for those kernels.
+  const bool early = a.ids != nullptr;
+  for (int i = tid; i < E; i += kThreads) cnt_s[i] = a.rows;
+  if (early) {
+    __syncthreads();
+    for (int i = tid; i < a.n_ids; i += kThreads) {
+      const int id = __ldg(a.ids + i);
+      bool drop = id < 0 || id >= E;
+      for (int j = i / a.top_k * a.top_k; j < i; ++j) drop |= __ldg(a.ids + j) == id;
+      if (!drop) atomicAdd(&cnt_s[id], 1);
+    }
+  } else {
+    pdl_wait();
+    if (a.counts != nullptr)
+      for (int i = tid; i < E; i += kThreads) cnt_s[i] = a.counts[i];
+  }
+  pdl_trigger();
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < E ? (cnt_s[e] + kBN - 1) / kBN : 0;
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (e < E) first_s[e] = run + incl - c;
+      run += __shfl_sync(kAll, incl, 31);
+    }
+    if (lane == 0) first_s[E] = run;
+  }
+  __syncthreads();
+  const int total = uniform(first_s[E]) * a.n_mtiles;
+  if ((int)blockIdx.x >= total) {  // uniform across the CTA
+    if (early) pdl_wait();  // this kernel's end must mean the end of those before it
+    return;
+  }
+
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
     tmem_relinquish();
@@ -285,16 +303,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = elect_one();
     const uint64_t pol_w = l2_policy_evict_normal();
     const uint64_t pol_x = l2_policy_evict_last();
+    const uint32_t row_bytes = kStageK / 2;
+    // Weights of stage kb into a slot, and the bytes they will count.
+    auto weight_bytes = [&](const WeightAt& w, int kb) {
+      const uint32_t sb = PERM ? kScaleStage  // a box is always whole
+                               : min(2, k_tiles - 2 * kb) * kMxTileBytes;
+      return (w.has1 ? 2u : 1u) * (kTileBytes + sb);
+    };
+    auto load_weights = [&](const WeightAt& w, int kb, uint32_t st, uint32_t fb) {
+      const uint32_t sc = st + 3 * kTileBytes;
+      const int kt = 2 * kb;  // first scale tile of the stage
+      if (PERM) {
+        tma_load_4d(st, &tmW, fb, kb * row_bytes, w.row0 / 32, pol_w);
+        tma_load_4d(sc, &tmS, fb, 0, (int)(w.st0 * k_tiles) + kt, pol_w);
+        if (w.has1) {
+          tma_load_4d(st + kTileBytes, &tmW, fb, kb * row_bytes, w.row1 / 32, pol_w);
+          tma_load_4d(sc + kScaleStage, &tmS, fb, 0, (int)(w.st1 * k_tiles) + kt, pol_w);
+        }
+      } else {
+        const uint32_t sb = min(2, k_tiles - kt) * kMxTileBytes;
+        tma_load_2d(st, &tmW, fb, kb * row_bytes, w.row0, pol_w);
+        bulk_load(sc, a.w_scales + (w.st0 * k_tiles + kt) * kMxTileBytes, sb, fb);
+        if (w.has1) {
+          tma_load_2d(st + kTileBytes, &tmW, fb, kb * row_bytes, w.row1, pol_w);
+          bulk_load(sc + kScaleStage, a.w_scales + (w.st1 * k_tiles + kt) * kMxTileBytes, sb, fb);
+        }
+      }
+    };
+    // Token rows of a stage: one box of 128, or up to three boxes of 32.
+    auto row_boxes = [](const Tile& t) { return t.nrows > 96 ? 4 : (t.nrows + 31) / 32; };
+    auto stage_bytes = [&](const Tile& t, const WeightAt& w, int kb) {
+      return weight_bytes(w, kb) + (uint32_t)row_boxes(t) * 4096u +
+             (uint32_t)min(2, k_tiles - 2 * kb) * kMxTileBytes;
+    };
+    auto load_rows = [&](const Tile& t, int kb, uint32_t st, uint32_t fb) {
+      const int nbox = row_boxes(t), kt = 2 * kb;
+      if (nbox == 4) {
+        tma_load_2d(st + 2 * kTileBytes, &tmX, fb, kb * row_bytes, t.row0, pol_x);
+      } else {
+        for (int b = 0; b < nbox; ++b)
+          tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX32, fb, kb * row_bytes, t.row0 + 32 * b,
+                      pol_x);
+      }
+      bulk_load(st + 3 * kTileBytes + 2 * kScaleStage,
+                a.x_scales + ((long long)(t.row0 / 128) * k_tiles + kt) * kMxTileBytes,
+                min(2, k_tiles - kt) * kMxTileBytes, fb);
+    };
+    int fetched = 0;  // stages of the first tile whose weights are already on their way
+    if (early) {
+      const Tile t = tile_at(blockIdx.x, a.n_mtiles, E, first_s, cnt_s);
+      const WeightAt w = weights_of<MODE>(a, t);
+      fetched = min(nk, kStages);
+      if (leader) {
+        for (int kb = first; kb < fetched; kb += kProdWarps) {
+          const uint32_t fb = smem_u32(&full[kb]);
+          mbar_arrive_expect_tx(fb, stage_bytes(t, w, kb));
+          load_weights(w, kb, smem_base + kb * kStageStride, fb);
+        }
+      }
+      __syncwarp();
+      pdl_wait();
+    }
     uint32_t ph = 1;  // parity of the empty barriers: the first fill waits for nothing
     int s = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       if (stopped(&stop_s)) break;
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
       const WeightAt w = weights_of<MODE>(a, t);
-      // Token rows: one box of 128, or up to three boxes of 32.
-      const int nbox = t.nrows > 96 ? 4 : (t.nrows + 31) / 32;
-      const uint8_t* xs = a.x_scales + (long long)(t.row0 / 128) * k_tiles * kMxTileBytes;
       for (int kb = 0; kb < nk; ++kb) {
         const int slot = s;
         const uint32_t parity = ph;
@@ -304,43 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (slot % kProdWarps != first) continue;
         const uint32_t st = smem_base + slot * kStageStride;
-        const uint32_t sc = st + 3 * kTileBytes;
         const uint32_t fb = smem_u32(&full[slot]);
-        if (!warp_wait(smem_u32(&empty[slot]), parity)) {
+        const bool todo = kb >= fetched || tile != (int)blockIdx.x;
+        if (todo && !warp_wait(smem_u32(&empty[slot]), parity)) {
           stop(&stop_s, a.err);
           ok = false;
           break;
         }
         if (leader) {
-          const int kt = 2 * kb;  // first scale tile of the stage
-          const uint32_t sb = min(2, k_tiles - kt) * kMxTileBytes;
-          const uint32_t wsb = PERM ? kScaleStage : sb;  // a box is always whole
-          mbar_arrive_expect_tx(
-              fb, (w.has1 ? 2u : 1u) * (kTileBytes + wsb) + (uint32_t)nbox * 4096u + sb);
-          if (PERM) {
-            tma_load_4d(st, &tmW, fb, kb * 128, w.row0 / 32, pol_w);
-            tma_load_4d(sc, &tmS, fb, 0, (int)(w.st0 * k_tiles) + kt, pol_w);
-            if (w.has1) {
-              tma_load_4d(st + kTileBytes, &tmW, fb, kb * 128, w.row1 / 32, pol_w);
-              tma_load_4d(sc + kScaleStage, &tmS, fb, 0, (int)(w.st1 * k_tiles) + kt, pol_w);
-            }
-          } else {
-            tma_load_2d(st, &tmW, fb, kb * 128, w.row0, pol_w);
-            bulk_load(sc, a.w_scales + (w.st0 * k_tiles + kt) * kMxTileBytes, sb, fb);
-            if (w.has1) {
-              tma_load_2d(st + kTileBytes, &tmW, fb, kb * 128, w.row1, pol_w);
-              bulk_load(sc + kScaleStage, a.w_scales + (w.st1 * k_tiles + kt) * kMxTileBytes, sb,
-                        fb);
-            }
+          if (todo) {
+            mbar_arrive_expect_tx(fb, stage_bytes(t, w, kb));
+            load_weights(w, kb, st, fb);
           }
-          if (nbox == 4) {
-            tma_load_2d(st + 2 * kTileBytes, &tmX, fb, kb * 128, t.row0, pol_x);
-          } else {
-            for (int b = 0; b < nbox; ++b)
-              tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX32, fb, kb * 128, t.row0 + 32 * b,
-                          pol_x);
-          }
-          bulk_load(sc + 2 * kScaleStage, xs + kt * kMxTileBytes, sb, fb);
+          load_rows(t, kb, st, fb);
         }
         __syncwarp();
       }
@@ -359,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0, it = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
       const bool work = warp == 0 || weights_of<MODE>(a, t).has1;
       if (!warp_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
         stop(&stop_s, a.err);
@@ -408,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, off_s, cnt_s);
+      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
       const bool has1 = weights_of<MODE>(a, t).has1;
       if (!warp_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
@@ -606,8 +658,12 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   a.out_fp32 = out_fp32 ? 1 : 0;
   const long long tiles = (long long)((M + kBN - 1) / kBN) * a.n_mtiles;
   const long long scale_tiles = (long long)mx_tiles(N) * mx_tiles(K);
-  // Whole groups of 32 output columns: four a lane, in wide stores.
-  if (N % 32 == 0)
+  // With whole groups of 32 output columns a thread can have four of them and
+  // store wide, but the boxes in that row order take longer to load. Long
+  // reductions over enough tiles to fill the SMs are bound by the loads
+  // (8192 x 4096, K = 4096: 56.7 us in that order, 54.3 without; K = 1024: 23.4
+  // and 24.3; 64 x 4096 x 4096, few tiles: 8.9 and 9.6).
+  if (N % 32 == 0 && (K <= 2048 || tiles < num_sms))
     return launch_mode<kDense, true>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
                                      st);
   return launch_mode<kDense, false>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
@@ -616,13 +672,17 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
 
 cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
                                       const uint8_t* w, const uint8_t* w_scales,
-                                      const int32_t* offsets, const int32_t* counts, int E, int I,
-                                      int H, long long capacity, long long max_chunks,
+                                      const int32_t* counts, const int32_t* ids, int T,
+                                      int top_k, int E, int I, int H, long long capacity, long long max_chunks,
                                       uint8_t* act, uint8_t* act_scales, int num_sms,
                                       unsigned* err, bool after_prev, cudaStream_t st) {
   MxGemmArgs a = {};
-  a.offsets = offsets;
   a.counts = counts;
+  if (T * top_k <= kMxEarlyIds) {
+    a.ids = ids;
+    a.n_ids = T * top_k;
+    a.top_k = top_k;
+  }
   a.w_scales = w_scales;
   a.x_scales = xs_scales;
   a.out = act;
@@ -637,12 +697,16 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
 }
 
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
-                                   const uint8_t* w_scales, const int32_t* offsets,
-                                   const int32_t* counts, int E, int H, int I, long long capacity, long long max_chunks,
+                                   const uint8_t* w_scales, const int32_t* counts,
+                                   const int32_t* ids, int T, int top_k, int E, int H, int I, long long capacity, long long max_chunks,
                                    uint16_t* y, uint8_t* y_scale, int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
   MxGemmArgs a = {};
-  a.offsets = offsets;
   a.counts = counts;
+  if (T * top_k <= kMxEarlyIds) {
+    a.ids = ids;
+    a.n_ids = T * top_k;
+    a.top_k = top_k;
+  }
   a.w_scales = w_scales;
   a.x_scales = act_scales;
   a.out = y;
