@@ -487,14 +487,15 @@ _DTYPES = {torch.float32: MM_DTYPE_FP32, torch.bfloat16: MM_DTYPE_BF16,
 def _dtype(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return dt
 
 
 def _shape(t, shape, name: str) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t is not None and t.shape != shape:  # torch.Size compares as a tuple
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _mask_ptr(mask, T: int):
@@ -644,13 +645,17 @@ def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
 
 def _matrix(codes, scales, name: str):
     """(rows, K) and the pointers of one 4-bit matrix (a leading dimension of 1 allowed)."""
-    if codes.dim() == 3 and codes.shape[0] == 1:
-        codes, scales = codes[0], scales[0]
-    if codes.dim() != 2:
+    shape = codes.shape
+    if len(shape) == 3 and shape[0] == 1:
+        shape = shape[1:]
+    if len(shape) != 2:
         raise ValueError(f"{name} must be one matrix, got codes of shape {tuple(codes.shape)}")
-    rows, K = codes.shape[0], 2 * codes.shape[1]
-    _shape(scales, mm_mxfp4_scales_shape(rows, K), f"{name} scales")
-    return rows, K, _ptr(codes, torch.uint8, name), _ptr(scales, torch.uint8, f"{name} scales")
+    rows, half = shape
+    tiles = ((rows + 127) // 128, (2 * half + 127) // 128, 512)
+    if scales.shape != tiles and scales.shape != (1, *tiles):
+        raise ValueError(f"{name} scales must have shape {tiles}, got {tuple(scales.shape)}")
+    return (rows, 2 * half, _ptr(codes, torch.uint8, name),
+            _ptr(scales, torch.uint8, "scales"))
 
 
 def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, stream=None):
