@@ -279,21 +279,34 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
 // free place. A slot whose id is outside [0, E) or repeats an earlier one of its
 // token is dropped and flagged, as in the layer's grouping.
 
-// Columns [16 i, 16 i + 16) of a token's row to all its places: `place` in
-// lane j < top_k is the row of slot j (-1: dropped), scale_at its scale offset.
-__device__ __forceinline__ void write_places(const float (&v)[16], int c, int H, int top_k,
-                                             int place, uint8_t* codes, uint8_t* scales,
+// U spans of a token's row (columns c, c + span, ...) to all its places: `place`
+// in lane j < top_k is the row of slot j (-1: dropped), scale_at its scale
+// offset.
+template <int U>
+__device__ __forceinline__ void write_places(const Raw16h (&raw)[U], int c, int span, int H,
+                                             int top_k, int place, uint8_t* codes, uint8_t* scales,
                                              size_t scale_at) {
-  uint32_t s4;
-  const uint2 code = encode16(v, s4);
-  const size_t tile = (size_t)(c / kMxTile) * kMxTileBytes;
+  uint2 code[U];
+  uint32_t s4[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float v[16];
+    unpack16<MM_DTYPE_BF16>(raw[u], v);
+    code[u] = encode16(v, s4[u]);
+  }
+  const int hp = (int)mx_tiles(H) * kMxTile;
   for (int j = 0; j < top_k; ++j) {
     const int r = __shfl_sync(kAll, place, j);
-    const size_t at = __shfl_sync(kAll, scale_at, j);
     if (r < 0) continue;
-    if (c < H) *reinterpret_cast<uint2*>(codes + (size_t)r * (H / 2) + c / 2) = code;
-    if ((threadIdx.x & 7) == 0 && c < (int)mx_tiles(H) * kMxTile)
-      *reinterpret_cast<uint32_t*>(scales + at + tile) = s4;
+    uint8_t* row = codes + (size_t)r * (H / 2);
+    uint8_t* srow = scales + __shfl_sync(kAll, scale_at, j);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int cu = c + u * span;
+      if (cu < H) *reinterpret_cast<uint2*>(row + cu / 2) = code[u];
+      if ((threadIdx.x & 7) == 0 && cu < hp)
+        *reinterpret_cast<uint32_t*>(srow + (size_t)(cu / kMxTile) * kMxTileBytes) = s4[u];
+    }
   }
 }
 
@@ -344,8 +357,9 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
   const unsigned char* row = a.hidden + (size_t)t * a.H * 2;
   const int hp = (int)mx_tiles(a.H) * kMxTile;
   int c = tid * 16;
-  Raw16h raw;
-  if (c < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw);
+  Raw16h raw[1];
+  zero16<MM_DTYPE_BF16>(raw[0]);
+  if (c < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw[0]);
   for (int i = tid; i < n; i += kNT) ids_s[i] = __ldg(a.ids + i);
   for (int e = tid; e < a.E; e += kNT) tot[e] = before[e] = 0;
   __syncthreads();
@@ -374,11 +388,9 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
   }
   const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
   for (; c - lane * 16 < hp; c += kNT * 16) {
-    if (c >= a.H) zero16<MM_DTYPE_BF16>(raw);
-    float v[16];
-    unpack16<MM_DTYPE_BF16>(raw, v);
-    if (c + kNT * 16 < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)(c + kNT * 16) * 2, raw);
-    write_places(v, c, a.H, k, place, a.codes, a.scales, scale_at);
+    write_places<1>(raw, c, 0, a.H, k, place, a.codes, a.scales, scale_at);
+    zero16<MM_DTYPE_BF16>(raw[0]);
+    if (c + kNT * 16 < a.H) load16<MM_DTYPE_BF16, false>(row + (size_t)(c + kNT * 16) * 2, raw[0]);
   }
 }
 
@@ -439,18 +451,33 @@ __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThr
   cluster_barrier();  // no block ends while its counts are being read
 }
 
-// ... then one warp a token takes the next free rows and fills them.
+// ... then one warp a token takes the next free rows and fills them. The
+// token's row and ids are the caller's, so they are read before the wait.
 __global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs a) {
   const int lane = threadIdx.x & 31, k = a.top_k;
   const int t = blockIdx.x * kMxWarps + (threadIdx.x >> 5);
+  constexpr int U = 4, kSpan = 512;
+  const unsigned char* row = a.hidden + (size_t)t * a.H * 2;
+  const int hp = (int)mx_tiles(a.H) * kMxTile;
+  Raw16h raw[U];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * kSpan;
+      if (c < a.H)
+        load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw[u]);
+      else
+        zero16<MM_DTYPE_BF16>(raw[u]);
+    }
+  };
+  int place = -1;
+  if (t < a.T) {
+    load(lane * 16);
+    if (lane < k) place = __ldg(a.ids + (size_t)t * k + lane);
+  }
   pdl_wait();
   pdl_trigger();
   if (t >= a.T) return;
-  constexpr int U = 4;
-  const unsigned char* row = a.hidden + (size_t)t * a.H * 2;
-  const int hp = (int)mx_tiles(a.H) * kMxTile;
-  int place = -1;
-  if (lane < k) place = __ldg(a.ids + (size_t)t * k + lane);
   const uint32_t same = __match_any_sync(kAll, place);
   if (place < 0 || place >= a.E || (same & ((1u << lane) - 1u)) != 0)
     place = -1;
@@ -458,24 +485,9 @@ __global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs 
     place = atomicAdd(a.cursor + place, 1);
   if (lane < k) a.pos[(size_t)t * k + lane] = place;
   const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
-  for (int c0 = lane * 16; c0 - lane * 16 < hp; c0 += U * 512) {
-    Raw16h raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * 512;
-      if (c < a.H)
-        load16<MM_DTYPE_BF16, false>(row + (size_t)c * 2, raw[u]);
-      else
-        zero16<MM_DTYPE_BF16>(raw[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * 512;
-      if (c - lane * 16 >= hp) break;
-      float v[16];
-      unpack16<MM_DTYPE_BF16>(raw[u], v);
-      write_places(v, c, a.H, k, place, a.codes, a.scales, scale_at);
-    }
+  for (int c0 = lane * 16; c0 - lane * 16 < hp; c0 += U * kSpan) {
+    if (c0 != lane * 16) load(c0);
+    write_places<U>(raw, c0, kSpan, a.H, k, place, a.codes, a.scales, scale_at);
   }
 }
 
@@ -495,24 +507,38 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
     float s[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) s[q] = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < top_k; ++j) {
-      const int r = __ldg(pos + f0 + j);
-      const bool use = r >= 0;
-      const float wj = __ldg(w + f0 + j);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      float unit = 0.f;
-      if (use) {
-        v = __ldg(y + (size_t)r * h8 + h);
-        unit = mx_y_unit(__ldg(y_scale + ((size_t)r * h8 + h) / 4));
-      }
-      const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-      const float wu = use ? wj : 0.f;
+    // Eight slots at a time: their rows first, then all their loads, then the sum.
+    for (int j0 = 0; j0 < top_k; j0 += 8) {
+      int r[8];
+      float wj[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
-        s[2 * q] += wu * (f.x * unit);
-        s[2 * q + 1] += wu * (f.y * unit);
+      for (int j = 0; j < 8; ++j) {
+        const bool in = j0 + j < top_k;
+        r[j] = in ? __ldg(pos + f0 + j0 + j) : -1;
+        wj[j] = in ? __ldg(w + f0 + j0 + j) : 0.f;
+      }
+      uint4 v[8];
+      uint32_t byte[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        byte[j] = 15u;
+        if (r[j] >= 0) {
+          v[j] = __ldg(y + (size_t)r[j] * h8 + h);
+          byte[j] = __ldg(y_scale + ((size_t)r[j] * h8 + h) / 4);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (r[j] < 0) continue;  // a NaN or infinite weight of a dropped slot stays out
+        const float unit = mx_y_unit(byte[j]);
+        const uint32_t p[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
+          s[2 * q] += wj[j] * (f.x * unit);
+          s[2 * q + 1] += wj[j] * (f.y * unit);
+        }
       }
     }
     out[i] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
