@@ -59,13 +59,8 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
 // 2^-28 of it keeps 11 bits: a rounding of at most 2^-11 per slot, under the
 // 2^-8 of the bf16 output (bf16 here would double that output's rounding error).
 // The byte is the biased exponent of the largest magnitude, kept in [15, 254]
-// so that both factors are normal floats; infinity and NaN pass through fp16.
-__device__ __forceinline__ uint32_t mx_y_byte(uint32_t amax_bits) {
-  return min(max(amax_bits >> 23, 15u), 254u);
-}
-__device__ __forceinline__ float mx_y_inv(uint32_t byte) {  // 2^(141 - byte)
-  return __uint_as_float((268u - byte) << 23);
-}
+// so that both factors, 2^(141 - byte) and its inverse, are normal floats;
+// infinity and NaN pass through fp16.
 __device__ __forceinline__ float mx_y_unit(uint32_t byte) {  // 2^(byte - 141)
   return __uint_as_float((byte - 14u) << 23);
 }

@@ -161,16 +161,52 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, Piece& p) {
   tmem_ld_16x256b_x4(taddr + (16u << 16), p.r[1]);  // lanes 16-31
 }
 
-// Largest magnitude of the piece's 32 columns for the token rows (g, 0) in the
-// low and (g, 1) in the high half: the upper 16 bits of the float, which hold
-// its exponent. A NaN gives an exponent of 255.
-__device__ __forceinline__ uint32_t amax_pair(const float (&a)[4], const float (&b)[4]) {
+// Biased exponents of the largest magnitude of the piece's 32 columns, for the
+// token rows (g, 0) in the low and (g, 1) in the high half (255: an infinity or
+// a NaN among them). Below, both rows are handled in one word as far as it goes.
+__device__ __forceinline__ uint32_t exponent_pair(const float (&a)[4], const float (&b)[4]) {
   const float x = max_nan(max_nan(fabsf(a[0]), fabsf(a[1])), max_nan(fabsf(a[2]), fabsf(a[3])));
   const float y = max_nan(max_nan(fabsf(b[0]), fabsf(b[1])), max_nan(fabsf(b[2]), fabsf(b[3])));
   uint32_t m = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
   m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 4));
   m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 8));
-  return __vmaxu2(m, __shfl_xor_sync(kAll, m, 16));
+  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 16));
+  return (m >> 7) & 0x00FF00FFu;
+}
+
+// The factors 2^(f - 127) of two biased exponents f in the halves of a word.
+__device__ __forceinline__ void factor_pair(uint32_t f, float (&inv)[2]) {
+  inv[0] = __uint_as_float(f << 23);
+  inv[1] = __uint_as_float((f << 7) & 0xFF800000u);
+}
+
+// mx_scale_byte and mx_inv_scale of two exponents.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t e, float (&inv)[2]) {
+  uint32_t s = __vmaxu2(e, 0x00020002u) - 0x00020002u;
+  factor_pair(0x00FE00FEu - s, inv);
+  const uint32_t bad = (e + 0x00010001u) & 0x01000100u;  // exponents of 255
+  if (bad != 0) {
+    s += (bad >> 7);  // 253 -> 255
+    if (bad & 0xFFFFu) inv[0] = 0.f;
+    if (bad >> 16) inv[1] = 0.f;
+  }
+  return s;
+}
+
+// The bytes of y (see mx_y_unit) and the factors 2^(141 - byte) for two exponents.
+__device__ __forceinline__ uint32_t y_pair(uint32_t e, float (&inv)[2]) {
+  const uint32_t b = __vminu2(__vmaxu2(e, 0x000F000Fu), 0x00FE00FEu);
+  factor_pair(0x010C010Cu - b, inv);
+  return b;
+}
+
+// The byte of token row 8 (lane / 8) + 2 (lane % 4) + (lane / 4) % 2 out of the
+// four pairs, which every lane of one lane % 4 holds.
+__device__ __forceinline__ uint32_t own_byte(const uint32_t (&b)[4]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t lo = lane & 8 ? b[1] : b[0], hi = lane & 8 ? b[3] : b[2];
+  const uint32_t w = lane & 16 ? hi : lo;
+  return lane & 4 ? w >> 16 : w & 0xFFFFu;
 }
 
 // Issues one stage of one accumulator: the scale tiles of its `steps` / 2
@@ -487,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
           uint8_t* codes = static_cast<uint8_t*>(a.out) + row0 * (a.N / 2) + (blk * 32 + col4) / 2;
           const int k_tiles_act = (a.N + 127) / 128;
-          uint32_t my_scale = 0;  // of token row lane / 4's place among the thread's eight
+          uint32_t sb[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             float x[2][4];
@@ -500,23 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float gate = p0.at(j, g, c), up = p1.at(j, g, c);
                 x[c][j] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
               }
-            const uint32_t m = amax_pair(x[0], x[1]);
+            float inv[2];
+            sb[g] = scale_pair(exponent_pair(x[0], x[1]), inv);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const uint32_t sb = mx_scale_byte(c == 0 ? m << 16 : m & 0xFFFF0000u);
-              const float inv = mx_inv_scale(sb);
-              if ((lane >> 2) == 2 * g + c) my_scale = sb;
-              const uint16_t two = mx_pack4(x[c][0] * inv, x[c][1] * inv, x[c][2] * inv,
-                                            x[c][3] * inv);
+              const uint16_t two = mx_pack4(x[c][0] * inv[c], x[c][1] * inv[c], x[c][2] * inv[c],
+                                            x[c][3] * inv[c]);
               if (real && 8 * g + 2 * (lane & 3) + c < ncol)
                 *reinterpret_cast<uint16_t*>(codes + (8 * g + c) * (size_t)(a.N / 2)) = two;
             }
           }
-          // Lanes of one lane / 4 write the scales of token rows 8 g + 2 (lane % 4)
-          // + c with 2 g + c = lane / 4.
           const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
           if (r < ncol)
-            a.act_scales[mx_scale_offset(t.row0 + c0 + r, blk, k_tiles_act)] = real ? my_scale : 0;
+            a.act_scales[mx_scale_offset(t.row0 + c0 + r, blk, k_tiles_act)] = real ? own_byte(sb) : 0;
         } else {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -524,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = t.m * 256 + half * 128 + q * 32;
             if (n >= a.N) continue;
             const size_t at = (size_t)row0 * a.N + n + col4;
-            uint32_t my_byte = 0;
+            uint32_t yb[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               float x[2][4];
@@ -532,18 +564,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[c][j] = p.at(j, g, c);
-              uint32_t m = 0;
-              if (MODE == kDown) m = amax_pair(x[0], x[1]);
+              float inv[2];
+              if (MODE == kDown) yb[g] = y_pair(exponent_pair(x[0], x[1]), inv);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const bool in = 8 * g + 2 * (lane & 3) + c < ncol;
                 const size_t to = at + (size_t)(8 * g + c) * a.N;
                 if (MODE == kDown) {
-                  const uint32_t byte = mx_y_byte(c == 0 ? m << 16 : m & 0xFFFF0000u);
-                  const float inv = mx_y_inv(byte);
-                  if ((lane >> 2) == 2 * g + c) my_byte = byte;
-                  const __half2 lo = __floats2half2_rn(x[c][0] * inv, x[c][1] * inv);
-                  const __half2 hi = __floats2half2_rn(x[c][2] * inv, x[c][3] * inv);
+                  const __half2 lo = __floats2half2_rn(x[c][0] * inv[c], x[c][1] * inv[c]);
+                  const __half2 hi = __floats2half2_rn(x[c][2] * inv[c], x[c][3] * inv[c]);
                   if (in)
                     *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
@@ -561,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == kDown) {
               const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
               if (r < ncol)
-                a.act_scales[((size_t)(t.row0 + c0 + r) * a.N + n) / 32] = (uint8_t)my_byte;
+                a.act_scales[((size_t)(t.row0 + c0 + r) * a.N + n) / 32] = (uint8_t)own_byte(yb);
             }
           }
         }

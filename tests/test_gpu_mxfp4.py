@@ -412,3 +412,39 @@ def test_routing_and_experts_together():
     # first: sqrt(3) * 0.12 = 0.2.
     rel = (out.float() - full.float()).norm() / full.float().norm()
     assert rel < 0.3, rel
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+def test_experts_keep_bad_tokens_to_themselves(bad):
+    # Tokens that hold NaN, infinity or huge values share experts, chunks and
+    # 32-row pieces with the others, whose outputs must not change at all.
+    T, H, E, I, k = 100, 256, 6, 128, 3
+    d = _experts_case(77, T, H, E, I, k)
+    clean = _call(d)
+    d["hidden"][7, 5] = bad
+    d["hidden"][40] = bad
+    d["hidden"][41, 200:] = -bad
+    out = _call(d)
+    _status_ok()
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[[7, 40, 41]] = False
+    assert torch.equal(out[rows], clean[rows])
+    assert torch.isfinite(clean).all()
+    if bad != 3e38:
+        assert torch.isnan(out[~rows]).all()
+
+
+def test_experts_with_tiny_and_huge_weights():
+    # Expert outputs far below and above fp16's range pass through its block
+    # powers of two, subnormal and large floats on the way out.
+    T, H, E, I, k = 20, 128, 4, 64, 2
+    for exponent in (-100, -60, 60, 100):
+        d = _experts_case(78, T, H, E, I, k)
+        want, tol = _experts_ref(d)
+        scaled = dict(d, sdn=(d["sdn"].to(torch.int32) + exponent).clamp(1, 250).to(torch.uint8))
+        # the padding bytes are not read as scales of anything but zeros
+        out = _call(scaled)
+        _status_ok()
+        f = 2.0 ** exponent
+        off = np.abs(_np64(out) - want * f)
+        assert (off <= tol * f + 2.0 ** -133).all(), exponent
