@@ -525,6 +525,8 @@ def _launch(fn, name: str, di: int, stream, made, *args) -> None:
     else:
         s = (stream if isinstance(stream, torch.cuda.Stream)
              else torch.cuda.ExternalStream(int(stream), device=di))
+        if s.device_index != di:
+            raise ValueError(f"{name}: the stream is on another device than the tensors")
         for t in made:
             if t is not None and t.numel():
                 t.record_stream(s)

@@ -24,8 +24,14 @@
 // is three maxima in the thread and three exchanges for two rows at once, and
 // results leave the thread as they are. (A warp reduction for every column took
 // 90 us for gate_up and 93 for down at 4096 tokens, a transpose through shared
-// memory, whose bandwidth the MMAs need, 63 and 100; this: GU_US and DN_US.) The
+// memory, whose bandwidth the MMAs need, 63 and 100; this 64 and 65.) The
 // activation is quantised from the fp32 product and is rounded once.
+//
+// What bounds it, on one GB300: 8192 x 4096 x 4096 takes 55 us (5.0 PFLOP/s).
+// One stage of a tile alone on the chip takes 580 cycles, its 8 MMAs and 8
+// scale copies the tensor pipe's 576; with all SMs at work 640, as the 52 KB of
+// a stage come at 80 bytes a cycle and SM, 14 TB/s out of L2. Few rows per
+// expert (64 tokens) are bound by the weights' bytes.
 #include <algorithm>
 
 #include "mm.h"
@@ -48,11 +54,11 @@ constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = kStages * kStageStride + 1024;
 static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
 
-// Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue,
-// 18, 19 = producers (every other ring slot). There is one pair of accumulators (the
-// scales take the columns a second pair would need), so the epilogue first
-// empties tensor memory into registers, 16 warps with a 32 x 32 piece of D0 and
-// of D1 each, hands it back to the MMA warp and then does its work.
+// Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue, 18, 19 = producers
+// (every other ring slot). There is one pair of accumulators (the scales take
+// the columns a second pair would need), so the epilogue first empties tensor
+// memory into registers, 16 warps with a 32 x 32 piece of D0 and of D1 each,
+// hands it back to the MMA warps and then does its work.
 constexpr int kEpiWarp0 = 2, kEpiWarps = 16;
 constexpr int kProdWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kProdWarps = 2;
@@ -403,8 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 1;  // parity of the empty barriers: the first fill waits for nothing
     int s = 0;
     bool ok = true;
+    uint32_t fills[kStages / kProdWarps] = {};  // of this warp's slots
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      if (stopped(&stop_s)) break;
+      if (stopped(&stop_s)) {
+        ok = false;
+        break;
+      }
       const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
       const WeightAt w = weights_of<MODE>(a, t);
       for (int kb = 0; kb < nk; ++kb) {
@@ -430,15 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           load_rows(t, kb, st, fb);
         }
+        ++fills[slot / kProdWarps];
         __syncwarp();
       }
+    }
+    // Given up: no copy of this warp is in flight when the CTA ends (a slot's
+    // last fill completes its barrier's phase whether or not anybody reads it).
+    if (!ok) {
+#pragma unroll
+      for (int i = 0; i < kStages / kProdWarps; ++i)
+        if (fills[i] > 0) warp_wait(smem_u32(&full[i * kProdWarps + first]), (fills[i] - 1) & 1u);
     }
   } else if (warp < 2) {
     // ------------------------------------------------- MMA issuers (0, 1) ---
     // Warp 0 feeds D0, warp 1 D1. A tcgen05 instruction takes its thread about
     // 30 cycles and a stage's wait 200 more, together above the 60 cycles an
     // MMA of N = 128 takes to run, so one thread for both accumulators leaves
-    // the tensor cores waiting (57 us for 8192 x 4096 x 4096; two: DUAL_US).
+    // the tensor cores waiting (57 us for 8192 x 4096 x 4096; two: 54).
     // The whole warp runs the loops, so that addresses, descriptors and columns
     // are warp-uniform; one elected lane issues.
     const bool leader = elect_one();

@@ -448,3 +448,69 @@ def test_experts_with_tiny_and_huge_weights():
         f = 2.0 ** exponent
         off = np.abs(_np64(out) - want * f)
         assert (off <= tol * f + 2.0 ** -133).all(), exponent
+
+
+@pytest.mark.parametrize("T", [40, 900])  # grouped by every kernel itself, and by one of its own
+def test_experts_bad_ids_in_small_and_large_batches(T):
+    H, E, I, k = 128, 8, 64, 4
+    d = _experts_case(80, T, H, E, I, k)
+    rng = np.random.default_rng(1)
+    hit = rng.choice(T * k, T // 4, replace=False)
+    flat = d["ids"].view(-1)
+    flat[torch.from_numpy(hit).cuda()] = torch.from_numpy(
+        rng.choice([-1, E, 1 << 30, -(1 << 31)], hit.size).astype(np.int32)).cuda()
+    d["ids"][T // 2] = 5        # one expert in every slot: the first stays
+    d["w"][T // 2, 1:] = float("nan")  # weights of dropped slots are not read
+    out = _call(d)
+    torch.cuda.synchronize()
+    assert mm.mm_poll_device_status() == mm.MM_ERR_DEVICE
+    ok = dict(d, ids=d["ids"].clone(), w=d["w"].clone())
+    drop = (ok["ids"] < 0) | (ok["ids"] >= E)
+    drop[T // 2, 1:] = True
+    # the same with the dropped slots' ids out of every float64 expert's way
+    ok["ids"][drop] = -1
+    ok["w"][drop] = 0
+    want, tol = _experts_ref(ok)
+    assert (np.abs(_np64(out) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_experts_without_a_valid_id(T):
+    # Nothing to multiply: the call still writes zeros, after the kernels
+    # before it, however often it runs.
+    d = _experts_case(81, T, 128, 8, 64, 4)
+    want = _call(d)
+    none = dict(d, ids=torch.full_like(d["ids"], -7))
+    for _ in range(20):
+        out = torch.full((T, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        _call(none, out=out)
+        assert not out.any()
+        assert torch.equal(_call(d), want)
+    torch.cuda.synchronize()
+    assert mm.mm_poll_device_status() == mm.MM_ERR_DEVICE
+
+
+def test_experts_back_to_back_in_one_workspace():
+    # Calls of different sizes one after another in the same workspace, ids
+    # written on the same stream just before: nothing starts too early.
+    H, E, I, k = 256, 16, 128, 4
+    cases = [_experts_case(90 + i, T, H, E, I, k) for i, T in enumerate((1, 600, 64, 512, 513, 5))]
+    want = [_call(d) for d in cases]
+    ws = torch.empty(mm.mm_moe_experts_mxfp4_workspace_size(600, H, E, I, k), dtype=torch.uint8,
+                     device="cuda")
+    got = []
+    for rep in range(5):
+        for d in cases:
+            ids = torch.empty_like(d["ids"]).copy_(d["ids"])
+            hid = torch.empty_like(d["hidden"]).copy_(d["hidden"])
+            got.append(_call(dict(d, ids=ids, hidden=hid), workspace=ws))
+            ids.zero_(), hid.zero_()
+    _status_ok()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % len(cases)]), i
+
+
+def test_run_layer_with_4_bit_experts(capsys):
+    from mixture_experts_layer_mm_gb300 import run_layer
+    assert run_layer.main(["--workload", "tiny", "--passes", "2", "--mxfp4"]) == 0
+    assert "status MM_OK" in capsys.readouterr().out
