@@ -72,6 +72,14 @@ SIGNATURES = {
 
 _lib: Optional[ctypes.CDLL] = None
 
+# The marshalling of the short calls as an extension (csrc/marshal.cpp). Its
+# functions return None for a call that is not an ordinary one, and everything
+# is marshalled here where it has not been built.
+try:
+    from . import _marshal as _fast
+except ImportError:
+    _fast = None
+
 
 class MMError(RuntimeError):
     def __init__(self, code: int, where: str):
@@ -545,6 +553,10 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     the statistics of the balance loss. Returns (topk_ids int32 [T, k],
     topk_w fp32 [T, k], expert_counts int32 [E], prob_sums fp32 [E],
     loss fp32 [1]). token_mask [T] (bool or uint8): zero for padding tokens."""
+    if _fast is not None and stream is None:
+        r = _fast.route_logits(logits, top_k, renorm, token_mask)
+        if r is not None:
+            return r
     dt = _dtype(logits, "logits")
     T, E = logits.shape
     dev = logits.device
@@ -571,6 +583,11 @@ def mm_route_logits_backward(logits, topk_ids, expert_counts, renorm: bool, d_to
     """The gradient of mm_route_logits: d_logits [T, E] of the logits' dtype
     from d_topk_w [T, k] fp32 and / or d_loss [1] fp32. expert_counts may be
     the sum over several replicas (the loss is then the one over all of them)."""
+    if _fast is not None and stream is None:
+        r = _fast.route_logits_backward(logits, topk_ids, expert_counts, renorm, d_topk_w, d_loss,
+                                        token_mask)
+        if r is not None:
+            return r
     dt = _dtype(logits, "logits")
     T, E = logits.shape
     k = topk_ids.shape[1]
@@ -611,6 +628,10 @@ def mm_mxfp4_quantize(x, stream=None):
     """x [rows, K] or [batch, rows, K] (float32, bfloat16, float16; K % 32 == 0)
     as microscaled 4-bit floats. Returns (codes uint8 [..., rows, K/2],
     scales uint8 [..., ceil(rows/128), ceil(K/128), 512])."""
+    if _fast is not None and stream is None:
+        r = _fast.mxfp4_quantize(x)
+        if r is not None:
+            return r
     dt = _dtype(x, "x")
     if x.dim() not in (2, 3):
         raise ValueError("x must have 2 or 3 dimensions")
@@ -630,6 +651,10 @@ def mm_mxfp4_quantize(x, stream=None):
 
 def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     """The values [..., rows, K] of codes [..., rows, K/2] and their scale tiles."""
+    if _fast is not None and stream is None:
+        r = _fast.mxfp4_dequantize(codes, scales, _DTYPES.get(dtype, -1))
+        if r is not None:
+            return r
     if codes.dim() not in (2, 3):
         raise ValueError("codes must have 2 or 3 dimensions")
     lead, (rows, half) = codes.shape[:-2], codes.shape[-2:]
@@ -662,6 +687,10 @@ def _matrix(codes, scales, name: str):
 
 def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, stream=None):
     """C [M, N] = A B^T of two 4-bit matrices [M, K] and [N, K]; bfloat16 or float32."""
+    if _fast is not None and stream is None:
+        r = _fast.mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, _DTYPES.get(out_dtype, -1))
+        if r is not None:
+            return r
     M, K, a, sa = _matrix(a_codes, a_scales, "a")
     N, Kb, b, sb = _matrix(b_codes, b_scales, "b")
     if K != Kb:
@@ -686,6 +715,11 @@ def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, 
     scale tiles of 2E matrices [I, H]; w_down: codes [E, H, I/2]. workspace:
     uint8 of mm_moe_experts_mxfp4_workspace_size bytes (allocated per call if
     None)."""
+    if _fast is not None and stream is None:
+        r = _fast.experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, w_down,
+                                w_down_scales, out, workspace)
+        if r is not None:
+            return r
     T, H = hidden.shape
     k = topk_ids.shape[1]
     E, _, half = w_down.shape

@@ -3,6 +3,11 @@
 Each ``csrc/*.cu`` is compiled by nvcc in parallel, then linked with the
 static CUDA runtime into ``mixture_experts_layer_mm_gb300/libmm.so``. A file is
 recompiled only when it or a header is newer than its object.
+
+``csrc/marshal.cpp``, the binding's argument marshalling as a Python extension
+(``_marshal.so``), is built beside it against the torch that is installed. The
+package works without it (``_lib.py`` marshals in Python, more slowly), so where
+it cannot be built the build says so and goes on.
 """
 from __future__ import annotations
 
@@ -11,6 +16,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmm.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -48,22 +56,67 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_marshal() -> str | None:
+    """The object of marshal.cpp; None (with a line saying why) if it does not compile."""
+    obj = os.path.join(BUILD, "marshal.cpp.o")
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(MARSHAL_SRC),
+                                                            _headers_mtime()):
+        return obj
+    try:
+        import torch
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        cmd = [os.environ.get("CXX", "g++"), "-c", MARSHAL_SRC, "-o", obj + ".tmp", "-O2",
+               "-std=c++17", "-fPIC", "-w", "-I" + INCLUDE, "-I" + inc,
+               "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I" + sysconfig.get_paths()["include"], "-I" + cuda_inc]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError((r.stderr or r.stdout).strip().splitlines()[-1][:200])
+        os.replace(obj + ".tmp", obj)
+        return obj
+    except Exception as e:  # no compiler, no headers: the package works without
+        print(f"_marshal.so not built (calls are marshalled in Python): {e}")
+        return None
+
+
+def _link_marshal(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", MARSHAL + ".tmp", obj, LIB, "-L" + lib,
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print("_marshal.so not built (calls are marshalled in Python): "
+              + (r.stderr or r.stdout).strip()[-200:])
+        return
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every csrc/*.cu and link libmm.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra or [])
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        marshal = marshal.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static",
+                                                              "-Xlinker", "-soname,libmm.so",
                                                               "-Xlinker", "-z,defs",
                                                               "-lpthread", "-ldl", "-lrt"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link of libmm.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if marshal is not None and (not os.path.exists(MARSHAL) or
+                                os.path.getmtime(MARSHAL) < max(os.path.getmtime(marshal),
+                                                                os.path.getmtime(LIB))):
+        _link_marshal(marshal)
     if verbose:
         print(f"built {LIB}")
     return LIB

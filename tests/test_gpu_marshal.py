@@ -1,0 +1,142 @@
+"""The binding's two ways of marshalling a call (the extension, and Python where
+it is absent or declines): the same results, and the same refusals."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_mm_gb300 as mm
+import mixture_experts_layer_mm_gb300._lib as binding
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(mmlib):
+    if binding._fast is None:
+        pytest.skip("the extension is not built")
+    return mmlib
+
+
+def _calls():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(300, 24, generator=g, device="cuda")
+    mask = torch.rand(300, generator=g, device="cuda") > 0.3
+    dw = torch.randn(300, 3, generator=g, device="cuda")
+    dl = torch.ones(1, device="cuda")
+    ids, w, counts, _, _ = mm.mm_route_logits(x, 3, True)
+    m2 = torch.randn(70, 96, generator=g, device="cuda")
+    m3 = torch.randn(3, 70, 96, generator=g, device="cuda").to(torch.float16)
+    q2, q3 = mm.mm_mxfp4_quantize(m2), mm.mm_mxfp4_quantize(m3)
+    T, H, E, I, k = 9, 128, 24, 64, 3
+    hid = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    gu = mm.mm_mxfp4_quantize(torch.randn(2 * E, I, H, generator=g, device="cuda"))
+    dn = mm.mm_mxfp4_quantize(torch.randn(E, H, I, generator=g, device="cuda"))
+    some = (ids[:T].contiguous(), w[:T].contiguous())
+    ws = torch.empty(mm.mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty_like(hid)
+    return {
+        "route": lambda: mm.mm_route_logits(x, 3, True),
+        "route masked": lambda: mm.mm_route_logits(x.to(torch.bfloat16), 2, False, token_mask=mask),
+        "backward": lambda: mm.mm_route_logits_backward(x, ids, counts, True, dw, dl),
+        "backward masked": lambda: mm.mm_route_logits_backward(
+            x.to(torch.bfloat16), ids, counts, False, d_loss=dl, token_mask=mask.to(torch.uint8)),
+        "quantise": lambda: mm.mm_mxfp4_quantize(m2),
+        "quantise batch": lambda: mm.mm_mxfp4_quantize(m3),
+        "dequantise": lambda: mm.mm_mxfp4_dequantize(*q2, dtype=torch.float32),
+        "dequantise batch": lambda: mm.mm_mxfp4_dequantize(*q3),
+        "product": lambda: mm.mm_mxfp4_gemm(*q2, q3[0][1:2], q3[1][1:2]),
+        "product fp32": lambda: mm.mm_mxfp4_gemm(*q2, *q2, out_dtype=torch.float32),
+        "experts": lambda: mm.mm_moe_experts_mxfp4(hid, *some, *gu, *dn),
+        "experts given": lambda: mm.mm_moe_experts_mxfp4(
+            hid, *some, gu[0].view(E, 2 * I, H // 2), gu[1], *dn, out=out, workspace=ws).clone(),
+        "no tokens": lambda: mm.mm_route_logits(x[:0], 3, True),
+        "no rows": lambda: mm.mm_mxfp4_quantize(m2[:0]),
+    }
+
+
+NAMES = ["route", "route masked", "backward", "backward masked", "quantise", "quantise batch",
+         "dequantise", "dequantise batch", "product", "product fp32", "experts", "experts given",
+         "no tokens", "no rows"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_both_ways_agree(name, monkeypatch):
+    call = _calls()[name]
+    declined = []
+
+    class Spy:  # the extension, with a note of the calls it declines
+        def __getattr__(self, fn):
+            def f(*a):
+                r = getattr(binding_fast, fn)(*a)
+                if r is None:
+                    declined.append(fn)
+                return r
+            return f
+
+    binding_fast = binding._fast
+    monkeypatch.setattr(binding, "_fast", Spy())
+    fast = call()
+    assert not declined
+    monkeypatch.setattr(binding, "_fast", None)
+    slow = call()
+    fast, slow = (r if isinstance(r, tuple) else (r,) for r in (fast, slow))
+    assert len(fast) == len(slow)
+    for a, b in zip(fast, slow):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.device == b.device
+        assert torch.equal(a, b)
+
+
+def test_declined_calls_raise_as_in_python(monkeypatch):
+    x = torch.randn(8, 64, device="cuda")
+    q = mm.mm_mxfp4_quantize(x)
+    ids, w, counts, _, _ = mm.mm_route_logits(x, 2, True)
+    bad = [
+        lambda: mm.mm_route_logits(x, 65, True), lambda: mm.mm_route_logits(x, 0, True),
+        lambda: mm.mm_route_logits(x.half(), 2, True), lambda: mm.mm_route_logits(x.cpu(), 2, True),
+        lambda: mm.mm_route_logits(x.t(), 2, True), lambda: mm.mm_route_logits(3, 2, True),
+        lambda: mm.mm_route_logits(x, 2, True, token_mask=torch.ones(7, device="cuda").bool()),
+        lambda: mm.mm_route_logits(x, 2, True, token_mask=torch.ones(8, device="cuda")),
+        lambda: mm.mm_route_logits(x, "2", True),
+        lambda: mm.mm_route_logits_backward(x, ids.long(), counts, True),
+        lambda: mm.mm_route_logits_backward(x, ids, counts[:5], True),
+        lambda: mm.mm_route_logits_backward(x, ids, counts, True, d_topk_w=w[:, :1]),
+        lambda: mm.mm_route_logits_backward(x, ids, counts, True, d_loss=torch.ones(2).cuda()),
+        lambda: mm.mm_mxfp4_quantize(x[:, :40].contiguous()),
+        lambda: mm.mm_mxfp4_quantize(x[:, ::2]), lambda: mm.mm_mxfp4_quantize(x.double()),
+        lambda: mm.mm_mxfp4_quantize(x[0]),
+        lambda: mm.mm_mxfp4_dequantize(q[0], q[1][:, :, :256]),
+        lambda: mm.mm_mxfp4_dequantize(*q, dtype=torch.int32),
+        lambda: mm.mm_mxfp4_gemm(*q, *mm.mm_mxfp4_quantize(x[:, :32].contiguous())),
+        lambda: mm.mm_mxfp4_gemm(*q, *q, out_dtype=torch.float16),
+        lambda: mm.mm_moe_experts_mxfp4(x, ids, w, *q, *q),
+        lambda: mm.mm_moe_experts_mxfp4(x.bfloat16(), ids, w, q[0][None], q[1][None], q[0][None],
+                                        q[1][None]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(Exception) as fast:
+            call()
+        with monkeypatch.context() as m:
+            m.setattr(binding, "_fast", None)
+            with pytest.raises(Exception) as slow:
+                call()
+        assert (type(fast.value), str(fast.value)) == (type(slow.value), str(slow.value)), i
+    torch.cuda.synchronize()
+    assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+def test_results_are_the_callers():
+    # Results are ordinary tensors: they survive the inputs, and the current
+    # stream of the moment is the one that is used.
+    side = torch.cuda.Stream()
+    x = torch.randn(64, 256, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        c, s = mm.mm_mxfp4_quantize(x)
+        v = mm.mm_mxfp4_dequantize(c, s, torch.float32)
+    side.synchronize()
+    want = mm.mm_mxfp4_dequantize(*mm.mm_mxfp4_quantize(x), dtype=torch.float32)
+    assert torch.equal(v, want)
+    keep = [mm.mm_route_logits(torch.randn(5, 8, device="cuda"), 2, True) for _ in range(50)]
+    assert all(int(r[2].sum()) == 10 for r in keep)
+    assert np.isfinite([float(r[4]) for r in keep]).all()
