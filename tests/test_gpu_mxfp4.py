@@ -514,3 +514,41 @@ def test_run_layer_with_4_bit_experts(capsys):
     from mixture_experts_layer_mm_gb300 import run_layer
     assert run_layer.main(["--workload", "tiny", "--passes", "2", "--mxfp4"]) == 0
     assert "status MM_OK" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 256, 1536), (64, 4096, 4096), (40, 1000, 2080),
+                                   (130, 300, 4096), (128, 256, 8192), (257, 96, 3104),
+                                   (33, 4864, 2048), (200, 640, 1568)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_product_with_a_long_reduction(M, N, K, out):
+    # Few tiles and many stages: every ring slot is filled several times.
+    a, sa, av = _matrix(M + K, M, K)
+    b, sb, bv = _matrix(N + 7 * K, N, K, std=0.02)
+    c = mm.mm_mxfp4_gemm(a, sa, b, sb, out_dtype=out)
+    again = [mm.mm_mxfp4_gemm(a, sa, b, sb, out_dtype=out) for _ in range(3)]
+    _status_ok()
+    assert all(torch.equal(c, x) for x in again)
+    want = av @ bv.T
+    # as in test_product
+    tol = K * 2.0 ** -23 * (np.abs(av) @ np.abs(bv).T)
+    if out == torch.bfloat16:
+        tol = tol + (np.abs(want) + tol) * 2.0 ** -8
+    assert (np.abs(_np64(c) - want) <= tol).all()
+
+
+def test_products_on_two_streams_and_in_a_graph():
+    a, sa, _ = _matrix(1, 60, 4096)
+    b, sb, _ = _matrix(2, 2000, 4096)
+    want = mm.mm_mxfp4_gemm(a, sa, b, sb)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [mm.mm_mxfp4_gemm(a, sa, b, sb, stream=streams[i % 2]) for i in range(12)]
+    g = torch.cuda.CUDAGraph()
+    for s in streams:
+        s.synchronize()
+    with torch.cuda.graph(g):
+        one = mm.mm_mxfp4_gemm(a, sa, b, sb)
+    for _ in range(3):
+        g.replay()
+    _status_ok()
+    assert all(torch.equal(x, want) for x in got + [one])
