@@ -337,23 +337,30 @@ struct MxPlaceArgs {
   int T, E, top_k, H;
 };
 
-// First rows of the segments from the counts, by one warp; off[E] the total.
+// First rows of the segments from the counts, by one warp (lane l the experts
+// from 8 l on).
 __device__ __forceinline__ void scan_segments(const int* cnt, int E, int* off) {
   const int lane = threadIdx.x & 31;
-  int run = 0;
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    const int v = e < E ? (cnt[e] + kMxBlockM - 1) / kMxBlockM * kMxBlockM : 0;
-    int incl = v;
+  constexpr int kPer = kMaxExperts / 32;
+  int v[kPer], sum = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(kAll, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (e < E) off[e] = run + incl - v;
-    run += __shfl_sync(kAll, incl, 31);
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane * kPer + i;
+    v[i] = e < E ? (cnt[e] + kMxBlockM - 1) / kMxBlockM * kMxBlockM : 0;
+    sum += v[i];
   }
-  if (lane == 0) off[E] = run;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += u;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (lane * kPer + i < E) off[lane * kPer + i] = run;
+    run += v[i];
+  }
 }
 
 // Up to kMxEarlyIds slots: one block a token, one launch. Every block counts
@@ -363,7 +370,7 @@ constexpr int kPlaceWarps = 4;
 
 __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const MxPlaceArgs a) {
   __shared__ int ids_s[kMxEarlyIds];
-  __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts + 1];
+  __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kNT = kPlaceWarps * 32;
   const int t = blockIdx.x, k = a.top_k, n = a.T * k;
@@ -429,7 +436,7 @@ __device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {  // CTA 
 
 __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThreads)
     mx_group_kernel(const MxPlaceArgs a) {
-  __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts + 1];
+  __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts];
   const int tid = threadIdx.x;
   const uint32_t k = a.top_k;
   pdl_wait();

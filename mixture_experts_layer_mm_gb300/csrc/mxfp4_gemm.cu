@@ -102,22 +102,45 @@ struct Tile {
   int e, m, row0, nrows;
 };
 
+// Exclusive sums of the segments' chunks, by one warp: lane l takes the experts
+// from 8 l on (at most 256 in all). first[E] is the total.
+__device__ __forceinline__ void scan_chunks(const int* cnt, int E, int* first) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = kMaxExperts / 32;
+  int c[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane * kPer + i;
+    c[i] = e < E ? (cnt[e] + kBN - 1) / kBN : 0;
+    sum += c[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (lane * kPer + i < E) first[lane * kPer + i] = run;
+    run += c[i];
+  }
+  if (lane == 31) first[E] = incl;
+}
+
 // Chunks of a segment follow one another, and segments begin at whole chunks:
 // chunk ch of the table is rows [128 ch, 128 ch + 128) of the token matrix.
 __device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int* first_chunk,
                                         const int* cnt) {
   Tile t;
+  const int lane = threadIdx.x & 31;
   const int ch = tile / n_mtiles;
   t.m = tile - ch * n_mtiles;
-  int lo = 0, hi = E;  // first_chunk[lo] <= ch < first_chunk[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first_chunk[mid] <= ch)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  lo = uniform(lo);
+  int below = 0;  // experts whose first chunk is at or before ch: the last is ch's
+  for (int e0 = 0; e0 < E; e0 += 32)
+    below += __popc(__ballot_sync(kAll, e0 + lane < E && first_chunk[e0 + lane] <= ch));
+  const int lo = uniform(below - 1);
   t.e = lo;
   t.row0 = ch * kBN;
   t.nrows = min(kBN, uniform(cnt[lo]) - (ch - uniform(first_chunk[lo])) * kBN);
@@ -275,6 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmX32);
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
+    tmem_relinquish();
+  }
   // With the slots' ids at hand (a small batch) the segments are counted here,
   // while the kernels before this one still run, and the first weights are
   // fetched; only the token rows wait for those kernels.
@@ -295,43 +322,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_trigger();
   __syncthreads();
-  if (warp == 0) {
-    int run = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < E ? (cnt_s[e] + kBN - 1) / kBN : 0;
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (e < E) first_s[e] = run + incl - c;
-      run += __shfl_sync(kAll, incl, 31);
-    }
-    if (lane == 0) first_s[E] = run;
-  }
+  if (warp == 0) scan_chunks(cnt_s, E, first_s);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   const int total = uniform(first_s[E]) * a.n_mtiles;
   if ((int)blockIdx.x >= total) {  // uniform across the CTA
+    if (warp == 1) tmem_dealloc(tmem_base_s, kTmemCols);
     if (early) pdl_wait();  // this kernel's end must mean the end of those before it
     return;
   }
 
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   // All 512 columns are this CTA's, so they begin at column 0: a constant in
   // the MMA's operands. (Were it ever otherwise, nothing below would run.)
   constexpr uint32_t tmem_base = 0;
   if (tmem_base_s != tmem_base) {
     if (tid == 0) atomicOr(a.err, kDevErrTimeout);
     if (warp == 1) tmem_dealloc(tmem_base_s, kTmemCols);
+    if (early) pdl_wait();
     return;
   }
   const int k_tiles = (a.K + 127) / 128;         // scale tiles per row
