@@ -14,8 +14,11 @@ namespace mm {
 // Launches kern<<<grid, block, smem, st>>>(args...). With after_prev the
 // launch uses programmatic stream serialisation: it may be scheduled while
 // the previous kernel of the layer finishes, and the kernel waits for it
-// (griddepcontrol.wait) in every CTA before it touches memory. Only kernels
-// that follow another kernel of the same layer call are launched this way.
+// (griddepcontrol.wait) in every CTA before it touches memory. The layer's
+// kernels are launched this way when they follow another kernel of the same
+// call; the routing from logits and the 4-bit operators always, whatever comes
+// before them on the stream (their calls are short, and the launch is a good
+// part of them: 1 to 3 us a call back to back).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             cudaStream_t st, bool after_prev, Args... args) {

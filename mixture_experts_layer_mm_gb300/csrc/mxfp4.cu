@@ -183,6 +183,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const unsigned 
                                                                  int K, int lanes_log2,
                                                                  uint8_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
   const int per_warp = 32 >> lanes_log2;
   const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
                         ((threadIdx.x & 31) >> lanes_log2);
@@ -258,6 +260,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long nrows, int rows,
     int K, int lanes_log2, unsigned char* __restrict__ out) {
   constexpr int kU = 4;
+  pdl_wait();
+  pdl_trigger();
   const int per_warp = 32 >> lanes_log2;
   const long long row = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * per_warp +
                         ((threadIdx.x & 31) >> lanes_log2);
@@ -521,6 +525,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
     const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int top_k, int h8,
     uint4* __restrict__ out) {
   pdl_wait();
+  pdl_trigger();
   const long long n = (long long)T * h8;
   for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kMxThreads) {
@@ -578,14 +583,14 @@ template <int DT>
 cudaError_t quantize_t(const unsigned char* x, long long prows, int rows, int rp, int K, int ll,
                        uint8_t* codes, uint8_t* scales, dim3 grid, cudaStream_t st) {
   return launch_k(aligned32(x) ? mx_quantize_kernel<DT, true> : mx_quantize_kernel<DT, false>, grid,
-                  dim3(kMxThreads), 0, st, false, x, prows, rows, rp, K, ll, codes, scales);
+                  dim3(kMxThreads), 0, st, true, x, prows, rows, rp, K, ll, codes, scales);
 }
 
 template <int DT>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, long long nrows, int rows,
                          int K, int ll, unsigned char* out, dim3 grid, cudaStream_t st) {
   return launch_k(aligned32(out) ? mx_dequantize_kernel<DT, true> : mx_dequantize_kernel<DT, false>,
-                  grid, dim3(kMxThreads), 0, st, false, codes, scales, nrows, rows, K, ll, out);
+                  grid, dim3(kMxThreads), 0, st, true, codes, scales, nrows, rows, K, ll, out);
 }
 
 }  // namespace
@@ -625,9 +630,8 @@ cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, i
   const MxPlaceArgs a = {reinterpret_cast<const unsigned char*>(hidden), ids, counts,
                          cursor, pos, codes, scales, err, T, E, top_k, H};
   if (T * top_k <= kMxEarlyIds)
-    return launch_k(mx_place_small_kernel, dim3(T), dim3(kPlaceWarps * 32), 0, st, false, a);
-  cudaError_t e = launch_k(mx_group_kernel, dim3(kGroupBlocks), dim3(kGroupThreads), 0, st, false,
-                           a);
+    return launch_k(mx_place_small_kernel, dim3(T), dim3(kPlaceWarps * 32), 0, st, true, a);
+  cudaError_t e = launch_k(mx_group_kernel, dim3(kGroupBlocks), dim3(kGroupThreads), 0, st, true, a);
   if (e != cudaSuccess) return e;
   return launch_k(mx_place_kernel, dim3((T + kMxWarps - 1) / kMxWarps), dim3(kMxThreads), 0, st,
                   true, a);

@@ -720,9 +720,9 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   // (8192 x 4096, K = 4096: 56.7 us in that order, 54.3 without; K = 1024: 23.4
   // and 24.3; 64 x 4096 x 4096, few tiles: 8.9 and 9.6).
   if (N % 32 == 0 && (K <= 2048 || tiles < num_sms))
-    return launch_mode<kDense, true>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
+    return launch_mode<kDense, true>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true,
                                      st);
-  return launch_mode<kDense, false>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, false,
+  return launch_mode<kDense, false>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true,
                                     st);
 }
 

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kRlFinish) route_logits_finish_kernel(int rows
   __shared__ int4 cs[G][C];
   const int c4 = threadIdx.x % C, g = threadIdx.x / C;
   pdl_wait();
+  pdl_trigger();
   float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
   int4 c = make_int4(0, 0, 0, 0);
   const float4* pp = reinterpret_cast<const float4*>(a.part_p) + c4;
@@ -556,9 +557,9 @@ template <int EP, typename TL>
 cudaError_t forward_ep(const TL* logits, const RouteLogitsArgs& a, int blocks, cudaStream_t st) {
   if (blocks == 1)
     return launch_k(route_logits_kernel<EP, kRlOneBlockWarps, TL>, dim3(1),
-                    dim3(kRlOneBlockWarps * 32), 0, st, false, logits, a);
+                    dim3(kRlOneBlockWarps * 32), 0, st, true, logits, a);
   cudaError_t e = launch_k(route_logits_kernel<EP, kRlWarps, TL>, dim3(blocks), dim3(kRlThreads), 0,
-                           st, false, logits, a);
+                           st, true, logits, a);
   if (e != cudaSuccess) return e;
   return launch_k(route_logits_finish_kernel<EP>, dim3(1), dim3(kRlFinish), 0, st, true, blocks,
                   a);
@@ -577,12 +578,12 @@ cudaError_t backward_t(const TL* logits, TL* grad, const RouteLogitsBwdArgs& a, 
                        cudaStream_t st) {
   const dim3 g(blocks), b(kRlThreads);
   if (a.E <= 32)
-    return launch_k(route_logits_backward_kernel<32, TL>, g, b, 0, st, false, logits, grad, a);
+    return launch_k(route_logits_backward_kernel<32, TL>, g, b, 0, st, true, logits, grad, a);
   if (a.E <= 64)
-    return launch_k(route_logits_backward_kernel<64, TL>, g, b, 0, st, false, logits, grad, a);
+    return launch_k(route_logits_backward_kernel<64, TL>, g, b, 0, st, true, logits, grad, a);
   if (a.E <= 128)
-    return launch_k(route_logits_backward_kernel<128, TL>, g, b, 0, st, false, logits, grad, a);
-  return launch_k(route_logits_backward_kernel<256, TL>, g, b, 0, st, false, logits, grad, a);
+    return launch_k(route_logits_backward_kernel<128, TL>, g, b, 0, st, true, logits, grad, a);
+  return launch_k(route_logits_backward_kernel<256, TL>, g, b, 0, st, true, logits, grad, a);
 }
 
 int ep_of(int E) { return E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256; }
