@@ -183,6 +183,9 @@ struct Piece {
   __device__ __forceinline__ float at(int j, int g, int c) const {
     return __uint_as_float(r[j >> 1][4 * g + 2 * (j & 1) + c]);
   }
+  __device__ __forceinline__ void set(int j, int g, int c, float v) {
+    r[j >> 1][4 * g + 2 * (j & 1) + c] = __float_as_uint(v);
+  }
 };
 
 __device__ __forceinline__ void load_piece(uint32_t taddr, Piece& p) {
@@ -190,17 +193,26 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, Piece& p) {
   tmem_ld_16x256b_x4(taddr + (16u << 16), p.r[1]);  // lanes 16-31
 }
 
-// Biased exponents of the largest magnitude of the piece's 32 columns, for the
-// token rows (g, 0) in the low and (g, 1) in the high half (255: an infinity or
-// a NaN among them). Below, both rows are handled in one word as far as it goes.
-__device__ __forceinline__ uint32_t exponent_pair(const float (&a)[4], const float (&b)[4]) {
-  const float x = max_nan(max_nan(fabsf(a[0]), fabsf(a[1])), max_nan(fabsf(a[2]), fabsf(a[3])));
-  const float y = max_nan(max_nan(fabsf(b[0]), fabsf(b[1])), max_nan(fabsf(b[2]), fabsf(b[3])));
-  uint32_t m = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 4));
-  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 8));
-  m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 16));
-  return (m >> 7) & 0x00FF00FFu;
+// Biased exponents of the largest magnitude of the piece's 32 columns (255: an
+// infinity or a NaN among them): e[g] for the token rows (g, 0) in the low and
+// (g, 1) in the high half. Below, both rows are handled in one word as far as
+// it goes, and all four words go through the exchanges together.
+__device__ __forceinline__ void row_exponents(const Piece& p, uint32_t (&e)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float m[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      m[c] = max_nan(max_nan(fabsf(p.at(0, g, c)), fabsf(p.at(1, g, c))),
+                     max_nan(fabsf(p.at(2, g, c)), fabsf(p.at(3, g, c))));
+    e[g] = __byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x7632);  // upper halves
+  }
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) e[g] = __vmaxu2(e[g], __shfl_xor_sync(kAll, e[g], o));
+#pragma unroll
+  for (int g = 0; g < 4; ++g) e[g] = (e[g] >> 7) & 0x00FF00FFu;
 }
 
 // The factors 2^(f - 127) of two biased exponents f in the halves of a word.
@@ -550,10 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
           uint8_t* codes = static_cast<uint8_t*>(a.out) + row0 * (a.N / 2) + (blk * 32 + col4) / 2;
           const int k_tiles_act = (a.N + 127) / 128;
-          uint32_t sb[4];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float x[2][4];
+          for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -561,14 +571,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The divide and the exponential are off by a few units of the
                 // 24th bit; the 4-bit rounding that follows keeps 2 bits.
                 const float gate = p0.at(j, g, c), up = p1.at(j, g, c);
-                x[c][j] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+                p0.set(j, g, c, __fdividef(gate, 1.0f + __expf(-gate)) * up);
               }
+          uint32_t e[4], sb[4];
+          row_exponents(p0, e);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
             float inv[2];
-            sb[g] = scale_pair(exponent_pair(x[0], x[1]), inv);
+            sb[g] = scale_pair(e[g], inv);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const uint16_t two = mx_pack4(x[c][0] * inv[c], x[c][1] * inv[c], x[c][2] * inv[c],
-                                            x[c][3] * inv[c]);
+              const uint16_t two = mx_pack4(p0.at(0, g, c) * inv[c], p0.at(1, g, c) * inv[c],
+                                            p0.at(2, g, c) * inv[c], p0.at(3, g, c) * inv[c]);
               if (real && 8 * g + 2 * (lane & 3) + c < ncol)
                 *reinterpret_cast<uint16_t*>(codes + (8 * g + c) * (size_t)(a.N / 2)) = two;
             }
@@ -577,29 +591,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r < ncol)
             a.act_scales[mx_scale_offset(t.row0 + c0 + r, blk, k_tiles_act)] = real ? own_byte(sb) : 0;
         } else {
+          uint32_t e[2][4], yb[4];
+          if (MODE == kDown) {
+            row_exponents(p0, e[0]);
+            row_exponents(p1, e[1]);
+          }
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const Piece& p = half == 0 ? p0 : p1;
             const int n = t.m * 256 + half * 128 + q * 32;
             if (n >= a.N) continue;
             const size_t at = (size_t)row0 * a.N + n + col4;
-            uint32_t yb[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              float x[2][4];
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[c][j] = p.at(j, g, c);
               float inv[2];
-              if (MODE == kDown) yb[g] = y_pair(exponent_pair(x[0], x[1]), inv);
+              if (MODE == kDown) yb[g] = y_pair(e[half][g], inv);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const bool in = 8 * g + 2 * (lane & 3) + c < ncol;
                 const size_t to = at + (size_t)(8 * g + c) * a.N;
+                const float x[4] = {p.at(0, g, c), p.at(1, g, c), p.at(2, g, c), p.at(3, g, c)};
                 if (MODE == kDown) {
-                  const __half2 lo = __floats2half2_rn(x[c][0] * inv[c], x[c][1] * inv[c]);
-                  const __half2 hi = __floats2half2_rn(x[c][2] * inv[c], x[c][3] * inv[c]);
+                  const __half2 lo = __floats2half2_rn(x[0] * inv[c], x[1] * inv[c]);
+                  const __half2 hi = __floats2half2_rn(x[2] * inv[c], x[3] * inv[c]);
                   if (in)
                     *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
@@ -607,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (a.out_fp32) {
                   if (in)
                     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) =
-                        make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+                        make_float4(x[0], x[1], x[2], x[3]);
                 } else if (in) {
                   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
-                      make_uint2(bf16x2(x[c][0], x[c][1]), bf16x2(x[c][2], x[c][3]));
+                      make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
                 }
               }
             }
