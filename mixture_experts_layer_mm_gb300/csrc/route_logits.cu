@@ -16,9 +16,16 @@
 // sum does not.
 //
 // One warp takes one token; lane l holds the Q = 1, 2, 4 or 8 consecutive
-// experts from l Q on (one vector load). Both passes read each logit once. The sums over tokens stay in the lane that owns the
-// expert, then go block by block through the caller's workspace in a fixed
-// order, so every output is the same on every call.
+// experts from l Q on (one vector load). Both passes read each logit once. The
+// sums over tokens stay in the lane that owns the expert, then go block by block
+// through the caller's workspace in a fixed order, so every output is the same
+// on every call.
+//
+// What bounds it: small batches are launches (64 tokens x 128 experts 6.5 us,
+// 4096 x 128 in bf16 forward and backward 12.4 us). 131072 x 256 fp32 logits
+// take 84 us forward and 60 us backward, 134 and 268 MB: the forward issues 600
+// instructions a token (selection and the exact exponentials), 78 % of the
+// issue slots; the backward 318, at 4.5 TB/s.
 #include <math.h>
 
 #include "mm_device.cuh"
