@@ -72,13 +72,19 @@ SIGNATURES = {
 
 _lib: Optional[ctypes.CDLL] = None
 
-# The marshalling of the short calls as an extension (csrc/marshal.cpp). Its
-# functions return None for a call that is not an ordinary one, and everything
-# is marshalled here where it has not been built.
-try:
-    from . import _marshal as _fast
-except ImportError:
-    _fast = None
+# The marshalling of the short calls as an extension (csrc/marshal.cpp), loaded
+# with the library. Its functions return None for a call that is not an ordinary
+# one, and everything is marshalled here where it has not been built for this
+# torch.
+_fast = None
+
+
+def _load_fast():
+    try:
+        from . import _marshal
+    except ImportError:
+        return None
+    return _marshal if getattr(_marshal, "torch_version", None) == torch.__version__ else None
 
 
 class MMError(RuntimeError):
@@ -89,7 +95,7 @@ class MMError(RuntimeError):
 
 def lib() -> ctypes.CDLL:
     """Load libmm.so (built by __graft_entry__.build()); raises if absent."""
-    global _lib
+    global _lib, _fast
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"CUDA library not built: {LIB_PATH} is missing "
@@ -100,6 +106,7 @@ def lib() -> ctypes.CDLL:
             fn.restype = res
             fn.argtypes = args
         _lib = l
+        _fast = _load_fast()
     return _lib
 
 

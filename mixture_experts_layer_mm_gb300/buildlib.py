@@ -58,16 +58,16 @@ def _compile(src: str, extra: list[str]) -> str:
 
 def _compile_marshal() -> str | None:
     """The object of marshal.cpp; None (with a line saying why) if it does not compile."""
-    obj = os.path.join(BUILD, "marshal.cpp.o")
-    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(MARSHAL_SRC),
-                                                            _headers_mtime()):
-        return obj
     try:
         import torch
+        obj = os.path.join(BUILD, f"marshal.cpp.{torch.__version__}.o")
+        if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(MARSHAL_SRC),
+                                                                _headers_mtime()):
+            return obj
         inc = os.path.join(os.path.dirname(torch.__file__), "include")
         cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
         cmd = [os.environ.get("CXX", "g++"), "-c", MARSHAL_SRC, "-o", obj + ".tmp", "-O2",
-               "-std=c++17", "-fPIC", "-w", "-I" + INCLUDE, "-I" + inc,
+               "-std=c++17", "-fPIC", "-w", f'-DMARSHAL_TORCH="{torch.__version__}"', "-I" + INCLUDE, "-I" + inc,
                "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
                "-I" + sysconfig.get_paths()["include"], "-I" + cuda_inc]
         r = subprocess.run(cmd, capture_output=True, text=True)

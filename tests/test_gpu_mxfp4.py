@@ -552,3 +552,22 @@ def test_products_on_two_streams_and_in_a_graph():
         g.replay()
     _status_ok()
     assert all(torch.equal(x, want) for x in got + [one])
+
+
+@pytest.mark.parametrize("M,N,K", [(2560, 2048, 2304), (8200, 700, 2080), (20000, 256, 256)])
+def test_large_products(M, N, K):
+    # Enough tiles for all SMs, in both orders of the weight rows; the float64
+    # product on the GPU.
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a = mm.mm_mxfp4_quantize(torch.randn(M, K, generator=g, device="cuda"))
+    b = mm.mm_mxfp4_quantize(torch.randn(N, K, generator=g, device="cuda") * 0.05)
+    av = mm.mm_mxfp4_dequantize(*a, dtype=torch.float32).double()
+    bv = mm.mm_mxfp4_dequantize(*b, dtype=torch.float32).double()
+    want, mag = av @ bv.T, av.abs() @ bv.abs().T
+    for dt in (torch.float32, torch.bfloat16):
+        c = mm.mm_mxfp4_gemm(*a, *b, out_dtype=dt).double()
+        tol = K * 2.0 ** -23 * mag  # as in test_product
+        if dt == torch.bfloat16:
+            tol = tol + (want.abs() + tol) * 2.0 ** -8
+        assert bool(((c - want).abs() <= tol).all())
+    _status_ok()
