@@ -491,8 +491,9 @@ int mm_route_logits_backward(const void* logits, int dtype, const uint8_t* token
  * mm_mxfp4_quantize: s = max(floor(log2 max|x|) - 2, -127) + 127 per block,
  * codes = x 2^(127 - s) to the nearest e2m1, ties to the even code, beyond 6
  * to 6. A block that holds an infinity or a NaN becomes NaN. x
- * [batch, rows, K] of any MM_DTYPE. K % 32 == 0 (else MM_ERR_UNSUPPORTED);
- * x, codes and scales 16-byte aligned. batch == 0 or rows == 0: no-op.
+ * [batch, rows, K] of any MM_DTYPE. K % 32 == 0, and K as well as batch times
+ * rows (in whole tiles) at most 2^31 - 4096 (else MM_ERR_UNSUPPORTED); x, codes
+ * and scales 16-byte aligned. batch == 0 or rows == 0: no-op.
  */
 int mm_mxfp4_quantize(const void* x, int dtype, int batch, int rows, int K, uint8_t* codes,
                       uint8_t* scales, void* stream);
@@ -502,8 +503,10 @@ int64_t mm_mxfp4_scales_size(int batch, int rows, int K);
 
 /*
  * The values of stored 4-bit matrices, out [batch, rows, K] of any MM_DTYPE.
- * Every value is exact in fp32 and bf16; fp16 rounds, beyond its range to
- * infinity or zero. Otherwise as mm_mxfp4_quantize.
+ * Scale bytes up to 252 (all that mm_mxfp4_quantize writes besides 255) give
+ * values that are exact in fp32 and bf16; with 253 and 254 the values beyond
+ * their range become infinite. fp16 rounds, beyond its range to infinity or
+ * zero. Otherwise as mm_mxfp4_quantize.
  */
 int mm_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int batch, int rows, int K,
                         void* out, int dtype, void* stream);
@@ -511,8 +514,8 @@ int mm_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int batch, 
 /*
  * C[M,N] = A B^T of a [M,K] and b [N,K] in 4-bit floats, on the block-scaled
  * tensor cores with fp32 accumulation: one rounding to out_dtype
- * (MM_DTYPE_BF16) or none (MM_DTYPE_FP32). M, N >= 0, K % 32 == 0. Scales and
- * alignment as above. M == 0 or N == 0: no-op.
+ * (MM_DTYPE_BF16) or none (MM_DTYPE_FP32). M, N >= 0, K % 32 == 0. Scales,
+ * alignment and limits as above. M == 0 or N == 0: no-op.
  */
 int mm_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                   const uint8_t* b_scales, int M, int N, int K, void* c, int out_dtype,

@@ -29,8 +29,9 @@ int check_logits(int dtype, int T, int E, int top_k) {
 int check_mx(int batch, int rows, int K) {
   if (batch < 0 || rows < 0 || K <= 0) return MM_ERR_INVALID_ARG;
   if (K % kMxBlock != 0) return MM_ERR_UNSUPPORTED;
-  // Row indices (of the padded scale rows too) stay within 31 bits.
-  if ((long long)batch * mx_tiles(rows) * kMxTile >= (1LL << 31)) return MM_ERR_UNSUPPORTED;
+  // Row indices (of the padded scale rows too) and column indices are 32-bit.
+  if ((long long)batch * mx_tiles(rows) * kMxTile > kMxMaxExtent || K > kMxMaxExtent)
+    return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
 
@@ -48,11 +49,11 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
     return MM_ERR_UNSUPPORTED;
   ExpertsLayout L;
   const long long Tk = (long long)T * k;
-  // Whole 128-row tiles: a segment is padded to them, and so is the buffer.
-  L.capacity = Tk + (long long)E * (kMxBlockM - 1);
-  const long long rows = mx_tiles(L.capacity) * kMxTile;
-  if (rows >= (1LL << 31) || 2LL * E * std::max(I, H) >= (1LL << 31)) return MM_ERR_UNSUPPORTED;
   const long long busy = std::min<long long>(E, Tk);  // segments that hold rows
+  // Whole 128-row tiles: a segment is padded to them, and so is the buffer.
+  L.capacity = Tk + busy * (kMxBlockM - 1);
+  const long long rows = mx_tiles(L.capacity) * kMxTile;
+  if (rows > kMxMaxExtent || 2LL * E * std::max(I, H) > kMxMaxExtent) return MM_ERR_UNSUPPORTED;
   L.max_chunks = busy + (Tk - busy) / kMxBlockM;
   if (L.max_chunks * ((std::max(I, H) + 127) / 128) >= (1LL << 31)) return MM_ERR_UNSUPPORTED;
   size_t off = 0;

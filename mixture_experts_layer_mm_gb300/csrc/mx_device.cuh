@@ -23,6 +23,9 @@ namespace mm {
 constexpr int kMxBlock = 32;      // columns per scale
 constexpr int kMxTile = 128;      // rows and columns per scale tile
 constexpr int kMxTileBytes = 512;
+// Most rows (of a batch, in whole tiles) and columns: loops that step past the
+// end by less than 4096 stay within 31 bits.
+constexpr long long kMxMaxExtent = (1LL << 31) - 4096;
 
 __host__ __device__ constexpr long long mx_tiles(long long n) { return (n + kMxTile - 1) / kMxTile; }
 

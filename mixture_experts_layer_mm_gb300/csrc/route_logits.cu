@@ -604,8 +604,8 @@ bool rows_are_vectors(const void* p, int E, int size) {
 }
 
 int blocks_for(int T, int num_sms) {
-  const int want = (T + kRlWarps - 1) / kRlWarps;
-  return want < 2 * num_sms ? want : 2 * num_sms;
+  const long long want = ((long long)T + kRlWarps - 1) / kRlWarps;
+  return (int)(want < 2 * num_sms ? want : 2 * num_sms);
 }
 
 }  // namespace
@@ -616,7 +616,7 @@ constexpr int kRlMaxBlocks = 320;
 
 long long route_logits_workspace(int T, int E) {
   if (T <= kRlOneBlockTokens) return 0;
-  const long long rows = (T + kRlWarps - 1) / kRlWarps;
+  const long long rows = ((long long)T + kRlWarps - 1) / kRlWarps;
   return (rows < kRlMaxBlocks ? rows : kRlMaxBlocks) * ep_of(E) * 8;
 }
 

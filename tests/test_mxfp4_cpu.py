@@ -104,6 +104,34 @@ def test_experts_refusals(L):
     assert size(64, 2048, 128, 768, 8) >= 512 * (2048 // 2 + 768 // 2 + 2048 * 2)
 
 
+def test_sizes_at_the_end_of_the_index_range(L):
+    top = (1 << 31) - 1
+    # The most tokens: the workspace of any long batch, not one of a wrapped count.
+    assert L.mm_route_logits_workspace_size(top, 8) == L.mm_route_logits_workspace_size(1 << 20, 8)
+    # Rows and columns end 4096 short of 2^31, so that steps beyond them stay in range.
+    last = (1 << 31) - 4096
+    assert L.mm_mxfp4_scales_size(1, 1, last) == last // 128 * 512
+    assert L.mm_mxfp4_scales_size(1, last, 32) == last // 128 * 512
+    assert L.mm_mxfp4_scales_size(1, 1, last + 32) == -1
+    assert L.mm_mxfp4_scales_size(1, last + 1, 32) == -1
+    assert L.mm_mxfp4_scales_size(2, 1 << 30, 32) == -1
+    for K in (last + 32, (1 << 31) - 32):
+        assert L.mm_mxfp4_quantize(16, F32, 1, 1, K, 16, 16, None) == UNS
+        assert L.mm_mxfp4_dequantize(16, 16, 1, 1, K, 16, F32, None) == UNS
+        assert L.mm_mxfp4_gemm(16, 16, 16, 16, 1, 1, K, 16, F32, None) == UNS
+    for rows in (last + 1, (1 << 31) - 128, top):
+        assert L.mm_mxfp4_gemm(16, 16, 16, 16, 1, rows, 32, 16, F32, None) == UNS
+        assert L.mm_mxfp4_gemm(16, 16, 16, 16, rows, 1, 32, 16, F32, None) == UNS
+
+
+def test_experts_workspace_counts_the_segments_that_can_hold_rows(L):
+    size = L.mm_moe_experts_mxfp4_workspace_size
+    # One token of 8 slots: 8 segments of 128 rows, whatever the number of experts.
+    row = 2048 // 2 + 768 // 2 + 2048 * 2 + 2048 // 32 + (2048 + 768) // 32  # bytes a row
+    assert 8 * 128 * row <= size(1, 2048, 256, 768, 8) <= 8 * 128 * row + 16384
+    assert size(1, 2048, 128, 768, 8) <= size(1, 2048, 256, 768, 8)
+
+
 def test_binding_refusals(mmlib):
     x = torch.zeros(4, 64)
     with pytest.raises(ValueError, match="CUDA"):
