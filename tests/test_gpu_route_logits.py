@@ -324,3 +324,86 @@ def test_writes_only_its_outputs():
         torch.cuda.synchronize()
         for name, g in b.items():
             assert g.intact(), name
+
+
+def test_as_many_tokens_as_an_index_counts():
+    # One expert, 2^31 - 1 tokens: every token selects it with weight 1.
+    T = (1 << 31) - 1
+    x = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    ids, w, counts, sums, loss = mm.mm_route_logits(x, 1, False)
+    assert not ids.any() and int(counts) == T
+    assert float(w.min()) == 1.0 and float(w.max()) == 1.0
+    # Sums of ones: exact up to 2^24 in a lane (T / (304 * 16) ones) and a block,
+    # then 320 additions at most.
+    assert abs(float(sums) / T - 1) <= 320 * U and abs(float(loss) - 1) <= 324 * U
+    dw = w  # ones
+    g = mm.mm_route_logits_backward(x, ids, counts, False, dw, loss)
+    del ids, w, dw
+    # p = 1: dl = (dw + c) p - p (sum_i p_i (dw_i + c_i)), both terms the same value
+    assert not g.any()
+
+
+def _behind(step, x, src):
+    """`step` on an x that is written late: by a copy on the same stream, by
+    another stream that this one waits for, and by two streams at once."""
+    cur = torch.cuda.current_stream()
+    outs = []
+    for way in range(3):
+        x.zero_()
+        if way == 0:
+            torch.cuda._sleep(200_000)
+            x.copy_(src)
+        else:
+            sides = [torch.cuda.Stream() for _ in range(way)]
+            parts = list(zip(sides, x.chunk(way), src.chunk(way)))
+            for s, a, b in parts:
+                s.wait_stream(cur)
+                with torch.cuda.stream(s):
+                    torch.cuda._sleep(200_000)
+                    a.copy_(b)
+            for s in sides:
+                cur.wait_stream(s)
+        outs.append([t.clone() for t in step(x)])
+    return outs
+
+
+@pytest.mark.parametrize("T", [48, 3000])
+def test_order_behind_copies_and_other_streams(T):
+    # The kernels are launched programmatically: what the stream waits for comes
+    # first all the same, in eager calls and in a captured graph.
+    E, k, H, I = 8, 2, 128, 64
+    rng = np.random.default_rng(T)
+    src = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).cuda()
+    gu = mm.mm_mxfp4_quantize(torch.from_numpy(
+        rng.standard_normal((2 * E, I, H)).astype(np.float32)).cuda())
+    dn = mm.mm_mxfp4_quantize(torch.from_numpy(
+        rng.standard_normal((E, H, I)).astype(np.float32)).cuda())
+
+    def step(x):
+        logits = x[:, :E].contiguous()
+        ids, w, counts, sums, loss = mm.mm_route_logits(logits, k, True)
+        out = mm.mm_moe_experts_mxfp4(x, ids, w, *gu, *dn)
+        g = mm.mm_route_logits_backward(logits, ids, counts, True, w, loss)
+        codes, scales = mm.mm_mxfp4_quantize(x)
+        c = mm.mm_mxfp4_gemm(codes, scales, gu[0][0], gu[1][0])
+        return ids, w, counts, sums, loss, out, g, codes, c
+
+    def first(x):  # each operator directly behind what wrote its input
+        return (*mm.mm_mxfp4_quantize(x),)
+
+    want = [[t.clone() for t in f(src)] for f in (step, first)]
+    torch.cuda.synchronize()
+    x = torch.empty_like(src)
+    for f, w in zip((step, first), want):
+        for got in _behind(f, x, src):
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = _behind(f, x, src)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        for got in outs:
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+    assert mm.mm_poll_device_status() == mm.MM_OK
