@@ -70,7 +70,7 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
   L.act = take((size_t)rows * I / 2);
   L.act_scales = take((size_t)(rows / kMxTile) * mx_tiles(I) * kMxTileBytes);
   L.y = take((size_t)rows * H * 2);
-  L.y_scale = take((size_t)rows * H / 32);
+  L.y_scale = take((size_t)rows * mx_y_row_bytes(H));
   L.total = off;
   *out = L;
   return MM_OK;

@@ -278,7 +278,7 @@ cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, i
                             int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,
                             cudaStream_t st);
 // out[t] = bf16(sum_j w[t,j] y[pos[t top_k + j]]), y fp16 under y_scale (one
-// byte for 32 columns).
+// byte for 32 columns, mx_y_row_bytes(H) a row).
 cudaError_t launch_mx_combine(const uint16_t* y, const uint8_t* y_scale, const int32_t* pos,
                               const float* w, int T, int top_k, int H, uint16_t* out, int num_sms,
                               bool after_prev, cudaStream_t st);

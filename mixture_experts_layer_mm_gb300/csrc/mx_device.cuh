@@ -63,7 +63,11 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
 // 2^-8 of the bf16 output (bf16 here would double that output's rounding error).
 // The byte is the biased exponent of the largest magnitude, kept in [15, 254]
 // so that both factors, 2^(141 - byte) and its inverse, are normal floats;
-// infinity and NaN pass through fp16.
+// infinity and NaN pass through fp16. A row's bytes are in groups of 8, one for
+// each 256 columns (a tile of the product), block b of the row at place
+// mx_y_place(b): a thread of the product has blocks b and b + 4 of a row.
+__host__ __device__ constexpr long long mx_y_row_bytes(long long h) { return (h + 255) / 256 * 8; }
+__device__ __forceinline__ int mx_y_place(int b) { return (b & ~7) + 2 * (b & 3) + ((b >> 2) & 1); }
 __device__ __forceinline__ float mx_y_unit(uint32_t byte) {  // 2^(byte - 141)
   return __uint_as_float((byte - 14u) << 23);
 }
@@ -96,11 +100,52 @@ __device__ __forceinline__ uint16_t mx_pack4(float v0, float v1, float v2, float
   return r;
 }
 
-// The larger value, NaN if either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest magnitude, NaN if any value is one.
+__device__ __forceinline__ float max_abs4(float a, float b, float c, float d) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(fabsf(d)));
   return r;
+}
+
+// Two floats at once.
+struct Pair {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t pair_bits(Pair a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ Pair bits_pair(uint64_t v) {
+  Pair r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+
+// g / (1 + e^-g) * u for two values: 2^t and 1 / x as the hardware gives them,
+// off by |g| 2^-24 and a few units of the 24th bit. Where e^-g is beyond 2^126
+// (g < -87.3) the quotient is 0 (silu is above -2e-36 there).
+__device__ __forceinline__ Pair swiglu(Pair g, Pair u) {
+  constexpr float kLog2e = 1.44269504088896341f;
+  const Pair t = g * Pair{-kLog2e, -kLog2e};
+  Pair e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const Pair d = e + Pair{1.f, 1.f};
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return g * r * u;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

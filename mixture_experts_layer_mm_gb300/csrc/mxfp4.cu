@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
     const uint4* __restrict__ y, const uint8_t* __restrict__ y_scale,
     const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int top_k, int h8,
     uint4* __restrict__ out) {
+  const int row_bytes = (int)mx_y_row_bytes(8LL * h8);
   pdl_wait();
   pdl_trigger();
   const long long n = (long long)T * h8;
@@ -549,13 +550,14 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
       }
       uint4 v[8];
       uint32_t byte[8];
+      const int place = mx_y_place(h >> 2);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] = make_uint4(0u, 0u, 0u, 0u);
         byte[j] = 15u;
         if (r[j] >= 0) {
           v[j] = __ldg(y + (size_t)r[j] * h8 + h);
-          byte[j] = __ldg(y_scale + ((size_t)r[j] * h8 + h) / 4);
+          byte[j] = __ldg(y_scale + (size_t)r[j] * row_bytes + place);
         }
       }
 #pragma unroll

@@ -103,8 +103,9 @@ struct Tile {
 };
 
 // Exclusive sums of the segments' chunks, by one warp: lane l takes the experts
-// from 8 l on (at most 256 in all). first[E] is the total.
-__device__ __forceinline__ void scan_chunks(const int* cnt, int E, int* first) {
+// from 8 l on (at most 256 in all). first[E] is the total; each count is
+// replaced by the row behind the segment's last.
+__device__ __forceinline__ void scan_chunks(int* cnt, int E, int* first) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = kMaxExperts / 32;
   int c[kPer], sum = 0;
@@ -123,29 +124,57 @@ __device__ __forceinline__ void scan_chunks(const int* cnt, int E, int* first) {
   int run = incl - sum;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (lane * kPer + i < E) first[lane * kPer + i] = run;
+    if (lane * kPer + i < E) {
+      first[lane * kPer + i] = run;
+      cnt[lane * kPer + i] += run * kBN;
+    }
     run += c[i];
   }
   if (lane == 31) first[E] = incl;
 }
 
+// The tiles of a CTA: blockIdx.x, then every gridDim.x-th, m-tiles within chunks.
 // Chunks of a segment follow one another, and segments begin at whole chunks:
-// chunk ch of the table is rows [128 ch, 128 ch + 128) of the token matrix.
-__device__ __forceinline__ Tile tile_at(int tile, int n_mtiles, int E, const int* first_chunk,
-                                        const int* cnt) {
+// chunk ch of the table is rows [128 ch, 128 ch + 128) of the token matrix. Every
+// warp walks on its own; a step finds the chunk's expert from the last one on.
+struct Walk {
   Tile t;
-  const int lane = threadIdx.x & 31;
-  const int ch = tile / n_mtiles;
-  t.m = tile - ch * n_mtiles;
-  int below = 0;  // experts whose first chunk is at or before ch: the last is ch's
-  for (int e0 = 0; e0 < E; e0 += 32)
-    below += __popc(__ballot_sync(kAll, e0 + lane < E && first_chunk[e0 + lane] <= ch));
-  const int lo = uniform(below - 1);
-  t.e = lo;
-  t.row0 = ch * kBN;
-  t.nrows = min(kBN, uniform(cnt[lo]) - (ch - uniform(first_chunk[lo])) * kBN);
-  return t;
-}
+  int ch, dch, dm;
+
+  __device__ __forceinline__ Walk(int n_mtiles, int E, const int* first, const int* end) {
+    ch = blockIdx.x / n_mtiles;
+    t.m = blockIdx.x - ch * n_mtiles;
+    dch = gridDim.x / n_mtiles;
+    dm = gridDim.x - dch * n_mtiles;
+    t.e = 0;
+    find(E, first, end);
+  }
+  __device__ __forceinline__ void step(int n_mtiles, int E, const int* first, const int* end) {
+    ch += dch;
+    t.m += dm;
+    if (t.m >= n_mtiles) {
+      t.m -= n_mtiles;
+      ++ch;
+    }
+    find(E, first, end);
+  }
+
+ private:
+  // The last expert whose first chunk is at or before ch (first is ascending).
+  __device__ __forceinline__ void find(int E, const int* first, const int* end) {
+    const int lane = threadIdx.x & 31;
+    int e = t.e;
+    while (true) {
+      const int i = e + 1 + lane;
+      const int n = __popc(__ballot_sync(kAll, i < E && first[i] <= ch));
+      e += n;
+      if (n < 32) break;
+    }
+    t.e = uniform(e);
+    t.row0 = ch * kBN;
+    t.nrows = min(kBN, uniform(end[t.e]) - t.row0);
+  }
+};
 
 // The first two m-tile halves of a tile in the weight matrices: 128-row tile
 // index (also of the scales) and code row of A0; A1 exists if has1.
@@ -183,8 +212,10 @@ struct Piece {
   __device__ __forceinline__ float at(int j, int g, int c) const {
     return __uint_as_float(r[j >> 1][4 * g + 2 * (j & 1) + c]);
   }
-  __device__ __forceinline__ void set(int j, int g, int c, float v) {
-    r[j >> 1][4 * g + 2 * (j & 1) + c] = __float_as_uint(v);
+  __device__ __forceinline__ Pair rows(int j, int g) const { return {at(j, g, 0), at(j, g, 1)}; }
+  __device__ __forceinline__ void set(int j, int g, Pair v) {
+    r[j >> 1][4 * g + 2 * (j & 1)] = __float_as_uint(v.x);
+    r[j >> 1][4 * g + 2 * (j & 1) + 1] = __float_as_uint(v.y);
   }
 };
 
@@ -193,61 +224,51 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, Piece& p) {
   tmem_ld_16x256b_x4(taddr + (16u << 16), p.r[1]);  // lanes 16-31
 }
 
-// Biased exponents of the largest magnitude of the piece's 32 columns (255: an
-// infinity or a NaN among them): e[g] for the token rows (g, 0) in the low and
-// (g, 1) in the high half. Below, both rows are handled in one word as far as
-// it goes, and all four words go through the exchanges together.
-__device__ __forceinline__ void row_exponents(const Piece& p, uint32_t (&e)[4]) {
+// Block exponents. A block is a token row of the piece, its 32 columns spread
+// over the 8 lanes of one lane % 4. Each thread takes the largest magnitude of
+// its 4 columns; the upper halves of two rows (c = 0, 1) go into one word, which
+// orders them by exponent (255: an infinity or a NaN). The exchanges fold as
+// they reduce: at each step a lane keeps half of its words and gives the other
+// half away, so that lane 8 g + i ends with the two rows of word g, and the
+// factors come back by one shuffle a word.
+__device__ __forceinline__ void local_max(const Piece& p, uint32_t (&w)[4]) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float m[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      m[c] = max_nan(max_nan(fabsf(p.at(0, g, c)), fabsf(p.at(1, g, c))),
-                     max_nan(fabsf(p.at(2, g, c)), fabsf(p.at(3, g, c))));
-    e[g] = __byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x7632);  // upper halves
-  }
-#pragma unroll
-  for (int o = 4; o <= 16; o <<= 1)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) e[g] = __vmaxu2(e[g], __shfl_xor_sync(kAll, e[g], o));
-#pragma unroll
-  for (int g = 0; g < 4; ++g) e[g] = (e[g] >> 7) & 0x00FF00FFu;
+  for (int g = 0; g < 4; ++g)
+    w[g] = __byte_perm(
+        __float_as_uint(max_abs4(p.at(0, g, 0), p.at(1, g, 0), p.at(2, g, 0), p.at(3, g, 0))),
+        __float_as_uint(max_abs4(p.at(0, g, 1), p.at(1, g, 1), p.at(2, g, 1), p.at(3, g, 1))),
+        0x7632);  // upper halves, signs are 0
 }
 
-// The factors 2^(f - 127) of two biased exponents f in the halves of a word.
-__device__ __forceinline__ void factor_pair(uint32_t f, float (&inv)[2]) {
-  inv[0] = __uint_as_float(f << 23);
-  inv[1] = __uint_as_float((f << 7) & 0xFF800000u);
+// Keeps `mine` of two words, gives the other to lane ^ o, takes the maximum.
+__device__ __forceinline__ uint32_t fold(uint32_t low, uint32_t high, int o) {
+  const bool up = threadIdx.x & o;
+  return __vmaxu2(up ? high : low, __shfl_xor_sync(kAll, up ? low : high, o));
 }
 
-// mx_scale_byte and mx_inv_scale of two exponents.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t e, float (&inv)[2]) {
+__device__ __forceinline__ uint32_t exponents(uint32_t w) { return (w >> 7) & 0x00FF00FFu; }
+
+// mx_scale_byte of two exponents, and f with mx_inv_scale = 2^(f - 127) (0 for f = 0).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t e, uint32_t& f) {
   uint32_t s = __vmaxu2(e, 0x00020002u) - 0x00020002u;
-  factor_pair(0x00FE00FEu - s, inv);
+  f = 0x00FE00FEu - s;
   const uint32_t bad = (e + 0x00010001u) & 0x01000100u;  // exponents of 255
-  if (bad != 0) {
-    s += (bad >> 7);  // 253 -> 255
-    if (bad & 0xFFFFu) inv[0] = 0.f;
-    if (bad >> 16) inv[1] = 0.f;
-  }
+  s += bad >> 7;                                          // 253 -> 255
+  if (bad & 0xFFFFu) f &= 0xFFFF0000u;
+  if (bad >> 16) f &= 0xFFFFu;
   return s;
 }
 
-// The bytes of y (see mx_y_unit) and the factors 2^(141 - byte) for two exponents.
-__device__ __forceinline__ uint32_t y_pair(uint32_t e, float (&inv)[2]) {
+// The bytes of y (see mx_y_unit) of two exponents, and f with 2^(141 - byte) = 2^(f - 127).
+__device__ __forceinline__ uint32_t y_pair(uint32_t e, uint32_t& f) {
   const uint32_t b = __vminu2(__vmaxu2(e, 0x000F000Fu), 0x00FE00FEu);
-  factor_pair(0x010C010Cu - b, inv);
+  f = 0x010C010Cu - b;
   return b;
 }
 
-// The byte of token row 8 (lane / 8) + 2 (lane % 4) + (lane / 4) % 2 out of the
-// four pairs, which every lane of one lane % 4 holds.
-__device__ __forceinline__ uint32_t own_byte(const uint32_t (&b)[4]) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t lo = lane & 8 ? b[1] : b[0], hi = lane & 8 ? b[3] : b[2];
-  const uint32_t w = lane & 16 ? hi : lo;
-  return lane & 4 ? w >> 16 : w & 0xFFFFu;
+// 2^(f - 127) of the two halves of a word, 0 for f = 0.
+__device__ __forceinline__ Pair factors(uint32_t f) {
+  return {__uint_as_float(f << 23), __uint_as_float((f << 7) & 0xFF800000u)};
 }
 
 // Issues one stage of one accumulator: the scale tiles of its `steps` / 2
@@ -273,6 +294,12 @@ __device__ __forceinline__ void issue_stage(uint32_t st, int a_tile, uint32_t ts
     umma_mxf4(d, da + kk * 2, db + kk * 2, idesc | idesc_mxf4_pair((kk & 1) * 2), col, col + 4,
               accumulate || kk != 0);
   }
+}
+
+// Four floats to fp16.
+__device__ __forceinline__ uint2 half4(float a, float b, float c, float d) {
+  const __half2 lo = __floats2half2_rn(a, b), hi = __floats2half2_rn(c, d);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 template <int MODE, bool PERM>
@@ -334,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_trigger();
   __syncthreads();
-  if (warp == 0) scan_chunks(cnt_s, E, first_s);
+  if (warp == 0) scan_chunks(cnt_s, E, first_s);  // cnt_s: now the segments' ends
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -412,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.x_scales + ((long long)(t.row0 / 128) * k_tiles + kt) * kMxTileBytes,
                 min(2, k_tiles - kt) * kMxTileBytes, fb);
     };
+    Walk walk(a.n_mtiles, E, first_s, cnt_s);
     int fetched = 0;  // stages of the first tile whose weights are already on their way
     if (early) {
-      const Tile t = tile_at(blockIdx.x, a.n_mtiles, E, first_s, cnt_s);
+      const Tile& t = walk.t;
       const WeightAt w = weights_of<MODE>(a, t);
       fetched = min(nk, kStages);
       if (leader) {
@@ -436,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
+      if (tile != (int)blockIdx.x) walk.step(a.n_mtiles, E, first_s, cnt_s);
+      const Tile& t = walk.t;
       const WeightAt w = weights_of<MODE>(a, t);
       for (int kb = 0; kb < nk; ++kb) {
         const int slot = s;
@@ -484,9 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t d = tmem_base + warp * kBN;
     int s = 0;
     uint32_t ph = 0, it = 0;
+    Walk walk(a.n_mtiles, E, first_s, cnt_s);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
+      if (it != 0) walk.step(a.n_mtiles, E, first_s, cnt_s);
+      const Tile& t = walk.t;
       const bool work = warp == 0 || weights_of<MODE>(a, t).has1;
       if (!warp_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
         stop(&stop_s, a.err);
@@ -533,9 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;                    // tensor-memory lane quarter of this warp
     const int c0 = ((warp - kEpiWarp0) >> 2) * 32;  // first column (token row) of this warp
     uint32_t it = 0;
+    Walk walk(a.n_mtiles, E, first_s, cnt_s);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       if (stopped(&stop_s)) break;
-      const Tile t = tile_at(tile, a.n_mtiles, E, first_s, cnt_s);
+      if (it != 0) walk.step(a.n_mtiles, E, first_s, cnt_s);
+      const Tile& t = walk.t;
       const bool has1 = weights_of<MODE>(a, t).has1;
       if (!warp_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
@@ -555,8 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(tempty));
         const int ncol = t.nrows - c0;  // token rows of this piece (may exceed 32)
         if (ncol <= 0) continue;
-        const long long row0 = t.row0 + c0 + 2 * (lane & 3);
-        const int col4 = (lane >> 2) * 4;
+        const int lane4 = lane & 3, col4 = (lane >> 2) * 4;
+        const long long row0 = t.row0 + c0 + 2 * lane4;
+        const int left = ncol - 2 * lane4;  // row (g, c) is one of them if 8 g + c < left
+        // The row whose bytes this lane holds after the folds, with c = lane / 4 % 2.
+        const int own = 8 * (lane >> 3) + 2 * lane4 + ((lane >> 2) & 1);
+        const int from = lane & 7;  // lane 8 g + from has word g
         if (MODE == kGateUp) {
           const int blk = t.m * 4 + q;       // block of 32 intermediates: this warp's lanes
           const bool real = blk * 32 < a.N;  // else the padding of the last scale tile
@@ -565,75 +602,85 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                // The divide and the exponential are off by a few units of the
-                // 24th bit; the 4-bit rounding that follows keeps 2 bits. Below
-                // gate = -87.3 the quotient is 0 (silu is above -2e-36 there).
-                const float gate = p0.at(j, g, c), up = p1.at(j, g, c);
-                p0.set(j, g, c, __fdividef(gate, 1.0f + __expf(-gate)) * up);
-              }
-          uint32_t e[4], sb[4];
-          row_exponents(p0, e);
+            for (int j = 0; j < 4; ++j) p0.set(j, g, swiglu(p0.rows(j, g), p1.rows(j, g)));
+          uint32_t w[4], f;
+          local_max(p0, w);
+          uint32_t k = fold(fold(w[0], w[2], 16), fold(w[1], w[3], 16), 8);
+          k = __vmaxu2(k, __shfl_xor_sync(kAll, k, 4));
+          const uint32_t sb = scale_pair(exponents(k), f);
+          if (own < ncol)
+            a.act_scales[mx_scale_offset(t.row0 + c0 + own, blk, k_tiles_act)] =
+                real ? (uint8_t)(lane & 4 ? sb >> 16 : sb) : 0;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            float inv[2];
-            sb[g] = scale_pair(e[g], inv);
+            const Pair inv = factors(__shfl_sync(kAll, f, 8 * g + from));
+            Pair x[4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint16_t two = mx_pack4(p0.at(0, g, c) * inv[c], p0.at(1, g, c) * inv[c],
-                                            p0.at(2, g, c) * inv[c], p0.at(3, g, c) * inv[c]);
-              if (real && 8 * g + 2 * (lane & 3) + c < ncol)
-                *reinterpret_cast<uint16_t*>(codes + (8 * g + c) * (size_t)(a.N / 2)) = two;
-            }
+            for (int j = 0; j < 4; ++j) x[j] = p0.rows(j, g) * inv;
+            if (real && 8 * g < left)
+              *reinterpret_cast<uint16_t*>(codes + (8 * g) * (size_t)(a.N / 2)) =
+                  mx_pack4(x[0].x, x[1].x, x[2].x, x[3].x);
+            if (real && 8 * g + 1 < left)
+              *reinterpret_cast<uint16_t*>(codes + (8 * g + 1) * (size_t)(a.N / 2)) =
+                  mx_pack4(x[0].y, x[1].y, x[2].y, x[3].y);
           }
-          const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
-          if (r < ncol)
-            a.act_scales[mx_scale_offset(t.row0 + c0 + r, blk, k_tiles_act)] = real ? own_byte(sb) : 0;
         } else {
-          uint32_t e[2][4], yb[4];
+          const int n = t.m * 256 + q * 32;  // and n + 128 from the second accumulator
+          const bool in0 = n < a.N, in1 = n + 128 < a.N;
           if (MODE == kDown) {
-            row_exponents(p0, e[0]);
-            row_exponents(p1, e[1]);
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const Piece& p = half == 0 ? p0 : p1;
-            const int n = t.m * 256 + half * 128 + q * 32;
-            if (n >= a.N) continue;
-            const size_t at = (size_t)row0 * a.N + n + col4;
+            uint32_t w0[4], w1[4], f;
+            local_max(p0, w0);
+            local_max(p1, w1);
+            // Lanes with bit 2 keep the second accumulator's words.
+            const uint32_t k0 = fold(fold(w0[0], w0[2], 16), fold(w0[1], w0[3], 16), 8);
+            const uint32_t k1 = fold(fold(w1[0], w1[2], 16), fold(w1[1], w1[3], 16), 8);
+            const uint32_t b = y_pair(exponents(fold(k0, k1, 4)), f);
+            // Both bytes of row `own`: c = 0 for the lanes without bit 2, 1 for the others.
+            const uint32_t other = __shfl_xor_sync(kAll, b, 4);
+            const uint32_t two = lane & 4 ? __byte_perm(other, b, 0x0062) : __byte_perm(b, other, 0x0040);
+            if (own < ncol)
+              *reinterpret_cast<uint16_t*>(a.act_scales +
+                                           (size_t)(t.row0 + c0 + own) * mx_y_row_bytes(a.N) +
+                                           t.m * 8 + q * 2) = (uint16_t)two;
+            __half* y = static_cast<__half*>(a.out) + row0 * a.N + n + col4;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              float inv[2];
-              if (MODE == kDown) yb[g] = y_pair(e[half][g], inv);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const bool in = 8 * g + 2 * (lane & 3) + c < ncol;
-                const size_t to = at + (size_t)(8 * g + c) * a.N;
-                const float x[4] = {p.at(0, g, c), p.at(1, g, c), p.at(2, g, c), p.at(3, g, c)};
-                if (MODE == kDown) {
-                  const __half2 lo = __floats2half2_rn(x[0] * inv[c], x[1] * inv[c]);
-                  const __half2 hi = __floats2half2_rn(x[2] * inv[c], x[3] * inv[c]);
-                  if (in)
-                    *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + to) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                   *reinterpret_cast<const uint32_t*>(&hi));
-                } else if (a.out_fp32) {
-                  if (in)
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) =
-                        make_float4(x[0], x[1], x[2], x[3]);
-                } else if (in) {
-                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
-                      make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-                }
+              for (int half = 0; half < 2; ++half) {
+                const Pair inv = factors(__shfl_sync(kAll, f, 8 * g + (half ? from | 4 : from & 3)));
+                Pair x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = (half ? p1 : p0).rows(j, g) * inv;
+                __half* to = y + (8 * g) * (size_t)a.N + 128 * half;
+                const bool in = half ? in1 : in0;
+                if (in && 8 * g < left)
+                  *reinterpret_cast<uint2*>(to) = half4(x[0].x, x[1].x, x[2].x, x[3].x);
+                if (in && 8 * g + 1 < left)
+                  *reinterpret_cast<uint2*>(to + a.N) = half4(x[0].y, x[1].y, x[2].y, x[3].y);
               }
             }
-            if (MODE == kDown) {
-              const int r = 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1);
-              if (r < ncol)
-                a.act_scales[((size_t)(t.row0 + c0 + r) * a.N + n) / 32] = (uint8_t)own_byte(yb);
-            }
+          } else {
+            const size_t at = (size_t)row0 * a.N + n + col4;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (8 * g + c >= left) continue;
+                const size_t to = at + (8 * g + c) * (size_t)a.N;
+                if (a.out_fp32) {
+                  float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + to);
+                  if (in0) d[0] = make_float4(p0.at(0, g, c), p0.at(1, g, c), p0.at(2, g, c), p0.at(3, g, c));
+                  if (in1) d[32] = make_float4(p1.at(0, g, c), p1.at(1, g, c), p1.at(2, g, c), p1.at(3, g, c));
+                } else {
+                  uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to);
+                  if (in0)
+                    d[0] = make_uint2(bf16x2(p0.at(0, g, c), p0.at(1, g, c)),
+                                      bf16x2(p0.at(2, g, c), p0.at(3, g, c)));
+                  if (in1)
+                    d[32] = make_uint2(bf16x2(p1.at(0, g, c), p1.at(1, g, c)),
+                                       bf16x2(p1.at(2, g, c), p1.at(3, g, c)));
+                }
+              }
           }
         }
       } else {
