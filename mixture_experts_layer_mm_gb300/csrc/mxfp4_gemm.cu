@@ -86,6 +86,7 @@ struct MxGemmArgs {
   int N, K;       // output columns (gate_up: intermediates), reduction
   int n_mtiles;
   int out_fp32;   // dense
+  int narrow;     // dense: tiles of 128 output columns, not 256
 };
 
 // Whether a warp of this CTA gave up a wait (asked by a converged warp).
@@ -195,11 +196,13 @@ __device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& 
     w.st1 = w.st0 + tiles;
     w.has1 = true;
   } else {
-    w.row0 = t.e * a.N + t.m * 256;
+    const bool narrow = MODE == kDense && a.narrow;
+    const int m = narrow ? t.m : 2 * t.m;
+    w.row0 = t.e * a.N + m * 128;
     w.row1 = w.row0 + 128;
-    w.st0 = (long long)t.e * tiles + 2 * t.m;
+    w.st0 = (long long)t.e * tiles + m;
     w.st1 = w.st0 + 1;
-    w.has1 = 2 * t.m + 1 < tiles;
+    w.has1 = !narrow && m + 1 < tiles;
   }
   return w;
 }
@@ -569,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stopped(&stop_s)) break;
       if (it != 0) walk.step(a.n_mtiles, E, first_s, cnt_s);
       const Tile& t = walk.t;
-      const bool has1 = weights_of<MODE>(a, t).has1;
       if (!warp_wait(smem_u32(tfull), it & 1u)) {
         stop(&stop_s, a.err);
         break;
@@ -625,8 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mx_pack4(x[0].y, x[1].y, x[2].y, x[3].y);
           }
         } else {
-          const int n = t.m * 256 + q * 32;  // and n + 128 from the second accumulator
-          const bool in0 = n < a.N, in1 = n + 128 < a.N;
+          const bool narrow = MODE == kDense && a.narrow;
+          const int n = t.m * (narrow ? 128 : 256) + q * 32;  // and n + 128 from the second accumulator
+          const bool in0 = n < a.N, in1 = !narrow && n + 128 < a.N;
           if (MODE == kDown) {
             uint32_t w0[4], w1[4], f;
             local_max(p0, w0);
@@ -694,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(tempty));
-        const int ncol = t.nrows - c0, n0 = t.m * 256 + q * 32 + lane;
-        const bool in0 = n0 < a.N, in1 = n0 + 128 < a.N;
+        const int ncol = t.nrows - c0, n0 = t.m * (a.narrow ? 128 : 256) + q * 32 + lane;
+        const bool in0 = n0 < a.N, in1 = !a.narrow && n0 + 128 < a.N;
         size_t at = (size_t)(t.row0 + c0) * a.N + n0;
 #pragma unroll
         for (int j = 0; j < 32; ++j, at += a.N) {
@@ -772,9 +775,16 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   a.rows = M;
   a.N = N;
   a.K = K;
-  a.n_mtiles = (N + 255) / 256;
   a.out_fp32 = out_fp32 ? 1 : 0;
-  const long long tiles = (long long)((M + kBN - 1) / kBN) * a.n_mtiles;
+  const long long chunks = (M + kBN - 1) / kBN;
+  // Tiles of 128 output columns where they still leave every CTA at most one: a
+  // CTA takes in some 90 bytes a cycle, so it is the bytes of a tile that count
+  // (64 x 4096 x 4096: 9.0 -> 8.2 us; 1111 x 1000 x 2080: 10.6 -> 8.1. Not the
+  // experts' down product, whose CTAs fetch weights beside those of gate_up: one
+  // token 15.2 -> 16.7).
+  a.narrow = chunks * ((N + 127) / 128) <= num_sms ? 1 : 0;
+  a.n_mtiles = (N + (a.narrow ? 127 : 255)) / (a.narrow ? 128 : 256);
+  const long long tiles = chunks * a.n_mtiles;
   const long long scale_tiles = (long long)mx_tiles(N) * mx_tiles(K);
   // With whole groups of 32 output columns a thread can have four of them and
   // store wide, but the boxes in that row order take longer to load. Long
