@@ -27,11 +27,12 @@
 // memory, whose bandwidth the MMAs need, 63 and 100; this 64 and 65.) The
 // activation is quantised from the fp32 product and is rounded once.
 //
-// What bounds it, on one GB300: 8192 x 4096 x 4096 takes 55 us (5.0 PFLOP/s).
+// What bounds it, on one GB300: 8192 x 4096 x 4096 takes 54 us (5.1 PFLOP/s).
 // One stage of a tile alone on the chip takes 580 cycles, its 8 MMAs and 8
 // scale copies the tensor pipe's 576; with all SMs at work 640, as the 52 KB of
-// a stage come at 80 bytes a cycle and SM, 14 TB/s out of L2. Few rows per
-// expert (64 tokens) are bound by the weights' bytes.
+// a stage come at 80 bytes a cycle and SM, 14 TB/s out of L2. Few tiles (64 x
+// 4096 x 4096, 6.9 us) are bound by what one SM takes in, 90 bytes a cycle. Few
+// rows per expert (64 tokens) are bound by the weights' bytes.
 #include <algorithm>
 
 #include "mm.h"
@@ -45,14 +46,21 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kBN = 128;   // token rows per chunk
-constexpr int kStages = 4;
 constexpr int kStageK = 256;                // columns per stage (128 bytes a row)
 constexpr int kTileBytes = 128 * 128;       // 128 rows of one stage
 constexpr int kScaleStage = 2 * kMxTileBytes;  // scale bytes of 128 rows of one stage
-constexpr int kStageBytes = 3 * kTileBytes + 3 * kScaleStage;
-constexpr int kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-constexpr int kSmemBytes = kStages * kStageStride + 1024;
-static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
+
+// The ring of stages: NA weight tiles and the token rows a slot, then the scales
+// of each. A ring of one weight tile a slot holds six.
+template <int NA>
+struct Ring {
+  static constexpr int kStages = NA == 1 ? 6 : 4;
+  static constexpr int kRowsAt = NA * kTileBytes;
+  static constexpr int kScalesAt = kRowsAt + kTileBytes;
+  static constexpr int kStride = (kScalesAt + (NA + 1) * kScaleStage + 1023) / 1024 * 1024;
+  static constexpr int kSmemBytes = kStages * kStride + 1024;
+  static_assert(kSmemBytes <= 227 * 1024 - 4096, "shared memory");
+};
 
 // Warp roles: 0, 1 = MMA issuers (D0, D1), 2-17 = epilogue, 18, 19 = producers
 // (every other ring slot). There is one pair of accumulators (the scales take
@@ -70,6 +78,8 @@ constexpr int kThreads = (kProdWarp0 + kProdWarps) * 32;  // 640: 96 registers a
 // neither depends on the other's order).
 constexpr uint32_t kScaleCol0 = 2 * kBN, kScaleCols = 32;
 constexpr uint32_t kTmemCols = 512;
+static_assert(kScaleCol0 + Ring<1>::kStages * kScaleCols <= kTmemCols, "tensor memory");
+static_assert(kScaleCol0 + Ring<2>::kStages * kScaleCols <= kTmemCols, "tensor memory");
 
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
@@ -86,7 +96,6 @@ struct MxGemmArgs {
   int N, K;       // output columns (gate_up: intermediates), reduction
   int n_mtiles;
   int out_fp32;   // dense
-  int narrow;     // dense: tiles of 128 output columns, not 256
 };
 
 // Whether a warp of this CTA gave up a wait (asked by a converged warp).
@@ -185,7 +194,7 @@ struct WeightAt {
   bool has1;
 };
 
-template <int MODE>
+template <int MODE, int NA>
 __device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& t) {
   WeightAt w;
   const int tiles = (a.N + 127) / 128;  // scale tile rows per weight matrix
@@ -196,13 +205,12 @@ __device__ __forceinline__ WeightAt weights_of(const MxGemmArgs& a, const Tile& 
     w.st1 = w.st0 + tiles;
     w.has1 = true;
   } else {
-    const bool narrow = MODE == kDense && a.narrow;
-    const int m = narrow ? t.m : 2 * t.m;
+    const int m = NA * t.m;
     w.row0 = t.e * a.N + m * 128;
     w.row1 = w.row0 + 128;
     w.st0 = (long long)t.e * tiles + m;
     w.st1 = w.st0 + 1;
-    w.has1 = !narrow && m + 1 < tiles;
+    w.has1 = NA == 2 && m + 1 < tiles;
   }
   return w;
 }
@@ -277,12 +285,13 @@ __device__ __forceinline__ Pair factors(uint32_t f) {
 // Issues one stage of one accumulator: the scale tiles of its `steps` / 2
 // halves (weights, token rows) to tensor memory, then `steps` MMAs of K = 64.
 // One thread. a_tile 0 or 1: A0 into D0, A1 into D1.
+template <int NA>
 __device__ __forceinline__ void issue_stage(uint32_t st, int a_tile, uint32_t tsc, uint32_t d,
                                             uint32_t idesc, bool accumulate, int steps) {
   const uint64_t da = sdesc_kmajor<128>(st + a_tile * kTileBytes);
-  const uint64_t db = sdesc_kmajor<128>(st + 2 * kTileBytes);
-  const uint64_t sa = sdesc_scales(st + 3 * kTileBytes + a_tile * kScaleStage);
-  const uint64_t sb = sdesc_scales(st + 3 * kTileBytes + 2 * kScaleStage);
+  const uint64_t db = sdesc_kmajor<128>(st + Ring<NA>::kRowsAt);
+  const uint64_t sa = sdesc_scales(st + Ring<NA>::kScalesAt + a_tile * kScaleStage);
+  const uint64_t sb = sdesc_scales(st + Ring<NA>::kScalesAt + NA * kScaleStage);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (2 * h >= steps) break;
@@ -305,12 +314,16 @@ __device__ __forceinline__ uint2 half4(float a, float b, float c, float d) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <int MODE, bool PERM>
+// NA: weight tiles of 128 rows a tile (1: dense only).
+template <int MODE, bool PERM, int NA>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
                    const MxGemmArgs a) {
   static_assert(PERM || MODE == kDense, "blocks along the output columns need the row order");
+  static_assert(NA == 2 || MODE == kDense, "the experts' epilogues take pairs");
+  using R = Ring<NA>;
+  constexpr int kStages = R::kStages, kStageStride = R::kStride;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 3];
   __shared__ uint32_t tmem_base_s;
@@ -327,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 2);  // one commit of each issuer
+      mbar_init(smem_u32(&empty[s]), NA);  // one commit of each issuer that reads it
     }
     mbar_init(smem_u32(tfull), 2);
     mbar_init(smem_u32(tempty), kEpiWarps);
@@ -404,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return (w.has1 ? 2u : 1u) * (kTileBytes + sb);
     };
     auto load_weights = [&](const WeightAt& w, int kb, uint32_t st, uint32_t fb) {
-      const uint32_t sc = st + 3 * kTileBytes;
+      const uint32_t sc = st + R::kScalesAt;
       const int kt = 2 * kb;  // first scale tile of the stage
       if (PERM) {
         tma_load_4d(st, &tmW, fb, kb * row_bytes, w.row0 / 32, pol_w);
@@ -423,8 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // Token rows of a stage: one box of 128, or up to three boxes of 32.
-    auto row_boxes = [](const Tile& t) { return t.nrows > 96 ? 4 : (t.nrows + 31) / 32; };
+    // Token rows of a stage: one box of 128, or up to three boxes of 32. Behind
+    // the last rows of a dense product a box reads nothing (zeros), so there the
+    // one box is always the cheaper (64 rows in two boxes: 7.9 us, in one: 6.9).
+    auto row_boxes = [](const Tile& t) {
+      return MODE == kDense || t.nrows > 96 ? 4 : (t.nrows + 31) / 32;
+    };
     auto stage_bytes = [&](const Tile& t, const WeightAt& w, int kb) {
       return weight_bytes(w, kb) + (uint32_t)row_boxes(t) * 4096u +
              (uint32_t)min(2, k_tiles - 2 * kb) * kMxTileBytes;
@@ -432,13 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_rows = [&](const Tile& t, int kb, uint32_t st, uint32_t fb) {
       const int nbox = row_boxes(t), kt = 2 * kb;
       if (nbox == 4) {
-        tma_load_2d(st + 2 * kTileBytes, &tmX, fb, kb * row_bytes, t.row0, pol_x);
+        tma_load_2d(st + R::kRowsAt, &tmX, fb, kb * row_bytes, t.row0, pol_x);
       } else {
         for (int b = 0; b < nbox; ++b)
-          tma_load_2d(st + 2 * kTileBytes + b * 4096, &tmX32, fb, kb * row_bytes, t.row0 + 32 * b,
+          tma_load_2d(st + R::kRowsAt + b * 4096, &tmX32, fb, kb * row_bytes, t.row0 + 32 * b,
                       pol_x);
       }
-      bulk_load(st + 3 * kTileBytes + 2 * kScaleStage,
+      bulk_load(st + R::kScalesAt + NA * kScaleStage,
                 a.x_scales + ((long long)(t.row0 / 128) * k_tiles + kt) * kMxTileBytes,
                 min(2, k_tiles - kt) * kMxTileBytes, fb);
     };
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int fetched = 0;  // stages of the first tile whose weights are already on their way
     if (early) {
       const Tile& t = walk.t;
-      const WeightAt w = weights_of<MODE>(a, t);
+      const WeightAt w = weights_of<MODE, NA>(a, t);
       fetched = min(nk, kStages);
       if (leader) {
         for (int kb = first; kb < fetched; kb += kProdWarps) {
@@ -469,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tile != (int)blockIdx.x) walk.step(a.n_mtiles, E, first_s, cnt_s);
       const Tile& t = walk.t;
-      const WeightAt w = weights_of<MODE>(a, t);
+      const WeightAt w = weights_of<MODE, NA>(a, t);
       for (int kb = 0; kb < nk; ++kb) {
         const int slot = s;
         const uint32_t parity = ph;
@@ -506,10 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 2) {
     // ------------------------------------------------- MMA issuers (0, 1) ---
-    // Warp 0 feeds D0, warp 1 D1. A tcgen05 instruction takes its thread about
+    // Warp 0 feeds D0, warp 1 D1; with one weight tile, D0 from the even and D1
+    // from the odd stages, which the epilogue adds up. A tcgen05 instruction takes its thread about
     // 30 cycles and a stage's wait 200 more, together above the 60 cycles an
     // MMA of N = 128 takes to run, so one thread for both accumulators leaves
-    // the tensor cores waiting (57 us for 8192 x 4096 x 4096; two: 54).
+    // the tensor cores waiting (57 us for 8192 x 4096 x 4096, two: 54; with one
+    // weight tile 8.3 and 7.5 for 128 x 4096 x 4096).
     // The whole warp runs the loops, so that addresses, descriptors and columns
     // are warp-uniform; one elected lane issues.
     const bool leader = elect_one();
@@ -521,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stopped(&stop_s)) break;
       if (it != 0) walk.step(a.n_mtiles, E, first_s, cnt_s);
       const Tile& t = walk.t;
-      const bool work = warp == 0 || weights_of<MODE>(a, t).has1;
+      const bool work = NA == 1 || warp == 0 || weights_of<MODE, NA>(a, t).has1;
       if (!warp_wait(smem_u32(tempty), (it & 1u) ^ 1u)) {
         stop(&stop_s, a.err);
         break;
@@ -530,29 +549,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_mxf4(128, (t.nrows + 15) & ~15);
       bool ok = true;
       for (int kb = 0; kb < nk; ++kb) {
-        if (!warp_wait(smem_u32(&full[s]), ph)) {
+        const int slot = s;
+        const uint32_t parity = ph;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if (NA == 1 && (kb & 1) != warp) continue;
+        if (!warp_wait(smem_u32(&full[slot]), parity)) {
           stop(&stop_s, a.err);
           ok = false;
           break;
         }
         tc_fence_after();
         if (leader) {
-          const uint32_t st = smem_base + s * kStageStride;
+          const uint32_t st = smem_base + slot * kStageStride;
           // Each slot has scale columns of its own: the MMAs that read their
           // last contents were complete before the slot was filled again.
-          const uint32_t tsc = tmem_base + kScaleCol0 + s * kScaleCols + warp * (kScaleCols / 2);
+          const uint32_t tsc = tmem_base + kScaleCol0 + slot * kScaleCols + warp * (kScaleCols / 2);
           const int steps = min(4, (a.K - kb * kStageK + 63) / 64);
+          const int a_tile = NA == 1 ? 0 : warp;
+          const bool more = NA == 1 ? kb > 1 : kb > 0;
           if (work && steps == 4)
-            issue_stage(st, warp, tsc, d, idesc, kb != 0, 4);
+            issue_stage<NA>(st, a_tile, tsc, d, idesc, more, 4);
           else if (work)
-            issue_stage(st, warp, tsc, d, idesc, kb != 0, steps);
-          umma_commit(smem_u32(&empty[s]));
+            issue_stage<NA>(st, a_tile, tsc, d, idesc, more, steps);
+          umma_commit(smem_u32(&empty[slot]));
         }
         __syncwarp();
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
       }
       if (!ok) break;
       if (leader) umma_commit(smem_u32(tfull));
@@ -627,9 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mx_pack4(x[0].y, x[1].y, x[2].y, x[3].y);
           }
         } else {
-          const bool narrow = MODE == kDense && a.narrow;
-          const int n = t.m * (narrow ? 128 : 256) + q * 32;  // and n + 128 from the second accumulator
-          const bool in0 = n < a.N, in1 = !narrow && n + 128 < a.N;
+          const int n = t.m * (NA * 128) + q * 32;  // and n + 128 from the second accumulator
+          const bool in0 = n < a.N, in1 = NA == 2 && n + 128 < a.N;
           if (MODE == kDown) {
             uint32_t w0[4], w1[4], f;
             local_max(p0, w0);
@@ -663,6 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           } else {
+            if (NA == 1 && nk > 1) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p0.set(j, g, p0.rows(j, g) + p1.rows(j, g));
+            }
             const size_t at = (size_t)row0 * a.N + n + col4;
 #pragma unroll
             for (int g = 0; g < 4; ++g)
@@ -697,13 +726,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(tempty));
-        const int ncol = t.nrows - c0, n0 = t.m * (a.narrow ? 128 : 256) + q * 32 + lane;
-        const bool in0 = n0 < a.N, in1 = !a.narrow && n0 + 128 < a.N;
+        if (NA == 1 && nk > 1) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            d0[j] = __float_as_uint(__uint_as_float(d0[j]) + __uint_as_float(d1[j]));
+        }
+        const int ncol = t.nrows - c0, n0 = t.m * (NA * 128) + q * 32 + lane;
+        const bool in0 = n0 < a.N, in1 = NA == 2 && n0 + 128 < a.N;
         size_t at = (size_t)(t.row0 + c0) * a.N + n0;
 #pragma unroll
         for (int j = 0; j < 32; ++j, at += a.N) {
           if (j >= ncol) break;
-          const float x0 = __uint_as_float(d0[j]), x1 = __uint_as_float(d1[j]);
+          const float x1 = __uint_as_float(d1[j]);
+          const float x0 = __uint_as_float(d0[j]);
           if (a.out_fp32) {
             float* c = static_cast<float*>(a.out);
             if (in0) c[at] = x0;
@@ -728,12 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // w: w_rows rows of weight codes (scale_tiles tiles of 512 bytes); x: x_rows
 // rows of token codes.
-template <int MODE, bool PERM>
+template <int MODE, bool PERM, int NA>
 cudaError_t launch_mode(const uint8_t* w, long long w_rows, long long scale_tiles, const uint8_t* x,
                         long long x_rows, const MxGemmArgs& a, long long max_tiles, int num_sms,
                         bool after_prev, cudaStream_t st) {
   static DeviceFlags attr_done;
-  if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE, PERM>, kSmemBytes);
+  if (cudaError_t e = smem_attr_once(attr_done, mx_gemm_kernel<MODE, PERM, NA>, Ring<NA>::kSmemBytes);
       e != cudaSuccess)
     return e;
   CUtensorMap tmW, tmS = {}, tmX, tmX32;
@@ -757,7 +792,7 @@ cudaError_t launch_mode(const uint8_t* w, long long w_rows, long long scale_tile
   }
   if (!ok) return cudaErrorInvalidValue;
   const int grid = (int)std::min<long long>(max_tiles, num_sms);
-  return launch_k(mx_gemm_kernel<MODE, PERM>, dim3(grid), dim3(kThreads), kSmemBytes, st,
+  return launch_k(mx_gemm_kernel<MODE, PERM, NA>, dim3(grid), dim3(kThreads), Ring<NA>::kSmemBytes, st,
                   after_prev, tmW, tmS, tmX, tmX32, a);
 }
 
@@ -777,13 +812,13 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   a.K = K;
   a.out_fp32 = out_fp32 ? 1 : 0;
   const long long chunks = (M + kBN - 1) / kBN;
-  // Tiles of 128 output columns where they still leave every CTA at most one: a
-  // CTA takes in some 90 bytes a cycle, so it is the bytes of a tile that count
-  // (64 x 4096 x 4096: 9.0 -> 8.2 us; 1111 x 1000 x 2080: 10.6 -> 8.1. Not the
-  // experts' down product, whose CTAs fetch weights beside those of gate_up: one
-  // token 15.2 -> 16.7).
-  a.narrow = chunks * ((N + 127) / 128) <= num_sms ? 1 : 0;
-  a.n_mtiles = (N + (a.narrow ? 127 : 255)) / (a.narrow ? 128 : 256);
+  // Tiles of 128 output columns where they still leave every CTA at most one: an
+  // SM takes in some 90 bytes a cycle, so with few tiles the bytes of a tile
+  // count (64 x 4096 x 4096: 8.9 us with tiles of 256, 6.9 with 128; 1111 x 1000
+  // x 2080: 10.6 and 7.9). (Not the experts' down product, whose CTAs
+  // fetch weights beside those of gate_up: one token 15.2 -> 16.7 us.)
+  const bool narrow = chunks * ((N + 127) / 128) <= num_sms;
+  a.n_mtiles = narrow ? (N + 127) / 128 : (N + 255) / 256;
   const long long tiles = chunks * a.n_mtiles;
   const long long scale_tiles = (long long)mx_tiles(N) * mx_tiles(K);
   // With whole groups of 32 output columns a thread can have four of them and
@@ -791,11 +826,10 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   // reductions over enough tiles to fill the SMs are bound by the loads
   // (8192 x 4096, K = 4096: 56.7 us in that order, 54.3 without; K = 1024: 23.4
   // and 24.3; 64 x 4096 x 4096, few tiles: 8.9 and 9.6).
-  if (N % 32 == 0 && (K <= 2048 || tiles < num_sms))
-    return launch_mode<kDense, true>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true,
-                                     st);
-  return launch_mode<kDense, false>(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true,
-                                    st);
+  const bool perm = N % 32 == 0 && (K <= 2048 || narrow || tiles < num_sms);
+  auto launch = perm ? (narrow ? launch_mode<kDense, true, 1> : launch_mode<kDense, true, 2>)
+                     : (narrow ? launch_mode<kDense, false, 1> : launch_mode<kDense, false, 2>);
+  return launch(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true, st);
 }
 
 cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scales,
@@ -820,7 +854,7 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
   a.N = I;
   a.K = H;
   a.n_mtiles = (I + 127) / 128;
-  return launch_mode<kGateUp, true>(w, 2LL * E * I, 2LL * E * mx_tiles(I) * mx_tiles(H), xs, capacity,
+  return launch_mode<kGateUp, true, 2>(w, 2LL * E * I, 2LL * E * mx_tiles(I) * mx_tiles(H), xs, capacity,
                                     a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
 }
 
@@ -844,7 +878,7 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
   a.N = H;
   a.K = I;
   a.n_mtiles = (H + 255) / 256;
-  return launch_mode<kDown, true>(w, (long long)E * H, (long long)E * mx_tiles(H) * mx_tiles(I), act,
+  return launch_mode<kDown, true, 2>(w, (long long)E * H, (long long)E * mx_tiles(H) * mx_tiles(I), act,
                                   capacity, a, max_chunks * a.n_mtiles, num_sms, after_prev, st);
 }
 

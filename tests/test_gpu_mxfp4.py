@@ -571,3 +571,25 @@ def test_large_products(M, N, K):
             tol = tol + (want.abs() + tol) * 2.0 ** -8
         assert bool(((c - want).abs() <= tol).all())
     _status_ok()
+
+
+# Few tiles (128 columns each, the reduction in two accumulators) next to many
+# (256 columns, the last of them 128 or less), with whole groups of 32 columns
+# and without, one stage of columns and several.
+@pytest.mark.parametrize("M,N,K", [(1, 32, 32), (33, 100, 256), (96, 416, 288), (64, 1000, 544),
+                                   (128, 19456, 512), (128, 19457, 512), (9984, 320, 96),
+                                   (9900, 300, 512), (9900, 288, 2304), (13000, 290, 2080)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_products_of_few_and_many_tiles(M, N, K, out):
+    a, sa, va = _matrix(M, M, K)
+    b, sb, vb = _matrix(N + 1, N, K)
+    got = _np64(mm.mm_mxfp4_gemm(a, sa, b, sb, out_dtype=out))
+    ta, tb = torch.from_numpy(va).cuda(), torch.from_numpy(vb).cuda()
+    want = _np64(ta @ tb.T)
+    # fp32 sums of K exact products: every addition rounds once (or truncates: a
+    # whole step), of partial sums below the sum of magnitudes.
+    bound = (K + 2) * 2.0 ** -23 * _np64(ta.abs() @ tb.abs().T)
+    if out == torch.bfloat16:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want) + 2.0 ** -133
+    assert (np.abs(got - want) <= bound).all()
+    _status_ok()
