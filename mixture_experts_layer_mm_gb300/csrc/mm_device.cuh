@@ -243,4 +243,37 @@ __device__ __forceinline__ void red_add_v4_f32(float* addr, float a, float b, fl
                "f"(a), "f"(b), "f"(c), "f"(d), "l"(policy));
 }
 
+// Two floats in one instruction (each rounded as by the scalar one).
+struct Pair {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t pair_bits(Pair a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ Pair bits_pair(uint64_t v) {
+  Pair r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(r);
+}
+
 }  // namespace mm

@@ -108,31 +108,6 @@ __device__ __forceinline__ float max_abs4(float a, float b, float c, float d) {
   return r;
 }
 
-// Two floats at once.
-struct Pair {
-  float x, y;
-};
-__device__ __forceinline__ uint64_t pair_bits(Pair a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-  return r;
-}
-__device__ __forceinline__ Pair bits_pair(uint64_t v) {
-  Pair r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-  return bits_pair(r);
-}
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-  return bits_pair(r);
-}
-
 // g / (1 + e^-g) * u for two values: 2^t and 1 / x as the hardware gives them,
 // off by |g| 2^-24 and a few units of the 24th bit. Where e^-g is beyond 2^126
 // (g < -87.3) the quotient is 0 (silu is above -2e-36 there).

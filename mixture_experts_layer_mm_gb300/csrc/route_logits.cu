@@ -21,11 +21,11 @@
 // through the caller's workspace in a fixed order, so every output is the same
 // on every call.
 //
-// What bounds it: small batches are launches (64 tokens x 128 experts 6.5 us,
-// 4096 x 128 in bf16 forward and backward 12.4 us). 131072 x 256 fp32 logits
-// take 84 us forward and 60 us backward, 134 and 268 MB: the forward issues 600
-// instructions a token (selection and the exact exponentials), 78 % of the
-// issue slots; the backward 318, at 4.5 TB/s.
+// What bounds it: small batches are launches (64 tokens x 128 experts 6.2 us,
+// 4096 x 128 in bf16 forward and backward 11.7 us). 131072 x 256 fp32 logits
+// take 78 us forward and 53 us backward, 134 and 268 MB: the forward issues 530
+// instructions a token (selection and the exact exponentials, mostly of the half-
+// rate kind), 75 % of the issue slots; the backward 260, at 5 TB/s.
 #include <math.h>
 
 #include "mm_device.cuh"
@@ -51,8 +51,7 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) {
 __device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(uint16_t* p, float v) { *p = f32_to_bf16_bits(v); }
 
-// Q consecutive values as one access (p aligned to its size, at most 16 bytes
-// an access).
+// Q consecutive values as one access (p aligned to its size, up to 32 bytes).
 template <int Q>
 __device__ __forceinline__ void load_vec(const float* p, float (&l)[Q]) {
   if constexpr (Q == 1) {
@@ -61,15 +60,17 @@ __device__ __forceinline__ void load_vec(const float* p, float (&l)[Q]) {
     const float2 v = __ldg(reinterpret_cast<const float2*>(p));
     l[0] = v.x;
     l[1] = v.y;
+  } else if constexpr (Q == 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    l[0] = v.x;
+    l[1] = v.y;
+    l[2] = v.z;
+    l[3] = v.w;
   } else {
-#pragma unroll
-    for (int i = 0; i < Q / 4; ++i) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-      l[4 * i] = v.x;
-      l[4 * i + 1] = v.y;
-      l[4 * i + 2] = v.z;
-      l[4 * i + 3] = v.w;
-    }
+    asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(l[0]), "=f"(l[1]), "=f"(l[2]), "=f"(l[3]), "=f"(l[4]), "=f"(l[5]), "=f"(l[6]),
+          "=f"(l[7])
+        : "l"(p));
   }
 }
 template <int Q>
@@ -97,12 +98,11 @@ template <int Q>
 __device__ __forceinline__ void store_vec(float* p, const float (&g)[Q]) {
   if constexpr (Q == 1) *p = g[0];
   if constexpr (Q == 2) *reinterpret_cast<float2*>(p) = make_float2(g[0], g[1]);
-  if constexpr (Q >= 4) {
-#pragma unroll
-    for (int i = 0; i < Q / 4; ++i)
-      reinterpret_cast<float4*>(p)[i] =
-          make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-  }
+  if constexpr (Q == 4) *reinterpret_cast<float4*>(p) = make_float4(g[0], g[1], g[2], g[3]);
+  if constexpr (Q == 8)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(g[0]),
+                 "f"(g[1]), "f"(g[2]), "f"(g[3]), "f"(g[4]), "f"(g[5]), "f"(g[6]), "f"(g[7])
+                 : "memory");
 }
 template <int Q>
 __device__ __forceinline__ void store_vec(uint16_t* p, const float (&g)[Q]) {
@@ -117,6 +117,16 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&g)[Q]) {
     if constexpr (Q == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     if constexpr (Q == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// Q values of a lane to shared memory, p aligned to 4 Q bytes or 16.
+template <int Q>
+__device__ __forceinline__ void stage(float* p, const float (&g)[Q]) {
+  if constexpr (Q == 1) *p = g[0];
+  if constexpr (Q == 2) *reinterpret_cast<float2*>(p) = make_float2(g[0], g[1]);
+#pragma unroll
+  for (int i = 0; i + 3 < Q; i += 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -179,14 +189,25 @@ __device__ __forceinline__ float redux_max(float v) {
 
 // e^x for x <= 0 (or NaN): 2^t with t = x log2(e) in two parts, the second the
 // rounding of the first product, so that the error stays at that of the
-// hardware's 2^t (2^-22) for any x. Below 2^-126: 0.
-__device__ __forceinline__ float exp_neg(float x) {
+// hardware's 2^t (2^-22) for any x. Below 2^-126: 0. Two values, or one.
+__device__ __forceinline__ Pair exp_neg(Pair x) {
   constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-  const float t = x * kLog2e;
-  const float rest = x > -200.f ? __fmaf_rn(x, kLog2e, -t) : 0.f;
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
-  return __fmaf_rn(r, rest * kLn2, r);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-200.f));  // e^-200 is below 2^-126 too
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-200.f));
+  const Pair t = x * Pair{kLog2e, kLog2e};
+  const Pair rest = fma2(x, Pair{-kLog2e, -kLog2e}, t);  // negative
+  Pair r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+  return fma2(r, rest * Pair{-kLn2, -kLn2}, r);
+}
+__device__ __forceinline__ float exp_neg(float x) { return exp_neg(Pair{x, x}).x; }
+
+// f of pairs (or, of a lane's one value, a pair of it) of a lane's Q values.
+template <int Q, typename F>
+__device__ __forceinline__ void each_pair(F f) {
+#pragma unroll
+  for (int q = 0; q < Q; q += 2) f(q, Q == 1 ? 0 : q + 1);
 }
 
 // p = exp(l - m) (not yet divided by the returned sum), m the row's largest
@@ -203,13 +224,14 @@ __device__ __forceinline__ float exp_row(const float (&l)[Q], float m, float (&p
     for (int q = 0; q < Q; ++q) p[q] = 0.f;
     return nan ? __uint_as_float(0x7fffffffu) : 0.f;
   }
-  float s = 0.f;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    p[q] = exp_neg(l[q] - m);  // 0 past E
-    s += p[q];
-  }
-  return warp_sum(s);
+  Pair s = {0.f, 0.f};
+  each_pair<Q>([&](int a, int b) {
+    const Pair e = exp_neg(Pair{l[a], l[b]} + Pair{-m, -m});  // 0 past E
+    s = s + e;
+    p[a] = e.x;
+    p[b] = e.y;
+  });
+  return warp_sum(Q == 1 ? s.x : s.x + s.y);
 }
 
 // Descending order of Q values (compare-exchange networks of 1, 5 and 19
@@ -337,8 +359,8 @@ template <int EP, int W, typename TL>
 __global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restrict__ logits,
                                                               const RouteLogitsArgs a) {
   constexpr int Q = EP / 32;
-  __shared__ float sp[W * EP];
-  __shared__ int sc[EP];
+  __shared__ __align__(16) float sp[W * EP];  // a warp's p of its token; at the end its sums
+  __shared__ int sc[EP], sid[W * 32];         // counts; a warp's selection, ascending
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t stride = gridDim.x * W, T = (uint32_t)a.T;  // t + stride < 2^32
   pdl_wait();
@@ -346,12 +368,8 @@ __global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restri
   if (threadIdx.x < EP) sc[threadIdx.x] = 0;
   __syncthreads();
   float psum[Q];
-  int cnt[Q];
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    psum[q] = 0.f;
-    cnt[q] = 0;
-  }
+  for (int q = 0; q < Q; ++q) psum[q] = 0.f;
   float next[Q];
   uint32_t t = blockIdx.x * W + warp;
   if (t < T) load_row<Q>(logits, t, a.E, a.vec, next);
@@ -364,40 +382,45 @@ __global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restri
     const uint32_t sel = select_topk<Q>(l, a.E, a.top_k, m);
     const float sum = exp_row<Q>(l, m, p);
     const bool valid = sum != 0.f && (a.mask == nullptr || a.mask[t] != 0);
+    // The selected in ascending order (place = number of selected with a lower
+    // id) and all p go through shared memory, so that lane j has the j-th.
+    __syncwarp();
+    int at = exclusive_sum(__popc(sel));
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if ((sel >> q) & 1u) sid[warp * 32 + at++] = lane * Q + q;
+    stage<Q>(&sp[warp * EP + lane * Q], p);
+    __syncwarp();
+    int id = 0;
+    float pj = 0.f;
+    if (lane < a.top_k) {
+      id = sid[warp * 32 + lane];
+      pj = sp[warp * EP + id];
+    }
     // Weights of the selected: p / sum, or p over the selected p alone.
     float scale = 0.f;
     if (valid) {
       const float inv = 1.f / sum;
       scale = inv;
       if (a.renorm) {
-        float total = 0.f;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          if ((sel >> q) & 1u) total += p[q];
-        total = warp_sum(total);
+        const float total = warp_sum(pj);
         scale = sum == sum ? 1.f / total : sum;  // a NaN in the row: all its weights
       }
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        psum[q] += p[q] * inv;
-        if ((sel >> q) & 1u) ++cnt[q];
-      }
+      each_pair<Q>([&](int a, int b) {
+        const Pair n = fma2(Pair{p[a], p[b]}, Pair{inv, inv}, Pair{psum[a], psum[b]});
+        psum[a] = n.x;
+        psum[b] = n.y;
+      });
     }
-    // Ascending ids: slot = number of selected experts with a lower id.
-    size_t at = (size_t)t * a.top_k + exclusive_sum(__popc(sel));
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if ((sel >> q) & 1u) {
-        a.ids[at] = lane * Q + q;
-        a.w[at] = valid ? p[q] * scale : 0.f;
-        ++at;
-      }
+    if (lane < a.top_k) {
+      a.ids[(size_t)t * a.top_k + lane] = id;
+      a.w[(size_t)t * a.top_k + lane] = valid ? pj * scale : 0.f;
+      if (valid) atomicAdd(&sc[id], 1);  // integers: any order
+    }
   }
+  __syncwarp();
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    sp[warp * EP + lane * Q + q] = psum[q];
-    if (cnt[q] != 0) atomicAdd(&sc[lane * Q + q], cnt[q]);  // integers: any order
-  }
+  for (int q = 0; q < Q; ++q) sp[warp * EP + lane * Q + q] = psum[q];
   __syncthreads();
   float p = 0.f;
   int c = 0;
@@ -473,6 +496,7 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
     const TL* __restrict__ logits, TL* __restrict__ grad, const RouteLogitsBwdArgs a) {
   constexpr int Q = EP / 32;
   __shared__ float c_s[EP];
+  __shared__ __align__(16) float sp[kRlWarps * EP];  // a warp's p of its token
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t stride = gridDim.x * kRlWarps, T = (uint32_t)a.T;  // t + stride < 2^32
   pdl_wait();
@@ -496,14 +520,26 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
     }
   }
   __syncthreads();
-  float next[Q];
+  // The next token's logits and selected are on their way meanwhile.
+  float next[Q], next_d = 0.f;
+  int next_id = -1;
+  const bool slot = a.dw != nullptr && lane < a.top_k;
+  auto load = [&](uint32_t t) {
+    load_row<Q>(logits, t, a.E, a.vec, next);
+    if (slot) {
+      next_id = __ldg(a.ids + (size_t)t * a.top_k + lane);
+      next_d = __ldg(a.dw + (size_t)t * a.top_k + lane);
+    }
+  };
   uint32_t t = blockIdx.x * kRlWarps + warp;
-  if (t < T) load_row<Q>(logits, t, a.E, a.vec, next);
+  if (t < T) load(t);
   for (; t < T; t += stride) {
     float l[Q], p[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) l[q] = next[q];
-    if (t + stride < T) load_row<Q>(logits, t + stride, a.E, a.vec, next);
+    int id = next_id;
+    float dj = next_d;
+    if (t + stride < T) load(t + stride);
     float m = l[0];
 #pragma unroll
     for (int q = 1; q < Q; ++q) m = fmaxf(m, l[q]);
@@ -518,29 +554,27 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
       continue;
     }
     const float inv = 1.f / sum;
-    float pc = 0.f;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      p[q] *= inv;
-      pc += p[q] * c[q];
-    }
-    pc = warp_sum(pc);
-    // The selected experts, one a lane: lane j < k forms p at its id anew (the
-    // same operations on the same logit). An id outside [0, E) or repeated
-    // within the row takes no part.
-    int id = -1;
-    float pj = 0.f, dj = 0.f, sel_term = 0.f, mean = 0.f;
+    Pair both = {0.f, 0.f};
+    each_pair<Q>([&](int a, int b) {
+      const Pair n = Pair{p[a], p[b]} * Pair{inv, inv};
+      both = fma2(n, Pair{c[a], c[b]}, both);
+      p[a] = n.x;
+      p[b] = n.y;
+    });
+    const float pc = warp_sum(Q == 1 ? both.x : both.x + both.y);
+    // The selected experts, one a lane. An id outside [0, E) or repeated within
+    // the row takes no part.
+    float pj = 0.f, sel_term = 0.f, mean = 0.f;
     if (a.dw != nullptr) {
-      if (lane < a.top_k) {
-        id = __ldg(a.ids + (size_t)t * a.top_k + lane);
-        dj = __ldg(a.dw + (size_t)t * a.top_k + lane);
-      }
+      __syncwarp();
+      stage<Q>(&sp[warp * EP + lane * Q], p);
       const uint32_t same = __match_any_sync(kFullMask, id);
       if (id < 0 || id >= a.E || (same & ((1u << lane) - 1u)) != 0) {
         id = -1;
         dj = 0.f;
       }
-      if (id >= 0) pj = exp_neg(load_logit(logits + (size_t)t * a.E + id) - m) * inv;
+      __syncwarp();
+      if (id >= 0) pj = sp[warp * EP + id];
       mean = warp_sum(pj * dj);
       if (a.renorm) {
         const float tot = warp_sum(pj);
@@ -552,8 +586,11 @@ __global__ void __launch_bounds__(kRlThreads) route_logits_backward_kernel(
       }
     }
     const float shift = pc + mean;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) p[q] *= c[q] - shift;
+    each_pair<Q>([&](int a, int b) {
+      const Pair n = Pair{p[a], p[b]} * (Pair{c[a], c[b]} + Pair{-shift, -shift});
+      p[a] = n.x;
+      p[b] = n.y;
+    });
     store_row<Q>(row, a.E, a.vec, p);
     if (a.dw != nullptr) {
       __syncwarp();  // the row's stores above come before these
@@ -599,7 +636,7 @@ int ep_of(int E) { return E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256; }
 
 // Rows of E values that lanes may take Q at a time.
 bool rows_are_vectors(const void* p, int E, int size) {
-  const int Q = ep_of(E) / 32, bytes = Q * size < 16 ? Q * size : 16;
+  const int Q = ep_of(E) / 32, bytes = Q * size;  // up to 32
   return E % Q == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 

@@ -407,3 +407,19 @@ def test_order_behind_copies_and_other_streams(T):
         for got in outs:
             assert all(torch.equal(a, b) for a, b in zip(got, w))
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("E", [256, 200, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [4, 8])
+def test_logits_aligned_to_less_than_a_lane_takes(E, dtype, offset):
+    # A lane takes up to 32 bytes at once where the rows allow it; results do not
+    # depend on it.
+    flat = torch.randn(offset + 70 * E, device="cuda").to(dtype)
+    x = flat[offset:].view(70, E)
+    y = x.clone()
+    dw = torch.randn(70, 5, device="cuda")
+    got, same = mm.mm_route_logits(x, 5, True), mm.mm_route_logits(y, 5, True)
+    assert all(torch.equal(a, b) for a, b in zip(got, same))
+    g = mm.mm_route_logits_backward(x, got[0], got[2], True, dw, got[4])
+    assert torch.equal(g, mm.mm_route_logits_backward(y, got[0], got[2], True, dw, got[4]))
