@@ -640,29 +640,34 @@ bool rows_are_vectors(const void* p, int E, int size) {
   return E % Q == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
-int blocks_for(int T, int num_sms) {
+// As many blocks as run at once: two an SM with 8 experts a lane (62 registers a
+// thread), three with fewer (44 at most).
+int blocks_per_sm(int E) { return ep_of(E) == 256 ? 2 : 3; }
+
+int blocks_for(int T, int E, int num_sms) {
   const long long want = ((long long)T + kRlWarps - 1) / kRlWarps;
-  return (int)(want < 2 * num_sms ? want : 2 * num_sms);
+  const int most = blocks_per_sm(E) * num_sms;
+  return (int)(want < most ? want : most);
 }
 
 }  // namespace
 
-// Rows of partial sums the forward may write (one per block; the grid never
-// exceeds 2 * 160 blocks).
-constexpr int kRlMaxBlocks = 320;
+// Rows of partial sums the forward may write: one per block, of blocks on 160
+// SMs at most.
+static int max_blocks(int E) { return 160 * blocks_per_sm(E); }
 
 long long route_logits_workspace(int T, int E) {
   if (T <= kRlOneBlockTokens) return 0;
   const long long rows = ((long long)T + kRlWarps - 1) / kRlWarps;
-  return (rows < kRlMaxBlocks ? rows : kRlMaxBlocks) * ep_of(E) * 8;
+  return (rows < max_blocks(E) ? rows : max_blocks(E)) * ep_of(E) * 8;
 }
 
 cudaError_t launch_route_logits(const void* logits, bool is_bf16, const uint8_t* mask, int T, int E,
                                 int top_k, int renorm, int32_t* ids, float* w, int32_t* counts,
                                 float* prob_sums, float* loss, void* workspace, int num_sms,
                                 cudaStream_t st) {
-  int blocks = T > kRlOneBlockTokens ? blocks_for(T, num_sms) : 1;
-  if (blocks > kRlMaxBlocks) blocks = kRlMaxBlocks;
+  int blocks = T > kRlOneBlockTokens ? blocks_for(T, E, num_sms) : 1;
+  if (blocks > max_blocks(E)) blocks = max_blocks(E);
   const int EP = ep_of(E);
   RouteLogitsArgs a = {mask, ids, w, nullptr, nullptr, counts, prob_sums, loss, T, E, top_k, renorm,
                        rows_are_vectors(logits, E, is_bf16 ? 2 : 4)};
@@ -681,7 +686,7 @@ cudaError_t launch_route_logits_backward(const void* logits, bool is_bf16, const
   const RouteLogitsBwdArgs a = {mask, ids, counts, dw, dloss, T, E, top_k, renorm,
                                 rows_are_vectors(logits, E, is_bf16 ? 2 : 4) &&
                                     rows_are_vectors(grad, E, is_bf16 ? 2 : 4)};
-  const int blocks = blocks_for(T, num_sms);
+  const int blocks = blocks_for(T, E, num_sms);
   return is_bf16 ? backward_t(static_cast<const uint16_t*>(logits), static_cast<uint16_t*>(grad), a,
                               blocks, st)
                  : backward_t(static_cast<const float*>(logits), static_cast<float*>(grad), a,
