@@ -243,6 +243,24 @@ __device__ __forceinline__ void red_add_v4_f32(float* addr, float a, float b, fl
                "f"(a), "f"(b), "f"(c), "f"(d), "l"(policy));
 }
 
+// Barrier of a cluster's blocks (all threads call it); orders shared memory.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// Block `rank`'s copy of *p, in shared memory.
+__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
+  return __int_as_float(load_peer(reinterpret_cast<const int*>(p), rank));
+}
+
 // Two floats in one instruction (each rounded as by the scalar one).
 struct Pair {
   float x, y;

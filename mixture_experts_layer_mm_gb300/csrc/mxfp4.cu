@@ -428,19 +428,6 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupBlocks = 8;
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
-}
-__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {  // CTA rank's copy of *p
-  uint32_t at;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-
 __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThreads)
     mx_group_kernel(const MxPlaceArgs a) {
   __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts];

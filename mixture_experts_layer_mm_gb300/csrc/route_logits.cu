@@ -21,11 +21,11 @@
 // through the caller's workspace in a fixed order, so every output is the same
 // on every call.
 //
-// What bounds it: small batches are launches (64 tokens x 128 experts 6.2 us,
+// What bounds it: small batches are launches (64 tokens x 128 experts 3.9 us,
 // 4096 x 128 in bf16 forward and backward 11.7 us). 131072 x 256 fp32 logits
 // take 78 us forward and 53 us backward, 134 and 268 MB: the forward issues 530
 // instructions a token (selection and the exact exponentials, mostly of the half-
-// rate kind), 75 % of the issue slots; the backward 260, at 5 TB/s.
+// rate kind), 75 % of the issue slots; the backward 290, at 5 TB/s.
 #include <math.h>
 
 #include "mm_device.cuh"
@@ -36,12 +36,16 @@ namespace {
 
 constexpr int kRlThreads = 512;
 constexpr int kRlWarps = kRlThreads / 32;
-// One block does a batch of up to kRlOneBlockTokens alone: one launch, no
-// workspace, two tokens a warp at most (64 tokens of 128 experts 6.5 us, against
-// 4.9 in two launches, the second of which costs the host as much as is gained;
-// 128 tokens would take 9.9 against 4.9).
+// Small batches take one launch and no workspace: one block up to
+// kRlOneBlockTokens, one cluster up to kRlClusterTokens, two tokens a warp at
+// most. 128 experts, us a call in a captured graph: 64 tokens 3.9 in a cluster,
+// 5.8 in one block; 128 tokens 3.9, 4.9 in two launches; 256 tokens 5.4 and 4.9,
+// but 6.4 and 9.3 outside of a graph, where a launch costs the host as much as the
+// kernel takes.
 constexpr int kRlOneBlockWarps = 32;
-constexpr int kRlOneBlockTokens = 64;
+constexpr int kRlOneBlockTokens = 32;
+constexpr uint32_t kRlClusterBlocks = 8;
+constexpr int kRlClusterTokens = 2 * kRlClusterBlocks * kRlWarps;
 constexpr uint32_t kFullMask = 0xffffffffu;
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
@@ -355,9 +359,10 @@ __device__ __forceinline__ void write_batch(float p, int c, const RouteLogitsArg
   }
 }
 
-template <int EP, int W, typename TL>
-__global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restrict__ logits,
-                                                              const RouteLogitsArgs a) {
+// CLUSTER: the grid is one cluster, whose first block adds the blocks' sums up.
+template <int EP, int W, bool CLUSTER, typename TL>
+__device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits,
+                                                   const RouteLogitsArgs& a) {
   constexpr int Q = EP / 32;
   __shared__ __align__(16) float sp[W * EP];  // a warp's p of its token; at the end its sums
   __shared__ int sc[EP], sid[W * 32];         // counts; a warp's selection, ascending
@@ -429,7 +434,22 @@ __global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restri
     for (int w = 0; w < W; ++w) p += sp[w * EP + threadIdx.x];
     c = sc[threadIdx.x];
   }
-  if (gridDim.x > 1) {
+  if constexpr (CLUSTER) {
+    __syncthreads();  // sp has been read
+    if (threadIdx.x < EP) sp[threadIdx.x] = p;
+    cluster_barrier();
+    if (blockIdx.x == 0 && threadIdx.x < EP) {
+      p = 0.f;
+      c = 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kRlClusterBlocks; ++r) {
+        p += load_peer(&sp[threadIdx.x], r);
+        c += load_peer(&sc[threadIdx.x], r);
+      }
+    }
+    cluster_barrier();  // all sums have been read
+    if (blockIdx.x != 0) return;
+  } else if (gridDim.x > 1) {
     if (threadIdx.x < EP) {
       a.part_p[(size_t)blockIdx.x * EP + threadIdx.x] = p;
       a.part_c[(size_t)blockIdx.x * EP + threadIdx.x] = c;
@@ -438,6 +458,18 @@ __global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restri
   }
   __syncthreads();
   write_batch<EP>(p, c, a, sp, sc);
+}
+
+template <int EP, int W, typename TL>
+__global__ void __launch_bounds__(W * 32) route_logits_kernel(const TL* __restrict__ logits,
+                                                              const RouteLogitsArgs a) {
+  route_logits_block<EP, W, false>(logits, a);
+}
+
+template <int EP, typename TL>
+__global__ void __cluster_dims__(kRlClusterBlocks, 1, 1) __launch_bounds__(kRlThreads)
+    route_logits_cluster_kernel(const TL* __restrict__ logits, const RouteLogitsArgs a) {
+  route_logits_block<EP, kRlWarps, true>(logits, a);
 }
 
 // The blocks' sums, added in block order: EP / 4 threads a row take 4 experts
@@ -604,6 +636,9 @@ cudaError_t forward_ep(const TL* logits, const RouteLogitsArgs& a, int blocks, c
   if (blocks == 1)
     return launch_k(route_logits_kernel<EP, kRlOneBlockWarps, TL>, dim3(1),
                     dim3(kRlOneBlockWarps * 32), 0, st, true, logits, a);
+  if (blocks == 0)
+    return launch_k(route_logits_cluster_kernel<EP, TL>, dim3(kRlClusterBlocks), dim3(kRlThreads),
+                    0, st, true, logits, a);
   cudaError_t e = launch_k(route_logits_kernel<EP, kRlWarps, TL>, dim3(blocks), dim3(kRlThreads), 0,
                            st, true, logits, a);
   if (e != cudaSuccess) return e;
@@ -657,7 +692,7 @@ int blocks_for(int T, int E, int num_sms) {
 static int max_blocks(int E) { return 160 * blocks_per_sm(E); }
 
 long long route_logits_workspace(int T, int E) {
-  if (T <= kRlOneBlockTokens) return 0;
+  if (T <= kRlClusterTokens) return 0;
   const long long rows = ((long long)T + kRlWarps - 1) / kRlWarps;
   return (rows < max_blocks(E) ? rows : max_blocks(E)) * ep_of(E) * 8;
 }
@@ -666,7 +701,7 @@ cudaError_t launch_route_logits(const void* logits, bool is_bf16, const uint8_t*
                                 int top_k, int renorm, int32_t* ids, float* w, int32_t* counts,
                                 float* prob_sums, float* loss, void* workspace, int num_sms,
                                 cudaStream_t st) {
-  int blocks = T > kRlOneBlockTokens ? blocks_for(T, E, num_sms) : 1;
+  int blocks = T <= kRlOneBlockTokens ? 1 : T <= kRlClusterTokens ? 0 : blocks_for(T, E, num_sms);
   if (blocks > max_blocks(E)) blocks = max_blocks(E);
   const int EP = ep_of(E);
   RouteLogitsArgs a = {mask, ids, w, nullptr, nullptr, counts, prob_sums, loss, T, E, top_k, renorm,

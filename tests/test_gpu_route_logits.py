@@ -423,3 +423,15 @@ def test_logits_aligned_to_less_than_a_lane_takes(E, dtype, offset):
     assert all(torch.equal(a, b) for a, b in zip(got, same))
     g = mm.mm_route_logits_backward(x, got[0], got[2], True, dw, got[4])
     assert torch.equal(g, mm.mm_route_logits_backward(y, got[0], got[2], True, dw, got[4]))
+
+
+@pytest.mark.parametrize("E,k", [(256, 8), (100, 5), (40, 3), (7, 7)])
+@pytest.mark.parametrize("T", [31, 32, 33, 128, 129, 255, 256, 257])
+def test_batches_around_one_block_and_one_cluster(T, E, k):
+    x, mask, _ = _case(T + E, T, E, k, masked=0.2)
+    got = mm.mm_route_logits(x, k, True, token_mask=mask)
+    _check(x, mask, k, True, got)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in
+                   zip(got, mm.mm_route_logits(x, k, True, token_mask=mask)))
+    assert mm.mm_poll_device_status() == mm.MM_OK
