@@ -559,7 +559,8 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     """Top-k routing of given router logits [T, E] (float32 or bfloat16) with
     the statistics of the balance loss. Returns (topk_ids int32 [T, k],
     topk_w fp32 [T, k], expert_counts int32 [E], prob_sums fp32 [E],
-    loss fp32 [1]). token_mask [T] (bool or uint8): zero for padding tokens."""
+    loss fp32 [1]). token_mask [T] (bool or uint8): zero for padding tokens.
+    (Ids and weights may share one allocation, and so may the other three.)"""
     if _fast is not None and stream is None:
         r = _fast.route_logits(logits, top_k, renorm, token_mask)
         if r is not None:

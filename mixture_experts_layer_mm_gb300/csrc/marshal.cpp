@@ -20,6 +20,8 @@ namespace {
 
 using at::Tensor;
 
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
 // One call: the device of its first tensor, and whether all fit so far.
 struct Call {
   bool ok = true;
@@ -59,6 +61,19 @@ struct Call {
   Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
     return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)device),
                                   std::nullopt);
+  }
+
+  // Tensors of `type` and the next shapes out of one allocation, 256-byte aligned
+  // each: an allocation takes longer than the rest of a tensor.
+  Tensor part(const Tensor& bytes, int64_t& at, at::IntArrayRef shape, at::ScalarType type) const {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(bytes.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+        c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* i = t.unsafeGetTensorImpl();
+    i->set_sizes_contiguous(shape);
+    i->set_storage_offset(at / (int64_t)c10::elementSize(type));
+    at += round256(t.numel() * (int64_t)c10::elementSize(type));
+    return t;
   }
 
   void* stream() const {
@@ -126,9 +141,17 @@ PyObject* route_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int64_t need = mm_route_logits_workspace_size((int)T, (int)E);
   if (need < 0) Py_RETURN_NONE;
-  Tensor ids = c.make({T, k}, at::kInt), w = c.make({T, k}, at::kFloat),
-         counts = c.make({E}, at::kInt), sums = c.make({E}, at::kFloat),
-         loss = c.make({1}, at::kFloat), ws;
+  // Two allocations for five results: what is the tokens', what is the batch's
+  // (64 tokens: 6.6 -> 5.2 us a call). Codes and scales keep one each: weights are
+  // stored, and formats that store tensors refuse shared memory.
+  const Tensor tokens = c.make({2 * round256(4 * T * k)}, at::kByte),
+               batch = c.make({2 * round256(4 * E) + 4}, at::kByte);
+  int64_t in_tokens = 0, in_batch = 0;
+  Tensor ids = c.part(tokens, in_tokens, {T, k}, at::kInt),
+         w = c.part(tokens, in_tokens, {T, k}, at::kFloat),
+         counts = c.part(batch, in_batch, {E}, at::kInt),
+         sums = c.part(batch, in_batch, {E}, at::kFloat),
+         loss = c.part(batch, in_batch, {1}, at::kFloat), ws;
   if (need > 0) ws = c.make({need}, at::kByte);
   const int rc = mm_route_logits(
       x->data_ptr(), dt, mask ? static_cast<const uint8_t*>(mask->data_ptr()) : nullptr, (int)T,
