@@ -264,6 +264,10 @@ constexpr int kMxBlockM = 128;
 // Up to this many slots every kernel of the 4-bit experts groups them by itself.
 constexpr int kMxEarlyIds = 2048;
 
+// The experts' counters of free rows lie this many ints apart, a line each: side
+// by side their atomics wait for one another (4096 tokens of 8 slots: 4 us).
+constexpr int kMxCursorStep = 32;
+
 // Microscaled 4-bit rows (mxfp4.cu): dtype is an MM_DTYPE, K % 32 == 0.
 cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int rows, int K,
                                uint8_t* codes, uint8_t* scales, cudaStream_t st);
@@ -272,7 +276,7 @@ cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, lo
 // The 4-bit experts' grouping and token rows: segments of kMxBlockM-row
 // multiples (counts [E] rows in each), pos[f] the row of slot f = t top_k +
 // j (-1: dropped id), and that row of codes / scales = hidden[t] quantised.
-// cursor: [E] scratch.
+// cursor: [E * kMxCursorStep] scratch.
 cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, int top_k, int E,
                             int H, int32_t* counts, int32_t* cursor,
                             int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,

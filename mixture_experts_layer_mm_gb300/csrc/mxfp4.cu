@@ -13,8 +13,8 @@
 // its codes and scale bytes are written once, so the kernels are bound by
 // memory: 256 x 768 x 2048 bf16 values take 164 us to quantise (1.02 GB, 6.2
 // TB/s) and 145 us to decode (7.0 TB/s). At 4096 tokens of 2048 values, 8 slots
-// each, the experts' grouping takes 10 us, the rows 20 (17 MB read, 35 MB
-// written, 32768 atomics), the weighted sum 30 (154 MB).
+// each, the experts' grouping takes 9 us, the rows 17 (17 MB read, 35 MB
+// written, 32768 atomics), the weighted sum 24 (154 MB).
 #include "mm.h"
 #include "mm_internal.h"
 #include "mx_device.cuh"
@@ -336,7 +336,7 @@ struct MxPlaceArgs {
   const unsigned char* hidden;
   const int32_t* ids;
   int32_t* counts;   // [E]
-  int32_t* cursor;   // [E] next free row (large batches)
+  int32_t* cursor;   // [E * kMxCursorStep] next free row (large batches)
   int32_t* pos;      // [T * top_k] row of a slot, -1 if dropped
   uint8_t* codes;
   uint8_t* scales;
@@ -461,7 +461,7 @@ __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThr
     __syncthreads();
     for (int e = tid; e < a.E; e += kGroupThreads) {
       a.counts[e] = sum[e];
-      a.cursor[e] = off[e];
+      a.cursor[e * kMxCursorStep] = off[e];
     }
   }
   cluster_barrier();  // no block ends while its counts are being read
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs 
   if (place < 0 || place >= a.E || (same & ((1u << lane) - 1u)) != 0)
     place = -1;
   else
-    place = atomicAdd(a.cursor + place, 1);
+    place = atomicAdd(a.cursor + place * kMxCursorStep, 1);
   if (lane < k) a.pos[(size_t)t * k + lane] = place;
   const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
   for (int c0 = lane * 16; c0 - lane * 16 < hp; c0 += U * kSpan) {
