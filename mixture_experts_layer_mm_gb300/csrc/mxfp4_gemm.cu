@@ -24,7 +24,7 @@
 // is three maxima in the thread and three exchanges for two rows at once, and
 // results leave the thread as they are. (A warp reduction for every column took
 // 90 us for gate_up and 93 for down at 4096 tokens, a transpose through shared
-// memory, whose bandwidth the MMAs need, 63 and 100; this 64 and 65.) The
+// memory, whose bandwidth the MMAs need, 63 and 100; this 62 and 60.) The
 // activation is quantised from the fp32 product and is rounded once.
 //
 // What bounds it, on one GB300: 8192 x 4096 x 4096 takes 54 us (5.1 PFLOP/s).

@@ -140,3 +140,22 @@ def test_results_are_the_callers():
     keep = [mm.mm_route_logits(torch.randn(5, 8, device="cuda"), 2, True) for _ in range(50)]
     assert all(int(r[2].sum()) == 10 for r in keep)
     assert np.isfinite([float(r[4]) for r in keep]).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 3), (65, 70, 7), (300, 256, 8)])
+def test_results_of_one_allocation_are_apart(T, E, k):
+    x = torch.randn(T, E, device="cuda")
+    got = mm.mm_route_logits(x, k, True)
+    assert all(t.data_ptr() % 16 == 0 and t.is_contiguous() for t in got)
+    for i, t in enumerate(got):
+        before = [u.clone() for u in got]
+        t.fill_(77)
+        assert all(torch.equal(u, b) for j, (u, b) in enumerate(zip(got, before)) if j != i)
+        t.copy_(before[i])
+    # and each goes on living without the others, and as an input
+    ids, w = got[0], got[1]
+    counts, loss = got[2].clone(), got[4]
+    del got
+    g = mm.mm_route_logits_backward(x, ids, counts, True, w, loss)
+    torch.cuda.synchronize()
+    assert torch.isfinite(g).all() and w.shape == (T, k)
