@@ -593,3 +593,27 @@ def test_products_of_few_and_many_tiles(M, N, K, out):
         bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want) + 2.0 ** -133
     assert (np.abs(got - want) <= bound).all()
     _status_ok()
+
+
+@pytest.mark.parametrize("k", [1, 7, 8, 9, 20, 32])
+def test_experts_of_many_slots_a_token(k):
+    # Slots are read eight at a time: repeated and bad ids within and across the
+    # eights are dropped, in a batch that is grouped by a kernel of its own.
+    T, H, E, I = 2100 if k == 1 else 300, 64, 40, 64
+    rng = np.random.default_rng(k)
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    bad = rng.random((T, k)) < 0.1
+    if k > 1:
+        ids[bad] = np.where(rng.random(bad.sum()) < 0.5, -3, ids[np.nonzero(bad)[0], 0])
+        first = np.nonzero(bad[:, 0])[0]
+        ids[first, 0] = np.argsort(rng.random((len(first), E)), axis=1)[:, 0]
+    # What counts by definition: an id in range that no earlier slot of its row has.
+    clean = np.array([[e if 0 <= e < E and e not in row[:j] else E + 5
+                       for j, e in enumerate(row)] for row in ids.tolist()], dtype=np.int32)
+    assert (k == 1) == bool((clean == ids).all())
+    d = _experts_case(5, T, H, E, I, k, ids=ids)
+    got = _call(d)
+    d["ids"] = torch.from_numpy(clean).cuda()
+    want = _call(d)
+    assert mm.mm_poll_device_status() == (mm.MM_OK if k == 1 else mm.MM_ERR_DEVICE)
+    assert torch.equal(got, want)
