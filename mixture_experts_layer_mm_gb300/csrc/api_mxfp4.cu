@@ -63,7 +63,7 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
     return o;
   };
   L.counts = take((size_t)E * 4);
-  L.cursor = take((size_t)E * kMxCursorStep * 4);
+  L.cursor = take(Tk > kMxEarlyIds ? (size_t)E * kMxCursorStep * 4 : 0);  // else unused
   L.pos = take((size_t)Tk * 4);
   L.xs = take((size_t)rows * H / 2);
   L.xs_scales = take((size_t)(rows / kMxTile) * mx_tiles(H) * kMxTileBytes);
