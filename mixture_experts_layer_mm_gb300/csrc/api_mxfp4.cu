@@ -39,7 +39,7 @@ bool is_dtype(int d) { return d == MM_DTYPE_FP32 || d == MM_DTYPE_BF16 || d == M
 
 // Workspace of the 4-bit experts.
 struct ExpertsLayout {
-  size_t counts, cursor, pos, xs, xs_scales, act, act_scales, y, y_scale, total;
+  size_t counts, cursor, pos, xs, xs_scales, act, act_scales, y, total;
   long long capacity, max_chunks;
 };
 
@@ -69,8 +69,10 @@ int experts_layout(int T, int H, int E, int I, int k, ExpertsLayout* out) {
   L.xs_scales = take((size_t)(rows / kMxTile) * mx_tiles(H) * kMxTileBytes);
   L.act = take((size_t)rows * I / 2);
   L.act_scales = take((size_t)(rows / kMxTile) * mx_tiles(I) * kMxTileBytes);
-  L.y = take((size_t)rows * H * 2);
-  L.y_scale = take((size_t)rows * mx_y_row_bytes(H));
+  // One fp32 row a slot. Few slots in many segments: no less than two bytes a
+  // value of every padded row and one for 32 values, which the reported size has
+  // always counted.
+  L.y = take(std::max((size_t)Tk * H * 4, (size_t)rows * (2 * (size_t)H + (H + 255) / 256 * 8)));
   L.total = off;
   *out = L;
   return MM_OK;
@@ -222,8 +224,7 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
   uint8_t* act = at<uint8_t>(workspace, L.act);
   uint8_t* act_scales = at<uint8_t>(workspace, L.act_scales);
   int32_t* pos = at<int32_t>(workspace, L.pos);
-  uint16_t* y = at<uint16_t>(workspace, L.y);
-  uint8_t* y_scale = at<uint8_t>(workspace, L.y_scale);
+  float* y = at<float>(workspace, L.y);
   const long long rows = mx_tiles(L.capacity) * kMxTile;
   cudaError_t e = launch_mx_place(hidden, topk_ids, T, top_k, E, H, counts,
                                   at<int32_t>(workspace, L.cursor), pos, xs, xs_scales,
@@ -233,9 +234,9 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
                                   top_k, E, I, H, rows, L.max_chunks, act, act_scales, sms, status, true, st);
   if (e == cudaSuccess)
     e = launch_mx_experts_down(act, act_scales, w_down, w_down_scales, counts, topk_ids, T,
-                               top_k, E, H, I, rows, L.max_chunks, y, y_scale, sms, status, true, st);
+                               top_k, E, H, I, rows, L.max_chunks, y, sms, status, true, st);
   if (e == cudaSuccess)
-    e = launch_mx_combine(y, y_scale, pos, topk_w, T, top_k, H, out, sms, true, st);
+    e = launch_mx_combine(y, pos, topk_w, T, top_k, H, out, true, st);
   return cuda_status(e);
 }
 

@@ -274,24 +274,23 @@ cudaError_t launch_mx_quantize(const void* x, int dtype, long long batch, int ro
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long batch,
                                  int rows, int K, void* out, int dtype, cudaStream_t st);
 // The 4-bit experts' grouping and token rows: segments of kMxBlockM-row
-// multiples (counts [E] rows in each), pos[f] the row of slot f = t top_k +
-// j (-1: dropped id), and that row of codes / scales = hidden[t] quantised.
-// cursor: [E * kMxCursorStep] scratch.
+// multiples (counts [E] rows in each), a row of codes / scales = hidden[t]
+// quantised for every slot f = t top_k + j, and pos[f] that row without the
+// segments' padding (-1: dropped id). cursor: [E * kMxCursorStep] scratch.
 cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, int top_k, int E,
                             int H, int32_t* counts, int32_t* cursor,
                             int32_t* pos, uint8_t* codes, uint8_t* scales, unsigned* err,
                             cudaStream_t st);
-// out[t] = bf16(sum_j w[t,j] y[pos[t top_k + j]]), y fp16 under y_scale (one
-// byte for 32 columns, mx_y_row_bytes(H) a row).
-cudaError_t launch_mx_combine(const uint16_t* y, const uint8_t* y_scale, const int32_t* pos,
-                              const float* w, int T, int top_k, int H, uint16_t* out, int num_sms,
-                              bool after_prev, cudaStream_t st);
+// out[t] = bf16(sum_j w[t,j] y[pos[t top_k + j]]).
+cudaError_t launch_mx_combine(const float* y, const int32_t* pos, const float* w, int T, int top_k,
+                              int H, uint16_t* out, bool after_prev, cudaStream_t st);
 
 // Products of 4-bit matrices (mxfp4_gemm.cu). The experts' segments begin at
 // multiples of kMxBlockM rows (capacity rows in all) and make at most
 // max_chunks chunks of kMxBlockM rows. ids [T, top_k]: the routing; with at most
 // kMxEarlyIds slots it is read in place of counts, and before the kernels that
-// precede the launch on its stream have completed (they must not write it).
+// precede the launch on its stream have completed (they must not write it). y
+// holds the segments' rows without their padding: at most T top_k.
 cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                            const uint8_t* b_scales, int M, int N, int K, void* c, bool out_fp32,
                            int num_sms, unsigned* err, cudaStream_t st);
@@ -304,6 +303,6 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
                                    const uint8_t* w_scales, const int32_t* counts,
                                    const int32_t* ids, int T, int top_k, int E, int H, int I, long long capacity, long long max_chunks,
-                                   uint16_t* y, uint8_t* y_scale, int num_sms, unsigned* err, bool after_prev, cudaStream_t st);
+                                   float* y, int num_sms, unsigned* err, bool after_prev, cudaStream_t st);
 
 }  // namespace mm

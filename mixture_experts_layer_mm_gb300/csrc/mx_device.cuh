@@ -55,23 +55,6 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
                  : s == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
 }
 
-// Expert outputs between the down product and the weighted sum: fp16 under one
-// power of two for each 32 columns, so that the sum reads and the product
-// writes half of fp32's bytes (268 MB each way at 4096 tokens x 8 slots x 2048).
-// The block's largest magnitude lands in [2^14, 2^15), so every value down to
-// 2^-28 of it keeps 11 bits: a rounding of at most 2^-11 per slot, under the
-// 2^-8 of the bf16 output (bf16 here would double that output's rounding error).
-// The byte is the biased exponent of the largest magnitude, kept in [15, 254]
-// so that both factors, 2^(141 - byte) and its inverse, are normal floats;
-// infinity and NaN pass through fp16. A row's bytes are in groups of 8, one for
-// each 256 columns (a tile of the product), block b of the row at place
-// mx_y_place(b): a thread of the product has blocks b and b + 4 of a row.
-__host__ __device__ constexpr long long mx_y_row_bytes(long long h) { return (h + 255) / 256 * 8; }
-__device__ __forceinline__ int mx_y_place(int b) { return (b & ~7) + 2 * (b & 3) + ((b >> 2) & 1); }
-__device__ __forceinline__ float mx_y_unit(uint32_t byte) {  // 2^(byte - 141)
-  return __uint_as_float((byte - 14u) << 23);
-}
-
 // Eight floats to e2m1 (nearest, ties to even, beyond 6 to 6), v[0] in the
 // lowest nibble. A NaN only reaches this under the factor 0 of a NaN block
 // and becomes whatever finite code the conversion gives it.
@@ -125,6 +108,18 @@ __device__ __forceinline__ Pair swiglu(Pair g, Pair u) {
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+}
+
+// Sum of v over the lanes below this one.
+__device__ __forceinline__ int exclusive_sum(int v) {
+  const int lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  return incl - v;
 }
 
 // ------------------------------------------------- warp-uniform control ---

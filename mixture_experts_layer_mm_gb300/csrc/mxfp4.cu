@@ -336,37 +336,40 @@ struct MxPlaceArgs {
   const unsigned char* hidden;
   const int32_t* ids;
   int32_t* counts;   // [E]
-  int32_t* cursor;   // [E * kMxCursorStep] next free row (large batches)
-  int32_t* pos;      // [T * top_k] row of a slot, -1 if dropped
+  // [E * kMxCursorStep] (large batches) an expert's next free row, and what leads
+  // from its rows to those without the segments' padding
+  int32_t* cursor;
+  int32_t* pos;      // [T * top_k] row of a slot without the padding, -1 if dropped
   uint8_t* codes;
   uint8_t* scales;
   unsigned* err;
   int T, E, top_k, H;
 };
 
-// First rows of the segments from the counts, by one warp (lane l the experts
-// from 8 l on).
-__device__ __forceinline__ void scan_segments(const int* cnt, int E, int* off) {
+// First rows of the segments from the counts, and what leads from a segment's
+// rows to those without padding, by one warp (lane l the experts from 8 l on).
+__device__ __forceinline__ void scan_segments(const int* cnt, int E, int* off, int* lead) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = kMaxExperts / 32;
-  int v[kPer], sum = 0;
+  int c[kPer], rows = 0, padded = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane * kPer + i;
-    v[i] = e < E ? (cnt[e] + kMxBlockM - 1) / kMxBlockM * kMxBlockM : 0;
-    sum += v[i];
+    c[i] = e < E ? cnt[e] : 0;
+    rows += c[i];
+    padded += (c[i] + kMxBlockM - 1) / kMxBlockM * kMxBlockM;
   }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(kAll, incl, o);
-    if (lane >= o) incl += u;
-  }
-  int run = incl - sum;
+  rows = exclusive_sum(rows);
+  padded = exclusive_sum(padded);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (lane * kPer + i < E) off[lane * kPer + i] = run;
-    run += v[i];
+    const int e = lane * kPer + i;
+    if (e < E) {
+      off[e] = padded;
+      lead[e] = rows - padded;
+    }
+    rows += c[i];
+    padded += (c[i] + kMxBlockM - 1) / kMxBlockM * kMxBlockM;
   }
 }
 
@@ -377,7 +380,7 @@ constexpr int kPlaceWarps = 4;
 
 __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const MxPlaceArgs a) {
   __shared__ int ids_s[kMxEarlyIds];
-  __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts];
+  __shared__ int tot[kMaxExperts], before[kMaxExperts], off[kMaxExperts], lead[kMaxExperts];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kNT = kPlaceWarps * 32;
   const int t = blockIdx.x, k = a.top_k, n = a.T * k;
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
   }
   if (bad && t == 0) atomicOr(a.err, kDevErrBadIds);
   __syncthreads();
-  if (warp == 0) scan_segments(tot, a.E, off);
+  if (warp == 0) scan_segments(tot, a.E, off, lead);
   __syncthreads();
   int place = -1;
   if (lane < k) {
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) mx_place_small_kernel(const 
     bool drop = id < 0 || id >= a.E;
     for (int j = 0; j < lane && !drop; ++j) drop = ids_s[t * k + j] == id;
     if (!drop) place = off[id] + before[id];
-    if (warp == 0) a.pos[t * k + lane] = place;
+    if (warp == 0) a.pos[t * k + lane] = drop ? -1 : place + lead[id];
   }
   const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
   for (; c - lane * 16 < hp; c += kNT * 16) {
@@ -430,7 +433,7 @@ constexpr int kGroupBlocks = 8;
 
 __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThreads, 1)
     mx_group_kernel(const MxPlaceArgs a) {
-  __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts];
+  __shared__ int tot[kMaxExperts], sum[kMaxExperts], off[kMaxExperts], lead[kMaxExperts];
   const int tid = threadIdx.x;
   const uint32_t k = a.top_k;
   pdl_wait();
@@ -468,11 +471,12 @@ __global__ void __cluster_dims__(kGroupBlocks, 1, 1) __launch_bounds__(kGroupThr
       sum[e] = v;
     }
     __syncthreads();
-    if (tid < 32) scan_segments(sum, a.E, off);
+    if (tid < 32) scan_segments(sum, a.E, off, lead);
     __syncthreads();
     for (int e = tid; e < a.E; e += kGroupThreads) {
       a.counts[e] = sum[e];
       a.cursor[e * kMxCursorStep] = off[e];
+      a.cursor[e * kMxCursorStep + 1] = lead[e];
     }
   }
   cluster_barrier();  // no block ends while its counts are being read
@@ -506,11 +510,16 @@ __global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs 
   pdl_trigger();
   if (t >= a.T) return;
   const uint32_t same = __match_any_sync(kAll, place);
-  if (place < 0 || place >= a.E || (same & ((1u << lane) - 1u)) != 0)
+  int pos = -1;
+  if (place < 0 || place >= a.E || (same & ((1u << lane) - 1u)) != 0) {
     place = -1;
-  else
-    place = atomicAdd(a.cursor + place * kMxCursorStep, 1);
-  if (lane < k) a.pos[(size_t)t * k + lane] = place;
+  } else {
+    int32_t* cursor = a.cursor + place * kMxCursorStep;
+    pos = __ldcg(cursor + 1);
+    place = atomicAdd(cursor, 1);
+    pos += place;
+  }
+  if (lane < k) a.pos[(size_t)t * k + lane] = pos;
   const size_t scale_at = place >= 0 ? mx_scale_offset(place, 0, (int)mx_tiles(a.H)) : 0;
   for (int c0 = lane * 16; c0 - lane * 16 < hp; c0 += U * kSpan) {
     if (c0 != lane * 16) load(c0);
@@ -518,29 +527,23 @@ __global__ void __launch_bounds__(kMxThreads) mx_place_kernel(const MxPlaceArgs 
   }
 }
 
-// out[t] = bf16(sum_j w[t,j] y[pos[t k + j]]) in slot order, 8 V columns a
-// thread; dropped slots (pos < 0) have no row in y and add nothing. y is fp16
-// under a power of two for each 32 columns (mx_y_unit). J slots at a time: their
-// rows first, then all their loads, then the sum.
-template <int V, int J>
+// out[t] = bf16(sum_j w[t,j] y[pos[t k + j]]) in slot order, 8 columns a thread;
+// dropped slots (pos < 0) have no row in y and add nothing. y is fp32: its values
+// are terms of a sum that may cancel, and one column says nothing of another's
+// range. J slots at a time: their rows first, then all their loads, then the sum.
+template <int J>
 __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
-    const unsigned char* __restrict__ y, const uint8_t* __restrict__ y_scale,
-    const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int top_k, int hv,
-    uint4* __restrict__ out) {
-  static_assert(V == 1 || V == 2, "16 or 32 bytes");
-  const int row_bytes = (int)mx_y_row_bytes(8LL * V * hv);
+    const float* __restrict__ y, const int32_t* __restrict__ pos, const float* __restrict__ w, int T,
+    int top_k, int h8, uint4* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
   const long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x;
-  if (i >= (long long)T * hv) return;
-  const int t = (int)(i / hv), h = (int)(i - (long long)t * hv);
+  if (i >= (long long)T * h8) return;
+  const int t = (int)(i / h8), h = (int)(i - (long long)t * h8);
   const size_t f0 = (size_t)t * top_k;
-  const int place = mx_y_place(h * V / 4);
-  float s[V][8];
+  float s[8];
 #pragma unroll
-  for (int u = 0; u < V; ++u)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s[u][q] = 0.f;
+  for (int q = 0; q < 8; ++q) s[q] = 0.f;
   for (int j0 = 0; j0 < top_k; j0 += J) {
     int r[J];
     float wj[J];
@@ -550,42 +553,25 @@ __global__ void __launch_bounds__(kMxThreads) mx_combine_kernel(
       r[j] = in ? __ldg(pos + f0 + j0 + j) : -1;
       wj[j] = in ? __ldg(w + f0 + j0 + j) : 0.f;
     }
-    uint4 v[J][V];
-    uint32_t byte[J];
+    uint4 v[J][2];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-#pragma unroll
-      for (int u = 0; u < V; ++u) v[j][u] = make_uint4(0u, 0u, 0u, 0u);
-      byte[j] = 15u;
-      if (r[j] >= 0) {
-        const unsigned char* at = y + ((size_t)r[j] * hv + h) * (16 * V);
-        if constexpr (V == 1)
-          v[j][0] = __ldg(reinterpret_cast<const uint4*>(at));
-        else
-          load32(at, v[j][0], v[j][V - 1]);
-        byte[j] = __ldg(y_scale + (size_t)r[j] * row_bytes + place);
-      }
+      v[j][0] = v[j][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r[j] >= 0)
+        load32(reinterpret_cast<const unsigned char*>(y + ((size_t)r[j] * h8 + h) * 8), v[j][0],
+               v[j][1]);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (r[j] < 0) continue;  // a NaN or infinite weight of a dropped slot stays out
-      const float unit = mx_y_unit(byte[j]);
+      const uint32_t p[8] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w,
+                             v[j][1].x, v[j][1].y, v[j][1].z, v[j][1].w};
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const uint32_t p[4] = {v[j][u].x, v[j][u].y, v[j][u].z, v[j][u].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[q]));
-          s[u][2 * q] += wj[j] * (f.x * unit);
-          s[u][2 * q + 1] += wj[j] * (f.y * unit);
-        }
-      }
+      for (int q = 0; q < 8; ++q) s[q] += wj[j] * __uint_as_float(p[q]);
     }
   }
-#pragma unroll
-  for (int u = 0; u < V; ++u)
-    out[i * V + u] = make_uint4(pack_bf16x2(s[u][0], s[u][1]), pack_bf16x2(s[u][2], s[u][3]),
-                                pack_bf16x2(s[u][4], s[u][5]), pack_bf16x2(s[u][6], s[u][7]));
+  out[i] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+                      pack_bf16x2(s[6], s[7]));
 }
 
 }  // namespace
@@ -652,22 +638,13 @@ cudaError_t launch_mx_place(const uint16_t* hidden, const int32_t* ids, int T, i
                   true, a);
 }
 
-cudaError_t launch_mx_combine(const uint16_t* y, const uint8_t* y_scale, const int32_t* pos,
-                              const float* w, int T, int top_k, int H, uint16_t* out, int num_sms,
-                              bool after_prev, cudaStream_t st) {
-  const unsigned char* yb = reinterpret_cast<const unsigned char*>(y);
-  uint4* o = reinterpret_cast<uint4*>(out);
-  // 32 bytes a load and two slots at a time, which leaves many threads, are the
-  // better use of the memory (4096 tokens of 2048 values, 8 slots: 6.5 us less
-  // than 16 bytes and eight slots; four slots 2 us more, eight 6 us more); 16
-  // bytes give a small batch twice the threads (64 tokens: 0.6 us less).
-  const long long wide = ((long long)T * (H / 16) + kMxThreads - 1) / kMxThreads;
-  if (wide >= 4LL * num_sms)
-    return launch_k(mx_combine_kernel<2, 2>, dim3((unsigned)wide), dim3(kMxThreads), 0, st,
-                    after_prev, yb, y_scale, pos, w, T, top_k, H / 16, o);
+cudaError_t launch_mx_combine(const float* y, const int32_t* pos, const float* w, int T, int top_k,
+                              int H, uint16_t* out, bool after_prev, cudaStream_t st) {
+  // Eight slots' loads at once (all of a call at T = 1 / 64 / 4096: 15.3 / 60.1 /
+  // 201 us; four at once 15.9 / 62.7 / 204, two 16.2 / 61.9 / 204).
   const long long blocks = ((long long)T * (H / 8) + kMxThreads - 1) / kMxThreads;
-  return launch_k(mx_combine_kernel<1, 8>, dim3((unsigned)blocks), dim3(kMxThreads), 0, st,
-                  after_prev, yb, y_scale, pos, w, T, top_k, H / 8, o);
+  return launch_k(mx_combine_kernel<8>, dim3((unsigned)blocks), dim3(kMxThreads), 0, st, after_prev,
+                  y, pos, w, T, top_k, H / 8, reinterpret_cast<uint4*>(out));
 }
 
 }  // namespace mm

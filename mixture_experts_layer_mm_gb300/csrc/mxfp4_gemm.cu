@@ -5,7 +5,7 @@
 //   dense    C[r, n] = x_r . w_n                       (bf16 or fp32)
 //   gate_up  act[r, i] = Q(silu(g) u), g = x_r . w_i (gate), u = x_r . w_i (up)
 //            for the rows r of every expert's segment; Q: 4-bit blocks along i
-//   down     y[r, h] = x_r . w_h (fp16 under a power of two for each 32 h)
+//   down     y[r, h] = x_r . w_h (fp32)
 //
 // Orientation as in gemm.cu: the weight rows are the MMA's M side (128 rows
 // an MMA), the token rows its N side (any multiple of 16 up to 128). A tile
@@ -17,7 +17,7 @@
 // The products of two e2m1 values and two powers of two are exact; the
 // accumulation is in fp32 in tensor memory.
 //
-// gate_up's blocks (and those of y) run along the output columns, which are the
+// gate_up's blocks run along the output columns, which are the
 // lanes of tensor memory. The weight tile's rows are loaded in an order (row 4 a
 // + j of a group of 32 at place 8 j + a) that gives a thread of a 16 x 256-bit
 // tensor-memory load four consecutive columns of a token row: a block's maximum
@@ -38,8 +38,6 @@
 #include "mm.h"
 #include "mm_internal.h"
 #include "mx_device.cuh"
-
-#include <cuda_fp16.h>
 
 namespace mm {
 namespace {
@@ -90,7 +88,7 @@ struct MxGemmArgs {
   const uint8_t* w_scales;
   const uint8_t* x_scales;
   void* out;               // dense: C; gate_up: act codes; down: y
-  uint8_t* act_scales;     // gate_up: scales of act; down: block exponents of y
+  uint8_t* act_scales;     // gate_up: scales of act
   unsigned* err;
   int E, rows;    // rows: of the one segment of a dense product (else 0)
   int N, K;       // output columns (gate_up: intermediates), reduction
@@ -114,17 +112,20 @@ struct Tile {
 
 // Exclusive sums of the segments' chunks, by one warp: lane l takes the experts
 // from 8 l on (at most 256 in all). first[E] is the total; each count is
-// replaced by the row behind the segment's last.
-__device__ __forceinline__ void scan_chunks(int* cnt, int E, int* first) {
+// replaced by the row behind the segment's last. lead (or NULL): what leads from
+// a segment's rows to its rows of y, which lie without gaps between segments.
+__device__ __forceinline__ void scan_chunks(int* cnt, int E, int* first, int* lead) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = kMaxExperts / 32;
-  int c[kPer], sum = 0;
+  int c[kPer], sum = 0, rows = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane * kPer + i;
     c[i] = e < E ? (cnt[e] + kBN - 1) / kBN : 0;
     sum += c[i];
+    rows += e < E ? cnt[e] : 0;
   }
+  if (lead != nullptr) rows = exclusive_sum(rows);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -134,9 +135,14 @@ __device__ __forceinline__ void scan_chunks(int* cnt, int E, int* first) {
   int run = incl - sum;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (lane * kPer + i < E) {
-      first[lane * kPer + i] = run;
-      cnt[lane * kPer + i] += run * kBN;
+    const int e = lane * kPer + i;
+    if (e < E) {
+      if (lead != nullptr) {
+        lead[e] = rows - run * kBN;
+        rows += cnt[e];
+      }
+      first[e] = run;
+      cnt[e] += run * kBN;
     }
     run += c[i];
   }
@@ -270,13 +276,6 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t e, uint32_t& f) {
   return s;
 }
 
-// The bytes of y (see mx_y_unit) of two exponents, and f with 2^(141 - byte) = 2^(f - 127).
-__device__ __forceinline__ uint32_t y_pair(uint32_t e, uint32_t& f) {
-  const uint32_t b = __vminu2(__vmaxu2(e, 0x000F000Fu), 0x00FE00FEu);
-  f = 0x010C010Cu - b;
-  return b;
-}
-
 // 2^(f - 127) of the two halves of a word, 0 for f = 0.
 __device__ __forceinline__ Pair factors(uint32_t f) {
   return {__uint_as_float(f << 23), __uint_as_float((f << 7) & 0xFF800000u)};
@@ -308,12 +307,6 @@ __device__ __forceinline__ void issue_stage(uint32_t st, int a_tile, uint32_t ts
   }
 }
 
-// Four floats to fp16.
-__device__ __forceinline__ uint2 half4(float a, float b, float c, float d) {
-  const __half2 lo = __floats2half2_rn(a, b), hi = __floats2half2_rn(c, d);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
 // NA: weight tiles of 128 rows a tile (1: dense only).
 template <int MODE, bool PERM, int NA>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -329,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_s;
   __shared__ int stop_s;
   __shared__ int cnt_s[kMaxExperts], first_s[kMaxExperts + 1];
+  __shared__ int lead_s[MODE == kDown ? kMaxExperts : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = a.E;
@@ -377,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_trigger();
   __syncthreads();
-  if (warp == 0) scan_chunks(cnt_s, E, first_s);  // cnt_s: now the segments' ends
+  // cnt_s: from here on the segments' ends
+  if (warp == 0) scan_chunks(cnt_s, E, first_s, MODE == kDown ? lead_s : nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -653,67 +648,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const int n = t.m * (NA * 128) + q * 32;  // and n + 128 from the second accumulator
           const bool in0 = n < a.N, in1 = NA == 2 && n + 128 < a.N;
-          if (MODE == kDown) {
-            uint32_t w0[4], w1[4], f;
-            local_max(p0, w0);
-            local_max(p1, w1);
-            // Lanes with bit 2 keep the second accumulator's words.
-            const uint32_t k0 = fold(fold(w0[0], w0[2], 16), fold(w0[1], w0[3], 16), 8);
-            const uint32_t k1 = fold(fold(w1[0], w1[2], 16), fold(w1[1], w1[3], 16), 8);
-            const uint32_t b = y_pair(exponents(fold(k0, k1, 4)), f);
-            // Both bytes of row `own`: c = 0 for the lanes without bit 2, 1 for the others.
-            const uint32_t other = __shfl_xor_sync(kAll, b, 4);
-            const uint32_t two = lane & 4 ? __byte_perm(other, b, 0x0062) : __byte_perm(b, other, 0x0040);
-            if (own < ncol)
-              *reinterpret_cast<uint16_t*>(a.act_scales +
-                                           (size_t)(t.row0 + c0 + own) * mx_y_row_bytes(a.N) +
-                                           t.m * 8 + q * 2) = (uint16_t)two;
-            __half* y = static_cast<__half*>(a.out) + row0 * a.N + n + col4;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const Pair inv = factors(__shfl_sync(kAll, f, 8 * g + (half ? from | 4 : from & 3)));
-                Pair x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = (half ? p1 : p0).rows(j, g) * inv;
-                __half* to = y + (8 * g) * (size_t)a.N + 128 * half;
-                const bool in = half ? in1 : in0;
-                if (in && 8 * g < left)
-                  *reinterpret_cast<uint2*>(to) = half4(x[0].x, x[1].x, x[2].x, x[3].x);
-                if (in && 8 * g + 1 < left)
-                  *reinterpret_cast<uint2*>(to + a.N) = half4(x[0].y, x[1].y, x[2].y, x[3].y);
-              }
-            }
-          } else {
-            if (NA == 1 && nk > 1) {
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p0.set(j, g, p0.rows(j, g) + p1.rows(j, g));
-            }
-            const size_t at = (size_t)row0 * a.N + n + col4;
+          if (NA == 1 && nk > 1) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                if (8 * g + c >= left) continue;
-                const size_t to = at + (8 * g + c) * (size_t)a.N;
-                if (a.out_fp32) {
-                  float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + to);
-                  if (in0) d[0] = make_float4(p0.at(0, g, c), p0.at(1, g, c), p0.at(2, g, c), p0.at(3, g, c));
-                  if (in1) d[32] = make_float4(p1.at(0, g, c), p1.at(1, g, c), p1.at(2, g, c), p1.at(3, g, c));
-                } else {
-                  uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to);
-                  if (in0)
-                    d[0] = make_uint2(bf16x2(p0.at(0, g, c), p0.at(1, g, c)),
-                                      bf16x2(p0.at(2, g, c), p0.at(3, g, c)));
-                  if (in1)
-                    d[32] = make_uint2(bf16x2(p1.at(0, g, c), p1.at(1, g, c)),
-                                       bf16x2(p1.at(2, g, c), p1.at(3, g, c)));
-                }
-              }
+              for (int j = 0; j < 4; ++j) p0.set(j, g, p0.rows(j, g) + p1.rows(j, g));
           }
+          const long long lead = MODE == kDown ? lead_s[t.e] : 0;
+          const size_t at = (size_t)(row0 + lead) * a.N + n + col4;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (8 * g + c >= left) continue;
+              const size_t to = at + (8 * g + c) * (size_t)a.N;
+              if (MODE == kDown || a.out_fp32) {
+                float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + to);
+                if (in0) d[0] = make_float4(p0.at(0, g, c), p0.at(1, g, c), p0.at(2, g, c), p0.at(3, g, c));
+                if (in1) d[32] = make_float4(p1.at(0, g, c), p1.at(1, g, c), p1.at(2, g, c), p1.at(3, g, c));
+              } else {
+                uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to);
+                if (in0)
+                  d[0] = make_uint2(bf16x2(p0.at(0, g, c), p0.at(1, g, c)),
+                                    bf16x2(p0.at(2, g, c), p0.at(3, g, c)));
+                if (in1)
+                  d[32] = make_uint2(bf16x2(p1.at(0, g, c), p1.at(1, g, c)),
+                                     bf16x2(p1.at(2, g, c), p1.at(3, g, c)));
+              }
+            }
         }
       } else {
         // Any N: lane = output column, one value of 32 token rows a lane.
@@ -861,7 +823,7 @@ cudaError_t launch_mx_experts_gate_up(const uint8_t* xs, const uint8_t* xs_scale
 cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales, const uint8_t* w,
                                    const uint8_t* w_scales, const int32_t* counts,
                                    const int32_t* ids, int T, int top_k, int E, int H, int I, long long capacity, long long max_chunks,
-                                   uint16_t* y, uint8_t* y_scale, int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
+                                   float* y, int num_sms, unsigned* err, bool after_prev, cudaStream_t st) {
   MxGemmArgs a = {};
   a.counts = counts;
   if (T * top_k <= kMxEarlyIds) {
@@ -872,7 +834,6 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
   a.w_scales = w_scales;
   a.x_scales = act_scales;
   a.out = y;
-  a.act_scales = y_scale;
   a.err = err;
   a.E = E;
   a.N = H;

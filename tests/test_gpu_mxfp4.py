@@ -617,3 +617,68 @@ def test_experts_of_many_slots_a_token(k):
     want = _call(d)
     assert mm.mm_poll_device_status() == (mm.MM_OK if k == 1 else mm.MM_ERR_DEVICE)
     assert torch.equal(got, want)
+
+
+def _scale_at(tiles, row, block):
+    """The scale byte of (row, block) in every matrix of stored tiles [E, ...], as a view."""
+    return tiles[:, row // 128, block // 4, row % 32 * 16 + row % 128 // 32 * 4 + block % 4]
+
+
+@pytest.mark.parametrize("T", [9, 700])
+def test_experts_keep_an_output_column_to_itself(T):
+    # A column of the result takes its row of w_down alone, whatever the rows
+    # beside it hold: NaN, products beyond fp32, values 2^60 times larger.
+    H, E, I, k, h = 320, 8, 64, 4, 170
+    d = _experts_case(82, T, H, E, I, k)
+    clean = _call(d)
+    others = torch.arange(H, device="cuda") != h
+    for byte in (255, 254):
+        s = d["sdn"].clone()
+        _scale_at(s, h, 1)[2] = byte  # the columns 32 to 63 of w_down[2, h]
+        out = _call(dict(d, sdn=s))
+        assert torch.equal(out[:, others], clean[:, others])
+        hit = (d["ids"] == 2).any(1)
+        assert torch.equal(out[~hit, h], clean[~hit, h])
+        bad = torch.isnan(out[hit, h]) if byte == 255 else ~torch.isfinite(out[hit, h])
+        assert bad.all() if byte == 255 else bad.any()
+    s = d["sdn"].clone()
+    for block in range(I // 32):
+        _scale_at(s, h, block)[:] += 60
+    out = _call(dict(d, sdn=s))
+    _status_ok()
+    assert torch.equal(out[:, others], clean[:, others])
+    assert torch.equal(out[:, h].float(), clean[:, h].float() * 2.0 ** 60)
+
+
+@pytest.mark.parametrize("T", [3, 1100])
+def test_experts_sum_their_slots_in_32_bits(T):
+    # Two experts that differ in one intermediate of w_down, under weights 1 and
+    # -1: the slots cancel but for that one, so that what each lost shows.
+    H, I, i0 = 192, 128, 37
+    d = _experts_case(83, T, H, 2, I, 2, ids=np.tile([[0, 1]], (T, 1)))
+    d["gu"][2:], d["sgu"][2:] = d["gu"][:2].clone(), d["sgu"][:2].clone()
+    d["dn"][1], d["sdn"][1] = d["dn"][0].clone(), d["sdn"][0].clone()
+    d["dn"][1, :, i0 // 2] &= 0x0F  # the odd column's code
+    d["w"][:, 0], d["w"][:, 1] = 1.0, -1.0
+    out = _np64(_call(d))
+    _status_ok()
+    x = ref.quantised(_np64(d["hidden"]))
+    gu = _np64(mm.mm_mxfp4_dequantize(d["gu"], d["sgu"], torch.float32))
+    dn = _np64(mm.mm_mxfp4_dequantize(d["dn"], d["sdn"], torch.float32))
+    assert not dn[1][:, i0].any() and np.array_equal(np.delete(dn[0], i0, 1), np.delete(dn[1], i0, 1))
+    g, u = x @ gu[0].T, x @ gu[1].T
+    silu = g / (1 + np.exp(-g))
+    # As in _experts_ref; the sums of gate and up are within H steps.
+    eg = H * 2.0 ** -23 * (np.abs(x) @ np.abs(gu[0]).T)
+    eu = H * 2.0 ** -23 * (np.abs(x) @ np.abs(gu[1]).T)
+    err = (1.1 * eg + np.abs(silu) * (8 + 2 * np.abs(g)) * 2.0 ** -23) * (np.abs(u) + eu) \
+        + np.abs(silu) * eu
+    q, da = ref.quantised(silu * u), ref.slack(silu * u, err)
+    want = np.outer(q[:, i0], dn[0][:, i0]).reshape(T, H)
+    # Both slots hold the same activation. Each sum is within I steps of its
+    # magnitudes, the two additions of the slots within one each (of a value
+    # below these magnitudes, 2^-24), then one rounding to bf16.
+    mag = (np.abs(q) + da) @ np.abs(dn[0]).T
+    tol = np.outer(da[:, i0], np.abs(dn[0][:, i0])) + (2 * I * 2.0 ** -23 + 2 * 2.0 ** -24) * mag
+    tol = tol + (np.abs(want) + tol) * 2.0 ** -8
+    assert (np.abs(out - want) <= tol).all(), (np.abs(out - want) / tol).max()
