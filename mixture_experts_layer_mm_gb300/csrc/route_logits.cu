@@ -269,8 +269,8 @@ __device__ __forceinline__ void sort_desc(float (&v)[Q]) {
 // lane Q + q. Every lane sorts its values; then the warp takes the largest
 // head, drops it from every lane that shows it, and so on until top_k values
 // are gone: that head is the top_k-th largest value, and what is at or above
-// it is the selection. Only when more values equal it than have room (or it
-// is -inf, which NaN and the lanes past E rank as) do the ids decide: the
+// it is the selection. Only when more values equal it than have room, or it is
+// -inf, which NaN and the places past E rank as, do the ids below E decide: the
 // lowest stay. m: the largest value.
 template <int Q>
 __device__ __forceinline__ uint32_t select_topk(const float (&l)[Q], int E, int top_k, float& m) {
@@ -298,7 +298,7 @@ __device__ __forceinline__ uint32_t select_topk(const float (&l)[Q], int E, int 
   for (int q = 0; q < Q; ++q)
     if (l[q] >= top) sel |= 1u << q;
   const uint32_t total = __reduce_add_sync(kFullMask, (uint32_t)__popc(sel));
-  if (total != (uint32_t)top_k) {
+  if (total != (uint32_t)top_k || top == -INFINITY) {
     uint32_t above = 0, equal = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {

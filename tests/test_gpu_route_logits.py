@@ -435,3 +435,60 @@ def test_batches_around_one_block_and_one_cluster(T, E, k):
         assert all(torch.equal(a, b) for a, b in
                    zip(got, mm.mm_route_logits(x, k, True, token_mask=mask)))
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+def _nan_rows(rng, T, E, k):
+    """Rows with 0 to E logits that are NaN, others -inf, and seldom k above it."""
+    x = np.where(rng.random((T, E)) < rng.random((T, 1)), -np.inf, rng.standard_normal((T, E)))
+    few = rng.random((T, 1)) < 0.7  # at most k - 1 above -inf
+    rank = np.argsort(np.argsort(rng.random((T, E)), axis=1), axis=1)
+    x = np.where(few & (rank >= rng.integers(0, k, (T, 1))), -np.inf, x)
+    places = 32 if E <= 32 else 64 if E <= 64 else 128 if E <= 128 else 256
+    count = rng.integers(0, E + 1, T)
+    count[::3] = E                                   # all of them
+    count[1::3] = np.clip(places - k, 0, E)          # as many as leave k places without
+    count[::5] = 0
+    order = np.argsort(rng.random((T, E)) - (x > -np.inf), axis=1)[:, ::-1]  # -inf first
+    put = np.argsort(order, axis=1) < count[:, None]
+    return np.where(put, np.nan, x)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T", [24, 200, 1500])  # one block, one cluster, many blocks
+@pytest.mark.parametrize("E,k", [(60, 4), (24, 8), (30, 2), (31, 1), (63, 1), (120, 8), (127, 1),
+                                 (248, 8), (255, 1), (250, 6), (32, 32), (30, 30), (40, 4),
+                                 (128, 8), (256, 1), (1, 1)])
+def test_rows_with_nan_select_experts_that_exist(E, k, T, masked):
+    # NaN ranks as -inf, equal values by id, and a place past the experts never.
+    rng = np.random.default_rng(E * 1000 + T + k)
+    x64 = _nan_rows(rng, T, E, k)
+    x = torch.from_numpy(x64.astype(np.float32)).cuda()
+    x64 = _np64(x)
+    rank = np.where(np.isnan(x64), -np.inf, x64)
+    want = np.sort(np.argsort(-rank, axis=1, kind="stable")[:, :k], axis=1)
+    mask = torch.from_numpy(rng.random(T) < 0.5).cuda() if masked else None
+    ids, w, counts, sums, loss = mm.mm_route_logits(x, k, True, token_mask=mask)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    counted = ~np.isneginf(x64).all(1)
+    if masked:
+        counted &= mask.cpu().numpy()
+    assert np.array_equal(counts.cpu().numpy(), np.bincount(want[counted].ravel(), minlength=E))
+    assert int(counts.sum()) == counted.sum() * k
+    bad = counted & np.isnan(x64).any(1)
+    assert torch.isnan(w[torch.from_numpy(bad).cuda()]).all()
+    assert not w[torch.from_numpy(~counted).cuda()].any()
+    assert torch.isnan(sums).all() == bad.any() and torch.isnan(loss).all() == bad.any()
+    # The gradient of the rows that hold no NaN takes n from the counts.
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    g = _np64(mm.mm_route_logits_backward(x, ids, counts, True, dw, torch.ones(1, device="cuda"),
+                                          mask))
+    fine = counted & ~bad
+    if fine.any():
+        exact = ref.route_grad(x64[fine], k, True, _np64(dw)[fine], 1.0, ids=want[fine],
+                               counts=counts.cpu().numpy())
+        n = max(int(counted.sum()), 1)
+        # terms of at most max |dw| and E k / (n k) n / n ..., each within 300 half steps
+        size = np.abs(_np64(dw)).max() + E * counts.cpu().numpy().max() / (n * n * k)
+        assert np.abs(g[fine] - exact).max() <= 300 * U * size
+    assert not g[~counted].any()
+    assert mm.mm_poll_device_status() == mm.MM_OK
