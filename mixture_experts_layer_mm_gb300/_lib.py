@@ -531,28 +531,46 @@ def _device(name: str, *tensors) -> int:
     return di
 
 
-def _launch(fn, name: str, di: int, stream, made, *args) -> None:
-    """fn(*args, stream handle) on device di, on `stream` or that device's
-    current stream. `made`: tensors allocated for this call; with a stream of
-    the caller's, the allocator keeps them until that stream is done."""
-    if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(di)
-    else:
-        s = (stream if isinstance(stream, torch.cuda.Stream)
-             else torch.cuda.ExternalStream(int(stream), device=di))
-        if s.device_index != di:
-            raise ValueError(f"{name}: the stream is on another device than the tensors")
-        for t in made:
-            if t is not None and t.numel():
-                t.record_stream(s)
-        st = s.cuda_stream
-    if torch._C._cuda_getDevice() == di:
-        rc = fn(*args, st)
-    else:
-        with torch.cuda.device(di):
+class _On:
+    """Where a call runs: device `di` and `stream` (the caller's, else the
+    device's current one). Results and workspaces come from that stream's
+    memory: a block of another stream's may still be in use there by work that
+    this one does not wait for."""
+
+    def __init__(self, name: str, di: int, stream):
+        self.name, self.di, self.stream, self.made = name, di, None, []
+        if stream is not None:
+            s = (stream if isinstance(stream, torch.cuda.Stream)
+                 else torch.cuda.ExternalStream(int(stream), device=di))
+            if s.device_index != di:
+                raise ValueError(f"{name}: the stream is on another device than the tensors")
+            if s.cuda_stream != torch._C._cuda_getCurrentRawStream(di):
+                self.stream = s
+
+    def empty(self, shape, dtype, result: bool = True) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.di))
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.di))
+        if result:
+            self.made.append(t)
+        return t
+
+    def launch(self, fn, *args) -> None:
+        """fn(*args, stream handle)."""
+        st = (torch._C._cuda_getCurrentRawStream(self.di) if self.stream is None
+              else self.stream.cuda_stream)
+        if torch._C._cuda_getDevice() == self.di:
             rc = fn(*args, st)
-    if rc != MM_OK:
-        raise MMError(rc, name)
+        else:
+            with torch.cuda.device(self.di):
+                rc = fn(*args, st)
+        if rc != MM_OK:
+            raise MMError(rc, self.name)
+        # The results are read on the caller's stream, once that waits for this one.
+        for t in self.made:
+            if t.numel():
+                t.record_stream(torch.cuda.current_stream(self.di))
 
 
 def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=None):
@@ -567,22 +585,21 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
             return r
     dt = _dtype(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
     x = _ptr(logits, logits.dtype, "logits")
     mask = _mask_ptr(token_mask, T)
     di = _device("mm_route_logits", logits, token_mask)
     l = lib()
     need = l.mm_route_logits_workspace_size(T, E)
-    ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=dev)
-    w = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    sums = torch.empty(E, dtype=torch.float32, device=dev)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    _launch(l.mm_route_logits, "mm_route_logits", di, stream, (ids, w, counts, sums, loss, ws),
-            x, dt, mask, T, E, top_k, 1 if renorm else 0, ids.data_ptr(), w.data_ptr(),
-            counts.data_ptr(), sums.data_ptr(), loss.data_ptr(),
-            None if ws is None else ws.data_ptr(), need if need > 0 else 0)
+    on = _On("mm_route_logits", di, stream)
+    ids = on.empty((T, max(top_k, 0)), torch.int32)
+    w = on.empty((T, max(top_k, 0)), torch.float32)
+    counts = on.empty(E, torch.int32)
+    sums = on.empty(E, torch.float32)
+    loss = on.empty(1, torch.float32)
+    ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
+    on.launch(l.mm_route_logits, x, dt, mask, T, E, top_k, 1 if renorm else 0, ids.data_ptr(),
+              w.data_ptr(), counts.data_ptr(), sums.data_ptr(), loss.data_ptr(),
+              None if ws is None else ws.data_ptr(), need if need > 0 else 0)
     return ids, w, counts, sums, loss
 
 
@@ -610,9 +627,10 @@ def mm_route_logits_backward(logits, topk_ids, expert_counts, renorm: bool, d_to
     dw, dl = _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(d_loss, torch.float32, "d_loss")
     di = _device("mm_route_logits_backward", logits, token_mask, topk_ids, expert_counts, d_topk_w,
                  d_loss)
-    grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _launch(lib().mm_route_logits_backward, "mm_route_logits_backward", di, stream, (grad,), x, dt,
-            mask, ids, counts, dw, dl, T, E, k, 1 if renorm else 0, grad.data_ptr())
+    on = _On("mm_route_logits_backward", di, stream)
+    grad = on.empty((T, E), logits.dtype)
+    on.launch(lib().mm_route_logits_backward, x, dt, mask, ids, counts, dw, dl, T, E, k,
+              1 if renorm else 0, grad.data_ptr())
     return grad
 
 
@@ -649,11 +667,11 @@ def mm_mxfp4_quantize(x, stream=None):
     if K % 32 != 0 or K == 0:
         raise MMError(MM_ERR_UNSUPPORTED if K else MM_ERR_INVALID_ARG, "mm_mxfp4_quantize")
     di = _device("mm_mxfp4_quantize", x)
-    codes = torch.empty((*lead, rows, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*lead, *mm_mxfp4_scales_shape(rows, K)), dtype=torch.uint8,
-                         device=x.device)
-    _launch(lib().mm_mxfp4_quantize, "mm_mxfp4_quantize", di, stream, (codes, scales), xp, dt,
-            batch, rows, K, codes.data_ptr(), scales.data_ptr())
+    on = _On("mm_mxfp4_quantize", di, stream)
+    codes = on.empty((*lead, rows, K // 2), torch.uint8)
+    scales = on.empty((*lead, *mm_mxfp4_scales_shape(rows, K)), torch.uint8)
+    on.launch(lib().mm_mxfp4_quantize, xp, dt, batch, rows, K, codes.data_ptr(),
+              scales.data_ptr())
     return codes, scales
 
 
@@ -672,9 +690,9 @@ def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     cp, sp = _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales")
     _shape(scales, (*lead, *mm_mxfp4_scales_shape(rows, K)), "scales")
     di = _device("mm_mxfp4_dequantize", codes, scales)
-    out = torch.empty((*lead, rows, K), dtype=dtype, device=codes.device)
-    _launch(lib().mm_mxfp4_dequantize, "mm_mxfp4_dequantize", di, stream, (out,), cp, sp, batch,
-            rows, K, out.data_ptr(), _DTYPES[dtype])
+    on = _On("mm_mxfp4_dequantize", di, stream)
+    out = on.empty((*lead, rows, K), dtype)
+    on.launch(lib().mm_mxfp4_dequantize, cp, sp, batch, rows, K, out.data_ptr(), _DTYPES[dtype])
     return out
 
 
@@ -706,9 +724,9 @@ def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16
     if out_dtype not in _DTYPES:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     di = _device("mm_mxfp4_gemm", a_codes, a_scales, b_codes, b_scales)
-    c = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
-    _launch(lib().mm_mxfp4_gemm, "mm_mxfp4_gemm", di, stream, (c,), a, sa, b, sb, M, N, K,
-            c.data_ptr(), _DTYPES[out_dtype])
+    on = _On("mm_mxfp4_gemm", di, stream)
+    c = on.empty((M, N), out_dtype)
+    on.launch(lib().mm_mxfp4_gemm, a, sa, b, sb, M, N, K, c.data_ptr(), _DTYPES[out_dtype])
     return c
 
 
@@ -745,21 +763,20 @@ def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, 
                _ptr(w_gate_up_scales, torch.uint8, "w_gate_up_scales"))
     dn, sdn = (_ptr(w_down, torch.uint8, "w_down"),
                _ptr(w_down_scales, torch.uint8, "w_down_scales"))
-    l = lib()
-    made = []
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
-        made.append(out)
     _shape(out, (T, H), "out")
-    if workspace is None:
-        need = l.mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k)
-        workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=hidden.device)
-        made.append(workspace)
     outp, ws = _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace")
     di = _device("mm_moe_experts_mxfp4", hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales,
                  w_down, w_down_scales, out, workspace)
-    _launch(l.mm_moe_experts_mxfp4, "mm_moe_experts_mxfp4", di, stream, made, x, ids, w, gu, sgu,
-            dn, sdn, T, H, E, I, k, outp, ws, workspace.numel())
+    l, on = lib(), _On("mm_moe_experts_mxfp4", di, stream)
+    if out is None:
+        out = on.empty((T, H), torch.bfloat16)
+        outp = out.data_ptr()
+    if workspace is None:
+        need = l.mm_moe_experts_mxfp4_workspace_size(T, H, E, I, k)
+        workspace = on.empty(max(need, 0), torch.uint8, result=False)
+        ws = workspace.data_ptr()
+    on.launch(l.mm_moe_experts_mxfp4, x, ids, w, gu, sgu, dn, sdn, T, H, E, I, k, outp, ws,
+              workspace.numel())
     return out
 
 

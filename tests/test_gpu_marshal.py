@@ -159,3 +159,101 @@ def test_results_of_one_allocation_are_apart(T, E, k):
     g = mm.mm_route_logits_backward(x, ids, counts, True, w, loss)
     torch.cuda.synchronize()
     assert torch.isfinite(g).all() and w.shape == (T, k)
+
+
+def _on_a_stream():
+    """Calls that take stream=, by name, with inputs that stay."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn(40000, 64, generator=g, device="cuda")
+    dw = torch.randn(40000, 6, generator=g, device="cuda")
+    ids, w, counts, _, _ = mm.mm_route_logits(x, 6, True)
+    m = torch.randn(2048, 2048, generator=g, device="cuda")
+    q = mm.mm_mxfp4_quantize(m)
+    T, H, E, I, k = 700, 256, 16, 128, 4
+    hid = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    gu = mm.mm_mxfp4_quantize(torch.randn(2 * E, I, H, generator=g, device="cuda"))
+    dn = mm.mm_mxfp4_quantize(torch.randn(E, H, I, generator=g, device="cuda"))
+    some = mm.mm_route_logits(x[:T, :E].contiguous(), k, True)[:2]
+    return {
+        "route": lambda s=None: mm.mm_route_logits(x, 6, True, stream=s),
+        "backward": lambda s=None: mm.mm_route_logits_backward(x, ids, counts, True, dw, stream=s),
+        "quantise": lambda s=None: mm.mm_mxfp4_quantize(m, stream=s),
+        "dequantise": lambda s=None: mm.mm_mxfp4_dequantize(*q, stream=s),
+        "product": lambda s=None: mm.mm_mxfp4_gemm(*q, *q, stream=s),
+        "experts": lambda s=None: mm.mm_moe_experts_mxfp4(hid, *some, *gu, *dn, stream=s),
+    }
+
+
+STREAM_CALLS = ["route", "backward", "quantise", "dequantise", "product", "experts"]
+
+
+def _tuple(r):
+    return r if isinstance(r, tuple) else (r,)
+
+
+@pytest.mark.parametrize("by_handle", [False, True])
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_results_on_a_given_stream_share_no_memory_in_use(name, by_handle):
+    # Memory that the current stream has freed, but still writes: a call on a
+    # stream of its own does not wait for those writes, so it may not take it.
+    call = _on_a_stream()[name]
+    want = [t.clone() for t in _tuple(call())]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8, device="cuda")
+              for t in want]
+    torch.cuda._sleep(200_000_000)
+    for b in blocks:
+        b.fill_(0x5A)
+    del blocks, b
+    got = _tuple(call(side.cuda_stream if by_handle else side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_results_of_a_given_stream_outlive_their_readers(name):
+    # Freed while the current stream still reads them: the next call on the
+    # given stream takes other memory.
+    call = _on_a_stream()[name]
+    want = [t.clone() for t in _tuple(call())]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    cur = torch.cuda.current_stream()
+    got = _tuple(call(side))
+    cur.wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    copies = [t.clone() for t in got]
+    del got
+    for _ in range(3):  # other values into whatever the side stream's memory is
+        with torch.cuda.stream(side):
+            for t in want:
+                torch.empty(t.numel() * t.element_size(), dtype=torch.uint8,
+                            device="cuda").fill_(0x5A)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_a_given_stream_inside_a_capture(name):
+    call = _on_a_stream()[name]
+    want = [t.clone() for t in _tuple(call())]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        got = _tuple(call(side))
+        cur.wait_stream(side)
+        out = [t.clone() for t in got]
+        same = _tuple(call(cur))
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for r in (out, same):
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
