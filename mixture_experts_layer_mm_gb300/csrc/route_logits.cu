@@ -191,15 +191,19 @@ __device__ __forceinline__ float redux_max(float v) {
   return r;
 }
 
-// e^x for x <= 0 (or NaN): 2^t with t = x log2(e) in two parts, the second the
-// rounding of the first product, so that the error stays at that of the
-// hardware's 2^t (2^-22) for any x. Below 2^-126: 0. Two values, or one.
+// e^x for x <= 0 (or NaN): 2^t with t = x log2(e) in two parts, the second what
+// the first product and the constant's rounding leave out (both grow with |x|), so
+// that the error stays at that of the hardware's 2^t (2^-22) and one rounding
+// (2^-24) for any x. Below 2^-126: 0. Two values, or one.
 __device__ __forceinline__ Pair exp_neg(Pair x) {
-  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  constexpr double kLog2eExact = 1.44269504088896341;
+  constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - kLog2e);
+  constexpr float kLn2 = 0.693147180559945309f;
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-200.f));  // e^-200 is below 2^-126 too
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-200.f));
   const Pair t = x * Pair{kLog2e, kLog2e};
-  const Pair rest = fma2(x, Pair{-kLog2e, -kLog2e}, t);  // negative
+  const Pair rest = fma2(x, Pair{-kLog2eRest, -kLog2eRest},
+                         fma2(x, Pair{-kLog2e, -kLog2e}, t));  // negative
   Pair r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));

@@ -492,3 +492,27 @@ def test_rows_with_nan_select_experts_that_exist(E, k, T, masked):
         assert np.abs(g[fine] - exact).max() <= 300 * U * size
     assert not g[~counted].any()
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("T", [30, 250, 20000])
+def test_probabilities_far_below_the_largest(T):
+    # Two experts d apart: p_1 = e^-d / (1 + e^-d), to the same relative error
+    # for every d down to the smallest normal number.
+    rng = np.random.default_rng(T)
+    d = np.sort(rng.uniform(0, 87, T)).astype(np.float32)
+    x = torch.from_numpy(np.stack([np.zeros_like(d), -d], 1)).cuda()
+    ids, w, _, _, _ = mm.mm_route_logits(x, 2, False)
+    want = np.exp(-d.astype(np.float64))
+    want = want / (1 + want)
+    # e^-d: the hardware's 2^t within 2^-22 = 4 U, the product with the rest's
+    # factor 1 U; the sum 1 + e^-d 1 U of its own and at most half of that
+    # error; its reciprocal and the product 1 U each.
+    assert (np.abs(_np64(w)[:, 1] / want - 1) <= (5 + 1 + 2.5 + 2 + 0.5) * U).all()
+    # dL/dl_1 = p_0 p_1 for dL/dw_1 = 1: p_1 (1 - p_1), one more rounding each in
+    # the sum, the difference and the product.
+    dw = torch.zeros(T, 2, device="cuda")
+    dw[:, 1] = 1
+    counts = torch.full((2,), T, dtype=torch.int32, device="cuda")
+    g = _np64(mm.mm_route_logits_backward(x, ids, counts, False, dw))[:, 1]
+    far = d > 2  # 1 - p_1 does not cancel
+    assert (np.abs(g / (want * (1 - want)) - 1)[far] <= (11 + 4) * U).all()
