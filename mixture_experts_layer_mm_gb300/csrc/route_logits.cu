@@ -19,7 +19,9 @@
 // experts from l Q on (one vector load). Both passes read each logit once. The
 // sums over tokens stay in the lane that owns the expert, then go block by block
 // through the caller's workspace in a fixed order, so every output is the same
-// on every call.
+// on every call. A lane adds kRlChain tokens' p at most in plain fp32; longer
+// sums (2^31 tokens are 440,000 a lane) keep their roundings, and all others are
+// added in pairs: a sum is off by some 25 half steps at most, whatever T.
 //
 // What bounds it: small batches are launches (64 tokens x 128 experts 3.9 us,
 // 4096 x 128 in bf16 forward and backward 11.7 us). 131072 x 256 fp32 logits
@@ -47,6 +49,7 @@ constexpr int kRlOneBlockTokens = 32;
 constexpr uint32_t kRlClusterBlocks = 8;
 constexpr int kRlClusterTokens = 2 * kRlClusterBlocks * kRlWarps;
 constexpr uint32_t kFullMask = 0xffffffffu;
+constexpr uint32_t kRlChain = 8;  // tokens between two additions to a lane's long sums
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_logit(const uint16_t* p) {
@@ -131,6 +134,23 @@ __device__ __forceinline__ void stage(float* p, const float (&g)[Q]) {
 #pragma unroll
   for (int i = 0; i + 3 < Q; i += 4)
     *reinterpret_cast<float4*>(p + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+}
+
+// a + b, and in b what its rounding left out (exact).
+__device__ __forceinline__ float add_keep(float a, float& b) {
+  const float s = a + b, bb = s - a;
+  b = (a - (s - bb)) + (b - bb);
+  return s;
+}
+
+// Sum of n values (a power of two) a stride apart, added in pairs.
+template <int N>
+__device__ __forceinline__ float pair_sum(const float* v, int stride) {
+  if constexpr (N == 1) {
+    return *v;
+  } else {
+    return pair_sum<N / 2>(v, stride) + pair_sum<N / 2>(v + N / 2 * stride, stride);
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -370,6 +390,9 @@ __device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits
   constexpr int Q = EP / 32;
   __shared__ __align__(16) float sp[W * EP];  // a warp's p of its token; at the end its sums
   __shared__ int sc[EP], sid[W * 32];         // counts; a warp's selection, ascending
+  // A warp's long sums; the small batches' warps have two tokens at most.
+  constexpr bool kLong = !CLUSTER && W == kRlWarps;
+  __shared__ __align__(16) float slong[kLong ? W * EP : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t stride = gridDim.x * W, T = (uint32_t)a.T;  // t + stride < 2^32
   pdl_wait();
@@ -379,6 +402,9 @@ __device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits
   float psum[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) psum[q] = 0.f;
+  float* mine = &slong[kLong ? warp * EP + lane * Q : 0];
+  if (kLong) stage<Q>(mine, psum);
+  uint32_t chain = 0;
   float next[Q];
   uint32_t t = blockIdx.x * W + warp;
   if (t < T) load_row<Q>(logits, t, a.E, a.vec, next);
@@ -421,6 +447,13 @@ __device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits
         psum[b] = n.y;
       });
     }
+    if (kLong && ++chain == kRlChain) {
+      chain = 0;
+      float l[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) l[q] = add_keep(mine[q], psum[q]);
+      stage<Q>(mine, l);
+    }
     if (lane < a.top_k) {
       a.ids[(size_t)t * a.top_k + lane] = id;
       a.w[(size_t)t * a.top_k + lane] = valid ? pj * scale : 0.f;
@@ -434,8 +467,8 @@ __device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits
   float p = 0.f;
   int c = 0;
   if (threadIdx.x < EP) {
-#pragma unroll
-    for (int w = 0; w < W; ++w) p += sp[w * EP + threadIdx.x];
+    p = pair_sum<W>(&sp[threadIdx.x], EP);
+    if (kLong) p += pair_sum<W>(&slong[threadIdx.x], EP);
     c = sc[threadIdx.x];
   }
   if constexpr (CLUSTER) {
@@ -443,13 +476,14 @@ __device__ __forceinline__ void route_logits_block(const TL* __restrict__ logits
     if (threadIdx.x < EP) sp[threadIdx.x] = p;
     cluster_barrier();
     if (blockIdx.x == 0 && threadIdx.x < EP) {
-      p = 0.f;
+      float part[kRlClusterBlocks];
       c = 0;
 #pragma unroll
       for (uint32_t r = 0; r < kRlClusterBlocks; ++r) {
-        p += load_peer(&sp[threadIdx.x], r);
+        part[r] = load_peer(&sp[threadIdx.x], r);
         c += load_peer(&sc[threadIdx.x], r);
       }
+      p = pair_sum<kRlClusterBlocks>(part, 1);
     }
     cluster_barrier();  // all sums have been read
     if (blockIdx.x != 0) return;
@@ -476,9 +510,10 @@ __global__ void __cluster_dims__(kRlClusterBlocks, 1, 1) __launch_bounds__(kRlTh
   route_logits_block<EP, kRlWarps, true>(logits, a);
 }
 
-// The blocks' sums, added in block order: EP / 4 threads a row take 4 experts
-// each, kRlFinish / (EP / 4) rows at a time.
-constexpr int kRlFinish = 1024;
+// The blocks' sums, added in a fixed order: EP / 4 threads a row take 4 experts
+// each, kRlFinish / (EP / 4) rows at a time. A thread adds kRlBatch rows in pairs
+// before it adds them to the others.
+constexpr int kRlFinish = 1024, kRlBatch = 8;
 
 template <int EP>
 __global__ void __launch_bounds__(kRlFinish) route_logits_finish_kernel(int rows,
@@ -493,12 +528,23 @@ __global__ void __launch_bounds__(kRlFinish) route_logits_finish_kernel(int rows
   int4 c = make_int4(0, 0, 0, 0);
   const float4* pp = reinterpret_cast<const float4*>(a.part_p) + c4;
   const int4* pc = reinterpret_cast<const int4*>(a.part_c) + c4;
-#pragma unroll 8
-  for (int r = g; r < rows; r += G) {
-    const float4 u = pp[(size_t)r * C];
-    const int4 v = pc[(size_t)r * C];
-    p.x += u.x; p.y += u.y; p.z += u.z; p.w += u.w;
-    c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+  for (int r0 = g; r0 < rows; r0 += kRlBatch * G) {
+    float4 u[kRlBatch];
+#pragma unroll
+    for (int i = 0; i < kRlBatch; ++i) {
+      const int r = r0 + i * G;
+      u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        u[i] = pp[(size_t)r * C];
+        const int4 v = pc[(size_t)r * C];
+        c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+      }
+    }
+    const float* f = reinterpret_cast<const float*>(u);
+    p.x += pair_sum<kRlBatch>(f, 4);
+    p.y += pair_sum<kRlBatch>(f + 1, 4);
+    p.z += pair_sum<kRlBatch>(f + 2, 4);
+    p.w += pair_sum<kRlBatch>(f + 3, 4);
   }
   ps[g][c4] = p;
   cs[g][c4] = c;
@@ -508,11 +554,9 @@ __global__ void __launch_bounds__(kRlFinish) route_logits_finish_kernel(int rows
   float sum = 0.f;
   int cnt = 0;
   if (threadIdx.x < EP) {
+    sum = pair_sum<G>(&pf[threadIdx.x], EP);
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      sum += pf[i * EP + threadIdx.x];
-      cnt += ci[i * EP + threadIdx.x];
-    }
+    for (int i = 0; i < G; ++i) cnt += ci[i * EP + threadIdx.x];
   }
   __syncthreads();
   write_batch<EP>(sum, cnt, a, pf, ci);

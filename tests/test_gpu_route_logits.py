@@ -516,3 +516,24 @@ def test_probabilities_far_below_the_largest(T):
     g = _np64(mm.mm_route_logits_backward(x, ids, counts, False, dw))[:, 1]
     far = d > 2  # 1 - p_1 does not cancel
     assert (np.abs(g / (want * (1 - want)) - 1)[far] <= (11 + 4) * U).all()
+
+
+@pytest.mark.parametrize("T", [4097, 100_000, 1 << 27])
+@pytest.mark.parametrize("E", [3, 40, 200])
+def test_sums_over_many_equal_tokens(T, E):
+    # Every p is 1 / E, not a number of the type, so that a plain fp32 sum rounds
+    # the same way at every token.
+    if E > 3 and T > 100_000:
+        T = (1 << 31) // E  # more than 2^31 logits
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    _, _, counts, sums, loss = mm.mm_route_logits(x, 1, False)
+    assert counts.tolist() == [T] + [0] * (E - 1)
+    # p: the exponentials are 1 and their sum is exact, its reciprocal is within 1
+    # U. A lane's partial sums of 8 tokens and what the last ones left: 9 U. Then
+    # additions in pairs: 16 warps and the two kinds of sums 5, 8 blocks 3, 32
+    # groups 5, and up to 480 blocks / (4 groups 8) = 15 U of those in turn.
+    tol = (1 + 9 + 5 + 3 + 5 + 15) * U
+    assert (np.abs(_np64(sums) / (T / E) - 1) <= tol).all()
+    # loss = E (T / T) (T / E) / T = 1: the counts, the tree, two quotients, two
+    # products
+    assert abs(float(loss) - 1) <= tol + 14 * U
