@@ -91,16 +91,25 @@ __device__ __forceinline__ float max_abs4(float a, float b, float c, float d) {
   return r;
 }
 
-// g / (1 + e^-g) * u for two values: 2^t and 1 / x as the hardware gives them,
-// off by |g| 2^-24 and a few units of the 24th bit. Where e^-g is beyond 2^126
-// (g < -87.3) the quotient is 0 (silu is above -2e-36 there).
+// g / (1 + e^-g) * u for two values, within 2^-20.5 of it: the hardware's 2^t
+// (2^-22) and 1 / x (2^-23), with what the product t = -g log2(e) and that constant
+// round off, which grows with |g|, made up for by a factor. Above g = 200 e^-g is 0
+// whatever t is; where it is beyond 2^126 (g < -87.3) the quotient is 0 (silu is
+// above -2e-36 there). An infinite or NaN g makes the block NaN.
 __device__ __forceinline__ Pair swiglu(Pair g, Pair u) {
-  constexpr float kLog2e = 1.44269504088896341f;
-  const Pair t = g * Pair{-kLog2e, -kLog2e};
+  constexpr double kLog2eExact = 1.44269504088896341;
+  constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - kLog2e);
+  constexpr float kLn2 = 0.693147180559945309f;
+  Pair x;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x.x) : "f"(g.x), "f"(200.f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x.y) : "f"(g.y), "f"(200.f));
+  const Pair t = x * Pair{-kLog2e, -kLog2e};
+  const Pair rest = fma2(x, Pair{kLog2eRest, kLog2eRest}, fma2(x, Pair{kLog2e, kLog2e}, t));
+  const Pair f = fma2(rest, Pair{-kLn2, -kLn2}, Pair{1.f, 1.f});
   Pair e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  const Pair d = e + Pair{1.f, 1.f};
+  const Pair d = fma2(e, f, Pair{1.f, 1.f});
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return g * r * u;

@@ -682,3 +682,79 @@ def test_experts_sum_their_slots_in_32_bits(T):
     tol = np.outer(da[:, i0], np.abs(dn[0][:, i0])) + (2 * I * 2.0 ** -23 + 2 * 2.0 ** -24) * mag
     tol = tol + (np.abs(want) + tol) * 2.0 ** -8
     assert (np.abs(out - want) <= tol).all(), (np.abs(out - want) / tol).max()
+
+
+def _digits(value, unit, blocks, rng):
+    """Codes [blocks, 32] and exponents [blocks]: under 2^exponent (7 apart, the
+    last one `unit`) their sum is the integer `value` times 2^unit."""
+    codes, left = np.zeros((blocks, 32), np.uint8), int(value)
+    for b in range(blocks):
+        step = 1 << 7 * (blocks - 1 - b)
+        n = int(round(left / step))
+        left -= n * step
+        sign, n, i = (8 if n < 0 else 0), abs(n), 0
+        while n:
+            c = max(c for c in (2, 4, 5, 6, 7) if ref.LEVELS[c] <= n)  # 1, 2, 3, 4, 6
+            codes[b, i] = c | sign
+            n -= int(ref.LEVELS[c])
+            i += 1
+        codes[b] = codes[b, rng.permutation(32)]
+    assert left == 0
+    return codes, unit + 7 * np.arange(blocks - 1, -1, -1)
+
+
+@pytest.mark.parametrize("low,high", [(-86, -60), (-60, -30), (-30, -8), (2, 40)])
+def test_activations_next_to_a_border(low, high):
+    # One token of ones, gate and up products g and u that are exact sums, and a
+    # w_down that hands the activations out as they are. Every silu(g) u lies
+    # 2^-20 to 2^-19 of itself beside a border between two 4-bit values; the
+    # kernel's is within 10 half steps (2^-20.67) of it: 2^t 4, its factor, the sum
+    # and two products 1 each, the reciprocal 2.
+    rng = np.random.default_rng(low + 1000)
+    H = I = 256
+    gate, up = np.zeros((I, H), np.uint8), np.zeros((I, H), np.uint8)
+    sg, su = np.full((I, H // 32), 127), np.full((I, H // 32), 127)
+    want = np.zeros(I)
+    silu = lambda g: g / (1 + np.exp(-g))  # noqa: E731
+    for i in range(I):
+        first = i % 32 == 0  # 4.5 in every block: the scale is 1
+        gi = round(4 * 2 ** 7) if first else int(round(rng.uniform(low, high) * 2 ** 7))
+        gate[i, :64], e = (a.reshape(-1) for a in _digits(gi, -7, 2, rng))
+        sg[i, :2] = e + 127
+        s = silu(gi / 2 ** 7)
+        if first:
+            ui, unit, want[i] = round(4.5 / s * 2 ** 20), -20, 4.0
+        else:
+            code = rng.integers(0, 7)
+            lo, hi = ref.LEVELS[code], ref.LEVELS[code + 1]
+            over = rng.random() < 0.5
+            target = (lo + hi) / 2 * (1 + (1.5 if over else -1.5) * 2.0 ** -20)
+            unit = int(np.floor(np.log2(target / abs(s)))) - 21
+            ui = round(target / s * 2.0 ** -unit)
+            want[i] = np.copysign(hi if over else lo, 1.0)
+        exact = s * ui * 2.0 ** unit
+        if not first:  # the products, not their targets, are what the test is about
+            off = exact / ((lo + hi) / 2) - 1
+            assert 2.0 ** -20 <= abs(off) <= 2.0 ** -19 and (off > 0) == over
+        else:
+            assert 4.4 < exact < 4.6
+        codes, e = _digits(ui, unit, 4, rng)
+        up[i, 64:192], su[i, 2:6] = codes.reshape(-1), e + 127
+        # sums in 32 bits are exact: the magnitudes stay below 2^24 units
+        assert sum(ref.LEVELS[codes & 7].sum(1) * 2.0 ** (e - unit)) < 2 ** 24
+    assert su.max() <= 254 and su.min() >= 1
+    dn = np.zeros((H, I), np.uint8)
+    dn[np.arange(H), np.arange(H)] = 2  # 1.0
+
+    def stored(c, s):
+        return (torch.from_numpy(ref.pack(c)).cuda(),
+                torch.from_numpy(ref.tile(s.astype(np.uint8))).cuda())
+
+    (g, sg), (u, su) = stored(gate, sg), stored(up, su)
+    dn, sdn = stored(dn, np.full((H, I // 32), 127))
+    out = mm.mm_moe_experts_mxfp4(
+        torch.ones(1, H, dtype=torch.bfloat16, device="cuda"),
+        torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 1, device="cuda"),
+        torch.stack([g, u]), torch.stack([sg, su]), dn[None], sdn[None])
+    _status_ok()
+    assert np.array_equal(_np64(out)[0], want)
