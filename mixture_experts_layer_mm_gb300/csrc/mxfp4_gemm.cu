@@ -475,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t fills[kStages / kProdWarps] = {};  // of this warp's slots
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      if (stopped(&stop_s)) {
-        ok = false;
-        break;
+      // (The stages begun above are completed in any case: their weights are on
+      // their way, and a barrier's phase ends only with all of its bytes.)
+      if (tile != (int)blockIdx.x) {
+        if (stopped(&stop_s)) break;
+        walk.step(a.n_mtiles, E, first_s, cnt_s);
       }
-      if (tile != (int)blockIdx.x) walk.step(a.n_mtiles, E, first_s, cnt_s);
       const Tile& t = walk.t;
       const WeightAt w = weights_of<MODE, NA>(a, t);
       for (int kb = 0; kb < nk; ++kb) {
@@ -509,13 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // Given up: no copy of this warp is in flight when the CTA ends (a slot's
-    // last fill completes its barrier's phase whether or not anybody reads it).
-    if (!ok) {
+    // No copy of this warp is in flight when the CTA ends, also where the warps that
+    // read the slots have given up (a slot's last fill completes its barrier's phase
+    // whether or not anybody reads it).
 #pragma unroll
-      for (int i = 0; i < kStages / kProdWarps; ++i)
-        if (fills[i] > 0) warp_wait(smem_u32(&full[i * kProdWarps + first]), (fills[i] - 1) & 1u);
-    }
+    for (int i = 0; i < kStages / kProdWarps; ++i)
+      if (fills[i] > 0) warp_wait(smem_u32(&full[i * kProdWarps + first]), (fills[i] - 1) & 1u);
   } else if (warp < 2) {
     // ------------------------------------------------- MMA issuers (0, 1) ---
     // Warp 0 feeds D0, warp 1 D1; with one weight tile, D0 from the even and D1
