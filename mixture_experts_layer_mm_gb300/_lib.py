@@ -74,17 +74,18 @@ _lib: Optional[ctypes.CDLL] = None
 
 # The marshalling of the short calls as an extension (csrc/marshal.cpp), loaded
 # with the library. Its functions return None for a call that is not an ordinary
-# one, and everything is marshalled here where it has not been built for this
-# torch.
+# one, and everything is marshalled here where it has not been built from these
+# sources for this torch.
 _fast = None
 
 
 def _load_fast():
+    from . import buildlib
     try:
         from . import _marshal
-    except ImportError:
+        return _marshal if getattr(_marshal, "tag", None) == buildlib.marshal_tag() else None
+    except (ImportError, OSError):
         return None
-    return _marshal if getattr(_marshal, "torch_version", None) == torch.__version__ else None
 
 
 class MMError(RuntimeError):

@@ -345,11 +345,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-// MARSHAL_TORCH: the version of the torch whose headers this was compiled with.
-// The binding uses the module with that version only.
+// MARSHAL_TAG: a digest of this file, the C ABI and the torch and Python it was
+// compiled for. The binding uses the module where it would be built from the same.
 PyMODINIT_FUNC PyInit__marshal(void) {
   PyObject* m = PyModule_Create(&module);
-  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", MARSHAL_TORCH) != 0) {
+  if (m != nullptr && PyModule_AddStringConstant(m, "tag", MARSHAL_TAG) != 0) {
     Py_DECREF(m);
     return nullptr;
   }
