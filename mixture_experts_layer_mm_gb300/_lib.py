@@ -591,16 +591,21 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     di = _device("mm_route_logits", logits, token_mask)
     l = lib()
     need = l.mm_route_logits_workspace_size(T, E)
+    # Refused here already: results of such a size are not to be allocated.
+    if E == 0 or top_k <= 0:
+        raise MMError(MM_ERR_INVALID_ARG, "mm_route_logits")
+    if need < 0 or top_k > E or T * top_k >= 1 << 31:
+        raise MMError(MM_ERR_UNSUPPORTED, "mm_route_logits")
     on = _On("mm_route_logits", di, stream)
-    ids = on.empty((T, max(top_k, 0)), torch.int32)
-    w = on.empty((T, max(top_k, 0)), torch.float32)
+    ids = on.empty((T, top_k), torch.int32)
+    w = on.empty((T, top_k), torch.float32)
     counts = on.empty(E, torch.int32)
     sums = on.empty(E, torch.float32)
     loss = on.empty(1, torch.float32)
     ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
     on.launch(l.mm_route_logits, x, dt, mask, T, E, top_k, 1 if renorm else 0, ids.data_ptr(),
               w.data_ptr(), counts.data_ptr(), sums.data_ptr(), loss.data_ptr(),
-              None if ws is None else ws.data_ptr(), need if need > 0 else 0)
+              None if ws is None else ws.data_ptr(), need)
     return ids, w, counts, sums, loss
 
 

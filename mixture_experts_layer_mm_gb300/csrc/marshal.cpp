@@ -135,7 +135,8 @@ PyObject* route_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int64_t T = x->size(0), E = x->size(1);
   const int dt = dtype_code(x->scalar_type());
-  if (dt < 0 || k < 1 || !fits_int(T) || !fits_int(E)) Py_RETURN_NONE;
+  if (dt < 0 || !fits_int(T) || !fits_int(E) || k < 1 || k > E || !fits_int(T * k))
+    Py_RETURN_NONE;
   if (mask != nullptr && (!shape_is(*mask, {T}) || (mask->scalar_type() != at::kBool &&
                                                     mask->scalar_type() != at::kByte)))
     Py_RETURN_NONE;

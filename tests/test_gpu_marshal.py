@@ -257,3 +257,20 @@ def test_a_given_stream_inside_a_capture(name):
     torch.cuda.synchronize()
     for r in (out, same):
         assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+@pytest.mark.parametrize("top_k", [9, 33, 1 << 20, 1 << 30, (1 << 31) - 1, 1 << 31, 1 << 70])
+@pytest.mark.parametrize("fast", [True, False])
+def test_too_many_slots_are_refused_before_any_memory_is_taken(top_k, fast, monkeypatch):
+    if not fast:
+        monkeypatch.setattr(binding, "_fast", None)
+    for E, code in ((8, mm.MM_ERR_UNSUPPORTED), (300, mm.MM_ERR_UNSUPPORTED),
+                    (0, mm.MM_ERR_INVALID_ARG)):
+        x = torch.randn(1000, E, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with pytest.raises(mm.MMError) as e:
+            mm.mm_route_logits(x, top_k, True)
+        assert e.value.code == code
+        assert torch.cuda.max_memory_allocated() == before
