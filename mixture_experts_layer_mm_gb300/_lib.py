@@ -7,6 +7,7 @@ There is no fallback: if the library is missing the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -557,6 +558,18 @@ class _On:
             self.made.append(t)
         return t
 
+    def parts(self, *parts) -> list:
+        """Tensors (shape, dtype) of one allocation, 256-byte aligned each, as
+        the extension makes them."""
+        sizes = [math.prod(shape) * dtype.itemsize for shape, dtype in parts]
+        at = [0]
+        for n in sizes:
+            at.append(at[-1] + (n + 255) // 256 * 256)
+        whole = self.empty(at[-1], torch.uint8)
+        return [torch.empty(0, dtype=dtype, device=whole.device).set_(
+                    whole.untyped_storage(), o // dtype.itemsize, shape)
+                for (shape, dtype), o in zip(parts, at)]
+
     def launch(self, fn, *args) -> None:
         """fn(*args, stream handle)."""
         st = (torch._C._cuda_getCurrentRawStream(self.di) if self.stream is None
@@ -579,7 +592,9 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     the statistics of the balance loss. Returns (topk_ids int32 [T, k],
     topk_w fp32 [T, k], expert_counts int32 [E], prob_sums fp32 [E],
     loss fp32 [1]). token_mask [T] (bool or uint8): zero for padding tokens.
-    (Ids and weights may share one allocation, and so may the other three.)"""
+    Ids and weights share one allocation, and so do the other three: clone()
+    what is to be stored on its own. Results carry no autograd graph:
+    mm_route_logits_backward is the gradient."""
     if _fast is not None and stream is None:
         r = _fast.route_logits(logits, top_k, renorm, token_mask)
         if r is not None:
@@ -597,11 +612,9 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     if need < 0 or top_k > E or T * top_k >= 1 << 31:
         raise MMError(MM_ERR_UNSUPPORTED, "mm_route_logits")
     on = _On("mm_route_logits", di, stream)
-    ids = on.empty((T, top_k), torch.int32)
-    w = on.empty((T, top_k), torch.float32)
-    counts = on.empty(E, torch.int32)
-    sums = on.empty(E, torch.float32)
-    loss = on.empty(1, torch.float32)
+    ids, w = on.parts(((T, top_k), torch.int32), ((T, top_k), torch.float32))
+    counts, sums, loss = on.parts(((E,), torch.int32), ((E,), torch.float32),
+                                  ((1,), torch.float32))
     ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
     on.launch(l.mm_route_logits, x, dt, mask, T, E, top_k, 1 if renorm else 0, ids.data_ptr(),
               w.data_ptr(), counts.data_ptr(), sums.data_ptr(), loss.data_ptr(),

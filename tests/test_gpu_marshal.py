@@ -274,3 +274,24 @@ def test_too_many_slots_are_refused_before_any_memory_is_taken(top_k, fast, monk
             mm.mm_route_logits(x, top_k, True)
         assert e.value.code == code
         assert torch.cuda.max_memory_allocated() == before
+
+
+@pytest.mark.parametrize("T,E,k", [(0, 5, 2), (1, 1, 1), (65, 70, 7), (3000, 256, 8)])
+def test_results_share_storage_whether_or_not_the_extension_is_built(T, E, k, monkeypatch):
+    x = torch.randn(T, E, device="cuda")
+    fast = mm.mm_route_logits(x, k, True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    given = mm.mm_route_logits(x, k, True, stream=side)
+    monkeypatch.setattr(binding, "_fast", None)
+    slow = mm.mm_route_logits(x, k, True)
+    torch.cuda.synchronize()
+    for got in (fast, given, slow):
+        place = [(t.untyped_storage().data_ptr(), t.storage_offset() * t.element_size())
+                 for t in got]
+        assert [p[0] == q[0] for p in place for q in place] == \
+            [p == q for p in "aabbb" for q in "aabbb"]
+        assert [p[1] for p in place] == [p[1] for p in [
+            (t.untyped_storage().data_ptr(), t.storage_offset() * t.element_size()) for t in fast]]
+        assert not any(t._is_view() or t.requires_grad for t in got)
+        assert all(torch.equal(a, b) and a.stride() == b.stride() for a, b in zip(got, fast))
