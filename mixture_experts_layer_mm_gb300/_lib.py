@@ -143,6 +143,25 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _given(stream, di: int):
+    """The caller's stream as torch's (a handle is one of device `di`)."""
+    return (stream if isinstance(stream, torch.cuda.Stream)
+            else torch.cuda.ExternalStream(int(stream), device=di))
+
+
+def _empty(shape, dtype, like, stream, result: bool = True) -> torch.Tensor:
+    """A result (or a workspace) on the device of `like` for a call on `stream`:
+    of that stream's memory, since a block of the current one's may still be in
+    use there by work that a given stream does not wait for."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(_given(stream, like.get_device())):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if result and t.numel():  # read on the caller's stream, once that waits for this one
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def mm_align_capacity(T: int, top_k: int, E: int, block_m: int) -> int:
     return int(lib().mm_align_capacity(T, top_k, E, block_m))
 
@@ -191,9 +210,9 @@ def mm_route(hidden, router_w, top_k: int, renorm: bool, router_bias=None,
     T, H = hidden.shape
     E = router_w.shape[0]
     if topk_ids is None:
-        topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=hidden.device)
+        topk_ids = _empty((T, top_k), torch.int32, hidden, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, top_k), dtype=torch.float32, device=hidden.device)
+        topk_w = _empty((T, top_k), torch.float32, hidden, stream)
     _check(lib().mm_route(_ptr(hidden, torch.bfloat16, "hidden"),
                           _ptr(router_w, torch.bfloat16, "router_w"),
                           _ptr(router_bias, torch.float32, "router_bias"),
@@ -207,16 +226,15 @@ def mm_align(topk_ids, E: int, block_m: int, sorted_token_ids=None, expert_offse
              expert_counts=None, stream=None):
     """Block-padded grouping by expert. Returns (sorted_token_ids, expert_offsets, expert_counts)."""
     T, k = topk_ids.shape
-    dev = topk_ids.device
     cap = mm_align_capacity(T, k, E, block_m)
     if cap < 0:
         raise MMError(MM_ERR_INVALID_ARG, "mm_align_capacity")
     if sorted_token_ids is None:
-        sorted_token_ids = torch.empty(cap, dtype=torch.int32, device=dev)
+        sorted_token_ids = _empty(cap, torch.int32, topk_ids, stream)
     if expert_offsets is None:
-        expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        expert_offsets = _empty(E + 1, torch.int32, topk_ids, stream)
     if expert_counts is None:
-        expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+        expert_counts = _empty(E, torch.int32, topk_ids, stream)
     _check(lib().mm_align(_ptr(topk_ids, torch.int32, "topk_ids"), T, k, E, block_m,
                           _ptr(sorted_token_ids, torch.int32, "sorted_token_ids"),
                           _ptr(expert_offsets, torch.int32, "expert_offsets"),
@@ -263,7 +281,7 @@ def mm_moe_forward(hidden, router_w, w_gate_up, w_down, top_k: int, renorm: bool
     E = router_w.shape[0]
     I = w_down.shape[2]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, H), torch.bfloat16, hidden, stream)
     if router_bias is None and workspace is None:
         _check(lib().mm_moe_forward(_ptr(hidden, torch.bfloat16, "hidden"),
                                     _ptr(router_w, torch.bfloat16, "router_w"),
@@ -295,7 +313,7 @@ def mm_moe_forward_single_launch(hidden, router_w, w_gate_up, w_down, top_k: int
     E = router_w.shape[0]
     I = w_down.shape[2]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, H), torch.bfloat16, hidden, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = _ptr(workspace, torch.uint8, "workspace"), workspace.numel()
@@ -337,7 +355,7 @@ def mm_moe_forward_partial(hidden, router_w, w_gate_up_slice, w_down_slice, top_
     E = router_w.shape[0]
     I = w_down_slice.shape[2]
     if partial is None:
-        partial = torch.empty((T, H), dtype=torch.float32, device=hidden.device)
+        partial = _empty((T, H), torch.float32, hidden, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = _ptr(workspace, torch.uint8, "workspace"), workspace.numel()
@@ -355,7 +373,7 @@ def mm_moe_forward_partial(hidden, router_w, w_gate_up_slice, w_down_slice, top_
 def mm_round_bf16(x, out=None, stream=None):
     """bf16 rounding (to nearest even) of an fp32 tensor, on the GPU."""
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = _empty(x.shape, torch.bfloat16, x, stream)
     _check(lib().mm_round_bf16(_ptr(x, torch.float32, "x"), _ptr(out, torch.bfloat16, "out"),
                                x.numel(), _stream(stream)), "mm_round_bf16")
     return out
@@ -370,7 +388,7 @@ def mm_gated_mlp(hidden, w_gate_up, w_down, out=None, stream=None):
     T, H = hidden.shape
     I = w_down.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, H), torch.bfloat16, hidden, stream)
     _check(lib().mm_gated_mlp(_ptr(hidden, torch.bfloat16, "hidden"),
                               _ptr(w_gate_up, torch.bfloat16, "w_gate_up"),
                               _ptr(w_down, torch.bfloat16, "w_down"), T, H, I,
@@ -383,7 +401,7 @@ def mm_add_rmsnorm(x, norm_w, eps: float, residual=None, normed=None, stream=Non
     residual); returns normed = rmsnorm(residual, norm_w, eps) [T, H] bf16."""
     T, H = x.shape
     if normed is None:
-        normed = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        normed = _empty((T, H), torch.bfloat16, x, stream)
     _check(lib().mm_add_rmsnorm(_ptr(x, torch.bfloat16, "x"),
                                 _ptr(residual, torch.bfloat16, "residual"),
                                 _ptr(norm_w, torch.bfloat16, "norm_w"), float(eps), T, H,
@@ -400,7 +418,7 @@ def mm_moe_forward_add_norm(x, norm_w, eps: float, router_w, w_gate_up, w_down, 
     E = router_w.shape[0]
     I = w_down.shape[2]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, H), torch.bfloat16, x, stream)
     _check(lib().mm_moe_forward_add_norm(_ptr(x, torch.bfloat16, "x"),
                                          _ptr(residual, torch.bfloat16, "residual"),
                                          _ptr(norm_w, torch.bfloat16, "norm_w"), float(eps),
@@ -424,9 +442,10 @@ def mm_moe_forward_add_norm_residual(x, norm_w, eps: float, router_w, w_gate_up,
     E = router_w.shape[0]
     I = w_down.shape[2]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, H), torch.bfloat16, x, stream)
     if residual_out is None:
-        residual_out = residual if residual is not None else torch.empty_like(x)
+        residual_out = (residual if residual is not None
+                        else _empty(x.shape, x.dtype, x, stream))
     _check(lib().mm_moe_forward_add_norm_residual(
         _ptr(x, torch.bfloat16, "x"), _ptr(residual, torch.bfloat16, "residual"),
         _ptr(norm_w, torch.bfloat16, "norm_w"), float(eps),
@@ -450,7 +469,7 @@ def mm_moe_forward_profiled(hidden, router_w, w_gate_up, w_down, top_k: int, ren
     if len(events) != len(PROFILE_STAGES) + 1:
         raise ValueError(f"need {len(PROFILE_STAGES) + 1} events")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, H), torch.bfloat16, hidden, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = _ptr(workspace, torch.uint8, "workspace"), workspace.numel()
@@ -488,7 +507,7 @@ def mm_selftest_layer_barrier_timeout(hidden, router_w, w_gate_up, w_down, top_k
     E = router_w.shape[0]
     I = w_down.shape[2]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        out = _empty((T, H), torch.bfloat16, hidden, stream)
     _check(lib().mm_selftest_layer_barrier_timeout(
         _ptr(hidden, torch.bfloat16, "hidden"), _ptr(router_w, torch.bfloat16, "router_w"),
         _ptr(w_gate_up, torch.bfloat16, "w_gate_up"), _ptr(w_down, torch.bfloat16, "w_down"),
@@ -524,39 +543,29 @@ def _mask_ptr(mask, T: int):
     return _ptr(mask, mask.dtype, "token_mask")
 
 
-def _device(name: str, *tensors) -> int:
-    """The index of the one device that all tensors (None: absent) are on."""
+def _device(name: str, *tensors) -> None:
+    """All tensors (None: absent) have to be on the first one's device."""
     di = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != di:
             raise ValueError(f"{name}: all tensors must be on {tensors[0].device}, got {t.device}")
-    return di
 
 
 class _On:
-    """Where a call runs: device `di` and `stream` (the caller's, else the
-    device's current one). Results and workspaces come from that stream's
-    memory: a block of another stream's may still be in use there by work that
-    this one does not wait for."""
+    """Where a call runs: the device of `like`, and `stream` (the caller's, else
+    that device's current one)."""
 
-    def __init__(self, name: str, di: int, stream):
-        self.name, self.di, self.stream, self.made = name, di, None, []
+    def __init__(self, name: str, like: torch.Tensor, stream):
+        self.name, self.like, self.di, self.stream = name, like, like.get_device(), None
         if stream is not None:
-            s = (stream if isinstance(stream, torch.cuda.Stream)
-                 else torch.cuda.ExternalStream(int(stream), device=di))
-            if s.device_index != di:
+            s = _given(stream, self.di)
+            if s.device_index != self.di:
                 raise ValueError(f"{name}: the stream is on another device than the tensors")
-            if s.cuda_stream != torch._C._cuda_getCurrentRawStream(di):
+            if s.cuda_stream != torch._C._cuda_getCurrentRawStream(self.di):
                 self.stream = s
 
     def empty(self, shape, dtype, result: bool = True) -> torch.Tensor:
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.di))
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.di))
-        if result:
-            self.made.append(t)
-        return t
+        return _empty(shape, dtype, self.like, self.stream, result)
 
     def parts(self, *parts) -> list:
         """Tensors (shape, dtype) of one allocation, 256-byte aligned each, as
@@ -581,10 +590,6 @@ class _On:
                 rc = fn(*args, st)
         if rc != MM_OK:
             raise MMError(rc, self.name)
-        # The results are read on the caller's stream, once that waits for this one.
-        for t in self.made:
-            if t.numel():
-                t.record_stream(torch.cuda.current_stream(self.di))
 
 
 def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=None):
@@ -603,7 +608,7 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
     T, E = logits.shape
     x = _ptr(logits, logits.dtype, "logits")
     mask = _mask_ptr(token_mask, T)
-    di = _device("mm_route_logits", logits, token_mask)
+    _device("mm_route_logits", logits, token_mask)
     l = lib()
     need = l.mm_route_logits_workspace_size(T, E)
     # Refused here already: results of such a size are not to be allocated.
@@ -611,7 +616,7 @@ def mm_route_logits(logits, top_k: int, renorm: bool, token_mask=None, stream=No
         raise MMError(MM_ERR_INVALID_ARG, "mm_route_logits")
     if need < 0 or top_k > E or T * top_k >= 1 << 31:
         raise MMError(MM_ERR_UNSUPPORTED, "mm_route_logits")
-    on = _On("mm_route_logits", di, stream)
+    on = _On("mm_route_logits", logits, stream)
     ids, w = on.parts(((T, top_k), torch.int32), ((T, top_k), torch.float32))
     counts, sums, loss = on.parts(((E,), torch.int32), ((E,), torch.float32),
                                   ((1,), torch.float32))
@@ -644,9 +649,9 @@ def mm_route_logits_backward(logits, topk_ids, expert_counts, renorm: bool, d_to
     ids, counts = (_ptr(topk_ids, torch.int32, "topk_ids"),
                    _ptr(expert_counts, torch.int32, "expert_counts"))
     dw, dl = _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(d_loss, torch.float32, "d_loss")
-    di = _device("mm_route_logits_backward", logits, token_mask, topk_ids, expert_counts, d_topk_w,
-                 d_loss)
-    on = _On("mm_route_logits_backward", di, stream)
+    _device("mm_route_logits_backward", logits, token_mask, topk_ids, expert_counts, d_topk_w,
+            d_loss)
+    on = _On("mm_route_logits_backward", logits, stream)
     grad = on.empty((T, E), logits.dtype)
     on.launch(lib().mm_route_logits_backward, x, dt, mask, ids, counts, dw, dl, T, E, k,
               1 if renorm else 0, grad.data_ptr())
@@ -685,8 +690,7 @@ def mm_mxfp4_quantize(x, stream=None):
     xp = _ptr(x, x.dtype, "x")
     if K % 32 != 0 or K == 0:
         raise MMError(MM_ERR_UNSUPPORTED if K else MM_ERR_INVALID_ARG, "mm_mxfp4_quantize")
-    di = _device("mm_mxfp4_quantize", x)
-    on = _On("mm_mxfp4_quantize", di, stream)
+    on = _On("mm_mxfp4_quantize", x, stream)
     codes = on.empty((*lead, rows, K // 2), torch.uint8)
     scales = on.empty((*lead, *mm_mxfp4_scales_shape(rows, K)), torch.uint8)
     on.launch(lib().mm_mxfp4_quantize, xp, dt, batch, rows, K, codes.data_ptr(),
@@ -708,8 +712,8 @@ def mm_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
     cp, sp = _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales")
     _shape(scales, (*lead, *mm_mxfp4_scales_shape(rows, K)), "scales")
-    di = _device("mm_mxfp4_dequantize", codes, scales)
-    on = _On("mm_mxfp4_dequantize", di, stream)
+    _device("mm_mxfp4_dequantize", codes, scales)
+    on = _On("mm_mxfp4_dequantize", codes, stream)
     out = on.empty((*lead, rows, K), dtype)
     on.launch(lib().mm_mxfp4_dequantize, cp, sp, batch, rows, K, out.data_ptr(), _DTYPES[dtype])
     return out
@@ -742,8 +746,8 @@ def mm_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16
         raise ValueError(f"a has {K} columns, b has {Kb}")
     if out_dtype not in _DTYPES:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-    di = _device("mm_mxfp4_gemm", a_codes, a_scales, b_codes, b_scales)
-    on = _On("mm_mxfp4_gemm", di, stream)
+    _device("mm_mxfp4_gemm", a_codes, a_scales, b_codes, b_scales)
+    on = _On("mm_mxfp4_gemm", a_codes, stream)
     c = on.empty((M, N), out_dtype)
     on.launch(lib().mm_mxfp4_gemm, a, sa, b, sb, M, N, K, c.data_ptr(), _DTYPES[out_dtype])
     return c
@@ -784,9 +788,9 @@ def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, 
                _ptr(w_down_scales, torch.uint8, "w_down_scales"))
     _shape(out, (T, H), "out")
     outp, ws = _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace")
-    di = _device("mm_moe_experts_mxfp4", hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales,
-                 w_down, w_down_scales, out, workspace)
-    l, on = lib(), _On("mm_moe_experts_mxfp4", di, stream)
+    _device("mm_moe_experts_mxfp4", hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales,
+            w_down, w_down_scales, out, workspace)
+    l, on = lib(), _On("mm_moe_experts_mxfp4", hidden, stream)
     if out is None:
         out = on.empty((T, H), torch.bfloat16)
         outp = out.data_ptr()

@@ -295,3 +295,53 @@ def test_results_share_storage_whether_or_not_the_extension_is_built(T, E, k, mo
             (t.untyped_storage().data_ptr(), t.storage_offset() * t.element_size()) for t in fast]]
         assert not any(t._is_view() or t.requires_grad for t in got)
         assert all(torch.equal(a, b) and a.stride() == b.stride() for a, b in zip(got, fast))
+
+
+def _layer_on_a_stream():
+    """The layer's own calls that allocate results, with inputs that stay."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    T, H, E, I, k = 1500, 512, 16, 128, 4
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, rw, gu, dn, nw = rand(T, H), rand(E, H), rand(E, 2 * I, H), rand(E, H, I), rand(H)
+    ids, _ = mm.mm_route(x, rw, k, True)
+    part = mm.mm_moe_forward_partial(x, rw, gu, dn, k, True)
+    return {
+        "route": lambda s=None: mm.mm_route(x, rw, k, True, stream=s),
+        "align": lambda s=None: mm.mm_align(ids, E, 16, stream=s)[1:],
+        "forward": lambda s=None: mm.mm_moe_forward(x, rw, gu, dn, k, True, stream=s),
+        "partial": lambda s=None: mm.mm_moe_forward_partial(x, rw, gu, dn, k, True, stream=s),
+        "round": lambda s=None: mm.mm_round_bf16(part, stream=s),
+        "dense": lambda s=None: mm.mm_gated_mlp(x, gu[0], dn[0], stream=s),
+        "norm": lambda s=None: mm.mm_add_rmsnorm(x, nw, 1e-6, stream=s),
+        "norm and layer": lambda s=None: mm.mm_moe_forward_add_norm(x, nw, 1e-6, rw, gu, dn, k,
+                                                                    True, stream=s),
+        "residual": lambda s=None: mm.mm_moe_forward_add_norm_residual(x, nw, 1e-6, rw, gu, dn, k,
+                                                                       True, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["route", "align", "forward", "partial", "round", "dense", "norm",
+                                  "norm and layer", "residual"])
+def test_layer_results_on_a_given_stream_share_no_memory_in_use(name):
+    # By address: the layer adds its slots up in no fixed order, so two calls may
+    # differ in a rounding.
+    call = _layer_on_a_stream()[name]
+    side = torch.cuda.Stream()
+    sizes = [t.numel() * t.element_size() for t in _tuple(call())]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda._sleep(200_000_000)
+    in_use = []
+    for b in blocks:
+        b.fill_(0x5A)
+        in_use.append((b.data_ptr(), b.data_ptr() + b.numel()))
+    del blocks, b
+    got = _tuple(call(side))
+    for t, n in zip(got, sizes):
+        assert all(t.data_ptr() + n <= lo or hi <= t.data_ptr() for lo, hi in in_use)
+    torch.cuda.synchronize()
+    assert mm.mm_poll_device_status() == mm.MM_OK
