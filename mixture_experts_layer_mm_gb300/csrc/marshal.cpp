@@ -14,6 +14,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
+
 #include "mm.h"
 
 namespace {
@@ -22,10 +24,19 @@ using at::Tensor;
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// One call: the device of its first tensor, and whether all fit so far.
+// Other threads of Python run while this lives: a launch waits where the device's
+// queue is full, and an allocation may wait for the device.
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
+// One call: the device of its first tensor, and whether all fit so far. Python is
+// released from its first allocation to the end of the library's call.
 struct Call {
   bool ok = true;
   int device = -1;
+  std::optional<Released> released;
 
   // A contiguous tensor of `type` on the one device; NULL (ok stays) for None
   // if `optional`.
@@ -58,7 +69,8 @@ struct Call {
     return &t;
   }
 
-  Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
+  Tensor make(at::IntArrayRef shape, at::ScalarType type) {
+    if (!released) released.emplace();
     return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)device),
                                   std::nullopt);
   }
@@ -74,6 +86,14 @@ struct Call {
     i->set_storage_offset(at / (int64_t)c10::elementSize(type));
     at += round256(t.numel() * (int64_t)c10::elementSize(type));
     return t;
+  }
+
+  template <typename... P, typename... A>
+  int run(int (*fn)(P...), A... a) {
+    if (!released) released.emplace();
+    const int rc = fn(a...);
+    released.reset();
+    return rc;
   }
 
   void* stream() const {
@@ -154,8 +174,9 @@ PyObject* route_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
          sums = c.part(batch, in_batch, {E}, at::kFloat),
          loss = c.part(batch, in_batch, {1}, at::kFloat), ws;
   if (need > 0) ws = c.make({need}, at::kByte);
-  const int rc = mm_route_logits(
-      x->data_ptr(), dt, mask ? static_cast<const uint8_t*>(mask->data_ptr()) : nullptr, (int)T,
+  const int rc = c.run(
+      mm_route_logits, x->data_ptr(), dt,
+      mask ? static_cast<const uint8_t*>(mask->data_ptr()) : nullptr, (int)T,
       (int)E, (int)k, renorm, static_cast<int32_t*>(ids.data_ptr()),
       static_cast<float*>(w.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
       static_cast<float*>(sums.data_ptr()), static_cast<float*>(loss.data_ptr()),
@@ -197,8 +218,9 @@ PyObject* route_logits_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                     mask->scalar_type() != at::kByte)))
     Py_RETURN_NONE;
   Tensor grad = c.make({T, E}, x->scalar_type());
-  const int rc = mm_route_logits_backward(
-      x->data_ptr(), dt, mask ? static_cast<const uint8_t*>(mask->data_ptr()) : nullptr,
+  const int rc = c.run(
+      mm_route_logits_backward, x->data_ptr(), dt,
+      mask ? static_cast<const uint8_t*>(mask->data_ptr()) : nullptr,
       static_cast<const int32_t*>(ids->data_ptr()), static_cast<const int32_t*>(counts->data_ptr()),
       dw ? static_cast<const float*>(dw->data_ptr()) : nullptr,
       dl ? static_cast<const float*>(dl->data_ptr()) : nullptr, (int)T, (int)E, (int)k, renorm,
@@ -223,9 +245,10 @@ PyObject* mxfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor codes = lead ? c.make({batch, rows, K / 2}, at::kByte) : c.make({rows, K / 2}, at::kByte);
   Tensor scales = lead ? c.make({batch, tiles(rows), tiles(K), 512}, at::kByte)
                        : c.make({tiles(rows), tiles(K), 512}, at::kByte);
-  const int rc = mm_mxfp4_quantize(x->data_ptr(), dt, (int)batch, (int)rows, (int)K,
-                                   static_cast<uint8_t*>(codes.data_ptr()),
-                                   static_cast<uint8_t*>(scales.data_ptr()), c.stream());
+  const int rc = c.run(
+      mm_mxfp4_quantize, x->data_ptr(), dt, (int)batch, (int)rows, (int)K,
+      static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
+      c.stream());
   if (rc != MM_OK) Py_RETURN_NONE;
   PyObject* r = PyTuple_New(2);
   if (r == nullptr) return nullptr;
@@ -251,9 +274,10 @@ PyObject* mxfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
              : shape_is(*scales, {tiles(rows), tiles(K), 512})))
     Py_RETURN_NONE;
   Tensor out = lead ? c.make({batch, rows, K}, dtype_of(dt)) : c.make({rows, K}, dtype_of(dt));
-  const int rc = mm_mxfp4_dequantize(static_cast<const uint8_t*>(codes->data_ptr()),
-                                     static_cast<const uint8_t*>(scales->data_ptr()), (int)batch,
-                                     (int)rows, (int)K, out.data_ptr(), (int)dt, c.stream());
+  const int rc = c.run(
+      mm_mxfp4_dequantize, static_cast<const uint8_t*>(codes->data_ptr()),
+      static_cast<const uint8_t*>(scales->data_ptr()), (int)batch, (int)rows, (int)K,
+      out.data_ptr(), (int)dt, c.stream());
   if (rc != MM_OK) Py_RETURN_NONE;
   return wrap(std::move(out));
   MARSHAL_END
@@ -282,8 +306,9 @@ PyObject* mxfp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!c.ok || dt > 1 || !matrix(*x, *sx, M, K) || !matrix(*w, *sw, N, Kw) || K != Kw)
     Py_RETURN_NONE;
   Tensor out = c.make({M, N}, dtype_of(dt));
-  const int rc = mm_mxfp4_gemm(
-      static_cast<const uint8_t*>(x->data_ptr()), static_cast<const uint8_t*>(sx->data_ptr()),
+  const int rc = c.run(
+      mm_mxfp4_gemm, static_cast<const uint8_t*>(x->data_ptr()),
+      static_cast<const uint8_t*>(sx->data_ptr()),
       static_cast<const uint8_t*>(w->data_ptr()), static_cast<const uint8_t*>(sw->data_ptr()),
       (int)M, (int)N, (int)K, out.data_ptr(), (int)dt, c.stream());
   if (rc != MM_OK) Py_RETURN_NONE;
@@ -313,10 +338,13 @@ PyObject* experts_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t need =
       mm_moe_experts_mxfp4_workspace_size((int)T, (int)H, (int)E, (int)I, (int)k);
   if (need < 0) Py_RETURN_NONE;
-  Tensor out = given != nullptr ? *given : c.make({T, H}, at::kBFloat16);
-  Tensor ws = space != nullptr ? *space : c.make({need}, at::kByte);
-  const int rc = mm_moe_experts_mxfp4(
-      static_cast<const uint16_t*>(x->data_ptr()), static_cast<const int32_t*>(ids->data_ptr()),
+  Tensor made, scratch;
+  if (given == nullptr) made = c.make({T, H}, at::kBFloat16);
+  if (space == nullptr) scratch = c.make({need}, at::kByte);
+  const Tensor &out = given != nullptr ? *given : made, &ws = space != nullptr ? *space : scratch;
+  const int rc = c.run(
+      mm_moe_experts_mxfp4, static_cast<const uint16_t*>(x->data_ptr()),
+      static_cast<const int32_t*>(ids->data_ptr()),
       static_cast<const float*>(w->data_ptr()), static_cast<const uint8_t*>(gu->data_ptr()),
       static_cast<const uint8_t*>(sgu->data_ptr()), static_cast<const uint8_t*>(dn->data_ptr()),
       static_cast<const uint8_t*>(sdn->data_ptr()), (int)T, (int)H, (int)E, (int)I, (int)k,
@@ -326,7 +354,7 @@ PyObject* experts_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_INCREF(a[7]);
     return a[7];
   }
-  return wrap(std::move(out));
+  return wrap(std::move(made));
   MARSHAL_END
 }
 

@@ -345,3 +345,34 @@ def test_layer_results_on_a_given_stream_share_no_memory_in_use(name):
         assert all(t.data_ptr() + n <= lo or hi <= t.data_ptr() for lo, hi in in_use)
     torch.cuda.synchronize()
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_other_threads_run_while_a_launch_waits(name):
+    # Behind a kernel of about a second the launches fill the device's queue and
+    # wait; a thread beside them goes on.
+    import threading
+    import time
+    call = _on_a_stream()[name]
+    keep = [call() for _ in range(3)]
+    torch.cuda.synchronize()
+    done, gaps = threading.Event(), []
+
+    def beside():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    thread = threading.Thread(target=beside)
+    thread.start()
+    torch.cuda._sleep(2_000_000_000)
+    begun = time.perf_counter()
+    while time.perf_counter() - begun < 0.5:
+        keep = keep[-10:] + [call()]
+    torch.cuda.synchronize()
+    done.set()
+    thread.join()
+    assert max(gaps) < 0.3, max(gaps)
