@@ -784,11 +784,11 @@ cudaError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, cons
   const long long tiles = chunks * a.n_mtiles;
   const long long scale_tiles = (long long)mx_tiles(N) * mx_tiles(K);
   // With whole groups of 32 output columns a thread can have four of them and
-  // store wide, but the boxes in that row order take longer to load. Long
-  // reductions over enough tiles to fill the SMs are bound by the loads
-  // (8192 x 4096, K = 4096: 56.7 us in that order, 54.3 without; K = 1024: 23.4
-  // and 24.3; 64 x 4096 x 4096, few tiles: 8.9 and 9.6).
-  const bool perm = N % 32 == 0 && (K <= 2048 || narrow || tiles < num_sms);
+  // store wide, but the boxes in that row order take longer to load. Where tiles
+  // fill the SMs it pays for short reductions only (8192 x 4096, in that order and
+  // without: K = 512 19.2 and 20.1 us, 1024 24.5 and 23.7, 2048 37.9 and 35.3, 4096
+  // 59.9 and 54.8); few tiles are bound by latency (64 x 4096 x 4096: 8.9 and 9.6).
+  const bool perm = N % 32 == 0 && (K < 1024 || narrow || tiles < num_sms);
   auto launch = perm ? (narrow ? launch_mode<kDense, true, 1> : launch_mode<kDense, true, 2>)
                      : (narrow ? launch_mode<kDense, false, 1> : launch_mode<kDense, false, 2>);
   return launch(b_codes, N, scale_tiles, a_codes, M, a, tiles, num_sms, true, st);

@@ -723,9 +723,10 @@ bool rows_are_vectors(const void* p, int E, int size) {
   return E % Q == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
-// As many blocks as run at once: two an SM with 8 experts a lane (62 registers a
-// thread), three with fewer (44 at most).
-int blocks_per_sm(int E) { return ep_of(E) == 256 ? 2 : 3; }
+// As many blocks as run at once: two an SM with 4 or 8 experts a lane (52 and 63
+// registers a thread), three with fewer (40). 131072 tokens forward, two and three:
+// 128 experts 60.8 and 64.9 us, 64 experts 67.2 and 49.1, 32 experts 62.7 and 44.9.
+int blocks_per_sm(int E) { return ep_of(E) >= 128 ? 2 : 3; }
 
 int blocks_for(int T, int E, int num_sms) {
   const long long want = ((long long)T + kRlWarps - 1) / kRlWarps;
