@@ -23,11 +23,12 @@
 // sums (2^31 tokens are 440,000 a lane) keep their roundings, and all others are
 // added in pairs: a sum is off by some 25 half steps at most, whatever T.
 //
-// What bounds it: small batches are launches (64 tokens x 128 experts 3.9 us,
-// 4096 x 128 in bf16 forward and backward 11.7 us). 131072 x 256 fp32 logits
-// take 78 us forward and 53 us backward, 134 and 268 MB: the forward issues 530
-// instructions a token (selection and the exact exponentials, mostly of the half-
-// rate kind), 75 % of the issue slots; the backward 290, at 5 TB/s.
+// What bounds it: small batches are launches (64 tokens x 128 experts 3.7 us in a
+// captured graph, 5.4 a call back to back; 4096 x 128 in bf16 forward and backward
+// 11.3 us a call). 131072 x 256 fp32 logits take 80 us forward and 54 us backward,
+// 134 and 268 MB: the forward issues some 540 instructions a token (selection and
+// the exponentials, mostly of the half-rate kind), 75 % of the issue slots; the
+// backward 290, at 5 TB/s.
 #include <math.h>
 
 #include "mm_device.cuh"
@@ -40,10 +41,10 @@ constexpr int kRlThreads = 512;
 constexpr int kRlWarps = kRlThreads / 32;
 // Small batches take one launch and no workspace: one block up to
 // kRlOneBlockTokens, one cluster up to kRlClusterTokens, two tokens a warp at
-// most. 128 experts, us a call in a captured graph: 64 tokens 3.9 in a cluster,
-// 5.8 in one block; 128 tokens 3.9, 4.9 in two launches; 256 tokens 5.4 and 4.9,
-// but 6.4 and 9.3 outside of a graph, where a launch costs the host as much as the
-// kernel takes.
+// most. 128 experts, us a call in a captured graph: 64 tokens 3.7 in a cluster,
+// 5.8 in one block; 128 tokens 3.9, 4.9 in two launches; 256 tokens 5.1 and 4.9,
+// but 5.6 and 9.3 outside of a graph, where a launch costs the host as much as the
+// kernel takes: the cluster up to there gives up a little in a graph for that.
 constexpr int kRlOneBlockWarps = 32;
 constexpr int kRlOneBlockTokens = 32;
 constexpr uint32_t kRlClusterBlocks = 8;
@@ -727,10 +728,13 @@ bool rows_are_vectors(const void* p, int E, int size) {
 // registers a thread), three with fewer (40). 131072 tokens forward, two and three:
 // 128 experts 60.8 and 64.9 us, 64 experts 67.2 and 49.1, 32 experts 62.7 and 44.9.
 int blocks_per_sm(int E) { return ep_of(E) >= 128 ? 2 : 3; }
+// The backward's (57 registers with 8 experts a lane, 39 with 4). 131072 tokens, two
+// and three: 128 experts 37.8 and 36.3 us, 64 experts 33.0 and 31.4.
+int backward_blocks_per_sm(int E) { return ep_of(E) == 256 ? 2 : 3; }
 
-int blocks_for(int T, int E, int num_sms) {
+int blocks_for(int T, int per_sm, int num_sms) {
   const long long want = ((long long)T + kRlWarps - 1) / kRlWarps;
-  const int most = blocks_per_sm(E) * num_sms;
+  const int most = per_sm * num_sms;
   return (int)(want < most ? want : most);
 }
 
@@ -750,7 +754,8 @@ cudaError_t launch_route_logits(const void* logits, bool is_bf16, const uint8_t*
                                 int top_k, int renorm, int32_t* ids, float* w, int32_t* counts,
                                 float* prob_sums, float* loss, void* workspace, int num_sms,
                                 cudaStream_t st) {
-  int blocks = T <= kRlOneBlockTokens ? 1 : T <= kRlClusterTokens ? 0 : blocks_for(T, E, num_sms);
+  int blocks = T <= kRlOneBlockTokens ? 1
+               : T <= kRlClusterTokens ? 0 : blocks_for(T, blocks_per_sm(E), num_sms);
   if (blocks > max_blocks(E)) blocks = max_blocks(E);
   const int EP = ep_of(E);
   RouteLogitsArgs a = {mask, ids, w, nullptr, nullptr, counts, prob_sums, loss, T, E, top_k, renorm,
@@ -770,7 +775,7 @@ cudaError_t launch_route_logits_backward(const void* logits, bool is_bf16, const
   const RouteLogitsBwdArgs a = {mask, ids, counts, dw, dloss, T, E, top_k, renorm,
                                 rows_are_vectors(logits, E, is_bf16 ? 2 : 4) &&
                                     rows_are_vectors(grad, E, is_bf16 ? 2 : 4)};
-  const int blocks = blocks_for(T, E, num_sms);
+  const int blocks = blocks_for(T, backward_blocks_per_sm(E), num_sms);
   return is_bf16 ? backward_t(static_cast<const uint16_t*>(logits), static_cast<uint16_t*>(grad), a,
                               blocks, st)
                  : backward_t(static_cast<const float*>(logits), static_cast<float*>(grad), a,
