@@ -442,10 +442,11 @@ enum { MM_DTYPE_FP32 = 0, MM_DTYPE_BF16 = 1, MM_DTYPE_FP16 = 2 };
  * the counts, the sums nor the loss, whatever its logits hold (NaN and
  * infinities included); its ids are still distinct and in range. A row whose
  * logits are all -inf is treated as masked. An expert with logit -inf has
- * p = 0 and is selected only when fewer than top_k others remain. A NaN or
- * +inf logit of a counted token makes that row's p NaN, and with it prob_sums
- * and loss. All sums are fp32 in a fixed order: the outputs are the same on
- * every call. topk_ids [T,top_k], topk_w [T,top_k], expert_counts [E],
+ * p = 0 and is selected only when fewer than top_k others remain; NaN ranks as
+ * -inf. A NaN or +inf logit of a counted token makes that row's p NaN, and with
+ * it prob_sums and loss. All sums are fp32 in a fixed order: the outputs are the
+ * same on every call; long sums keep their roundings (some 25 half steps at most,
+ * whatever T). topk_ids [T,top_k], topk_w [T,top_k], expert_counts [E],
  * prob_sums [E], loss [1]. T == 0 writes zero counts, sums and loss.
  *
  * logits need the alignment of their elements only. workspace: at least

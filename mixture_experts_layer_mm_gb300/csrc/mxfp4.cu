@@ -14,7 +14,7 @@
 // memory: 256 x 768 x 2048 bf16 values take 164 us to quantise (1.02 GB, 6.2
 // TB/s) and 145 us to decode (7.0 TB/s). At 4096 tokens of 2048 values, 8 slots
 // each, the experts' grouping takes 7 us, the rows 15 (17 MB read, 35 MB
-// written, 32768 atomics), the weighted sum 24 (154 MB).
+// written, 32768 atomics), the weighted sum 45 (268 MB of fp32 rows, 6.2 TB/s).
 #include "mm.h"
 #include "mm_internal.h"
 #include "mx_device.cuh"

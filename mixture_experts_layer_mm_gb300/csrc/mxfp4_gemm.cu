@@ -17,22 +17,23 @@
 // The products of two e2m1 values and two powers of two are exact; the
 // accumulation is in fp32 in tensor memory.
 //
-// gate_up's blocks run along the output columns, which are the
-// lanes of tensor memory. The weight tile's rows are loaded in an order (row 4 a
+// gate_up's blocks run along the output columns, which are the lanes of tensor
+// memory. The weight tile's rows are loaded in an order (row 4 a
 // + j of a group of 32 at place 8 j + a) that gives a thread of a 16 x 256-bit
 // tensor-memory load four consecutive columns of a token row: a block's maximum
 // is three maxima in the thread and three exchanges for two rows at once, and
-// results leave the thread as they are. (A warp reduction for every column took
-// 90 us for gate_up and 93 for down at 4096 tokens, a transpose through shared
-// memory, whose bandwidth the MMAs need, 63 and 100; this 62 and 60.) The
-// activation is quantised from the fp32 product and is rounded once.
+// results leave the thread as they are. (For gate_up at 4096 tokens a warp
+// reduction for every column took 90 us, a transpose through shared memory, whose
+// bandwidth the MMAs need, 63; this 62.) The activation is quantised from the fp32
+// product and is rounded once; y stays fp32 (70 us for down, 268 MB of y).
 //
-// What bounds it, on one GB300: 8192 x 4096 x 4096 takes 54 us (5.1 PFLOP/s).
+// What bounds it, on one GB300: 8192 x 4096 x 4096 takes 56 us (4.9 PFLOP/s).
 // One stage of a tile alone on the chip takes 580 cycles, its 8 MMAs and 8
 // scale copies the tensor pipe's 576; with all SMs at work 640, as the 52 KB of
 // a stage come at 80 bytes a cycle and SM, 14 TB/s out of L2. Few tiles (64 x
-// 4096 x 4096, 6.9 us) are bound by what one SM takes in, 90 bytes a cycle. Few
-// rows per expert (64 tokens) are bound by the weights' bytes.
+// 4096 x 4096, 6.8 us on 32 of the SMs) take in 416 KB a tile at some 90 bytes a
+// cycle, 2.5 us; the launch, the prologue and the epilogue are the rest. Few rows
+// per expert (64 tokens) are bound by the weights' bytes.
 #include <algorithm>
 
 #include "mm.h"
