@@ -549,6 +549,131 @@ int mm_moe_experts_mxfp4(const uint16_t* hidden, const int32_t* topk_ids, const 
 /* Bytes of workspace mm_moe_experts_mxfp4 needs (-1 for invalid sizes). Host-only. */
 int64_t mm_moe_experts_mxfp4_workspace_size(int T, int H, int E, int I, int top_k);
 
+/*
+ * Training the routed experts. The router's part is mm_route_logits and its
+ * gradient; these are the experts', one call a step:
+ *
+ *   forward                                     backward
+ *   mm_group_slots      places, offsets         mm_dispatch_rows    d_out by slot
+ *   mm_dispatch_rows    token rows by slot      mm_grouped_product_dx    da (down)
+ *   mm_grouped_product  z (gate_up)             mm_swiglu_pack_backward  dz, a, d_topk_w by row
+ *   mm_swiglu_pack      a, and z in 8 bits      mm_grouped_product_dw    both weights'
+ *   mm_grouped_product  y (down)                mm_grouped_product_dx    dx (gate_up)
+ *   mm_combine_rows     out, weighted           mm_combine_rows     d_hidden, d_topk_w
+ *
+ * Rows are 16-bit floats, dtype MM_DTYPE_BF16 or MM_DTYPE_FP16 (MM_DTYPE_FP32:
+ * MM_ERR_UNSUPPORTED), contiguous, 16-byte aligned. Sums are fp32 and every
+ * result is rounded once. All results are the same on every call. Nothing is
+ * kept between calls; calls with distinct results and workspaces may overlap.
+ */
+
+/*
+ * Slots by expert: a stable counting sort of the slots f = t*top_k + j by
+ * topk_ids[f]. places[f] is the slot's row, offsets[e] the first row of expert
+ * e, offsets[E] the number of rows in use. Segments are not padded. Slots of a
+ * token whose token_mask byte is 0 (token_mask [T] or NULL) have no row: place
+ * -1, whatever their ids. Ids outside [0,E) of other tokens have none either
+ * and flag MM_ERR_DEVICE. An id may be repeated within a token.
+ *
+ * topk_ids, places [T,top_k] int32, offsets [E+1] int32; 1 <= E <= 256,
+ * 1 <= top_k <= 32 (it may exceed E), T*top_k < 2^31. workspace: at least
+ * mm_group_slots_workspace_size(T, top_k, E) bytes, 16-byte aligned (NULL if
+ * that is 0). T == 0 writes zero offsets.
+ */
+int mm_group_slots(const int32_t* topk_ids, const uint8_t* token_mask, int T, int top_k, int E,
+                   int32_t* places, int32_t* offsets, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Bytes of workspace mm_group_slots needs (-1 for invalid sizes). Host-only. */
+int64_t mm_group_slots_workspace_size(int T, int top_k, int E);
+
+/*
+ * rows[places[t,j]] = x[t] for every slot with a row, and row_w[places[t,j]] =
+ * topk_w[t,j] where topk_w and row_w are given (both or neither). Rows that no
+ * place names stay as they are. x [T,H], rows [R,H], topk_w [T,top_k] fp32,
+ * row_w [R] fp32; H % 8 == 0. places: distinct but for -1 (of two slots with
+ * one place either may be written); a place outside [-1,R) is taken as -1 and
+ * flags MM_ERR_DEVICE. T == 0 is a no-op.
+ */
+int mm_dispatch_rows(const void* x, int dtype, const int32_t* places, const float* topk_w, int T,
+                     int top_k, int H, int R, void* rows, float* row_w, void* stream);
+
+/*
+ * out[t] = sum_j topk_w[t,j] * rows[places[t,j]] over the slots with a row, in
+ * slot order (topk_w NULL: weights of 1; no slot: zeros). With row_values [R]
+ * and values [T,top_k] (both or neither): values[t,j] = row_values[places[t,j]],
+ * 0 without a row. Rows that no place names are not read. Places and sizes as in
+ * mm_dispatch_rows; one place may be named by several slots.
+ */
+int mm_combine_rows(const void* rows, int dtype, const int32_t* places, const float* topk_w,
+                    const float* row_values, int T, int top_k, int H, int R, void* out,
+                    float* values, void* stream);
+
+/*
+ * y[r,:] = W[e] x[r,:] for the rows r in [offsets[e], offsets[e+1]) of every
+ * expert e. x [R,K], w [E,N,K], y [R,N], all of dtype; offsets [E+1] int32 on
+ * the device, ascending, within [0,R] (segments of any length, 0 among them;
+ * else nothing is written and MM_ERR_DEVICE is flagged). Rows outside the
+ * segments are neither used nor written. N, K multiples of 8, R >= 0, 1 <= E <=
+ * 256; N, K <= 2^20, R < 2^31 - 4096 (else MM_ERR_UNSUPPORTED). R == 0: no-op.
+ */
+int mm_grouped_product(const void* x, const void* w, int dtype, const int32_t* offsets, int R,
+                       int E, int N, int K, void* y, void* stream);
+
+/* dx[r,:] = W[e]^T dy[r,:]: dy [R,N], w [E,N,K], dx [R,K]; otherwise as above. */
+int mm_grouped_product_dx(const void* dy, const void* w, int dtype, const int32_t* offsets, int R,
+                          int E, int N, int K, void* dx, void* stream);
+
+/*
+ * dw[e] = sum of dy[r,:] x[r,:]^T over the rows of expert e (zeros without
+ * rows), added to what dw holds if accumulate != 0. dy [R,N], x [R,K] of dtype;
+ * dw [E,N,K] of dw_dtype: MM_DTYPE_FP32 or the same as dtype. Rows outside the
+ * segments are not used. Otherwise as above; R == 0 writes zeros (accumulate: a
+ * no-op).
+ */
+int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_t* offsets, int R,
+                          int E, int N, int K, void* dw, int dw_dtype, int accumulate,
+                          void* stream);
+
+/*
+ * The SwiGLU of training: act[r,i] = silu(z[r,i]) * z[r,I+i], and z stored in 8
+ * bits for the backward pass: blocks of 32 consecutive columns of a row as
+ * integers q in [-127,127] under one power of two, values q 2^(s - 127),
+ *   s = max(floor(log2 max|z|) - 6, -127) + 127,  q = z 2^(127 - s) to the
+ *   nearest integer, ties to even, beyond 127 to 127 (the OCP MXINT8 form).
+ * A block that holds an infinity or a NaN becomes NaN (s = 255, q = 0).
+ *
+ * z [R,2I] (gate columns first), act [R,I] of dtype; codes [R,2I] int8, scales
+ * [R,2I/32] bytes. I % 32 == 0, R <= 2^31 - 4096, 2I <= 2^20. rows_used (or
+ * NULL): the device address of an int32, such as offsets + E: rows from there
+ * on are neither read nor written. R == 0: no-op.
+ */
+int mm_swiglu_pack(const void* z, int dtype, const int32_t* rows_used, int R, int I, void* act,
+                   int8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * Its gradient at the stored pre-activations z' = (g, u), with a weight row_w[r]
+ * (fp32 [R], NULL: 1) that multiplies the row's activations later on:
+ *   dz[r]      = row_w[r] * d_act[r] * (u silu'(g), silu(g))        [R,2I]
+ *   act[r]     = row_w[r] * silu(g) * u                             [R,I]
+ *   d_row_w[r] = sum_i d_act[r,i] silu(g_i) u_i                     [R] fp32
+ * d_act is the gradient of the weighted activations (for the down product:
+ * W_down^T d_out of the slot's token); with act, dW_down = sum d_out act^T needs
+ * no weight. d_row_w NULL: not computed. Otherwise as mm_swiglu_pack.
+ */
+int mm_swiglu_pack_backward(const int8_t* codes, const uint8_t* scales, const void* d_act,
+                            int dtype, const float* row_w, const int32_t* rows_used, int R, int I,
+                            void* dz, void* act, float* d_row_w, void* stream);
+
+/*
+ * The values [rows,K] of stored 8-bit rows (codes [rows,K], scales [rows,K/32]),
+ * of any MM_DTYPE: exact in fp32 and bf16 for what mm_swiglu_pack writes; fp16
+ * rounds, beyond its range to infinity or zero. K % 32 == 0, K <= 2^20, rows <=
+ * 2^31 - 4096.
+ */
+int mm_mxint8_dequantize(const int8_t* codes, const uint8_t* scales, int rows, int K, void* out,
+                         int dtype, void* stream);
+
 /* Frees the internal workspaces of every device. Not thread-safe with calls in flight. */
 void mm_shutdown(void);
 

@@ -68,6 +68,16 @@ SIGNATURES = {
     "mm_moe_experts_mxfp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ,
                                   _P]),
     "mm_moe_experts_mxfp4_workspace_size": (_I64, [_I, _I, _I, _I, _I]),
+    "mm_group_slots": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "mm_group_slots_workspace_size": (_I64, [_I, _I, _I]),
+    "mm_dispatch_rows": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "mm_combine_rows": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "mm_grouped_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
+    "mm_grouped_product_dx": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
+    "mm_grouped_product_dw": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P]),
+    "mm_swiglu_pack": (_I, [_P, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "mm_swiglu_pack_backward": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "mm_mxint8_dequantize": (_I, [_P, _P, _I, _I, _P, _I, _P]),
     "mm_shutdown": (None, []),
 }
 
@@ -800,6 +810,227 @@ def mm_moe_experts_mxfp4(hidden, topk_ids, topk_w, w_gate_up, w_gate_up_scales, 
         ws = workspace.data_ptr()
     on.launch(l.mm_moe_experts_mxfp4, x, ids, w, gu, sgu, dn, sdn, T, H, E, I, k, outp, ws,
               workspace.numel())
+    return out
+
+
+def _rows_dtype(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _dims(t, n: int, name: str):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _result(on: _On, given, shape, dtype, name: str, like) -> torch.Tensor:
+    """`given` as a result of that shape and type, or a new tensor."""
+    if given is None:
+        return on.empty(shape, dtype)
+    _ptr(given, dtype, name)
+    _shape(given, tuple(shape), name)
+    _device(on.name, like, given)
+    return given
+
+
+def mm_group_slots_workspace_size(T: int, top_k: int, E: int) -> int:
+    return int(lib().mm_group_slots_workspace_size(T, top_k, E))
+
+
+def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
+    """Slots by expert: topk_ids [T, k] int32 -> (places int32 [T, k], offsets
+    int32 [E + 1]). places[t, j] is the slot's row among all slots sorted by
+    expert (stable), -1 for tokens that token_mask [T] (bool or uint8) drops;
+    the rows of expert e are offsets[e] .. offsets[e + 1] - 1."""
+    T, k = _dims(topk_ids, 2, "topk_ids")
+    ids, mask = _ptr(topk_ids, torch.int32, "topk_ids"), _mask_ptr(token_mask, T)
+    _device("mm_group_slots", topk_ids, token_mask)
+    l = lib()
+    need = l.mm_group_slots_workspace_size(T, k, E)
+    if E <= 0 or k == 0:
+        raise MMError(MM_ERR_INVALID_ARG, "mm_group_slots")
+    if need < 0:
+        raise MMError(MM_ERR_UNSUPPORTED, "mm_group_slots")
+    on = _On("mm_group_slots", topk_ids, stream)
+    places, offsets = on.empty((T, k), torch.int32), on.empty((E + 1,), torch.int32)
+    ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
+    on.launch(l.mm_group_slots, ids, mask, T, k, E, places.data_ptr(), offsets.data_ptr(),
+              None if ws is None else ws.data_ptr(), need)
+    return places, offsets
+
+
+def mm_dispatch_rows(x, places, w=None, rows=None, row_w=None, stream=None):
+    """Token rows x [T, H] (bfloat16 or float16) to their slots' rows. Returns
+    (rows [R, H], row_w fp32 [R], None without w [T, k] fp32). rows and row_w:
+    results to write into (R rows; default T * k); rows that no place names stay
+    as they are there, and are undefined in new tensors."""
+    dt = _rows_dtype(x, "x")
+    T, H = _dims(x, 2, "x")
+    k = _dims(places, 2, "places")[1]
+    _shape(places, (T, k), "places")
+    _shape(w, (T, k), "w")
+    xp, pp, wp = (_ptr(x, x.dtype, "x"), _ptr(places, torch.int32, "places"),
+                  _ptr(w, torch.float32, "w"))
+    _device("mm_dispatch_rows", x, places, w)
+    if w is None and row_w is not None:
+        raise ValueError("row_w needs w")
+    R = T * k if rows is None else _dims(rows, 2, "rows")[0]
+    on = _On("mm_dispatch_rows", x, stream)
+    rows = _result(on, rows, (R, H), x.dtype, "rows", x)
+    if w is not None:
+        row_w = _result(on, row_w, (R,), torch.float32, "row_w", x)
+    on.launch(lib().mm_dispatch_rows, xp, dt, pp, wp, T, k, H, R, rows.data_ptr(),
+              None if row_w is None else row_w.data_ptr())
+    return rows, row_w
+
+
+def mm_combine_rows(rows, places, w=None, row_values=None, out=None, stream=None):
+    """out [T, H] = the sum of a token's rows (weighted by w [T, k] fp32 if
+    given). With row_values [R] fp32 returns (out, values [T, k]) where
+    values[t, j] is the value of the slot's row (0 without one)."""
+    dt = _rows_dtype(rows, "rows")
+    R, H = _dims(rows, 2, "rows")
+    T, k = _dims(places, 2, "places")
+    _shape(w, (T, k), "w")
+    _shape(row_values, (R,), "row_values")
+    rp, pp = _ptr(rows, rows.dtype, "rows"), _ptr(places, torch.int32, "places")
+    wp, vp = _ptr(w, torch.float32, "w"), _ptr(row_values, torch.float32, "row_values")
+    _device("mm_combine_rows", rows, places, w, row_values)
+    on = _On("mm_combine_rows", rows, stream)
+    out = _result(on, out, (T, H), rows.dtype, "out", rows)
+    values = None if row_values is None else on.empty((T, k), torch.float32)
+    on.launch(lib().mm_combine_rows, rp, dt, pp, wp, vp, T, k, H, R, out.data_ptr(),
+              None if values is None else values.data_ptr())
+    return out if values is None else (out, values)
+
+
+def _product(name: str, x, w, offsets, out, stream, transposed: bool):
+    dt = _rows_dtype(x, "dy" if transposed else "x")
+    E, N, K = _dims(w, 3, "w")
+    R = _dims(x, 2, "dy" if transposed else "x")[0]
+    _shape(x, (R, N if transposed else K), "dy" if transposed else "x")
+    _shape(offsets, (E + 1,), "offsets")
+    xp, wp, op = (_ptr(x, x.dtype, "x"), _ptr(w, x.dtype, "w"),
+                  _ptr(offsets, torch.int32, "offsets"))
+    _device(name, x, w, offsets)
+    on = _On(name, x, stream)
+    out = _result(on, out, (R, K if transposed else N), x.dtype, "out", x)
+    on.launch(getattr(lib(), name), xp, wp, dt, op, R, E, N, K, out.data_ptr())
+    return out
+
+
+def mm_grouped_product(x, w, offsets, out=None, stream=None):
+    """y [R, N]: y[r] = w[e] x[r] for the rows r of expert e (offsets[e] ..
+    offsets[e + 1] - 1). x [R, K], w [E, N, K] (both bfloat16 or float16), offsets
+    [E + 1] int32. Rows outside the segments are not written."""
+    return _product("mm_grouped_product", x, w, offsets, out, stream, False)
+
+
+def mm_grouped_product_dx(dy, w, offsets, out=None, stream=None):
+    """The gradient of mm_grouped_product's rows: dx [R, K], dx[r] = w[e]^T dy[r]."""
+    return _product("mm_grouped_product_dx", dy, w, offsets, out, stream, True)
+
+
+def mm_grouped_product_dw(dy, x, offsets, out=None, out_dtype=None, accumulate: bool = False,
+                          stream=None):
+    """The gradient of mm_grouped_product's weights: dw [E, N, K], dw[e] = sum of
+    dy[r] x[r]^T over the rows of expert e, of out_dtype (dy's, the default, or
+    float32). accumulate: added to what `out` holds."""
+    dt = _rows_dtype(dy, "dy")
+    R, N = _dims(dy, 2, "dy")
+    K = _dims(x, 2, "x")[1]
+    _shape(x, (R, K), "x")
+    E = _dims(offsets, 1, "offsets")[0] - 1
+    yp, xp, op = (_ptr(dy, dy.dtype, "dy"), _ptr(x, dy.dtype, "x"),
+                  _ptr(offsets, torch.int32, "offsets"))
+    _device("mm_grouped_product_dw", dy, x, offsets)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out_dtype is None:
+        out_dtype = dy.dtype if out is None else out.dtype
+    if out_dtype not in (dy.dtype, torch.float32):
+        raise TypeError(f"out_dtype must be {dy.dtype} or float32, got {out_dtype}")
+    if E <= 0 or N % 8 or K % 8 or not N or not K:  # before a result is allocated
+        raise MMError(MM_ERR_UNSUPPORTED if E > 0 and N and K else MM_ERR_INVALID_ARG,
+                      "mm_grouped_product_dw")
+    on = _On("mm_grouped_product_dw", dy, stream)
+    out = _result(on, out, (E, N, K), out_dtype, "out", dy)
+    on.launch(lib().mm_grouped_product_dw, yp, xp, dt, op, R, E, N, K, out.data_ptr(),
+              _DTYPES[out_dtype], 1 if accumulate else 0)
+    return out
+
+
+def _rows_end(offsets):
+    """The address of the number of rows in use: the last of `offsets`."""
+    if offsets is None:
+        return None
+    n = _dims(offsets, 1, "offsets")[0]
+    if n == 0:
+        raise ValueError("offsets must not be empty")
+    return _ptr(offsets, torch.int32, "offsets") + 4 * (n - 1)
+
+
+def mm_swiglu_pack(z, offsets=None, stream=None):
+    """The SwiGLU of z [R, 2I] (gate columns first; bfloat16 or float16), and z in
+    8 bits for mm_swiglu_pack_backward. Returns (act [R, I], codes int8 [R, 2I],
+    scales uint8 [R, 2I / 32]). offsets int32 [E + 1]: only the rows before its
+    last value are used and written."""
+    dt = _rows_dtype(z, "z")
+    R, C = _dims(z, 2, "z")
+    zp, end = _ptr(z, z.dtype, "z"), _rows_end(offsets)
+    _device("mm_swiglu_pack", z, offsets)
+    if C % 64 != 0 or C == 0:
+        raise MMError(MM_ERR_UNSUPPORTED if C else MM_ERR_INVALID_ARG, "mm_swiglu_pack")
+    on = _On("mm_swiglu_pack", z, stream)
+    act, codes, scales = (on.empty((R, C // 2), z.dtype), on.empty((R, C), torch.int8),
+                          on.empty((R, C // 32), torch.uint8))
+    on.launch(lib().mm_swiglu_pack, zp, dt, end, R, C // 2, act.data_ptr(), codes.data_ptr(),
+              scales.data_ptr())
+    return act, codes, scales
+
+
+def mm_swiglu_pack_backward(codes, scales, d_act, row_w=None, offsets=None, stream=None):
+    """The gradient of mm_swiglu_pack at the stored pre-activations: returns (dz
+    [R, 2I], act [R, I], d_row_w [R] fp32) of d_act's type. row_w [R] fp32: a weight
+    that multiplies the row's activations later on; dz and act are weighted by it,
+    and d_row_w is its gradient (None without row_w)."""
+    dt = _rows_dtype(d_act, "d_act")
+    R, I = _dims(d_act, 2, "d_act")
+    _shape(codes, (R, 2 * I), "codes")
+    _shape(scales, (R, 2 * I // 32), "scales")
+    _shape(row_w, (R,), "row_w")
+    cp, sp, dp = (_ptr(codes, torch.int8, "codes"), _ptr(scales, torch.uint8, "scales"),
+                  _ptr(d_act, d_act.dtype, "d_act"))
+    wp, end = _ptr(row_w, torch.float32, "row_w"), _rows_end(offsets)
+    _device("mm_swiglu_pack_backward", codes, scales, d_act, row_w, offsets)
+    if I % 32 != 0 or I == 0:
+        raise MMError(MM_ERR_UNSUPPORTED if I else MM_ERR_INVALID_ARG, "mm_swiglu_pack_backward")
+    on = _On("mm_swiglu_pack_backward", codes, stream)
+    dz, act = on.empty((R, 2 * I), d_act.dtype), on.empty((R, I), d_act.dtype)
+    d_row_w = None if row_w is None else on.empty((R,), torch.float32)
+    on.launch(lib().mm_swiglu_pack_backward, cp, sp, dp, dt, wp, end, R, I, dz.data_ptr(),
+              act.data_ptr(), None if d_row_w is None else d_row_w.data_ptr())
+    return dz, act, d_row_w
+
+
+def mm_mxint8_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
+    """The values [rows, K] of 8-bit rows (codes int8 [rows, K], scales uint8
+    [rows, K / 32]) as mm_swiglu_pack stores them."""
+    rows, K = _dims(codes, 2, "codes")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    cp, sp = _ptr(codes, torch.int8, "codes"), _ptr(scales, torch.uint8, "scales")
+    if K % 32 != 0 or K == 0:
+        raise MMError(MM_ERR_UNSUPPORTED if K else MM_ERR_INVALID_ARG, "mm_mxint8_dequantize")
+    _shape(scales, (rows, K // 32), "scales")
+    _device("mm_mxint8_dequantize", codes, scales)
+    on = _On("mm_mxint8_dequantize", codes, stream)
+    out = on.empty((rows, K), dtype)
+    on.launch(lib().mm_mxint8_dequantize, cp, sp, rows, K, out.data_ptr(), _DTYPES[dtype])
     return out
 
 

@@ -305,4 +305,38 @@ cudaError_t launch_mx_experts_down(const uint8_t* act, const uint8_t* act_scales
                                    const int32_t* ids, int T, int top_k, int E, int H, int I, long long capacity, long long max_chunks,
                                    float* y, int num_sms, unsigned* err, bool after_prev, cudaStream_t st);
 
+// Training the experts. Rows are 16-bit floats (fp16, else bf16), 16-byte aligned;
+// `end` (or NULL: all R) the device address of the number of rows in use.
+//
+// Token rows and their experts' segments (expert_rows.cu): H % 8 == 0.
+long long group_slots_workspace(long long n, int E);
+cudaError_t launch_group_slots(const int32_t* ids, const uint8_t* mask, int T, int top_k, int E,
+                               int32_t* places, int32_t* offsets, void* workspace, unsigned* err,
+                               cudaStream_t st);
+cudaError_t launch_dispatch_rows(const void* x, const int32_t* places, const float* w, int T,
+                                 int top_k, int H, long long R, void* rows, float* row_w,
+                                 unsigned* err, cudaStream_t st);
+cudaError_t launch_combine_rows(const void* rows, bool fp16, const int32_t* places, const float* w,
+                                const float* row_values, int T, int top_k, int H, long long R,
+                                void* out, float* values, unsigned* err, cudaStream_t st);
+// Products by expert (grouped_product.cu): N % 8 == 0, K % 8 == 0, R > 0.
+// transposed: out [R, K] = rows of x [R, N] times W[e] [N, K], else out [R, N] = rows
+// of x [R, K] times its transpose.
+cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w,
+                                   const int32_t* offsets, int R, int E, int N, int K, bool fp16,
+                                   void* out, int num_sms, unsigned* err, cudaStream_t st);
+cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32_t* offsets, int R,
+                                      int E, int N, int K, bool fp16, void* out, bool out_fp32,
+                                      bool accumulate, int num_sms, unsigned* err,
+                                      cudaStream_t st);
+// The SwiGLU with its pre-activations in 8 bits (swiglu_pack.cu): I % 32 == 0.
+cudaError_t launch_swiglu_pack(const uint16_t* z, bool fp16, const int32_t* end, int R, int I,
+                               uint16_t* act, int8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_swiglu_pack_backward(const int8_t* codes, const uint8_t* scales,
+                                        const uint16_t* da, bool fp16, const float* row_w,
+                                        const int32_t* end, int R, int I, uint16_t* dz,
+                                        uint16_t* act, float* d_row_w, cudaStream_t st);
+cudaError_t launch_i8_dequantize(const int8_t* codes, const uint8_t* scales, long long n,
+                                 void* out, int dtype, cudaStream_t st);
+
 }  // namespace mm

@@ -1,0 +1,364 @@
+// The SwiGLU between the experts' products in training, and its backward pass
+// from pre-activations that were kept in 8 bits.
+//
+//   pack      a = g sigma(g) u of z = (g, u); z stored as 8-bit integers
+//   backward  from the stored z' and the gradient da of a, with a weight w a row:
+//               dg = w da u sigma(g) (1 + g (1 - sigma(g))),  du = w da g sigma(g)
+//               a' = w g sigma(g) u   (again: it was not kept)
+//               dw = sum_i da_i g_i sigma(g_i) u_i
+//
+// The 8 bits (the MXINT8 form of the OCP microscaling formats): blocks of 32
+// columns under one power of two, values q 2^(s - 127), q in [-127, 127], s - 127
+// = floor(log2 max|z|) - 6 but at least -127. The largest value is 64 to 128
+// steps, so a value is off by at most half a step, 2^-7 of the block's largest; for
+// normally distributed values 0.7 % of their size. (Floats of 4 significant bits in
+// the same bytes, e4m3, leave 2.6 %.) Only a value above 127.5 steps is cut to 127.
+// The scaling is exact, so the one rounding is that to an integer. A block with an
+// infinity or a NaN: s = 255, and all of it NaN.
+//
+// A group of 4 to 32 lanes takes a row, 8 columns a lane and step: a block of 32
+// is four lanes, its largest magnitude two exchanges; the sum for dw runs over a
+// lane's steps and then over the lanes, the same on every call. Both kernels read
+// and write every byte once and are bound by memory.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "mm.h"
+#include "mm_internal.h"
+#include "mx_device.cuh"
+
+namespace mm {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kSwThreads = 256;
+constexpr int kSwWarps = kSwThreads / 32;
+
+template <bool FP16>
+__device__ __forceinline__ Pair unpack2(uint32_t w) {
+  if (FP16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return {f.x, f.y};
+  }
+  return {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(Pair v) {
+  if (FP16) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return bf16x2(v.x, v.y);
+}
+
+// Largest magnitude (float32 bits) of 8 values of 16 bits: compared as integers, which
+// puts infinity and NaN on top.
+template <bool FP16>
+__device__ __forceinline__ uint32_t amax8(const uint4& r) {
+  uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu),
+                        __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu));
+  m = max(m >> 16, m & 0xFFFFu);
+  return FP16 ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) : m << 16;
+}
+
+// Scale byte of a block: floor(log2 amax) - 6 + 127, at least 0; 255 for infinity and NaN.
+__device__ __forceinline__ uint32_t i8_scale_byte(uint32_t amax_bits) {
+  const uint32_t be = amax_bits >> 23;  // 0 for zero and subnormals
+  return be == 255u ? 255u : be > 6u ? be - 6u : 0u;
+}
+
+// v 2^(127 - s) to the nearest integer (ties to even) within +-127, in the low byte.
+// Adding 1.5 2^23 leaves integers as the last bit; the product is exact.
+__device__ __forceinline__ uint32_t i8_code(float v, float inv) {
+  constexpr float kMagic = 12582912.f;
+  const float r = __fmaf_rn(v, inv, kMagic);
+  return __float_as_uint(fminf(fmaxf(r, kMagic - 127.f), kMagic + 127.f));
+}
+
+// The codes of 8 values.
+__device__ __forceinline__ uint2 i8_codes(const Pair (&v)[4], uint32_t s) {
+  const float inv = mx_inv_scale(s);
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = __byte_perm(i8_code(v[2 * i].x, inv), i8_code(v[2 * i].y, inv), 0x0040);
+    const uint32_t b =
+        __byte_perm(i8_code(v[2 * i + 1].x, inv), i8_code(v[2 * i + 1].y, inv), 0x0040);
+    w[i] = s == 255u ? 0u : __byte_perm(a, b, 0x5410);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Four codes times `scale`. A code + 128 in the last bits of 2^23 is a float.
+__device__ __forceinline__ void i8_values(uint32_t codes, float scale, Pair& a, Pair& b) {
+  constexpr float kBase = 8388608.f + 128.f;
+  codes ^= 0x80808080u;
+  auto one = [&](uint32_t sel) { return __uint_as_float(__byte_perm(codes, 0x4B000000u, sel)); };
+  const Pair m = {-kBase, -kBase}, s = {scale, scale};
+  a = (Pair{one(0x7440), one(0x7441)} + m) * s;
+  b = (Pair{one(0x7442), one(0x7443)} + m) * s;
+}
+
+// Rows in use: all, or up to the last segment's end.
+__device__ __forceinline__ int rows_used(const int32_t* end, int R) {
+  return end != nullptr ? min(__ldcg(end), R) : R;
+}
+
+// A group's lane and row. LPR: lanes of a row, a power of two.
+struct Place {
+  int row, lane;
+};
+__device__ __forceinline__ Place place_of(int lpr_log2) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Place p;
+  p.lane = lane & ((1 << lpr_log2) - 1);
+  p.row = ((blockIdx.x * kSwWarps + warp) << (5 - lpr_log2)) + (lane >> lpr_log2);
+  return p;
+}
+
+// sigma(g) within 2^-20.5, by the hardware's 2^t and 1 / x, with what the product
+// t = -g log2(e) and that constant round off made up for by a factor. Beyond 200
+// either way the exponential is 0 or infinite, and sigma 1 or 0, whatever g is.
+__device__ __forceinline__ Pair sigmoid(Pair g) {
+  constexpr double kLog2eExact = 1.44269504088896341;
+  constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - kLog2e);
+  constexpr float kLn2 = 0.693147180559945309f;
+  Pair x, e, s;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x.x) : "f"(g.x), "f"(200.f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x.y) : "f"(g.y), "f"(200.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.x) : "f"(x.x), "f"(-200.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.y) : "f"(x.y), "f"(-200.f));
+  const Pair t = x * Pair{-kLog2e, -kLog2e};
+  const Pair off = fma2(x, Pair{kLog2eRest, kLog2eRest}, fma2(x, Pair{kLog2e, kLog2e}, t));
+  const Pair f = fma2(off, Pair{-kLn2, -kLn2}, Pair{1.f, 1.f});
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const Pair d = fma2(e, f, Pair{1.f, 1.f});
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+  return s;
+}
+
+// U: steps whose loads are in flight together.
+template <bool FP16, int U>
+__global__ void __launch_bounds__(kSwThreads)
+    swiglu_pack_kernel(const uint16_t* __restrict__ z, const int32_t* __restrict__ end, int R,
+                       int I, int lpr_log2, uint16_t* __restrict__ act, int8_t* __restrict__ codes,
+                       uint8_t* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const Place p = place_of(lpr_log2);
+  const int step = 8 << lpr_log2;
+  const bool used = p.row < rows_used(end, R);
+  const size_t zr = (size_t)p.row * (2 * I);
+  for (int c0 = p.lane * 8; __any_sync(kAll, c0 < I && used); c0 += U * step) {
+    uint4 g[U], u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      g[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (used && c < I) {
+        g[i] = __ldcs(reinterpret_cast<const uint4*>(z + zr + c));
+        u[i] = __ldcs(reinterpret_cast<const uint4*>(z + zr + I + c));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      uint32_t mg = amax8<FP16>(g[i]), mu = amax8<FP16>(u[i]);
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        mg = max(mg, __shfl_xor_sync(kAll, mg, o));
+        mu = max(mu, __shfl_xor_sync(kAll, mu, o));
+      }
+      if (!used || c >= I) continue;
+      const uint32_t sg = i8_scale_byte(mg), su = i8_scale_byte(mu);
+      const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+      const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      Pair gv[4], uv[4];
+      uint32_t a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        gv[j] = unpack2<FP16>(gw[j]);
+        uv[j] = unpack2<FP16>(uw[j]);
+        a[j] = pack2<FP16>(gv[j] * sigmoid(gv[j]) * uv[j]);
+      }
+      *reinterpret_cast<uint4*>(act + (size_t)p.row * I + c) = make_uint4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<uint2*>(codes + zr + c) = i8_codes(gv, sg);
+      *reinterpret_cast<uint2*>(codes + zr + I + c) = i8_codes(uv, su);
+      if ((c & 31) == 0) {
+        uint8_t* s = scales + (size_t)p.row * (I / 16) + c / 32;
+        s[0] = (uint8_t)sg;
+        s[I / 32] = (uint8_t)su;
+      }
+    }
+  }
+}
+
+template <bool FP16, int U>
+__global__ void __launch_bounds__(kSwThreads)
+    swiglu_unpack_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                         const uint16_t* __restrict__ da, const float* __restrict__ row_w,
+                         const int32_t* __restrict__ end, int R, int I, int lpr_log2,
+                         uint16_t* __restrict__ dz, uint16_t* __restrict__ act,
+                         float* __restrict__ d_row_w) {
+  pdl_wait();
+  pdl_trigger();
+  const Place p = place_of(lpr_log2);
+  const int step = 8 << lpr_log2;
+  const bool used = p.row < rows_used(end, R);
+  const size_t zr = (size_t)p.row * (2 * I), ar = (size_t)p.row * I;
+  const uint8_t* sr = scales + (size_t)p.row * (I / 16);
+  const float w = used && row_w != nullptr ? __ldcg(row_w + p.row) : 1.f;
+  const Pair ww = {w, w};
+  float dot = 0.f;
+  for (int c0 = p.lane * 8; used && c0 < I; c0 += U * step) {
+    uint2 g[U], u[U];
+    uint4 d[U];
+    uint32_t sg[U], su[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      if (c < I) {
+        g[i] = __ldcs(reinterpret_cast<const uint2*>(codes + zr + c));
+        u[i] = __ldcs(reinterpret_cast<const uint2*>(codes + zr + I + c));
+        d[i] = __ldcs(reinterpret_cast<const uint4*>(da + ar + c));
+        sg[i] = __ldcg(sr + c / 32);
+        su[i] = __ldcg(sr + I / 32 + c / 32);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      if (c >= I) break;
+      const float fg = mx_scale(sg[i]), fu = mx_scale(su[i]);
+      Pair gv[4], uv[4];
+      i8_values(g[i].x, fg, gv[0], gv[1]);
+      i8_values(g[i].y, fg, gv[2], gv[3]);
+      i8_values(u[i].x, fu, uv[0], uv[1]);
+      i8_values(u[i].y, fu, uv[2], uv[3]);
+      const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+      uint32_t og[4], ou[4], oa[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Pair dv = unpack2<FP16>(dw[j]);
+        const Pair s = sigmoid(gv[j]);
+        const Pair silu = gv[j] * s, a = silu * uv[j], wd = ww * dv;
+        // sigma (1 + g (1 - sigma)); 1 - sigma is off by 2^-23 where it is small, which
+        // the sum with 1 leaves at g 2^-23.
+        const Pair slope = s * fma2(gv[j], fma2(s, Pair{-1.f, -1.f}, Pair{1.f, 1.f}), Pair{1.f, 1.f});
+        dot = __fmaf_rn(dv.x, a.x, dot);
+        dot = __fmaf_rn(dv.y, a.y, dot);
+        og[j] = pack2<FP16>(wd * uv[j] * slope);
+        ou[j] = pack2<FP16>(wd * silu);
+        oa[j] = pack2<FP16>(ww * a);
+      }
+      *reinterpret_cast<uint4*>(dz + zr + c) = make_uint4(og[0], og[1], og[2], og[3]);
+      *reinterpret_cast<uint4*>(dz + zr + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+      *reinterpret_cast<uint4*>(act + ar + c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+    }
+  }
+  if (d_row_w != nullptr) {
+    for (int o = (1 << lpr_log2) >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+    if (used && p.lane == 0) d_row_w[p.row] = dot;
+  }
+}
+
+// 16 values a thread. DT: MM_DTYPE of the result.
+template <int DT>
+__global__ void __launch_bounds__(kSwThreads)
+    i8_dequantize_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                         long long n16, void* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const long long i = (long long)blockIdx.x * kSwThreads + threadIdx.x;
+  if (i >= n16) return;
+  const uint4 q = __ldcs(reinterpret_cast<const uint4*>(codes) + i);
+  const float f = mx_scale(__ldcg(scales + i / 2));
+  Pair v[8];
+  i8_values(q.x, f, v[0], v[1]);
+  i8_values(q.y, f, v[2], v[3]);
+  i8_values(q.z, f, v[4], v[5]);
+  i8_values(q.w, f, v[6], v[7]);
+  if (DT == MM_DTYPE_FP32) {
+    float4* o = static_cast<float4*>(out) + 4 * i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+  } else {
+    uint4* o = static_cast<uint4*>(out) + 2 * i;
+    constexpr bool h = DT == MM_DTYPE_FP16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      o[j] = make_uint4(pack2<h>(v[4 * j]), pack2<h>(v[4 * j + 1]), pack2<h>(v[4 * j + 2]),
+                        pack2<h>(v[4 * j + 3]));
+  }
+}
+
+struct Shape {
+  int lpr_log2, u;
+  unsigned blocks;
+};
+
+// The lanes of a row: a power of two that covers it in one step, at most 32; then
+// the steps whose loads go out together.
+Shape shape_of(int R, int I) {
+  Shape s;
+  s.lpr_log2 = 2;
+  while (s.lpr_log2 < 5 && (8 << s.lpr_log2) < I) ++s.lpr_log2;
+  const int steps = (I + (8 << s.lpr_log2) - 1) / (8 << s.lpr_log2);
+  s.u = std::min(steps, 3);
+  const int rows = kSwWarps << (5 - s.lpr_log2);
+  s.blocks = (unsigned)(((long long)R + rows - 1) / rows);
+  return s;
+}
+
+template <bool FP16>
+cudaError_t pack_as(const uint16_t* z, const int32_t* end, int R, int I, uint16_t* act,
+                    int8_t* codes, uint8_t* scales, cudaStream_t st) {
+  const Shape s = shape_of(R, I);
+  auto k = s.u == 1 ? swiglu_pack_kernel<FP16, 1>
+         : s.u == 2 ? swiglu_pack_kernel<FP16, 2> : swiglu_pack_kernel<FP16, 3>;
+  return launch_k(k, dim3(s.blocks), dim3(kSwThreads), 0, st, true, z, end, R, I, s.lpr_log2, act,
+                  codes, scales);
+}
+
+template <bool FP16>
+cudaError_t unpack_as(const int8_t* codes, const uint8_t* scales, const uint16_t* da,
+                      const float* row_w, const int32_t* end, int R, int I, uint16_t* dz,
+                      uint16_t* act, float* d_row_w, cudaStream_t st) {
+  const Shape s = shape_of(R, I);
+  auto k = s.u == 1 ? swiglu_unpack_kernel<FP16, 1>
+         : s.u == 2 ? swiglu_unpack_kernel<FP16, 2> : swiglu_unpack_kernel<FP16, 3>;
+  return launch_k(k, dim3(s.blocks), dim3(kSwThreads), 0, st, true, codes, scales, da, row_w, end,
+                  R, I, s.lpr_log2, dz, act, d_row_w);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu_pack(const uint16_t* z, bool fp16, const int32_t* end, int R, int I,
+                               uint16_t* act, int8_t* codes, uint8_t* scales, cudaStream_t st) {
+  return fp16 ? pack_as<true>(z, end, R, I, act, codes, scales, st)
+              : pack_as<false>(z, end, R, I, act, codes, scales, st);
+}
+
+cudaError_t launch_swiglu_pack_backward(const int8_t* codes, const uint8_t* scales,
+                                        const uint16_t* da, bool fp16, const float* row_w,
+                                        const int32_t* end, int R, int I, uint16_t* dz,
+                                        uint16_t* act, float* d_row_w, cudaStream_t st) {
+  return fp16 ? unpack_as<true>(codes, scales, da, row_w, end, R, I, dz, act, d_row_w, st)
+              : unpack_as<false>(codes, scales, da, row_w, end, R, I, dz, act, d_row_w, st);
+}
+
+cudaError_t launch_i8_dequantize(const int8_t* codes, const uint8_t* scales, long long n,
+                                 void* out, int dtype, cudaStream_t st) {
+  const long long n16 = n / 16;
+  auto k = dtype == MM_DTYPE_FP32   ? i8_dequantize_kernel<MM_DTYPE_FP32>
+           : dtype == MM_DTYPE_BF16 ? i8_dequantize_kernel<MM_DTYPE_BF16>
+                                    : i8_dequantize_kernel<MM_DTYPE_FP16>;
+  return launch_k(k, dim3((unsigned)((n16 + kSwThreads - 1) / kSwThreads)), dim3(kSwThreads), 0, st,
+                  true, codes, scales, n16, out);
+}
+
+}  // namespace mm
