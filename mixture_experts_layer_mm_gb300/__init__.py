@@ -19,6 +19,7 @@ from ._lib import (  # noqa: F401
     mm_moe_experts_mxfp4_workspace_size, mm_mxfp4_dequantize, mm_mxfp4_gemm, mm_mxfp4_quantize,
     mm_mxfp4_scales_shape, mm_route_logits, mm_route_logits_backward, mxfp4_tile_scales,
     mm_combine_rows, mm_dispatch_rows, mm_group_slots, mm_group_slots_workspace_size,
-    mm_grouped_product, mm_grouped_product_dw, mm_grouped_product_dx, mm_mxint8_dequantize,
+    mm_grouped_product, mm_grouped_product_dw, mm_grouped_product_dw_workspace_size,
+    mm_grouped_product_dx, mm_mxint8_dequantize,
     mm_swiglu_pack, mm_swiglu_pack_backward,
 )

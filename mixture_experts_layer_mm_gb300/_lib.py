@@ -74,7 +74,8 @@ SIGNATURES = {
     "mm_combine_rows": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "mm_grouped_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
     "mm_grouped_product_dx": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
-    "mm_grouped_product_dw": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P]),
+    "mm_grouped_product_dw": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P, _SZ, _P]),
+    "mm_grouped_product_dw_workspace_size": (_I64, [_I, _I, _I, _I]),
     "mm_swiglu_pack": (_I, [_P, _I, _P, _I, _I, _P, _P, _P, _P]),
     "mm_swiglu_pack_backward": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
     "mm_mxint8_dequantize": (_I, [_P, _P, _I, _I, _P, _I, _P]),
@@ -908,6 +909,10 @@ def mm_combine_rows(rows, places, w=None, row_values=None, out=None, stream=None
     return out if values is None else (out, values)
 
 
+def mm_grouped_product_dw_workspace_size(R: int, E: int, N: int, K: int) -> int:
+    return int(lib().mm_grouped_product_dw_workspace_size(R, E, N, K))
+
+
 def _product(name: str, x, w, offsets, out, stream, transposed: bool):
     dt = _rows_dtype(x, "dy" if transposed else "x")
     E, N, K = _dims(w, 3, "w")
@@ -957,10 +962,13 @@ def mm_grouped_product_dw(dy, x, offsets, out=None, out_dtype=None, accumulate: 
     if E <= 0 or N % 8 or K % 8 or not N or not K:  # before a result is allocated
         raise MMError(MM_ERR_UNSUPPORTED if E > 0 and N and K else MM_ERR_INVALID_ARG,
                       "mm_grouped_product_dw")
-    on = _On("mm_grouped_product_dw", dy, stream)
+    l, on = lib(), _On("mm_grouped_product_dw", dy, stream)
     out = _result(on, out, (E, N, K), out_dtype, "out", dy)
-    on.launch(lib().mm_grouped_product_dw, yp, xp, dt, op, R, E, N, K, out.data_ptr(),
-              _DTYPES[out_dtype], 1 if accumulate else 0)
+    need = max(l.mm_grouped_product_dw_workspace_size(R, E, N, K), 0)
+    ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
+    on.launch(l.mm_grouped_product_dw, yp, xp, dt, op, R, E, N, K, out.data_ptr(),
+              _DTYPES[out_dtype], 1 if accumulate else 0, None if ws is None else ws.data_ptr(),
+              need)
     return out
 
 

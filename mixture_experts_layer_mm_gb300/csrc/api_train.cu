@@ -141,9 +141,14 @@ int mm_grouped_product_dx(const void* dy, const void* w, int dtype, const int32_
   return product(true, dy, w, dtype, offsets, R, E, N, K, dx, stream);
 }
 
+int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K) {
+  if (check_product(MM_DTYPE_BF16, R, E, N, K) != MM_OK) return -1;
+  return R == 0 ? 0 : (int64_t)grouped_product_dw_workspace(R, E, N, K);
+}
+
 int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_t* offsets, int R,
                           int E, int N, int K, void* dw, int dw_dtype, int accumulate,
-                          void* stream) {
+                          void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_product(dtype, R, E, N, K);
   if (rc != MM_OK) return rc;
   if (dw_dtype != MM_DTYPE_FP32 && dw_dtype != dtype)
@@ -157,12 +162,15 @@ int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_
     const size_t bytes = (size_t)E * N * K * (dw_dtype == MM_DTYPE_FP32 ? 4 : 2);
     return cuda_status(cudaMemsetAsync(dw, 0, bytes, on(stream)));
   }
+  const long long need = grouped_product_dw_workspace(R, E, N, K);
+  if (!aligned(workspace, 16) || (need > 0 && !workspace)) return MM_ERR_INVALID_ARG;
+  if ((long long)workspace_bytes < need) return MM_ERR_NO_MEMORY;
   int sms = 0;
   unsigned* status = nullptr;
   if ((rc = current_device_info(&sms, &status)) != MM_OK) return rc;
-  return cuda_status(launch_grouped_product_dw(dy, x, offsets, R, E, N, K, dtype == MM_DTYPE_FP16,
-                                               dw, dw_dtype == MM_DTYPE_FP32, accumulate != 0, sms,
-                                               status, on(stream)));
+  return cuda_status(launch_grouped_product_dw(
+      dy, x, offsets, R, E, N, K, dtype == MM_DTYPE_FP16, dw, dw_dtype == MM_DTYPE_FP32,
+      accumulate != 0, workspace, sms, status, on(stream)));
 }
 
 int mm_swiglu_pack(const void* z, int dtype, const int32_t* rows_used, int R, int I, void* act,

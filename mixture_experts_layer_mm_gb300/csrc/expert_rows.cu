@@ -255,14 +255,7 @@ __global__ void __launch_bounds__(256)
     }
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (FP16) {
-        const __half2 h = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
-        o[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        o[i] = bf16x2(s[2 * i], s[2 * i + 1]);
-      }
-    }
+    for (int i = 0; i < 4; ++i) o[i] = pack16x2(s[2 * i], s[2 * i + 1], FP16);
     out[t * chunks + c] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }

@@ -679,6 +679,24 @@ bool make_tensor_map_sw128(CUtensorMap* m, const void* base, uint32_t rank,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t batch,
+                          uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const uint32_t el = dtype == MM_DTYPE_FP32 ? 4 : 2;
+  cuuint64_t dims[3] = {cols, rows, batch};
+  cuuint64_t strides[2] = {cols * el, cols * rows * el};
+  cuuint32_t box[3] = {128 / el, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m,
+            dtype == MM_DTYPE_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+            : dtype == MM_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tensor_map_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K,
                            uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();

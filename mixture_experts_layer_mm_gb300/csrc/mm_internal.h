@@ -72,6 +72,42 @@ inline cudaError_t smem_attr_once(DeviceFlags& done, Kern kern, int bytes) {
   return e;
 }
 
+// Launches kern on clusters of two CTAs, behind what the stream runs before it:
+// `max_pairs` of them (what there is to do), or as many as can be resident at once
+// (asked for once per device and kept in `resident`).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pairs(void (*kern)(KArgs...), std::atomic<int> (&resident)[kMaxDevices],
+                                int threads, int smem, long long max_pairs, int num_sms,
+                                cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int dev = current_device();
+  int pairs = resident[dev].load(std::memory_order_relaxed);
+  if (pairs <= 0) {
+    cfg.gridDim = dim3((unsigned)num_sms / 2 * 2, 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs <= 0) {
+      cudaGetLastError();
+      pairs = num_sms / 2;
+    }
+    resident[dev].store(pairs, std::memory_order_relaxed);
+  }
+  if (max_pairs < pairs) pairs = max_pairs < 1 ? 1 : (int)max_pairs;
+  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Device address of the current device's status word (see
 // mm_poll_device_status); sets up the device state on first use.
 int current_status_word(unsigned** out);
@@ -157,6 +193,11 @@ bool make_tensor_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_
 // Elements outside the dimensions read as zeros.
 bool make_tensor_map_sw128(CUtensorMap* m, const void* base, uint32_t rank,
                            const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
+
+// Tensor map of [batch, rows, cols] of an MM_DTYPE, to write in boxes of 128 bytes x
+// box_rows rows with the 128-byte swizzle.
+bool make_tensor_map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t batch,
+                          uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 // Tensor map of 4-bit codes, a row-major [rows, K/2] byte matrix read in boxes
 // of 128 bytes (256 columns) x box_rows rows with the 128-byte swizzle.
@@ -325,10 +366,13 @@ cudaError_t launch_combine_rows(const void* rows, bool fp16, const int32_t* plac
 cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w,
                                    const int32_t* offsets, int R, int E, int N, int K, bool fp16,
                                    void* out, int num_sms, unsigned* err, cudaStream_t st);
+// The gradient of their weights (grouped_product_dw.cu); workspace: as many bytes as
+// grouped_product_dw_workspace gives.
+long long grouped_product_dw_workspace(int R, int E, int N, int K);
 cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32_t* offsets, int R,
                                       int E, int N, int K, bool fp16, void* out, bool out_fp32,
-                                      bool accumulate, int num_sms, unsigned* err,
-                                      cudaStream_t st);
+                                      bool accumulate, void* workspace, int num_sms,
+                                      unsigned* err, cudaStream_t st);
 // The SwiGLU with its pre-activations in 8 bits (swiglu_pack.cu): I % 32 == 0.
 cudaError_t launch_swiglu_pack(const uint16_t* z, bool fp16, const int32_t* end, int R, int I,
                                uint16_t* act, int8_t* codes, uint8_t* scales, cudaStream_t st);

@@ -46,11 +46,7 @@ __device__ __forceinline__ Pair unpack2(uint32_t w) {
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(Pair v) {
-  if (FP16) {
-    const __half2 h = __floats2half2_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return bf16x2(v.x, v.y);
+  return pack16x2(v.x, v.y, FP16);
 }
 
 // Largest magnitude (float32 bits) of 8 values of 16 bits: compared as integers, which
