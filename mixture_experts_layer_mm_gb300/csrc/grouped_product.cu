@@ -67,6 +67,7 @@ struct Segments {
 
 struct GTile {
   int e, m, row0, nrows;
+  bool one;  // the expert's only chunk
 };
 
 __device__ __forceinline__ GTile tile_at(int tile, const ProductArgs& a, const Segments& S) {
@@ -82,6 +83,7 @@ __device__ __forceinline__ GTile tile_at(int tile, const ProductArgs& a, const S
       hi = mid;
   }
   t.e = lo;
+  t.one = S.first[lo + 1] - S.first[lo] == 1;
   t.row0 = S.off[lo] + (ch - S.first[lo]) * S.size[lo];
   t.nrows = min(S.size[lo], S.off[lo + 1] - t.row0);
   return t;
@@ -137,15 +139,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
   for (int i = tid; i < E; i += kGThreads)
     if (S.off[i] < 0 || S.off[i + 1] < S.off[i] || S.off[i + 1] > a.R) S.bad = 1;
   __syncthreads();
+  const bool bad = S.bad != 0;
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
   if (warp == 0) {  // chunks: ceil(rows / 256) near-equal ones for each expert
-    const bool bad = S.bad != 0;
-    if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
-    const int per = (E + 31) / 32, e0 = lane * per;
+    const int per = (E + 31) / 32, e0 = lane * per, e1 = bad ? 0 : min(e0 + per, E);
     int sum = 0;
-    for (int e = e0; e < min(e0 + per, E) && !bad; ++e)
-      sum += (S.off[e + 1] - S.off[e] + kGMaxN - 1) / kGMaxN;
+    for (int e = e0; e < e1; ++e) sum += (S.off[e + 1] - S.off[e] + kGMaxN - 1) / kGMaxN;
     int run = exclusive_sum(sum);
-    for (int e = e0; e < min(e0 + per, E) && !bad; ++e) {
+    for (int e = e0; e < e1; ++e) {
       const int L = S.off[e + 1] - S.off[e], n = (L + kGMaxN - 1) / kGMaxN;
       S.first[e] = run;
       S.size[e] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const uint32_t bytes = kGHalf + (nh > 96 ? kGHalf : (uint32_t)boxes * 32 * kGK * 2);
       const int f = t.m * 256 + (int)rank * 128;
       // W is read by every chunk of the expert, the rows by every m-tile.
-      const uint64_t pol_w = S.first[t.e + 1] - S.first[t.e] > 1 ? pol_normal : pol_once;
+      const uint64_t pol_w = t.one ? pol_once : pol_normal;
       for (int kb = 0; kb < nk; ++kb) {
         const bool mine = q == slot;
         if (++q == kGStages) q = 0;
@@ -354,8 +355,8 @@ cudaError_t launch_way(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUt
       e != cudaSuccess)
     return e;
   static std::atomic<int> resident[kMaxDevices];
-  return launch_pairs(product_kernel<WAY>, resident, kGThreads, kGSmemBytes, max_tiles, num_sms, st,
-                      tmA, tmB, tmB32, a);
+  return launch_clusters(product_kernel<WAY>, 2, resident, kGThreads, kGSmemBytes, max_tiles,
+                         num_sms, st, tmA, tmB, tmB32, a);
 }
 
 // A 2-D matrix [rows, cols] in boxes of 64 columns x box_rows rows, or W [E, rows,

@@ -19,8 +19,8 @@
 // filled ahead, are handed over between the two.
 //
 // Rows beyond a segment belong to another expert: the last stage is cut to whole
-// steps of 16 rows, and where those hold rows of the next segment the producer
-// writes zeros over them, in both operands (0 times another expert's infinity is
+// steps of 16 rows, and where those hold rows of the next segment the issuing
+// warp writes zeros over them, in both operands (0 times another expert's infinity is
 // NaN). Columns beyond a matrix are zeros out of the copy. The results leave
 // through shared memory as boxes of 32 rows x 128 bytes, which the copy cuts at the
 // matrix's edges (stores out of registers, 32 bytes a lane in 32 rows: 302 us where
@@ -61,6 +61,7 @@ constexpr int kStaticBytes = 2000;           // at most: barriers, offsets, part
 static_assert(kSmemBytes <= 227 * 1024 - kStaticBytes, "shared memory");
 constexpr int kAccCols = 256;                // columns of an accumulator, of which there are two
 constexpr int kSliceRows = 512;
+constexpr int kCtas = 2;                     // of a cluster: 128 features n each
 constexpr int kPairs = 76;                   // clusters on the chip, for the choice of parts
 
 struct DwArgs {
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
               const DwArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[3 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, bad_s;
   __shared__ int32_t off_s[kMaxExperts + 1];
@@ -119,19 +120,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int E = a.E;
   const uint32_t rank = pair_rank();
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int pair = blockIdx.x / kCtas, npairs = gridDim.x / kCtas;
 
   uint64_t* full = bars;
   uint64_t* empty = full + kStages;
-  uint64_t* land = empty + kStages;  // the copies of a segment's last stage
-  uint64_t* tfull = land + kStages;
+  uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 2);  // both CTAs' MMAs: either's copies fill both
-      mbar_init(smem_u32(&land[s]), 1);
+      mbar_init(smem_u32(&empty[s]), kCtas);  // every CTA's MMAs: its copies fill all
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
@@ -168,12 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = bad ? 0 : (a.part_rows != 0 ? (int)first_s[E] : E) * per;
   const uint32_t tmem_base = tmem_base_s;
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t peer_abort = peer_addr(smem_u32(&abort_s), rank ^ 1u);
   auto fail = [&]() {
-    *reinterpret_cast<volatile int*>(&abort_s) = 1;
-    st_cluster_u32(peer_abort, 1u);
+    for (int r = 0; r < kCtas; ++r) st_cluster_u32(peer_addr(smem_u32(&abort_s), r), 1u);
     atomicOr(a.err, kDevErrTimeout);
   };
+  constexpr uint16_t all = (1 << kCtas) - 1;
   auto aborted = [&]() {
     return __any_sync(kAll, *reinterpret_cast<volatile int*>(&abort_s) != 0);
   };
@@ -217,20 +215,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = warp - kProd0;
     const bool leader = elect_one();
     const uint32_t st = smem_base + slot * kStageBytes;
-    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]),
-                   lb = smem_u32(&land[slot]);
+    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
     const uint64_t pol = l2_policy_evict_last();  // read by every tile of the expert
-    const int boxes = a.bn / 128;                 // of 64 columns, for this CTA to load
-    const uint32_t bytes = kABytes + 2 * boxes * kBlock;
-    const uint32_t bst = st + kABytes + rank * boxes * kBlock;
-    uint32_t use = 0, landed = 0;
+    const int boxes = a.bn / 64;                  // of 64 columns, loaded by the CTAs in turn
+    const uint32_t bytes = kABytes + boxes * kBlock;
+    uint32_t use = 0;  // fills of this slot so far
     int q = 0;  // stage counter modulo the ring
     bool ok = true;
     for (int i = pair; i < total && ok; i += npairs) {
       if (aborted()) break;
       const Item t = item_at(i);
       const int nsl = slices(t), step = slice_rows(t);
-      const int f = t.m * 256 + (int)rank * 128, c = t.n * a.bn + (int)rank * (a.bn / 2);
+      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * a.bn;
       for (int sl = 0; sl < nsl && ok; ++sl) {
         const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
         for (int kb = 0; kb < nk; ++kb) {
@@ -242,35 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const int left = len - kb * kRows;  // rows of this stage, if fewer than 64
-          const bool tail = left < kRows && (left & 15) != 0;
-          const uint32_t bar = tail ? lb : fb;
           if (leader) {
             const int r = t.row0 + sl * step + kb * kRows;
-            mbar_arrive_expect_tx(bar, bytes);
-            tma_load_2d(st, &tmA, bar, f, r, pol);
-            tma_load_2d(st + kBlock, &tmA, bar, f + 64, r, pol);
-            tma_load_2d_both(bst, &tmB, bar, c, r, pol);
-            if (boxes == 2) tma_load_2d_both(bst + kBlock, &tmB, bar, c + 64, r, pol);
+            mbar_arrive_expect_tx(fb, bytes);
+            tma_load_2d(st, &tmA, fb, f, r, pol);
+            tma_load_2d(st + kBlock, &tmA, fb, f + 64, r, pol);
+            for (int b = rank; b < boxes; b += kCtas)
+              tma_load_2d_all(st + kABytes + b * kBlock, &tmB, fb, c + 64 * b, r, all, pol);
           }
           __syncwarp();
-          if (tail) {
-            if (!warp_wait(lb, landed & 1u)) {
-              fail();
-              ok = false;
-              break;
-            }
-            ++landed;
-            // Rows [left, next multiple of 16) of every block: 128 bytes each.
-            const int n = (16 - (left & 15)) * 8, blocks = 2 + 2 * boxes;
-            for (int b = 0; b < blocks; ++b)
-              for (int j = lane; j < n; j += 32)
-                st_shared_zero16(st + b * kBlock + left * 128 + j * 16);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (leader) mbar_arrive(fb);
-            __syncwarp();
-          }
           ++use;
         }
       }
@@ -314,9 +290,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          const uint32_t st = smem_base + s * kStageBytes;
+          const int left = len - kb * kRows;  // rows of this stage, if fewer than 64
+          if (left < kRows && (left & 15) != 0) {
+            // Rows [left, next multiple of 16) of every block: 128 bytes each. (The MMAs
+            // of the stages before run meanwhile. Straight-line code: in loops it took the
+            // warp 900 cycles, 14 us of 224 for 32768 rows of uneven load.)
+            const uint32_t z = st + (left + (lane >> 3)) * 128 + (lane & 7) * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // four rows at a time
+              if ((left & 15) + (lane >> 3) + 4 * j < 16) {
+#pragma unroll
+                for (int k = 0; k < 6; ++k)
+                  if (k < 4 || a.bn == 256) st_shared_zero16(z + k * kBlock + j * 512);
+              }
+            __syncwarp();
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           tc_fence_after();
           if (leader) {
-            const uint32_t st = smem_base + s * kStageBytes;
             const uint64_t da = sdesc_mnmajor(st, kBlock), db = sdesc_mnmajor(st + kABytes, kBlock);
             const int steps = min(4, (len - kb * kRows + 15) / 16);
             // 16 rows are 128 descriptor units of 16 bytes.
@@ -328,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < steps; ++kk)
                 umma_bf16(d, da + kk * 128, db + kk * 128, idesc, (kb | kk) != 0);
             }
-            umma_commit_both(smem_u32(&empty[s]));
+            umma_commit_all(smem_u32(&empty[s]), all);
           }
           __syncwarp();
           if (++s == kStages) {
@@ -356,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (aborted()) break;
       const Item t = item_at(i);
       const int nsl = slices(t);
-      const int f0 = t.m * 256 + (int)rank * 128 + q * 32;  // this warp's 32 features n
+      const int f0 = (t.m * kCtas + (int)rank) * 128 + q * 32;  // this warp's 32 features n
       const int k0 = t.n * a.bn, k1 = min(k0 + a.bn, a.K);
       const bool fp32 = a.out_fp32 || t.part >= 0;
       // 32 rows of 128 bytes at column c, through this warp's buffer in the 128-byte
@@ -617,8 +610,8 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
   if (cudaError_t e = smem_attr_once(attr_done, dw_kernel, kSmemBytes); e != cudaSuccess) return e;
   static std::atomic<int> resident[kMaxDevices];
   const long long items = s.max_parts * s.m_tiles * s.n_tiles;
-  if (cudaError_t e = launch_pairs(dw_kernel, resident, kThreads, kSmemBytes, items, num_sms, st,
-                                   tmA, tmB, tmC, tmP, a);
+  if (cudaError_t e = launch_clusters(dw_kernel, kCtas, resident, kThreads,
+                                      kSmemBytes, items, num_sms, st, tmA, tmB, tmC, tmP, a);
       e != cudaSuccess || s.part_rows == 0)
     return e;
   const long long blocks = ((long long)N * K / 8 + 255) / 256;

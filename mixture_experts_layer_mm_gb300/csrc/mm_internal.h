@@ -72,20 +72,21 @@ inline cudaError_t smem_attr_once(DeviceFlags& done, Kern kern, int bytes) {
   return e;
 }
 
-// Launches kern on clusters of two CTAs, behind what the stream runs before it:
-// `max_pairs` of them (what there is to do), or as many as can be resident at once
+// Launches kern on clusters of `ctas` CTAs, behind what the stream runs before it:
+// `max_clusters` of them (what there is to do), or as many as can be resident at once
 // (asked for once per device and kept in `resident`).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pairs(void (*kern)(KArgs...), std::atomic<int> (&resident)[kMaxDevices],
-                                int threads, int smem, long long max_pairs, int num_sms,
-                                cudaStream_t st, const Args&... args) {
+inline cudaError_t launch_clusters(void (*kern)(KArgs...), int ctas,
+                                   std::atomic<int> (&resident)[kMaxDevices], int threads,
+                                   int smem, long long max_clusters, int num_sms,
+                                   cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -93,17 +94,17 @@ inline cudaError_t launch_pairs(void (*kern)(KArgs...), std::atomic<int> (&resid
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int dev = current_device();
-  int pairs = resident[dev].load(std::memory_order_relaxed);
-  if (pairs <= 0) {
-    cfg.gridDim = dim3((unsigned)num_sms / 2 * 2, 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs <= 0) {
+  int n = resident[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    cfg.gridDim = dim3((unsigned)num_sms / ctas * ctas, 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
-      pairs = num_sms / 2;
+      n = num_sms / ctas;
     }
-    resident[dev].store(pairs, std::memory_order_relaxed);
+    resident[dev].store(n, std::memory_order_relaxed);
   }
-  if (max_pairs < pairs) pairs = max_pairs < 1 ? 1 : (int)max_pairs;
-  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  if (max_clusters < n) n = max_clusters < 1 ? 1 : (int)max_clusters;
+  cfg.gridDim = dim3((unsigned)(ctas * n), 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }

@@ -108,25 +108,25 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
-// A box at the same place of both CTAs' shared memory, counted on the barrier at the same
-// place of each.
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const void* map, uint32_t bar,
-                                                 int c0, int c1, uint64_t policy) {
+// A box at the same place of the shared memory of every CTA in `mask`, counted on the
+// barrier at the same place of each.
+__device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const void* map, uint32_t bar,
+                                                 int c0, int c1, uint16_t mask, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1),
-      "h"(static_cast<uint16_t>(3)), "l"(policy)
+      "h"(mask), "l"(policy)
       : "memory");
 }
 
-// One arrival on the barrier at `bar` in both CTAs once the MMAs of this CTA issued so
+// One arrival on the barrier at `bar` in every CTA of `mask` once the MMAs of this CTA issued so
 // far by this thread have completed.
-__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+__device__ __forceinline__ void umma_commit_all(uint32_t bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(mask)
       : "memory");
 }
 
