@@ -629,15 +629,15 @@ int mm_grouped_product_dx(const void* dy, const void* w, int dtype, const int32_
  * rows), added to what dw holds if accumulate != 0. dy [R,N], x [R,K] of dtype;
  * dw [E,N,K] of dw_dtype: MM_DTYPE_FP32 or the same as dtype. Rows outside the
  * segments are not used. Otherwise as above; R == 0 writes zeros (accumulate: a
- * no-op). workspace: at least mm_grouped_product_dw_workspace_size(R, E, N, K)
- * bytes, 16-byte aligned (NULL if that is 0).
+ * no-op). workspace: at least mm_grouped_product_dw_workspace_size(R, E, N, K,
+ * dw_dtype) bytes, 16-byte aligned (NULL if that is 0).
  */
 int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_t* offsets, int R,
                           int E, int N, int K, void* dw, int dw_dtype, int accumulate,
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace mm_grouped_product_dw needs (-1 for invalid sizes). Host-only. */
-int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K);
+int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K, int dw_dtype);
 
 /*
  * The SwiGLU of training: act[r,i] = silu(z[r,i]) * z[r,I+i], and z stored in 8

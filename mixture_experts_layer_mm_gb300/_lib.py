@@ -75,7 +75,7 @@ SIGNATURES = {
     "mm_grouped_product": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
     "mm_grouped_product_dx": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P]),
     "mm_grouped_product_dw": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P, _SZ, _P]),
-    "mm_grouped_product_dw_workspace_size": (_I64, [_I, _I, _I, _I]),
+    "mm_grouped_product_dw_workspace_size": (_I64, [_I, _I, _I, _I, _I]),
     "mm_swiglu_pack": (_I, [_P, _I, _P, _I, _I, _P, _P, _P, _P]),
     "mm_swiglu_pack_backward": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
     "mm_mxint8_dequantize": (_I, [_P, _P, _I, _I, _P, _I, _P]),
@@ -909,8 +909,9 @@ def mm_combine_rows(rows, places, w=None, row_values=None, out=None, stream=None
     return out if values is None else (out, values)
 
 
-def mm_grouped_product_dw_workspace_size(R: int, E: int, N: int, K: int) -> int:
-    return int(lib().mm_grouped_product_dw_workspace_size(R, E, N, K))
+def mm_grouped_product_dw_workspace_size(R: int, E: int, N: int, K: int, dtype) -> int:
+    """dtype: of the result."""
+    return int(lib().mm_grouped_product_dw_workspace_size(R, E, N, K, _DTYPES.get(dtype, -1)))
 
 
 def _product(name: str, x, w, offsets, out, stream, transposed: bool):
@@ -964,7 +965,7 @@ def mm_grouped_product_dw(dy, x, offsets, out=None, out_dtype=None, accumulate: 
                       "mm_grouped_product_dw")
     l, on = lib(), _On("mm_grouped_product_dw", dy, stream)
     out = _result(on, out, (E, N, K), out_dtype, "out", dy)
-    need = max(l.mm_grouped_product_dw_workspace_size(R, E, N, K), 0)
+    need = max(l.mm_grouped_product_dw_workspace_size(R, E, N, K, _DTYPES[out_dtype]), 0)
     ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
     on.launch(l.mm_grouped_product_dw, yp, xp, dt, op, R, E, N, K, out.data_ptr(),
               _DTYPES[out_dtype], 1 if accumulate else 0, None if ws is None else ws.data_ptr(),

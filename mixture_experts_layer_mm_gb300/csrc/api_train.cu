@@ -141,9 +141,11 @@ int mm_grouped_product_dx(const void* dy, const void* w, int dtype, const int32_
   return product(true, dy, w, dtype, offsets, R, E, N, K, dx, stream);
 }
 
-int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K) {
-  if (check_product(MM_DTYPE_BF16, R, E, N, K) != MM_OK) return -1;
-  return R == 0 ? 0 : (int64_t)grouped_product_dw_workspace(R, E, N, K);
+int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K, int dw_dtype) {
+  if (check_product(MM_DTYPE_BF16, R, E, N, K) != MM_OK ||
+      (dw_dtype != MM_DTYPE_FP32 && check_dtype(dw_dtype) != MM_OK))
+    return -1;
+  return R == 0 ? 0 : (int64_t)grouped_product_dw_workspace(R, E, N, K, dw_dtype == MM_DTYPE_FP32);
 }
 
 int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_t* offsets, int R,
@@ -162,7 +164,7 @@ int mm_grouped_product_dw(const void* dy, const void* x, int dtype, const int32_
     const size_t bytes = (size_t)E * N * K * (dw_dtype == MM_DTYPE_FP32 ? 4 : 2);
     return cuda_status(cudaMemsetAsync(dw, 0, bytes, on(stream)));
   }
-  const long long need = grouped_product_dw_workspace(R, E, N, K);
+  const long long need = grouped_product_dw_workspace(R, E, N, K, dw_dtype == MM_DTYPE_FP32);
   if (!aligned(workspace, 16) || (need > 0 && !workspace)) return MM_ERR_INVALID_ARG;
   if ((long long)workspace_bytes < need) return MM_ERR_NO_MEMORY;
   int sms = 0;

@@ -26,16 +26,19 @@
 // matrix's edges (stores out of registers, 32 bytes a lane in 32 rows: 302 us where
 // boxes took 273).
 //
-// fp32 results (and parts) take kSliceRows rows of a segment at a time, each slice
-// added to memory in fp32: the tensor cores cut what they add, and 512 rows leave 5e-7
-// of it where 4096 leave 4e-6. 16-bit results are one accumulation.
+// fp32 results (and parts, below) are made of kSliceRows rows of the segment at a time:
+// the tensor cores cut what they add, and 512 rows leave 5e-7 of it where 4096 leave
+// 4e-6. In tiles of 128 columns the slices are summed in the epilogue's registers; in
+// tiles of 256, which do not fit there, they are added up in memory, each after the one
+// before (20011 rows x 8 x 640 x 328: 41 us that way, 30 in registers; but 32768 x 128 x
+// 1536 x 2048, where few segments have a second slice, 313 and 411). 16-bit results are
+// one accumulation.
 //
-// Few tiles with long reductions are cut into parts of `part_rows` rows, whose fp32 results go
-// to the workspace and are summed in order by a second launch (the rule is at
-// split_of).
+// Few tiles with long reductions are cut into parts of `part_rows` rows, whose fp32
+// results go to the workspace and are summed in order by a second launch (the rule is
+// at split_of).
 #include <algorithm>
-
-#include <cuda_fp16.h>
+#include <cmath>
 
 #include "mm.h"
 #include "mm_device.cuh"
@@ -49,16 +52,23 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 64;                    // rows of the reduction a stage
 constexpr int kBlock = kRows * 128;          // 8 KB: 64 rows x 64 columns
-constexpr int kStages = 4;
 constexpr int kABytes = 2 * kBlock;          // this CTA's 128 features n
-constexpr int kStageBytes = kABytes + 4 * kBlock;  // and up to 256 features k
 constexpr int kEpiWarp0 = 1, kEpiWarps = 8;
-constexpr int kProd0 = kEpiWarp0 + kEpiWarps;      // producers: one warp a slot
-constexpr int kThreads = (kProd0 + kStages) * 32;  // 416
+constexpr int kProd0 = kEpiWarp0 + kEpiWarps;  // producers: one warp a slot
 constexpr int kStore = 32 * 128;             // 4 KB a warp: results on their way out
-constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kStore + 1024;
 constexpr int kStaticBytes = 2000;           // at most: barriers, offsets, parts
-static_assert(kSmemBytes <= 227 * 1024 - kStaticBytes, "shared memory");
+
+// The ring: 192 KB of stages in flight, whatever their size. (A stage is under way for
+// some 1.5 us, so few slots bound the rate: 24000 rows x 4 x 512 x 1024 take 30.2 us with 4 slots
+// of narrow stages, 24.7 with 6.)
+template <int BN>
+struct Ring {
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStageBytes = kABytes + BN / 64 * kBlock;
+  static constexpr int kThreads = (kProd0 + kStages) * 32;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kStore + 1024;
+  static_assert(kSmemBytes <= 227 * 1024 - kStaticBytes, "shared memory");
+};
 constexpr int kAccCols = 256;                // columns of an accumulator, of which there are two
 constexpr int kSliceRows = 512;
 constexpr int kCtas = 2;                     // of a cluster: 128 features n each
@@ -70,7 +80,7 @@ struct DwArgs {
   float* parts;            // [parts][N][K] (part_rows != 0)
   unsigned* err;
   int E, R, N, K;
-  int m_tiles, n_tiles, bn;
+  int m_tiles, n_tiles;
   int part_rows;           // 0: segments are whole
   int fp16, out_fp32, accumulate;
 };
@@ -104,11 +114,14 @@ struct Item {
   int part;   // its place in the workspace, -1: the result itself
 };
 
-// tmC: the result, tmP: the parts.
-__global__ void __launch_bounds__(kThreads, 1)
+// BN: features k of a tile. tmC: the result, tmP: the parts.
+template <int BN>
+__global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
     dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
               const DwArgs a) {
+  constexpr int kStages = Ring<BN>::kStages, kStageBytes = Ring<BN>::kStageBytes;
+  constexpr int kThreads = Ring<BN>::kThreads;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_base_s;
@@ -203,7 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t;
   };
   // Slices of an item's reduction, and the rows of one.
-  auto slice_rows = [&](const Item& t) { return a.out_fp32 || t.part >= 0 ? kSliceRows : 1 << 30; };
+  auto slice_rows = [&](const Item& t) {
+    return a.out_fp32 || t.part >= 0 ? kSliceRows : 1 << 30;
+  };
   auto slices = [&](const Item& t) {
     return t.rows == 0 ? 0 : (t.rows - 1) / slice_rows(t) + 1;
   };
@@ -217,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t st = smem_base + slot * kStageBytes;
     const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
     const uint64_t pol = l2_policy_evict_last();  // read by every tile of the expert
-    const int boxes = a.bn / 64;                  // of 64 columns, loaded by the CTAs in turn
+    constexpr int boxes = BN / 64;                  // of 64 columns, loaded by the CTAs in turn
     const uint32_t bytes = kABytes + boxes * kBlock;
     uint32_t use = 0;  // fills of this slot so far
     int q = 0;  // stage counter modulo the ring
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (aborted()) break;
       const Item t = item_at(i);
       const int nsl = slices(t), step = slice_rows(t);
-      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * a.bn;
+      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN;
       for (int sl = 0; sl < nsl && ok; ++sl) {
         const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
         for (int kb = 0; kb < nk; ++kb) {
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loops, so that descriptors stay in uniform
     // registers; one elected lane issues.
     const bool leader = elect_one();
-    const uint32_t idesc = idesc_16(a.fp16 != 0, true, true) | idesc_shape(128, a.bn);
+    const uint32_t idesc = idesc_16(a.fp16 != 0, true, true) | idesc_shape(128, BN);
     int s = 0;
     uint32_t ph = 0, it = 0;
     bool ok = true;
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((left & 15) + (lane >> 3) + 4 * j < 16) {
 #pragma unroll
                 for (int k = 0; k < 6; ++k)
-                  if (k < 4 || a.bn == 256) st_shared_zero16(z + k * kBlock + j * 512);
+                  if (k < 4 || BN == 256) st_shared_zero16(z + k * kBlock + j * 512);
               }
             __syncwarp();
             fence_proxy_async_smem();
@@ -350,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item t = item_at(i);
       const int nsl = slices(t);
       const int f0 = (t.m * kCtas + (int)rank) * 128 + q * 32;  // this warp's 32 features n
-      const int k0 = t.n * a.bn, k1 = min(k0 + a.bn, a.K);
-      const bool fp32 = a.out_fp32 || t.part >= 0;
+      const int k0 = t.n * BN, k1 = min(k0 + BN, a.K);
       // 32 rows of 128 bytes at column c, through this warp's buffer in the 128-byte
       // swizzle; the copy cuts what lies beyond the matrix.
       auto put = [&](int c, bool add, const uint32_t* v) {
@@ -365,91 +379,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (t.part >= 0) {
-            if (add)
-              tma_add_3d(&tmP, buf, c, f0, t.part);
-            else
-              tma_store_3d(&tmP, buf, c, f0, t.part);
-          } else if (add) {
+          if (t.part >= 0)
+            tma_store_3d(&tmP, buf, c, f0, t.part);
+          else if (add)
             tma_add_3d(&tmC, buf, c, f0, t.e);
-          } else {
+          else
             tma_store_3d(&tmC, buf, c, f0, t.e);
-          }
           bulk_commit();
         }
         __syncwarp();
       };
-      if (nsl == 0 && !a.accumulate) {  // an expert without rows
-        const uint32_t zero[32] = {};
-        for (int c = side * (fp32 ? 32 : 64); c < a.bn; c += fp32 ? 64 : 128)
-          put(k0 + c, false, zero);
-      }
-      for (int sl = 0; sl < nsl; ++sl, ++it) {
-        const uint32_t b = it & 1u, use = it >> 1;
-        if (!warp_wait(smem_u32(&tfull[b]), use & 1u)) {
-          fail();
-          ok = false;
-          break;
-        }
+      // Accumulator `b` for slice number `it`: waits for it; the function it returns
+      // hands it back.
+      auto take = [&]() {
+        ok = warp_wait(smem_u32(&tfull[it & 1u]), (it >> 1) & 1u);
+        if (!ok) fail();
         tc_fence_after();
-        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + b * kAccCols;
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
-          __syncwarp();
-        };
-        if (fp32) {
-          const bool add = sl > 0 || (a.accumulate && t.part < 0);
+        return tmem_base + ((uint32_t)(q * 32) << 16) + (it & 1u) * kAccCols;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty[it & 1u]));
+        __syncwarp();
+        ++it;
+      };
+      if constexpr (BN == 128) {
+        if (a.out_fp32 || t.part >= 0) {
+          // 64 columns a warp, summed over the slices in registers.
+          uint32_t sum[2][32] = {};
+          for (int sl = 0; sl < nsl && ok; ++sl) {
+            const uint32_t tb = take();
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tb + side * 64 + h * 32, v);
+              tmem_wait_ld();
+              if (sl == 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[h][j] = v[j];
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  sum[h][j] = __float_as_uint(__uint_as_float(sum[h][j]) + __uint_as_float(v[j]));
+              }
+            }
+            release();
+          }
+          if (!ok) break;
+          if (nsl == 0 && a.accumulate) continue;
+          const bool add = a.accumulate && t.part < 0;
+          put(k0 + side * 64, add, sum[0]);
+          put(k0 + side * 64 + 32, add, sum[1]);
+          continue;
+        }
+      }
+      if (nsl == 0) {  // an expert without rows
+        const uint32_t zero[32] = {};
+        const int per = a.out_fp32 ? 32 : 64;
+        for (int c = side * per; c < BN && !a.accumulate; c += 2 * per) put(k0 + c, false, zero);
+        continue;
+      }
+      if (BN == 256 && a.out_fp32) {
+        for (int sl = 0; sl < nsl; ++sl) {
+          const uint32_t tb = take();
+          if (!ok) break;
           // A slice is added to the ones before it once they are in memory.
           if (sl > 0 && lane == 0) bulk_wait();
           __syncwarp();
-          for (int c = side * 32; c < a.bn; c += 64) {
+          for (int c = side * 32; c < BN; c += 64) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(tb + c, v);
             tmem_wait_ld();
-            if (c + 64 >= a.bn) release();
-            put(k0 + c, add, v);
+            if (c + 64 >= BN) release();
+            put(k0 + c, a.accumulate || sl > 0, v);
           }
-        } else if (a.accumulate) {
-          for (int c = side * 32; c < a.bn; c += 64) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(tb + c, v);
-            tmem_wait_ld();
-            if (f0 + lane < a.N && k0 + c < k1)
-              add_row(static_cast<uint16_t*>(a.out) + ((size_t)t.e * a.N + f0 + lane) * a.K + k0 + c,
-                      min(32, k1 - k0 - c) / 8, v, a.fp16);
-            __syncwarp();
-          }
-          release();
-        } else {
-          // Two boxes of 64 columns (one, if bn is 128): the accumulator is free again
-          // once they are in registers, before they are written.
-          uint32_t w[2][32];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int c = (h >> 1) * 128 + side * 64 + (h & 1) * 32;
-            if (c < a.bn) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(tb + c, v);
-              tmem_wait_ld();
-              if (a.fp16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  w[h >> 1][(h & 1) * 16 + j] =
-                      f16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  w[h >> 1][(h & 1) * 16 + j] =
-                      bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              }
-            }
-          }
-          release();
-          put(k0 + side * 64, false, w[0]);
-          if (a.bn == 256) put(k0 + 128 + side * 64, false, w[1]);
         }
+        continue;
+      }
+      const uint32_t tb = take();
+      if (!ok) break;
+      if (a.accumulate) {
+        for (int c = side * 32; c < BN; c += 64) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tb + c, v);
+          tmem_wait_ld();
+          if (f0 + lane < a.N && k0 + c < k1)
+            add_row(static_cast<uint16_t*>(a.out) + ((size_t)t.e * a.N + f0 + lane) * a.K + k0 + c,
+                    min(32, k1 - k0 - c) / 8, v, a.fp16);
+          __syncwarp();
+        }
+        release();
+      } else {
+        // Boxes of 64 columns: the accumulator is free again once they are in registers,
+        // before they are written.
+        uint32_t w[BN / 128][32];
+#pragma unroll
+        for (int h = 0; h < BN / 64; ++h) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tb + (h >> 1) * 128 + side * 64 + (h & 1) * 32, v);
+          tmem_wait_ld();
+          if (a.fp16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[h >> 1][(h & 1) * 16 + j] =
+                  f16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[h >> 1][(h & 1) * 16 + j] =
+                  bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          }
+        }
+        release();
+#pragma unroll
+        for (int h = 0; h < BN / 128; ++h) put(k0 + h * 128 + side * 64, false, w[h]);
       }
     }
     if (lane == 0) bulk_wait();
@@ -465,12 +510,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// out[e] (+)= the sum of the expert's parts, in order, for experts with several.
-// blockIdx.y: expert; 8 values a thread.
+// out[e] (+)= the sum of the expert's parts, for experts with several. blockIdx.y:
+// expert. Four values a thread; the eight warps of a block take every eighth part of
+// the same 128 values, and their sums are added in the warps' order.
 __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
   __shared__ int32_t off_s[kMaxExperts + 1];
   __shared__ uint16_t first_s[kMaxExperts + 1];
   __shared__ int bad_s;
+  __shared__ float4 sum_s[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) bad_s = 0;
   pdl_wait();
   pdl_trigger();
@@ -480,44 +528,43 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
     if (bad_at(off_s, e, a.R)) bad_s = 1;
   __syncthreads();
   if (bad_s) return;
-  if (threadIdx.x < 32) scan_parts(off_s, a.E, a.part_rows, first_s);
+  if (warp == 0) scan_parts(off_s, a.E, a.part_rows, first_s);
   __syncthreads();
   const int e = blockIdx.y, p0 = first_s[e], p1 = first_s[e + 1];
-  const long long n = (long long)a.N * a.K, i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (p1 - p0 <= 1 || i >= n) return;
-  float s[8] = {};
-  const size_t o = (size_t)e * n + i;
-  if (a.accumulate) {
-    if (a.out_fp32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.out) + o);
-      const float4 x = p[0], y = p[1];
-      s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w, s[4] = y.x, s[5] = y.y, s[6] = y.z, s[7] = y.w;
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.out) + o);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[2 * j] = from16(w[j] & 0xFFFFu, a.fp16);
-        s[2 * j + 1] = from16(w[j] >> 16, a.fp16);
-      }
+  if (p1 - p0 <= 1) return;
+  const long long n = (long long)a.N * a.K, i = ((long long)blockIdx.x * 32 + lane) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n) {
+    const float* p = a.parts + (size_t)p0 * n + i;
+#pragma unroll 4
+    for (int k = p0 + warp; k < p1; k += 8) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(p + (size_t)(k - p0) * n));
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
   }
-  const float* p = a.parts + (size_t)p0 * n + i;
-#pragma unroll 4
-  for (int k = p0; k < p1; ++k, p += n) {
-    const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 y = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
-    s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+  sum_s[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || i >= n) return;
+  for (int k = 1; k < 8; ++k) {
+    const float4 x = sum_s[k][lane];
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
   }
+  const size_t o = (size_t)e * n + i;
   if (a.out_fp32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-    d[0] = make_float4(s[0], s[1], s[2], s[3]);
-    d[1] = make_float4(s[4], s[5], s[6], s[7]);
+    if (a.accumulate) {
+      const float4 x = *d;
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    *d = s;
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o) =
-        make_uint4(pack16x2(s[0], s[1], a.fp16), pack16x2(s[2], s[3], a.fp16),
-                   pack16x2(s[4], s[5], a.fp16), pack16x2(s[6], s[7], a.fp16));
+    uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o);
+    if (a.accumulate) {
+      const uint2 x = *d;
+      s.x += from16(x.x & 0xFFFFu, a.fp16), s.y += from16(x.x >> 16, a.fp16);
+      s.z += from16(x.y & 0xFFFFu, a.fp16), s.w += from16(x.y >> 16, a.fp16);
+    }
+    *d = make_uint2(pack16x2(s.x, s.y, a.fp16), pack16x2(s.z, s.w, a.fp16));
   }
 }
 
@@ -528,51 +575,68 @@ bool make_map(CUtensorMap* m, const void* base, int rows, int cols) {
   return make_tensor_map_sw128(m, base, 2, dims, strides, box);
 }
 
+template <int BN>
+cudaError_t launch_tiles(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
+                         const CUtensorMap& tmP, const DwArgs& a, long long items, int num_sms,
+                         cudaStream_t st) {
+  static DeviceFlags attr_done;
+  if (cudaError_t e = smem_attr_once(attr_done, dw_kernel<BN>, Ring<BN>::kSmemBytes);
+      e != cudaSuccess)
+    return e;
+  static std::atomic<int> resident[kMaxDevices];
+  return launch_clusters(dw_kernel<BN>, kCtas, resident, Ring<BN>::kThreads, Ring<BN>::kSmemBytes,
+                         items, num_sms, st, tmA, tmB, tmC, tmP, a);
+}
+
 struct Split {
   int m_tiles, n_tiles, bn;
   int part_rows;        // 0: whole segments
   long long max_parts;  // of all experts
 };
 
-// The tiles' width and the parts of long segments, by sizes alone.
+// The tiles' width and the parts of long segments, by sizes alone: the choice of least
+// estimated time.
 //
-// bn: 256, whose stages carry more MMAs for their bytes; 128 where that leaves less of
-// a tile empty (up to 384 columns) or where the tiles of 256 fill less than half of the
-// chip.
-//
-// Parts: a row costs a tile 4 (bn = 128: 2) ns on its cluster. Whole segments take the
-// rows of the longest (1.5 times the mean, say) as often as the clusters go round; in
-// parts, about two a cluster, the rows are spread over all of them, but the parts' fp32
-// results go to memory and back at 4 bytes a ps and a second launch adds them up.
-Split split_of(int R, int E, int N, int K) {
-  Split s;
-  s.m_tiles = (N + 255) / 256;
-  const bool narrow = K <= 128 || (K > 256 && K <= 384) ||
-                      (long long)E * s.m_tiles * ((K + 255) / 256) < kPairs / 2;
-  s.bn = narrow ? 128 : 256;
-  s.n_tiles = (K + s.bn - 1) / s.bn;
-  const double per = (double)s.m_tiles * s.n_tiles, row = s.bn == 128 ? 2 : 4;
-  const double rounds = std::max(1.0, E * per / kPairs);
-  const double whole = rounds * 1.5 * R / E * row;
-  const double want = std::max(256.0, R * per / (2 * kPairs));
-  s.part_rows = 0;
-  s.max_parts = E;
-  if (want < R) {
-    const int rows = ((int)want + kRows - 1) / kRows * kRows;
-    const long long parts = (long long)E + R / rows;
-    const double cut = R * per / kPairs * row + parts * (double)N * K * 8 / 4000 + 3000;
-    if (cut < whole && parts < 65536 && parts * (long long)per < (1LL << 31)) {
-      s.part_rows = rows;
-      s.max_parts = parts;
+// A row costs a tile 5.1 ns on its cluster at 256 columns (24576 rows x 2048 x 2048: 125
+// us) and 3.2 at 128 (32768 x 64 x 64 in one piece: 103), a tile 0.3 us beside its rows,
+// and the clusters take tiles in turn. Segments are taken to be of equal length, the
+// longest of several half as long again. Cut into parts, the tiles are more, but the
+// parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
+// them. Parts need the narrow tiles, and fp32 results where segments have several slices.
+Split split_of(int R, int E, int N, int K, bool out_fp32) {
+  Split best = {};
+  double least = 0;
+  const double rows = (double)R / E;
+  for (const int bn : {256, 128}) {
+    if (bn == 256 && out_fp32 && rows > kSliceRows) continue;
+    const int m = (N + 255) / 256, n = (K + bn - 1) / bn;
+    const double tiles = (double)E * m * n, row = bn == 256 ? 5.1 : 3.2;
+    for (int parts = 1; parts <= (bn == 128 && R > 512 ? 128 : 1); ++parts) {
+      Split s = {m, n, bn, 0, E};
+      double t = std::ceil(tiles * parts / kPairs) * (rows / parts * row + 300);
+      if (parts == 1) {
+        if (E > 1 && tiles < 4 * kPairs) t += 0.5 * rows * row;
+      } else {
+        const double len = std::max(256.0, rows / parts);
+        s.part_rows = ((int)len + kRows - 1) / kRows * kRows;
+        s.max_parts = (long long)E + R / s.part_rows;
+        if (s.max_parts >= 65536 || s.max_parts * m * n >= (1LL << 31)) break;
+        t += s.max_parts * (double)N * K * 8 / 4000 + 3000;
+      }
+      if (best.bn == 0 || t < least) {
+        best = s;
+        least = t;
+      }
+      if (rows / parts < 256) break;
     }
   }
-  return s;
+  return best;
 }
 
 }  // namespace
 
-long long grouped_product_dw_workspace(int R, int E, int N, int K) {
-  const Split s = split_of(R, E, N, K);
+long long grouped_product_dw_workspace(int R, int E, int N, int K, bool out_fp32) {
+  const Split s = split_of(R, E, N, K, out_fp32);
   return s.part_rows == 0 ? 0 : s.max_parts * N * K * 4;
 }
 
@@ -580,7 +644,7 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
                                       int E, int N, int K, bool fp16, void* out, bool out_fp32,
                                       bool accumulate, void* workspace, int num_sms,
                                       unsigned* err, cudaStream_t st) {
-  const Split s = split_of(R, E, N, K);
+  const Split s = split_of(R, E, N, K, out_fp32);
   DwArgs a = {};
   a.offsets = offsets;
   a.out = out;
@@ -592,7 +656,6 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
   a.K = K;
   a.m_tiles = s.m_tiles;
   a.n_tiles = s.n_tiles;
-  a.bn = s.bn;
   a.part_rows = s.part_rows;
   a.fp16 = fp16;
   a.out_fp32 = out_fp32;
@@ -606,15 +669,12 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
   if (s.part_rows != 0 &&
       !make_tensor_map_rows(&tmP, workspace, MM_DTYPE_FP32, (uint64_t)s.max_parts, N, K, 32))
     return cudaErrorInvalidValue;
-  static DeviceFlags attr_done;
-  if (cudaError_t e = smem_attr_once(attr_done, dw_kernel, kSmemBytes); e != cudaSuccess) return e;
-  static std::atomic<int> resident[kMaxDevices];
   const long long items = s.max_parts * s.m_tiles * s.n_tiles;
-  if (cudaError_t e = launch_clusters(dw_kernel, kCtas, resident, kThreads,
-                                      kSmemBytes, items, num_sms, st, tmA, tmB, tmC, tmP, a);
+  if (cudaError_t e = s.bn == 256 ? launch_tiles<256>(tmA, tmB, tmC, tmP, a, items, num_sms, st)
+                                  : launch_tiles<128>(tmA, tmB, tmC, tmP, a, items, num_sms, st);
       e != cudaSuccess || s.part_rows == 0)
     return e;
-  const long long blocks = ((long long)N * K / 8 + 255) / 256;
+  const long long blocks = ((long long)N * K / 4 + 31) / 32;
   return launch_k(sum_parts_kernel, dim3((unsigned)blocks, (unsigned)E), dim3(256), 0, st, true, a);
 }
 

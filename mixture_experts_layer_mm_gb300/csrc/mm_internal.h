@@ -369,7 +369,7 @@ cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w
                                    void* out, int num_sms, unsigned* err, cudaStream_t st);
 // The gradient of their weights (grouped_product_dw.cu); workspace: as many bytes as
 // grouped_product_dw_workspace gives.
-long long grouped_product_dw_workspace(int R, int E, int N, int K);
+long long grouped_product_dw_workspace(int R, int E, int N, int K, bool out_fp32);
 cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32_t* offsets, int R,
                                       int E, int N, int K, bool fp16, void* out, bool out_fp32,
                                       bool accumulate, void* workspace, int num_sms,
