@@ -847,6 +847,10 @@ def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
     int32 [E + 1]). places[t, j] is the slot's row among all slots sorted by
     expert (stable), -1 for tokens that token_mask [T] (bool or uint8) drops;
     the rows of expert e are offsets[e] .. offsets[e + 1] - 1."""
+    if _fast is not None and stream is None:
+        r = _fast.group_slots(topk_ids, E, token_mask)
+        if r is not None:
+            return r
     T, k = _dims(topk_ids, 2, "topk_ids")
     ids, mask = _ptr(topk_ids, torch.int32, "topk_ids"), _mask_ptr(token_mask, T)
     _device("mm_group_slots", topk_ids, token_mask)
@@ -869,6 +873,10 @@ def mm_dispatch_rows(x, places, w=None, rows=None, row_w=None, stream=None):
     (rows [R, H], row_w fp32 [R], None without w [T, k] fp32). rows and row_w:
     results to write into (R rows; default T * k); rows that no place names stay
     as they are there, and are undefined in new tensors."""
+    if _fast is not None and stream is None:
+        r = _fast.dispatch_rows(x, places, w, rows, row_w)
+        if r is not None:
+            return r
     dt = _rows_dtype(x, "x")
     T, H = _dims(x, 2, "x")
     k = _dims(places, 2, "places")[1]
@@ -893,6 +901,10 @@ def mm_combine_rows(rows, places, w=None, row_values=None, out=None, stream=None
     """out [T, H] = the sum of a token's rows (weighted by w [T, k] fp32 if
     given). With row_values [R] fp32 returns (out, values [T, k]) where
     values[t, j] is the value of the slot's row (0 without one)."""
+    if _fast is not None and stream is None:
+        r = _fast.combine_rows(rows, places, w, row_values, out)
+        if r is not None:
+            return r
     dt = _rows_dtype(rows, "rows")
     R, H = _dims(rows, 2, "rows")
     T, k = _dims(places, 2, "places")
@@ -915,6 +927,10 @@ def mm_grouped_product_dw_workspace_size(R: int, E: int, N: int, K: int, dtype) 
 
 
 def _product(name: str, x, w, offsets, out, stream, transposed: bool):
+    if _fast is not None and stream is None:
+        r = _fast.grouped_product(x, w, offsets, out, transposed)
+        if r is not None:
+            return r
     dt = _rows_dtype(x, "dy" if transposed else "x")
     E, N, K = _dims(w, 3, "w")
     R = _dims(x, 2, "dy" if transposed else "x")[0]
@@ -946,6 +962,12 @@ def mm_grouped_product_dw(dy, x, offsets, out=None, out_dtype=None, accumulate: 
     """The gradient of mm_grouped_product's weights: dw [E, N, K], dw[e] = sum of
     dy[r] x[r]^T over the rows of expert e, of out_dtype (dy's, the default, or
     float32). accumulate: added to what `out` holds."""
+    if out_dtype is None:
+        out_dtype = (dy if out is None else out).dtype
+    if _fast is not None and stream is None:
+        r = _fast.grouped_product_dw(dy, x, offsets, out, _DTYPES.get(out_dtype, -1), accumulate)
+        if r is not None:
+            return r
     dt = _rows_dtype(dy, "dy")
     R, N = _dims(dy, 2, "dy")
     K = _dims(x, 2, "x")[1]
@@ -956,8 +978,6 @@ def mm_grouped_product_dw(dy, x, offsets, out=None, out_dtype=None, accumulate: 
     _device("mm_grouped_product_dw", dy, x, offsets)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if out_dtype is None:
-        out_dtype = dy.dtype if out is None else out.dtype
     if out_dtype not in (dy.dtype, torch.float32):
         raise TypeError(f"out_dtype must be {dy.dtype} or float32, got {out_dtype}")
     if E <= 0 or N % 8 or K % 8 or not N or not K:  # before a result is allocated
@@ -988,6 +1008,10 @@ def mm_swiglu_pack(z, offsets=None, stream=None):
     8 bits for mm_swiglu_pack_backward. Returns (act [R, I], codes int8 [R, 2I],
     scales uint8 [R, 2I / 32]). offsets int32 [E + 1]: only the rows before its
     last value are used and written."""
+    if _fast is not None and stream is None:
+        r = _fast.swiglu_pack(z, offsets)
+        if r is not None:
+            return r
     dt = _rows_dtype(z, "z")
     R, C = _dims(z, 2, "z")
     zp, end = _ptr(z, z.dtype, "z"), _rows_end(offsets)
@@ -1007,6 +1031,10 @@ def mm_swiglu_pack_backward(codes, scales, d_act, row_w=None, offsets=None, stre
     [R, 2I], act [R, I], d_row_w [R] fp32) of d_act's type. row_w [R] fp32: a weight
     that multiplies the row's activations later on; dz and act are weighted by it,
     and d_row_w is its gradient (None without row_w)."""
+    if _fast is not None and stream is None:
+        r = _fast.swiglu_pack_backward(codes, scales, d_act, row_w, offsets)
+        if r is not None:
+            return r
     dt = _rows_dtype(d_act, "d_act")
     R, I = _dims(d_act, 2, "d_act")
     _shape(codes, (R, 2 * I), "codes")
@@ -1029,6 +1057,10 @@ def mm_swiglu_pack_backward(codes, scales, d_act, row_w=None, offsets=None, stre
 def mm_mxint8_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     """The values [rows, K] of 8-bit rows (codes int8 [rows, K], scales uint8
     [rows, K / 32]) as mm_swiglu_pack stores them."""
+    if _fast is not None and stream is None:
+        r = _fast.mxint8_dequantize(codes, scales, _DTYPES.get(dtype, -1))
+        if r is not None:
+            return r
     rows, K = _dims(codes, 2, "codes")
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")

@@ -358,6 +358,269 @@ PyObject* experts_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   MARSHAL_END
 }
 
+// bf16 and fp16, the types of rows.
+bool is_row_type(at::ScalarType t) { return t == at::kBFloat16 || t == at::kHalf; }
+
+template <typename T>
+T* ptr(const Tensor* t) {
+  return t != nullptr ? static_cast<T*>(t->data_ptr()) : nullptr;
+}
+template <typename T>
+T* ptr(const Tensor& t) {
+  return static_cast<T*>(t.data_ptr());
+}
+
+// A result: the given tensor (a reference to it for the caller) or a new one.
+PyObject* result(PyObject* given, const Tensor* g, Tensor& made) {
+  if (g == nullptr) return wrap(std::move(made));
+  Py_INCREF(given);
+  return given;
+}
+
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* r = PyTuple_New(2);
+  if (r == nullptr) return nullptr;
+  PyTuple_SET_ITEM(r, 0, a);
+  PyTuple_SET_ITEM(r, 1, b);
+  return r;
+}
+
+PyObject* none() {
+  Py_INCREF(Py_None);
+  return Py_None;
+}
+
+// (topk_ids, E, token_mask) -> (places, offsets)
+PyObject* group_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 3) Py_RETURN_NONE;
+  Call c;
+  const Tensor* ids = c.take(a[0], at::kInt);
+  const long E = integer(a[1], c.ok);
+  const Tensor* mask = c.any(a[2], true);
+  if (!c.ok || ids->dim() != 2) Py_RETURN_NONE;
+  const int64_t T = ids->size(0), k = ids->size(1);
+  if (!fits_int(T) || !fits_int(k) ||
+      (mask && (!shape_is(*mask, {T}) ||
+                (mask->scalar_type() != at::kBool && mask->scalar_type() != at::kByte))))
+    Py_RETURN_NONE;
+  const int64_t need = mm_group_slots_workspace_size((int)T, (int)k, (int)E);
+  if (need < 0) Py_RETURN_NONE;
+  Tensor places = c.make({T, k}, at::kInt), offsets = c.make({E + 1}, at::kInt), ws;
+  if (need > 0) ws = c.make({need}, at::kByte);
+  const int rc = c.run(mm_group_slots, ptr<const int32_t>(ids), ptr<const uint8_t>(mask), (int)T,
+                       (int)k, (int)E, ptr<int32_t>(places), ptr<int32_t>(offsets),
+                       need > 0 ? ws.data_ptr() : nullptr, (size_t)need, c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  return pair(wrap(std::move(places)), wrap(std::move(offsets)));
+  MARSHAL_END
+}
+
+// (x, places, w, rows, row_w) -> (rows, row_w)
+PyObject* dispatch_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const Tensor *x = c.any(a[0]), *places = c.take(a[1], at::kInt),
+               *w = c.take(a[2], at::kFloat, true), *rows = c.any(a[3], true),
+               *row_w = c.take(a[4], at::kFloat, true);
+  if (!c.ok || x->dim() != 2 || places->dim() != 2 || !is_row_type(x->scalar_type()))
+    Py_RETURN_NONE;
+  const int64_t T = x->size(0), H = x->size(1), k = places->size(1);
+  if (places->size(0) != T || (w && !shape_is(*w, {T, k})) || (row_w && !w) ||
+      (rows && (rows->dim() != 2 || rows->size(1) != H ||
+                rows->scalar_type() != x->scalar_type())))
+    Py_RETURN_NONE;
+  const int64_t R = rows ? rows->size(0) : T * k;
+  if (!fits_int(T) || !fits_int(H) || !fits_int(k) || !fits_int(R) ||
+      (row_w && !shape_is(*row_w, {R})))
+    Py_RETURN_NONE;
+  Tensor new_rows, new_w;
+  if (rows == nullptr) new_rows = c.make({R, H}, x->scalar_type());
+  if (w != nullptr && row_w == nullptr) new_w = c.make({R}, at::kFloat);
+  const int rc = c.run(mm_dispatch_rows, ptr<const void>(x), dtype_code(x->scalar_type()),
+                       ptr<const int32_t>(places), ptr<const float>(w), (int)T, (int)k, (int)H,
+                       (int)R, rows ? ptr<void>(rows) : ptr<void>(new_rows),
+                       w == nullptr ? nullptr : row_w ? ptr<float>(row_w) : ptr<float>(new_w),
+                       c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  return pair(result(a[3], rows, new_rows), w == nullptr ? none() : result(a[4], row_w, new_w));
+  MARSHAL_END
+}
+
+// (rows, places, w, row_values, out) -> out, or (out, values) with row_values
+PyObject* combine_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const Tensor *rows = c.any(a[0]), *places = c.take(a[1], at::kInt),
+               *w = c.take(a[2], at::kFloat, true), *vals = c.take(a[3], at::kFloat, true),
+               *out = c.any(a[4], true);
+  if (!c.ok || rows->dim() != 2 || places->dim() != 2 || !is_row_type(rows->scalar_type()))
+    Py_RETURN_NONE;
+  const int64_t R = rows->size(0), H = rows->size(1), T = places->size(0), k = places->size(1);
+  if (!fits_int(T) || !fits_int(H) || !fits_int(k) || !fits_int(R) ||
+      (w && !shape_is(*w, {T, k})) || (vals && !shape_is(*vals, {R})) ||
+      (out && (!shape_is(*out, {T, H}) || out->scalar_type() != rows->scalar_type())))
+    Py_RETURN_NONE;
+  Tensor new_out, values;
+  if (out == nullptr) new_out = c.make({T, H}, rows->scalar_type());
+  if (vals != nullptr) values = c.make({T, k}, at::kFloat);
+  const int rc = c.run(mm_combine_rows, ptr<const void>(rows), dtype_code(rows->scalar_type()),
+                       ptr<const int32_t>(places), ptr<const float>(w), ptr<const float>(vals),
+                       (int)T, (int)k, (int)H, (int)R, out ? ptr<void>(out) : ptr<void>(new_out),
+                       vals ? ptr<float>(values) : nullptr, c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  PyObject* r = result(a[4], out, new_out);
+  return vals ? pair(r, wrap(std::move(values))) : r;
+  MARSHAL_END
+}
+
+// (x, w, offsets, out, transposed) -> out
+PyObject* grouped_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const Tensor *x = c.any(a[0]), *w = c.any(a[1]), *off = c.take(a[2], at::kInt),
+               *out = c.any(a[3], true);
+  const bool tr = a[4] == Py_True;
+  if (!c.ok || x->dim() != 2 || w->dim() != 3 || !is_row_type(x->scalar_type()) ||
+      w->scalar_type() != x->scalar_type())
+    Py_RETURN_NONE;
+  const int64_t R = x->size(0), E = w->size(0), N = w->size(1), K = w->size(2), M = tr ? K : N;
+  if (!fits_int(R) || !fits_int(E) || !fits_int(N) || !fits_int(K) ||
+      x->size(1) != (tr ? N : K) || !shape_is(*off, {E + 1}) ||
+      (out && (!shape_is(*out, {R, M}) || out->scalar_type() != x->scalar_type())))
+    Py_RETURN_NONE;
+  Tensor made;
+  if (out == nullptr) made = c.make({R, M}, x->scalar_type());
+  const int rc = c.run(tr ? mm_grouped_product_dx : mm_grouped_product, ptr<const void>(x),
+                       ptr<const void>(w), dtype_code(x->scalar_type()), ptr<const int32_t>(off),
+                       (int)R, (int)E, (int)N, (int)K, out ? ptr<void>(out) : ptr<void>(made),
+                       c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  return result(a[3], out, made);
+  MARSHAL_END
+}
+
+// (dy, x, offsets, out, dtype code of the result, accumulate) -> out
+PyObject* grouped_product_dw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 6) Py_RETURN_NONE;
+  Call c;
+  const Tensor *dy = c.any(a[0]), *x = c.any(a[1]), *off = c.take(a[2], at::kInt),
+               *out = c.any(a[3], true);
+  const long dt = integer(a[4], c.ok);
+  const bool add = a[5] == Py_True;
+  if (!c.ok || dt > 2 || dy->dim() != 2 || x->dim() != 2 || off->dim() != 1 ||
+      !is_row_type(dy->scalar_type()) || x->scalar_type() != dy->scalar_type() || (add && !out))
+    Py_RETURN_NONE;
+  const int64_t R = dy->size(0), N = dy->size(1), K = x->size(1), E = off->size(0) - 1;
+  const at::ScalarType type = dtype_of(dt);
+  if (!fits_int(R) || !fits_int(E) || !fits_int(N) || !fits_int(K) || x->size(0) != R || E < 1 ||
+      (type != at::kFloat && type != dy->scalar_type()) ||
+      (out && (!shape_is(*out, {E, N, K}) || out->scalar_type() != type)))
+    Py_RETURN_NONE;
+  const int64_t need =
+      mm_grouped_product_dw_workspace_size((int)R, (int)E, (int)N, (int)K, (int)dt);
+  if (need < 0) Py_RETURN_NONE;
+  Tensor made, ws;
+  if (out == nullptr) made = c.make({E, N, K}, type);
+  if (need > 0) ws = c.make({need}, at::kByte);
+  const int rc = c.run(mm_grouped_product_dw, ptr<const void>(dy), ptr<const void>(x),
+                       dtype_code(dy->scalar_type()), ptr<const int32_t>(off), (int)R, (int)E,
+                       (int)N, (int)K, out ? ptr<void>(out) : ptr<void>(made), (int)dt, (int)add,
+                       need > 0 ? ws.data_ptr() : nullptr, (size_t)need, c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  return result(a[3], out, made);
+  MARSHAL_END
+}
+
+// The address of the number of rows in use, the last of `offsets`.
+const int32_t* rows_end(const Tensor* offsets, bool& ok) {
+  if (offsets == nullptr) return nullptr;
+  if (offsets->dim() != 1 || offsets->size(0) == 0) {
+    ok = false;
+    return nullptr;
+  }
+  return ptr<const int32_t>(offsets) + offsets->size(0) - 1;
+}
+
+// (z, offsets) -> (act, codes, scales)
+PyObject* swiglu_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 2) Py_RETURN_NONE;
+  Call c;
+  const Tensor *z = c.any(a[0]), *off = c.take(a[1], at::kInt, true);
+  if (!c.ok || z->dim() != 2 || !is_row_type(z->scalar_type())) Py_RETURN_NONE;
+  const int64_t R = z->size(0), C = z->size(1);
+  const int32_t* end = rows_end(off, c.ok);
+  if (!c.ok || !fits_int(R) || !fits_int(C) || C == 0 || C % 64 != 0) Py_RETURN_NONE;
+  Tensor act = c.make({R, C / 2}, z->scalar_type()), codes = c.make({R, C}, at::kChar),
+         scales = c.make({R, C / 32}, at::kByte);
+  const int rc = c.run(mm_swiglu_pack, ptr<const void>(z), dtype_code(z->scalar_type()), end,
+                       (int)R, (int)(C / 2), ptr<void>(act), ptr<int8_t>(codes),
+                       ptr<uint8_t>(scales), c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  PyObject* r = PyTuple_New(3);
+  if (r == nullptr) return nullptr;
+  PyTuple_SET_ITEM(r, 0, wrap(std::move(act)));
+  PyTuple_SET_ITEM(r, 1, wrap(std::move(codes)));
+  PyTuple_SET_ITEM(r, 2, wrap(std::move(scales)));
+  return r;
+  MARSHAL_END
+}
+
+// (codes, scales, d_act, row_w, offsets) -> (dz, act, d_row_w or None)
+PyObject* swiglu_pack_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const Tensor *codes = c.take(a[0], at::kChar), *scales = c.take(a[1], at::kByte),
+               *da = c.any(a[2]), *w = c.take(a[3], at::kFloat, true),
+               *off = c.take(a[4], at::kInt, true);
+  if (!c.ok || da->dim() != 2 || !is_row_type(da->scalar_type())) Py_RETURN_NONE;
+  const int64_t R = da->size(0), I = da->size(1);
+  const int32_t* end = rows_end(off, c.ok);
+  if (!c.ok || !fits_int(R) || !fits_int(2 * I) || I == 0 || I % 32 != 0 ||
+      !shape_is(*codes, {R, 2 * I}) || !shape_is(*scales, {R, I / 16}) || (w && !shape_is(*w, {R})))
+    Py_RETURN_NONE;
+  Tensor dz = c.make({R, 2 * I}, da->scalar_type()), act = c.make({R, I}, da->scalar_type()), dw;
+  if (w != nullptr) dw = c.make({R}, at::kFloat);
+  const int rc = c.run(mm_swiglu_pack_backward, ptr<const int8_t>(codes),
+                       ptr<const uint8_t>(scales), ptr<const void>(da),
+                       dtype_code(da->scalar_type()), ptr<const float>(w), end, (int)R, (int)I,
+                       ptr<void>(dz), ptr<void>(act), w ? ptr<float>(dw) : nullptr, c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  PyObject* r = PyTuple_New(3);
+  if (r == nullptr) return nullptr;
+  PyTuple_SET_ITEM(r, 0, wrap(std::move(dz)));
+  PyTuple_SET_ITEM(r, 1, wrap(std::move(act)));
+  PyTuple_SET_ITEM(r, 2, w ? wrap(std::move(dw)) : none());
+  return r;
+  MARSHAL_END
+}
+
+// (codes, scales, dtype code) -> values
+PyObject* mxint8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  MARSHAL_BEGIN
+  if (n != 3) Py_RETURN_NONE;
+  Call c;
+  const Tensor *codes = c.take(a[0], at::kChar), *scales = c.take(a[1], at::kByte);
+  const long dt = integer(a[2], c.ok);
+  if (!c.ok || dt > 2 || codes->dim() != 2) Py_RETURN_NONE;
+  const int64_t rows = codes->size(0), K = codes->size(1);
+  if (!fits_int(rows) || !fits_int(K) || K == 0 || K % 32 != 0 ||
+      !shape_is(*scales, {rows, K / 32}))
+    Py_RETURN_NONE;
+  Tensor out = c.make({rows, K}, dtype_of(dt));
+  const int rc = c.run(mm_mxint8_dequantize, ptr<const int8_t>(codes), ptr<const uint8_t>(scales),
+                       (int)rows, (int)K, ptr<void>(out), (int)dt, c.stream());
+  if (rc != MM_OK) Py_RETURN_NONE;
+  return wrap(std::move(out));
+  MARSHAL_END
+}
+
 #define MARSHAL_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 
@@ -367,6 +630,14 @@ PyMethodDef methods[] = {MARSHAL_METHOD(route_logits),
                          MARSHAL_METHOD(mxfp4_dequantize),
                          MARSHAL_METHOD(mxfp4_gemm),
                          MARSHAL_METHOD(experts_mxfp4),
+                         MARSHAL_METHOD(group_slots),
+                         MARSHAL_METHOD(dispatch_rows),
+                         MARSHAL_METHOD(combine_rows),
+                         MARSHAL_METHOD(grouped_product),
+                         MARSHAL_METHOD(grouped_product_dw),
+                         MARSHAL_METHOD(swiglu_pack),
+                         MARSHAL_METHOD(swiglu_pack_backward),
+                         MARSHAL_METHOD(mxint8_dequantize),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
