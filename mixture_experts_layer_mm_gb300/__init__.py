@@ -23,3 +23,6 @@ from ._lib import (  # noqa: F401
     mm_grouped_product_dx, mm_mxint8_dequantize,
     mm_swiglu_pack, mm_swiglu_pack_backward,
 )
+from .experts_train import (  # noqa: F401
+    ExpertsGrads, ExpertsSaved, moe_experts_train, moe_experts_train_backward,
+)

@@ -8,7 +8,8 @@ checking an installation and for profilers: with --passes P the layer's
 kernels run P times back to back, so a profiler can skip the first passes'
 launches and capture the last one's. --single-launch calls
 mm_moe_forward_single_launch instead of mm_moe_forward; --mxfp4 quantises the
-experts to 4 bits once and calls mm_route and mm_moe_experts_mxfp4. Exits
+experts to 4 bits once and calls mm_route and mm_moe_experts_mxfp4; --train calls
+mm_route, then the experts forward and backward (moe_experts_train). Exits
 non-zero if the device status word reports an error.
 """
 import argparse
@@ -19,6 +20,7 @@ import torch
 
 from . import _lib as mm
 from . import synthetic
+from .experts_train import moe_experts_train, moe_experts_train_backward
 
 
 def main(argv=None) -> int:
@@ -30,9 +32,10 @@ def main(argv=None) -> int:
     p.add_argument("--passes", type=int, default=4)
     p.add_argument("--single-launch", action="store_true")
     p.add_argument("--mxfp4", action="store_true", help="the experts in microscaled 4-bit floats")
+    p.add_argument("--train", action="store_true", help="the experts forward and backward")
     args = p.parse_args(argv)
-    if args.single_launch and args.mxfp4:
-        p.error("--single-launch and --mxfp4 exclude one another")
+    if args.single_launch + args.mxfp4 + args.train > 1:
+        p.error("--single-launch, --mxfp4 and --train exclude one another")
     shape = (synthetic.SWEEP.with_T(args.sweep_T) if args.sweep_T
              else synthetic.WORKLOADS[args.workload])
     d = synthetic.make_inputs(shape)
@@ -51,6 +54,11 @@ def main(argv=None) -> int:
         for _ in range(args.passes):
             ids, w = mm.mm_route(hidden, router_w, shape.top_k, shape.renorm, router_bias=bias)
             mm.mm_moe_experts_mxfp4(hidden, ids, w, gu, gu_scales, dn, dn_scales, out=out)
+    elif args.train:
+        for _ in range(args.passes):
+            ids, w = mm.mm_route(hidden, router_w, shape.top_k, shape.renorm, router_bias=bias)
+            out, saved = moe_experts_train(hidden, ids, w, w_gate_up, w_down)
+            moe_experts_train_backward(out, saved, w_gate_up, w_down)
     else:
         fwd = mm.mm_moe_forward_single_launch if args.single_launch else mm.mm_moe_forward
         for _ in range(args.passes):
