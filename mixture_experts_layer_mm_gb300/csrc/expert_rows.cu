@@ -31,7 +31,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kGrThreads = 1024, kGrWarps = kGrThreads / 32;
-constexpr int kGroupOne = 8192;
+constexpr int kGroupOne = 2048;  // (8192 slots: 16.4 us in one block, 5.4 in spans)
 constexpr int kMaxSpans = 152;  // one block an SM
 
 // Slots a block takes, in whole chunks of kGrThreads.
@@ -204,10 +204,10 @@ __device__ __forceinline__ void add_row(float (&s)[8], const uint4& v, float w) 
   }
 }
 
-// The token's slots with a row, in order, are in shared memory; eight rows' loads are
-// in flight at a time.
-template <bool FP16>
-__global__ void __launch_bounds__(256)
+// The token's slots with a row, in order, are in shared memory; U rows' loads are in
+// flight at a time.
+template <bool FP16, int U>
+__global__ void __launch_bounds__(256, U == 8 ? 4 : 6)
     combine_kernel(const uint4* __restrict__ rows, const int32_t* __restrict__ places,
                    const float* __restrict__ w, const float* __restrict__ row_values, int k,
                    int chunks, long long R, uint4* __restrict__ out, float* __restrict__ values,
@@ -244,13 +244,13 @@ __global__ void __launch_bounds__(256)
   const int used = used_s;
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
     float s[8] = {};
-    for (int j0 = 0; j0 < used; j0 += 8) {
-      uint4 v[8];
+    for (int j0 = 0; j0 < used; j0 += U) {
+      uint4 v[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < U; ++j)
         if (j0 + j < used) v[j] = __ldcs(rows + (size_t)place_s[j0 + j] * chunks + c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < U; ++j)
         if (j0 + j < used) add_row<FP16>(s, v[j], w_s[j0 + j]);
     }
     uint32_t o[4];
@@ -306,7 +306,9 @@ cudaError_t launch_combine_rows(const void* rows, bool fp16, const int32_t* plac
                                 const float* row_values, int T, int top_k, int H, long long R,
                                 void* out, float* values, unsigned* err, cudaStream_t st) {
   const int chunks = H / 8;
-  return launch_k(fp16 ? combine_kernel<true> : combine_kernel<false>, dim3((unsigned)T),
+  auto k = top_k > 4 ? (fp16 ? combine_kernel<true, 8> : combine_kernel<false, 8>)
+                     : (fp16 ? combine_kernel<true, 4> : combine_kernel<false, 4>);
+  return launch_k(k, dim3((unsigned)T),
                   row_threads(chunks), 0, st, true, static_cast<const uint4*>(rows), places, w,
                   row_values, top_k, chunks, R, static_cast<uint4*>(out), values, err);
 }
