@@ -615,7 +615,8 @@ int mm_combine_rows(const void* rows, int dtype, const int32_t* places, const fl
  * the device, ascending, within [0,R] (segments of any length, 0 among them;
  * else nothing is written and MM_ERR_DEVICE is flagged). Rows outside the
  * segments are neither used nor written. N, K multiples of 8, R >= 0, 1 <= E <=
- * 256; N, K <= 2^20, R < 2^31 - 4096 (else MM_ERR_UNSUPPORTED). R == 0: no-op.
+ * 256; N, K <= 2^20, N * K < 2^37, R < 2^31 - 4096 (else MM_ERR_UNSUPPORTED).
+ * R == 0: no-op.
  */
 int mm_grouped_product(const void* x, const void* w, int dtype, const int32_t* offsets, int R,
                        int E, int N, int K, void* y, void* stream);

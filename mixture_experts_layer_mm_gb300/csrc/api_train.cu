@@ -38,16 +38,20 @@ int check_product(int dtype, int R, int E, int N, int K) {
   if (const int rc = check_dtype(dtype); rc != MM_OK) return rc;
   if (E > kMaxExperts || N % 8 != 0 || K % 8 != 0 || N > kMaxCols || K > kMaxCols || R >= kMaxRows)
     return MM_ERR_UNSUPPORTED;
-  // Tiles are counted in 31 bits.
+  // A matrix's bytes are a 40-bit stride of the copies; tiles are counted in 31 bits, and
+  // loops step past the end by the clusters of a chip.
+  if ((long long)N * K >= (1LL << 37)) return MM_ERR_UNSUPPORTED;
   const long long m = (N > K ? N : K) / 256 + 1;
-  if ((R / 256LL + E) * m >= (1LL << 31) || E * (N / 256 + 1LL) * (K / 128 + 1LL) >= (1LL << 31))
+  if ((R / 256LL + E) * m >= kMaxRows || E * (N / 256 + 1LL) * (K / 128 + 1LL) >= kMaxRows)
     return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
 
 int check_swiglu(int R, int C) {
   if (R < 0 || C <= 0) return MM_ERR_INVALID_ARG;
-  if (C % 32 != 0 || C > kMaxCols || R > kMaxRows) return MM_ERR_UNSUPPORTED;
+  // (the product: blocks of 4096 values in a grid's 31 bits)
+  if (C % 32 != 0 || C > kMaxCols || R > kMaxRows || (long long)R * C >= (1LL << 42))
+    return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
 

@@ -13,8 +13,8 @@
 //   dx       features k, W's columns   up to 256 rows     N, W's rows; contiguous in dy
 //
 // The token rows are the N side because its size goes in steps of 16: a segment
-// is cut into near-equal chunks of at most 256 rows, and nothing is computed for
-// rows it does not have. W is not transposed in memory: where the reduction runs
+// is cut into near-equal chunks of at most 256 rows (fewer where there would be too few
+// tiles, see chunk_rows), and nothing is computed for rows it does not have. W is not transposed in memory: where the reduction runs
 // along its rows, a tile of 64 rows x 64 columns (128 bytes a row, 128-byte
 // swizzle) is an MN-major operand, and the MMA is told so.
 //
@@ -55,6 +55,7 @@ struct ProductArgs {
   int F;         // features of the result: N (forward), K (dx)
   int D;         // length of the reduction
   int m_tiles;   // of 256 features
+  int max_rows;  // of a chunk
   int fp16;      // type of the rows and weights (else bf16)
 };
 
@@ -141,13 +142,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __syncthreads();
   const bool bad = S.bad != 0;
   if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
-  if (warp == 0) {  // chunks: ceil(rows / 256) near-equal ones for each expert
+  if (warp == 0) {  // chunks: ceil(rows / max_rows) near-equal ones for each expert
     const int per = (E + 31) / 32, e0 = lane * per, e1 = bad ? 0 : min(e0 + per, E);
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += (S.off[e + 1] - S.off[e] + kGMaxN - 1) / kGMaxN;
+    for (int e = e0; e < e1; ++e) sum += (S.off[e + 1] - S.off[e] + a.max_rows - 1) / a.max_rows;
     int run = exclusive_sum(sum);
     for (int e = e0; e < e1; ++e) {
-      const int L = S.off[e + 1] - S.off[e], n = (L + kGMaxN - 1) / kGMaxN;
+      const int L = S.off[e + 1] - S.off[e], n = (L + a.max_rows - 1) / a.max_rows;
       S.first[e] = run;
       S.size[e] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
       run += n;
@@ -359,6 +360,17 @@ cudaError_t launch_way(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUt
                          num_sms, st, tmA, tmB, tmB32, a);
 }
 
+// Rows of a chunk: 256, or as few as 64 while the tiles of segments of equal length do not
+// fill the chip's 76 pairs. (Every chunk reads the weights again, and below 64 rows a
+// stage's MMAs take less than its waits: 512 rows x 2048 x 2048 14.3 us in chunks of 256,
+// 9.9 of 64, 14.6 of 32.)
+int chunk_rows(int R, int E, int m_tiles) {
+  const long long rows = (R + E - 1) / E;
+  int c = kGMaxN;
+  while (c > 64 && rows > c / 2 && E * ((rows + c - 1) / c) * m_tiles < 76) c /= 2;
+  return c;
+}
+
 // A 2-D matrix [rows, cols] in boxes of 64 columns x box_rows rows, or W [E, rows,
 // cols] likewise (E > 0).
 bool make_map(CUtensorMap* m, const void* base, int E, int rows, int cols, uint32_t box_rows) {
@@ -382,12 +394,13 @@ cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w
   a.F = transposed ? K : N;
   a.D = transposed ? N : K;
   a.m_tiles = (a.F + 255) / 256;
+  a.max_rows = chunk_rows(R, E, a.m_tiles);
   a.fp16 = fp16;
   CUtensorMap tmA, tmB, tmB32;
   if (!make_map(&tmA, w, E, N, K, transposed ? 64 : 128) || !make_map(&tmB, x, 0, R, a.D, 128) ||
       !make_map(&tmB32, x, 0, R, a.D, 32))
     return cudaErrorInvalidValue;
-  const long long chunks = std::min<long long>(R, (long long)E + R / kGMaxN);
+  const long long chunks = std::min<long long>(R, (long long)E + R / a.max_rows);
   return transposed
              ? launch_way<kDx>(tmA, tmB, tmB32, a, chunks * a.m_tiles, num_sms, st)
              : launch_way<kForward>(tmA, tmB, tmB32, a, chunks * a.m_tiles, num_sms, st);

@@ -603,7 +603,8 @@ struct Split {
 // longest of several half as long again. Cut into parts, the tiles are more, but the
 // parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
 // them. Parts need the narrow tiles, and fp32 results where segments have several slices.
-Split split_of(int R, int E, int N, int K, bool out_fp32) {
+// Not inlined: the reported size and the launch have to come to the same choice.
+__attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp32) {
   Split best = {};
   double least = 0;
   const double rows = (double)R / E;

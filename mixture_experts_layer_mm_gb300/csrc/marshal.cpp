@@ -511,9 +511,11 @@ PyObject* grouped_product_dw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *dy = c.any(a[0]), *x = c.any(a[1]), *off = c.take(a[2], at::kInt),
                *out = c.any(a[3], true);
   const long dt = integer(a[4], c.ok);
-  const bool add = a[5] == Py_True;
+  const int add = PyObject_IsTrue(a[5]);
+  if (add < 0) PyErr_Clear();
   if (!c.ok || dt > 2 || dy->dim() != 2 || x->dim() != 2 || off->dim() != 1 ||
-      !is_row_type(dy->scalar_type()) || x->scalar_type() != dy->scalar_type() || (add && !out))
+      !is_row_type(dy->scalar_type()) || x->scalar_type() != dy->scalar_type() || add < 0 ||
+      (add && !out))
     Py_RETURN_NONE;
   const int64_t R = dy->size(0), N = dy->size(1), K = x->size(1), E = off->size(0) - 1;
   const at::ScalarType type = dtype_of(dt);
@@ -529,7 +531,7 @@ PyObject* grouped_product_dw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (need > 0) ws = c.make({need}, at::kByte);
   const int rc = c.run(mm_grouped_product_dw, ptr<const void>(dy), ptr<const void>(x),
                        dtype_code(dy->scalar_type()), ptr<const int32_t>(off), (int)R, (int)E,
-                       (int)N, (int)K, out ? ptr<void>(out) : ptr<void>(made), (int)dt, (int)add,
+                       (int)N, (int)K, out ? ptr<void>(out) : ptr<void>(made), (int)dt, add,
                        need > 0 ? ws.data_ptr() : nullptr, (size_t)need, c.stream());
   if (rc != MM_OK) Py_RETURN_NONE;
   return result(a[3], out, made);

@@ -219,6 +219,8 @@ def _calls():
         "dw parts": lambda: mm.mm_grouped_product_dw(big, big, one, out_dtype=torch.float32),
         "dw added": lambda: mm.mm_grouped_product_dw(
             z, rows, off, out=torch.ones(6, 64, 64, device="cuda"), accumulate=True),
+        "dw added, by a number": lambda: mm.mm_grouped_product_dw(
+            z, rows, off, out=torch.ones(6, 64, 64, device="cuda"), accumulate=1),
         "pack": lambda: mm.mm_swiglu_pack(z),
         "pack rows": lambda: tuple(t[:60] for t in mm.mm_swiglu_pack(z, offsets=off // 2)),
         "backward": lambda: mm.mm_swiglu_pack_backward(q, s, act)[:2],
@@ -230,7 +232,8 @@ def _calls():
 
 
 NAMES = ["group", "group masked", "dispatch", "dispatch weights", "dispatch given", "combine",
-         "combine values", "product", "dx", "dw", "dw parts", "dw added", "pack", "pack rows",
+         "combine values", "product", "dx", "dw", "dw parts", "dw added",
+         "dw added, by a number", "pack", "pack rows",
          "backward", "backward weighted", "dequantise", "no tokens"]
 
 
@@ -322,3 +325,33 @@ def test_declined_calls_raise_as_in_python(monkeypatch):
         errors.append(got)
     assert errors[0] == errors[1]
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+_FIRST = """
+import torch, mixture_experts_layer_mm_gb300 as mm
+g = torch.cuda.CUDAGraph()
+ids = torch.randint(0, 8, (2000, 2), dtype=torch.int32, device="cuda")
+w = torch.rand(2000, 2, device="cuda")
+x = torch.randn(2000, 64, device="cuda").bfloat16()
+gu, dn = (torch.randn(8, n, k, device="cuda").bfloat16() for n, k in ((64, 64), (64, 32)))
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    out, s = mm.moe_experts_train(x, ids, w, gu, dn)
+    grads = mm.moe_experts_train_backward(x, s, gu, dn)
+g.replay()
+torch.cuda.synchronize()
+out2, s = mm.moe_experts_train(x, ids, w, gu, dn)
+again = mm.moe_experts_train_backward(x, s, gu, dn)
+assert torch.equal(out, out2) and all(torch.equal(a, b) for a, b in zip(grads, again))
+assert mm.mm_poll_device_status() == mm.MM_OK
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(mm.__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -68,6 +68,7 @@ def test_product_refusals(L):
         assert f(R=-1) == INV and f(E=0) == INV and f(N=0) == INV and f(K=0) == INV
         assert f(N=60) == UNS and f(K=60) == UNS and f(E=257) == UNS and f(R=(1 << 31) - 1) == UNS
         assert f(N=(1 << 20) + 8) == UNS and f(K=(1 << 20) + 8) == UNS
+        assert f(N=1 << 19, K=1 << 18) == UNS and f(R=1 << 30, N=1 << 20, K=8) == UNS
         assert f(dt=F32) == UNS and f(dt=5) == INV
         assert f(x=None) == INV and f(w=None) == INV and f(off=None) == INV and f(out=None) == INV
         assert f(x=8) == INV and f(w=8) == INV and f(off=18) == INV and f(out=8) == INV
