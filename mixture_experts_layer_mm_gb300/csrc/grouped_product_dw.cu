@@ -511,60 +511,79 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
 }
 
 // out[e] (+)= the sum of the expert's parts, for experts with several. blockIdx.y:
-// expert. Four values a thread; the eight warps of a block take every eighth part of
-// the same 128 values, and their sums are added in the warps' order.
+// expert; a block takes 1024 values, four a thread. Up to 8 parts a thread sums its
+// values' parts in order; of more, the eight warps take every eighth part of 128 values
+// at a time, and their sums are added in the warps' order (129 parts of 64 x 64, one
+// thread after another: 20 us).
 __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
-  __shared__ int32_t off_s[kMaxExperts + 1];
-  __shared__ uint16_t first_s[kMaxExperts + 1];
-  __shared__ int bad_s;
+  __shared__ int before_s[8];
   __shared__ float4 sum_s[8][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) bad_s = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i <= a.E; i += 256) off_s[i] = a.offsets[i];
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256)
-    if (bad_at(off_s, e, a.R)) bad_s = 1;
-  __syncthreads();
-  if (bad_s) return;
-  if (warp == 0) scan_parts(off_s, a.E, a.part_rows, first_s);
-  __syncthreads();
-  const int e = blockIdx.y, p0 = first_s[e], p1 = first_s[e + 1];
-  if (p1 - p0 <= 1) return;
-  const long long n = (long long)a.N * a.K, i = ((long long)blockIdx.x * 32 + lane) * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (i < n) {
-    const float* p = a.parts + (size_t)p0 * n + i;
+  // The parts of the experts before this one, an expert a thread.
+  static_assert(kMaxExperts == 256, "an expert a thread");
+  int before = 0, bad = 0;
+  if ((int)threadIdx.x < a.E) {
+    bad = bad_at(a.offsets, threadIdx.x, a.R);
+    if ((int)threadIdx.x < e)
+      before = parts_of(a.offsets[threadIdx.x + 1] - a.offsets[threadIdx.x], a.part_rows);
+  }
+  before = __reduce_add_sync(kAll, before);
+  if (lane == 0) before_s[warp] = before;
+  const int n_parts = parts_of(a.offsets[e + 1] - a.offsets[e], a.part_rows);
+  if (__syncthreads_or(bad) || n_parts <= 1) return;
+  int p0 = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p0 += before_s[i];
+  const long long n = (long long)a.N * a.K, i0 = (long long)blockIdx.x * 1024;
+  const float* parts = a.parts + (size_t)p0 * n;
+  auto finish = [&](long long i, float4 s) {
+    const size_t o = (size_t)e * n + i;
+    if (a.out_fp32) {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
+      if (a.accumulate) {
+        const float4 x = *d;
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+      }
+      *d = s;
+    } else {
+      uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o);
+      if (a.accumulate) {
+        const uint2 x = *d;
+        s.x += from16(x.x & 0xFFFFu, a.fp16), s.y += from16(x.x >> 16, a.fp16);
+        s.z += from16(x.y & 0xFFFFu, a.fp16), s.w += from16(x.y >> 16, a.fp16);
+      }
+      *d = make_uint2(pack16x2(s.x, s.y, a.fp16), pack16x2(s.z, s.w, a.fp16));
+    }
+  };
+  auto sum = [&](long long i, int k0, int step) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = p0 + warp; k < p1; k += 8) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(p + (size_t)(k - p0) * n));
+    for (int k = k0; k < n_parts; k += step) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(parts + (size_t)k * n + i));
       s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
+    return s;
+  };
+  if (n_parts <= 8) {
+    const long long i = i0 + threadIdx.x * 4;
+    if (i < n) finish(i, sum(i, 0, 1));
+    return;
   }
-  sum_s[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0 || i >= n) return;
-  for (int k = 1; k < 8; ++k) {
-    const float4 x = sum_s[k][lane];
-    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-  }
-  const size_t o = (size_t)e * n + i;
-  if (a.out_fp32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-    if (a.accumulate) {
-      const float4 x = *d;
-      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  for (int j = 0; j < 8 && i0 + j * 128 < n; ++j) {
+    const long long i = i0 + j * 128 + lane * 4;
+    sum_s[warp][lane] = i < n ? sum(i, warp, 8) : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (warp == 0 && i < n) {
+      float4 s = sum_s[0][lane];
+      for (int k = 1; k < 8; ++k) {
+        const float4 x = sum_s[k][lane];
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+      }
+      finish(i, s);
     }
-    *d = s;
-  } else {
-    uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o);
-    if (a.accumulate) {
-      const uint2 x = *d;
-      s.x += from16(x.x & 0xFFFFu, a.fp16), s.y += from16(x.x >> 16, a.fp16);
-      s.z += from16(x.y & 0xFFFFu, a.fp16), s.w += from16(x.y >> 16, a.fp16);
-    }
-    *d = make_uint2(pack16x2(s.x, s.y, a.fp16), pack16x2(s.z, s.w, a.fp16));
+    __syncthreads();
   }
 }
 
@@ -675,7 +694,7 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
                                   : launch_tiles<128>(tmA, tmB, tmC, tmP, a, items, num_sms, st);
       e != cudaSuccess || s.part_rows == 0)
     return e;
-  const long long blocks = ((long long)N * K / 4 + 31) / 32;
+  const long long blocks = ((long long)N * K + 1023) / 1024;
   return launch_k(sum_parts_kernel, dim3((unsigned)blocks, (unsigned)E), dim3(256), 0, st, true, a);
 }
 
