@@ -21,6 +21,14 @@
 // Edges. Columns beyond a matrix are zeros out of the copy, and so are W's rows
 // beyond an expert's (W is a 3-D tensor to the copies). Rows beyond a segment
 // belong to another expert; they give columns of the accumulator that nobody reads.
+//
+// What bounds it, on one GB300: 512 rows over 128 experts x 1536 x 2048 are the weights'
+// bytes, 113 us (7.0 TB/s). 32768 rows of uneven load over them take 181 us forward, and
+// dx of the down product (2048 x 768) 100; their bytes at the copy rate 154 and 87. The
+// SMs take in 2.3 GB there, 13 TB/s out of L2: an expert of more than 256 rows reads its
+// weights for each chunk (168 us with 256 rows each). 1024 rows an expert run at 1.75
+// PFLOP/s. 5003 rows over 60 experts x 1000 x 1016 take 26 us, of 21, in 2.5 rounds of
+// tiles.
 #include <algorithm>
 
 #include "mm.h"
