@@ -10,13 +10,14 @@
 // the other operand for both (TMA multicast), so that a stage brings 32 KB into an
 // SM instead of 48.
 //
-// Why no MMA over the pair, as in grouped_product.cu: a segment of some 256 rows is
-// four stages, 2000 cycles of MMAs, after which 64 KB leave each SM. Signals between
+// Long segments take one MMA over the pair instead, as in grouped_product.cu (PAIR: M =
+// 256, half of the other operand in each CTA, 32 KB of shared memory a stage for 48).
+// Why not all: a segment of some 256 rows is four stages, 2000 cycles of MMAs, after which 64 KB leave each SM. Signals between
 // the CTAs queue behind those stores (measured: 2.2 us from the last MMA to the
 // pair's completion signal, 1.6 us back from the epilogue), and with two accumulators
-// that was what 32768 rows x 128 experts x 1536 x 2048 waited for: 237 us. Here
-// the accumulators' signals stay within a CTA; only the ring's slots, which are
-// filled ahead, are handed over between the two.
+// that is what 32768 rows x 128 experts x 1536 x 2048 wait for: 264 us, where the
+// form of two MMAs takes 189. Its accumulators' signals stay within a CTA; only the ring's
+// slots, which are filled ahead, are handed over between the two.
 //
 // Rows beyond a segment belong to another expert: the last stage is cut to whole
 // steps of 16 rows, and where those hold rows of the next segment the issuing
@@ -38,13 +39,12 @@
 // results go to the workspace and are summed in order by a second launch (the rule is
 // at split_of).
 //
-// What bounds it, on one GB300: the case above takes 191 us with even segments and 205
+// What bounds it, on one GB300: the case above takes 189 us with even segments and 205
 // to 220 with uneven ones (154 at the copy rate of its bytes). 1.6 GB of loads and 0.8
 // GB of stores pass between L2 and the SMs, 12.6 TB/s (without the stores 134 us, 12
 // TB/s), and shared memory moves 512 KB a tile, 107 of its 128 bytes a cycle. Long
-// segments run at 1.5 PFLOP/s, bound by shared memory too (MMAs over the pair, which
-// read a third less of it: 10 % faster for segments of over 1000 rows, 262 us for the
-// case above). Few narrow tiles wait for their ring: a slot's turn takes 1.2 us.
+// segments run at 1.64 to 1.82 PFLOP/s (two MMAs: 1.5, bound by shared memory). Few
+// narrow tiles wait for their ring: a slot's turn takes 1.2 us.
 #include <algorithm>
 #include <cmath>
 
@@ -66,13 +66,14 @@ constexpr int kProd0 = kEpiWarp0 + kEpiWarps;  // producers: one warp a slot
 constexpr int kStore = 32 * 128;             // 4 KB a warp: results on their way out
 constexpr int kStaticBytes = 2000;           // at most: barriers, offsets, parts
 
-// The ring: 192 KB of stages in flight, whatever their size. (A stage is under way for
-// some 1.5 us, so few slots bound the rate: 24000 rows x 4 x 512 x 1024 take 30.2 us with 4 slots
-// of narrow stages, 24.7 with 6.)
-template <int BN>
+// The ring. A slot's turn takes some 1.2 us, so the bytes in flight bound the rate where
+// nothing else does: 24000 rows x 4 x 512 x 1024 take 30.2 us with 4 slots of the narrow
+// tiles' stages, 24.7 with 6. (One producer warp a slot.)
+template <int BN, bool PAIR>
 struct Ring {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kStageBytes = kABytes + BN / 64 * kBlock;
+  static constexpr int kStages = BN == 256 && !PAIR ? 4 : 6;
+  static constexpr int kBoxes = BN / 64 / (PAIR ? 2 : 1);  // of 64 features k, in one SM
+  static constexpr int kStageBytes = kABytes + kBoxes * kBlock;
   static constexpr int kThreads = (kProd0 + kStages) * 32;
   static constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kStore + 1024;
   static_assert(kSmemBytes <= 227 * 1024 - kStaticBytes, "shared memory");
@@ -90,6 +91,7 @@ struct DwArgs {
   int E, R, N, K;
   int m_tiles, n_tiles;
   int part_rows;           // 0: segments are whole
+  int sum_values;          // of a block that sums parts: 1024, or 128 for many parts
   int fp16, out_fp32, accumulate;
 };
 
@@ -122,16 +124,18 @@ struct Item {
   int part;   // its place in the workspace, -1: the result itself
 };
 
-// BN: features k of a tile. tmC: the result, tmP: the parts.
-template <int BN>
-__global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
+// BN: features k of a tile. PAIR: one MMA over the cluster. tmC: the result, tmP: the
+// parts.
+template <int BN, bool PAIR>
+__global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
     dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
               const DwArgs a) {
-  constexpr int kStages = Ring<BN>::kStages, kStageBytes = Ring<BN>::kStageBytes;
-  constexpr int kThreads = Ring<BN>::kThreads;
+  using R = Ring<BN, PAIR>;
+  constexpr int kStages = R::kStages, kStageBytes = R::kStageBytes, kThreads = R::kThreads;
+  static_assert(!PAIR || BN == 256, "narrow tiles are made by each CTA for itself");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[(PAIR ? 3 : 2) * kStages + 5];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, bad_s;
   __shared__ int32_t off_s[kMaxExperts + 1];
@@ -148,14 +152,19 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
+  uint64_t* land = done + 1;  // PAIR: this CTA's copies of a segment's last stage
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), kCtas);  // every CTA's MMAs: its copies fill all
+      // A CTA's copies and MMAs are its own, but half of an operand comes from the other,
+      // which therefore waits for both. PAIR: the leader's barrier counts both CTAs' copies,
+      // and its MMAs free the slots of both.
+      mbar_init(smem_u32(&full[s]), PAIR ? kCtas : 1);
+      mbar_init(smem_u32(&empty[s]), PAIR ? 1 : kCtas);
+      if (PAIR) mbar_init(smem_u32(&land[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), kEpiWarps);
+      mbar_init(smem_u32(&tempty[b]), PAIR ? kCtas * kEpiWarps : kEpiWarps);
     }
     mbar_init(smem_u32(done), 1);
     abort_s = 0;
@@ -166,8 +175,13 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
     tma_prefetch_desc(&tmC);
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(&tmem_base_s), 2 * kAccCols);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(&tmem_base_s), 2 * kAccCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&tmem_base_s), 2 * kAccCols);
+      tmem_relinquish();
+    }
   }
   pdl_wait();
   pdl_trigger();
@@ -223,6 +237,21 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
     }
     return t;
   };
+  // Zeros over the rows of a stage from `left` up to the next multiple of 16, in every block:
+  // 128 bytes each. Straight-line code: in loops it took a warp 900 cycles, 14 us of 224
+  // for 32768 rows of uneven load.
+  auto clear = [&](uint32_t st, int left) {
+    const uint32_t z = st + (left + (lane >> 3)) * 128 + (lane & 7) * 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // four rows at a time
+      if ((left & 15) + (lane >> 3) + 4 * j < 16) {
+#pragma unroll
+        for (int k = 0; k < 2 + R::kBoxes; ++k) st_shared_zero16(z + k * kBlock + j * 512);
+      }
+    __syncwarp();
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
   // Slices of an item's reduction, and the rows of one.
   auto slice_rows = [&](const Item& t) {
     return a.out_fp32 || t.part >= 0 ? kSliceRows : 1 << 30;
@@ -238,18 +267,18 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
     const int slot = warp - kProd0;
     const bool leader = elect_one();
     const uint32_t st = smem_base + slot * kStageBytes;
-    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
+    const uint32_t fb = PAIR ? peer_addr(smem_u32(&full[slot]), 0) : smem_u32(&full[slot]);
+    const uint32_t eb = smem_u32(&empty[slot]), lb = smem_u32(&land[slot]);
     const uint64_t pol = l2_policy_evict_last();  // read by every tile of the expert
-    constexpr int boxes = BN / 64;                  // of 64 columns, loaded by the CTAs in turn
-    const uint32_t bytes = kABytes + boxes * kBlock;
-    uint32_t use = 0;  // fills of this slot so far
-    int q = 0;  // stage counter modulo the ring
+    constexpr uint32_t bytes = kABytes + R::kBoxes * kBlock;
+    uint32_t use = 0, landed = 0;  // fills of this slot so far
+    int q = 0;                     // stage counter modulo the ring
     bool ok = true;
     for (int i = pair; i < total && ok; i += npairs) {
       if (aborted()) break;
       const Item t = item_at(i);
       const int nsl = slices(t), step = slice_rows(t);
-      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN;
+      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN + (int)rank * (BN / 2);
       for (int sl = 0; sl < nsl && ok; ++sl) {
         const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
         for (int kb = 0; kb < nk; ++kb) {
@@ -261,15 +290,43 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
             ok = false;
             break;
           }
-          if (leader) {
-            const int r = t.row0 + sl * step + kb * kRows;
-            mbar_arrive_expect_tx(fb, bytes);
-            tma_load_2d(st, &tmA, fb, f, r, pol);
-            tma_load_2d(st + kBlock, &tmA, fb, f + 64, r, pol);
-            for (int b = rank; b < boxes; b += kCtas)
-              tma_load_2d_all(st + kABytes + b * kBlock, &tmB, fb, c + 64 * b, r, all, pol);
+          const int r = t.row0 + sl * step + kb * kRows;
+          if constexpr (PAIR) {
+            const int left = len - kb * kRows;  // rows of this stage, if fewer than 64
+            const bool tail = left < kRows && (left & 15) != 0;
+            const uint32_t bar = tail ? peer_addr(lb, rank) : fb;
+            if (leader) {
+              mbar_expect_tx_cluster(bar, bytes);
+              tma_load_2d_pair(st, &tmA, bar, f, r, pol);
+              tma_load_2d_pair(st + kBlock, &tmA, bar, f + 64, r, pol);
+#pragma unroll
+              for (int b = 0; b < R::kBoxes; ++b)
+                tma_load_2d_pair(st + kABytes + b * kBlock, &tmB, bar, c + 64 * b, r, pol);
+            }
+            __syncwarp();
+            if (tail) {
+              if (!warp_wait(lb, landed & 1u)) {
+                fail();
+                ok = false;
+                break;
+              }
+              ++landed;
+              clear(st, left);
+              if (leader) mbar_arrive_cluster(fb);
+              __syncwarp();
+            }
+          } else {
+            if (leader) {
+              mbar_arrive_expect_tx(fb, bytes);
+              tma_load_2d(st, &tmA, fb, f, r, pol);
+              tma_load_2d(st + kBlock, &tmA, fb, f + 64, r, pol);
+              const uint32_t half = st + kABytes + rank * (R::kBoxes / 2) * kBlock;
+#pragma unroll
+              for (int b = 0; b < R::kBoxes / 2; ++b)
+                tma_load_2d_all(half + b * kBlock, &tmB, fb, c + 64 * b, r, all, pol);
+            }
+            __syncwarp();
           }
-          __syncwarp();
           ++use;
         }
       }
@@ -285,82 +342,93 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 0) {
-    // ------------------------------------------------------ MMA issuer ---
+    // ------------------------------------- MMA issuer (PAIR: the leader's) ---
     // The whole warp runs the loops, so that descriptors stay in uniform
     // registers; one elected lane issues.
-    const bool leader = elect_one();
-    const uint32_t idesc = idesc_16(a.fp16 != 0, true, true) | idesc_shape(128, BN);
-    int s = 0;
-    uint32_t ph = 0, it = 0;
-    bool ok = true;
-    for (int i = pair; i < total && ok; i += npairs) {
-      if (aborted()) break;
-      const Item t = item_at(i);
-      const int nsl = slices(t), step = slice_rows(t);
-      for (int sl = 0; sl < nsl && ok; ++sl, ++it) {
-        const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
-        const uint32_t b = it & 1u, use = it >> 1;
-        if (!warp_wait(smem_u32(&tempty[b]), (use & 1u) ^ 1u)) {
-          fail();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + b * kAccCols;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!warp_wait(smem_u32(&full[s]), ph)) {
+    if (!PAIR || rank == 0) {
+      const bool leader = elect_one();
+      const uint32_t idesc = idesc_16(a.fp16 != 0, true, true) | idesc_shape(PAIR ? 256 : 128, BN);
+      auto wait = [](uint32_t bar, uint32_t parity) {
+        return PAIR ? warp_wait_cluster(bar, parity) : warp_wait(bar, parity);
+      };
+      auto mma = [&](uint32_t d, uint64_t da, uint64_t db, bool more) {
+        if (PAIR)
+          umma_pair_bf16(d, da, db, idesc, more);
+        else
+          umma_bf16(d, da, db, idesc, more);
+      };
+      int s = 0;
+      uint32_t ph = 0, it = 0;
+      bool ok = true;
+      for (int i = pair; i < total && ok; i += npairs) {
+        if (aborted()) break;
+        const Item t = item_at(i);
+        const int nsl = slices(t), step = slice_rows(t);
+        for (int sl = 0; sl < nsl && ok; ++sl, ++it) {
+          const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
+          const uint32_t b = it & 1u, use = it >> 1;
+          if (!wait(smem_u32(&tempty[b]), (use & 1u) ^ 1u)) {
             fail();
             ok = false;
             break;
           }
-          const uint32_t st = smem_base + s * kStageBytes;
-          const int left = len - kb * kRows;  // rows of this stage, if fewer than 64
-          if (left < kRows && (left & 15) != 0) {
-            // Rows [left, next multiple of 16) of every block: 128 bytes each. (The MMAs
-            // of the stages before run meanwhile. Straight-line code: in loops it took the
-            // warp 900 cycles, 14 us of 224 for 32768 rows of uneven load.)
-            const uint32_t z = st + (left + (lane >> 3)) * 128 + (lane & 7) * 16;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // four rows at a time
-              if ((left & 15) + (lane >> 3) + 4 * j < 16) {
-#pragma unroll
-                for (int k = 0; k < 6; ++k)
-                  if (k < 4 || BN == 256) st_shared_zero16(z + k * kBlock + j * 512);
-              }
-            __syncwarp();
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
           tc_fence_after();
-          if (leader) {
-            const uint64_t da = sdesc_mnmajor(st, kBlock), db = sdesc_mnmajor(st + kABytes, kBlock);
-            const int steps = min(4, (len - kb * kRows + 15) / 16);
-            // 16 rows are 128 descriptor units of 16 bytes.
-            if (steps == 4) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(d, da + kk * 128, db + kk * 128, idesc, (kb | kk) != 0);
-            } else {
-              for (int kk = 0; kk < steps; ++kk)
-                umma_bf16(d, da + kk * 128, db + kk * 128, idesc, (kb | kk) != 0);
+          const uint32_t d = tmem_base + b * kAccCols;
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!wait(smem_u32(&full[s]), ph)) {
+              fail();
+              ok = false;
+              break;
             }
-            umma_commit_all(smem_u32(&empty[s]), all);
+            const uint32_t st = smem_base + s * kStageBytes;
+            const int left = len - kb * kRows;  // rows of this stage, if fewer than 64
+            // (The MMAs of the stages before run meanwhile. With PAIR the rows lie in both
+            // CTAs, whose producers clear them.)
+            if (!PAIR && left < kRows && (left & 15) != 0) clear(st, left);
+            tc_fence_after();
+            if (leader) {
+              const uint64_t da = sdesc_mnmajor(st, kBlock), db = sdesc_mnmajor(st + kABytes, kBlock);
+              const int steps = min(4, (left + 15) / 16);
+              // 16 rows are 128 descriptor units of 16 bytes.
+              if (steps == 4) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma(d, da + kk * 128, db + kk * 128, (kb | kk) != 0);
+              } else {
+                for (int kk = 0; kk < steps; ++kk)
+                  mma(d, da + kk * 128, db + kk * 128, (kb | kk) != 0);
+              }
+              if (PAIR)
+                umma_pair_commit(smem_u32(&empty[s]), all);
+              else
+                umma_commit_all(smem_u32(&empty[s]), all);
+            }
+            __syncwarp();
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (leader) {
+            if (PAIR)
+              umma_pair_commit(smem_u32(&tfull[b]), all);
+            else
+              umma_commit(smem_u32(&tfull[b]));
           }
           __syncwarp();
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (!ok) break;
-        if (leader) umma_commit(smem_u32(&tfull[b]));
-        __syncwarp();
       }
+      // Every MMA issued above has finished before tensor memory is freed.
+      if (leader) {
+        if (PAIR)
+          umma_pair_commit(smem_u32(done), 1);
+        else
+          umma_commit(smem_u32(done));
+      }
+      __syncwarp();
+      if (!warp_wait(smem_u32(done), 0)) fail();
     }
-    // Every MMA issued above has finished before tensor memory is freed.
-    if (leader) umma_commit(smem_u32(done));
-    __syncwarp();
-    if (!warp_wait(smem_u32(done), 0)) fail();
   } else {
     // -------------------------------------------------------- epilogue ---
     const int q = warp & 3;                     // tensor-memory lane quarter of this warp
@@ -397,10 +465,10 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
         }
         __syncwarp();
       };
-      // Accumulator `b` for slice number `it`: waits for it; the function it returns
-      // hands it back.
+      // Waits for slice number `it`'s accumulator (its address), and hands it back.
       auto take = [&]() {
-        ok = warp_wait(smem_u32(&tfull[it & 1u]), (it >> 1) & 1u);
+        const uint32_t bar = smem_u32(&tfull[it & 1u]), parity = (it >> 1) & 1u;
+        ok = PAIR ? warp_wait_cluster(bar, parity) : warp_wait(bar, parity);
         if (!ok) fail();
         tc_fence_after();
         return tmem_base + ((uint32_t)(q * 32) << 16) + (it & 1u) * kAccCols;
@@ -408,7 +476,13 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tempty[it & 1u]));
+        const uint32_t bar = smem_u32(&tempty[it & 1u]);
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(peer_addr(bar, 0));
+          else
+            mbar_arrive(bar);
+        }
         __syncwarp();
         ++it;
       };
@@ -514,15 +588,18 @@ __global__ void __launch_bounds__(Ring<BN>::kThreads, 1)
   pair_sync();  // neither CTA ends while the other's copies or signals may still reach it
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 2 * kAccCols);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, 2 * kAccCols);
+    else
+      tmem_dealloc(tmem_base, 2 * kAccCols);
   }
 }
 
 // out[e] (+)= the sum of the expert's parts, for experts with several. blockIdx.y:
-// expert; a block takes 1024 values, four a thread. Up to 8 parts a thread sums its
-// values' parts in order; of more, the eight warps take every eighth part of 128 values
-// at a time, and their sums are added in the warps' order (129 parts of 64 x 64, one
-// thread after another: 20 us).
+// expert. Four values a thread: a block takes 1024 and a thread sums its values' parts
+// in order; or, of many parts, 128, whose parts the eight warps take in turn, and their
+// sums are added in the warps' order (with the product, 129 parts of 64 x 64: 20.1 us in
+// the first way, 12.3 in the second; 3 parts of 1024 x 1024: 72 and 82).
 __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
   __shared__ int before_s[8];
   __shared__ float4 sum_s[8][32];
@@ -544,7 +621,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
   int p0 = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) p0 += before_s[i];
-  const long long n = (long long)a.N * a.K, i0 = (long long)blockIdx.x * 1024;
+  const long long n = (long long)a.N * a.K, i0 = (long long)blockIdx.x * a.sum_values;
   const float* parts = a.parts + (size_t)p0 * n;
   auto finish = [&](long long i, float4 s) {
     const size_t o = (size_t)e * n + i;
@@ -574,24 +651,21 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const DwArgs a) {
     }
     return s;
   };
-  if (n_parts <= 8) {
+  if (a.sum_values == 1024) {
     const long long i = i0 + threadIdx.x * 4;
     if (i < n) finish(i, sum(i, 0, 1));
     return;
   }
-  for (int j = 0; j < 8 && i0 + j * 128 < n; ++j) {
-    const long long i = i0 + j * 128 + lane * 4;
-    sum_s[warp][lane] = i < n ? sum(i, warp, 8) : make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncthreads();
-    if (warp == 0 && i < n) {
-      float4 s = sum_s[0][lane];
-      for (int k = 1; k < 8; ++k) {
-        const float4 x = sum_s[k][lane];
-        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-      }
-      finish(i, s);
+  const long long i = i0 + lane * 4;
+  sum_s[warp][lane] = i < n ? sum(i, warp, 8) : make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  if (warp == 0 && i < n) {
+    float4 s = sum_s[0][lane];
+    for (int k = 1; k < 8; ++k) {
+      const float4 x = sum_s[k][lane];
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
-    __syncthreads();
+    finish(i, s);
   }
 }
 
@@ -602,21 +676,22 @@ bool make_map(CUtensorMap* m, const void* base, int rows, int cols) {
   return make_tensor_map_sw128(m, base, 2, dims, strides, box);
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 cudaError_t launch_tiles(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
                          const CUtensorMap& tmP, const DwArgs& a, long long items, int num_sms,
                          cudaStream_t st) {
   static DeviceFlags attr_done;
-  if (cudaError_t e = smem_attr_once(attr_done, dw_kernel<BN>, Ring<BN>::kSmemBytes);
+  if (cudaError_t e = smem_attr_once(attr_done, dw_kernel<BN, PAIR>, Ring<BN, PAIR>::kSmemBytes);
       e != cudaSuccess)
     return e;
   static std::atomic<int> resident[kMaxDevices];
-  return launch_clusters(dw_kernel<BN>, kCtas, resident, Ring<BN>::kThreads, Ring<BN>::kSmemBytes,
+  return launch_clusters(dw_kernel<BN, PAIR>, kCtas, resident, Ring<BN, PAIR>::kThreads, Ring<BN, PAIR>::kSmemBytes,
                          items, num_sms, st, tmA, tmB, tmC, tmP, a);
 }
 
 struct Split {
   int m_tiles, n_tiles, bn;
+  bool pair;
   int part_rows;        // 0: whole segments
   long long max_parts;  // of all experts
 };
@@ -625,11 +700,16 @@ struct Split {
 // estimated time.
 //
 // A row costs a tile 5.1 ns on its cluster at 256 columns (24576 rows x 2048 x 2048: 125
-// us) and 3.2 at 128 (32768 x 64 x 64 in one piece: 103), a tile 0.3 us beside its rows,
-// and the clusters take tiles in turn. Segments are taken to be of equal length, the
+// us), 4.6 with MMAs over the pair (113) and 3.2 at 128 (32768 x 64 x 64 in one piece:
+// 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are taken to be of equal length, the
 // longest of several half as long again. Cut into parts, the tiles are more, but the
 // parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
 // them. Parts need the narrow tiles, and fp32 results where segments have several slices.
+//
+// MMAs over the pair pay from 768 rows a segment on where the clusters take several
+// tiles (128 experts x 1536 x 2048, even and uneven: 256 rows 264 / 257 us, where the
+// other form takes 189 / 209; 512 rows 295 / 349 and 336 / 345; 768 rows 385 / 478 and 458
+// / 494), where they take one from 8192 on (2048 x 2048: 4096 rows 24.6 and 23.8).
 // Not inlined: the reported size and the launch have to come to the same choice.
 __attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp32) {
   Split best = {};
@@ -638,9 +718,11 @@ __attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp
   for (const int bn : {256, 128}) {
     if (bn == 256 && out_fp32 && rows > kSliceRows) continue;
     const int m = (N + 255) / 256, n = (K + bn - 1) / bn;
-    const double tiles = (double)E * m * n, row = bn == 256 ? 5.1 : 3.2;
+    const double tiles = (double)E * m * n;
+    const bool pair = bn == 256 && rows >= (tiles > kPairs ? 768 : 8192);
+    const double row = bn == 128 ? 3.2 : pair ? 4.6 : 5.1;
     for (int parts = 1; parts <= (bn == 128 && R > 512 ? 128 : 1); ++parts) {
-      Split s = {m, n, bn, 0, E};
+      Split s = {m, n, bn, pair, 0, E};
       double t = std::ceil(tiles * parts / kPairs) * (rows / parts * row + 300);
       if (parts == 1) {
         if (E > 1 && tiles < 4 * kPairs) t += 0.5 * rows * row;
@@ -685,6 +767,7 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
   a.m_tiles = s.m_tiles;
   a.n_tiles = s.n_tiles;
   a.part_rows = s.part_rows;
+  a.sum_values = s.max_parts > 8LL * E ? 128 : 1024;
   a.fp16 = fp16;
   a.out_fp32 = out_fp32;
   a.accumulate = accumulate;
@@ -698,11 +781,12 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
       !make_tensor_map_rows(&tmP, workspace, MM_DTYPE_FP32, (uint64_t)s.max_parts, N, K, 32))
     return cudaErrorInvalidValue;
   const long long items = s.max_parts * s.m_tiles * s.n_tiles;
-  if (cudaError_t e = s.bn == 256 ? launch_tiles<256>(tmA, tmB, tmC, tmP, a, items, num_sms, st)
-                                  : launch_tiles<128>(tmA, tmB, tmC, tmP, a, items, num_sms, st);
+  auto launch = s.bn == 128 ? launch_tiles<128, false>
+                : s.pair    ? launch_tiles<256, true> : launch_tiles<256, false>;
+  if (cudaError_t e = launch(tmA, tmB, tmC, tmP, a, items, num_sms, st);
       e != cudaSuccess || s.part_rows == 0)
     return e;
-  const long long blocks = ((long long)N * K + 1023) / 1024;
+  const long long blocks = ((long long)N * K + a.sum_values - 1) / a.sum_values;
   return launch_k(sum_parts_kernel, dim3((unsigned)blocks, (unsigned)E), dim3(256), 0, st, true, a);
 }
 

@@ -146,6 +146,29 @@ def test_many_experts_of_uneven_load():
         ref.close(f(a, b, off), want, mag, terms + 16, way)
 
 
+@pytest.mark.parametrize("E,R,N,K", [(4, 5007, 1240, 2056), (1, 12300, 2040, 1992),
+                                     (12, 11000, 1240, 1544), (1, 8200, 2048, 1000)])
+@pytest.mark.parametrize("dtype", [B, H])
+def test_weights_of_long_segments(E, R, N, K, dtype):
+    """Mean lengths from which dw's MMAs run over both CTAs of a cluster."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    lens = torch.bincount(torch.randint(0, E, (R,), generator=g, device="cuda"),
+                          minlength=E).tolist()
+    if E == 12:
+        lens = [6000, 0, 1, 17, 4982] + [0] * 7
+    lead, trail = 3, 5
+    dy, x = (_rand(g, R + 8, c, dtype=dtype) for c in (N, K))
+    dy[:lead], x[:lead], dy[R + lead:], x[R + lead:] = [float("nan")] * 4
+    off = _offsets(lens, lead)
+    want, mag = ref.product(dy.nan_to_num(0), x.nan_to_num(0), off, "dw")
+    got = mm.mm_grouped_product_dw(dy, x, off)
+    ref.close(got, want, mag, max(lens) + 16, "dw")
+    assert torch.equal(mm.mm_grouped_product_dw(dy, x, off), got)
+    old = _rand(g, E, N, K, dtype=dtype, std=30.0)
+    acc = mm.mm_grouped_product_dw(dy, x, off, out=old.clone(), accumulate=True)
+    ref.close(acc, want + old.double(), mag + old.double().abs(), max(lens) + 17, "accumulated")
+
+
 def test_another_experts_infinities_stay_with_it():
     """Segments share tiles and stages of rows; their values do not meet."""
     lens = [37, 90, 5, 64]
