@@ -590,6 +590,12 @@ class _On:
                     whole.untyped_storage(), o // dtype.itemsize, shape)
                 for (shape, dtype), o in zip(parts, at)]
 
+    def together(self, *parts) -> list:
+        """As parts(), where they are under 1 MB together; an allocation each otherwise."""
+        if sum((math.prod(s) * t.itemsize + 255) // 256 * 256 for s, t in parts) < 1 << 20:
+            return self.parts(*parts)
+        return [self.empty(s, t) for s, t in parts]
+
     def launch(self, fn, *args) -> None:
         """fn(*args, stream handle)."""
         st = (torch._C._cuda_getCurrentRawStream(self.di) if self.stream is None
@@ -846,7 +852,9 @@ def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
     """Slots by expert: topk_ids [T, k] int32 -> (places int32 [T, k], offsets
     int32 [E + 1]). places[t, j] is the slot's row among all slots sorted by
     expert (stable), -1 for tokens that token_mask [T] (bool or uint8) drops;
-    the rows of expert e are offsets[e] .. offsets[e + 1] - 1."""
+    the rows of expert e are offsets[e] .. offsets[e + 1] - 1. The results of this
+    call and of the two mm_swiglu_pack calls share one allocation where they are
+    small (under 1 MB): clone() what is to be stored on its own."""
     if _fast is not None and stream is None:
         r = _fast.group_slots(topk_ids, E, token_mask)
         if r is not None:
@@ -861,7 +869,7 @@ def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
     if need < 0:
         raise MMError(MM_ERR_UNSUPPORTED, "mm_group_slots")
     on = _On("mm_group_slots", topk_ids, stream)
-    places, offsets = on.empty((T, k), torch.int32), on.empty((E + 1,), torch.int32)
+    places, offsets = on.together(((T, k), torch.int32), ((E + 1,), torch.int32))
     ws = on.empty(need, torch.uint8, result=False) if need > 0 else None
     on.launch(l.mm_group_slots, ids, mask, T, k, E, places.data_ptr(), offsets.data_ptr(),
               None if ws is None else ws.data_ptr(), need)
@@ -1019,8 +1027,8 @@ def mm_swiglu_pack(z, offsets=None, stream=None):
     if C % 64 != 0 or C == 0:
         raise MMError(MM_ERR_UNSUPPORTED if C else MM_ERR_INVALID_ARG, "mm_swiglu_pack")
     on = _On("mm_swiglu_pack", z, stream)
-    act, codes, scales = (on.empty((R, C // 2), z.dtype), on.empty((R, C), torch.int8),
-                          on.empty((R, C // 32), torch.uint8))
+    act, codes, scales = on.together(((R, C // 2), z.dtype), ((R, C), torch.int8),
+                                     ((R, C // 32), torch.uint8))
     on.launch(lib().mm_swiglu_pack, zp, dt, end, R, C // 2, act.data_ptr(), codes.data_ptr(),
               scales.data_ptr())
     return act, codes, scales
@@ -1047,8 +1055,11 @@ def mm_swiglu_pack_backward(codes, scales, d_act, row_w=None, offsets=None, stre
     if I % 32 != 0 or I == 0:
         raise MMError(MM_ERR_UNSUPPORTED if I else MM_ERR_INVALID_ARG, "mm_swiglu_pack_backward")
     on = _On("mm_swiglu_pack_backward", codes, stream)
-    dz, act = on.empty((R, 2 * I), d_act.dtype), on.empty((R, I), d_act.dtype)
-    d_row_w = None if row_w is None else on.empty((R,), torch.float32)
+    parts = [((R, 2 * I), d_act.dtype), ((R, I), d_act.dtype)]
+    if row_w is not None:
+        parts.append(((R,), torch.float32))
+    dz, act, *rest = on.together(*parts)
+    d_row_w = rest[0] if rest else None
     on.launch(lib().mm_swiglu_pack_backward, cp, sp, dp, dt, wp, end, R, I, dz.data_ptr(),
               act.data_ptr(), None if d_row_w is None else d_row_w.data_ptr())
     return dz, act, d_row_w

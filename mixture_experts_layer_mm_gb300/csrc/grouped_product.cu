@@ -71,7 +71,7 @@ struct Segments {
   int off[kMaxExperts + 1];
   int first[kMaxExperts + 1];  // first chunk of each expert
   int size[kMaxExperts];       // rows per chunk
-  int bad;
+  int sum[kMaxExperts / 32];   // chunks of 32 experts
 };
 
 struct GTile {
@@ -91,10 +91,11 @@ __device__ __forceinline__ GTile tile_at(int tile, const ProductArgs& a, const S
     else
       hi = mid;
   }
-  t.e = lo;
-  t.one = S.first[lo + 1] - S.first[lo] == 1;
-  t.row0 = S.off[lo] + (ch - S.first[lo]) * S.size[lo];
-  t.nrows = min(S.size[lo], S.off[lo + 1] - t.row0);
+  t.e = uniform(lo);
+  const int first = uniform(S.first[t.e]), size = uniform(S.size[t.e]);
+  t.one = uniform(S.first[t.e + 1]) - first == 1;
+  t.row0 = uniform(S.off[t.e]) + (ch - first) * size;
+  t.nrows = min(size, uniform(S.off[t.e + 1]) - t.row0);
   return t;
 }
 
@@ -130,7 +131,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     mbar_init(smem_u32(done), 1);
     abort_s = 0;
-    S.bad = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -140,35 +140,45 @@ __global__ void __launch_bounds__(kGThreads, 1)
     tmem_alloc_pair(smem_u32(&tmem_base_s), kGTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_wait();
-  pdl_trigger();
-  for (int i = tid; i <= E; i += kGThreads) S.off[i] = a.offsets[i];
-  __syncthreads();
-  // Offsets that fall or leave [0, R] are refused as a whole: no row is touched.
-  for (int i = tid; i < E; i += kGThreads)
-    if (S.off[i] < 0 || S.off[i + 1] < S.off[i] || S.off[i + 1] > a.R) S.bad = 1;
-  __syncthreads();
-  const bool bad = S.bad != 0;
-  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
-  if (warp == 0) {  // chunks: ceil(rows / max_rows) near-equal ones for each expert
-    const int per = (E + 31) / 32, e0 = lane * per, e1 = bad ? 0 : min(e0 + per, E);
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += (S.off[e + 1] - S.off[e] + a.max_rows - 1) / a.max_rows;
-    int run = exclusive_sum(sum);
-    for (int e = e0; e < e1; ++e) {
-      const int L = S.off[e + 1] - S.off[e], n = (L + a.max_rows - 1) / a.max_rows;
-      S.first[e] = run;
-      S.size[e] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
-      run += n;
-    }
-    if (lane == 31) S.first[E] = run;
-  }
   tc_fence_before();
   __syncthreads();
   pair_sync();  // both CTAs' barriers initialised, tensor memory allocated
   tc_fence_after();
-  const int total = S.first[E] * a.m_tiles;
-  const uint32_t tmem_base = tmem_base_s;
+  pdl_wait();
+  pdl_trigger();
+  // Segments and their chunks (ceil(rows / max_rows) near-equal ones), an expert a thread.
+  // Offsets that fall or leave [0, R] are refused as a whole: no row is touched.
+  static_assert(kMaxExperts <= kGThreads, "an expert a thread");
+  int n = 0, before = 0;
+  bool bad = false;
+  if (warp < kMaxExperts / 32) {
+    if (tid < E) {
+      const int o = a.offsets[tid], end = a.offsets[tid + 1], L = end - o;
+      bad = o < 0 || end < o || end > a.R;
+      if (!bad) n = (L + a.max_rows - 1) / a.max_rows;
+      S.off[tid] = o;
+      if (tid == E - 1) S.off[E] = end;
+      S.size[tid] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
+    }
+    before = exclusive_sum(n);
+    if (lane == 31) S.sum[warp] = before + n;
+  }
+  // (The vote tells the compiler that all lanes know the same, and with it how long their
+  // loops are: without it a stage took 8 % longer.)
+  bad = __any_sync(kAll, __syncthreads_or(bad));
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
+  int chunks = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    if (w == warp) before += chunks;
+    chunks += S.sum[w];
+  }
+  if (bad) chunks = 0;
+  if (tid < E) S.first[tid] = before;
+  if (tid == 0) S.first[E] = chunks;
+  __syncthreads();
+  const int total = uniform(chunks) * a.m_tiles;
+  const uint32_t tmem_base = uniform(tmem_base_s);
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t peer_abort = peer_addr(smem_u32(&abort_s), rank ^ 1u);
   auto fail = [&]() {
@@ -405,8 +415,12 @@ cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w
   a.max_rows = chunk_rows(R, E, a.m_tiles);
   a.fp16 = fp16;
   CUtensorMap tmA, tmB, tmB32;
-  if (!make_map(&tmA, w, E, N, K, transposed ? 64 : 128) || !make_map(&tmB, x, 0, R, a.D, 128) ||
-      !make_map(&tmB32, x, 0, R, a.D, 32))
+  if (!make_map(&tmA, w, E, N, K, transposed ? 64 : 128) || !make_map(&tmB32, x, 0, R, a.D, 32))
+    return cudaErrorInvalidValue;
+  // A CTA's half of a chunk has at most 96 rows where these say so: the large box goes
+  // unused (describing it takes the host 0.3 us).
+  tmB = tmB32;
+  if (std::min(R, a.max_rows) > 192 && !make_map(&tmB, x, 0, R, a.D, 128))
     return cudaErrorInvalidValue;
   const long long chunks = std::min<long long>(R, (long long)E + R / a.max_rows);
   return transposed

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[(PAIR ? 3 : 2) * kStages + 5];
   __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s, bad_s;
+  __shared__ int abort_s;
   __shared__ int32_t off_s[kMaxExperts + 1];
   __shared__ uint16_t first_s[kMaxExperts + 1];
   static_assert(sizeof(bars) + 12 + sizeof(off_s) + sizeof(first_s) <= kStaticBytes, "shared memory");
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
     }
     mbar_init(smem_u32(done), 1);
     abort_s = 0;
-    bad_s = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -183,24 +182,30 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
       tmem_relinquish();
     }
   }
-  pdl_wait();
-  pdl_trigger();
-  for (int i = tid; i <= E; i += kThreads) off_s[i] = a.offsets[i];
-  __syncthreads();
-  // Bad offsets are refused as a whole: nothing is written.
-  for (int e = tid; e < E; e += kThreads)
-    if (bad_at(off_s, e, a.R)) bad_s = 1;
-  __syncthreads();
-  const bool bad = bad_s != 0;
-  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
-  if (warp == 0 && a.part_rows != 0 && !bad) scan_parts(off_s, E, a.part_rows, first_s);
   tc_fence_before();
   __syncthreads();
   pair_sync();  // both CTAs' barriers are initialised
   tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  bool bad = false;
+  for (int e = tid; e < E; e += kThreads) {
+    off_s[e] = a.offsets[e];
+    if (e == E - 1) off_s[E] = a.offsets[E];
+    bad |= bad_at(a.offsets, e, a.R);
+  }
+  // Bad offsets are refused as a whole: nothing is written. (The vote tells the compiler
+  // that all lanes know the same, and with it how long their loops are: without it a stage
+  // took 10 % longer.)
+  bad = __any_sync(kAll, __syncthreads_or(bad));
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
+  if (a.part_rows != 0) {
+    if (warp == 0 && !bad) scan_parts(off_s, E, a.part_rows, first_s);
+    __syncthreads();
+  }
   const int per = a.m_tiles * a.n_tiles;
-  const int total = bad ? 0 : (a.part_rows != 0 ? (int)first_s[E] : E) * per;
-  const uint32_t tmem_base = tmem_base_s;
+  const int total = bad ? 0 : (a.part_rows != 0 ? uniform(first_s[E]) : E) * per;
+  const uint32_t tmem_base = uniform(tmem_base_s);
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto fail = [&]() {
     for (int r = 0; r < kCtas; ++r) st_cluster_u32(peer_addr(smem_u32(&abort_s), r), 1u);
@@ -217,8 +222,8 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
     t.n = j - t.m * a.n_tiles;
     if (a.part_rows == 0) {
       t.e = p;
-      t.row0 = off_s[p];
-      t.rows = off_s[p + 1] - t.row0;
+      t.row0 = uniform(off_s[p]);
+      t.rows = uniform(off_s[p + 1]) - t.row0;
       t.part = -1;
     } else {
       int lo = 0, hi = E;  // first[lo] <= p < first[hi]
@@ -229,11 +234,11 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
         else
           hi = mid;
       }
-      t.e = lo;
-      const int at = (p - first_s[lo]) * a.part_rows;
-      t.row0 = off_s[lo] + at;
-      t.rows = min(a.part_rows, off_s[lo + 1] - t.row0);
-      t.part = first_s[lo + 1] - first_s[lo] > 1 ? p : -1;
+      t.e = uniform(lo);
+      const int first = uniform(first_s[t.e]);
+      t.row0 = uniform(off_s[t.e]) + (p - first) * a.part_rows;
+      t.rows = min(a.part_rows, uniform(off_s[t.e + 1]) - t.row0);
+      t.part = uniform(first_s[t.e + 1]) - first > 1 ? p : -1;
     }
     return t;
   };

@@ -390,6 +390,22 @@ PyObject* none() {
   return Py_None;
 }
 
+// Results of one call: small ones (under 1 MB together, where an allocation takes
+// longer than the kernel needs) out of one allocation, as in _lib.py.
+struct Together {
+  Call& c;
+  Tensor bytes;
+  int64_t at = 0;
+  bool one;
+
+  Together(Call& call, int64_t total) : c(call), one(total < (int64_t(1) << 20)) {
+    if (one) bytes = c.make({total}, at::kByte);
+  }
+  Tensor make(at::IntArrayRef shape, at::ScalarType type) {
+    return one ? c.part(bytes, at, shape, type) : c.make(shape, type);
+  }
+};
+
 // (topk_ids, E, token_mask) -> (places, offsets)
 PyObject* group_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   MARSHAL_BEGIN
@@ -406,7 +422,8 @@ PyObject* group_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int64_t need = mm_group_slots_workspace_size((int)T, (int)k, (int)E);
   if (need < 0) Py_RETURN_NONE;
-  Tensor places = c.make({T, k}, at::kInt), offsets = c.make({E + 1}, at::kInt), ws;
+  Together both(c, round256(4 * T * k) + round256(4 * (E + 1)));
+  Tensor places = both.make({T, k}, at::kInt), offsets = both.make({E + 1}, at::kInt), ws;
   if (need > 0) ws = c.make({need}, at::kByte);
   const int rc = c.run(mm_group_slots, ptr<const int32_t>(ids), ptr<const uint8_t>(mask), (int)T,
                        (int)k, (int)E, ptr<int32_t>(places), ptr<int32_t>(offsets),
@@ -558,8 +575,9 @@ PyObject* swiglu_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t R = z->size(0), C = z->size(1);
   const int32_t* end = rows_end(off, c.ok);
   if (!c.ok || !fits_int(R) || !fits_int(C) || C == 0 || C % 64 != 0) Py_RETURN_NONE;
-  Tensor act = c.make({R, C / 2}, z->scalar_type()), codes = c.make({R, C}, at::kChar),
-         scales = c.make({R, C / 32}, at::kByte);
+  Together all(c, 2 * round256(R * C) + round256(R * (C / 32)));
+  Tensor act = all.make({R, C / 2}, z->scalar_type()), codes = all.make({R, C}, at::kChar),
+         scales = all.make({R, C / 32}, at::kByte);
   const int rc = c.run(mm_swiglu_pack, ptr<const void>(z), dtype_code(z->scalar_type()), end,
                        (int)R, (int)(C / 2), ptr<void>(act), ptr<int8_t>(codes),
                        ptr<uint8_t>(scales), c.stream());
@@ -587,8 +605,10 @@ PyObject* swiglu_pack_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!c.ok || !fits_int(R) || !fits_int(2 * I) || I == 0 || I % 32 != 0 ||
       !shape_is(*codes, {R, 2 * I}) || !shape_is(*scales, {R, I / 16}) || (w && !shape_is(*w, {R})))
     Py_RETURN_NONE;
-  Tensor dz = c.make({R, 2 * I}, da->scalar_type()), act = c.make({R, I}, da->scalar_type()), dw;
-  if (w != nullptr) dw = c.make({R}, at::kFloat);
+  Together all(c, round256(4 * R * I) + round256(2 * R * I) + (w ? round256(4 * R) : 0));
+  Tensor dz = all.make({R, 2 * I}, da->scalar_type()), act = all.make({R, I}, da->scalar_type()),
+         dw;
+  if (w != nullptr) dw = all.make({R}, at::kFloat);
   const int rc = c.run(mm_swiglu_pack_backward, ptr<const int8_t>(codes),
                        ptr<const uint8_t>(scales), ptr<const void>(da),
                        dtype_code(da->scalar_type()), ptr<const float>(w), end, (int)R, (int)I,

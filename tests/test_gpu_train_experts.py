@@ -264,6 +264,32 @@ def test_both_ways_of_marshalling_agree(name, monkeypatch):
         if a is not None:
             assert a.dtype == b.dtype and a.shape == b.shape and a.device == b.device
             assert torch.equal(a, b)
+    assert _shared(fast) == _shared(slow)
+
+
+def _shared(results):
+    """Which results lie in one allocation with which."""
+    at = [None if r is None else r.untyped_storage().data_ptr() for r in results]
+    return [[a == b for b in at] for a in at]
+
+
+@pytest.mark.parametrize("R,one", [(1, True), (100, True), (5000, False)])
+def test_small_results_share_an_allocation_and_do_not_meet(R, one):
+    z = torch.randn(R, 128, device="cuda").bfloat16()
+    act, q, s = mm.mm_swiglu_pack(z)
+    assert _shared((act, q, s))[0] == [True, one, one]
+    da, w = torch.randn(R, 64, device="cuda").bfloat16(), torch.rand(R, device="cuda")
+    dz, a, dw = mm.mm_swiglu_pack_backward(q, s, da, row_w=w)
+    assert _shared((dz, a, dw))[0] == [True, one, one]
+    ids = torch.randint(0, 9, (R * 20, 4), dtype=torch.int32, device="cuda")
+    p, o = mm.mm_group_slots(ids, 9)
+    assert _shared((p, o))[0] == [True, R < 5000 and R * 320 < (1 << 20) - 512]
+    for group in ((act, q, s), (dz, a, dw), (p, o)):
+        kept = [t.clone() for t in group]
+        for i, t in enumerate(group):                        # writing one leaves the others
+            t.fill_(1)
+            assert all(torch.equal(x, y) for x, y in zip(group[i + 1:], kept[i + 1:]))
+            assert t.data_ptr() % 256 == 0
 
 
 def test_declined_calls_raise_as_in_python(monkeypatch):
