@@ -16,7 +16,7 @@
 // the CTAs queue behind those stores (measured: 2.2 us from the last MMA to the
 // pair's completion signal, 1.6 us back from the epilogue), and with two accumulators
 // that is what 32768 rows x 128 experts x 1536 x 2048 wait for: 264 us, where the
-// form of two MMAs takes 189. Its accumulators' signals stay within a CTA; only the ring's
+// form of two MMAs took 189. Its accumulators' signals stay within a CTA; only the ring's
 // slots, which are filled ahead, are handed over between the two.
 //
 // Rows beyond a segment belong to another expert: the last stage is cut to whole
@@ -39,10 +39,11 @@
 // results go to the workspace and are summed in order by a second launch (the rule is
 // at split_of).
 //
-// What bounds it, on one GB300: the case above takes 189 us with even segments and 205
-// to 220 with uneven ones (154 at the copy rate of its bytes). 1.6 GB of loads and 0.8
-// GB of stores pass between L2 and the SMs, 12.6 TB/s (without the stores 134 us, 12
-// TB/s), and shared memory moves 512 KB a tile, 107 of its 128 bytes a cycle. Long
+// What bounds it, on one GB300: the case above takes 172 us with even segments and 195
+// to 210 with uneven ones (154 at the copy rate of its bytes; 120 for its results alone).
+// 1.6 GB of loads and 0.8 GB of stores pass between L2 and the SMs, 14 TB/s (without the
+// stores 134 us, 12 TB/s), and shared memory moves 512 KB a tile. With the rows in L2 from
+// before it takes 165. Long
 // segments run at 1.64 to 1.82 PFLOP/s (two MMAs: 1.5, bound by shared memory). Few
 // narrow tiles wait for their ring: a slot's turn takes 1.2 us.
 #include <algorithm>
@@ -91,6 +92,7 @@ struct DwArgs {
   int E, R, N, K;
   int m_tiles, n_tiles;
   int part_rows;           // 0: segments are whole
+  int ahead;               // bring the rows of the cluster's next tile into L2 (ahead_of)
   int sum_values;          // of a block that sums parts: 1024, or 128 for many parts
   int fp16, out_fp32, accumulate;
 };
@@ -284,6 +286,22 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
       const Item t = item_at(i);
       const int nsl = slices(t), step = slice_rows(t);
       const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN + (int)rank * (BN / 2);
+      if (BN == 256 && !PAIR && a.ahead && i + npairs < total) {
+        const Item u = item_at(i + npairs);
+        const int uf = (u.m * kCtas + (int)rank) * 128, uc = u.n * BN + (int)rank * (BN / 2);
+        if (leader) {
+          // Boxes 2 * stage + column block, shared out among the tiles that read them (all by
+          // the first tile of each: 179 us for 172, see ahead_of).
+          const int boxes = (u.rows + kRows - 1) / kRows * 2;
+          for (int x = u.n + slot * a.n_tiles; x < boxes; x += kStages * a.n_tiles)
+            if (uf + 64 * (x & 1) < a.N)
+              tma_prefetch_2d(&tmA, uf + 64 * (x & 1), u.row0 + (x >> 1) * kRows, pol);
+          for (int x = u.m + slot * a.m_tiles; x < boxes; x += kStages * a.m_tiles)
+            if (uc + 64 * (x & 1) < a.K)
+              tma_prefetch_2d(&tmB, uc + 64 * (x & 1), u.row0 + (x >> 1) * kRows, pol);
+        }
+        __syncwarp();
+      }
       for (int sl = 0; sl < nsl && ok; ++sl) {
         const int len = min(step, t.rows - sl * step), nk = (len + kRows - 1) / kRows;
         for (int kb = 0; kb < nk; ++kb) {
@@ -748,6 +766,17 @@ __attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp
   return best;
 }
 
+// Whether the tiles' rows go to L2 ahead, a tile before the copies that read them. Under
+// the stream of results first reads take long, and many tiles wait for the same ones: with
+// 128 experts x 1536 x 2048, 256 rows each, 187 us and 172 with this (uneven 205 and 195;
+// 2048 x 768: 101 and 91), 180 rows 166 and 152; two to three tiles before: the same, more:
+// slower. Rows that are in L2 already are only read twice: below its size no gain
+// (60 x 1000 x 1016, 250 rows: 46 and 52). Nor with fp32 results (301 and 318) or for longer
+// segments, which are bound by their MMAs (384 rows, uneven: 271 and 276).
+bool ahead_of(const Split& s, int R, int E, int N, int K, bool out_fp32) {
+  return s.bn == 256 && !s.pair && !out_fp32 && R <= 320LL * E && 2LL * R * (N + K) > 96LL << 20;
+}
+
 }  // namespace
 
 long long grouped_product_dw_workspace(int R, int E, int N, int K, bool out_fp32) {
@@ -772,6 +801,7 @@ cudaError_t launch_grouped_product_dw(const void* dy, const void* x, const int32
   a.m_tiles = s.m_tiles;
   a.n_tiles = s.n_tiles;
   a.part_rows = s.part_rows;
+  a.ahead = ahead_of(s, R, E, N, K, out_fp32);
   a.sum_values = s.max_parts > 8LL * E ? 128 : 1024;
   a.fp16 = fp16;
   a.out_fp32 = out_fp32;

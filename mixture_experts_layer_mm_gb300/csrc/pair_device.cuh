@@ -120,6 +120,14 @@ __device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const void* map, u
       : "memory");
 }
 
+// The box at (c0, c1), clipped as by a copy, into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int c0, int c1, uint64_t policy) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile.L2::cache_hint [%0, {%1, %2}], %3;" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "l"(policy)
+               : "memory");
+}
+
 // One arrival on the barrier at `bar` in every CTA of `mask` once the MMAs of this CTA issued so
 // far by this thread have completed.
 __device__ __forceinline__ void umma_commit_all(uint32_t bar, uint16_t mask) {
