@@ -169,6 +169,27 @@ def test_weights_of_long_segments(E, R, N, K, dtype):
     ref.close(acc, want + old.double(), mag + old.double().abs(), max(lens) + 17, "accumulated")
 
 
+@pytest.mark.parametrize("E,R,N,K", [(200, 26000, 1000, 1016), (128, 24001, 136, 2056),
+                                     (90, 25003, 1544, 520)])
+def test_weights_of_many_segments_beyond_the_cache(E, R, N, K):
+    """Rows of more bytes than L2 keeps, which dw brings there a tile ahead; one segment
+    of many tiles' rows, some of none."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    p = torch.exp(0.7 * torch.randn(E, generator=g, device="cuda"))
+    p[::17] = 0
+    lens = torch.bincount(torch.multinomial(p, R - 2500, replacement=True, generator=g),
+                          minlength=E).tolist()
+    lens[7] += 2500
+    lead, trail = 1, 3
+    dy, x = (_rand(g, R + 4, c) for c in (N, K))
+    dy[:lead], x[:lead], dy[R + lead:], x[R + lead:] = [float("nan")] * 4
+    off = _offsets(lens, lead)
+    want, mag = ref.product(dy.nan_to_num(0), x.nan_to_num(0), off, "dw")
+    got = mm.mm_grouped_product_dw(dy, x, off)
+    ref.close(got, want, mag, max(lens) + 16, "dw")
+    assert torch.equal(mm.mm_grouped_product_dw(dy, x, off), got)
+
+
 def test_another_experts_infinities_stay_with_it():
     """Segments share tiles and stages of rows; their values do not meet."""
     lens = [37, 90, 5, 64]
