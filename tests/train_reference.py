@@ -66,6 +66,13 @@ def product(x, w, offsets, way):
     return out, mag
 
 
+def _power(e):
+    """2^e of whole numbers e, made from its bits: the functions' own powers can be a last
+    bit off (2^-4 and 2^11 are, on a GPU), and a value half way between two codes then
+    falls to the wrong one (97.5 to 97)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def encode(z):
     """8-bit integers and scale bytes of z [R, C] (any float type)."""
     b = z.double().reshape(z.shape[0], -1, 32)
@@ -74,7 +81,7 @@ def encode(z):
                        b.abs().amax(-1))
     e = torch.where(amax == 0, torch.full_like(amax, -127),
                     (torch.frexp(amax)[1] - 7).clamp_min(-127).double())
-    q = torch.ldexp(b, -e[..., None]).nan_to_num(0, 0, 0).round().clamp(-127, 127)
+    q = (b * _power(-e[..., None])).nan_to_num(0, 0, 0).round().clamp(-127, 127)
     q = torch.where(bad[..., None], torch.zeros_like(q), q)
     s = torch.where(bad, torch.full_like(e, 255), e + 127)
     return q.reshape(z.shape).to(torch.int8), s.to(torch.uint8)
@@ -82,7 +89,7 @@ def encode(z):
 
 def decode(q, s):
     e = s.double() - 127
-    unit = torch.where(s == 255, torch.full_like(e, float("nan")), torch.exp2(e))
+    unit = torch.where(s == 255, torch.full_like(e, float("nan")), _power(e))
     return (q.double().reshape(q.shape[0], -1, 32) * unit[..., None]).reshape(q.shape)
 
 
