@@ -16,9 +16,9 @@
 // The scaling is exact, so the one rounding is that to an integer. A block with an
 // infinity or a NaN: s = 255, and all of it NaN.
 //
-// A group of 4 to 32 lanes takes a row, 8 columns a lane and step: a block of 32
+// A group of 4 to 256 lanes takes a row, 8 columns a lane and step: a block of 32
 // is four lanes, its largest magnitude two exchanges; the sum for dw runs over a
-// lane's steps and then over the lanes, the same on every call. The kernels read and
+// lane's steps and then over the lanes and warps, the same on every call. The kernels read and
 // write every byte once and are bound by memory: 32768 rows of 768 bf16 take 34 us to
 // pack (203 MB, 5.9 TB/s; 190 instructions a step of 16 values, the ALU 65 % busy), 41
 // backward (253 MB, 6.2 TB/s), 23 back to bf16 (6.5 TB/s); 512 rows 2 to 3 us each.
@@ -109,10 +109,9 @@ struct Place {
   int row, lane;
 };
 __device__ __forceinline__ Place place_of(int lpr_log2) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Place p;
-  p.lane = lane & ((1 << lpr_log2) - 1);
-  p.row = ((blockIdx.x * kSwWarps + warp) << (5 - lpr_log2)) + (lane >> lpr_log2);
+  p.lane = threadIdx.x & ((1 << lpr_log2) - 1);
+  p.row = blockIdx.x * (kSwThreads >> lpr_log2) + (threadIdx.x >> lpr_log2);
   return p;
 }
 
@@ -195,11 +194,9 @@ __global__ void __launch_bounds__(kSwThreads)
   }
 }
 
-// Many warps rather than many loads a warp: 32768 x 768 in 40.6 us with six blocks an
-// SM (6.2 TB/s) and one step at a time, 52 with two blocks and three steps' loads in
-// flight.
-template <bool FP16>
-__global__ void __launch_bounds__(kSwThreads, 6)
+// U: steps whose loads are in flight together, see unpack_as.
+template <bool FP16, int U>
+__global__ void __launch_bounds__(kSwThreads, U == 1 ? 6 : U == 2 ? 4 : 2)
     swiglu_unpack_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                          const uint16_t* __restrict__ da, const float* __restrict__ row_w,
                          const int32_t* __restrict__ end, int R, int I, int lpr_log2,
@@ -215,38 +212,63 @@ __global__ void __launch_bounds__(kSwThreads, 6)
   const float w = used && row_w != nullptr ? __ldcg(row_w + p.row) : 1.f;
   const Pair ww = {w, w};
   float dot = 0.f;
-  for (int c = p.lane * 8; used && c < I; c += step) {
-    const uint2 g = __ldcs(reinterpret_cast<const uint2*>(codes + zr + c));
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(codes + zr + I + c));
-    const uint4 d = __ldcs(reinterpret_cast<const uint4*>(da + ar + c));
-    const float fg = mx_scale(__ldcg(sr + c / 32)), fu = mx_scale(__ldcg(sr + I / 32 + c / 32));
-    Pair gv[4], uv[4];
-    i8_values(g.x, fg, gv[0], gv[1]);
-    i8_values(g.y, fg, gv[2], gv[3]);
-    i8_values(u.x, fu, uv[0], uv[1]);
-    i8_values(u.y, fu, uv[2], uv[3]);
-    const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-    uint32_t og[4], ou[4], oa[4];
+  for (int c0 = p.lane * 8; used && c0 < I; c0 += U * step) {
+    uint2 gs[U], us[U];
+    uint4 ds[U];
+    uint32_t sg[U], su[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const Pair dv = unpack2<FP16>(dw[j]);
-      const Pair s = sigmoid(gv[j]);
-      const Pair silu = gv[j] * s, a = silu * uv[j], wd = ww * dv;
-      // sigma (1 + g (1 - sigma)); 1 - sigma is off by 2^-23 where it is small, which
-      // the sum with 1 leaves at g 2^-23.
-      const Pair slope = s * fma2(gv[j], fma2(s, Pair{-1.f, -1.f}, Pair{1.f, 1.f}), Pair{1.f, 1.f});
-      dot = __fmaf_rn(dv.x, a.x, dot);
-      dot = __fmaf_rn(dv.y, a.y, dot);
-      og[j] = pack2<FP16>(wd * uv[j] * slope);
-      ou[j] = pack2<FP16>(wd * silu);
-      oa[j] = pack2<FP16>(ww * a);
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      if (c < I) {
+        gs[i] = __ldcs(reinterpret_cast<const uint2*>(codes + zr + c));
+        us[i] = __ldcs(reinterpret_cast<const uint2*>(codes + zr + I + c));
+        ds[i] = __ldcs(reinterpret_cast<const uint4*>(da + ar + c));
+        sg[i] = __ldcg(sr + c / 32);
+        su[i] = __ldcg(sr + I / 32 + c / 32);
+      }
     }
-    *reinterpret_cast<uint4*>(dz + zr + c) = make_uint4(og[0], og[1], og[2], og[3]);
-    *reinterpret_cast<uint4*>(dz + zr + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-    *reinterpret_cast<uint4*>(act + ar + c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * step;
+      if (c >= I) break;
+      const float fg = mx_scale(sg[i]), fu = mx_scale(su[i]);
+      Pair gv[4], uv[4];
+      i8_values(gs[i].x, fg, gv[0], gv[1]);
+      i8_values(gs[i].y, fg, gv[2], gv[3]);
+      i8_values(us[i].x, fu, uv[0], uv[1]);
+      i8_values(us[i].y, fu, uv[2], uv[3]);
+      const uint32_t dw[4] = {ds[i].x, ds[i].y, ds[i].z, ds[i].w};
+      uint32_t og[4], ou[4], oa[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Pair dv = unpack2<FP16>(dw[j]);
+        const Pair s = sigmoid(gv[j]);
+        const Pair silu = gv[j] * s, a = silu * uv[j], wd = ww * dv;
+        // sigma (1 + g (1 - sigma)); 1 - sigma is off by 2^-23 where it is small, which
+        // the sum with 1 leaves at g 2^-23.
+        const Pair slope =
+            s * fma2(gv[j], fma2(s, Pair{-1.f, -1.f}, Pair{1.f, 1.f}), Pair{1.f, 1.f});
+        dot = __fmaf_rn(dv.x, a.x, dot);
+        dot = __fmaf_rn(dv.y, a.y, dot);
+        og[j] = pack2<FP16>(wd * uv[j] * slope);
+        ou[j] = pack2<FP16>(wd * silu);
+        oa[j] = pack2<FP16>(ww * a);
+      }
+      *reinterpret_cast<uint4*>(dz + zr + c) = make_uint4(og[0], og[1], og[2], og[3]);
+      *reinterpret_cast<uint4*>(dz + zr + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+      *reinterpret_cast<uint4*>(act + ar + c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+    }
   }
   if (d_row_w != nullptr) {
-    for (int o = (1 << lpr_log2) >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+    for (int o = min(1 << lpr_log2, 32) >> 1; o > 0; o >>= 1)
+      dot += __shfl_xor_sync(kAll, dot, o);
+    if (lpr_log2 > 5) {  // a row over several warps
+      __shared__ float dot_s[kSwWarps];
+      if ((threadIdx.x & 31) == 0) dot_s[threadIdx.x >> 5] = dot;
+      __syncthreads();
+      if (p.lane == 0)
+        for (int w = 1; w < 1 << (lpr_log2 - 5); ++w) dot += dot_s[(threadIdx.x >> 5) + w];
+    }
     if (used && p.lane == 0) d_row_w[p.row] = dot;
   }
 }
@@ -289,14 +311,20 @@ struct Shape {
 // The lanes of a row: a power of two that covers it in one step, at most 32; 16 instead
 // where that leaves fewer of them idle in the last step and the rows are many (352
 // columns, 44 lanes' worth: three steps of 16 lanes, where 32 idle in 20 of 64 places).
+// Up to the whole block where the rows are so few that two blocks an SM hold them (us,
+// pack and back: 512 x 768 2.1 -> 1.7 and 3.1 -> 2.3, 200 x 2048 4.4 -> 1.8 and 6.0 -> 2.4,
+// 1 x 768 1.6 -> 1.1 and 2.5 -> 1.7; up to four blocks, 1000 x 768 back 2.9 and 3.4).
 Shape shape_of(int R, int I) {
   Shape s = {};
   const int n = I / 8;
   s.lpr_log2 = 2;
   while (s.lpr_log2 < 5 && (1 << s.lpr_log2) < n) ++s.lpr_log2;
   if (s.lpr_log2 == 5 && (n + 15) / 16 * 16 < (n + 31) / 32 * 32 && R >= 8192) s.lpr_log2 = 4;
+  while (s.lpr_log2 >= 5 && 1 << s.lpr_log2 < std::min(n, kSwThreads) &&
+         (long long)R << (s.lpr_log2 + 1) <= 2 * 152 * kSwThreads)
+    ++s.lpr_log2;
   s.u = std::min((n + (1 << s.lpr_log2) - 1) >> s.lpr_log2, 3);
-  const int rows = kSwWarps << (5 - s.lpr_log2);
+  const int rows = kSwThreads >> s.lpr_log2;
   s.blocks = (unsigned)(((long long)R + rows - 1) / rows);
   return s;
 }
@@ -316,7 +344,17 @@ cudaError_t unpack_as(const int8_t* codes, const uint8_t* scales, const uint16_t
                       const float* row_w, const int32_t* end, int R, int I, uint16_t* dz,
                       uint16_t* act, float* d_row_w, cudaStream_t st) {
   const Shape s = shape_of(R, I);
-  return launch_k(swiglu_unpack_kernel<FP16>, dim3(s.blocks), dim3(kSwThreads), 0, st, true, codes, scales, da, row_w, end,
+  // Many rows want warps rather than loads a warp: 32768 x 768 take 40.6 us with six blocks
+  // an SM and one step at a time, 44.5 with four and two, 52 with two and three. Where all
+  // blocks are under way at once the loads count (us, as many steps as fit and one at a
+  // time): two an SM, 2000 x 768 3.5 and 4.3; four, 4000 x 768 6.9 and 8.1, 5003 x 352 5.2 and
+  // 5.7. Three leave room for three of the next call's at one step, and none at two: 3000 x
+  // 768 6.4 and 5.2.
+  const int per_sm = (int)((s.blocks + 151) / 152);
+  const int u = per_sm <= 2 ? s.u : s.u > 1 && per_sm > 3 && s.blocks <= 9 * 76 ? 2 : 1;
+  auto k = u == 1 ? swiglu_unpack_kernel<FP16, 1>
+         : u == 2 ? swiglu_unpack_kernel<FP16, 2> : swiglu_unpack_kernel<FP16, 3>;
+  return launch_k(k, dim3(s.blocks), dim3(kSwThreads), 0, st, true, codes, scales, da, row_w, end,
                   R, I, s.lpr_log2, dz, act, d_row_w);
 }
 

@@ -75,6 +75,13 @@ def test_pack_and_backward(R, I, dtype):
     assert mm.mm_poll_device_status() == mm.MM_OK
 
 
+@pytest.mark.parametrize("R,I", [(65, 8192), (300, 1056), (1300, 768), (2001, 768), (3003, 800),
+                                 (4001, 768), (5003, 352), (6001, 768), (9001, 352)])
+def test_every_share_of_rows_and_lanes(R, I):
+    """Rows over one lane group or several warps, one to three steps at a time."""
+    test_pack_and_backward(R, I, B)
+
+
 @pytest.mark.parametrize("dtype", [B, H])
 def test_values_at_the_edges(dtype):
     """Zeros, the smallest and largest values, steps that tie, infinities and NaN."""
