@@ -12,14 +12,15 @@
 //
 // Group ranks slots by ballots: within a warp the lanes of one expert find each
 // other by a match, warps and chunks of 1024 slots are joined by counts in shared
-// memory. Up to kGroupOne slots one block does it all; beyond, blocks count their
+// memory. Up to kGroupOne slots one block does it all (up to 1024 with a slot a thread, in
+// a kernel of its own); beyond, blocks count their
 // spans first and every block of the second launch adds up the counts before its own.
 //
 // Dispatch and combine move 16 bytes a thread, a block a token: dispatch reads a
 // token's row once and writes it to its slots, combine has the loads of all slots in
 // flight before it adds. Both are bound by memory: 4096 tokens of 2048 bf16 and 8 slots
 // take 24.5 and 23.5 us (151 MB each, 6.2 and 6.4 TB/s) and their grouping 5.4; 64 tokens
-// 2.0, 2.1 and 3.0.
+// 2.0, 2.1 and 1.9.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -158,6 +159,47 @@ __global__ void __launch_bounds__(kGrThreads) group_place_kernel(const GroupArgs
   }
 }
 
+// A slot a thread, one block: the ids are read once (8 slots 1.5 us, 512 1.9, 1024 2.7;
+// 2.4, 2.9 and 3.4 in group_place_kernel).
+__global__ void __launch_bounds__(kGrThreads) group_few_kernel(const GroupArgs a) {
+  __shared__ int warp_count[kGrWarps][kMaxExperts];
+  __shared__ int warp_sum[kMaxExperts / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  for (int i = tid; i < warps * kMaxExperts / 4; i += blockDim.x)
+    reinterpret_cast<int4*>(warp_count)[i] = make_int4(0, 0, 0, 0);
+  pdl_wait();
+  pdl_trigger();
+  bool bad = false;
+  const int e = tid < a.n ? expert_of(a, tid, bad) : a.E;
+  if (bad) atomicOr(a.err, kDevErrBadIds);
+  const uint32_t same = __match_any_sync(kAll, e);
+  const int rank = __popc(same & ((1u << lane) - 1u));
+  __syncthreads();
+  if (rank == 0 && e < a.E) warp_count[warp][e] = __popc(same);
+  __syncthreads();
+  int sum = 0, mine = 0;
+  if (warp < kMaxExperts / 32) {
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) mine += warp_count[w][tid];
+    sum = exclusive_sum(mine);
+    if (lane == 31) warp_sum[warp] = sum + mine;
+  }
+  __syncthreads();
+  if (warp < kMaxExperts / 32) {
+    for (int i = 0; i < warp; ++i) sum += warp_sum[i];
+    if (tid < a.E) a.offsets[tid] = sum;
+    if (tid == a.E - 1) a.offsets[a.E] = sum + mine;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {  // counts -> first row of each warp's slots
+      const int c = warp_count[w][tid];
+      warp_count[w][tid] = sum;
+      sum += c;
+    }
+  }
+  __syncthreads();
+  if (tid < a.n) a.places[tid] = e < a.E ? warp_count[warp][e] + rank : -1;
+}
+
 // Column chunks of 16 bytes of a row.
 __global__ void __launch_bounds__(256)
     dispatch_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ places,
@@ -282,6 +324,10 @@ cudaError_t launch_group_slots(const int32_t* ids, const uint8_t* mask, int T, i
   a.n = (long long)T * top_k;
   a.k = top_k;
   a.E = E;
+  if (a.n <= kGrThreads) {
+    const unsigned threads = std::max(kMaxExperts, ((int)a.n + 31) / 32 * 32);
+    return launch_k(group_few_kernel, dim3(1), dim3(threads), 0, st, true, a);
+  }
   if (a.n <= kGroupOne) {
     a.span = a.n;
     return launch_k(group_place_kernel, dim3(1), dim3(kGrThreads), 0, st, true, a);

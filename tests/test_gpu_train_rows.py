@@ -54,6 +54,13 @@ def test_group(T, E, k, masked):
     assert torch.equal(again[0], places) and torch.equal(again[1], offsets)
 
 
+@pytest.mark.parametrize("T,E,k", [(128, 128, 8), (341, 5, 3), (1024, 256, 1), (32, 1, 32),
+                                   (1000, 2, 1)])
+def test_group_of_a_slot_a_thread(T, E, k):
+    for masked in (0.0, 0.4):
+        test_group(T, E, k, masked)
+
+
 def test_group_without_tokens():
     places, offsets = mm.mm_group_slots(torch.empty(0, 4, dtype=torch.int32, device="cuda"), 9)
     assert places.shape == (0, 4) and offsets.tolist() == [0] * 10
