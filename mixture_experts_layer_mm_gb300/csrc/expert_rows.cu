@@ -12,9 +12,10 @@
 //
 // Group ranks slots by ballots: within a warp the lanes of one expert find each
 // other by a match, warps and chunks of 1024 slots are joined by counts in shared
-// memory. Up to kGroupOne slots one block does it all (up to 1024 with a slot a thread, in
-// a kernel of its own); beyond, blocks count their
-// spans first and every block of the second launch adds up the counts before its own.
+// memory. Up to 1024 slots are one block's, a slot a thread; up to kGroupCluster those of a
+// cluster of eight, whose counts each block reads in the others' shared memory; beyond,
+// blocks count their spans first and every block of the second launch adds up the counts
+// before its own.
 //
 // Dispatch and combine move 16 bytes a thread, a block a token: dispatch reads a
 // token's row once and writes it to its slots, combine has the loads of all slots in
@@ -22,19 +23,23 @@
 // take 24.5 and 23.5 us (151 MB each, 6.2 and 6.4 TB/s) and their grouping 5.4; 64 tokens
 // 2.0, 2.1 and 1.9.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_fp16.h>
 
 #include "mm.h"
 #include "mm_internal.h"
 #include "mx_device.cuh"
+#include "pair_device.cuh"
 
 namespace mm {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kGrThreads = 1024, kGrWarps = kGrThreads / 32;
-constexpr int kGroupOne = 2048;  // (8192 slots: 16.4 us in one block, 5.4 in spans)
+constexpr int kGroupCtas = 8;          // of a cluster
+constexpr int kGroupChunks = 2;        // of kGrThreads slots, at most, in one of its blocks
+constexpr int kGroupCluster = kGroupCtas * kGroupChunks * kGrThreads;
 constexpr int kMaxSpans = 152;  // one block an SM
 
 // Slots a block takes, in whole chunks of kGrThreads.
@@ -48,7 +53,7 @@ struct GroupArgs {
   const uint8_t* mask;  // [T] or NULL
   int32_t* places;
   int32_t* offsets;
-  int32_t* counts;  // [blocks][E] slots of each expert in each span (NULL: one block)
+  int32_t* counts;  // [blocks][E] slots of each expert in each span (group_place_kernel)
   unsigned* err;
   long long n, span;
   int k, E;
@@ -94,27 +99,17 @@ __global__ void __launch_bounds__(kGrThreads) group_place_kernel(const GroupArgs
   pdl_trigger();
   for (int e = tid; e < kMaxExperts; e += kGrThreads) base[e] = total[e] = 0;
   __syncthreads();
-  if (a.counts != nullptr) {
-    // Counts of all spans, and of those before this one: an expert a thread, spans
-    // in turn over the thread's groups. Whole numbers: the order of the sums is free.
-    const int e = tid & (kMaxExperts - 1);
+  // Counts of all spans, and of those before this one: an expert a thread, spans
+  // in turn over the thread's groups. Whole numbers: the order of the sums is free.
+  if (const int e = tid & (kMaxExperts - 1); e < a.E) {
     int before = 0, all = 0;
-    if (e < a.E) {
-      for (int b = tid / kMaxExperts; b < (int)gridDim.x; b += kGrThreads / kMaxExperts) {
-        const int c = __ldcg(a.counts + (size_t)b * a.E + e);
-        all += c;
-        before += b < (int)blockIdx.x ? c : 0;
-      }
-      if (all > 0) atomicAdd(&total[e], all);
-      if (before > 0) atomicAdd(&base[e], before);
+    for (int b = tid / kMaxExperts; b < (int)gridDim.x; b += kGrThreads / kMaxExperts) {
+      const int c = __ldcg(a.counts + (size_t)b * a.E + e);
+      all += c;
+      before += b < (int)blockIdx.x ? c : 0;
     }
-  } else {
-    bool bad = false;
-    for (long long f = f0 + tid; f < f1; f += kGrThreads) {
-      const int e = expert_of(a, f, bad);
-      if (e < a.E) atomicAdd(&total[e], 1);
-    }
-    if (bad) atomicOr(a.err, kDevErrBadIds);
+    if (all > 0) atomicAdd(&total[e], all);
+    if (before > 0) atomicAdd(&base[e], before);
   }
   __syncthreads();
   // Exclusive sums of the totals over the experts, 256 in 8 warps.
@@ -198,6 +193,97 @@ __global__ void __launch_bounds__(kGrThreads) group_few_kernel(const GroupArgs a
   }
   __syncthreads();
   if (tid < a.n) a.places[tid] = e < a.E ? warp_count[warp][e] + rank : -1;
+}
+
+// One cluster, spans of up to kGroupChunks chunks a block (4096 slots 3.1 us, 8192 3.7 to
+// 4.0, 16384 5.4; counting and placing in two launches 4.8, 5.2 and 5.1, and 3 us more of
+// the host's time).
+__global__ void __launch_bounds__(kGrThreads) group_cluster_kernel(const GroupArgs a) {
+  __shared__ int hist[kMaxExperts];   // this block's slots of each expert
+  __shared__ int base[kMaxExperts], total[kMaxExperts];
+  __shared__ int warp_count[kGrWarps][kMaxExperts];
+  __shared__ int warp_sum[kMaxExperts / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank_in = (int)pair_rank();
+  const long long f0 = rank_in * a.span, f1 = min(f0 + a.span, a.n);
+  const int warps = (int)min((a.span + 31) / 32, (long long)kGrWarps);  // of a chunk, in use
+  if (tid < kMaxExperts) hist[tid] = base[tid] = total[tid] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  int e[kGroupChunks];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kGroupChunks; ++i) {
+    const long long f = f0 + i * kGrThreads + tid;
+    e[i] = f < f1 ? expert_of(a, f, bad) : a.E;
+  }
+#pragma unroll
+  for (int i = 0; i < kGroupChunks; ++i)
+    if (e[i] < a.E) atomicAdd(&hist[e[i]], 1);
+  if (bad) atomicOr(a.err, kDevErrBadIds);
+  __syncwarp();
+  pair_sync();
+  {
+    // Whole numbers: the order of the sums is free.
+    const int x = tid & (kMaxExperts - 1);
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kGroupCtas * kMaxExperts / kGrThreads; ++i) {
+      const int r = tid / kMaxExperts + i * (kGrThreads / kMaxExperts);
+      const int c = (int)ld_cluster_u32(peer_addr(smem_u32(&hist[x]), r));
+      all += c;
+      before += r < rank_in ? c : 0;
+    }
+    if (all > 0) atomicAdd(&total[x], all);
+    if (before > 0) atomicAdd(&base[x], before);
+  }
+  // (No block ends, or counts again, while another may still read its counts.)
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __syncthreads();
+  int sum = 0, mine = 0;
+  if (warp < kMaxExperts / 32) {
+    mine = total[tid];
+    sum = exclusive_sum(mine);
+    if (lane == 31) warp_sum[warp] = sum + mine;
+  }
+  __syncthreads();
+  if (warp < kMaxExperts / 32) {
+    for (int i = 0; i < warp; ++i) sum += warp_sum[i];
+    base[tid] += sum;
+    if (rank_in == 0) {
+      if (tid < a.E) a.offsets[tid] = sum;
+      if (tid == a.E - 1) a.offsets[a.E] = sum + mine;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kGroupChunks; ++i) {
+    const long long c0 = f0 + i * kGrThreads;
+    if (c0 >= f1) break;
+    for (int j = tid; j < warps * kMaxExperts / 4; j += kGrThreads)
+      reinterpret_cast<int4*>(warp_count)[j] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    const uint32_t same = __match_any_sync(kAll, e[i]);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (rank == 0 && e[i] < a.E) warp_count[warp][e[i]] = __popc(same);
+    __syncthreads();
+    if (tid < a.E) {  // counts -> first row of each warp's slots
+      int at = base[tid];
+#pragma unroll 8
+      for (int w = 0; w < warps; ++w) {
+        const int c = warp_count[w][tid];
+        warp_count[w][tid] = at;
+        at += c;
+      }
+      base[tid] = at;
+    }
+    __syncthreads();
+    if (c0 + tid < f1) a.places[c0 + tid] = e[i] < a.E ? warp_count[warp][e[i]] + rank : -1;
+    __syncthreads();
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Column chunks of 16 bytes of a row.
@@ -309,7 +395,7 @@ dim3 row_threads(int chunks) { return dim3((unsigned)std::min(256, (chunks + 31)
 }  // namespace
 
 long long group_slots_workspace(long long n, int E) {
-  return n <= kGroupOne ? 0 : (n + span_of(n) - 1) / span_of(n) * E * 4;
+  return n <= kGroupCluster ? 0 : (n + span_of(n) - 1) / span_of(n) * E * 4;
 }
 
 cudaError_t launch_group_slots(const int32_t* ids, const uint8_t* mask, int T, int top_k, int E,
@@ -328,9 +414,11 @@ cudaError_t launch_group_slots(const int32_t* ids, const uint8_t* mask, int T, i
     const unsigned threads = std::max(kMaxExperts, ((int)a.n + 31) / 32 * 32);
     return launch_k(group_few_kernel, dim3(1), dim3(threads), 0, st, true, a);
   }
-  if (a.n <= kGroupOne) {
-    a.span = a.n;
-    return launch_k(group_place_kernel, dim3(1), dim3(kGrThreads), 0, st, true, a);
+  if (a.n <= kGroupCluster) {
+    a.span = ((a.n + kGroupCtas - 1) / kGroupCtas + 31) / 32 * 32;
+    static std::atomic<int> resident[kMaxDevices];
+    return launch_clusters(group_cluster_kernel, kGroupCtas, resident, kGrThreads, 0, 1, 152, st,
+                           a);
   }
   a.span = span_of(a.n);
   a.counts = static_cast<int32_t*>(workspace);

@@ -61,6 +61,18 @@ def test_group_of_a_slot_a_thread(T, E, k):
         test_group(T, E, k, masked)
 
 
+@pytest.mark.parametrize("T,E,k", [(205, 5, 5), (1025, 1, 1), (1031, 200, 7), (2048, 256, 8),
+                                   (4096, 128, 4), (16383, 33, 1), (2731, 64, 6), (300, 256, 32)])
+def test_group_of_a_cluster(T, E, k):
+    """1025 to 16384 slots, and just beyond."""
+    for masked in (0.0, 0.4):
+        test_group(T, E, k, masked)
+
+
+def test_group_of_a_cluster_flags_bad_ids():
+    test_group_drops_and_flags_bad_ids(600)
+
+
 def test_group_without_tokens():
     places, offsets = mm.mm_group_slots(torch.empty(0, 4, dtype=torch.int32, device="cuda"), 9)
     assert places.shape == (0, 4) and offsets.tolist() == [0] * 10
