@@ -19,7 +19,7 @@
 // swizzle) is an MN-major operand, and the MMA is told so.
 //
 // Edges. Columns beyond a matrix are zeros out of the copy, and so are W's rows
-// beyond an expert's (W is a 3-D tensor to the copies). Rows beyond a segment
+// beyond an expert's (W is a 3-D tensor to the copies) in a box that has some of it. Rows beyond a segment
 // belong to another expert; they give columns of the accumulator that nobody reads.
 //
 // What bounds it, on one GB300: 512 rows over 128 experts x 1536 x 2048 are the weights'
@@ -30,6 +30,7 @@
 // PFLOP/s. 5003 rows over 60 experts x 1000 x 1016 take 26 us, of 21, in 2.5 rounds of
 // tiles.
 #include <algorithm>
+#include <cmath>
 
 #include "mm.h"
 #include "mm_device.cuh"
@@ -211,8 +212,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int nh = ((t.nrows + 15) & ~15) / 2;  // this CTA's half of the rows
       const int brow = t.row0 + (int)rank * nh;
       const int boxes = (nh + 31) / 32;
-      const uint32_t bytes = kGHalf + (nh > 96 ? kGHalf : (uint32_t)boxes * 32 * kGK * 2);
       const int f = t.m * 256 + (int)rank * 128;
+      // Boxes wholly beyond W's features are left out, nobody reads what they give: zeros
+      // take a copy longer than values (22886 rows x 128 x 128: 12.1 us with, 7.3 without).
+      const int halves = min(max((a.F - f + 63) / 64, 0), 2);  // of 64 features
+      const uint32_t bytes = (WAY == kForward ? (halves > 0 ? kGHalf : 0) : halves * kGBox) +
+                             (nh > 96 ? kGHalf : (uint32_t)boxes * 32 * kGK * 2);
       // W is read by every chunk of the expert, the rows by every m-tile.
       const uint64_t pol_w = t.one ? pol_once : pol_normal;
       for (int kb = 0; kb < nk; ++kb) {
@@ -227,10 +232,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
         if (leader) {
           mbar_expect_tx_cluster(fb, bytes);
           if (WAY == kForward) {
-            tma_load_3d_pair(st, &tmA, fb, kb * kGK, f, t.e, pol_w);
+            if (halves > 0) tma_load_3d_pair(st, &tmA, fb, kb * kGK, f, t.e, pol_w);
           } else {
-            tma_load_3d_pair(st, &tmA, fb, f, kb * kGK, t.e, pol_w);
-            tma_load_3d_pair(st + kGBox, &tmA, fb, f + 64, kb * kGK, t.e, pol_w);
+            if (halves > 0) tma_load_3d_pair(st, &tmA, fb, f, kb * kGK, t.e, pol_w);
+            if (halves > 1) tma_load_3d_pair(st + kGBox, &tmA, fb, f + 64, kb * kGK, t.e, pol_w);
           }
           if (nh > 96) {
             tma_load_2d_pair(st + kGHalf, &tmB, fb, kb * kGK, brow, pol_keep);
@@ -378,15 +383,18 @@ cudaError_t launch_way(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUt
                          num_sms, st, tmA, tmB, tmB32, a);
 }
 
-// Rows of a chunk: 256, or as few as 64 while the tiles of segments of equal length do not
-// fill the chip's 76 pairs. (Every chunk reads the weights again, and below 64 rows a
-// stage's MMAs take less than its waits: 512 rows x 2048 x 2048 14.3 us in chunks of 256,
-// 9.9 of 64, 14.6 of 32.)
+// Rows of a chunk, at most 256: where the chip's 76 pairs take a tile or two each, as many
+// chunks as they take then (uneven segments make half a chunk more each), of at least 64
+// rows. (Every chunk reads the weights again, and below 64 rows a stage's MMAs take less
+// than its waits: 512 rows x 2048 x 2048 14.3 us in chunks of 256, 9.1 of 64, 14.6 of 32;
+// 600 rows 9.7 us in chunks of 80, 13.4 of 64, which make two rounds; 2500 x 1024 x 1024 8.5
+// and 9.8; 22886 x 256 x 512, two rounds of 160 rows and of 256, 9.9 and 11.2.)
 int chunk_rows(int R, int E, int m_tiles) {
-  const long long rows = (R + E - 1) / E;
-  int c = kGMaxN;
-  while (c > 64 && rows > c / 2 && E * ((rows + c - 1) / c) * m_tiles < 76) c /= 2;
-  return c;
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    const double chunks = rounds * 76 / m_tiles - 0.5 * (E - 1);
+    if (chunks * kGMaxN >= R) return std::max(64, (int)std::ceil(R / chunks / 16) * 16);
+  }
+  return kGMaxN;
 }
 
 // A 2-D matrix [rows, cols] in boxes of 64 columns x box_rows rows, or W [E, rows,
