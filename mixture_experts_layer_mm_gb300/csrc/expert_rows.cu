@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kGrThreads) group_cluster_kernel(const GroupAr
     if (e[i] < a.E) atomicAdd(&hist[e[i]], 1);
   if (bad) atomicOr(a.err, kDevErrBadIds);
   __syncwarp();
-  pair_sync();
+  cluster_barrier();
   {
     // Whole numbers: the order of the sums is free.
     const int x = tid & (kMaxExperts - 1);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kGrThreads) group_cluster_kernel(const GroupAr
 #pragma unroll
     for (int i = 0; i < kGroupCtas * kMaxExperts / kGrThreads; ++i) {
       const int r = tid / kMaxExperts + i * (kGrThreads / kMaxExperts);
-      const int c = (int)ld_cluster_u32(peer_addr(smem_u32(&hist[x]), r));
+      const int c = load_peer(&hist[x], r);
       all += c;
       before += r < rank_in ? c : 0;
     }

@@ -52,6 +52,7 @@ constexpr int kGEpiWarp0 = 1, kGEpiWarps = 8;
 constexpr int kGProd0 = kGEpiWarp0 + kGEpiWarps;          // producers: one warp a slot
 constexpr int kGThreads = (kGProd0 + kGStages) * 32;      // 480
 constexpr int kGSmemBytes = kGStages * kGStageBytes + 1024;
+static_assert(kMaxExperts <= kGThreads, "an expert a thread");
 constexpr uint32_t kGTmemCols = 2 * kGMaxN;               // two accumulators
 
 enum { kForward = 0, kDx = 1 };
@@ -66,6 +67,7 @@ struct ProductArgs {
   int m_tiles;   // of 256 features
   int max_rows;  // of a chunk
   int fp16;      // type of the rows and weights (else bf16)
+  int splits;    // product_few_kernel: CTAs of a cluster
 };
 
 struct Segments {
@@ -100,6 +102,42 @@ __device__ __forceinline__ GTile tile_at(int tile, const ProductArgs& a, const S
   return t;
 }
 
+// Segments and their chunks (ceil(rows / max_rows) near-equal ones), an expert a thread of
+// the block. Offsets that fall or leave [0, R] are refused as a whole: no row is touched.
+// Returns the number of chunks.
+__device__ __forceinline__ int scan_chunks(const ProductArgs& a, Segments& S) {
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, E = a.E;
+  int n = 0, before = 0;
+  bool bad = false;
+  if (warp < kMaxExperts / 32) {
+    if (tid < E) {
+      const int o = a.offsets[tid], end = a.offsets[tid + 1], L = end - o;
+      bad = o < 0 || end < o || end > a.R;
+      if (!bad) n = (L + a.max_rows - 1) / a.max_rows;
+      S.off[tid] = o;
+      if (tid == E - 1) S.off[E] = end;
+      S.size[tid] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
+    }
+    before = exclusive_sum(n);
+    if (lane == 31) S.sum[warp] = before + n;
+  }
+  // (The vote tells the compiler that all lanes know the same, and with it how long their
+  // loops are: without it a stage took 8 % longer.)
+  bad = __any_sync(kAll, __syncthreads_or(bad));
+  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
+  int chunks = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    if (w == warp) before += chunks;
+    chunks += S.sum[w];
+  }
+  if (bad) chunks = 0;
+  if (tid < E) S.first[tid] = before;
+  if (tid == 0) S.first[E] = chunks;
+  __syncthreads();
+  return uniform(chunks);
+}
+
 // tmB32: the rows again, in boxes of 32, for chunks that do not fill a box of 128.
 template <int WAY>
 __global__ void __launch_bounds__(kGThreads, 1)
@@ -112,7 +150,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __shared__ Segments S;
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  const int E = a.E;
   const uint32_t rank = pair_rank();  // 0 = leader (issues the MMAs)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -147,38 +184,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  // Segments and their chunks (ceil(rows / max_rows) near-equal ones), an expert a thread.
-  // Offsets that fall or leave [0, R] are refused as a whole: no row is touched.
-  static_assert(kMaxExperts <= kGThreads, "an expert a thread");
-  int n = 0, before = 0;
-  bool bad = false;
-  if (warp < kMaxExperts / 32) {
-    if (tid < E) {
-      const int o = a.offsets[tid], end = a.offsets[tid + 1], L = end - o;
-      bad = o < 0 || end < o || end > a.R;
-      if (!bad) n = (L + a.max_rows - 1) / a.max_rows;
-      S.off[tid] = o;
-      if (tid == E - 1) S.off[E] = end;
-      S.size[tid] = n > 0 ? ((L + n - 1) / n + 15) / 16 * 16 : 0;
-    }
-    before = exclusive_sum(n);
-    if (lane == 31) S.sum[warp] = before + n;
-  }
-  // (The vote tells the compiler that all lanes know the same, and with it how long their
-  // loops are: without it a stage took 8 % longer.)
-  bad = __any_sync(kAll, __syncthreads_or(bad));
-  if (bad && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kDevErrBadIds);
-  int chunks = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxExperts / 32; ++w) {
-    if (w == warp) before += chunks;
-    chunks += S.sum[w];
-  }
-  if (bad) chunks = 0;
-  if (tid < E) S.first[tid] = before;
-  if (tid == 0) S.first[E] = chunks;
-  __syncthreads();
-  const int total = uniform(chunks) * a.m_tiles;
+  const int total = scan_chunks(a, S) * a.m_tiles;
   const uint32_t tmem_base = uniform(tmem_base_s);
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t peer_abort = peer_addr(smem_u32(&abort_s), rank ^ 1u);
@@ -371,6 +377,227 @@ __global__ void __launch_bounds__(kGThreads, 1)
   }
 }
 
+// Few chunks of few rows: a cluster a tile of 128 features x up to 64 rows, whose CTAs take a
+// share of the reduction each (a.splits of them) with MMAs of their own, M = 128. Their
+// sums, fp32, go to the CTA of the row in the cluster, which adds them in the CTAs' order.
+//
+// An SM takes in 64 bytes a cycle, 140 ns for 128 x 64 weights, whatever the rows are: what
+// bounds a tile is the weights' way into its SMs, and 2048 x 2048 of them are 16 SMs' in
+// the form above.
+constexpr int kFewRows = 64, kFewStages = 7;
+constexpr int kFewBytes = kGHalf + kFewRows * kGK * 2;   // of a stage
+constexpr int kFewProd0 = 5;                             // after the issuer and four of the epilogue
+constexpr int kFewThreads = (kFewProd0 + kFewStages) * 32;
+constexpr int kFewSums = kFewRows * 128 * 4;             // of all CTAs, for this one's rows
+constexpr int kFewSmemBytes = kFewStages * kFewBytes + kFewSums + 1024;
+static_assert(kMaxExperts <= kFewThreads, "an expert a thread");
+
+template <int WAY>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    product_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmB32, const ProductArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kFewStages + 1];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ Segments S;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int rank = uniform((int)pair_rank());
+  uint64_t *full = bars, *empty = full + kFewStages, *tfull = empty + kFewStages;
+  if (tid == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB32);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tmem_base_s), kFewRows);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_barrier();  // every CTA is there to be written to
+  pdl_wait();
+  pdl_trigger();
+  const int total = scan_chunks(a, S) * a.m_tiles;
+  const int tile = blockIdx.x / a.splits;
+  const bool active = tile < total;
+  const uint32_t tmem_base = uniform(tmem_base_s);
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sums = smem_base + kFewStages * kFewBytes;
+  // This CTA's stages of the reduction.
+  const int nk = (a.D + kGK - 1) / kGK, share = (nk + a.splits - 1) / a.splits;
+  const int kb0 = min(rank * share, nk), cnt = min(share, nk - kb0);
+  GTile t = {};
+  int n = 0, own = 0;  // columns of the accumulator; of those, the rows of a CTA
+  if (active) {
+    t = tile_at(tile, a, S);
+    n = (t.nrows + 15) & ~15;
+    own = n / a.splits;
+  }
+  auto fail = [&]() { atomicOr(a.err, kDevErrTimeout); };
+
+  if (!active) {
+  } else if (warp >= kFewProd0) {
+    // One warp a ring slot, as above.
+    const int slot = warp - kFewProd0;
+    const bool leader = elect_one();
+    const uint32_t st = smem_base + slot * kFewBytes;
+    const uint32_t fb = smem_u32(&full[slot]), eb = smem_u32(&empty[slot]);
+    const uint64_t pol_w = t.one ? l2_policy_evict_first() : l2_policy_evict_normal(),
+                   pol_keep = l2_policy_evict_last();
+    const int f = t.m * 128, boxes = (n + 31) / 32;
+    const bool upper = WAY == kForward || f + 64 < a.F;  // (see product_kernel)
+    const uint32_t bytes = (upper ? kGHalf : kGBox) + (uint32_t)boxes * 32 * kGK * 2;
+    bool ok = true;
+    for (int j = slot, use = 0; j < cnt; j += kFewStages, ++use) {
+      if (!warp_wait(eb, (use & 1) ^ 1)) {
+        fail();
+        ok = false;
+        break;
+      }
+      const int k = (kb0 + j) * kGK;
+      if (leader) {
+        mbar_arrive_expect_tx(fb, bytes);
+        if (WAY == kForward) {
+          tma_load_3d(st, &tmA, fb, k, f, t.e, pol_w);
+        } else {
+          tma_load_3d(st, &tmA, fb, f, k, t.e, pol_w);
+          if (upper) tma_load_3d(st + kGBox, &tmA, fb, f + 64, k, t.e, pol_w);
+        }
+        for (int i = 0; i < boxes; ++i)
+          tma_load_2d(st + kGHalf + i * (32 * kGK * 2), &tmB32, fb, k, t.row0 + 32 * i, pol_keep);
+      }
+      __syncwarp();
+    }
+    if (!ok) {  // copies issued before may still be landing
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 50000ull) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    const bool leader = elect_one();
+    constexpr bool a_mn = WAY == kDx;
+    const uint32_t idesc = idesc_16(a.fp16 != 0, a_mn, false) | idesc_shape(128, n);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < cnt; ++j) {
+      if (!warp_wait(smem_u32(&full[s]), ph)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      if (leader) {
+        const uint32_t st = smem_base + s * kFewBytes;
+        const uint64_t da = a_mn ? sdesc_mnmajor(st, kGBox) : sdesc_kmajor<128>(st);
+        const uint64_t db = sdesc_kmajor<128>(st + kGHalf);
+        constexpr uint64_t ia = a_mn ? 16 * 128 / 16 : 2, ib = 2;
+        const int steps = min(4, (a.D - (kb0 + j) * kGK + 15) / 16);
+        for (int kk = 0; kk < steps; ++kk)
+          umma_bf16(tmem_base, da + kk * ia, db + kk * ib, idesc, (j | kk) != 0);
+        umma_commit(smem_u32(&empty[s]));
+      }
+      __syncwarp();
+      if (++s == kFewStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    if (leader) umma_commit(smem_u32(tfull));
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    if (!warp_wait(smem_u32(tfull), 0)) fail();
+    tc_fence_after();
+    int to = 0, i = 0;  // CTA and place of the next column
+    uint32_t dst = peer_addr(sums, 0) + (rank * own * 128 + q * 32 + lane) * 4;
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + c0, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j < n) {
+          st_cluster_u32(dst + i * 512, cnt > 0 ? v[j] : 0u);
+          if (++i == own) {
+            i = 0;
+            ++to;
+            dst = peer_addr(sums, min(to, a.splits - 1)) + (rank * own * 128 + q * 32 + lane) * 4;
+          }
+        }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // all sums are in
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kFewRows);
+  }
+  // Eight features of a row a thread.
+  for (int i = tid; i < own * 16; i += kFewThreads) {
+    const int c = i >> 4, ch = i & 15, row = rank * own + c, f = t.m * 128 + ch * 8;
+    if (row >= t.nrows || f >= a.F) continue;
+    float v[8] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(
+          smem_raw + (sums - smem_u32(smem_raw)) + ((s * own + c) * 128 + ch * 8) * 4);
+      const float4 x = p[0], y = p[1];
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    uint4 o;
+    o.x = pack16x2(v[0], v[1], a.fp16);
+    o.y = pack16x2(v[2], v[3], a.fp16);
+    o.z = pack16x2(v[4], v[5], a.fp16);
+    o.w = pack16x2(v[6], v[7], a.fp16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(t.row0 + row) * a.F + f) = o;
+  }
+}
+
+template <int WAY>
+cudaError_t launch_few(const CUtensorMap& tmA, const CUtensorMap& tmB32, const ProductArgs& a,
+                       int clusters, cudaStream_t st) {
+  static DeviceFlags attr_done;
+  if (cudaError_t e = smem_attr_once(attr_done, product_few_kernel<WAY>, kFewSmemBytes);
+      e != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * a.splits));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, product_few_kernel<WAY>, tmA, tmB32, a);
+}
+
+// CTAs that share a tile's reduction: as many as the chip holds at once (12 clusters of
+// eight, 36 of four); 0: the form of pairs, where it takes less by these estimates, in us
+// (a stage 0.14 and 0.2, the way of a row's sums 0.025). Measured, pairs and this: 1 row x
+// 128 x 2048 7.6 and 4.8; 16 rows x 1024 x 2048 8.0 and 5.3, x 2048 x 2048 8.1 and 6.3; 64
+// rows 8.1 and 7.7; 128 rows x 1024 x 1024 6.0 and 6.6.
+int few_splits(long long clusters, int R, int D) {
+  const int nk = (D + kGK - 1) / kGK, s = clusters <= 12 ? 8 : clusters <= 36 ? 4 : 0;
+  if (s == 0) return 0;
+  const double few = 3.9 + 0.2 * ((nk + s - 1) / s) + 0.025 * std::min(R, kFewRows);
+  return few + 0.3 < 3.3 + 0.14 * nk ? s : 0;
+}
+
 template <int WAY>
 cudaError_t launch_way(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB32,
                        const ProductArgs& a, long long max_tiles, int num_sms, cudaStream_t st) {
@@ -425,6 +652,13 @@ cudaError_t launch_grouped_product(bool transposed, const void* x, const void* w
   CUtensorMap tmA, tmB, tmB32;
   if (!make_map(&tmA, w, E, N, K, transposed ? 64 : 128) || !make_map(&tmB32, x, 0, R, a.D, 32))
     return cudaErrorInvalidValue;
+  const long long few = std::min<long long>(R, (R + 63LL * E) / kFewRows) * ((a.F + 127) / 128);
+  if (a.splits = few_splits(few, R, a.D); a.splits > 0) {
+    a.m_tiles = (a.F + 127) / 128;
+    a.max_rows = kFewRows;
+    return transposed ? launch_few<kDx>(tmA, tmB32, a, (int)few, st)
+                      : launch_few<kForward>(tmA, tmB32, a, (int)few, st);
+  }
   // A CTA's half of a chunk has at most 96 rows where these say so: the large box goes
   // unused (describing it takes the host 0.3 us).
   tmB = tmB32;

@@ -190,6 +190,30 @@ def test_weights_of_many_segments_beyond_the_cache(E, R, N, K):
     assert torch.equal(mm.mm_grouped_product_dw(dy, x, off), got)
 
 
+@pytest.mark.parametrize("lens,lead,trail", [([1], 0, 0), ([0, 3, 0, 1, 2], 2, 1), ([64], 0, 5),
+                                             ([17, 0, 40], 3, 0), ([130], 0, 0), ([65, 33], 1, 1)])
+@pytest.mark.parametrize("F,D", [(8, 2048), (72, 1416), (128, 1992), (520, 1096), (1000, 4104)])
+@pytest.mark.parametrize("dtype", [B, H])
+def test_few_rows_of_long_reductions(lens, lead, trail, F, D, dtype):
+    """The reduction shared out among a cluster's blocks, forward and dx."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    R, off = sum(lens) + lead + trail, _offsets(lens, lead)
+    a, b = lead, R - trail
+    for way, shape in (("forward", (F, D)), ("dx", (D, F))):
+        w = _rand(g, len(lens), *shape, dtype=dtype, std=0.1)
+        x = _rand(g, R, D, dtype=dtype)
+        x[:a], x[b:] = float("inf"), float("nan")
+        out = torch.full((R, F), 3.0, dtype=dtype, device="cuda")
+        f = mm.mm_grouped_product if way == "forward" else mm.mm_grouped_product_dx
+        f(x, w, off, out=out)
+        want, mag = ref.product(x, w, off, way)
+        ref.close(out[a:b], want[a:b], mag[a:b], D + 16, way)
+        assert (out[:a] == 3).all() and (out[b:] == 3).all()
+        again = torch.full_like(out, 3.0)
+        f(x, w, off, out=again)
+        assert torch.equal(again, out)
+
+
 def test_another_experts_infinities_stay_with_it():
     """Segments share tiles and stages of rows; their values do not meet."""
     lens = [37, 90, 5, 64]
