@@ -14,21 +14,23 @@
 //
 // The token rows are the N side because its size goes in steps of 16: a segment
 // is cut into near-equal chunks of at most 256 rows (fewer where there would be too few
-// tiles, see chunk_rows), and nothing is computed for rows it does not have. W is not transposed in memory: where the reduction runs
-// along its rows, a tile of 64 rows x 64 columns (128 bytes a row, 128-byte
-// swizzle) is an MN-major operand, and the MMA is told so.
+// tiles, see chunk_rows), and nothing is computed for rows it does not have. W is not
+// transposed in memory: where the reduction runs along its rows, a tile of 64 rows x 64
+// columns (128 bytes a row, 128-byte swizzle) is an MN-major operand, and the MMA is told so.
 //
 // Edges. Columns beyond a matrix are zeros out of the copy, and so are W's rows
-// beyond an expert's (W is a 3-D tensor to the copies) in a box that has some of it. Rows beyond a segment
-// belong to another expert; they give columns of the accumulator that nobody reads.
+// beyond an expert's (W is a 3-D tensor to the copies) in a box that has some of it. Rows
+// beyond a segment belong to another expert; they give columns of the accumulator that
+// nobody reads.
 //
 // What bounds it, on one GB300: 512 rows over 128 experts x 1536 x 2048 are the weights'
-// bytes, 113 us (7.0 TB/s). 32768 rows of uneven load over them take 181 us forward, and
-// dx of the down product (2048 x 768) 100; their bytes at the copy rate 154 and 87. The
+// bytes, 111 us (7.2 TB/s). 32768 rows of uneven load over them take 180 us forward, and
+// dx of the down product (2048 x 768) 99; their bytes at the copy rate 154 and 87. The
 // SMs take in 2.3 GB there, 13 TB/s out of L2: an expert of more than 256 rows reads its
 // weights for each chunk (168 us with 256 rows each). 1024 rows an expert run at 1.75
-// PFLOP/s. 5003 rows over 60 experts x 1000 x 1016 take 26 us, of 21, in 2.5 rounds of
-// tiles.
+// PFLOP/s. 5003 rows over 60 experts x 1000 x 1016 take 24 us, of 21, in 2.5 rounds of
+// tiles. Rows whose bytes are no multiple of 128 cost each copy two lines for one: 28600
+// rows over 40 x 1680 x 1344 take 90 us, x 1352 140. One row x 64 x 64 takes 3.3 us.
 #include <algorithm>
 #include <cmath>
 
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
 // the form above.
 constexpr int kFewRows = 64, kFewStages = 7;
 constexpr int kFewBytes = kGHalf + kFewRows * kGK * 2;   // of a stage
-constexpr int kFewProd0 = 5;                             // after the issuer and four of the epilogue
+constexpr int kFewProd0 = 5;                             // after the issuer, four epilogues
 constexpr int kFewThreads = (kFewProd0 + kFewStages) * 32;
 constexpr int kFewSums = kFewRows * 128 * 4;             // of all CTAs, for this one's rows
 constexpr int kFewSmemBytes = kFewStages * kFewBytes + kFewSums + 1024;

@@ -12,12 +12,12 @@
 //
 // Long segments take one MMA over the pair instead, as in grouped_product.cu (PAIR: M =
 // 256, half of the other operand in each CTA, 32 KB of shared memory a stage for 48).
-// Why not all: a segment of some 256 rows is four stages, 2000 cycles of MMAs, after which 64 KB leave each SM. Signals between
-// the CTAs queue behind those stores (measured: 2.2 us from the last MMA to the
-// pair's completion signal, 1.6 us back from the epilogue), and with two accumulators
-// that is what 32768 rows x 128 experts x 1536 x 2048 wait for: 264 us, where the
-// form of two MMAs took 189. Its accumulators' signals stay within a CTA; only the ring's
-// slots, which are filled ahead, are handed over between the two.
+// Why not all: a segment of some 256 rows is four stages, 2000 cycles of MMAs, after
+// which 64 KB leave each SM. Signals between the CTAs queue behind those stores (measured:
+// 2.2 us from the last MMA to the pair's completion signal, 1.6 us back from the epilogue),
+// and with two accumulators that is what 32768 rows x 128 experts x 1536 x 2048 wait for:
+// 264 us, where the form of two MMAs took 189. Its accumulators' signals stay within a CTA;
+// only the ring's slots, which are filled ahead, are handed over between the two.
 //
 // Rows beyond a segment belong to another expert: the last stage is cut to whole
 // steps of 16 rows, and where those hold rows of the next segment the issuing
@@ -708,8 +708,8 @@ cudaError_t launch_tiles(const CUtensorMap& tmA, const CUtensorMap& tmB, const C
       e != cudaSuccess)
     return e;
   static std::atomic<int> resident[kMaxDevices];
-  return launch_clusters(dw_kernel<BN, PAIR>, kCtas, resident, Ring<BN, PAIR>::kThreads, Ring<BN, PAIR>::kSmemBytes,
-                         items, num_sms, st, tmA, tmB, tmC, tmP, a);
+  return launch_clusters(dw_kernel<BN, PAIR>, kCtas, resident, Ring<BN, PAIR>::kThreads,
+                         Ring<BN, PAIR>::kSmemBytes, items, num_sms, st, tmA, tmB, tmC, tmP, a);
 }
 
 struct Split {
@@ -724,8 +724,8 @@ struct Split {
 //
 // A row costs a tile 5.1 ns on its cluster at 256 columns (24576 rows x 2048 x 2048: 125
 // us), 4.6 with MMAs over the pair (113) and 3.2 at 128 (32768 x 64 x 64 in one piece:
-// 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are taken to be of equal length, the
-// longest of several half as long again. Cut into parts, the tiles are more, but the
+// 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are
+// taken to be of equal length, the longest of several half as long again. Cut into parts, the tiles are more, but the
 // parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
 // them. Parts need the narrow tiles, and fp32 results where segments have several slices.
 //

@@ -18,10 +18,10 @@
 //
 // A group of 4 to 256 lanes takes a row, 8 columns a lane and step: a block of 32
 // is four lanes, its largest magnitude two exchanges; the sum for dw runs over a
-// lane's steps and then over the lanes and warps, the same on every call. The kernels read and
-// write every byte once and are bound by memory: 32768 rows of 768 bf16 take 34 us to
-// pack (203 MB, 5.9 TB/s; 190 instructions a step of 16 values, the ALU 65 % busy), 41
-// backward (253 MB, 6.2 TB/s), 23 back to bf16 (6.5 TB/s); 512 rows 2 to 3 us each.
+// lane's steps and then over the lanes and warps, the same on every call. The kernels
+// read and write every byte once and are bound by memory: 32768 rows of 768 bf16 take 34
+// us to pack (203 MB, 5.9 TB/s; 190 instructions a step of 16 values, the ALU 65 % busy),
+// 41 backward (253 MB, 6.2 TB/s), 23 back to bf16 (6.5 TB/s); 512 rows 1.7, 2.3 and 1.8.
 #include <algorithm>
 
 #include <cuda_fp16.h>
