@@ -399,18 +399,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     product_few_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB32, const ProductArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kFewStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kFewStages + 2];
   __shared__ uint32_t tmem_base_s;
   __shared__ Segments S;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int rank = uniform((int)pair_rank());
-  uint64_t *full = bars, *empty = full + kFewStages, *tfull = empty + kFewStages;
+  uint64_t *full = bars, *empty = full + kFewStages, *tfull = empty + kFewStages,
+           *got = tfull + 1;  // got: the sums of every CTA
   if (tid == 0) {
     for (int s = 0; s < kFewStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(got), 1);
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB32);
@@ -516,33 +518,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int q = warp & 3;
     if (!warp_wait(smem_u32(tfull), 0)) fail();
     tc_fence_after();
-    int to = 0, i = 0;  // CTA and place of the next column
-    uint32_t dst = peer_addr(sums, 0) + (rank * own * 128 + q * 32 + lane) * 4;
+    // Into the ring, which the MMAs are done with, as [row][feature], and from there to the
+    // rows' CTAs in one copy each. (Stores to the other CTAs: 14 cycles for 32 values, 64
+    // rows x 1024 x 2048 6.7 us.)
+    const uint32_t mine = smem_base + (q * 32 + lane) * 4;
     for (int c0 = 0; c0 < n; c0 += 32) {
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + c0, v);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (c0 + j < n) {
-          st_cluster_u32(dst + i * 512, cnt > 0 ? v[j] : 0u);
-          if (++i == own) {
-            i = 0;
-            ++to;
-            dst = peer_addr(sums, min(to, a.splits - 1)) + (rank * own * 128 + q * 32 + lane) * 4;
-          }
-        }
+        if (c0 + j < n) st_shared_u32(mine + (c0 + j) * 512, cnt > 0 ? v[j] : 0u);
+    }
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 1) {
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(got), n * 512);
+      __syncwarp();
+      if (lane < a.splits)
+        bulk_copy_peer(peer_addr(sums + rank * own * 512, lane), smem_base + lane * own * 512,
+                       own * 512, peer_addr(smem_u32(got), lane));
     }
     __syncwarp();
   }
 
-  tc_fence_before();
-  __syncthreads();
-  cluster_barrier();  // all sums are in
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, kFewRows);
-  }
+  if (active && !warp_wait_cluster(smem_u32(got), 0)) fail();
   // Eight features of a row a thread.
   for (int i = tid; i < own * 16; i += kFewThreads) {
     const int c = i >> 4, ch = i & 15, row = rank * own + c, f = t.m * 128 + ch * 8;
@@ -561,6 +561,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     o.z = pack16x2(v[4], v[5], a.fp16);
     o.w = pack16x2(v[6], v[7], a.fp16);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(t.row0 + row) * a.F + f) = o;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // no CTA ends before the others have its sums
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kFewRows);
   }
 }
 
@@ -589,14 +596,14 @@ cudaError_t launch_few(const CUtensorMap& tmA, const CUtensorMap& tmB32, const P
 }
 
 // CTAs that share a tile's reduction: as many as the chip holds at once (12 clusters of
-// eight, 36 of four); 0: the form of pairs, where it takes less by these estimates, in us
-// (a stage 0.14 and 0.2, the way of a row's sums 0.025). Measured, pairs and this: 1 row x
-// 128 x 2048 7.6 and 4.8; 16 rows x 1024 x 2048 8.0 and 5.3, x 2048 x 2048 8.1 and 6.3; 64
-// rows 8.1 and 7.7; 128 rows x 1024 x 1024 6.0 and 6.6.
+// eight, 36 of four; 16 of eight took 10.8 us where four took 6.3); 0: the form of pairs,
+// where it takes less by these estimates, in us (a stage 0.14 and 0.2, the way of a row's
+// sums 0.02). Measured, pairs and this: 1 row x 128 x 2048 7.6 and 4.4; 16 rows x 1024 x 2048
+// 8.0 and 5.1, x 2048 x 2048 8.1 and 6.0; 64 rows 8.1 and 7.2.
 int few_splits(long long clusters, int R, int D) {
   const int nk = (D + kGK - 1) / kGK, s = clusters <= 12 ? 8 : clusters <= 36 ? 4 : 0;
   if (s == 0) return 0;
-  const double few = 3.9 + 0.2 * ((nk + s - 1) / s) + 0.025 * std::min(R, kFewRows);
+  const double few = 3.9 + 0.2 * ((nk + s - 1) / s) + 0.02 * std::min(R, kFewRows);
   return few + 0.3 < 3.3 + 0.14 * nk ? s : 0;
 }
 
