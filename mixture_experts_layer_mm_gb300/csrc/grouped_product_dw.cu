@@ -725,7 +725,8 @@ struct Split {
 // A row costs a tile 5.1 ns on its cluster at 256 columns (24576 rows x 2048 x 2048: 125
 // us), 4.6 with MMAs over the pair (113) and 3.2 at 128 (32768 x 64 x 64 in one piece:
 // 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are
-// taken to be of equal length, the longest of several half as long again. Cut into parts, the tiles are more, but the
+// taken to be of equal length, the longest of several half as long again. Cut into parts,
+// the tiles are more, but the
 // parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
 // them. Parts need the narrow tiles, and fp32 results where segments have several slices.
 //
