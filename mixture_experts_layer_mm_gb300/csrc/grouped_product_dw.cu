@@ -726,9 +726,9 @@ struct Split {
 // us), 4.6 with MMAs over the pair (113) and 3.2 at 128 (32768 x 64 x 64 in one piece:
 // 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are
 // taken to be of equal length, the longest of several half as long again. Cut into parts,
-// the tiles are more, but the
-// parts' fp32 results go to memory and back at 4 bytes a ps, and a second launch sums
-// them. Parts need the narrow tiles, and fp32 results where segments have several slices.
+// the tiles are more, but the parts' fp32 results go to memory and back at 4 bytes a ps, and
+// a second launch sums them. Parts need the narrow tiles, and fp32 results where segments
+// have several slices.
 //
 // MMAs over the pair pay from 768 rows a segment on where the clusters take several
 // tiles (128 experts x 1536 x 2048, even and uneven: 256 rows 264 / 257 us, where the

@@ -311,17 +311,18 @@ struct Shape {
 // The lanes of a row: a power of two that covers it in one step, at most 32; 16 instead
 // where that leaves fewer of them idle in the last step and the rows are many (352
 // columns, 44 lanes' worth: three steps of 16 lanes, where 32 idle in 20 of 64 places).
-// Up to the whole block where the rows are so few that two blocks an SM hold them (us,
+// Up to the whole block where the rows are so few that `per_sm` blocks an SM hold them (us,
 // pack and back: 512 x 768 2.1 -> 1.7 and 3.1 -> 2.3, 200 x 2048 4.4 -> 1.8 and 6.0 -> 2.4,
-// 1 x 768 1.6 -> 1.1 and 2.5 -> 1.7; up to four blocks, 1000 x 768 back 2.9 and 3.4).
-Shape shape_of(int R, int I) {
+// 1 x 768 1.6 -> 1.1 and 2.5 -> 1.7): four for pack, two for back (with two and four,
+// pack of 1000 x 2048 5.4 and 4.6, back of 1000 x 768 2.9 and 3.4).
+Shape shape_of(int R, int I, int per_sm) {
   Shape s = {};
   const int n = I / 8;
   s.lpr_log2 = 2;
   while (s.lpr_log2 < 5 && (1 << s.lpr_log2) < n) ++s.lpr_log2;
   if (s.lpr_log2 == 5 && (n + 15) / 16 * 16 < (n + 31) / 32 * 32 && R >= 8192) s.lpr_log2 = 4;
   while (s.lpr_log2 >= 5 && 1 << s.lpr_log2 < std::min(n, kSwThreads) &&
-         (long long)R << (s.lpr_log2 + 1) <= 2 * 152 * kSwThreads)
+         (long long)R << (s.lpr_log2 + 1) <= per_sm * 152 * kSwThreads)
     ++s.lpr_log2;
   s.u = std::min((n + (1 << s.lpr_log2) - 1) >> s.lpr_log2, 3);
   const int rows = kSwThreads >> s.lpr_log2;
@@ -332,7 +333,7 @@ Shape shape_of(int R, int I) {
 template <bool FP16>
 cudaError_t pack_as(const uint16_t* z, const int32_t* end, int R, int I, uint16_t* act,
                     int8_t* codes, uint8_t* scales, cudaStream_t st) {
-  const Shape s = shape_of(R, I);
+  const Shape s = shape_of(R, I, 4);
   auto k = s.u == 1 ? swiglu_pack_kernel<FP16, 1>
          : s.u == 2 ? swiglu_pack_kernel<FP16, 2> : swiglu_pack_kernel<FP16, 3>;
   return launch_k(k, dim3(s.blocks), dim3(kSwThreads), 0, st, true, z, end, R, I, s.lpr_log2, act,
@@ -343,7 +344,7 @@ template <bool FP16>
 cudaError_t unpack_as(const int8_t* codes, const uint8_t* scales, const uint16_t* da,
                       const float* row_w, const int32_t* end, int R, int I, uint16_t* dz,
                       uint16_t* act, float* d_row_w, cudaStream_t st) {
-  const Shape s = shape_of(R, I);
+  const Shape s = shape_of(R, I, 2);
   // Many rows want warps rather than loads a warp: 32768 x 768 take 40.6 us with six blocks
   // an SM and one step at a time, 44.5 with four and two, 52 with two and three. Where all
   // blocks are under way at once the loads count (us, as many steps as fit and one at a
