@@ -29,7 +29,7 @@ def _ids(T, E, k, seed=0, skew=True):
     return torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
 
 
-# One launch up to 8192 slots; spans of one chunk and of several beyond.
+# One launch up to 16384 slots; spans of one chunk and of several beyond.
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (5, 3, 3), (33, 7, 2), (64, 128, 8),
                                    (1024, 60, 8), (1025, 60, 8), (4099, 256, 8), (9000, 1, 1),
                                    (700, 4, 32), (60001, 40, 10)])
