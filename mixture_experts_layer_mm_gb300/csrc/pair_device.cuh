@@ -229,6 +229,12 @@ __device__ __forceinline__ void tma_add_3d(const void* map, uint32_t src, int c0
       "r"(src), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+// Contiguous bytes (a multiple of 16, both sides 16-byte aligned), in the same groups.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
