@@ -256,6 +256,55 @@ def test_bad_offsets_write_nothing(bad):
     assert (o == 2).all()
 
 
+@pytest.mark.parametrize("bad", [[0, 30, 20, 50], [0, 10, 20, 51], [-1, 10, 20, 50]])
+def test_bad_offsets_of_few_rows_write_nothing(bad):
+    """Where a cluster's blocks share the reduction; the next call is sound again."""
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = _rand(g, 50, 2048), _rand(g, 3, 136, 2048, std=0.1)
+    wt = w.transpose(1, 2).contiguous()
+    good = _offsets([20, 0, 30])
+    want, mag = ref.product(x, w, good, "forward")
+    for f, m in ((mm.mm_grouped_product, w), (mm.mm_grouped_product_dx, wt)):
+        o = torch.full((50, 136), 2.0, device="cuda").bfloat16()
+        f(x, m, off, out=o)
+        assert mm.mm_poll_device_status() == mm.MM_ERR_DEVICE
+        assert (o == 2).all()
+        ref.close(f(x, m, good, out=o), want, mag, 2048 + 16)
+
+
+def test_few_rows_on_streams_and_in_graphs():
+    """Calls that run at the same time, captured and not, with their own offsets."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = [_rand(g, 48, 2048) for _ in range(2)]
+    w = [_rand(g, 4, 520, 2048, std=0.1) for _ in range(2)]
+    off = [_offsets([10, 0, 33, 5]), _offsets([1, 40, 0, 7])]
+    want = [mm.mm_grouped_product(x[i], w[i], off[i]) for i in range(2)]
+    outs = [torch.empty_like(o) for o in want]
+    graphs = []
+    for i in range(2):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                mm.mm_grouped_product(x[i], w[i], off[i], out=outs[i])
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            outs[i].fill_(7)
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            eager = [mm.mm_grouped_product(x[i], w[i], off[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i]) and torch.equal(eager[i], want[i])
+
+
 def test_buffers_aligned_to_16_bytes_only():
     g = torch.Generator(device="cuda").manual_seed(3)
     R, N, K = 70, 72, 136

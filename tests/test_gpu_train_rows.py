@@ -211,3 +211,14 @@ def test_streams_and_graphs_share_nothing():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want[1]))
+
+
+def test_groups_of_a_cluster_at_the_same_time():
+    ids = [_ids(1000 + 400 * s, 64, 8, seed=s) for s in range(2)]
+    want = [mm.mm_group_slots(i, 64) for i in ids]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[mm.mm_group_slots(ids[i], 64, stream=streams[i]) for i in range(2)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(x, y) for a, b in zip(pair, want) for x, y in zip(a, b))
