@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int f = t.m * 256 + (int)rank * 128;
       // Boxes wholly beyond W's features are left out, nobody reads what they give: zeros
       // take a copy longer than values (22886 rows x 128 x 128: 12.1 us with, 7.3 without).
-      const int halves = min(max((a.F - f + 63) / 64, 0), 2);  // of 64 features
-      const uint32_t bytes = (WAY == kForward ? (halves > 0 ? kGHalf : 0) : halves * kGBox) +
+      const bool lower = f < a.F, upper = WAY == kForward ? lower : f + 64 < a.F;
+      const uint32_t bytes = (upper ? kGHalf : lower ? kGBox : 0) +
                              (nh > 96 ? kGHalf : (uint32_t)boxes * 32 * kGK * 2);
       // W is read by every chunk of the expert, the rows by every m-tile.
       const uint64_t pol_w = t.one ? pol_once : pol_normal;
@@ -240,10 +240,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
         if (leader) {
           mbar_expect_tx_cluster(fb, bytes);
           if (WAY == kForward) {
-            if (halves > 0) tma_load_3d_pair(st, &tmA, fb, kb * kGK, f, t.e, pol_w);
+            if (lower) tma_load_3d_pair(st, &tmA, fb, kb * kGK, f, t.e, pol_w);
           } else {
-            if (halves > 0) tma_load_3d_pair(st, &tmA, fb, f, kb * kGK, t.e, pol_w);
-            if (halves > 1) tma_load_3d_pair(st + kGBox, &tmA, fb, f + 64, kb * kGK, t.e, pol_w);
+            if (lower) tma_load_3d_pair(st, &tmA, fb, f, kb * kGK, t.e, pol_w);
+            if (upper) tma_load_3d_pair(st + kGBox, &tmA, fb, f + 64, kb * kGK, t.e, pol_w);
           }
           if (nh > 96) {
             tma_load_2d_pair(st + kGHalf, &tmB, fb, kb * kGK, brow, pol_keep);
