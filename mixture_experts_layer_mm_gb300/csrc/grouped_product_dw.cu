@@ -6,9 +6,10 @@
 // MN-major: tiles of 64 rows x 64 columns (128 bytes a row, 128-byte swizzle) as
 // they lie in memory, no transpose. A tile of the result is 256 features n x bn
 // (256 or 128) features k, made by a cluster of two CTAs: each has 128 of the
-// features n, its own accumulators and its own MMAs (M = 128), and each loads half of
-// the other operand for both (TMA multicast), so that a stage brings 32 KB into an
-// SM instead of 48.
+// features n, its own accumulators, its own copies and its own MMAs (M = 128). A stage
+// of 256 columns brings 48 KB into an SM, 32 of which the other CTA reads too: out of
+// L2, since the two run side by side. (Half of that loaded by each CTA and handed to the
+// other through distributed shared memory: 301 us where this takes 188.)
 //
 // Long segments take one MMA over the pair instead, as in grouped_product.cu (PAIR: M =
 // 256, half of the other operand in each CTA, 32 KB of shared memory a stage for 48).
@@ -16,8 +17,7 @@
 // which 64 KB leave each SM. Signals between the CTAs queue behind those stores (measured:
 // 2.2 us from the last MMA to the pair's completion signal, 1.6 us back from the epilogue),
 // and with two accumulators that is what 32768 rows x 128 experts x 1536 x 2048 wait for:
-// 264 us, where the form of two MMAs took 189. Its accumulators' signals stay within a CTA;
-// only the ring's slots, which are filled ahead, are handed over between the two.
+// 264 us, where the form of two MMAs takes 188. All of its signals stay within a CTA.
 //
 // Rows beyond a segment belong to another expert: the last stage is cut to whole
 // steps of 16 rows, and where those hold rows of the next segment the issuing
@@ -25,7 +25,7 @@
 // NaN). Columns beyond a matrix are zeros out of the copy. The results leave
 // through shared memory as boxes of 32 rows x 128 bytes, which the copy cuts at the
 // matrix's edges (stores out of registers, 32 bytes a lane in 32 rows: 245 us where
-// boxes take 191).
+// boxes took 191).
 //
 // fp32 results (and parts, below) are made of kSliceRows rows of the segment at a time:
 // the tensor cores cut what they add, and 512 rows leave 5e-7 of it where 4096 leave
@@ -39,13 +39,13 @@
 // results go to the workspace and are summed in order by a second launch (the rule is
 // at split_of).
 //
-// What bounds it, on one GB300: the case above takes 172 us with even segments and 195
-// to 210 with uneven ones (154 at the copy rate of its bytes; 120 for its results alone).
-// 1.6 GB of loads and 0.8 GB of stores pass between L2 and the SMs, 14 TB/s (without the
-// stores 134 us, 12 TB/s), and shared memory moves 512 KB a tile. With the rows in L2 from
-// before it takes 165. Long
-// segments run at 1.64 to 1.82 PFLOP/s (two MMAs: 1.5, bound by shared memory). Few
-// narrow tiles wait for their ring: a slot's turn takes 1.2 us.
+// What bounds it, on one GB300: the case above takes 188 us with even segments and 207
+// with uneven ones (154 at the copy rate of its bytes; 120 for its results alone). 2.4 GB
+// of loads and 0.8 GB of stores pass between L2 and the SMs, 17 TB/s, and shared memory
+// moves 512 KB a tile. Long segments run at 1.64 to 1.82 PFLOP/s (two MMAs: 1.5, bound by
+// shared memory). Few narrow tiles wait for their ring: a slot's turn takes 1.2 us, longer
+// where the rows are no whole number of lines (20011 rows x 8 experts x 640 x 328: 26 us, x
+// 320 21).
 #include <algorithm>
 #include <cmath>
 
@@ -157,11 +157,10 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
   uint64_t* land = done + 1;  // PAIR: this CTA's copies of a segment's last stage
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      // A CTA's copies and MMAs are its own, but half of an operand comes from the other,
-      // which therefore waits for both. PAIR: the leader's barrier counts both CTAs' copies,
-      // and its MMAs free the slots of both.
+      // A CTA's copies and MMAs are its own. PAIR: the leader's barrier counts both CTAs'
+      // copies, and its MMAs free the slots of both.
       mbar_init(smem_u32(&full[s]), PAIR ? kCtas : 1);
-      mbar_init(smem_u32(&empty[s]), PAIR ? 1 : kCtas);
+      mbar_init(smem_u32(&empty[s]), 1);
       if (PAIR) mbar_init(smem_u32(&land[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -285,13 +284,12 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
       if (aborted()) break;
       const Item t = item_at(i);
       const int nsl = slices(t), step = slice_rows(t);
-      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN + (int)rank * (BN / 2);
+      const int f = (t.m * kCtas + (int)rank) * 128, c = t.n * BN + (PAIR ? (int)rank * (BN / 2) : 0);
       if (BN == 256 && !PAIR && a.ahead && i + npairs < total) {
         const Item u = item_at(i + npairs);
         const int uf = (u.m * kCtas + (int)rank) * 128, uc = u.n * BN + (int)rank * (BN / 2);
         if (leader) {
-          // Boxes 2 * stage + column block, shared out among the tiles that read them (all by
-          // the first tile of each: 179 us for 172, see ahead_of).
+          // Boxes 2 * stage + column block, shared out among the tiles that read them.
           const int boxes = (u.rows + kRows - 1) / kRows * 2;
           for (int x = u.n + slot * a.n_tiles; x < boxes; x += kStages * a.n_tiles)
             if (uf + 64 * (x & 1) < a.N)
@@ -343,10 +341,9 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
               mbar_arrive_expect_tx(fb, bytes);
               tma_load_2d(st, &tmA, fb, f, r, pol);
               tma_load_2d(st + kBlock, &tmA, fb, f + 64, r, pol);
-              const uint32_t half = st + kABytes + rank * (R::kBoxes / 2) * kBlock;
 #pragma unroll
-              for (int b = 0; b < R::kBoxes / 2; ++b)
-                tma_load_2d_all(half + b * kBlock, &tmB, fb, c + 64 * b, r, all, pol);
+              for (int b = 0; b < R::kBoxes; ++b)
+                tma_load_2d(st + kABytes + b * kBlock, &tmB, fb, c + 64 * b, r, pol);
             }
             __syncwarp();
           }
@@ -424,7 +421,7 @@ __global__ void __launch_bounds__(Ring<BN, PAIR>::kThreads, 1)
               if (PAIR)
                 umma_pair_commit(smem_u32(&empty[s]), all);
               else
-                umma_commit_all(smem_u32(&empty[s]), all);
+                umma_commit(smem_u32(&empty[s]));
             }
             __syncwarp();
             if (++s == kStages) {
@@ -739,28 +736,41 @@ struct Split {
 // estimated time.
 //
 // A row costs a tile 5.1 ns on its cluster at 256 columns (24576 rows x 2048 x 2048: 125
-// us), 4.6 with MMAs over the pair (113) and 3.2 at 128 (32768 x 64 x 64 in one piece:
-// 103), a tile 0.3 us beside its rows, and the clusters take tiles in turn. Segments are
+// us), 4.6 with MMAs over the pair (115) and 3.2 at 128 (32768 x 64 x 64 in one piece:
+// 95); where x's rows are no whole number of 128-byte lines, each copy's row takes two for
+// one, which is 7 ns (x 2040: 178 us), 4.6 (119) and 4 (32768 x 64 x 72: 132). A tile takes
+// 0.3 us beside its rows, and the clusters take tiles in turn. Segments are
 // taken to be of equal length, the longest of several half as long again. Cut into parts,
 // the tiles are more, but the parts' fp32 results go to memory and back at 4 bytes a ps, and
 // a second launch sums them. Parts need the narrow tiles, and fp32 results where segments
 // have several slices.
 //
-// MMAs over the pair pay from 768 rows a segment on where the clusters take several
-// tiles (128 experts x 1536 x 2048, even and uneven: 256 rows 264 / 257 us, where the
-// other form takes 189 / 209; 512 rows 295 / 349 and 336 / 345; 768 rows 385 / 478 and 458
-// / 494), where they take one from 8192 on (2048 x 2048: 4096 rows 24.6 and 23.8).
+// MMAs over the pair, each of whose CTAs loads only its half of x, against two (16-bit
+// results; us):
+//   several tiles a cluster, from 512 rows a segment on (128 experts x 1536 x 2048, even and
+//   uneven: 256 rows 251 / 249 and 188 / 207, 512 rows 278 / 338 and 317 / 341, 640 rows 322
+//   / 415 and 389 / 404, 768 rows 370 / 429 and 448 / 470); from 224 on where x's copies
+//   touch two lines a row (x 1536 x 2040: 192 rows 260 / 260 and 237 / 258, 256 rows 265 /
+//   271 and 284 / 302; 60 x 1000 x 1016, 250 rows: 52.5 / 53.2 and 54.0 / 60.7), from 384
+//   where dy's do (x 1528 x 2048: 256 rows 246 / 257 and 222 / 243, 384 rows 272 / 297 and
+//   297 / 299);
+//   one tile a cluster, from 8192 on (2048 x 2048: 4096 rows 24.9 and 24.5); where x's copies
+//   do, from 1024 (x 2040: 512 rows 10.6 and 10.4, 1024 rows 13.3 and 14.2), dy's 2048
+//   (2040 x 2048: 1024 rows 13.2 and 12.4, 2048 rows 18.1 and 18.3, 4096 rows 25 and 29).
 // Not inlined: the reported size and the launch have to come to the same choice.
 __attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp32) {
   Split best = {};
   double least = 0;
   const double rows = (double)R / E;
+  const bool odd_k = K % 64 != 0, odd_n = N % 64 != 0;
   for (const int bn : {256, 128}) {
     if (bn == 256 && out_fp32 && rows > kSliceRows) continue;
     const int m = (N + 255) / 256, n = (K + bn - 1) / bn;
     const double tiles = (double)E * m * n;
-    const bool pair = bn == 256 && rows >= (tiles > kPairs ? 768 : 8192);
-    const double row = bn == 128 ? 3.2 : pair ? 4.6 : 5.1;
+    const bool pair =
+        bn == 256 && !out_fp32 && rows >= (tiles > kPairs ? (odd_k ? 224 : odd_n ? 384 : 512)
+                                                          : (odd_k ? 1024 : odd_n ? 2048 : 8192));
+    const double row = bn == 128 ? (odd_k ? 4.0 : 3.2) : pair ? 4.6 : odd_k ? 7.0 : 5.1;
     for (int parts = 1; parts <= (bn == 128 && R > 512 ? 128 : 1); ++parts) {
       Split s = {m, n, bn, pair, 0, E};
       double t = std::ceil(tiles * parts / kPairs) * (rows / parts * row + 300);
@@ -785,13 +795,13 @@ __attribute__((noinline)) Split split_of(int R, int E, int N, int K, bool out_fp
 
 // Whether the tiles' rows go to L2 ahead, a tile before the copies that read them. Under
 // the stream of results first reads take long, and many tiles wait for the same ones: with
-// 128 experts x 1536 x 2048, 256 rows each, 187 us and 172 with this (uneven 205 and 195;
-// 2048 x 768: 101 and 91), 180 rows 166 and 152; two to three tiles before: the same, more:
-// slower. Rows that are in L2 already are only read twice: below its size no gain
-// (60 x 1000 x 1016, 250 rows: 46 and 52). Nor with fp32 results (301 and 318) or for longer
-// segments, which are bound by their MMAs (384 rows, uneven: 271 and 276).
+// 128 experts x 1536 x 2048, 256 rows each, 191 us and 188 with this (uneven 210 and 207;
+// 2048 x 768: 103 and 101, 114 and 111), 180 rows 168 and 167 (180 and 175); 128 rows 151 and
+// 154. Rows that are in L2 already are only read twice: below its size no gain. Nor with fp32
+// results or for longer segments, which are bound by their MMAs (384 rows: 263 and 263).
 bool ahead_of(const Split& s, int R, int E, int N, int K, bool out_fp32) {
-  return s.bn == 256 && !s.pair && !out_fp32 && R <= 320LL * E && 2LL * R * (N + K) > 96LL << 20;
+  return s.bn == 256 && !s.pair && !out_fp32 && R >= 160LL * E && R <= 320LL * E &&
+         2LL * R * (N + K) > 96LL << 20;
 }
 
 }  // namespace

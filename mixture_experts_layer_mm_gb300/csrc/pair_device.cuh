@@ -132,34 +132,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
-// A box at the same place of the shared memory of every CTA in `mask`, counted on the
-// barrier at the same place of each.
-__device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const void* map, uint32_t bar,
-                                                 int c0, int c1, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1),
-      "h"(mask), "l"(policy)
-      : "memory");
-}
-
 // The box at (c0, c1), clipped as by a copy, into L2.
 __device__ __forceinline__ void tma_prefetch_2d(const void* map, int c0, int c1, uint64_t policy) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile.L2::cache_hint [%0, {%1, %2}], %3;" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1), "l"(policy)
                : "memory");
-}
-
-// One arrival on the barrier at `bar` in every CTA of `mask` once the MMAs of this CTA issued so
-// far by this thread have completed.
-__device__ __forceinline__ void umma_commit_all(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
 }
 
 // As warp_wait, and what the peer CTA's threads wrote before they arrived is visible.

@@ -431,3 +431,29 @@ def test_back_to_back_calls_wait_for_one_another():
         for i in range(6):
             y = mm.mm_grouped_product(y, w[i % 2], off)
         assert torch.equal(y, step[-1])
+
+
+@pytest.mark.parametrize("E,R,N,K", [(60, 15020, 1000, 1016), (128, 33000, 264, 520),
+                                     (40, 15800, 1000, 1024), (2, 2100, 520, 2040),
+                                     (1, 2049, 1000, 2048), (100, 51300, 264, 512)])
+@pytest.mark.parametrize("dtype", [B, H])
+def test_weights_where_copies_take_two_lines_a_row(E, R, N, K, dtype):
+    """Mean lengths from which dw's MMAs run over both CTAs: of rows that are no whole number
+    of 128-byte lines (of x, then of dy), and of others; a long segment, some of none."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    p = torch.exp(0.5 * torch.randn(E, generator=g, device="cuda"))
+    p[1::9] = 0
+    lens = torch.bincount(torch.multinomial(p, R, replacement=True, generator=g),
+                          minlength=E).tolist()
+    lead, trail = 2, 3
+    dy, x = (_rand(g, R + 5, c, dtype=dtype) for c in (N, K))
+    dy[:lead], x[:lead], dy[R + lead:], x[R + lead:] = [float("nan")] * 4
+    off = _offsets(lens, lead)
+    want, mag = ref.product(dy.nan_to_num(0), x.nan_to_num(0), off, "dw")
+    for out in (dtype, F):
+        got = mm.mm_grouped_product_dw(dy, x, off, out_dtype=out)
+        ref.close(got, want, mag, max(lens) + 16, "dw")
+        assert torch.equal(mm.mm_grouped_product_dw(dy, x, off, out_dtype=out), got)
+        old = _rand(g, E, N, K, dtype=out, std=30.0)
+        acc = mm.mm_grouped_product_dw(dy, x, off, out=old.clone(), accumulate=True)
+        ref.close(acc, want + old.double(), mag + old.double().abs(), max(lens) + 17, "accumulated")

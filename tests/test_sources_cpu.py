@@ -1,0 +1,36 @@
+"""What the kernels' sources may not hold: the library is one file that every process of
+a run on several GPUs loads too."""
+import glob
+import os
+import re
+
+import pytest
+
+from mixture_experts_layer_mm_gb300 import buildlib
+
+SOURCES = sorted(glob.glob(os.path.join(buildlib.CSRC, "*.cu*")))
+
+
+def _assembly(text):
+    """The inline assembly of a source, each statement's literals joined."""
+    for m in re.finditer(r"\basm\b(?:\s+volatile)?\s*\(", text):
+        end, out = m.end(), []
+        while literal := re.match(r"\s*(?:\"((?:[^\"\\]|\\.)*)\"|//[^\n]*\n)", text[end:]):
+            out.append(literal.group(1) or "")
+            end += literal.end()
+        yield "".join(out)
+
+
+def test_assembly_is_found():
+    found = [a for p in SOURCES for a in _assembly(open(p).read())]
+    assert sum("cp.async.bulk.tensor" in a for a in found) > 5
+    assert list(_assembly('asm volatile("a.b" // note\n ".c %0;" : "=r"(x)); asm("d;")')) == \
+        ["a.b.c %0;", "d;"]
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_copy_goes_to_several_blocks(path):
+    """A copy into the shared memory of several blocks at once is allowed only in code that
+    runs on one GPU alone."""
+    for a in _assembly(open(path).read()):
+        assert not ("cp.async.bulk" in a and "multicast" in a), a
