@@ -54,14 +54,38 @@ def moe_experts_train(hidden, topk_ids, topk_w, w_gate_up, w_down, token_mask=No
     return out, ExpertsSaved(hidden, places, offsets, row_w, codes, scales)
 
 
+def _check_backward(d_out, s: ExpertsSaved, w_gate_up, w_down, d_w_gate_up, d_w_down,
+                    accumulate: bool) -> None:
+    """Refuses what a later call of the step would, before the first one writes: a gradient
+    that one call had added to would be added to twice when the step is tried again."""
+    if accumulate and (d_w_gate_up is None or d_w_down is None):
+        raise ValueError("accumulate needs d_w_gate_up and d_w_down")
+    (T, H), E, I = s.hidden.shape, s.offsets.shape[0] - 1, s.codes.shape[1] // 2
+    up, down = (E, 2 * I, H), (E, H, I)
+    for t, shape, name in ((d_out, (T, H), "d_out"), (w_gate_up, up, "w_gate_up"),
+                           (w_down, down, "w_down"), (d_w_gate_up, up, "d_w_gate_up"),
+                           (d_w_down, down, "d_w_down")):
+        _lib._shape(t, shape, name)
+    for t, name in ((d_out, "d_out"), (w_gate_up, "w_gate_up"), (w_down, "w_down"),
+                    (d_w_gate_up, "d_w_gate_up"), (d_w_down, "d_w_down")):
+        fp32 = name.startswith("d_w") and t is not None and t.dtype == torch.float32
+        at = _lib._ptr(t, torch.float32 if fp32 else s.hidden.dtype, name)
+        if at is not None and at % 16 and T > 0:
+            raise ValueError(f"{name} must be 16-byte aligned")
+    _lib._device("moe_experts_train_backward", s.hidden, d_out, w_gate_up, w_down,
+                 d_w_gate_up, d_w_down)
+
+
 def moe_experts_train_backward(d_out, saved: ExpertsSaved, w_gate_up, w_down,
                                d_w_gate_up: Optional[torch.Tensor] = None,
                                d_w_down: Optional[torch.Tensor] = None, accumulate: bool = False,
                                weight_dtype=None, stream=None) -> ExpertsGrads:
     """The gradients of moe_experts_train for d_out [T, H]. d_w_gate_up and d_w_down:
-    results to write into, or to add to with accumulate (of the weights' type or
-    float32); weight_dtype: the type of new ones."""
+    results to write into, or to add to with accumulate, which needs both (of the weights'
+    type or float32); weight_dtype: the type of new ones. A call that is refused has
+    written nothing."""
     s = saved
+    _check_backward(d_out, s, w_gate_up, w_down, d_w_gate_up, d_w_down, accumulate)
     d_rows, _ = _lib.mm_dispatch_rows(d_out, s.places, stream=stream)
     da = _lib.mm_grouped_product_dx(d_rows, w_down, s.offsets, stream=stream)
     dz, act, d_row_w = _lib.mm_swiglu_pack_backward(s.codes, s.scales, da, row_w=s.row_w,

@@ -381,3 +381,31 @@ def test_the_first_calls_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_refused_backward_leaves_the_gradients():
+    """Whichever argument is refused, the gradients are as before, and the call made right
+    adds the micro-batch once."""
+    d = _inputs(40, 64, 6, 32, 2)
+    gu, dn, d_out = d["gu"], d["dn"], d["d_out"]
+    ids, w, _, _, _ = mm.mm_route_logits(d["logits"], 2, True)
+    _, s = mm.moe_experts_train(d["hidden"], ids, w, gu, dn)
+    ones = lambda t, dtype=torch.float32: torch.ones(t.shape, dtype=dtype, device="cuda")
+    d_gu, d_dn = ones(gu), ones(dn)
+    odd = torch.ones(gu.numel() + 1, device="cuda")[1:].view(gu.shape)
+    odd_gu = torch.zeros(gu.numel() + 1, device="cuda").bfloat16()[1:].view(gu.shape)
+    bad = [dict(d_w_gate_up=None), dict(d_w_down=None), dict(d_w_gate_up=d_gu[:5]),
+           dict(d_w_gate_up=d_gu.half()), dict(d_w_gate_up=d_gu.cpu()), dict(d_w_gate_up=odd),
+           dict(d_w_gate_up=ones(gu.transpose(1, 2)).transpose(1, 2)), dict(d_w_down=d_dn[:, :8]),
+           dict(gu=gu.half()), dict(gu=odd_gu), dict(gu=gu[:, :32]), dict(dn=dn[:3]), dict(dn=dn.float()),
+           dict(d_out=d_out.half()), dict(d_out=d_out[:7])]
+    for change in bad:
+        a = dict(d_out=d_out, gu=gu, dn=dn, d_w_gate_up=d_gu, d_w_down=d_dn) | change
+        with pytest.raises((TypeError, ValueError, mm.MMError)):
+            mm.moe_experts_train_backward(a["d_out"], s, a["gu"], a["dn"], a["d_w_gate_up"],
+                                          a["d_w_down"], accumulate=True)
+        assert (d_gu == 1).all() and (d_dn == 1).all() and (odd == 1).all()
+    want = mm.moe_experts_train_backward(d_out, s, gu, dn, weight_dtype=torch.float32)
+    mm.moe_experts_train_backward(d_out, s, gu, dn, d_gu, d_dn, accumulate=True)
+    assert torch.equal(d_gu, 1 + want.d_w_gate_up) and torch.equal(d_dn, 1 + want.d_w_down)
+    assert mm.mm_poll_device_status() == mm.MM_OK

@@ -192,3 +192,33 @@ def test_group_by_hand():
     places, offsets = ref.group(ids, 3, torch.tensor([True, True, True, False]))
     assert offsets.tolist() == [0, 2, 3, 5]
     assert places.tolist() == [[3, 0], [1, 4], [-1, 2], [-1, -1]]
+
+
+def test_a_refused_backward_makes_no_call(mmlib, monkeypatch):
+    """Both gradients are looked at before the first call, which would add to one."""
+    from mixture_experts_layer_mm_gb300 import _lib, experts_train
+    made = []
+    for name in ("mm_dispatch_rows", "mm_grouped_product_dx", "mm_grouped_product_dw",
+                 "mm_swiglu_pack_backward", "mm_combine_rows"):
+        monkeypatch.setattr(_lib, name, lambda *a, name=name, **k: made.append(name) or (a[0],) * 3)
+    b, E, H, I, T, k = torch.bfloat16, 3, 16, 32, 4, 2
+    s = experts_train.ExpertsSaved(
+        torch.zeros(T, H, dtype=b), torch.zeros(T, k, dtype=torch.int32),
+        torch.zeros(E + 1, dtype=torch.int32), torch.zeros(T * k),
+        torch.zeros(T * k, 2 * I, dtype=torch.int8), torch.zeros(T * k, I // 16, dtype=torch.uint8))
+    gu, dn = torch.zeros(E, 2 * I, H, dtype=b), torch.zeros(E, H, I, dtype=b)
+    d_gu, d_dn = torch.zeros(gu.shape), torch.zeros(dn.shape)
+
+    def call(match, error=ValueError, d_out=s.hidden, gu=gu, dn=dn, accumulate=True, **given):
+        with pytest.raises(error, match=match):
+            mm.moe_experts_train_backward(d_out, s, gu, dn, accumulate=accumulate, **given)
+
+    call("accumulate needs", d_w_down=d_dn)
+    call("accumulate needs", d_w_gate_up=d_gu)
+    call("accumulate needs")
+    call("d_w_gate_up must have shape", d_w_down=d_dn, d_w_gate_up=d_gu[:2], accumulate=False)
+    call("d_out must have shape", d_out=s.hidden[:2], d_w_down=d_dn, d_w_gate_up=d_gu)
+    call("w_gate_up must have shape", gu=gu[:, :32], d_w_down=d_dn, d_w_gate_up=d_gu)
+    call("CUDA", d_w_down=d_dn, d_w_gate_up=d_gu)
+    call("d_out must be torch", TypeError, d_out=s.hidden.float(), d_w_down=d_dn, d_w_gate_up=d_gu)
+    assert not made
