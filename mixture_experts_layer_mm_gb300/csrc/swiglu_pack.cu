@@ -347,12 +347,18 @@ cudaError_t unpack_as(const int8_t* codes, const uint8_t* scales, const uint16_t
   const Shape s = shape_of(R, I, 2);
   // Many rows want warps rather than loads a warp: 32768 x 768 take 40.6 us with six blocks
   // an SM and one step at a time, 44.5 with four and two, 52 with two and three. Where all
-  // blocks are under way at once the loads count (us, as many steps as fit and one at a
-  // time): two an SM, 2000 x 768 3.5 and 4.3; four, 4000 x 768 6.9 and 8.1, 5003 x 352 5.2 and
-  // 5.7. Three leave room for three of the next call's at one step, and none at two: 3000 x
-  // 768 6.4 and 5.2.
+  // blocks are under way at once the loads count: two blocks an SM take as many steps as
+  // fit (304 blocks of 768 columns 3.5 us, one at a time 4.0). Three leave room for three of
+  // the next call's at one step, and none at two (456 blocks 5.1 and 6.2). Four take two
+  // steps, which fill the SM, and so do up to 76 blocks more: a second round on half the
+  // SMs takes less than one step at a time loses. One step and two, in us, by blocks:
+  //                  480          608          626          650          684          720
+  //     352 columns  5.33  4.31   5.44  4.31   5.44  5.03   5.35  5.03   5.25  5.12   5.44  5.23
+  //     768          7.84  6.35   8.15  6.79   8.29  8.21   8.29  8.35   8.42  8.62   8.50  8.86
+  //    1056         12.07  9.52  12.39  9.79  12.43 11.62  12.49 11.76  12.60 11.91  12.77 12.57
+  //    2048         18.76 14.03  19.06 14.61  19.17 18.04  19.26 18.54  19.25 19.49  19.19 20.80
   const int per_sm = (int)((s.blocks + 151) / 152);
-  const int u = per_sm <= 2 ? s.u : s.u > 1 && per_sm > 3 && s.blocks <= 9 * 76 ? 2 : 1;
+  const int u = per_sm <= 2 ? s.u : s.u > 1 && per_sm > 3 && s.blocks <= 4 * 152 + 76 ? 2 : 1;
   auto k = u == 1 ? swiglu_unpack_kernel<FP16, 1>
          : u == 2 ? swiglu_unpack_kernel<FP16, 2> : swiglu_unpack_kernel<FP16, 3>;
   return launch_k(k, dim3(s.blocks), dim3(kSwThreads), 0, st, true, codes, scales, da, row_w, end,
