@@ -645,8 +645,11 @@ int64_t mm_grouped_product_dw_workspace_size(int R, int E, int N, int K, int dw_
  * bits for the backward pass: blocks of 32 consecutive columns of a row as
  * integers q in [-127,127] under one power of two, values q 2^(s - 127),
  *   s = max(floor(log2 max|z|) - 6, -127) + 127,  q = z 2^(127 - s) to the
- *   nearest integer, ties to even, beyond 127 to 127 (the OCP MXINT8 form).
- * A block that holds an infinity or a NaN becomes NaN (s = 255, q = 0).
+ *   nearest integer, ties to even, beyond 127 to 127.
+ * A block that holds an infinity or a NaN becomes NaN (s = 255, q = 0). This is
+ * MXINT8 of the OCP microscaling formats but for the byte: s is the exponent of one
+ * step, theirs (q / 64 under 2^(s' - 127)) that of 64, s' = s + 6. So their smallest
+ * step is 2^-133 and this one 2^-127; rows of theirs with s' < 6 have no form here.
  *
  * z [R,2I] (gate columns first), act [R,I] of dtype; codes [R,2I] int8, scales
  * [R,2I/32] bytes. I % 32 == 0, R <= 2^31 - 4096, 2I <= 2^20. rows_used (or
@@ -671,8 +674,9 @@ int mm_swiglu_pack_backward(const int8_t* codes, const uint8_t* scales, const vo
                             void* dz, void* act, float* d_row_w, void* stream);
 
 /*
- * The values [rows,K] of stored 8-bit rows (codes [rows,K], scales [rows,K/32]),
- * of any MM_DTYPE: exact in fp32 and bf16 for what mm_swiglu_pack writes; fp16
+ * The values q 2^(s - 127) [rows,K] of stored 8-bit rows (codes [rows,K], scales
+ * [rows,K/32] as mm_swiglu_pack writes them: six less than OCP's MXINT8 has, see
+ * there; 255 is NaN in both), of any MM_DTYPE: exact in fp32 and bf16 for what mm_swiglu_pack writes; fp16
  * rounds, beyond its range to infinity or zero. K % 32 == 0, K <= 2^20, rows <=
  * 2^31 - 4096.
  */

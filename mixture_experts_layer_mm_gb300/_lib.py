@@ -1067,7 +1067,8 @@ def mm_swiglu_pack_backward(codes, scales, d_act, row_w=None, offsets=None, stre
 
 def mm_mxint8_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     """The values [rows, K] of 8-bit rows (codes int8 [rows, K], scales uint8
-    [rows, K / 32]) as mm_swiglu_pack stores them."""
+    [rows, K / 32]) as mm_swiglu_pack stores them: q 2^(s - 127). (Rows of OCP's
+    MXINT8 from elsewhere have scales that are six more: subtract 6, but from 255.)"""
     if _fast is not None and stream is None:
         r = _fast.mxint8_dequantize(codes, scales, _DTYPES.get(dtype, -1))
         if r is not None:

@@ -7,8 +7,8 @@
 //               a' = w g sigma(g) u   (again: it was not kept)
 //               dw = sum_i da_i g_i sigma(g_i) u_i
 //
-// The 8 bits (the MXINT8 form of the OCP microscaling formats): blocks of 32
-// columns under one power of two, values q 2^(s - 127), q in [-127, 127], s - 127
+// The 8 bits (as MXINT8 of the OCP microscaling formats, whose byte is six more: it is
+// that of 64 steps, this one of one): blocks of 32 columns under one power of two, values q 2^(s - 127), q in [-127, 127], s - 127
 // = floor(log2 max|z|) - 6 but at least -127. The largest value is 64 to 128
 // steps, so a value is off by at most half a step, 2^-7 of the block's largest; for
 // normally distributed values 0.9 % of their norm. (Floats of 4 significant bits in

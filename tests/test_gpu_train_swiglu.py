@@ -208,3 +208,18 @@ def test_streams_and_graphs_share_nothing():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, r) for p, r in zip(got, want[1]))
+
+
+def test_rows_of_the_interchange_format():
+    """MXINT8 of the OCP formats, q / 64 under 2^(s' - 127): its bytes less six."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randint(-127, 128, (40, 96), generator=g, device="cuda").to(torch.int8)
+    theirs = torch.randint(6, 254, (40, 3), generator=g, device="cuda").to(torch.uint8)
+    theirs[3, 1] = 255
+    ours = torch.where(theirs == 255, theirs, theirs - 6)
+    unit = torch.ldexp(torch.ones((), dtype=torch.float64), theirs.cpu().int() - 127)
+    want = q.cpu().double().view(40, 3, 32) / 64 * unit[..., None]
+    want[3, 1] = float("nan")
+    got = mm.mm_mxint8_dequantize(q, ours, dtype=torch.float32).cpu().double().view(40, 3, 32)
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(0), want.nan_to_num(0))

@@ -222,3 +222,12 @@ def test_a_refused_backward_makes_no_call(mmlib, monkeypatch):
     call("CUDA", d_w_down=d_dn, d_w_gate_up=d_gu)
     call("d_out must be torch", TypeError, d_out=s.hidden.float(), d_w_down=d_dn, d_w_gate_up=d_gu)
     assert not made
+
+
+def test_the_byte_is_six_less_than_the_interchange_formats():
+    """In OCP's MXINT8 a block whose largest value is 1 has the byte 127 and codes q / 64."""
+    z = torch.zeros(1, 32)
+    z[0, :3] = torch.tensor([1.0, -0.75, 1 / 64])
+    q, s = ref.encode(z)
+    assert s.item() == 127 - 6 and q[0, :3].tolist() == [64, -48, 1]
+    assert torch.equal(ref.decode(q, s), (q.double() / 64) * 2.0 ** (s.double().item() + 6 - 127))
