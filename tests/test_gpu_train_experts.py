@@ -409,3 +409,36 @@ def test_a_refused_backward_leaves_the_gradients():
     mm.moe_experts_train_backward(d_out, s, gu, dn, d_gu, d_dn, accumulate=True)
     assert torch.equal(d_gu, 1 + want.d_w_gate_up) and torch.equal(d_dn, 1 + want.d_w_down)
     assert mm.mm_poll_device_status() == mm.MM_OK
+
+
+@pytest.mark.parametrize("T,H,E,I,k", [(16, 128, 8, 64, 2), (37, 72, 5, 96, 3),
+                                       (60, 264, 12, 160, 4)])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_weights_gradient_against_float64(T, H, E, I, k, masked, dtype):
+    """d_topk_w by itself, and d_logits against a scale that no result of the kernels enters.
+    A weight's gradient is the product of a row of da with one of activations, both with
+    the errors of the other gradients: over many slots its share is theirs."""
+    d = _inputs(T, H, E, I, k, dtype, seed=3)
+    mask = None
+    if masked:
+        mask = torch.arange(T, device="cuda") % 3 > 0
+    ids, w, counts, _, _ = mm.mm_route_logits(d["logits"], k, True, token_mask=mask)
+    _, saved = mm.moe_experts_train(d["hidden"], ids, w, d["gu"], d["dn"], token_mask=mask)
+    got = mm.moe_experts_train_backward(d["d_out"], saved, d["gu"], d["dn"]).d_topk_w
+    d_logits = mm.mm_route_logits_backward(d["logits"], ids, counts, True, got, token_mask=mask)
+    leaf = w.double().cpu().requires_grad_(True)
+    cm = None if mask is None else mask.cpu()
+    out = ref.experts(d["hidden"].double().cpu(), ids.cpu(), leaf, d["gu"].double().cpu(),
+                      d["dn"].double().cpu(), mask=cm)
+    want, = torch.autograd.grad((out * d["d_out"].double().cpu()).sum(), leaf)
+    assert _off(got, want) <= BACKWARD
+    if masked:
+        assert not got[~mask].any()
+    logits = d["logits"].double().cpu().requires_grad_(True)
+    p = torch.softmax(logits, -1).gather(1, ids.cpu().long())
+    weights = p / p.sum(-1, keepdim=True)
+    want_logits, = torch.autograd.grad((weights * want).sum(), logits)
+    scale = _topk_scale(weights.detach(), want, want_logits)
+    assert _off(d_logits, want_logits) <= BACKWARD * max(1.0, scale)
+    assert mm.mm_poll_device_status() == mm.MM_OK

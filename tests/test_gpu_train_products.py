@@ -457,3 +457,34 @@ def test_weights_where_copies_take_two_lines_a_row(E, R, N, K, dtype):
         old = _rand(g, E, N, K, dtype=out, std=30.0)
         acc = mm.mm_grouped_product_dw(dy, x, off, out=old.clone(), accumulate=True)
         ref.close(acc, want + old.double(), mag + old.double().abs(), max(lens) + 17, "accumulated")
+
+
+# fp32 results of segments of several slices: in the epilogue's registers, added up in
+# memory, and in parts, which are sums of slices themselves. (E, N, K, rows of the
+# segments, parts)
+SLICED = {"registers": (8, 640, 328, [14000, 3000, 3000, 0, 1, 5, 4, 1], False),
+          "memory": (128, 264, 512, [20000] + [300] * 127, False),
+          "parts": (1, 512, 512, [20000], True)}
+
+
+@pytest.mark.parametrize("name", SLICED)
+def test_slices_of_long_segments_keep_their_roundings(name):
+    """Values of one sign. A slice of 512 rows is 32 steps of 16 rows; each cuts up to 2^-23
+    of the sum so far, which grows evenly: 16.5 of 2^-23 of the slice's at most (18 where
+    the rows' sizes differ by chance), half of it on average. Then one fp32 addition a slice
+    and a part, 2^-24 of the sum so far each. In one accumulation 2240 rows (the parts')
+    would lose 2.4e-6 on average and 14000 rows 15e-6."""
+    E, N, K, lens, parts = SLICED[name]
+    R, off = sum(lens), _offsets(lens)
+    assert (mm.mm_grouped_product_dw_workspace_size(R, E, N, K, F) > 0) == parts
+    g = torch.Generator(device="cuda").manual_seed(8)
+    dy, x = ((1 + torch.rand(R, c, generator=g, device="cuda")).bfloat16() for c in (N, K))
+    got = mm.mm_grouped_product_dw(dy, x, off, out_dtype=F)
+    for e in [e for e in range(E) if lens[e] > 512] + [E - 1]:
+        a, b = off[e].item(), off[e + 1].item()
+        want = dy[a:b].double().T @ x[a:b].double()
+        err = (got[e].double() - want) / want
+        adds = lens[e] // 512 + 2 + (lens[e] // 2240 + 1 if parts else 0)
+        most = 18 * 2.0 ** -23 + (adds + 1) / 2 * 2.0 ** -24
+        assert err.abs().max() <= most
+        assert err.mean().abs() <= 9 * 2.0 ** -23 + 0.1 * (adds + 1) / 2 * 2.0 ** -24

@@ -222,3 +222,28 @@ def test_groups_of_a_cluster_at_the_same_time():
     torch.cuda.synchronize()
     for pair in got:
         assert all(torch.equal(x, y) for a, b in zip(pair, want) for x, y in zip(a, b))
+
+
+def test_good_places_are_written_beside_bad_ones():
+    """Every row: copies of their tokens, and those that only a bad place would have had
+    as they were."""
+    x = torch.randn(6, 64, device="cuda").bfloat16()
+    w = torch.rand(6, 2, device="cuda")
+    places = torch.arange(11, -1, -1, dtype=torch.int32, device="cuda").view(6, 2)
+    places[2, 1], places[4, 0], places[5, 1] = 12, -2, -1     # not 6, 3 and 0
+    rows, row_w = torch.full((12, 64), 3.0, device="cuda").bfloat16(), torch.full((12,), 3.0, device="cuda")
+    want, want_w = rows.clone(), row_w.clone()
+    for f, p in enumerate(places.flatten().tolist()):
+        if 0 <= p < 12:
+            want[p], want_w[p] = x[f // 2], w[f // 2, f % 2]
+    mm.mm_dispatch_rows(x, places, w=w, rows=rows, row_w=row_w)
+    assert mm.mm_poll_device_status() == mm.MM_ERR_DEVICE
+    assert torch.equal(rows, want) and torch.equal(row_w, want_w)
+    assert (want == 3).all(1).sum() == 3
+    vals = torch.rand(12, device="cuda")
+    out, v = mm.mm_combine_rows(rows, places, row_values=vals)
+    assert mm.mm_poll_device_status() == mm.MM_ERR_DEVICE
+    good = torch.where((places >= 0) & (places < 12), places, -1)
+    total, mag = ref.combine(rows, good)
+    ref.close(out, total, mag, 3)
+    assert torch.equal(v, torch.where(good >= 0, vals[good.clamp_min(0).long()], 0.0))
