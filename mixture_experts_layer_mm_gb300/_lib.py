@@ -828,9 +828,16 @@ def _rows_dtype(t, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
+def _ints(*sizes) -> bool:
+    """Whether these are ints to the library too: ctypes drops the bits beyond 32."""
+    return all(-1 << 31 <= n < 1 << 31 for n in sizes)
+
+
 def _dims(t, n: int, name: str):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    if not _ints(*t.shape):
+        raise ValueError(f"{name} must have sizes below 2^31, got shape {tuple(t.shape)}")
     return t.shape
 
 
@@ -845,7 +852,8 @@ def _result(on: _On, given, shape, dtype, name: str, like) -> torch.Tensor:
 
 
 def mm_group_slots_workspace_size(T: int, top_k: int, E: int) -> int:
-    return int(lib().mm_group_slots_workspace_size(T, top_k, E))
+    l = lib()
+    return int(l.mm_group_slots_workspace_size(T, top_k, E)) if _ints(T, top_k, E) else -1
 
 
 def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
@@ -863,9 +871,9 @@ def mm_group_slots(topk_ids, E: int, token_mask=None, stream=None):
     ids, mask = _ptr(topk_ids, torch.int32, "topk_ids"), _mask_ptr(token_mask, T)
     _device("mm_group_slots", topk_ids, token_mask)
     l = lib()
-    need = l.mm_group_slots_workspace_size(T, k, E)
     if E <= 0 or k == 0:
         raise MMError(MM_ERR_INVALID_ARG, "mm_group_slots")
+    need = mm_group_slots_workspace_size(T, k, E)
     if need < 0:
         raise MMError(MM_ERR_UNSUPPORTED, "mm_group_slots")
     on = _On("mm_group_slots", topk_ids, stream)
@@ -931,7 +939,8 @@ def mm_combine_rows(rows, places, w=None, row_values=None, out=None, stream=None
 
 def mm_grouped_product_dw_workspace_size(R: int, E: int, N: int, K: int, dtype) -> int:
     """dtype: of the result."""
-    return int(lib().mm_grouped_product_dw_workspace_size(R, E, N, K, _DTYPES.get(dtype, -1)))
+    l, dt = lib(), _DTYPES.get(dtype, -1)
+    return int(l.mm_grouped_product_dw_workspace_size(R, E, N, K, dt)) if _ints(R, E, N, K) else -1
 
 
 def _product(name: str, x, w, offsets, out, stream, transposed: bool):

@@ -416,7 +416,7 @@ PyObject* group_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* mask = c.any(a[2], true);
   if (!c.ok || ids->dim() != 2) Py_RETURN_NONE;
   const int64_t T = ids->size(0), k = ids->size(1);
-  if (!fits_int(T) || !fits_int(k) ||
+  if (!fits_int(T) || !fits_int(k) || !fits_int(E) ||
       (mask && (!shape_is(*mask, {T}) ||
                 (mask->scalar_type() != at::kBool && mask->scalar_type() != at::kByte))))
     Py_RETURN_NONE;

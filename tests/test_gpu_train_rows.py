@@ -247,3 +247,10 @@ def test_good_places_are_written_beside_bad_ones():
     total, mag = ref.combine(rows, good)
     ref.close(out, total, mag, 3)
     assert torch.equal(v, torch.where(good >= 0, vals[good.clamp_min(0).long()], 0.0))
+
+
+@pytest.mark.parametrize("E", [(1 << 32) + 8, 1 << 31, 257])
+def test_too_many_experts_are_refused(E):
+    with pytest.raises(mm.MMError) as e:
+        mm.mm_group_slots(_ids(4, 8, 2), E)
+    assert e.value.code == mm.MM_ERR_UNSUPPORTED

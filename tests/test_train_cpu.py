@@ -231,3 +231,28 @@ def test_the_byte_is_six_less_than_the_interchange_formats():
     q, s = ref.encode(z)
     assert s.item() == 127 - 6 and q[0, :3].tolist() == [64, -48, 1]
     assert torch.equal(ref.decode(q, s), (q.double() / 64) * 2.0 ** (s.double().item() + 6 - 127))
+
+
+def test_sizes_beyond_an_int_are_refused(mmlib):
+    """Not taken as what their lower 32 bits say."""
+    big = (1 << 32) + 4
+    assert mm.mm_group_slots_workspace_size(4096, 8, 128) > 0
+    for sizes in ((big, 2, 8), (4, big, 8), (4, 2, big), (1 << 31, 1, 8)):
+        assert mm.mm_group_slots_workspace_size(*sizes) == -1
+    for i in range(4):
+        sizes = [32768, 1, 64, 64]
+        assert mm.mm_grouped_product_dw_workspace_size(*sizes, torch.float32) > 0
+        sizes[i] += 1 << 32
+        assert mm.mm_grouped_product_dw_workspace_size(*sizes, torch.float32) == -1
+    b, i32 = torch.bfloat16, torch.int32
+    rows, slots = torch.zeros(1, 8, dtype=b).expand(big, 8), torch.zeros(1, 1, dtype=i32).expand(big, 1)
+    w, off = torch.zeros(1, 8, 8, dtype=b), torch.zeros(2, dtype=i32)
+    for f in (lambda: mm.mm_group_slots(slots, 8), lambda: mm.mm_dispatch_rows(rows, slots),
+              lambda: mm.mm_combine_rows(rows[:4], slots), lambda: mm.mm_combine_rows(rows, slots[:4]),
+              lambda: mm.mm_grouped_product(rows, w, off), lambda: mm.mm_grouped_product_dx(rows, w, off),
+              lambda: mm.mm_grouped_product_dw(rows, rows, off),
+              lambda: mm.mm_swiglu_pack(rows[:, :1].expand(big, 64)),
+              lambda: mm.mm_mxint8_dequantize(torch.zeros(1, 32, dtype=torch.int8).expand(big, 32),
+                                              torch.zeros(1, 1, dtype=torch.uint8).expand(big, 1))):
+        with pytest.raises(ValueError, match="below 2"):
+            f()
