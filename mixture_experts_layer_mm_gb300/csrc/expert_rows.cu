@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kGrThreads) group_place_kernel(const GroupArgs
 // A slot a thread, one block: the ids are read once (8 slots 1.5 us, 512 1.9, 1024 2.7;
 // 2.4, 2.9 and 3.4 in group_place_kernel).
 __global__ void __launch_bounds__(kGrThreads) group_few_kernel(const GroupArgs a) {
-  __shared__ int warp_count[kGrWarps][kMaxExperts];
+  __shared__ __align__(16) int warp_count[kGrWarps][kMaxExperts];
   __shared__ int warp_sum[kMaxExperts / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   for (int i = tid; i < warps * kMaxExperts / 4; i += blockDim.x)
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kGrThreads) group_few_kernel(const GroupArgs a
 __global__ void __launch_bounds__(kGrThreads) group_cluster_kernel(const GroupArgs a) {
   __shared__ int hist[kMaxExperts];   // this block's slots of each expert
   __shared__ int base[kMaxExperts], total[kMaxExperts];
-  __shared__ int warp_count[kGrWarps][kMaxExperts];
+  __shared__ __align__(16) int warp_count[kGrWarps][kMaxExperts];
   __shared__ int warp_sum[kMaxExperts / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank_in = (int)pair_rank();

@@ -34,3 +34,12 @@ def test_no_copy_goes_to_several_blocks(path):
     runs on one GPU alone."""
     for a in _assembly(open(path).read()):
         assert not ("cp.async.bulk" in a and "multicast" in a), a
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_shared_arrays_read_16_bytes_at_a_time_are_aligned_to_them(path):
+    """An array of ints in shared memory is aligned to 4 bytes unless it says otherwise."""
+    text = open(path).read()
+    wide = set(re.findall(r"reinterpret_cast<(?:const )?u?(?:int|float)4\s*\*>\(&?(\w+)", text))
+    for align, name in re.findall(r"__shared__\s+(__align__\(\d+\)\s+)?\w+\s+(\w+)\s*\[", text):
+        assert name not in wide or align.strip() in ("__align__(16)", "__align__(1024)"), name
