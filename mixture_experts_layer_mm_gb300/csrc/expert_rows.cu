@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kGrThreads) group_count_kernel(const GroupArgs
 __global__ void __launch_bounds__(kGrThreads) group_place_kernel(const GroupArgs a) {
   __shared__ int base[kMaxExperts + 1];   // next row of each expert
   __shared__ int total[kMaxExperts];
-  __shared__ int warp_count[kGrWarps][kMaxExperts];
+  __shared__ __align__(16) int warp_count[kGrWarps][kMaxExperts];
   __shared__ int warp_sum[kMaxExperts / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long f0 = blockIdx.x * a.span, f1 = min(f0 + a.span, a.n);
