@@ -563,8 +563,11 @@ int64_t mm_moe_experts_mxfp4_workspace_size(int T, int H, int E, int I, int top_
  *
  * Rows are 16-bit floats, dtype MM_DTYPE_BF16 or MM_DTYPE_FP16 (MM_DTYPE_FP32:
  * MM_ERR_UNSUPPORTED), contiguous, 16-byte aligned. Sums are fp32 and every
- * result is rounded once. All results are the same on every call. Nothing is
- * kept between calls; calls with distinct results and workspaces may overlap.
+ * result is rounded once. (The tensor cores cut what they add to a sum, which
+ * then is low by some 1e-9 of its terms' magnitudes for each term: 2e-6 for 2048,
+ * 1e-3 for 2^20. fp32 results of dw are sums of 512 rows at a time, added in
+ * fp32.) All results are the same on every call. Nothing is kept between calls;
+ * calls with distinct results and workspaces may overlap.
  */
 
 /*
@@ -667,7 +670,8 @@ int mm_swiglu_pack(const void* z, int dtype, const int32_t* rows_used, int R, in
  *   d_row_w[r] = sum_i d_act[r,i] silu(g_i) u_i                     [R] fp32
  * d_act is the gradient of the weighted activations (for the down product:
  * W_down^T d_out of the slot's token); with act, dW_down = sum d_out act^T needs
- * no weight. d_row_w NULL: not computed. Otherwise as mm_swiglu_pack.
+ * no weight. d_row_w NULL: not computed. Otherwise as mm_swiglu_pack. In both, a
+ * sigmoid below 2^-126 (g under -87.3) is 0.
  */
 int mm_swiglu_pack_backward(const int8_t* codes, const uint8_t* scales, const void* d_act,
                             int dtype, const float* row_w, const int32_t* rows_used, int R, int I,

@@ -117,7 +117,8 @@ __device__ __forceinline__ Place place_of(int lpr_log2) {
 
 // sigma(g) within 2^-20.5, by the hardware's 2^t and 1 / x, with what the product
 // t = -g log2(e) and that constant round off made up for by a factor. Beyond 200
-// either way the exponential is 0 or infinite, and sigma 1 or 0, whatever g is.
+// either way the exponential is 0 or infinite, and sigma 1 or 0, whatever g is. Where sigma
+// is below 2^-126 (g under -87.3) it is 0: g sigma is above -2e-36 there.
 __device__ __forceinline__ Pair sigmoid(Pair g) {
   constexpr double kLog2eExact = 1.44269504088896341;
   constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - kLog2e);
